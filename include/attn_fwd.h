@@ -47,7 +47,8 @@ typedef enum {
   ATTN_ERR_ALIGNMENT = 3,    /* q/k/v/o not 16-byte aligned, lse/kv_valid_len not 4-byte */
   ATTN_ERR_LAUNCH = 4,       /* the CUDA launch (or tensor-map encoding) failed */
   ATTN_ERR_TIMEOUT = 5,      /* a bounded in-kernel wait gave up (see attn_fwd_debug_status) */
-  ATTN_ERR_DEVICE = 6        /* CUDA runtime / driver error outside the launch */
+  ATTN_ERR_DEVICE = 6,       /* CUDA runtime / driver error outside the launch */
+  ATTN_ERR_CAPACITY = 7      /* an append dropped entries (see attn_cache4_append) */
 } attn_status_t;
 
 /*
@@ -241,13 +242,181 @@ attn_status_t attn_fwd_splitkv_static(const void* q, const void* k, const void* 
                                       float scale, int causal, const int32_t* kv_valid_len,
                                       int n_splits, void* stream);
 
+/* Element types of the calls below that take one. */
+typedef enum { ATTN_BF16 = 0, ATTN_FP16 = 1, ATTN_FP32 = 2 } attn_dtype_t;
+
+/*
+ * attn_fwd_varlen -- attention over whole prompts of different lengths, packed
+ * one behind the other, with grouped query heads.
+ *
+ *   For sequence s, rows seq_start[s] .. seq_start[s+1] - 1 of the packed
+ *   buffers, query head h and its key head h / (H_q / H_kv): attn_fwd's O and
+ *   LSE over that sequence's own keys (causal: those up to the row itself).
+ *   Nothing outside a sequence reaches it, whatever it holds (NaN included).
+ *
+ *   q, k, v     device bf16 or fp16: row t of q is H_q heads of D elements at
+ *               q + t * q_stride, and likewise H_kv heads in k and v.  Slices of
+ *               one fused projection's rows will do.  16-byte aligned, strides
+ *               (in elements) multiples of 8.
+ *   o           device, type of q, [total][H_q][D], 16-byte aligned, written.
+ *   lse         device fp32 [H_q][total], written (natural log).
+ *   total       rows of the buffers, 0 .. 2^31 - 1.  Rows that belong to no
+ *               sequence (behind the last one) are left as they were.
+ *   seq_start   device int32[n_seqs + 1], not read by the host: ascending from
+ *               0 or more to `total` or less.  A sequence may be empty.  Entries
+ *               out of range or order are clamped to the rows there are.
+ *   dtype       ATTN_BF16 or ATTN_FP16 (q, k, v and o).
+ *   H_q / H_kv  a whole number, at most 128.  D is 64 or 128.
+ *   workspace   caller-owned device buffer, 16-byte aligned, of at least
+ *               attn_fwd_varlen_workspace_bytes(...) bytes; overwritten.
+ * Values within a sequence are finite (a NaN or infinity in V reaches, as a
+ * product with zero, rows of its own sequence that do not see it).
+ * Asynchronous (two kernel launches); argument errors are reported before
+ * anything is launched.  Calls that share a workspace must be ordered.
+ */
+attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int64_t total, const int32_t* seq_start, int n_seqs, int H_q, int H_kv,
+                              int D, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              float scale, int causal, void* workspace, uint64_t workspace_bytes,
+                              void* stream);
+
+/* Workspace bytes attn_fwd_varlen needs (0 for invalid arguments). */
+uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int H_kv, int D);
+
+/*
+ * attn_cache4_t -- a K/V cache held in 4 bits.  Every buffer is the caller's, in
+ * device memory; the host reads only this struct.
+ *
+ *   The cache of sequence b and key head h is `capacity` slots, of which the
+ *   first length[b] hold an entry: a K row and a V row of D channels.  Every 64
+ *   channels of a row share a scale s and a minimum m, both bf16; a value is
+ *   held as a code c in 0 .. 15 and stands for c*s + m, with
+ *     m = bf16(min x), s = bf16((max x - min x) / 15),
+ *     c = clamp(rint((x - m) / s), 0, 15), or 0 where s is 0.
+ *   A group with a value that is not finite stands for NaN.
+ *
+ *   k_codes, v_codes  uint8 [B][H_kv][capacity][D/2], 16-byte aligned: channel
+ *                     2i in the low half of byte i, 2i + 1 in the high half
+ *   k_meta, v_meta    bf16 [B][H_kv][capacity][D/64][2]: (s, m)
+ *   weight            fp32 [B][H_kv][capacity]: attention weight each entry has
+ *                     received, or NULL where the call does not use it
+ *   pos               int32 [B][H_kv][capacity]: position of each entry's token
+ *                     in its sequence, or NULL where the call does not use it
+ *   length            int32 [B]; calls clamp it to 0 .. capacity (or max_len)
+ * D is 64 or 128.  Entries behind length[b] are never read.
+ */
+typedef struct {
+  void* k_codes;
+  void* k_meta;
+  void* v_codes;
+  void* v_meta;
+  float* weight;
+  int32_t* pos;
+  int32_t* length;
+  int B;
+  int H_kv;
+  int capacity;
+  int D;
+} attn_cache4_t;
+
+/*
+ * attn_cache4_append -- quantise new rows of K and V into the cache.
+ *
+ *   k, v        device bf16 or fp16 (dtype): row t is H_kv heads of D elements at
+ *               k + t * k_stride; 16-byte aligned, strides multiples of 8.
+ *   rows        rows of k and v.
+ *   seq_start   device int32[B + 1] as attn_fwd_varlen takes it: rows
+ *               seq_start[b] .. seq_start[b+1] - 1 are sequence b's; rows behind
+ *               the last are left out.  NULL: one row for each sequence (rows = B).
+ *   first_pos   device int32[B]: position of each sequence's first new token.
+ *               NULL: its slot's number.
+ *   length_out  device int32[B], written: the lengths after the call.  It may be
+ *               cache->length (one more small launch).
+ * Row i of sequence b goes to slot length[b] + i of every key head, with weight
+ * 0 and position first_pos[b] + i (where the cache has those buffers).  Rows for
+ * which there is no room are dropped, the length stays at the capacity, and
+ * attn_fwd_debug_status reports ATTN_ERR_CAPACITY.  Asynchronous.
+ */
+attn_status_t attn_cache4_append(const attn_cache4_t* cache, const void* k, const void* v, int64_t rows,
+                                 int64_t k_stride, int64_t v_stride, int dtype, const int32_t* seq_start,
+                                 const int32_t* first_pos, int32_t* length_out, void* stream);
+
+/*
+ * attn_cache4_read -- the values that entries stand for, as packed rows: row i
+ * of sequence b is slot first_slot[b] + i (first_slot NULL: slot i).  dtype is
+ * ATTN_BF16, ATTN_FP16 or ATTN_FP32 (strides multiples of 8, or 4); rows of
+ * slots outside the capacity, and rows of no sequence, are left as they were.
+ * The lengths are not looked at.  Other arguments as attn_cache4_append.
+ */
+attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int64_t rows,
+                               int64_t k_stride, int64_t v_stride, int dtype, const int32_t* seq_start,
+                               const int32_t* first_slot, void* stream);
+
+/*
+ * attn_cache4_decode -- attention of one token per sequence over the cache:
+ * every query head of sequence b sees its key head's first length[b] entries.
+ *
+ *   q           device bf16 or fp16 (dtype): H_q heads of D elements at
+ *               q + b * q_stride; 16-byte aligned, stride a multiple of 8.
+ *   o           device, type of q, [B][H_q][D], written.  lse fp32 [B][H_q].
+ *               A sequence without entries gets O = 0, LSE = -inf.
+ *   max_len     1 .. capacity: a bound on the lengths (they are clamped to it);
+ *               it sizes the workspace.
+ *   weight_in, weight_out
+ *               both NULL, or fp32 [B][H_kv][capacity]: weight_out = weight_in +
+ *               the softmax weight of the entry, summed over the query heads of
+ *               its group.  They may be the same buffer (cache->weight).  Places
+ *               behind a length are left as they were.
+ *   workspace   at least attn_cache4_decode_workspace_bytes(...) bytes, 16-byte
+ *               aligned; overwritten.  Calls that share one must be ordered.
+ * H_q / H_kv is a whole number, at most 128.  Results are the same from call to
+ * call.  Asynchronous (two kernel launches).
+ */
+attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int64_t q_stride, void* o,
+                                 float* lse, int H_q, int dtype, float scale, int max_len,
+                                 const float* weight_in, float* weight_out, void* workspace,
+                                 uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_cache4_decode needs (0 for invalid arguments). */
+uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int max_len,
+                                            int with_weight);
+
+/*
+ * attn_cache4_evict -- shorten every sequence of more than `budget` entries to
+ * `budget`: each key head keeps the entries of the `recent` newest positions
+ * (pos > newest - recent), then those of the highest weight; ties keep the lower
+ * slot, a NaN counts as the highest weight.
+ *
+ *   A kept entry in a slot below the budget stays there; the i-th kept entry
+ *   behind it (in slot order) moves to the i-th slot that became free.  So the
+ *   entries are no longer in the order of their positions, which attention does
+ *   not need, and what lies behind the budget is left as it was.
+ *
+ *   budget 1 or more, recent 0 .. budget, max_len as attn_cache4_decode.
+ *   weight_out, pos_out, length_out
+ *               the cache's weight, pos and length after the call.  Each may be
+ *               the cache's own buffer (the length costs one more small launch)
+ *               or another that does not overlap it; places behind the new
+ *               length are left as they were.
+ *   workspace   at least attn_cache4_evict_workspace_bytes(...) bytes, 16-byte
+ *               aligned; overwritten.  Calls that share one must be ordered.
+ * cache->weight and cache->pos are needed.  Asynchronous.
+ */
+attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int recent, int max_len,
+                                float* weight_out, int32_t* pos_out, int32_t* length_out,
+                                void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_cache4_evict needs (0 for invalid arguments). */
+uint64_t attn_cache4_evict_workspace_bytes(int B, int H_kv, int max_len, int budget);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* attn_status_str(attn_status_t status);
 
 /*
  * attn_fwd_debug_status -- synchronise `stream`, then read and clear the
  * device status word that the kernels set when a bounded wait gives up.
- * Returns ATTN_OK, ATTN_ERR_TIMEOUT, or ATTN_ERR_DEVICE if the
+ * Returns ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_CAPACITY if an append dropped
+ * entries (attn_cache4_append), or ATTN_ERR_DEVICE if the
  * synchronisation itself reported a CUDA error or the backward kernel found
  * its dynamic shared memory off a 1024-byte boundary (it then runs nothing).
  */

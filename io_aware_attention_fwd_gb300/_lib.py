@@ -18,14 +18,31 @@ ATTN_ERR_ALIGNMENT = 3
 ATTN_ERR_LAUNCH = 4
 ATTN_ERR_TIMEOUT = 5
 ATTN_ERR_DEVICE = 6
+ATTN_ERR_CAPACITY = 7
+
+# attn_dtype_t
+ATTN_BF16 = 0
+ATTN_FP16 = 1
+ATTN_FP32 = 2
 
 # every extern "C" function include/attn_fwd.h declares
 EXPORTED = ("attn_fwd", "attn_fwd_fp8", "attn_bwd", "attn_bwd_workspace_bytes", "attn_fwd_splitkv", "attn_fwd_splitkv_workspace_bytes",
             "attn_fwd_splitkv_suggest", "attn_fwd_schedule", "attn_merge", "attn_fwd_splitkv_static", "attn_status_str", "attn_fwd_debug_status",
-            "attn_watchdog_selftest", "attn_fwd_abi_version")
+            "attn_watchdog_selftest", "attn_fwd_abi_version", "attn_fwd_varlen", "attn_fwd_varlen_workspace_bytes",
+            "attn_cache4_append", "attn_cache4_read", "attn_cache4_decode", "attn_cache4_decode_workspace_bytes",
+            "attn_cache4_evict", "attn_cache4_evict_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class attn_cache4_t(ctypes.Structure):
+    """The struct of the same name: a 4-bit K/V cache's buffers and sizes."""
+
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_meta", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_meta", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("length", ctypes.c_void_p), ("B", ctypes.c_int), ("H_kv", ctypes.c_int),
+                ("capacity", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 class AttnError(RuntimeError):
@@ -39,6 +56,8 @@ class AttnError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load the built library (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not LIB_PATH.exists():
@@ -69,6 +88,23 @@ def load() -> ctypes.CDLL:
             lib.attn_fwd_splitkv_static.argtypes = [p, p, p, p, p, i, i, i, i, i, ctypes.c_float, i, p, i, p]
             lib.attn_merge.restype = i
             lib.attn_merge.argtypes = [p, p, i, i64, i, p, p, p]
+            c4 = ctypes.POINTER(attn_cache4_t)
+            lib.attn_fwd_varlen.restype = i
+            lib.attn_fwd_varlen.argtypes = [p, p, p, p, p, i64, p, i, i, i, i, i, i64, i64, i64, f, i, p, u64, p]
+            lib.attn_fwd_varlen_workspace_bytes.restype = u64
+            lib.attn_fwd_varlen_workspace_bytes.argtypes = [i64, i, i, i, i]
+            lib.attn_cache4_append.restype = i
+            lib.attn_cache4_append.argtypes = [c4, p, p, i64, i64, i64, i, p, p, p, p]
+            lib.attn_cache4_read.restype = i
+            lib.attn_cache4_read.argtypes = [c4, p, p, i64, i64, i64, i, p, p, p]
+            lib.attn_cache4_decode.restype = i
+            lib.attn_cache4_decode.argtypes = [c4, p, i64, p, p, i, i, f, i, p, p, p, u64, p]
+            lib.attn_cache4_decode_workspace_bytes.restype = u64
+            lib.attn_cache4_decode_workspace_bytes.argtypes = [i, i, i, i, i, i]
+            lib.attn_cache4_evict.restype = i
+            lib.attn_cache4_evict.argtypes = [c4, i, i, i, p, p, p, p, u64, p]
+            lib.attn_cache4_evict_workspace_bytes.restype = u64
+            lib.attn_cache4_evict_workspace_bytes.argtypes = [i, i, i, i]
             lib.attn_status_str.restype = ctypes.c_char_p
             lib.attn_status_str.argtypes = [i]
             lib.attn_fwd_debug_status.restype = i
@@ -207,6 +243,66 @@ def attn_fwd_splitkv_static(q, k, v, o, lse, B: int, H: int, S_q: int, S_kv: int
                                         _stream(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_splitkv_static")
+
+
+def attn_fwd_varlen(q, k, v, o, lse, total: int, seq_start, n_seqs: int, H_q: int, H_kv: int, D: int, dtype: int,
+                    q_stride: int, k_stride: int, v_stride: int, scale: float, causal: bool, workspace,
+                    workspace_bytes: int, stream=None) -> None:
+    """Enqueue attention over packed prompts with grouped heads (see include/attn_fwd.h)."""
+    st = load().attn_fwd_varlen(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), total, _addr(seq_start), n_seqs, H_q,
+                                H_kv, D, dtype, q_stride, k_stride, v_stride, scale, int(bool(causal)),
+                                _addr(workspace), workspace_bytes, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_varlen")
+
+
+def attn_fwd_varlen_workspace_bytes(total: int, n_seqs: int, H_q: int, H_kv: int, D: int) -> int:
+    return load().attn_fwd_varlen_workspace_bytes(total, n_seqs, H_q, H_kv, D)
+
+
+def attn_cache4_append(cache: attn_cache4_t, k, v, rows: int, k_stride: int, v_stride: int, dtype: int, seq_start,
+                       first_pos, length_out, stream=None) -> None:
+    """Enqueue the quantising append of K and V rows (see include/attn_fwd.h)."""
+    st = load().attn_cache4_append(cache, _addr(k), _addr(v), rows, k_stride, v_stride, dtype, _addr(seq_start),
+                                   _addr(first_pos), _addr(length_out), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache4_append")
+
+
+def attn_cache4_read(cache: attn_cache4_t, k, v, rows: int, k_stride: int, v_stride: int, dtype: int, seq_start,
+                     first_slot, stream=None) -> None:
+    """Enqueue the read-back of cache entries (see include/attn_fwd.h)."""
+    st = load().attn_cache4_read(cache, _addr(k), _addr(v), rows, k_stride, v_stride, dtype, _addr(seq_start),
+                                 _addr(first_slot), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache4_read")
+
+
+def attn_cache4_decode(cache: attn_cache4_t, q, q_stride: int, o, lse, H_q: int, dtype: int, scale: float,
+                       max_len: int, weight_in, weight_out, workspace, workspace_bytes: int, stream=None) -> None:
+    """Enqueue attention of one token per sequence over the cache (see include/attn_fwd.h)."""
+    st = load().attn_cache4_decode(cache, _addr(q), q_stride, _addr(o), _addr(lse), H_q, dtype, scale, max_len,
+                                   _addr(weight_in), _addr(weight_out), _addr(workspace), workspace_bytes,
+                                   _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache4_decode")
+
+
+def attn_cache4_decode_workspace_bytes(B: int, H_q: int, H_kv: int, D: int, max_len: int, with_weight: bool) -> int:
+    return load().attn_cache4_decode_workspace_bytes(B, H_q, H_kv, D, max_len, int(bool(with_weight)))
+
+
+def attn_cache4_evict(cache: attn_cache4_t, budget: int, recent: int, max_len: int, weight_out, pos_out, length_out,
+                      workspace, workspace_bytes: int, stream=None) -> None:
+    """Enqueue the eviction by accumulated weight (see include/attn_fwd.h)."""
+    st = load().attn_cache4_evict(cache, budget, recent, max_len, _addr(weight_out), _addr(pos_out), _addr(length_out),
+                                  _addr(workspace), workspace_bytes, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache4_evict")
+
+
+def attn_cache4_evict_workspace_bytes(B: int, H_kv: int, max_len: int, budget: int) -> int:
+    return load().attn_cache4_evict_workspace_bytes(B, H_kv, max_len, budget)
 
 
 def call_status(fn, *args, **kwargs) -> int:

@@ -77,3 +77,104 @@ def attention_backward(q, k, v, o, lse, d_o, scale: float | None = None, causal:
     _lib.attn_bwd(q, k, v, o, lse, d_o, dq, dk, dv, B, H, S_q, S_kv, D, scale, causal, kv_valid_len,
                   ws, nbytes, stream)
     return dq, dk, dv
+
+
+def on_stream(device, stream, call):
+    """call(handle) with `device` current and, where a stream is given, that
+    stream too, so that what the call allocates belongs to it."""
+    import torch
+
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _lib._stream(stream)
+            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def element_type(dtype, also_fp32: bool = False) -> int:
+    """attn_dtype_t of a torch dtype the serving calls take."""
+    import torch
+
+    if dtype == torch.bfloat16:
+        return _lib.ATTN_BF16
+    if dtype == torch.float16:
+        return _lib.ATTN_FP16
+    if also_fp32 and dtype == torch.float32:
+        return _lib.ATTN_FP32
+    raise TypeError(f"{dtype}: must be bfloat16 or float16" + (" or float32" if also_fp32 else ""))
+
+
+def row_stride(t, name: str) -> int:
+    """Elements from one row of t [rows, H, D] to the next; the heads of a row lie side by side."""
+    s, (rows, H, D) = t.stride(), t.shape
+    if (s[2] != 1 and D > 1) or (s[1] != D and H > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if rows > 1 else H * D
+
+
+def check_out(t, shape, dtype, device, name: str) -> None:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+
+
+def check_int32(t, n: int, device, name: str) -> None:
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+
+
+def attention_varlen(q, k, v, seq_start, scale: float | None = None, causal: bool = True, out=None, lse=None,
+                     stream=None):
+    """O and LSE of whole prompts packed one behind the other, with grouped heads.
+
+    q [total, H_q, D], k and v [total, H_kv, D]: bf16 or fp16 CUDA tensors (all
+    of one type) whose rows may lie apart, as slices of one projection's output
+    do; H_q is a multiple of H_kv, D is 64 or 128.  seq_start: int32 CUDA tensor
+    [n + 1], sequence s being rows seq_start[s] .. seq_start[s + 1] - 1; query
+    head h sees key head h // (H_q // H_kv) of its own sequence, up to its own
+    row if causal.  Returns (o, lse): o [total, H_q, D] of q's type, lse fp32
+    [H_q, total].  Rows that belong to no sequence are left as they were, which
+    in outputs allocated here means undefined.
+    """
+    import torch
+
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("q must be [total, H_q, D], k and v [total, H_kv, D]")
+    total, H_q, D = q.shape
+    H_kv = k.shape[1]
+    if k.shape[0] != total or k.shape[2] != D or H_kv < 1 or H_q % H_kv:
+        raise ValueError("k and v must be [total, H_kv, D] matching q, H_q a multiple of H_kv")
+    dtype, device = q.dtype, q.device
+    code = element_type(dtype)
+    if k.dtype != dtype or v.dtype != dtype:
+        raise TypeError("q, k, v must be of one type")
+    if not q.is_cuda or k.device != device or v.device != device:
+        raise ValueError("q, k, v must be CUDA tensors of one device")
+    n = seq_start.shape[0] - 1 if seq_start.dim() == 1 else 0
+    if n < 1:
+        raise ValueError("seq_start must have at least two entries")
+    check_int32(seq_start, n + 1, device, "seq_start")
+    strides = row_stride(q, "q"), row_stride(k, "k"), row_stride(v, "v")
+    if out is not None:
+        check_out(out, q.shape, dtype, device, "out")
+    if lse is not None:
+        check_out(lse, (H_q, total), torch.float32, device, "lse")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    nbytes = _lib.attn_fwd_varlen_workspace_bytes(total, n, H_q, H_kv, D)
+
+    def call(handle):
+        o = out if out is not None else torch.empty((total, H_q, D), dtype=dtype, device=device)
+        z = lse if lse is not None else torch.empty((H_q, total), dtype=torch.float32, device=device)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        _lib.attn_fwd_varlen(q, k, v, o, z, total, seq_start, n, H_q, H_kv, D, code, *strides, scale, causal, ws,
+                             nbytes, handle)
+        return o, z
+
+    return on_stream(device, stream, call)

@@ -1,0 +1,1435 @@
+// A K/V cache held in 4 bits: appending to it, reading it back, attention of
+// one token per sequence over it, and its eviction by accumulated attention
+// weight.  Part of attn_fwd.cu (same PTX wrappers, same launch helpers).
+//
+// Format.  The cache of one (batch b, key head h) is `cap` slots.  Each slot
+// holds a K row and a V row of D channels; every 64 channels share a scale s
+// and a minimum m (both bf16), and each value is a code c in 0 .. 15 that
+// stands for c*s + m:
+//     m = bf16(min x),  s = bf16((max x - min x) / 15),
+//     c = clamp(rint((x - m) / s), 0, 15)   (0 where s is 0).
+// Channel 2i of a row is the low half of byte i, channel 2i + 1 the high half.
+// That is 4.5 bits a value.  A row stays whole in D/2 consecutive bytes, so
+// eviction moves rows and nothing is ever requantised.  A group that holds a
+// value that is not finite gets s = m = NaN.
+
+namespace {
+
+constexpr int kC4Group = 64;       // channels that share a scale and a minimum
+constexpr unsigned kC4Overflow = 4u;  // g_attn_status: entries beyond the capacity were dropped
+
+struct Cache4 {
+  uint8_t* k;        // [B][H][cap][D/2]
+  uint8_t* v;
+  uint32_t* km;      // [B][H][cap][D/64], bf16 (s, m): s in the low half
+  uint32_t* vm;
+  int H;
+  int cap;
+};
+
+// Number of cache entries of sequence b that a call sees.
+__device__ __forceinline__ int c4_len(const int32_t* __restrict__ len, int b, int most) {
+  return min(max(__ldg(len + b), 0), most);
+}
+
+// The sequence that packed row `row` belongs to: the last b with start[b] <=
+// row (sequences of no rows are stepped over), or n when row lies behind them
+// all or before the first.
+__device__ __forceinline__ int seq_of_row(const int32_t* __restrict__ start, int n, int row) {
+  if (row < __ldg(start) || row >= __ldg(start + n)) return n;
+  int lo = 0, hi = n;  // start[lo] <= row < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(start + mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+struct Cache4Rows {
+  const int32_t* seq_start;  // [B + 1], or null: row b belongs to sequence b
+  const int32_t* slot0;      // [B] first slot of each sequence's rows, or null: 0
+  int B;
+  int64_t rows;
+  int64_t k_stride, v_stride;  // elements from one packed row to the next
+};
+
+// Blocks of kC4RowsThreads threads; 8 channels (one 4-byte word of codes) a
+// thread.  A block takes the same 16 (D = 128) or 32 (D = 64) tokens of one
+// key head: consecutive blocks read neighbouring heads of those tokens, and
+// each block writes one contiguous piece of the cache.
+constexpr int kC4RowsThreads = 256;
+template <int D>
+constexpr int kC4RowLanes = D / 8;
+template <int D>
+constexpr int kC4BlockRows = kC4RowsThreads / kC4RowLanes<D>;
+
+// Finds this thread's row: token row, head and cache entry index
+// ((b*H + h)*cap + slot), or -1 for nothing to do.
+template <int D>
+__device__ __forceinline__ int64_t c4_row(const Cache4Rows& g, const Cache4& c, int64_t row, int h, int* b_out,
+                                          int* slot_out, bool* dropped) {
+  *dropped = false;
+  if (row >= g.rows) return -1;
+  int b = static_cast<int>(row), i = 0;
+  if (g.seq_start != nullptr) {
+    b = seq_of_row(g.seq_start, g.B, static_cast<int>(row));
+    if (b >= g.B) return -1;
+    i = static_cast<int>(row) - __ldg(g.seq_start + b);
+  }
+  const int64_t slot = static_cast<int64_t>(i) + (g.slot0 != nullptr ? __ldg(g.slot0 + b) : 0);
+  *b_out = b;
+  *slot_out = static_cast<int>(slot);
+  if (slot < 0 || slot >= c.cap) {
+    *dropped = true;
+    return -1;
+  }
+  return (static_cast<int64_t>(b) * c.H + h) * c.cap + slot;
+}
+
+// One row's 8 channels of this thread: the group's statistics over its 8
+// lanes, the codes and the (s, m) word.
+__device__ __forceinline__ uint32_t c4_quantise(const float* x, uint32_t* meta) {
+  float lo = x[0], hi = x[0];
+  bool finite = isfinite(x[0]);
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+    finite = finite && isfinite(x[e]);
+  }
+  if (!finite) lo = -INFINITY, hi = INFINITY;  // marks the whole group
+#pragma unroll
+  for (int off = 1; off < 8; off <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  // IEEE subtraction and division, no contraction: the codes are the format's
+  const uint32_t sm = pack_bf16x2(__fdiv_rn(__fsub_rn(hi, lo), 15.f), lo);
+  if (hi == INFINITY || lo == -INFINITY) {
+    *meta = 0x7fc07fc0u;  // (NaN, NaN)
+    return 0u;
+  }
+  *meta = sm;
+  const float s = bf16_lo(sm), m = bf16_hi(sm);
+  uint32_t w = 0u;
+  if (s != 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], m), s)), 0.f), 15.f);
+      w |= static_cast<uint32_t>(q) << (4 * e);
+    }
+  }
+  return w;
+}
+
+// Appends packed rows of K and V (bf16 or fp16): quantises each row, writes
+// it at its sequence's next slot, its position, and a zero weight.
+// HBM-bound: 4*D bytes read and D + D/8 + 8 written per row and head.
+template <int D, int kType>
+__global__ void __launch_bounds__(kC4RowsThreads)
+    attn_cache4_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, Cache4Rows g, Cache4 c,
+                              float* __restrict__ weight, int32_t* __restrict__ pos,
+                              const int32_t* __restrict__ first_pos, int32_t* __restrict__ len_out) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x) % kC4RowLanes<D>;
+  const int64_t n_chunks = (g.rows + kC4BlockRows<D> - 1) / kC4BlockRows<D>;
+  for (int64_t u = blockIdx.x; u < n_chunks * c.H; u += gridDim.x) {
+    const int h = static_cast<int>(u % c.H);
+    const int64_t row = (u / c.H) * kC4BlockRows<D> + threadIdx.x / kC4RowLanes<D>;
+    uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
+    if (row < g.rows) {  // the loads need no sequence: they go out before its search
+      xk = __ldg(reinterpret_cast<const uint4*>(k + row * g.k_stride + h * D + lane * 8));
+      xv = __ldg(reinterpret_cast<const uint4*>(v + row * g.v_stride + h * D + lane * 8));
+    }
+    int b = 0, slot = 0;
+    bool dropped;
+    const int64_t at = c4_row<D>(g, c, row, h, &b, &slot, &dropped);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint4 raw = kv ? xv : xk;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_16x2<kType>((&raw.x)[e]);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+      }
+      uint32_t meta;
+      const uint32_t w = c4_quantise(x, &meta);
+      if (at >= 0) {
+        reinterpret_cast<uint32_t*>(kv ? c.v : c.k)[at * (D / 8) + lane] = w;
+        if ((lane & 7) == 0) (kv ? c.vm : c.km)[at * (D / kC4Group) + (lane >> 3)] = meta;
+      }
+    }
+    if (lane == 0) {
+      if (at >= 0) {
+        if (weight != nullptr) weight[at] = 0.f;
+        if (pos != nullptr)
+          pos[at] = first_pos != nullptr ? __ldg(first_pos + b) + (slot - (g.slot0 != nullptr ? __ldg(g.slot0 + b) : 0))
+                                         : slot;
+      } else if (dropped) {
+        atomicOr(&g_attn_status, kC4Overflow);
+      }
+    }
+  }
+  if (len_out != nullptr) {
+    for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
+         b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      const int64_t n = g.seq_start != nullptr ? max(0, __ldg(g.seq_start + b + 1) - __ldg(g.seq_start + b)) : 1;
+      const int64_t l = max(0, __ldg(g.slot0 + b)) + n;
+      len_out[b] = static_cast<int32_t>(l < c.cap ? l : c.cap);
+    }
+  }
+}
+
+// The same update where len_out is the cache's own length: a launch behind
+// the one whose blocks all read it.
+__global__ void attn_cache4_grow_kernel(const int32_t* __restrict__ seq_start, int32_t* len, int B, int cap) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < B;
+       b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t n = seq_start != nullptr ? max(0, __ldg(seq_start + b + 1) - __ldg(seq_start + b)) : 1;
+    const int64_t l = max(0, len[b]) + n;
+    len[b] = static_cast<int32_t>(l < cap ? l : cap);
+  }
+}
+
+// Reads entries back into packed rows: c*s + m, rounded once to the output's
+// type.  c*s + m is exact in fp32 wherever s and m are within 2^12 of each
+// other (4 + 8 bits of c*s against 8 of m).
+template <int D, int kType>
+__global__ void __launch_bounds__(kC4RowsThreads)
+    attn_cache4_read_kernel(void* __restrict__ k, void* __restrict__ v, Cache4Rows g, Cache4 c) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x) % kC4RowLanes<D>;
+  const int64_t n_chunks = (g.rows + kC4BlockRows<D> - 1) / kC4BlockRows<D>;
+  for (int64_t u = blockIdx.x; u < n_chunks * c.H; u += gridDim.x) {
+    const int h = static_cast<int>(u % c.H);
+    const int64_t row = (u / c.H) * kC4BlockRows<D> + threadIdx.x / kC4RowLanes<D>;
+    int b, slot;
+    bool dropped;
+    const int64_t at = c4_row<D>(g, c, row, h, &b, &slot, &dropped);
+    if (at < 0) continue;
+    const uint32_t wk = __ldg(reinterpret_cast<const uint32_t*>(c.k) + at * (D / 8) + lane);
+    const uint32_t wv = __ldg(reinterpret_cast<const uint32_t*>(c.v) + at * (D / 8) + lane);
+    const uint32_t mk = __ldg(c.km + at * (D / kC4Group) + (lane >> 3));
+    const uint32_t mv = __ldg(c.vm + at * (D / kC4Group) + (lane >> 3));
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint32_t w = kv ? wv : wk, sm = kv ? mv : mk;
+      const float s = bf16_lo(sm), m = bf16_hi(sm);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(static_cast<float>((w >> (4 * e)) & 15u), s, m);
+      const int64_t to = row * (kv ? g.v_stride : g.k_stride) + h * D + lane * 8;
+      if constexpr (kType == kFP32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(kv ? v : k) + to);
+        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? v : k) + to) =
+            make_uint4(pack_16x2<kType>(x[0], x[1]), pack_16x2<kType>(x[2], x[3]), pack_16x2<kType>(x[4], x[5]),
+                       pack_16x2<kType>(x[6], x[7]));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention of one token per sequence over the cache
+// ---------------------------------------------------------------------------
+//
+// For a group of G query heads that share a key head,
+//     x_gj = scale * <q_g, k_j>,  O_g = sum_j softmax_j(x_g.) v_j.
+// With k_j = s*(c - 8) + (m + 8 s) in each group of 64 channels, the codes go
+// through the tensor core as they are and the scales are applied to sums:
+//     <q, k_j>  = sum over groups of  s * <q, c - 8> + (m + 8 s) * sum q
+//     sum_j p_j v_j = sum_j (p_j s) (c - 8) + sum_j p_j (m + 8 s).
+// c - 8 is exact in bf16 and fp16: a code is ORed into the mantissa of 128
+// (bf16) or 1024 (fp16) and 136 or 1032 subtracted, two values at a time.
+//
+// mma.sync m16n8k16 serves here, with keys as the M rows of S^T = K Q^T, and
+// channels as the M rows of O^T = V^T P^T: the A operands are then the cache's
+// codes, dequantised in registers straight from global memory, and N = 8 is
+// one block of up to 8 query heads.  The pass is bound by HBM (4.5 bits a
+// value), so tcgen05, which wants its operands in shared memory, would only
+// add a round trip.  The order of the channels within an MMA is free as long
+// as both operands use the same one: slot (2i, 2i + 1) takes nibbles (e, e + 4)
+// of a word, which one mask extracts together.
+//
+// Work split: the cache entries of all sequences and key heads, in tiles of 64
+// keys, form one list, cut into equal contiguous shares, one per CTA, whatever
+// the lengths are.  A CTA's share of one (sequence, key head) is a segment;
+// its four warps take 16 keys of every tile each, with running statistics of
+// their own, and join at the segment's end into one partial (m, l, O).  The
+// merge kernel joins the partials of a row.
+
+constexpr int kC4DecThreads = 128;  // 4 warps
+constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
+constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
+constexpr int kC4DecCtasPerSm = 4;
+// A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
+// so that a size asked for on one device (or with none) holds on any.
+constexpr int kC4WorkspaceSms = 152;
+
+struct DecParams {
+  Cache4 c;
+  const uint16_t* q;  // [B][q_stride]: H_q rows of D
+  int64_t q_stride;
+  const int32_t* len;
+  int B;
+  int G;         // query heads per key head
+  int HB;        // blocks of 8 of them
+  int most;      // bound on the lengths
+  float scale_log2;
+  float* o_part;    // [slots][8][D], unnormalised
+  float2* ml_part;  // [slots][8]: (m in log2 units, l)
+  float* scores;    // [tile of a (sequence, key head)][G][64], log2 units, or null
+};
+
+__device__ __forceinline__ int c4_tiles(const DecParams& p, int b) {
+  return (c4_len(p.len, b, p.most) + kC4TileKeys - 1) / kC4TileKeys;
+}
+
+// Total tiles (per key head) over all sequences, and the sequence that holds
+// tile `x` of key-head rows' flattened list: every sequence b counts `per`
+// times its tiles.  All threads of the block call it.
+struct C4Find {
+  int64_t total;  // per * sum of tiles
+  int b;          // sequence of x (B when x lies behind the last)
+  int64_t before; // per * tiles of the sequences before b
+};
+__device__ __forceinline__ int64_t c4_total_tiles(const DecParams& p, int64_t* warp_sums, int64_t* mine_before,
+                                                  int64_t* mine) {
+  const int tid = static_cast<int>(threadIdx.x), n_thr = static_cast<int>(blockDim.x);
+  const int stripe = (p.B + n_thr - 1) / n_thr;
+  const int b0 = min(p.B, tid * stripe), b1 = min(p.B, b0 + stripe);
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += c4_tiles(p, b);
+  int64_t incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+    if ((tid & 31) >= off) incl += y;
+  }
+  if ((tid & 31) == 31) warp_sums[tid >> 5] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < n_thr / 32; ++w) {
+    if (w < (tid >> 5)) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  *mine_before = before + incl - sum;
+  *mine = sum;
+  return total;
+}
+// The sequence whose tiles hold tile y (0 <= y < total): the thread whose
+// stripe holds it walks the stripe and tells the block.
+__device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int64_t mine_before, int64_t mine, int* b_out,
+                                        int64_t* before_out) {
+  if (mine_before <= y && y < mine_before + mine) {
+    const int stripe = (p.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    int b = static_cast<int>(threadIdx.x) * stripe;
+    int64_t at = mine_before;
+    while (true) {
+      const int n = c4_tiles(p, b);
+      if (y < at + n) break;
+      at += n;
+      ++b;
+    }
+    *b_out = b;
+    *before_out = at;
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (kType == kFP16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Nibbles e and e + 4 of w as two values c - 8, exact.
+template <int kType>
+__device__ __forceinline__ uint32_t c4_pair(uint32_t w_shifted) {
+  uint32_t x, r;
+  if constexpr (kType == kFP16) {
+    x = (w_shifted & 0x000f000fu) | 0x64006400u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64086408u));
+  } else {
+    x = (w_shifted & 0x000f000fu) | 0x43004300u;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
+  }
+  return r;
+}
+
+// 8 x 8 matrix of 16-bit values across the warp, transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// What a warp holds of its 16 keys of one tile.  lane = 4r + c: K rows r and
+// r + 8 (words 2c, 2c + 1 of each channel group), V rows 2c, 2c + 1, 2c + 8,
+// 2c + 9 (word r of each group), and the (s, m) of keys r and r + 8.
+template <int D>
+struct C4Raw {
+  static constexpr int kGroups = D / kC4Group;
+  uint2 k[2][kGroups];
+  uint32_t v[4][kGroups];
+  uint32_t km[2][kGroups];
+  uint32_t vm[2][kGroups];
+};
+
+template <int D>
+__device__ __forceinline__ void c4_load(C4Raw<D>& t, const Cache4& cc, int64_t row_base, int key0, int n, int r,
+                                        int c) {
+  constexpr int kG = D / kC4Group;
+  // keys past the end read the last one again: they are masked, and nothing
+  // is read that was never written
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t at = row_base + min(key0 + r + 8 * i, n - 1);
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      t.k[i][g] = __ldg(reinterpret_cast<const uint2*>(cc.k + at * (D / 2) + g * 32) + c);
+      t.km[i][g] = __ldg(cc.km + at * kG + g);
+      t.vm[i][g] = __ldg(cc.vm + at * kG + g);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t at = row_base + min(key0 + 2 * c + (i & 1) + 8 * (i >> 1), n - 1);
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+      t.v[i][g] = __ldg(reinterpret_cast<const uint32_t*>(cc.v + at * (D / 2) + g * 32) + r);
+  }
+}
+
+// kFine: P.V with each p*s split into two bf16 terms (fp16 results need more
+// than bf16's 8 bits; fp16 itself has not the range for p*s).
+template <int D, int kType, bool kWeight>
+__global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
+    attn_cache4_decode_kernel(const DecParams p) {
+  constexpr int kG = D / kC4Group;
+  constexpr bool kFine = kType == kFP16;
+  constexpr int kWarps = kC4DecThreads / 32;
+  __shared__ __align__(16) float o_s[kWarps][kC4Heads][D + 4];
+  __shared__ float2 ml_s[kWarps][kC4Heads];
+  __shared__ int64_t sums_s[kWarps];
+  __shared__ int64_t before_s;
+  __shared__ int b_s;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  grid_dependency_wait();
+  int64_t mine_before, mine;
+  const int rows_per_b = p.c.H * p.HB;
+  const int64_t total = c4_total_tiles(p, sums_s, &mine_before, &mine) * rows_per_b;
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  int64_t x = static_cast<int64_t>(blockIdx.x) * share;
+  const int64_t x_end = x + share < total ? x + share : total;
+  if (x >= x_end) {
+    grid_launch_dependents();
+    return;
+  }
+  c4_find(p, x / rows_per_b, mine_before, mine, &b_s, &before_s);
+  __syncthreads();
+  int b = b_s;
+  int64_t before = before_s * rows_per_b;  // list index of sequence b's first tile
+  while (x < x_end) {
+    const int n = c4_len(p.len, b, p.most);
+    const int nt = (n + kC4TileKeys - 1) / kC4TileKeys;
+    if (x >= before + static_cast<int64_t>(nt) * rows_per_b) {
+      before += static_cast<int64_t>(nt) * rows_per_b;
+      ++b;
+      continue;
+    }
+    const int in_b = static_cast<int>((x - before) / nt);  // key head and head block
+    const int t0 = static_cast<int>((x - before) % nt);
+    const int t1 = static_cast<int>(x_end - x < nt - t0 ? t0 + (x_end - x) : nt);
+    const int h = in_b / p.HB, hb = in_b % p.HB;
+    const int heads = min(kC4Heads, p.G - hb * kC4Heads);
+
+    // Q of head r of the block, in the channel order of the K words.
+    uint32_t q[kG][4][2];
+    float qsum[kG][2];
+    {
+      const bool there = r < heads;
+      const uint16_t* qr =
+          p.q + b * p.q_stride + static_cast<int64_t>(h * p.G + hb * kC4Heads + (there ? r : 0)) * D;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        float sum = 0.f;
+        const uint4* src = reinterpret_cast<const uint4*>(qr + g * kC4Group + c * 16);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {  // the 8 channels of one word
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (there) raw = __ldg(src + w);
+          const uint32_t e[4] = {raw.x, raw.y, raw.z, raw.w};  // channels (0,1) (2,3) (4,5) (6,7)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_16x2<kType>(e[i]);
+            sum += f.x + f.y;
+          }
+          // pairs (e, e + 4)
+          q[g][2 * w][0] = __byte_perm(e[0], e[2], 0x5410);
+          q[g][2 * w][1] = __byte_perm(e[0], e[2], 0x7632);
+          q[g][2 * w + 1][0] = __byte_perm(e[1], e[3], 0x5410);
+          q[g][2 * w + 1][1] = __byte_perm(e[1], e[3], 0x7632);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qsum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);      // of head 2c
+        qsum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);  // of head 2c + 1
+      }
+    }
+
+    float m_ref[2] = {-INFINITY, -INFINITY};  // reference of p, heads 2c and 2c + 1
+    float l[2] = {0.f, 0.f};                  // this lane's share of the sums
+    float bias[kG][2];                        // this lane's share of sum p (m + 8 s)
+    float o[kG][4][4];                        // O^T: channels 64g + 8r + t (+ 4), heads 2c, 2c + 1
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      bias[g][0] = bias[g][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[g][t][e] = 0.f;
+    }
+    const int64_t row_base = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
+    // scores of (sequence, key head): its tiles in list order without the head blocks
+    float* const score_row =
+        kWeight ? p.scores + ((before / p.HB + static_cast<int64_t>(h) * nt) * p.G + hb * kC4Heads * 1) * kC4TileKeys
+                : nullptr;
+
+    C4Raw<D> cur, nxt;
+    c4_load<D>(cur, p.c, row_base, t0 * kC4TileKeys + warp * 16, n, r, c);
+    for (int t = t0; t < t1; ++t) {
+      const int key0 = t * kC4TileKeys + warp * 16;
+      if (t + 1 < t1) c4_load<D>(nxt, p.c, row_base, key0 + kC4TileKeys, n, r, c);
+      if (key0 < n) {  // a warp wholly past the end has nothing to add
+        float xs[4] = {0.f, 0.f, 0.f, 0.f};  // keys r, r, r + 8, r + 8; heads 2c, 2c + 1
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t wa = w ? cur.k[0][g].y : cur.k[0][g].x, wb = w ? cur.k[1][g].y : cur.k[1][g].x;
+            // nibbles (0,4), (1,5) against q's slots of (0,4), (1,5); then (2,6), (3,7)
+            mma_16816<kType>(d, c4_pair<kType>(wa), c4_pair<kType>(wb), c4_pair<kType>(wa >> 4),
+                             c4_pair<kType>(wb >> 4), q[g][2 * w][0], q[g][2 * w][1]);
+            mma_16816<kType>(d, c4_pair<kType>(wa >> 8), c4_pair<kType>(wb >> 8), c4_pair<kType>(wa >> 12),
+                             c4_pair<kType>(wb >> 12), q[g][2 * w + 1][0], q[g][2 * w + 1][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float s = bf16_lo(cur.km[i][g]), mm = fmaf(8.f, s, bf16_hi(cur.km[i][g]));
+            xs[2 * i] = fmaf(s, d[2 * i], fmaf(mm, qsum[g][0], xs[2 * i]));
+            xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(mm, qsum[g][1], xs[2 * i + 1]));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xs[e] *= p.scale_log2;
+        if (key0 + 16 > n) {
+          if (key0 + r >= n) xs[0] = xs[1] = -INFINITY;
+          if (key0 + r + 8 >= n) xs[2] = xs[3] = -INFINITY;
+        }
+        if constexpr (kWeight) {
+          float* dst = score_row + static_cast<int64_t>(t) * p.G * kC4TileKeys + warp * 16 + r;
+          if (2 * c < heads) {
+            dst[2 * c * kC4TileKeys] = xs[0];
+            dst[2 * c * kC4TileKeys + 8] = xs[2];
+          }
+          if (2 * c + 1 < heads) {
+            dst[(2 * c + 1) * kC4TileKeys] = xs[1];
+            dst[(2 * c + 1) * kC4TileKeys + 8] = xs[3];
+          }
+        }
+        // A new reference only where a score exceeds the old one by 2^8: p
+        // stays below 2^8, O / l does not depend on the reference, and most
+        // tiles need one vote instead of a reduction and a rescale.
+        const bool grow = fmaxf(xs[0], xs[2]) > m_ref[0] + kRescaleLog2 || fmaxf(xs[1], xs[3]) > m_ref[1] + kRescaleLog2;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(xs[e], xs[2 + e]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float to = fmaxf(top, m_ref[e]);
+            const float a = to == -INFINITY ? 1.f : ex2_approx(m_ref[e] - to);
+            m_ref[e] = to;
+            l[e] *= a;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              bias[g][e] *= a;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                o[g][u][e] *= a;
+                o[g][u][2 + e] *= a;
+              }
+            }
+          }
+        }
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m_ref[e & 1] == -INFINITY ? 0.f : m_ref[e & 1];
+          pr[e] = ex2_approx(xs[e] - ref);
+          l[e & 1] += pr[e];
+        }
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          uint32_t pb[2], pl[2];  // P^T as the B operand: keys 0-7 and 8-15
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float s = bf16_lo(cur.vm[i][g]), mm = fmaf(8.f, s, bf16_hi(cur.vm[i][g]));
+            const float p0 = pr[2 * i] * s, p1 = pr[2 * i + 1] * s;
+            bias[g][0] = fmaf(pr[2 * i], mm, bias[g][0]);
+            bias[g][1] = fmaf(pr[2 * i + 1], mm, bias[g][1]);
+            const uint32_t hi = pack_bf16x2(p0, p1);
+            pb[i] = movmatrix_trans(hi);
+            if constexpr (kFine) pl[i] = movmatrix_trans(pack_bf16x2(p0 - bf16_lo(hi), p1 - bf16_hi(hi)));
+          }
+          // words of keys (2c, 2c + 1) and (2c + 8, 2c + 9): channels 0-3 and 4-7 side by side
+          const uint32_t a_lo = __byte_perm(cur.v[0][g], cur.v[1][g], 0x5410);
+          const uint32_t a_hi = __byte_perm(cur.v[0][g], cur.v[1][g], 0x7632);
+          const uint32_t b_lo = __byte_perm(cur.v[2][g], cur.v[3][g], 0x5410);
+          const uint32_t b_hi = __byte_perm(cur.v[2][g], cur.v[3][g], 0x7632);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t a0 = c4_pair<kBF16>(a_lo >> (4 * u)), a1 = c4_pair<kBF16>(a_hi >> (4 * u));
+            const uint32_t a2 = c4_pair<kBF16>(b_lo >> (4 * u)), a3 = c4_pair<kBF16>(b_hi >> (4 * u));
+            mma_16816<kBF16>(o[g][u], a0, a1, a2, a3, pb[0], pb[1]);
+            if constexpr (kFine) mma_16816<kBF16>(o[g][u], a0, a1, a2, a3, pl[0], pl[1]);
+          }
+        }
+      }
+      cur = nxt;
+    }
+
+    // Join the four warps: statistics over the lanes of a head, then O
+    // relative to the segment's own maximum.
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) bias[g][e] += __shfl_xor_sync(0xffffffffu, bias[g][e], off);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o_s[warp][2 * c + (e & 1)][g * kC4Group + 8 * r + u + 4 * (e >> 1)] = o[g][u][e] + bias[g][e & 1];
+    if (r == 0) {
+      ml_s[warp][2 * c] = make_float2(m_ref[0], l[0]);
+      ml_s[warp][2 * c + 1] = make_float2(m_ref[1], l[1]);
+    }
+    __syncthreads();
+    const int64_t slot = blockIdx.x + static_cast<int64_t>(b) * rows_per_b + in_b;
+    for (int i = tid; i < heads * D; i += kC4DecThreads) {
+      const int hd = i / D, d = i % D;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_s[w][hd].x);
+      float sum = 0.f, ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float a = top == -INFINITY ? 0.f : ex2_approx(ml_s[w][hd].x - top);
+        sum = fmaf(a, o_s[w][hd][d], sum);
+        ls = fmaf(a, ml_s[w][hd].y, ls);
+      }
+      p.o_part[(slot * kC4Heads + hd) * D + d] = sum;
+      if (d == 0) p.ml_part[slot * kC4Heads + hd] = make_float2(top, ls);
+    }
+    __syncthreads();
+    x += t1 - t0;
+  }
+  grid_launch_dependents();
+}
+
+struct DecMergeParams {
+  DecParams d;
+  int dec_grid;  // CTAs of the decode kernel: the shares
+  uint16_t* o;   // [B][H*G][D]
+  float* lse;    // [B][H*G]
+  const float* w_in;
+  float* w_out;  // [B][H][cap]
+};
+
+constexpr int kC4MergeThreads = 256;
+constexpr int kC4MergeTiles = 4;  // tiles of weights one block takes at a time
+
+// The partials of list rows: row (b, in_b) owns tiles [first, first + nt) of
+// the list and was cut where the shares end.
+struct C4Parts {
+  int first, count;  // CTAs that hold a segment of it
+};
+__device__ __forceinline__ C4Parts c4_parts(int64_t first_tile, int nt, int64_t share) {
+  C4Parts r;
+  r.first = static_cast<int>(first_tile / share);
+  r.count = nt == 0 ? 0 : static_cast<int>((first_tile + nt - 1) / share) - r.first + 1;
+  return r;
+}
+
+// Joins the partials of every (sequence, query head) into O and LSE, and adds
+// each entry's attention weight, summed over the heads of its group, where
+// the scores were kept.
+template <int D, int kType, bool kWeight>
+__global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(const DecMergeParams m) {
+  constexpr int kWarps = kC4MergeThreads / 32;
+  constexpr int kPer = D / 32;
+  const DecParams& p = m.d;
+  __shared__ int64_t sums_s[kWarps];
+  __shared__ int64_t before_s;
+  __shared__ int b_s;
+  __shared__ float lse_s[128];
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int64_t mine_before, mine;
+  const int rows_per_b = p.c.H * p.HB;
+  const int64_t tiles = c4_total_tiles(p, sums_s, &mine_before, &mine);
+  const int64_t share = (tiles * rows_per_b + m.dec_grid - 1) / m.dec_grid;
+
+  // O and LSE: a block takes a sequence, a warp one of its query heads.
+  // (Blocks own sequences so that the tile counts before them are found once.)
+  const int hq = p.c.H * p.G;
+  const int per_b = (hq + kWarps - 1) / kWarps;
+  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * per_b; u += gridDim.x) {
+    const int b = static_cast<int>(u / per_b);
+    const int head = static_cast<int>(u % per_b) * kWarps + warp;
+    // tiles before sequence b: its stripe's owner knows
+    const int stripe = (p.B + kC4MergeThreads - 1) / kC4MergeThreads;
+    if (b / stripe == tid) {
+      int64_t at = mine_before;
+      for (int i = tid * stripe; i < b; ++i) at += c4_tiles(p, i);
+      before_s = at;
+    }
+    __syncthreads();
+    const int64_t before = before_s * rows_per_b;
+    __syncthreads();
+    if (head >= hq) continue;
+    const int h = head / p.G, g = head % p.G, hb = g / kC4Heads;
+    const int in_b = h * p.HB + hb;
+    const int nt = c4_tiles(p, b);
+    const C4Parts cut = c4_parts(before + static_cast<int64_t>(in_b) * nt, nt, share > 0 ? share : 1);
+    const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
+    const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
+    const float* op = p.o_part + (slot0 * kC4Heads + g % kC4Heads) * D + lane * kPer;
+    float top = -INFINITY;
+    for (int i = lane; i < cut.count; i += 32) top = fmaxf(top, __ldg(&ml[static_cast<int64_t>(i) * kC4Heads].x));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float acc[kPer], ls = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < cut.count; i0 += 32) {
+      float a = 0.f;
+      if (i0 + lane < cut.count) {
+        const float2 f = __ldg(&ml[static_cast<int64_t>(i0 + lane) * kC4Heads]);
+        a = top == -INFINITY ? 0.f : ex2_approx(f.x - top);
+        ls = fmaf(a, f.y, ls);
+      }
+      const int cnt = min(32, cut.count - i0);
+#pragma unroll 4
+      for (int j = 0; j < cnt; ++j) {
+        const float w = __shfl_sync(0xffffffffu, a, j);
+        const float* src = op + static_cast<int64_t>(i0 + j) * kC4Heads * D;
+        if constexpr (kPer == 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(src));
+          acc[0] = fmaf(w, f.x, acc[0]);
+          acc[1] = fmaf(w, f.y, acc[1]);
+          acc[2] = fmaf(w, f.z, acc[2]);
+          acc[3] = fmaf(w, f.w, acc[3]);
+        } else {
+          const float2 f = __ldg(reinterpret_cast<const float2*>(src));
+          acc[0] = fmaf(w, f.x, acc[0]);
+          acc[1] = fmaf(w, f.y, acc[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+    const float inv = cut.count == 0 ? 0.f : 1.f / ls;
+    const int64_t row = static_cast<int64_t>(b) * hq + head;
+    uint16_t* dst = m.o + row * D + lane * kPer;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_16x2<kType>(acc[0] * inv, acc[1] * inv), pack_16x2<kType>(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack_16x2<kType>(acc[0] * inv, acc[1] * inv);
+    if (lane == 0) m.lse[row] = cut.count == 0 ? -INFINITY : (top + log2f(ls)) * kLn2;
+  }
+
+  if constexpr (kWeight) {
+    // Weights: the tiles of every (sequence, key head), kC4MergeTiles at a
+    // time; a chunk may cross from one (sequence, key head) into the next, so
+    // it is walked in pieces.
+    const int64_t all = tiles * p.c.H;
+    for (int64_t y = static_cast<int64_t>(blockIdx.x) * kC4MergeTiles; y < all;
+         y += static_cast<int64_t>(gridDim.x) * kC4MergeTiles) {
+      const int64_t y_end = y + kC4MergeTiles < all ? y + kC4MergeTiles : all;
+      __syncthreads();
+      c4_find(p, y / p.c.H, mine_before, mine, &b_s, &before_s);
+      __syncthreads();
+      int b = b_s;
+      int64_t before = before_s * p.c.H;
+      int64_t z = y;
+      while (z < y_end) {
+        const int n = c4_len(p.len, b, p.most);
+        const int nt = (n + kC4TileKeys - 1) / kC4TileKeys;
+        if (z >= before + static_cast<int64_t>(nt) * p.c.H) {
+          before += static_cast<int64_t>(nt) * p.c.H;
+          ++b;
+          continue;
+        }
+        const int h = static_cast<int>((z - before) / nt), t0 = static_cast<int>((z - before) % nt);
+        const int t1 = static_cast<int>(y_end - z < nt - t0 ? t0 + (y_end - z) : nt);
+        // log2 of the sum of every head of the group, a warp a head
+        for (int g = warp; g < p.G; g += kWarps) {
+          const int in_b = h * p.HB + g / kC4Heads;
+          const C4Parts cut = c4_parts(before * p.HB + static_cast<int64_t>(in_b) * nt, nt, share);
+          const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
+          const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
+          float top = -INFINITY;
+          for (int i = lane; i < cut.count; i += 32) top = fmaxf(top, __ldg(&ml[static_cast<int64_t>(i) * kC4Heads].x));
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          float ls = 0.f;
+          for (int i = lane; i < cut.count; i += 32) {
+            const float2 f = __ldg(&ml[static_cast<int64_t>(i) * kC4Heads]);
+            ls = fmaf(top == -INFINITY ? 0.f : ex2_approx(f.x - top), f.y, ls);
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+          if (lane == 0) lse_s[g] = top + log2f(ls);
+        }
+        __syncthreads();
+        const float* sc = p.scores + (before + static_cast<int64_t>(h) * nt) * p.G * kC4TileKeys;
+        const int64_t at0 = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
+        for (int i = t0 * kC4TileKeys + tid; i < min(t1 * kC4TileKeys, n); i += kC4MergeThreads) {
+          const float* src = sc + static_cast<int64_t>(i / kC4TileKeys) * p.G * kC4TileKeys + i % kC4TileKeys;
+          float w = 0.f;
+          for (int g = 0; g < p.G; ++g) w += ex2_approx(__ldg(src + g * kC4TileKeys) - lse_s[g]);
+          m.w_out[at0 + i] = m.w_in[at0 + i] + w;
+        }
+        __syncthreads();
+        z += t1 - t0;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Eviction by accumulated attention weight
+// ---------------------------------------------------------------------------
+//
+// Of the n entries of one (sequence, key head), `left` = min(n, budget) stay:
+// first the protected ones (position > newest position - recent), then those
+// of the highest weight, ties to the lower slot.  Kept entries at slots >=
+// left move into the slots < left of the others, the i-th of the first to the
+// i-th of the second.  So an entry moves at most once, every source lies at or
+// behind `left` and every target before it, and nothing is read that the call
+// writes.
+//
+// One thread-block cluster per (sequence, key head): each CTA holds a slice of
+// the slots' rank keys in shared memory.  The left-th largest key is found by
+// a radix select, 8 bits a round, most significant first, over histograms
+// that the CTAs add up through distributed shared memory; counts of ties,
+// holes and movers before each slice come the same way.  Every key is read
+// from HBM once, whatever the budget.
+
+constexpr int kC4EvictThreads = 512;
+constexpr int kC4EvictCluster = 8;             // CTAs of a cluster at most
+constexpr int kC4EvictSmemKeys = 48 * 1024;    // keys a CTA can hold in shared memory
+
+struct EvictParams {
+  Cache4 c;
+  const float* w_in;
+  const int32_t* p_in;
+  const int32_t* len;
+  float* w_out;
+  int32_t* p_out;
+  int32_t* len_out;  // null: another launch writes the lengths
+  int most;          // bound on the lengths
+  int budget;
+  int recent;
+  int smem_keys;     // keys that fit into this launch's shared memory
+  uint32_t* keys;    // [B*H][most] for slices that do not, or null
+  int32_t* moves;    // [B*H][2][list]: holes, then movers
+  int list;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// 32-bit load from the same shared-memory variable of another CTA of the cluster
+__device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Order of the weights as unsigned integers: NaN above +inf, -0 equal to +0;
+// the protected entries above them all.
+constexpr uint32_t kC4Protected = 0xffffffffu;
+__device__ __forceinline__ uint32_t c4_rank_key(float w) {
+  if (w != w) return 0xfffffffeu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Sum over the block of (a, b) before this thread, and the totals.
+__device__ __forceinline__ uint2 block_scan2(uint2 v, uint2* warp_s, uint2* total) {
+  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+  uint2 incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, off), y = __shfl_up_sync(0xffffffffu, incl.y, off);
+    if (lane >= off) {
+      incl.x += x;
+      incl.y += y;
+    }
+  }
+  __syncthreads();  // warp_s is free again
+  if (lane == 31) warp_s[warp] = incl;
+  __syncthreads();
+  uint2 before = make_uint2(incl.x - v.x, incl.y - v.y), all = make_uint2(0, 0);
+  for (int w = 0; w < kC4EvictThreads / 32; ++w) {
+    const uint2 s = warp_s[w];
+    if (w < warp) {
+      before.x += s.x;
+      before.y += s.y;
+    }
+    all.x += s.x;
+    all.y += s.y;
+  }
+  *total = all;
+  return before;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kC4EvictThreads) attn_cache4_evict_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) uint32_t smem_keys[];
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t share[4];  // what the other CTAs read: newest, ties, holes, movers
+  __shared__ uint32_t found[2];  // digit, entries still to take
+  __shared__ uint2 warp_s[kC4EvictThreads / 32];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const uint32_t rank = cluster_rank(), R = cluster_size();
+  const int64_t bh = blockIdx.x / R;
+  const int b = static_cast<int>(bh / p.c.H);
+  grid_dependency_wait();
+  const int n = c4_len(p.len, b, p.most);
+  const int left = min(n, p.budget);
+  const int64_t base = bh * p.c.cap;
+  if (p.len_out != nullptr && bh % p.c.H == 0 && rank == 0 && tid == 0) p.len_out[b] = left;
+  const int slice = (n + static_cast<int>(R) - 1) / static_cast<int>(R);
+  const int i0 = min(n, static_cast<int>(rank) * slice), i1 = min(n, i0 + slice), mine = i1 - i0;
+  const bool copy_w = p.w_out != p.w_in, copy_p = p.p_out != p.p_in;
+  if (n <= p.budget) {  // every entry stays where it is (the same for the whole cluster)
+    for (int i = i0 + tid; i < i1; i += kC4EvictThreads) {
+      if (copy_w) p.w_out[base + i] = p.w_in[base + i];
+      if (copy_p) p.p_out[base + i] = p.p_in[base + i];
+    }
+    grid_launch_dependents();
+    return;
+  }
+  uint32_t* const key = slice <= p.smem_keys ? smem_keys : p.keys + bh * p.most + i0;
+
+  // Rank keys of the slice, and the newest position.
+  int newest = INT_MIN;
+  for (int i = tid; i < mine; i += kC4EvictThreads) {
+    newest = max(newest, p.p_in[base + i0 + i]);
+    key[i] = c4_rank_key(p.w_in[base + i0 + i]);
+  }
+  newest = __reduce_max_sync(0xffffffffu, newest);
+  if (lane == 0) warp_s[tid >> 5].x = static_cast<uint32_t>(newest);
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kC4EvictThreads / 32; ++w) newest = max(newest, static_cast<int>(warp_s[w].x));
+    share[0] = static_cast<uint32_t>(newest);
+  }
+  cluster_sync_all();
+  newest = INT_MIN;
+  for (uint32_t q = 0; q < R; ++q) newest = max(newest, static_cast<int>(ld_cluster_u32(&share[0], q)));
+  if (p.recent > 0) {
+    const int64_t old = static_cast<int64_t>(newest) - p.recent;
+    for (int i = tid; i < mine; i += kC4EvictThreads)
+      if (p.p_in[base + i0 + i] > old) key[i] = kC4Protected;
+  }
+
+  // The left-th largest key.
+  uint32_t prefix = 0u, take = static_cast<uint32_t>(left);
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int d = tid; d < 256; d += kC4EvictThreads) hist[d] = 0u;
+    __syncthreads();
+    const uint32_t seen = shift == 24 ? 0u : ~0u << (shift + 8);
+    for (int i = tid; i < mine; i += kC4EvictThreads) {
+      const uint32_t k = key[i];
+      if ((k & seen) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    }
+    cluster_sync_all();
+    if (tid < 32) {  // digits from the top: lane j has 255 - 8j .. 248 - 8j
+      uint32_t cnt[8], sum = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        cnt[e] = 0u;
+        for (uint32_t q = 0; q < R; ++q) cnt[e] += ld_cluster_u32(&hist[255 - 8 * lane - e], q);
+        sum += cnt[e];
+      }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      uint32_t before = incl - sum;
+      if (before < take && take <= incl) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (before < take && take <= before + cnt[e]) {
+            found[0] = static_cast<uint32_t>(255 - 8 * lane - e);
+            found[1] = take - before;
+          }
+          before += cnt[e];
+        }
+      }
+    }
+    cluster_sync_all();  // found is set; every CTA has read the histograms
+    prefix |= found[0] << shift;
+    take = found[1];
+  }
+
+  // Kept: keys above `prefix`, and the first `take` equal to it.  A thread
+  // walks consecutive slots (an odd count: no bank conflicts).
+  const int per = ((mine + kC4EvictThreads - 1) / kC4EvictThreads) | 1;
+  const int s0 = min(mine, tid * per), s1 = min(mine, s0 + per);
+  uint2 v = make_uint2(0, 0), all;
+  for (int i = s0; i < s1; ++i) v.x += key[i] == prefix;
+  const uint2 eq = block_scan2(v, warp_s, &all);
+  if (tid == 0) share[1] = all.x;
+  cluster_sync_all();
+  uint32_t eq_rank = eq.x;
+  for (uint32_t q = 0; q < rank; ++q) eq_rank += ld_cluster_u32(&share[1], q);
+  v = make_uint2(0, 0);
+  for (int i = s0; i < s1; ++i) {
+    const uint32_t k = key[i];
+    bool keep = k > prefix;
+    if (k == prefix) keep = eq_rank++ < take;
+    key[i] = keep;
+    v.x += !keep && i0 + i < left;  // a hole
+    v.y += keep && i0 + i >= left;  // a mover
+  }
+  const uint2 at = block_scan2(v, warp_s, &all);
+  if (tid == 0) {
+    share[2] = all.x;
+    share[3] = all.y;
+  }
+  cluster_sync_all();
+  uint32_t hole = at.x, mover = at.y, n_moves = 0u;
+  for (uint32_t q = 0; q < R; ++q) {
+    const uint32_t x = ld_cluster_u32(&share[2], q);
+    if (q < rank) {
+      hole += x;
+      mover += ld_cluster_u32(&share[3], q);
+    }
+    n_moves += x;
+  }
+  int32_t* const holes = p.moves + bh * 2 * p.list;
+  int32_t* const movers = holes + p.list;
+  for (int i = s0; i < s1; ++i) {
+    const bool keep = key[i] != 0u;
+    if (!keep && i0 + i < left) holes[hole++] = i0 + i;
+    if (keep && i0 + i >= left) movers[mover++] = i0 + i;
+  }
+  if (copy_w || copy_p) {
+    __syncthreads();
+    for (int i = tid; i < mine && i0 + i < left; i += kC4EvictThreads) {
+      if (key[i] == 0u) continue;
+      if (copy_w) p.w_out[base + i0 + i] = p.w_in[base + i0 + i];
+      if (copy_p) p.p_out[base + i0 + i] = p.p_in[base + i0 + i];
+    }
+  }
+  cluster_sync_all();  // the lists are written; no CTA reads another's shared memory any more
+  grid_launch_dependents();
+
+  // The moves, 16 bytes a lane: half of a move's lanes take K, half V.
+  constexpr int kLanes = D / 16;
+  constexpr int kWords = D / 32;  // 16-byte words of a row
+  const int part = tid % kLanes;
+  const bool is_v = part >= kWords;
+  uint8_t* const codes = is_v ? p.c.v : p.c.k;
+  uint32_t* const meta = is_v ? p.c.vm : p.c.km;
+  for (uint32_t m = rank * (kC4EvictThreads / kLanes) + tid / kLanes; m < n_moves;
+       m += R * (kC4EvictThreads / kLanes)) {
+    const int64_t to = base + __ldcg(holes + m), from = base + __ldcg(movers + m);
+    const uint4 x = *(reinterpret_cast<const uint4*>(codes + from * (D / 2)) + part % kWords);
+    *(reinterpret_cast<uint4*>(codes + to * (D / 2)) + part % kWords) = x;
+    if (part % kWords == 0) {
+#pragma unroll
+      for (int g = 0; g < D / kC4Group; ++g) meta[to * (D / kC4Group) + g] = meta[from * (D / kC4Group) + g];
+      if (is_v)
+        p.p_out[to] = p.p_in[from];
+      else
+        p.w_out[to] = p.w_in[from];
+    }
+  }
+}
+
+// Lengths after an eviction, where they take the place of the old ones: a
+// launch behind the one whose blocks read those.
+__global__ void attn_cache4_cut_kernel(int32_t* len, int B, int most, int budget) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < B;
+       b += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    len[b] = min(min(max(len[b], 0), most), budget);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+std::atomic<int> g_cache4_state[kMaxDevices];  // 1: shared-memory limits set
+
+attn_status_t prepare_cache4(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess) return ATTN_ERR_DEVICE;
+  const attn_status_t ps = prepare_device(*dev);
+  if (ps != ATTN_OK) return ps;
+  if (g_cache4_state[*dev].load(std::memory_order_acquire) == 0) {
+    if (cudaFuncSetAttribute(attn_cache4_evict_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kC4EvictSmemKeys * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_cache4_evict_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kC4EvictSmemKeys * 4) != cudaSuccess)
+      return ATTN_ERR_DEVICE;
+    g_cache4_state[*dev].store(1, std::memory_order_release);
+  }
+  *sms = g_dev_sms[*dev].load(std::memory_order_relaxed);
+  return ATTN_OK;
+}
+
+// The cache's own arguments (nothing is launched).
+attn_status_t check_cache4(const attn_cache4_t* c) {
+  if (c == nullptr || c->B < 1 || c->H_kv < 1 || c->capacity < 1) return ATTN_ERR_INVALID_ARG;
+  if (c->k_codes == nullptr || c->k_meta == nullptr || c->v_codes == nullptr || c->v_meta == nullptr ||
+      c->length == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (c->D != 64 && c->D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_meta, 4) || !aligned(c->v_meta, 4) ||
+      !aligned(c->length, 4) || !aligned(c->weight, 4) || !aligned(c->pos, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (static_cast<int64_t>(c->B) * c->H_kv > INT_MAX / 64) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+Cache4 cache4_of(const attn_cache4_t* c) {
+  Cache4 r;
+  r.k = static_cast<uint8_t*>(c->k_codes);
+  r.v = static_cast<uint8_t*>(c->v_codes);
+  r.km = static_cast<uint32_t*>(c->k_meta);
+  r.vm = static_cast<uint32_t*>(c->v_meta);
+  r.H = c->H_kv;
+  r.cap = c->capacity;
+  return r;
+}
+
+// Packed rows of K and V: sizes, strides, alignment to 8 elements.
+attn_status_t check_rows(const attn_cache4_t* c, const void* k, const void* v, int64_t rows, int64_t k_stride,
+                         int64_t v_stride, const int32_t* seq_start, int elem_bytes) {
+  if (rows < 0) return ATTN_ERR_INVALID_ARG;
+  if (seq_start == nullptr && rows != c->B) return ATTN_ERR_INVALID_ARG;
+  if (rows > 0 && (k == nullptr || v == nullptr)) return ATTN_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(c->H_kv) * c->D;
+  if (k_stride < row || v_stride < row) return ATTN_ERR_INVALID_ARG;
+  const int64_t unit = 16 / elem_bytes;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % unit != 0 || v_stride % unit != 0 || !aligned(seq_start, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (rows > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+template <int D>
+unsigned rows_grid(int64_t rows, int H, int sms) {
+  const int64_t units = (rows + kC4BlockRows<D> - 1) / kC4BlockRows<D> * H;
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(units, static_cast<int64_t>(sms) * 64)));
+}
+
+// Workspace of a decode call: partial O, partial (m, l), and with weights the
+// scores of every tile.
+struct DecLayout {
+  int64_t slots, o_bytes, ml_bytes, score_bytes;
+  int grid;
+};
+DecLayout decode_layout(int B, int H_q, int H_kv, int D, int max_len, bool weight, int sms) {
+  const int64_t G = H_q / H_kv, HB = (G + kC4Heads - 1) / kC4Heads;
+  const int64_t rows = static_cast<int64_t>(B) * H_kv * HB;
+  const int64_t tiles = (static_cast<int64_t>(max_len) + kC4TileKeys - 1) / kC4TileKeys;
+  DecLayout l;
+  l.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows * tiles, static_cast<int64_t>(sms) * kC4DecCtasPerSm)));
+  l.slots = l.grid + rows;
+  l.o_bytes = l.slots * kC4Heads * D * 4;
+  l.ml_bytes = l.slots * kC4Heads * 8;
+  l.score_bytes = weight ? static_cast<int64_t>(B) * H_kv * tiles * G * kC4TileKeys * 4 : 0;
+  return l;
+}
+
+template <int D, int kType>
+attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(m.dec_grid));
+  const bool weight = m.w_out != nullptr;
+  cudaError_t e = weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true>, grid, dim3(kC4DecThreads), 0, stream, m.d)
+                         : launch_pdl(attn_cache4_decode_kernel<D, kType, false>, grid, dim3(kC4DecThreads), 0, stream, m.d);
+  if (e != cudaSuccess) return ATTN_ERR_LAUNCH;
+  const int64_t heads = static_cast<int64_t>(m.d.B) * m.d.c.H * m.d.G;
+  const int64_t tiles = (static_cast<int64_t>(m.d.most) + kC4TileKeys - 1) / kC4TileKeys * m.d.B * m.d.c.H;
+  int64_t blocks = (heads + kC4MergeThreads / 32 - 1) / (kC4MergeThreads / 32);
+  if (weight) blocks = std::max(blocks, (tiles + kC4MergeTiles - 1) / kC4MergeTiles);
+  const dim3 mg(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 8)));
+  e = weight ? launch_pdl(attn_cache4_merge_kernel<D, kType, true>, mg, dim3(kC4MergeThreads), 0, stream, m)
+             : launch_pdl(attn_cache4_merge_kernel<D, kType, false>, mg, dim3(kC4MergeThreads), 0, stream, m);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+// CTAs of an eviction's clusters: enough to give the GPU about two CTAs an SM,
+// and slices of at least 1024 entries; or as many as hold the keys in shared
+// memory.
+int evict_cluster(int64_t BH, int max_len) {
+  int R = 1;
+  while (R < kC4EvictCluster && ((BH * R < kC4WorkspaceSms && max_len / (2 * R) >= 1024) || max_len > R * kC4EvictSmemKeys)) R *= 2;
+  return R;
+}
+int64_t evict_list(int max_len, int budget) {
+  return std::max<int64_t>(1, std::min<int64_t>(budget, static_cast<int64_t>(max_len) - budget));
+}
+// Whether some CTA's slice outgrows shared memory.
+bool evict_spills(int max_len, int R) { return (static_cast<int64_t>(max_len) + R - 1) / R > kC4EvictSmemKeys; }
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_cache4_append(const attn_cache4_t* cache, const void* k, const void* v, int64_t rows,
+                                 int64_t k_stride, int64_t v_stride, int dtype, const int32_t* seq_start,
+                                 const int32_t* first_pos, int32_t* length_out, void* stream) {
+  attn_status_t st = check_cache4(cache);
+  if (st != ATTN_OK) return st;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_UNSUPPORTED;
+  st = check_rows(cache, k, v, rows, k_stride, v_stride, seq_start, 2);
+  if (st != ATTN_OK) return st;
+  if (length_out == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(first_pos, 4) || !aligned(length_out, 4)) return ATTN_ERR_ALIGNMENT;
+  int dev = 0, sms = 0;
+  st = prepare_cache4(&dev, &sms);
+  if (st != ATTN_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Cache4 c = cache4_of(cache);
+  const Cache4Rows g{seq_start, cache->length, cache->B, rows, k_stride, v_stride};
+  const bool in_place = length_out == cache->length;
+  int32_t* const len_out = in_place ? nullptr : length_out;
+  const uint16_t* k16 = static_cast<const uint16_t*>(k);
+  const uint16_t* v16 = static_cast<const uint16_t*>(v);
+  const auto run = [&](auto kernel, unsigned grid) {
+    return launch_pdl(kernel, dim3(grid), dim3(kC4RowsThreads), 0, s, k16, v16, g, c, cache->weight, cache->pos, first_pos,
+                      len_out);
+  };
+  cudaError_t e;
+  if (cache->D == 64)
+    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<64, kBF16>, rows_grid<64>(rows, c.H, sms))
+                           : run(attn_cache4_append_kernel<64, kFP16>, rows_grid<64>(rows, c.H, sms));
+  else
+    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<128, kBF16>, rows_grid<128>(rows, c.H, sms))
+                           : run(attn_cache4_append_kernel<128, kFP16>, rows_grid<128>(rows, c.H, sms));
+  if (e == cudaSuccess && in_place)
+    e = launch_pdl(attn_cache4_grow_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
+                   seq_start, length_out, cache->B, cache->capacity);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int64_t rows, int64_t k_stride,
+                               int64_t v_stride, int dtype, const int32_t* seq_start, const int32_t* first_slot,
+                               void* stream) {
+  attn_status_t st = check_cache4(cache);
+  if (st != ATTN_OK) return st;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16 && dtype != ATTN_FP32) return ATTN_ERR_UNSUPPORTED;
+  st = check_rows(cache, k, v, rows, k_stride, v_stride, seq_start, dtype == ATTN_FP32 ? 4 : 2);
+  if (st != ATTN_OK) return st;
+  if (!aligned(first_slot, 4)) return ATTN_ERR_ALIGNMENT;
+  if (rows == 0) return ATTN_OK;
+  int dev = 0, sms = 0;
+  st = prepare_cache4(&dev, &sms);
+  if (st != ATTN_OK) return st;
+  const Cache4 c = cache4_of(cache);
+  const Cache4Rows g{seq_start, first_slot, cache->B, rows, k_stride, v_stride};
+  const auto run = [&](auto kernel, unsigned grid) {
+    return launch_pdl(kernel, dim3(grid), dim3(kC4RowsThreads), 0, static_cast<cudaStream_t>(stream), k, v, g, c);
+  };
+  cudaError_t e;
+  if (cache->D == 64) {
+    const unsigned grid = rows_grid<64>(rows, c.H, sms);
+    e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<64, kBF16>, grid)
+        : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<64, kFP16>, grid)
+                             : run(attn_cache4_read_kernel<64, kFP32>, grid);
+  } else {
+    const unsigned grid = rows_grid<128>(rows, c.H, sms);
+    e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<128, kBF16>, grid)
+        : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<128, kFP16>, grid)
+                             : run(attn_cache4_read_kernel<128, kFP32>, grid);
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int max_len, int with_weight) {
+  if (B < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || H_q / H_kv > 128 || (D != 64 && D != 128) || max_len < 1)
+    return 0;
+  const DecLayout l = decode_layout(B, H_q, H_kv, D, max_len, with_weight != 0, kC4WorkspaceSms);
+  return static_cast<uint64_t>(l.o_bytes + l.ml_bytes + l.score_bytes);
+}
+
+attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int64_t q_stride, void* o, float* lse, int H_q,
+                                 int dtype, float scale, int max_len, const float* weight_in, float* weight_out,
+                                 void* workspace, uint64_t workspace_bytes, void* stream) {
+  attn_status_t st = check_cache4(cache);
+  if (st != ATTN_OK) return st;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_UNSUPPORTED;
+  if (q == nullptr || o == nullptr || lse == nullptr || workspace == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (H_q < cache->H_kv || H_q % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (H_q / cache->H_kv > 128) return ATTN_ERR_UNSUPPORTED;
+  if (q_stride < static_cast<int64_t>(H_q) * cache->D) return ATTN_ERR_INVALID_ARG;
+  if (max_len < 1 || max_len > cache->capacity) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if ((weight_in == nullptr) != (weight_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      !aligned(weight_in, 4) || !aligned(weight_out, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (workspace_bytes < attn_cache4_decode_workspace_bytes(cache->B, H_q, cache->H_kv, cache->D, max_len, weight_out != nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  st = prepare_cache4(&dev, &sms);
+  if (st != ATTN_OK) return st;
+  sms = std::min(sms, kC4WorkspaceSms);
+  const DecLayout l = decode_layout(cache->B, H_q, cache->H_kv, cache->D, max_len, weight_out != nullptr, sms);
+  DecMergeParams m;
+  m.d.c = cache4_of(cache);
+  m.d.q = static_cast<const uint16_t*>(q);
+  m.d.q_stride = q_stride;
+  m.d.len = cache->length;
+  m.d.B = cache->B;
+  m.d.G = H_q / cache->H_kv;
+  m.d.HB = (m.d.G + kC4Heads - 1) / kC4Heads;
+  m.d.most = max_len;
+  m.d.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  char* ws = static_cast<char*>(workspace);
+  m.d.o_part = reinterpret_cast<float*>(ws);
+  m.d.ml_part = reinterpret_cast<float2*>(ws + l.o_bytes);
+  m.d.scores = weight_out != nullptr ? reinterpret_cast<float*>(ws + l.o_bytes + l.ml_bytes) : nullptr;
+  m.dec_grid = l.grid;
+  m.o = static_cast<uint16_t*>(o);
+  m.lse = lse;
+  m.w_in = weight_in;
+  m.w_out = weight_out;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->D == 64)
+    return dtype == ATTN_BF16 ? launch_decode<64, kBF16>(m, sms, s) : launch_decode<64, kFP16>(m, sms, s);
+  return dtype == ATTN_BF16 ? launch_decode<128, kBF16>(m, sms, s) : launch_decode<128, kFP16>(m, sms, s);
+}
+
+uint64_t attn_cache4_evict_workspace_bytes(int B, int H_kv, int max_len, int budget) {
+  if (B < 1 || H_kv < 1 || max_len < 1 || budget < 1) return 0;
+  if (budget >= max_len) return 16;
+  const int64_t BH = static_cast<int64_t>(B) * H_kv;
+  const bool spills = evict_spills(max_len, evict_cluster(BH, max_len));
+  return static_cast<uint64_t>(BH * (2 * evict_list(max_len, budget) + (spills ? max_len : 0)) * 4);
+}
+
+attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int recent, int max_len, float* weight_out,
+                                int32_t* pos_out, int32_t* length_out, void* workspace, uint64_t workspace_bytes,
+                                void* stream) {
+  attn_status_t st = check_cache4(cache);
+  if (st != ATTN_OK) return st;
+  if (cache->weight == nullptr || cache->pos == nullptr || weight_out == nullptr || pos_out == nullptr ||
+      length_out == nullptr || workspace == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || recent > budget || max_len < 1 || max_len > cache->capacity) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(length_out, 4) || !aligned(workspace, 16))
+    return ATTN_ERR_ALIGNMENT;
+  if (workspace_bytes < attn_cache4_evict_workspace_bytes(cache->B, cache->H_kv, max_len, budget)) return ATTN_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  st = prepare_cache4(&dev, &sms);
+  if (st != ATTN_OK) return st;
+  const int64_t BH = static_cast<int64_t>(cache->B) * cache->H_kv;
+  const int R = evict_cluster(BH, max_len);
+  const bool in_place = length_out == cache->length;
+  EvictParams p;
+  p.c = cache4_of(cache);
+  p.w_in = cache->weight;
+  p.p_in = cache->pos;
+  p.len = cache->length;
+  p.w_out = weight_out;
+  p.p_out = pos_out;
+  p.len_out = in_place ? nullptr : length_out;
+  p.most = max_len;
+  p.budget = budget;
+  p.recent = recent;
+  p.list = budget < max_len ? static_cast<int>(evict_list(max_len, budget)) : 1;
+  p.moves = static_cast<int32_t*>(workspace);
+  const bool spills = budget < max_len && evict_spills(max_len, R);
+  p.keys = spills ? reinterpret_cast<uint32_t*>(p.moves + BH * 2 * p.list) : nullptr;
+  const int slice = (max_len + R - 1) / R;
+  p.smem_keys = std::min(slice, kC4EvictSmemKeys);
+  const size_t smem = budget < max_len ? static_cast<size_t>(p.smem_keys) * 4 : 16;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(R);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(BH * R));
+  cfg.blockDim = dim3(kC4EvictThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cache->D == 64 ? cudaLaunchKernelEx(&cfg, attn_cache4_evict_kernel<64>, p)
+                                 : cudaLaunchKernelEx(&cfg, attn_cache4_evict_kernel<128>, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess && in_place)
+    e = launch_pdl(attn_cache4_cut_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
+                   length_out, cache->B, max_len, budget);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -142,7 +142,8 @@ struct Params {
 
 // Read and cleared by attn_fwd_debug_status.  Bit 0: a bounded wait gave up.
 // Bit 1: the backward kernel found its dynamic shared memory off a 1024-byte
-// boundary and ran nothing.
+// boundary and ran nothing.  Bit 2: an append dropped entries for which a
+// 4-bit cache had no room.
 __device__ unsigned int g_attn_status = 0;
 
 namespace {
@@ -1801,6 +1802,7 @@ const char* attn_status_str(attn_status_t s) {
     case ATTN_ERR_LAUNCH: return "kernel launch failed";
     case ATTN_ERR_TIMEOUT: return "in-kernel wait timed out";
     case ATTN_ERR_DEVICE: return "CUDA device error";
+    case ATTN_ERR_CAPACITY: return "entries beyond a cache's capacity were dropped";
   }
   return "unknown status";
 }
@@ -2030,7 +2032,8 @@ attn_status_t attn_fwd_debug_status(void* stream) {
   if (cudaMemcpyFromSymbol(&word, g_attn_status, sizeof word) != cudaSuccess) return ATTN_ERR_DEVICE;
   if (word != 0u && cudaMemcpyToSymbol(g_attn_status, &zero, sizeof zero) != cudaSuccess) return ATTN_ERR_DEVICE;
   if (word & 2u) return ATTN_ERR_DEVICE;  // a kernel found its shared memory misaligned and did not run
-  return word != 0u ? ATTN_ERR_TIMEOUT : ATTN_OK;
+  if (word & 1u) return ATTN_ERR_TIMEOUT;
+  return word != 0u ? ATTN_ERR_CAPACITY : ATTN_OK;
 }
 
 attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
@@ -2042,3 +2045,9 @@ attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
 }
 
 }  // extern "C"
+
+// Serving: packed prompts with grouped heads, and the 4-bit K/V cache (device
+// code, host code and entry points of each in one file).
+#include "attn_types.cuh"
+#include "attn_varlen.cuh"
+#include "attn_cache4.cuh"
