@@ -297,7 +297,7 @@ uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int
  *
  *   k_codes, v_codes  uint8 [B][H_kv][capacity][D/2], 16-byte aligned: channel
  *                     2i in the low half of byte i, 2i + 1 in the high half
- *   k_meta, v_meta    bf16 [B][H_kv][capacity][D/64][2]: (s, m)
+ *   k_meta, v_meta    bf16 [B][H_kv][capacity][D/64][2], 8-byte aligned: (s, m)
  *   weight            fp32 [B][H_kv][capacity]: attention weight each entry has
  *                     received, or NULL where the call does not use it
  *   pos               int32 [B][H_kv][capacity]: position of each entry's token

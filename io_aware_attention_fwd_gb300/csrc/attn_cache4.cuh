@@ -251,8 +251,19 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 // through the tensor core as they are and the scales are applied to sums:
 //     <q, k_j>  = sum over groups of  s * <q, c - 8> + (m + 8 s) * sum q
 //     sum_j p_j v_j = sum_j (p_j s) (c - 8) + sum_j p_j (m + 8 s).
-// c - 8 is exact in bf16 and fp16: a code is ORed into the mantissa of 128
-// (bf16) or 1024 (fp16) and 136 or 1032 subtracted, two values at a time.
+// The products run in fp16 with fp32 sums, whatever the type of q and o:
+//   * c - 8 is exact.  A code is ORed into the mantissa of 1024: a low nibble
+//     gives 1024 + c, from which 1032 is subtracted; a high one, left where it
+//     is, gives 1024 + 16 c, which one fused multiply-add turns into c - 8.
+//     So two nibbles of a 16-bit half need one mask and one operation each, and
+//     one shift serves four of the eight.
+//   * A bf16 q is scaled by a power of two that brings its head's largest
+//     channel to 1 .. 2, which fp16 holds exactly down to 2^-14 of it and to
+//     2^-25 of it absolutely; the scale goes back into the logits.
+//   * p s is held relative to a power of two at or above every s the warp has
+//     met in that group of channels, times 2^7: at most 2^15, with 11 bits down
+//     to 2^-29 of the largest.  When a larger s comes, O is rescaled, as it is
+//     when the running maximum grows.
 //
 // mma.sync m16n8k16 serves here, with keys as the M rows of S^T = K Q^T, and
 // channels as the M rows of O^T = V^T P^T: the A operands are then the cache's
@@ -274,6 +285,7 @@ constexpr int kC4DecThreads = 128;  // 4 warps
 constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
 constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
 constexpr int kC4DecCtasPerSm = 4;
+constexpr int kC4RowCost = 6;       // tiles' worth of time that a row costs a CTA
 // A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
 // so that a size asked for on one device (or with none) holds on any.
 constexpr int kC4WorkspaceSms = 152;
@@ -297,21 +309,26 @@ __device__ __forceinline__ int c4_tiles(const DecParams& p, int b) {
   return (c4_len(p.len, b, p.most) + kC4TileKeys - 1) / kC4TileKeys;
 }
 
-// Total tiles (per key head) over all sequences, and the sequence that holds
-// tile `x` of key-head rows' flattened list: every sequence b counts `per`
-// times its tiles.  All threads of the block call it.
-struct C4Find {
-  int64_t total;  // per * sum of tiles
-  int b;          // sequence of x (B when x lies behind the last)
-  int64_t before; // per * tiles of the sequences before b
-};
-__device__ __forceinline__ int64_t c4_total_tiles(const DecParams& p, int64_t* warp_sums, int64_t* mine_before,
-                                                  int64_t* mine) {
+// The list that is cut into shares: each row (a sequence's key head, or block of
+// query heads) that has entries counts `cost` units, for its start and its end,
+// and one for each of its tiles.  (Without the fixed part, a CTA whose share held
+// eight one-token rows took three times as long as the others.)
+//
+// Before a sequence lie so many tiles and so many sequences with entries, per
+// row; both in one 64-bit number.
+constexpr int64_t kC4Tiles = (1ll << 40) - 1;
+__device__ __forceinline__ int64_t c4_count(int nt) { return nt + (nt > 0 ? 1ll << 40 : 0ll); }
+__device__ __forceinline__ int64_t c4_units(int64_t count, int cost) { return (count & kC4Tiles) + cost * (count >> 40); }
+__device__ __forceinline__ int c4_row_units(int nt, int cost) { return nt > 0 ? nt + cost : 0; }
+
+// Counts over all sequences, over those before this thread's stripe of them and
+// over its stripe.  All threads of the block call it.
+__device__ __forceinline__ int64_t c4_total(const DecParams& p, int64_t* warp_sums, int64_t* mine_before, int64_t* mine) {
   const int tid = static_cast<int>(threadIdx.x), n_thr = static_cast<int>(blockDim.x);
   const int stripe = (p.B + n_thr - 1) / n_thr;
   const int b0 = min(p.B, tid * stripe), b1 = min(p.B, b0 + stripe);
   int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += c4_tiles(p, b);
+  for (int b = b0; b < b1; ++b) sum += c4_count(c4_tiles(p, b));
   int64_t incl = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -329,18 +346,19 @@ __device__ __forceinline__ int64_t c4_total_tiles(const DecParams& p, int64_t* w
   *mine = sum;
   return total;
 }
-// The sequence whose tiles hold tile y (0 <= y < total): the thread whose
-// stripe holds it walks the stripe and tells the block.
-__device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int64_t mine_before, int64_t mine, int* b_out,
-                                        int64_t* before_out) {
-  if (mine_before <= y && y < mine_before + mine) {
+// The sequence with unit y (of one row's units; 0 <= y < their sum) and the
+// counts before it: the thread whose stripe holds it walks the stripe and
+// tells the block.
+__device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int cost, int64_t mine_before, int64_t mine,
+                                        int* b_out, int64_t* before_out) {
+  if (c4_units(mine_before, cost) <= y && y < c4_units(mine_before + mine, cost)) {
     const int stripe = (p.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
     int b = static_cast<int>(threadIdx.x) * stripe;
     int64_t at = mine_before;
     while (true) {
-      const int n = c4_tiles(p, b);
-      if (y < at + n) break;
-      at += n;
+      const int64_t next = at + c4_count(c4_tiles(p, b));
+      if (y < c4_units(next, cost)) break;
+      at = next;
       ++b;
     }
     *b_out = b;
@@ -348,32 +366,63 @@ __device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int64_t m
   }
 }
 
-template <int kType>
+// A block's walk over its share [x, end) of a list with `rows` rows a sequence.
+struct C4Walk {
+  int64_t x, end;
+  int64_t before;   // counts before sequence b
+  int b, n, nt;     // sequence, its entries and tiles
+  int row, t0, t1;  // row of the sequence, tiles of it
+  // Moves to the next row whose tiles the share holds; false at the share's end.
+  __device__ bool next(const DecParams& p, int rows, int cost) {
+    while (x < end) {
+      n = c4_len(p.len, b, p.most);
+      nt = (n + kC4TileKeys - 1) / kC4TileKeys;
+      const int units = c4_row_units(nt, cost);
+      const int64_t at = x - c4_units(before, cost) * rows;
+      if (at >= static_cast<int64_t>(units) * rows) {
+        before += c4_count(nt);
+        ++b;
+        continue;
+      }
+      row = static_cast<int>(at / units);
+      const int u0 = static_cast<int>(at - static_cast<int64_t>(row) * units);
+      const int u1 = static_cast<int>(end - x < units - u0 ? u0 + (end - x) : units);
+      x += u1 - u0;
+      t0 = max(0, u0 - cost);
+      t1 = u1 - cost;
+      if (t0 < t1) return true;
+    }
+    return false;
+  }
+};
+
 __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  if constexpr (kType == kFP16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Nibbles e and e + 4 of w as two values c - 8, exact.
-template <int kType>
-__device__ __forceinline__ uint32_t c4_pair(uint32_t w_shifted) {
-  uint32_t x, r;
-  if constexpr (kType == kFP16) {
-    x = (w_shifted & 0x000f000fu) | 0x64006400u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64086408u));
-  } else {
-    x = (w_shifted & 0x000f000fu) | 0x43004300u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
-  }
+// The same onto zero.
+__device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// c - 8 of the low nibbles of both 16-bit halves' low bytes, and of the high
+// nibbles: exact.
+__device__ __forceinline__ uint32_t c4_low(uint32_t w) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((w & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));
+  return r;
+}
+__device__ __forceinline__ uint32_t c4_high(uint32_t w) {  // (1024 + 16 c) / 16 - 72
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((w & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
   return r;
 }
 
@@ -384,9 +433,97 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return r;
 }
 
-// What a warp holds of its 16 keys of one tile.  lane = 4r + c: K rows r and
-// r + 8 (words 2c, 2c + 1 of each channel group), V rows 2c, 2c + 1, 2c + 8,
-// 2c + 9 (word r of each group), and the (s, m) of keys r and r + 8.
+// A warp's 16 keys of a tile travel through a ring of shared-memory stages of
+// its own, filled by asynchronous copies: with four stages 16 warps keep about
+// 110 KB an SM in flight, against some 40 KB with loads into registers, which
+// measured 190 us instead of MEASURED us at 64 sequences of up to 16000 tokens.
+// A stage is K codes, V codes, K meta, V meta, row by row.
+//
+// MMA row i of the first 8 keys is key kappa(i) = 0, 6, 1, 7, 2, 4, 3, 5, and
+// the same + 8 for the others (any order will do as long as S's rows and P's
+// agree).  With D = 128 the two halves of every second pair of rows are also
+// swapped.  Then neither the reads of K (lane 4r + c: row kappa(r), 8 bytes at
+// 8c of a group) nor those of V (row kappa(2c) or kappa(2c + 1), word r of a
+// group) meet in a bank.
+__device__ __forceinline__ int c4_kappa(int i) { return (i & 1) ? 4 + (((i >> 1) + 2) & 3) : i >> 1; }
+
+template <int D>
+struct C4Ring {
+  static constexpr int kStages = 4;
+  static constexpr int kRow = D / 2;             // bytes of codes a row
+  static constexpr int kMeta = D / kC4Group * 4;  // bytes of (s, m) a row
+  static constexpr int kV = 16 * kRow;
+  static constexpr int kKm = 32 * kRow;
+  static constexpr int kVm = kKm + 16 * kMeta;
+  static constexpr int kStage = kVm + 16 * kMeta;
+  static constexpr int kWarp = kStages * kStage;
+  // byte of row `row`'s 32-byte group g
+  __device__ static uint32_t at(int row, int g) {
+    return static_cast<uint32_t>(row * kRow + (D == 128 ? (g ^ ((row >> 1) & 1)) * 32 : 0));
+  }
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// What this lane copies of every tile: 16-byte pieces of K and V codes and one
+// row's meta (lanes 0-15 of K, 16-31 of V).  The pointers are the next tile's.
+template <int D>
+struct C4Copy {
+  using R = C4Ring<D>;
+  static constexpr int kPieces = D / 64;  // of K, and of V: the second one is 8 rows further
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* meta;
+  uint32_t dst, meta_dst;
+  int row, meta_row;
+  __device__ void start(const Cache4& c, int64_t key0, int lane, uint32_t ring) {
+    constexpr int kPerRow = R::kRow / 16;
+    row = lane / kPerRow;
+    meta_row = lane & 15;
+    const int piece = lane % kPerRow;
+    k = c.k + (key0 + row) * R::kRow + piece * 16;
+    v = c.v + (key0 + row) * R::kRow + piece * 16;
+    meta = reinterpret_cast<const uint8_t*>(lane < 16 ? c.km : c.vm) + (key0 + meta_row) * R::kMeta;
+    dst = ring + R::at(row, piece >> 1) + static_cast<uint32_t>(piece & 1) * 16;
+    meta_dst = ring + R::kKm + static_cast<uint32_t>(lane) * R::kMeta;
+  }
+  __device__ void issue(uint32_t stage) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      cp_async_16(dst + stage + i * 8 * R::kRow, k + i * 8 * R::kRow);
+      cp_async_16(dst + stage + R::kV + i * 8 * R::kRow, v + i * 8 * R::kRow);
+    }
+    cp_async_small<R::kMeta>(meta_dst + stage, meta);
+    k += kC4TileKeys * R::kRow;
+    v += kC4TileKeys * R::kRow;
+    meta += kC4TileKeys * R::kMeta;
+  }
+  // The last tile, of which `left` < 16 keys exist: rows past the end take the
+  // last one again.  They are masked, and nothing is read that was never written.
+  __device__ void issue_tail(uint32_t stage, int left) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int off = (min(row + 8 * i, left - 1) - row) * R::kRow;
+      cp_async_16(dst + stage + i * 8 * R::kRow, k + off);
+      cp_async_16(dst + stage + R::kV + i * 8 * R::kRow, v + off);
+    }
+    cp_async_small<R::kMeta>(meta_dst + stage, meta + (min(meta_row, left - 1) - meta_row) * R::kMeta);
+  }
+};
+
+// What a lane holds of a tile: K rows kappa(r), kappa(r) + 8; V rows kappa(2c),
+// kappa(2c + 1) and those + 8; the (s, m) of keys kappa(r), kappa(r) + 8.
 template <int D>
 struct C4Raw {
   static constexpr int kGroups = D / kC4Group;
@@ -395,231 +532,348 @@ struct C4Raw {
   uint32_t km[2][kGroups];
   uint32_t vm[2][kGroups];
 };
-
+// This lane's shared-memory addresses in stage 0.
 template <int D>
-__device__ __forceinline__ void c4_load(C4Raw<D>& t, const Cache4& cc, int64_t row_base, int key0, int n, int r,
-                                        int c) {
-  constexpr int kG = D / kC4Group;
-  // keys past the end read the last one again: they are masked, and nothing
-  // is read that was never written
+struct C4Lane {
+  uint32_t k[D / kC4Group], v[2][D / kC4Group], meta;
+  __device__ void start(uint32_t ring, int r, int c) {
+    using R = C4Ring<D>;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t at = row_base + min(key0 + r + 8 * i, n - 1);
+    for (int g = 0; g < D / kC4Group; ++g) {
+      k[g] = ring + R::at(c4_kappa(r), g) + static_cast<uint32_t>(8 * c);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i][g] = ring + R::kV + R::at(c4_kappa(2 * c + i), g) + static_cast<uint32_t>(4 * r);
+    }
+    meta = ring + R::kKm + static_cast<uint32_t>(c4_kappa(r) * R::kMeta);
+  }
+};
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_b32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+template <int D>
+__device__ __forceinline__ void c4_load(C4Raw<D>& t, const C4Lane<D>& p, uint32_t stage) {
+  using R = C4Ring<D>;
+  constexpr int kG = D / kC4Group;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // 8 rows further: the same place in the row
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      t.k[i][g] = __ldg(reinterpret_cast<const uint2*>(cc.k + at * (D / 2) + g * 32) + c);
-      t.km[i][g] = __ldg(cc.km + at * kG + g);
-      t.vm[i][g] = __ldg(cc.vm + at * kG + g);
+      t.k[i][g] = ld_shared_v2(p.k[g] + stage + i * 8 * R::kRow);
+      t.v[2 * i][g] = ld_shared_b32(p.v[0][g] + stage + i * 8 * R::kRow);
+      t.v[2 * i + 1][g] = ld_shared_b32(p.v[1][g] + stage + i * 8 * R::kRow);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = row_base + min(key0 + 2 * c + (i & 1) + 8 * (i >> 1), n - 1);
-#pragma unroll
-    for (int g = 0; g < kG; ++g)
-      t.v[i][g] = __ldg(reinterpret_cast<const uint32_t*>(cc.v + at * (D / 2) + g * 32) + r);
+    if constexpr (kG == 2) {
+      const uint2 a = ld_shared_v2(p.meta + stage + i * 8 * R::kMeta);
+      const uint2 b = ld_shared_v2(p.meta + stage + (R::kVm - R::kKm) + i * 8 * R::kMeta);
+      t.km[i][0] = a.x, t.km[i][kG - 1] = a.y, t.vm[i][0] = b.x, t.vm[i][kG - 1] = b.y;
+    } else {
+      t.km[i][0] = ld_shared_b32(p.meta + stage + i * 8 * R::kMeta);
+      t.vm[i][0] = ld_shared_b32(p.meta + stage + (R::kVm - R::kKm) + i * 8 * R::kMeta);
+    }
   }
 }
 
-// kFine: P.V with each p*s split into two bf16 terms (fp16 results need more
-// than bf16's 8 bits; fp16 itself has not the range for p*s).
+// Q of a block of up to 8 heads as B operands, and what goes with it.
+template <int D>
+struct C4Query {
+  static constexpr int kGroups = D / kC4Group;
+  uint32_t q[kGroups][4][2];  // head r, in the channel order of the K words
+  float sum[kGroups][2];      // of heads 2c, 2c + 1, over a group's channels
+  float scale[2];             // logits of heads 2c, 2c + 1, log2 units
+};
+template <int D, int kType>
+__device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* rows, int heads, float scale_log2, int r, int c) {
+  constexpr int kG = D / kC4Group;
+  const bool there = r < heads;
+  const uint16_t* qr = rows + (there ? r : 0) * D;
+  uint32_t raw[kG][8];
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (there) x = __ldg(reinterpret_cast<const uint4*>(qr + g * kC4Group + c * 16) + w);
+      raw[g][4 * w] = x.x, raw[g][4 * w + 1] = x.y, raw[g][4 * w + 2] = x.z, raw[g][4 * w + 3] = x.w;
+    }
+  float back = 1.f;
+  if constexpr (kType == kBF16) {
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[g][i])), fabsf(bf16_hi(raw[g][i]))));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^-E for top in [2^E, 2^(E+1)), within 2^-126 .. 2^100; 1 for 0, and for
+    // infinity, which stays one
+    const int e = static_cast<int>(__float_as_uint(top) >> 23);
+    const int f = top == 0.f || e == 255 ? 127 : min(max(254 - e, 1), 227);
+    const float fwd = __uint_as_float(static_cast<uint32_t>(f) << 23);
+    back = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[g][i] = pack_f16x2(bf16_lo(raw[g][i]) * fwd, bf16_hi(raw[g][i]) * fwd);
+  }
+  t.scale[0] = scale_log2 * __shfl_sync(0xffffffffu, back, 8 * c);
+  t.scale[1] = scale_log2 * __shfl_sync(0xffffffffu, back, 8 * c + 4);
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = unpack_f16x2(raw[g][i]);
+      sum += f.x + f.y;
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    t.sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+    t.sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+    // nibbles e and e + 4 of a word meet in one register: channels (0, 4),
+    // (1, 5) go into one MMA, (2, 6), (3, 7) into the next
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t* e = raw[g] + 4 * w;
+      t.q[g][2 * w][0] = __byte_perm(e[0], e[2], 0x5410);
+      t.q[g][2 * w][1] = __byte_perm(e[0], e[2], 0x7632);
+      t.q[g][2 * w + 1][0] = __byte_perm(e[1], e[3], 0x5410);
+      t.q[g][2 * w + 1][1] = __byte_perm(e[1], e[3], 0x7632);
+    }
+  }
+}
+
+// Running state of a warp: heads 2c and 2c + 1.
+template <int D>
+struct C4State {
+  static constexpr int kGroups = D / kC4Group;
+  float ref[2];              // what p is relative to, log2 units
+  float sub[2];              // the same, 0 instead of -inf
+  float most[2];             // ref + kRescaleLog2
+  float l[2];                // this lane's share of sum p
+  float bias[kGroups][2];    // this lane's share of sum p (m + 8 s)
+  float top_s[kGroups];      // power of two at or above every s so far (0 at first)
+  float inv_s[kGroups];      // 2^7 / top_s
+  float o[kGroups][4][4];    // O^T in units of top_s / 2^7: channels 64g + 8r + t (+ 4), heads 2c, 2c + 1
+};
+
+// One tile's 16 keys, of which the first `left` exist (kTail; else all).
+// `scores`: where head 2c's score of key `key` goes, [head][64 keys of the tile].
+template <int D, bool kWeight, bool kTail>
+__device__ __forceinline__ void c4_step(C4State<D>& st, const C4Raw<D>& t, const C4Query<D>& q, int key, int left,
+                                        float* scores, bool head0, bool head1) {
+  constexpr int kG = D / kC4Group;
+  float xs[4] = {0.f, 0.f, 0.f, 0.f};  // keys key, key, key + 8, key + 8; heads 2c, 2c + 1, ...
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    float d[4];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t wa = w ? t.k[0][g].y : t.k[0][g].x, wb = w ? t.k[1][g].y : t.k[1][g].x;
+      if (w == 0)
+        mma_16816_zero(d, c4_low(wa), c4_low(wb), c4_high(wa), c4_high(wb), q.q[g][0][0], q.q[g][0][1]);
+      else
+        mma_16816(d, c4_low(wa), c4_low(wb), c4_high(wa), c4_high(wb), q.q[g][2][0], q.q[g][2][1]);
+      mma_16816(d, c4_low(wa >> 8), c4_low(wb >> 8), c4_high(wa >> 8), c4_high(wb >> 8), q.q[g][2 * w + 1][0],
+                q.q[g][2 * w + 1][1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = bf16_lo(t.km[i][g]), mm = fmaf(8.f, s, bf16_hi(t.km[i][g]));
+      xs[2 * i] = fmaf(s, d[2 * i], fmaf(mm, q.sum[g][0], xs[2 * i]));
+      xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(mm, q.sum[g][1], xs[2 * i + 1]));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) xs[e] *= q.scale[e & 1];
+  if constexpr (kTail) {
+    if (key >= left) xs[0] = xs[1] = -INFINITY;
+    if (key + 8 >= left) xs[2] = xs[3] = -INFINITY;
+  }
+  if constexpr (kWeight) {
+    if (head0) {
+      scores[0] = xs[0];
+      scores[8] = xs[2];
+    }
+    if (head1) {
+      scores[kC4TileKeys] = xs[1];
+      scores[kC4TileKeys + 8] = xs[3];
+    }
+  }
+  // New references only where a score exceeds the old one by 2^8 or an s the
+  // old bound: p stays below 2^8, the results do not depend on the references,
+  // and most tiles need one vote instead of reductions and a rescale.
+  bool grow = (fmaxf(xs[0], xs[2]) > st.most[0]) | (fmaxf(xs[1], xs[3]) > st.most[1]);
+#pragma unroll
+  for (int g = 0; g < kG; ++g) grow |= fmaxf(bf16_lo(t.vm[0][g]), bf16_lo(t.vm[1][g])) > st.top_s[g];
+  if (__any_sync(0xffffffffu, grow)) {
+    float a[2], f[kG];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = fmaxf(xs[e], xs[2 + e]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      // a reference that has held moves only when it has to: p of the keys so
+      // far keeps its bits
+      const float to = top > st.most[e] ? top : st.ref[e];
+      a[e] = to == st.ref[e] ? 1.f : ex2_approx(st.ref[e] - to);
+      st.ref[e] = to;
+      st.sub[e] = to == -INFINITY ? 0.f : to;
+      st.most[e] = to + kRescaleLog2;
+      st.l[e] *= a[e];
+    }
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      float top = fmaxf(bf16_lo(t.vm[0][g]), bf16_lo(t.vm[1][g]));
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const uint32_t up = (__float_as_uint(top) + 0x007fffffu) & 0x7f800000u;  // the next power of two
+      const uint32_t to = max(max(up, __float_as_uint(st.top_s[g])), 17u << 23);
+      f[g] = st.top_s[g] == __uint_as_float(to) ? 1.f : __fdividef(st.top_s[g], __uint_as_float(to));
+      st.top_s[g] = __uint_as_float(to);
+      st.inv_s[g] = __uint_as_float((261u << 23) - to);
+      st.bias[g][0] *= a[0];
+      st.bias[g][1] *= a[1];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[g][u][e] *= a[e & 1] * f[g];
+    }
+  }
+  float pr[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    pr[e] = ex2_approx(xs[e] - st.sub[e & 1]);
+    st.l[e & 1] += pr[e];
+  }
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    uint32_t pb[2];  // P^T as the B operand: keys 0-7 and 8-15
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = bf16_lo(t.vm[i][g]), mm = fmaf(8.f, s, bf16_hi(t.vm[i][g])), sr = s * st.inv_s[g];
+      st.bias[g][0] = fmaf(pr[2 * i], mm, st.bias[g][0]);
+      st.bias[g][1] = fmaf(pr[2 * i + 1], mm, st.bias[g][1]);
+      pb[i] = movmatrix_trans(pack_f16x2(pr[2 * i] * sr, pr[2 * i + 1] * sr));
+    }
+    // bytes j of the words of two neighbouring MMA rows side by side: their low
+    // nibbles are channel 2j, the high ones 2j + 1
+    uint32_t wa[4], wb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      wa[j] = __byte_perm(t.v[0][g], t.v[1][g], 0x0400 + 0x1111 * j);
+      wb[j] = __byte_perm(t.v[2][g], t.v[3][g], 0x0400 + 0x1111 * j);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // rows r: channels 8r + 2j (+ 1); rows r + 8: channels 8r + 4 + 2j (+ 1)
+      mma_16816(st.o[g][2 * j], c4_low(wa[j]), c4_low(wa[j + 2]), c4_low(wb[j]), c4_low(wb[j + 2]), pb[0], pb[1]);
+      mma_16816(st.o[g][2 * j + 1], c4_high(wa[j]), c4_high(wa[j + 2]), c4_high(wb[j]), c4_high(wb[j + 2]), pb[0], pb[1]);
+    }
+  }
+}
+
 template <int D, int kType, bool kWeight>
 __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     attn_cache4_decode_kernel(const DecParams p) {
   constexpr int kG = D / kC4Group;
-  constexpr bool kFine = kType == kFP16;
   constexpr int kWarps = kC4DecThreads / 32;
-  __shared__ __align__(16) float o_s[kWarps][kC4Heads][D + 4];
+  using Ring = C4Ring<D>;
+  __shared__ __align__(128) uint8_t ring_s[kWarps * Ring::kWarp];
+  // the warps' O at a segment's end, when the ring is empty
+  float(*const o_s)[kC4Heads][D + 4] = reinterpret_cast<float(*)[kC4Heads][D + 4]>(ring_s);
+  static_assert(sizeof(float) * kWarps * kC4Heads * (D + 4) <= sizeof(ring_s), "O in the ring");
   __shared__ float2 ml_s[kWarps][kC4Heads];
   __shared__ int64_t sums_s[kWarps];
   __shared__ int64_t before_s;
   __shared__ int b_s;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  const int key = c4_kappa(r);
   grid_dependency_wait();
   int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
-  const int64_t total = c4_total_tiles(p, sums_s, &mine_before, &mine) * rows_per_b;
+  const int64_t total = c4_units(c4_total(p, sums_s, &mine_before, &mine), kC4RowCost) * rows_per_b;
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  int64_t x = static_cast<int64_t>(blockIdx.x) * share;
-  const int64_t x_end = x + share < total ? x + share : total;
-  if (x >= x_end) {
+  C4Walk w;
+  w.x = static_cast<int64_t>(blockIdx.x) * share;
+  w.end = w.x + share < total ? w.x + share : total;
+  if (w.x >= w.end) {
     grid_launch_dependents();
     return;
   }
-  c4_find(p, x / rows_per_b, mine_before, mine, &b_s, &before_s);
+  c4_find(p, w.x / rows_per_b, kC4RowCost, mine_before, mine, &b_s, &before_s);
   __syncthreads();
-  int b = b_s;
-  int64_t before = before_s * rows_per_b;  // list index of sequence b's first tile
-  while (x < x_end) {
-    const int n = c4_len(p.len, b, p.most);
-    const int nt = (n + kC4TileKeys - 1) / kC4TileKeys;
-    if (x >= before + static_cast<int64_t>(nt) * rows_per_b) {
-      before += static_cast<int64_t>(nt) * rows_per_b;
-      ++b;
-      continue;
-    }
-    const int in_b = static_cast<int>((x - before) / nt);  // key head and head block
-    const int t0 = static_cast<int>((x - before) % nt);
-    const int t1 = static_cast<int>(x_end - x < nt - t0 ? t0 + (x_end - x) : nt);
+  w.b = b_s;
+  w.before = before_s;
+  const uint32_t ring = smem_u32(ring_s) + static_cast<uint32_t>(warp * Ring::kWarp);
+  C4Lane<D> at;
+  at.start(ring, r, c);
+  while (w.next(p, rows_per_b, kC4RowCost)) {
+    const int b = w.b, n = w.n, in_b = w.row, t0 = w.t0, t1 = w.t1;
     const int h = in_b / p.HB, hb = in_b % p.HB;
     const int heads = min(kC4Heads, p.G - hb * kC4Heads);
 
-    // Q of head r of the block, in the channel order of the K words.
-    uint32_t q[kG][4][2];
-    float qsum[kG][2];
-    {
-      const bool there = r < heads;
-      const uint16_t* qr =
-          p.q + b * p.q_stride + static_cast<int64_t>(h * p.G + hb * kC4Heads + (there ? r : 0)) * D;
+    const int64_t row_base = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
+    // This warp's keys of its tiles: 16 of each of `full`, then `last` < 16.
+    const int64_t there = n - (static_cast<int64_t>(t0) * kC4TileKeys + warp * 16);  // keys from its first on
+    const int full = there < 16 ? 0 : static_cast<int>(min(static_cast<int64_t>(t1 - t0), (there - 16) / kC4TileKeys + 1));
+    const int last = full < t1 - t0 ? static_cast<int>(max(static_cast<int64_t>(0), there - static_cast<int64_t>(full) * kC4TileKeys)) : 0;
+    C4Copy<D> copy;
+    copy.start(p.c, row_base + static_cast<int64_t>(t0) * kC4TileKeys + warp * 16, lane, ring);
+    const auto fetch = [&](int i, uint32_t stage) {
+      if (i < full)
+        copy.issue(stage);
+      else if (i == full && last > 0)
+        copy.issue_tail(stage, last);
+      cp_async_commit();
+    };
 #pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        float sum = 0.f;
-        const uint4* src = reinterpret_cast<const uint4*>(qr + g * kC4Group + c * 16);
+    for (int i = 0; i < Ring::kStages - 1; ++i) fetch(i, static_cast<uint32_t>(i * Ring::kStage));
+    C4Query<D> q;
+    c4_load_query<D, kType>(q, p.q + b * p.q_stride + static_cast<int64_t>(h * p.G + hb * kC4Heads) * D, heads, p.scale_log2,
+                            r, c);
+    C4State<D> st;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {  // the 8 channels of one word
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          if (there) raw = __ldg(src + w);
-          const uint32_t e[4] = {raw.x, raw.y, raw.z, raw.w};  // channels (0,1) (2,3) (4,5) (6,7)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack_16x2<kType>(e[i]);
-            sum += f.x + f.y;
-          }
-          // pairs (e, e + 4)
-          q[g][2 * w][0] = __byte_perm(e[0], e[2], 0x5410);
-          q[g][2 * w][1] = __byte_perm(e[0], e[2], 0x7632);
-          q[g][2 * w + 1][0] = __byte_perm(e[1], e[3], 0x5410);
-          q[g][2 * w + 1][1] = __byte_perm(e[1], e[3], 0x7632);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qsum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);      // of head 2c
-        qsum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);  // of head 2c + 1
-      }
-    }
-
-    float m_ref[2] = {-INFINITY, -INFINITY};  // reference of p, heads 2c and 2c + 1
-    float l[2] = {0.f, 0.f};                  // this lane's share of the sums
-    float bias[kG][2];                        // this lane's share of sum p (m + 8 s)
-    float o[kG][4][4];                        // O^T: channels 64g + 8r + t (+ 4), heads 2c, 2c + 1
+    for (int e = 0; e < 2; ++e) st.ref[e] = st.most[e] = -INFINITY, st.sub[e] = st.l[e] = 0.f;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      bias[g][0] = bias[g][1] = 0.f;
+      st.top_s[g] = st.inv_s[g] = st.bias[g][0] = st.bias[g][1] = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[g][t][e] = 0.f;
+        for (int e = 0; e < 4; ++e) st.o[g][u][e] = 0.f;
     }
-    const int64_t row_base = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
     // scores of (sequence, key head): its tiles in list order without the head blocks
-    float* const score_row =
-        kWeight ? p.scores + ((before / p.HB + static_cast<int64_t>(h) * nt) * p.G + hb * kC4Heads * 1) * kC4TileKeys
-                : nullptr;
-
-    C4Raw<D> cur, nxt;
-    c4_load<D>(cur, p.c, row_base, t0 * kC4TileKeys + warp * 16, n, r, c);
-    for (int t = t0; t < t1; ++t) {
-      const int key0 = t * kC4TileKeys + warp * 16;
-      if (t + 1 < t1) c4_load<D>(nxt, p.c, row_base, key0 + kC4TileKeys, n, r, c);
-      if (key0 < n) {  // a warp wholly past the end has nothing to add
-        float xs[4] = {0.f, 0.f, 0.f, 0.f};  // keys r, r, r + 8, r + 8; heads 2c, 2c + 1
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t wa = w ? cur.k[0][g].y : cur.k[0][g].x, wb = w ? cur.k[1][g].y : cur.k[1][g].x;
-            // nibbles (0,4), (1,5) against q's slots of (0,4), (1,5); then (2,6), (3,7)
-            mma_16816<kType>(d, c4_pair<kType>(wa), c4_pair<kType>(wb), c4_pair<kType>(wa >> 4),
-                             c4_pair<kType>(wb >> 4), q[g][2 * w][0], q[g][2 * w][1]);
-            mma_16816<kType>(d, c4_pair<kType>(wa >> 8), c4_pair<kType>(wb >> 8), c4_pair<kType>(wa >> 12),
-                             c4_pair<kType>(wb >> 12), q[g][2 * w + 1][0], q[g][2 * w + 1][1]);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float s = bf16_lo(cur.km[i][g]), mm = fmaf(8.f, s, bf16_hi(cur.km[i][g]));
-            xs[2 * i] = fmaf(s, d[2 * i], fmaf(mm, qsum[g][0], xs[2 * i]));
-            xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(mm, qsum[g][1], xs[2 * i + 1]));
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xs[e] *= p.scale_log2;
-        if (key0 + 16 > n) {
-          if (key0 + r >= n) xs[0] = xs[1] = -INFINITY;
-          if (key0 + r + 8 >= n) xs[2] = xs[3] = -INFINITY;
-        }
-        if constexpr (kWeight) {
-          float* dst = score_row + static_cast<int64_t>(t) * p.G * kC4TileKeys + warp * 16 + r;
-          if (2 * c < heads) {
-            dst[2 * c * kC4TileKeys] = xs[0];
-            dst[2 * c * kC4TileKeys + 8] = xs[2];
-          }
-          if (2 * c + 1 < heads) {
-            dst[(2 * c + 1) * kC4TileKeys] = xs[1];
-            dst[(2 * c + 1) * kC4TileKeys + 8] = xs[3];
-          }
-        }
-        // A new reference only where a score exceeds the old one by 2^8: p
-        // stays below 2^8, O / l does not depend on the reference, and most
-        // tiles need one vote instead of a reduction and a rescale.
-        const bool grow = fmaxf(xs[0], xs[2]) > m_ref[0] + kRescaleLog2 || fmaxf(xs[1], xs[3]) > m_ref[1] + kRescaleLog2;
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(xs[e], xs[2 + e]);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float to = fmaxf(top, m_ref[e]);
-            const float a = to == -INFINITY ? 1.f : ex2_approx(m_ref[e] - to);
-            m_ref[e] = to;
-            l[e] *= a;
-#pragma unroll
-            for (int g = 0; g < kG; ++g) {
-              bias[g][e] *= a;
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                o[g][u][e] *= a;
-                o[g][u][2 + e] *= a;
-              }
-            }
-          }
-        }
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m_ref[e & 1] == -INFINITY ? 0.f : m_ref[e & 1];
-          pr[e] = ex2_approx(xs[e] - ref);
-          l[e & 1] += pr[e];
-        }
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          uint32_t pb[2], pl[2];  // P^T as the B operand: keys 0-7 and 8-15
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float s = bf16_lo(cur.vm[i][g]), mm = fmaf(8.f, s, bf16_hi(cur.vm[i][g]));
-            const float p0 = pr[2 * i] * s, p1 = pr[2 * i + 1] * s;
-            bias[g][0] = fmaf(pr[2 * i], mm, bias[g][0]);
-            bias[g][1] = fmaf(pr[2 * i + 1], mm, bias[g][1]);
-            const uint32_t hi = pack_bf16x2(p0, p1);
-            pb[i] = movmatrix_trans(hi);
-            if constexpr (kFine) pl[i] = movmatrix_trans(pack_bf16x2(p0 - bf16_lo(hi), p1 - bf16_hi(hi)));
-          }
-          // words of keys (2c, 2c + 1) and (2c + 8, 2c + 9): channels 0-3 and 4-7 side by side
-          const uint32_t a_lo = __byte_perm(cur.v[0][g], cur.v[1][g], 0x5410);
-          const uint32_t a_hi = __byte_perm(cur.v[0][g], cur.v[1][g], 0x7632);
-          const uint32_t b_lo = __byte_perm(cur.v[2][g], cur.v[3][g], 0x5410);
-          const uint32_t b_hi = __byte_perm(cur.v[2][g], cur.v[3][g], 0x7632);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t a0 = c4_pair<kBF16>(a_lo >> (4 * u)), a1 = c4_pair<kBF16>(a_hi >> (4 * u));
-            const uint32_t a2 = c4_pair<kBF16>(b_lo >> (4 * u)), a3 = c4_pair<kBF16>(b_hi >> (4 * u));
-            mma_16816<kBF16>(o[g][u], a0, a1, a2, a3, pb[0], pb[1]);
-            if constexpr (kFine) mma_16816<kBF16>(o[g][u], a0, a1, a2, a3, pl[0], pl[1]);
-          }
-        }
-      }
-      cur = nxt;
+    float* sc = kWeight ? p.scores + (((w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * w.nt + t0) * p.G + hb * kC4Heads + 2 * c) * kC4TileKeys +
+                              warp * 16 + key
+                        : nullptr;
+    const int64_t sc_step = static_cast<int64_t>(p.G) * kC4TileKeys;
+    const bool head0 = 2 * c < heads, head1 = 2 * c + 1 < heads;
+    uint32_t stage = 0u, free = (Ring::kStages - 1) * Ring::kStage;  // of tile i, and the one consumed before it
+    for (int i = 0; i < full; ++i) {
+      cp_async_wait<Ring::kStages - 2>();  // this lane's copies of tile i, ...
+      __syncwarp();                        // ... and every lane's; the stage before is consumed
+      fetch(i + Ring::kStages - 1, free);
+      C4Raw<D> raw;
+      c4_load<D>(raw, at, stage);
+      free = stage;
+      stage = stage == (Ring::kStages - 1) * Ring::kStage ? 0u : stage + Ring::kStage;
+      c4_step<D, kWeight, false>(st, raw, q, key, 16, sc, head0, head1);
+      if (kWeight) sc += sc_step;
     }
+    if (last > 0) {
+      cp_async_wait<0>();
+      __syncwarp();
+      C4Raw<D> raw;
+      c4_load<D>(raw, at, stage);
+      c4_step<D, kWeight, true>(st, raw, q, key, last, sc, head0, head1);
+    }
+    __syncthreads();  // the ring is empty (the copies of every tile were waited for) and read
 
     // Join the four warps: statistics over the lanes of a head, then O
     // relative to the segment's own maximum.
@@ -627,9 +881,9 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+        st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], off);
 #pragma unroll
-        for (int g = 0; g < kG; ++g) bias[g][e] += __shfl_xor_sync(0xffffffffu, bias[g][e], off);
+        for (int g = 0; g < kG; ++g) st.bias[g][e] += __shfl_xor_sync(0xffffffffu, st.bias[g][e], off);
       }
     }
 #pragma unroll
@@ -638,10 +892,11 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          o_s[warp][2 * c + (e & 1)][g * kC4Group + 8 * r + u + 4 * (e >> 1)] = o[g][u][e] + bias[g][e & 1];
+          o_s[warp][2 * c + (e & 1)][g * kC4Group + 8 * r + u + 4 * (e >> 1)] =
+              fmaf(st.o[g][u][e], st.top_s[g] * 0x1p-7f, st.bias[g][e & 1]);
     if (r == 0) {
-      ml_s[warp][2 * c] = make_float2(m_ref[0], l[0]);
-      ml_s[warp][2 * c + 1] = make_float2(m_ref[1], l[1]);
+      ml_s[warp][2 * c] = make_float2(st.ref[0], st.l[0]);
+      ml_s[warp][2 * c + 1] = make_float2(st.ref[1], st.l[1]);
     }
     __syncthreads();
     const int64_t slot = blockIdx.x + static_cast<int64_t>(b) * rows_per_b + in_b;
@@ -649,19 +904,18 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       const int hd = i / D, d = i % D;
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_s[w][hd].x);
+      for (int i2 = 0; i2 < kWarps; ++i2) top = fmaxf(top, ml_s[i2][hd].x);
       float sum = 0.f, ls = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = top == -INFINITY ? 0.f : ex2_approx(ml_s[w][hd].x - top);
-        sum = fmaf(a, o_s[w][hd][d], sum);
-        ls = fmaf(a, ml_s[w][hd].y, ls);
+      for (int i2 = 0; i2 < kWarps; ++i2) {
+        const float a = top == -INFINITY ? 0.f : ex2_approx(ml_s[i2][hd].x - top);
+        sum = fmaf(a, o_s[i2][hd][d], sum);
+        ls = fmaf(a, ml_s[i2][hd].y, ls);
       }
       p.o_part[(slot * kC4Heads + hd) * D + d] = sum;
       if (d == 0) p.ml_part[slot * kC4Heads + hd] = make_float2(top, ls);
     }
     __syncthreads();
-    x += t1 - t0;
   }
   grid_launch_dependents();
 }
@@ -673,167 +927,184 @@ struct DecMergeParams {
   float* lse;    // [B][H*G]
   const float* w_in;
   float* w_out;  // [B][H][cap]
+  int warps;     // of the merge kernel that share a row's partials
 };
 
 constexpr int kC4MergeThreads = 256;
-constexpr int kC4MergeTiles = 4;  // tiles of weights one block takes at a time
+constexpr int kC4MergeTiles = 16;  // tiles of weights a block takes at once: 16 threads a tile, 4 keys each
+constexpr int kC4MergeRowCost = 24;  // tiles' worth of time that a row costs a block
 
-// The partials of list rows: row (b, in_b) owns tiles [first, first + nt) of
-// the list and was cut where the shares end.
+// The CTAs that hold a segment of a row whose units begin at `start` of the list.
 struct C4Parts {
-  int first, count;  // CTAs that hold a segment of it
+  int first, count;
 };
-__device__ __forceinline__ C4Parts c4_parts(int64_t first_tile, int nt, int64_t share) {
+__device__ __forceinline__ C4Parts c4_parts(int64_t start, int nt, int64_t share) {
   C4Parts r;
-  r.first = static_cast<int>(first_tile / share);
-  r.count = nt == 0 ? 0 : static_cast<int>((first_tile + nt - 1) / share) - r.first + 1;
+  r.first = static_cast<int>((start + kC4RowCost) / share);
+  r.count = nt == 0 ? 0 : static_cast<int>((start + kC4RowCost + nt - 1) / share) - r.first + 1;
   return r;
+}
+
+// Statistics of a row's partials, by one warp: the maximum and the sum
+// relative to it (log2 units).
+__device__ __forceinline__ float2 c4_join_stats(const float2* ml, int count, int lane) {
+  const float2 f0 = lane < count ? __ldg(&ml[static_cast<int64_t>(lane) * kC4Heads]) : make_float2(-INFINITY, 0.f);
+  float top = f0.x;
+  for (int i = lane + 32; i < count; i += 32) top = fmaxf(top, __ldg(&ml[static_cast<int64_t>(i) * kC4Heads].x));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float ls = fmaf(top == -INFINITY ? 0.f : ex2_approx(f0.x - top), f0.y, 0.f);
+  for (int i = lane + 32; i < count; i += 32) {
+    const float2 f = __ldg(&ml[static_cast<int64_t>(i) * kC4Heads]);
+    ls = fmaf(top == -INFINITY ? 0.f : ex2_approx(f.x - top), f.y, ls);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+  return make_float2(top, ls);
 }
 
 // Joins the partials of every (sequence, query head) into O and LSE, and adds
 // each entry's attention weight, summed over the heads of its group, where
-// the scores were kept.
+// the scores were kept.  `m.warps` (1, 2, 4, 8) warps share a row's partials,
+// four of them in flight each: with one warp, the 77 partials of a row of
+// 131072 keys took 33 us, most of it waiting for memory.
 template <int D, int kType, bool kWeight>
 __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(const DecMergeParams m) {
   constexpr int kWarps = kC4MergeThreads / 32;
   constexpr int kPer = D / 32;
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   const DecParams& p = m.d;
   __shared__ int64_t sums_s[kWarps];
   __shared__ int64_t before_s;
   __shared__ int b_s;
   __shared__ float lse_s[128];
+  __shared__ __align__(16) float o_s[kWarps][D];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_launch_dependents();
   int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
-  const int64_t tiles = c4_total_tiles(p, sums_s, &mine_before, &mine);
-  const int64_t share = (tiles * rows_per_b + m.dec_grid - 1) / m.dec_grid;
+  const int64_t count = c4_total(p, sums_s, &mine_before, &mine);
+  const int64_t share = max(static_cast<int64_t>(1), (c4_units(count, kC4RowCost) * rows_per_b + m.dec_grid - 1) / m.dec_grid);
 
-  // O and LSE: a block takes a sequence, a warp one of its query heads.
-  // (Blocks own sequences so that the tile counts before them are found once.)
-  const int hq = p.c.H * p.G;
-  const int per_b = (hq + kWarps - 1) / kWarps;
+  // O and LSE: m.warps warps a row, the blocks' rows all of one sequence.
+  const int hq = p.c.H * p.G, rows = kWarps / m.warps;
+  const int per_b = (hq + rows - 1) / rows;
   for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * per_b; u += gridDim.x) {
     const int b = static_cast<int>(u / per_b);
-    const int head = static_cast<int>(u % per_b) * kWarps + warp;
-    // tiles before sequence b: its stripe's owner knows
+    const int head = static_cast<int>(u % per_b) * rows + warp / m.warps;
     const int stripe = (p.B + kC4MergeThreads - 1) / kC4MergeThreads;
-    if (b / stripe == tid) {
+    if (b / stripe == tid) {  // what lies before sequence b: its stripe's owner knows
       int64_t at = mine_before;
-      for (int i = tid * stripe; i < b; ++i) at += c4_tiles(p, i);
+      for (int i = tid * stripe; i < b; ++i) at += c4_count(c4_tiles(p, i));
       before_s = at;
     }
     __syncthreads();
-    const int64_t before = before_s * rows_per_b;
-    __syncthreads();
-    if (head >= hq) continue;
-    const int h = head / p.G, g = head % p.G, hb = g / kC4Heads;
-    const int in_b = h * p.HB + hb;
-    const int nt = c4_tiles(p, b);
-    const C4Parts cut = c4_parts(before + static_cast<int64_t>(in_b) * nt, nt, share > 0 ? share : 1);
-    const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
-    const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
-    const float* op = p.o_part + (slot0 * kC4Heads + g % kC4Heads) * D + lane * kPer;
-    float top = -INFINITY;
-    for (int i = lane; i < cut.count; i += 32) top = fmaxf(top, __ldg(&ml[static_cast<int64_t>(i) * kC4Heads].x));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float acc[kPer], ls = 0.f;
+    const int64_t before = c4_units(before_s, kC4RowCost) * rows_per_b;
+    float acc[kPer], inv = 0.f;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int i0 = 0; i0 < cut.count; i0 += 32) {
-      float a = 0.f;
-      if (i0 + lane < cut.count) {
-        const float2 f = __ldg(&ml[static_cast<int64_t>(i0 + lane) * kC4Heads]);
-        a = top == -INFINITY ? 0.f : ex2_approx(f.x - top);
-        ls = fmaf(a, f.y, ls);
-      }
-      const int cnt = min(32, cut.count - i0);
-#pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
-        const float w = __shfl_sync(0xffffffffu, a, j);
-        const float* src = op + static_cast<int64_t>(i0 + j) * kC4Heads * D;
-        if constexpr (kPer == 4) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(src));
-          acc[0] = fmaf(w, f.x, acc[0]);
-          acc[1] = fmaf(w, f.y, acc[1]);
-          acc[2] = fmaf(w, f.z, acc[2]);
-          acc[3] = fmaf(w, f.w, acc[3]);
-        } else {
-          const float2 f = __ldg(reinterpret_cast<const float2*>(src));
-          acc[0] = fmaf(w, f.x, acc[0]);
-          acc[1] = fmaf(w, f.y, acc[1]);
+    const int64_t row = static_cast<int64_t>(b) * hq + head;
+    if (head < hq) {
+      const int h = head / p.G, g = head % p.G, hb = g / kC4Heads;
+      const int in_b = h * p.HB + hb;
+      const int nt = c4_tiles(p, b);
+      const C4Parts cut = c4_parts(before + static_cast<int64_t>(in_b) * c4_row_units(nt, kC4RowCost), nt, share);
+      const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
+      const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
+      const float* op = p.o_part + (slot0 * kC4Heads + g % kC4Heads) * D + lane * kPer;
+      const float2 tl = c4_join_stats(ml, cut.count, lane);
+      inv = cut.count == 0 ? 0.f : 1.f / tl.y;
+      const int step = m.warps;
+      for (int i = warp % step; i < cut.count; i += 4 * step) {
+        Vec v[4];
+        float a[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = min(i + j * step, cut.count - 1);
+          v[j] = __ldg(reinterpret_cast<const Vec*>(op + at * kC4Heads * D));
+          a[j] = __ldg(&ml[at * kC4Heads].x);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i + j * step >= cut.count) break;
+          const float w = tl.x == -INFINITY ? 0.f : ex2_approx(a[j] - tl.x);
+          const float* f = reinterpret_cast<const float*>(&v[j]);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, f[e], acc[e]);
         }
       }
+      if (lane == 0 && warp % step == 0) m.lse[row] = cut.count == 0 ? -INFINITY : (tl.x + log2f(tl.y)) * kLn2;
     }
+    if (m.warps > 1) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
-    const float inv = cut.count == 0 ? 0.f : 1.f / ls;
-    const int64_t row = static_cast<int64_t>(b) * hq + head;
-    uint16_t* dst = m.o + row * D + lane * kPer;
-    if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_16x2<kType>(acc[0] * inv, acc[1] * inv), pack_16x2<kType>(acc[2] * inv, acc[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = pack_16x2<kType>(acc[0] * inv, acc[1] * inv);
-    if (lane == 0) m.lse[row] = cut.count == 0 ? -INFINITY : (top + log2f(ls)) * kLn2;
+      for (int e = 0; e < kPer; ++e) o_s[warp][lane * kPer + e] = acc[e];
+      __syncthreads();
+      if (warp % m.warps == 0)
+        for (int w = 1; w < m.warps; ++w)
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] += o_s[warp + w][lane * kPer + e];
+    }
+    if (head < hq && warp % m.warps == 0) {
+      uint16_t* dst = m.o + row * D + lane * kPer;
+      const uint32_t lo = pack_16x2<kType>(acc[0] * inv, acc[1] * inv);
+      if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack_16x2<kType>(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = lo;
+    }
+    __syncthreads();
   }
 
   if constexpr (kWeight) {
-    // Weights: the tiles of every (sequence, key head), kC4MergeTiles at a
-    // time; a chunk may cross from one (sequence, key head) into the next, so
-    // it is walked in pieces.
-    const int64_t all = tiles * p.c.H;
-    for (int64_t y = static_cast<int64_t>(blockIdx.x) * kC4MergeTiles; y < all;
-         y += static_cast<int64_t>(gridDim.x) * kC4MergeTiles) {
-      const int64_t y_end = y + kC4MergeTiles < all ? y + kC4MergeTiles : all;
+    // Weights: the tiles of every (sequence, key head) in equal contiguous
+    // shares, one per block, walked row by row; 4 keys a thread.
+    const int64_t all = c4_units(count, kC4MergeRowCost) * p.c.H;
+    const int64_t mine_w = (all + gridDim.x - 1) / gridDim.x;
+    C4Walk w;
+    w.x = static_cast<int64_t>(blockIdx.x) * mine_w;
+    w.end = w.x + mine_w < all ? w.x + mine_w : all;
+    if (w.x < w.end) {
+      c4_find(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
       __syncthreads();
-      c4_find(p, y / p.c.H, mine_before, mine, &b_s, &before_s);
-      __syncthreads();
-      int b = b_s;
-      int64_t before = before_s * p.c.H;
-      int64_t z = y;
-      while (z < y_end) {
-        const int n = c4_len(p.len, b, p.most);
-        const int nt = (n + kC4TileKeys - 1) / kC4TileKeys;
-        if (z >= before + static_cast<int64_t>(nt) * p.c.H) {
-          before += static_cast<int64_t>(nt) * p.c.H;
-          ++b;
-          continue;
-        }
-        const int h = static_cast<int>((z - before) / nt), t0 = static_cast<int>((z - before) % nt);
-        const int t1 = static_cast<int>(y_end - z < nt - t0 ? t0 + (y_end - z) : nt);
+      w.b = b_s;
+      w.before = before_s;
+      while (w.next(p, p.c.H, kC4MergeRowCost)) {
+        const int b = w.b, n = w.n, nt = w.nt, h = w.row;
+        const int64_t before = c4_units(w.before, kC4RowCost) * rows_per_b;
         // log2 of the sum of every head of the group, a warp a head
         for (int g = warp; g < p.G; g += kWarps) {
           const int in_b = h * p.HB + g / kC4Heads;
-          const C4Parts cut = c4_parts(before * p.HB + static_cast<int64_t>(in_b) * nt, nt, share);
+          const C4Parts cut = c4_parts(before + static_cast<int64_t>(in_b) * c4_row_units(nt, kC4RowCost), nt, share);
           const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
-          const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
-          float top = -INFINITY;
-          for (int i = lane; i < cut.count; i += 32) top = fmaxf(top, __ldg(&ml[static_cast<int64_t>(i) * kC4Heads].x));
+          const float2 tl = c4_join_stats(p.ml_part + slot0 * kC4Heads + g % kC4Heads, cut.count, lane);
+          if (lane == 0) lse_s[g] = tl.x + log2f(tl.y);
+        }
+        __syncthreads();
+        const int64_t at0 = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
+        for (int t = w.t0 + (tid >> 4); t < w.t1; t += kC4MergeTiles) {
+          const int k0 = (tid & 15) * 4;
+          const int64_t at = at0 + static_cast<int64_t>(t) * kC4TileKeys + k0;
+          const int left = n - t * kC4TileKeys - k0;  // of these 4 keys on
+          const float4* src = reinterpret_cast<const float4*>(
+              p.scores + ((w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * nt + t) * p.G * kC4TileKeys + k0);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f}, in[4];
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          float ls = 0.f;
-          for (int i = lane; i < cut.count; i += 32) {
-            const float2 f = __ldg(&ml[static_cast<int64_t>(i) * kC4Heads]);
-            ls = fmaf(top == -INFINITY ? 0.f : ex2_approx(f.x - top), f.y, ls);
+          for (int e = 0; e < 4; ++e) in[e] = e < left ? m.w_in[at + e] : 0.f;
+#pragma unroll 8
+          for (int g = 0; g < p.G; ++g) {
+            const float4 x = __ldg(src + g * (kC4TileKeys / 4));
+            const float z2 = lse_s[g];
+            sum[0] += ex2_approx(x.x - z2);
+            sum[1] += ex2_approx(x.y - z2);
+            sum[2] += ex2_approx(x.z - z2);
+            sum[3] += ex2_approx(x.w - z2);
           }
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
-          if (lane == 0) lse_s[g] = top + log2f(ls);
+          for (int e = 0; e < 4; ++e)
+            if (e < left) m.w_out[at + e] = in[e] + sum[e];
         }
         __syncthreads();
-        const float* sc = p.scores + (before + static_cast<int64_t>(h) * nt) * p.G * kC4TileKeys;
-        const int64_t at0 = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
-        for (int i = t0 * kC4TileKeys + tid; i < min(t1 * kC4TileKeys, n); i += kC4MergeThreads) {
-          const float* src = sc + static_cast<int64_t>(i / kC4TileKeys) * p.G * kC4TileKeys + i % kC4TileKeys;
-          float w = 0.f;
-          for (int g = 0; g < p.G; ++g) w += ex2_approx(__ldg(src + g * kC4TileKeys) - lse_s[g]);
-          m.w_out[at0 + i] = m.w_in[at0 + i] + w;
-        }
-        __syncthreads();
-        z += t1 - t0;
       }
     }
   }
@@ -1146,7 +1417,7 @@ attn_status_t check_cache4(const attn_cache4_t* c) {
       c->length == nullptr)
     return ATTN_ERR_INVALID_ARG;
   if (c->D != 64 && c->D != 128) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_meta, 4) || !aligned(c->v_meta, 4) ||
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_meta, 8) || !aligned(c->v_meta, 8) ||
       !aligned(c->length, 4) || !aligned(c->weight, 4) || !aligned(c->pos, 4))
     return ATTN_ERR_ALIGNMENT;
   if (static_cast<int64_t>(c->B) * c->H_kv > INT_MAX / 64) return ATTN_ERR_UNSUPPORTED;
@@ -1196,7 +1467,7 @@ DecLayout decode_layout(int B, int H_q, int H_kv, int D, int max_len, bool weigh
   const int64_t rows = static_cast<int64_t>(B) * H_kv * HB;
   const int64_t tiles = (static_cast<int64_t>(max_len) + kC4TileKeys - 1) / kC4TileKeys;
   DecLayout l;
-  l.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows * tiles, static_cast<int64_t>(sms) * kC4DecCtasPerSm)));
+  l.grid = static_cast<int>(std::min<int64_t>(rows * (tiles + kC4RowCost), static_cast<int64_t>(sms) * kC4DecCtasPerSm));
   l.slots = l.grid + rows;
   l.o_bytes = l.slots * kC4Heads * D * 4;
   l.ml_bytes = l.slots * kC4Heads * 8;
@@ -1211,9 +1482,10 @@ attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t strea
   cudaError_t e = weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true>, grid, dim3(kC4DecThreads), 0, stream, m.d)
                          : launch_pdl(attn_cache4_decode_kernel<D, kType, false>, grid, dim3(kC4DecThreads), 0, stream, m.d);
   if (e != cudaSuccess) return ATTN_ERR_LAUNCH;
-  const int64_t heads = static_cast<int64_t>(m.d.B) * m.d.c.H * m.d.G;
+  // blocks for the rows, or for the weights' tiles where those want more
+  const int64_t rows = kC4MergeThreads / 32 / m.warps;
   const int64_t tiles = (static_cast<int64_t>(m.d.most) + kC4TileKeys - 1) / kC4TileKeys * m.d.B * m.d.c.H;
-  int64_t blocks = (heads + kC4MergeThreads / 32 - 1) / (kC4MergeThreads / 32);
+  int64_t blocks = m.d.B * ((static_cast<int64_t>(m.d.c.H) * m.d.G + rows - 1) / rows);
   if (weight) blocks = std::max(blocks, (tiles + kC4MergeTiles - 1) / kC4MergeTiles);
   const dim3 mg(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 8)));
   e = weight ? launch_pdl(attn_cache4_merge_kernel<D, kType, true>, mg, dim3(kC4MergeThreads), 0, stream, m)
@@ -1358,6 +1630,9 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
   m.lse = lse;
   m.w_in = weight_in;
   m.w_out = weight_out;
+  // a warp for every four partials that a row has on average
+  const int64_t parts = l.grid / (static_cast<int64_t>(m.d.B) * m.d.c.H * m.d.HB) + 1;
+  m.warps = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cache->D == 64)
     return dtype == ATTN_BF16 ? launch_decode<64, kBF16>(m, sms, s) : launch_decode<64, kFP16>(m, sms, s);
