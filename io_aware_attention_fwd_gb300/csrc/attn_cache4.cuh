@@ -89,38 +89,78 @@ __device__ __forceinline__ int64_t c4_row(const Cache4Rows& g, const Cache4& c, 
   return (static_cast<int64_t>(b) * c.H + h) * c.cap + slot;
 }
 
-// One row's 8 channels of this thread: the group's statistics over its 8
-// lanes, the codes and the (s, m) word.
-__device__ __forceinline__ uint32_t c4_quantise(const float* x, uint32_t* meta) {
-  float lo = x[0], hi = x[0];
-  bool finite = isfinite(x[0]);
-#pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-    finite = finite && isfinite(x[e]);
-  }
-  if (!finite) lo = -INFINITY, hi = INFINITY;  // marks the whole group
+// Packed 16-bit minimum and maximum that pass a NaN on.
+template <int kType>
+__device__ __forceinline__ uint32_t min_16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kType == kFP16)
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int kType>
+__device__ __forceinline__ uint32_t max_16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kType == kFP16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// One row's 8 channels of this thread (packed): the group's statistics over
+// its 8 lanes, the codes and the (s, m) word.
+//
+// The codes are those of IEEE subtraction and division.  With y the correctly
+// rounded 1 / s and q0 = d * y, q0 + (d - q0 * s) * y, each step a fused
+// multiply-add, is the correctly rounded d / s (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), as long
+// as nothing under- or overflows: s within 2^-100 .. 2^100, else the division
+// itself is used (a group of such values alone pays for it).
+template <int kType>
+__device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta) {
+  uint32_t lo2 = min_16x2<kType>(min_16x2<kType>(raw.x, raw.y), min_16x2<kType>(raw.z, raw.w));
+  uint32_t hi2 = max_16x2<kType>(max_16x2<kType>(raw.x, raw.y), max_16x2<kType>(raw.z, raw.w));
 #pragma unroll
   for (int off = 1; off < 8; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    lo2 = min_16x2<kType>(lo2, __shfl_xor_sync(0xffffffffu, lo2, off));
+    hi2 = max_16x2<kType>(hi2, __shfl_xor_sync(0xffffffffu, hi2, off));
   }
-  // IEEE subtraction and division, no contraction: the codes are the format's
-  const uint32_t sm = pack_bf16x2(__fdiv_rn(__fsub_rn(hi, lo), 15.f), lo);
-  if (hi == INFINITY || lo == -INFINITY) {
-    *meta = 0x7fc07fc0u;  // (NaN, NaN)
+  lo2 = min_16x2<kType>(lo2, __byte_perm(lo2, lo2, 0x1032));
+  hi2 = max_16x2<kType>(hi2, __byte_perm(hi2, hi2, 0x1032));
+  const float lo = unpack_16x2<kType>(lo2).x, hi = unpack_16x2<kType>(hi2).x;
+  if (!(lo > -INFINITY && hi < INFINITY)) {  // also where either is NaN
+    *meta = 0x7fc07fc0u;                     // (NaN, NaN)
     return 0u;
   }
+  const uint32_t sm = pack_bf16x2(__fdiv_rn(__fsub_rn(hi, lo), 15.f), lo);
   *meta = sm;
   const float s = bf16_lo(sm), m = bf16_hi(sm);
-  uint32_t w = 0u;
-  if (s != 0.f) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack_16x2<kType>((&raw.x)[e]);
+    x[2 * e] = __fsub_rn(f.x, m);
+    x[2 * e + 1] = __fsub_rn(f.y, m);
+  }
+  if (s >= 0x1p-100f && s <= 0x1p100f) {
+    const float y = __frcp_rn(s);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float q = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], m), s)), 0.f), 15.f);
-      w |= static_cast<uint32_t>(q) << (4 * e);
+      const float q0 = __fmul_rn(x[e], y);
+      x[e] = __fmaf_rn(__fmaf_rn(-q0, s, x[e]), y, q0);
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = s != 0.f ? __fdiv_rn(x[e], s) : 0.f;
+  }
+  // round half to even by adding 1.5 * 2^23; the code is then in the low bits
+  uint32_t w = 0u;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    const float c = __fadd_rn(fminf(fmaxf(x[e], 0.f), 15.f), 12582912.f);
+    w = w * 16u + (__float_as_uint(c) & 15u);
   }
   return w;
 }
@@ -128,6 +168,7 @@ __device__ __forceinline__ uint32_t c4_quantise(const float* x, uint32_t* meta) 
 // Appends packed rows of K and V (bf16 or fp16): quantises each row, writes
 // it at its sequence's next slot, its position, and a zero weight.
 // HBM-bound: 4*D bytes read and D + D/8 + 8 written per row and head.
+// MEASURED-APPEND
 template <int D, int kType>
 __global__ void __launch_bounds__(kC4RowsThreads)
     attn_cache4_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, Cache4Rows g, Cache4 c,
@@ -136,10 +177,10 @@ __global__ void __launch_bounds__(kC4RowsThreads)
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kC4RowLanes<D>;
-  const int64_t n_chunks = (g.rows + kC4BlockRows<D> - 1) / kC4BlockRows<D>;
-  for (int64_t u = blockIdx.x; u < n_chunks * c.H; u += gridDim.x) {
-    const int h = static_cast<int>(u % c.H);
-    const int64_t row = (u / c.H) * kC4BlockRows<D> + threadIdx.x / kC4RowLanes<D>;
+  const int h = static_cast<int>(blockIdx.x);
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kC4BlockRows<D>; row0 < g.rows;
+       row0 += static_cast<int64_t>(gridDim.y) * kC4BlockRows<D>) {
+    const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
     uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
     if (row < g.rows) {  // the loads need no sequence: they go out before its search
       xk = __ldg(reinterpret_cast<const uint4*>(k + row * g.k_stride + h * D + lane * 8));
@@ -148,37 +189,28 @@ __global__ void __launch_bounds__(kC4RowsThreads)
     int b = 0, slot = 0;
     bool dropped;
     const int64_t at = c4_row<D>(g, c, row, h, &b, &slot, &dropped);
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint4 raw = kv ? xv : xk;
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack_16x2<kType>((&raw.x)[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
+    uint32_t mk, mv;
+    const uint32_t wk = c4_quantise<kType>(xk, &mk), wv = c4_quantise<kType>(xv, &mv);
+    if (at >= 0) {
+      reinterpret_cast<uint32_t*>(c.k)[at * (D / 8) + lane] = wk;
+      reinterpret_cast<uint32_t*>(c.v)[at * (D / 8) + lane] = wv;
+      if ((lane & 7) == 0) {
+        c.km[at * (D / kC4Group) + (lane >> 3)] = mk;
+        c.vm[at * (D / kC4Group) + (lane >> 3)] = mv;
       }
-      uint32_t meta;
-      const uint32_t w = c4_quantise(x, &meta);
-      if (at >= 0) {
-        reinterpret_cast<uint32_t*>(kv ? c.v : c.k)[at * (D / 8) + lane] = w;
-        if ((lane & 7) == 0) (kv ? c.vm : c.km)[at * (D / kC4Group) + (lane >> 3)] = meta;
-      }
-    }
-    if (lane == 0) {
-      if (at >= 0) {
+      if (lane == 0) {
         if (weight != nullptr) weight[at] = 0.f;
         if (pos != nullptr)
           pos[at] = first_pos != nullptr ? __ldg(first_pos + b) + (slot - (g.slot0 != nullptr ? __ldg(g.slot0 + b) : 0))
                                          : slot;
-      } else if (dropped) {
-        atomicOr(&g_attn_status, kC4Overflow);
       }
+    } else if (dropped && lane == 0) {
+      atomicOr(&g_attn_status, kC4Overflow);
     }
   }
-  if (len_out != nullptr) {
-    for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
-         b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+  if (len_out != nullptr && h == 0) {
+    for (int64_t b = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
+         b += static_cast<int64_t>(gridDim.y) * blockDim.x) {
       const int64_t n = g.seq_start != nullptr ? max(0, __ldg(g.seq_start + b + 1) - __ldg(g.seq_start + b)) : 1;
       const int64_t l = max(0, __ldg(g.slot0 + b)) + n;
       len_out[b] = static_cast<int32_t>(l < c.cap ? l : c.cap);
@@ -208,10 +240,10 @@ __global__ void __launch_bounds__(kC4RowsThreads)
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kC4RowLanes<D>;
-  const int64_t n_chunks = (g.rows + kC4BlockRows<D> - 1) / kC4BlockRows<D>;
-  for (int64_t u = blockIdx.x; u < n_chunks * c.H; u += gridDim.x) {
-    const int h = static_cast<int>(u % c.H);
-    const int64_t row = (u / c.H) * kC4BlockRows<D> + threadIdx.x / kC4RowLanes<D>;
+  const int h = static_cast<int>(blockIdx.x);
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kC4BlockRows<D>; row0 < g.rows;
+       row0 += static_cast<int64_t>(gridDim.y) * kC4BlockRows<D>) {
+    const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
     int b, slot;
     bool dropped;
     const int64_t at = c4_row<D>(g, c, row, h, &b, &slot, &dropped);
@@ -1137,7 +1169,12 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
 // holes and movers before each slice come the same way.  Every key is read
 // from HBM once, whatever the budget.
 
-constexpr int kC4EvictThreads = 512;
+// Threads of a CTA.  1024 hide more of the latency of long slices and many moves
+// (24 sequences of up to 8192 entries cut to 2048: 26 us against 37 us with 512),
+// but an SM's registers hold one such CTA: where the slices are short, two of
+// 512 are faster (32 sequences of 2049 cut to 2048: 11 us against 20 us).
+constexpr int kC4EvictFew = 512, kC4EvictMany = 1024;
+constexpr int kC4EvictLong = 4096;  // a slice of more entries takes kC4EvictMany threads
 constexpr int kC4EvictCluster = 8;             // CTAs of a cluster at most
 constexpr int kC4EvictSmemKeys = 48 * 1024;    // keys a CTA can hold in shared memory
 
@@ -1189,6 +1226,7 @@ __device__ __forceinline__ uint32_t c4_rank_key(float w) {
 }
 
 // Sum over the block of (a, b) before this thread, and the totals.
+template <int kThreads>
 __device__ __forceinline__ uint2 block_scan2(uint2 v, uint2* warp_s, uint2* total) {
   const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
   uint2 incl = v;
@@ -1204,7 +1242,7 @@ __device__ __forceinline__ uint2 block_scan2(uint2 v, uint2* warp_s, uint2* tota
   if (lane == 31) warp_s[warp] = incl;
   __syncthreads();
   uint2 before = make_uint2(incl.x - v.x, incl.y - v.y), all = make_uint2(0, 0);
-  for (int w = 0; w < kC4EvictThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const uint2 s = warp_s[w];
     if (w < warp) {
       before.x += s.x;
@@ -1217,17 +1255,27 @@ __device__ __forceinline__ uint2 block_scan2(uint2 v, uint2* warp_s, uint2* tota
   return before;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kC4EvictThreads) attn_cache4_evict_kernel(const EvictParams p) {
+// kMulti: clusters of more than one CTA; without, the cluster barriers are the
+// block's own.
+template <int D, bool kMulti, int kThreads>
+__global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t smem_keys[];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t share[4];  // what the other CTAs read: newest, ties, holes, movers
-  __shared__ uint32_t found[2];  // digit, entries still to take
-  __shared__ uint2 warp_s[kC4EvictThreads / 32];
+  __shared__ uint32_t hist[2][256];  // rounds alternate, so that one is cleared while the other is read
+  __shared__ uint32_t share[4];      // what the other CTAs read: newest, ties, holes, movers
+  __shared__ uint32_t found[3];      // digit, entries still to take, entries with it
+  __shared__ uint2 warp_s[kThreads / 32];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
-  const uint32_t rank = cluster_rank(), R = cluster_size();
+  const uint32_t rank = kMulti ? cluster_rank() : 0u, R = kMulti ? cluster_size() : 1u;
+  const auto sync_all = [] {
+    if constexpr (kMulti)
+      cluster_sync_all();
+    else
+      __syncthreads();
+  };
+  const auto peer = [](const uint32_t* v, uint32_t q) { return kMulti ? ld_cluster_u32(v, q) : *static_cast<const volatile uint32_t*>(v); };
   const int64_t bh = blockIdx.x / R;
   const int b = static_cast<int>(bh / p.c.H);
+  if (tid < 256) hist[0][tid] = hist[1][tid] = 0u;
   grid_dependency_wait();
   const int n = c4_len(p.len, b, p.most);
   const int left = min(n, p.budget);
@@ -1235,56 +1283,80 @@ __global__ void __launch_bounds__(kC4EvictThreads) attn_cache4_evict_kernel(cons
   if (p.len_out != nullptr && bh % p.c.H == 0 && rank == 0 && tid == 0) p.len_out[b] = left;
   const int slice = (n + static_cast<int>(R) - 1) / static_cast<int>(R);
   const int i0 = min(n, static_cast<int>(rank) * slice), i1 = min(n, i0 + slice), mine = i1 - i0;
+  const float* const w_in = p.w_in + base + i0;
+  const int32_t* const p_in = p.p_in + base + i0;
   const bool copy_w = p.w_out != p.w_in, copy_p = p.p_out != p.p_in;
   if (n <= p.budget) {  // every entry stays where it is (the same for the whole cluster)
-    for (int i = i0 + tid; i < i1; i += kC4EvictThreads) {
-      if (copy_w) p.w_out[base + i] = p.w_in[base + i];
-      if (copy_p) p.p_out[base + i] = p.p_in[base + i];
+    for (int i = tid; i < mine; i += kThreads) {
+      if (copy_w) p.w_out[base + i0 + i] = w_in[i];
+      if (copy_p) p.p_out[base + i0 + i] = p_in[i];
     }
     grid_launch_dependents();
     return;
   }
   uint32_t* const key = slice <= p.smem_keys ? smem_keys : p.keys + bh * p.most + i0;
 
-  // Rank keys of the slice, and the newest position.
+  // Rank keys of the slice, and the newest position; four entries in flight a
+  // thread.
+  constexpr int kU = 4;
   int newest = INT_MIN;
-  for (int i = tid; i < mine; i += kC4EvictThreads) {
-    newest = max(newest, p.p_in[base + i0 + i]);
-    key[i] = c4_rank_key(p.w_in[base + i0 + i]);
+  for (int i = tid; i < mine; i += kU * kThreads) {
+    float w[kU];
+    int at[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int j = min(i + u * kThreads, mine - 1);
+      w[u] = w_in[j];
+      at[u] = p_in[j];
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      newest = max(newest, at[u]);
+      if (i + u * kThreads < mine) key[i + u * kThreads] = c4_rank_key(w[u]);
+    }
   }
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) warp_s[tid >> 5].x = static_cast<uint32_t>(newest);
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kC4EvictThreads / 32; ++w) newest = max(newest, static_cast<int>(warp_s[w].x));
-    share[0] = static_cast<uint32_t>(newest);
+  if (tid < 32) {
+    newest = tid < kThreads / 32 ? static_cast<int>(warp_s[tid].x) : INT_MIN;
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (tid == 0) share[0] = static_cast<uint32_t>(newest);
   }
-  cluster_sync_all();
-  newest = INT_MIN;
-  for (uint32_t q = 0; q < R; ++q) newest = max(newest, static_cast<int>(ld_cluster_u32(&share[0], q)));
+  sync_all();
   if (p.recent > 0) {
+    newest = INT_MIN;
+    for (uint32_t q = 0; q < R; ++q) newest = max(newest, static_cast<int>(peer(&share[0], q)));
     const int64_t old = static_cast<int64_t>(newest) - p.recent;
-    for (int i = tid; i < mine; i += kC4EvictThreads)
-      if (p.p_in[base + i0 + i] > old) key[i] = kC4Protected;
+    for (int i = tid; i < mine; i += kU * kThreads) {
+      int at[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) at[u] = p_in[min(i + u * kThreads, mine - 1)];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i + u * kThreads < mine && at[u] > old) key[i + u * kThreads] = kC4Protected;
+    }
   }
 
-  // The left-th largest key.
-  uint32_t prefix = 0u, take = static_cast<uint32_t>(left);
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int d = tid; d < 256; d += kC4EvictThreads) hist[d] = 0u;
-    __syncthreads();
-    const uint32_t seen = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int i = tid; i < mine; i += kC4EvictThreads) {
+  // The left-th largest key, digit by digit: `take` of the keys that agree with
+  // `prefix` in the digits seen are kept, and all above.  It ends early where
+  // all of them are (for weights that differ, mostly a digit early).
+  uint32_t prefix = 0u, take = static_cast<uint32_t>(left), seen = 0u;
+  bool ties = true;
+  for (int round = 0; round < 4 && ties; ++round) {
+    const int shift = 24 - 8 * round;
+    uint32_t* const h = hist[round & 1];
+    for (int i = tid; i < mine; i += kThreads) {
       const uint32_t k = key[i];
-      if ((k & seen) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      if ((k & seen) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1u);
     }
-    cluster_sync_all();
+    sync_all();
     if (tid < 32) {  // digits from the top: lane j has 255 - 8j .. 248 - 8j
       uint32_t cnt[8], sum = 0u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         cnt[e] = 0u;
-        for (uint32_t q = 0; q < R; ++q) cnt[e] += ld_cluster_u32(&hist[255 - 8 * lane - e], q);
+        for (uint32_t q = 0; q < R; ++q) cnt[e] += peer(&h[255 - 8 * lane - e], q);
         sum += cnt[e];
       }
       uint32_t incl = sum;
@@ -1300,50 +1372,65 @@ __global__ void __launch_bounds__(kC4EvictThreads) attn_cache4_evict_kernel(cons
           if (before < take && take <= before + cnt[e]) {
             found[0] = static_cast<uint32_t>(255 - 8 * lane - e);
             found[1] = take - before;
+            found[2] = cnt[e];
           }
           before += cnt[e];
         }
       }
+    } else if (tid < 32 + 256) {
+      // the other histogram: read in the round before, by every CTA before the
+      // barrier above
+      hist[(round & 1) ^ 1][tid - 32] = 0u;
     }
-    cluster_sync_all();  // found is set; every CTA has read the histograms
+    __syncthreads();
     prefix |= found[0] << shift;
+    seen |= 255u << shift;
     take = found[1];
+    ties = found[2] != take;
+    __syncthreads();  // found may be written again
   }
 
-  // Kept: keys above `prefix`, and the first `take` equal to it.  A thread
-  // walks consecutive slots (an odd count: no bank conflicts).
-  const int per = ((mine + kC4EvictThreads - 1) / kC4EvictThreads) | 1;
+  // Kept: keys above `prefix` in the digits seen, and the first `take` equal to
+  // it.  A thread walks consecutive slots (an odd count: no bank conflicts).
+  const int per = ((mine + kThreads - 1) / kThreads) | 1;
   const int s0 = min(mine, tid * per), s1 = min(mine, s0 + per);
   uint2 v = make_uint2(0, 0), all;
-  for (int i = s0; i < s1; ++i) v.x += key[i] == prefix;
-  const uint2 eq = block_scan2(v, warp_s, &all);
-  if (tid == 0) share[1] = all.x;
-  cluster_sync_all();
-  uint32_t eq_rank = eq.x;
-  for (uint32_t q = 0; q < rank; ++q) eq_rank += ld_cluster_u32(&share[1], q);
+  uint32_t eq_rank = 0u;
+  if (ties) {  // which of the equal ones: by their order
+    for (int i = s0; i < s1; ++i) v.x += (key[i] & seen) == prefix;
+    eq_rank = block_scan2<kThreads>(v, warp_s, &all).x;
+    if (kMulti) {
+      if (tid == 0) share[1] = all.x;
+      sync_all();
+      for (uint32_t q = 0; q < rank; ++q) eq_rank += peer(&share[1], q);
+    }
+  }
   v = make_uint2(0, 0);
   for (int i = s0; i < s1; ++i) {
-    const uint32_t k = key[i];
+    const uint32_t k = key[i] & seen;
     bool keep = k > prefix;
-    if (k == prefix) keep = eq_rank++ < take;
+    if (k == prefix) keep = !ties || eq_rank++ < take;
     key[i] = keep;
     v.x += !keep && i0 + i < left;  // a hole
     v.y += keep && i0 + i >= left;  // a mover
   }
-  const uint2 at = block_scan2(v, warp_s, &all);
-  if (tid == 0) {
-    share[2] = all.x;
-    share[3] = all.y;
-  }
-  cluster_sync_all();
-  uint32_t hole = at.x, mover = at.y, n_moves = 0u;
-  for (uint32_t q = 0; q < R; ++q) {
-    const uint32_t x = ld_cluster_u32(&share[2], q);
-    if (q < rank) {
-      hole += x;
-      mover += ld_cluster_u32(&share[3], q);
+  const uint2 at = block_scan2<kThreads>(v, warp_s, &all);
+  uint32_t hole = at.x, mover = at.y, n_moves = all.x;
+  if (kMulti) {
+    if (tid == 0) {
+      share[2] = all.x;
+      share[3] = all.y;
     }
-    n_moves += x;
+    sync_all();
+    n_moves = 0u;
+    for (uint32_t q = 0; q < R; ++q) {
+      const uint32_t x = peer(&share[2], q);
+      if (q < rank) {
+        hole += x;
+        mover += peer(&share[3], q);
+      }
+      n_moves += x;
+    }
   }
   int32_t* const holes = p.moves + bh * 2 * p.list;
   int32_t* const movers = holes + p.list;
@@ -1352,36 +1439,57 @@ __global__ void __launch_bounds__(kC4EvictThreads) attn_cache4_evict_kernel(cons
     if (!keep && i0 + i < left) holes[hole++] = i0 + i;
     if (keep && i0 + i >= left) movers[mover++] = i0 + i;
   }
+  sync_all();  // the lists are written; no CTA reads another's shared memory any more
+  grid_launch_dependents();
   if (copy_w || copy_p) {
-    __syncthreads();
-    for (int i = tid; i < mine && i0 + i < left; i += kC4EvictThreads) {
+    for (int i = tid; i < min(mine, left - i0); i += kThreads) {
       if (key[i] == 0u) continue;
-      if (copy_w) p.w_out[base + i0 + i] = p.w_in[base + i0 + i];
-      if (copy_p) p.p_out[base + i0 + i] = p.p_in[base + i0 + i];
+      if (copy_w) p.w_out[base + i0 + i] = w_in[i];
+      if (copy_p) p.p_out[base + i0 + i] = p_in[i];
     }
   }
-  cluster_sync_all();  // the lists are written; no CTA reads another's shared memory any more
-  grid_launch_dependents();
 
-  // The moves, 16 bytes a lane: half of a move's lanes take K, half V.
+  // The moves, 16 bytes a lane: half of a move's lanes take K, half V; four
+  // moves in flight each.
   constexpr int kLanes = D / 16;
   constexpr int kWords = D / 32;  // 16-byte words of a row
-  const int part = tid % kLanes;
+  constexpr int kMeta = D / kC4Group;
+  const int part = tid % kLanes, word = part % kWords;
   const bool is_v = part >= kWords;
   uint8_t* const codes = is_v ? p.c.v : p.c.k;
   uint32_t* const meta = is_v ? p.c.vm : p.c.km;
-  for (uint32_t m = rank * (kC4EvictThreads / kLanes) + tid / kLanes; m < n_moves;
-       m += R * (kC4EvictThreads / kLanes)) {
-    const int64_t to = base + __ldcg(holes + m), from = base + __ldcg(movers + m);
-    const uint4 x = *(reinterpret_cast<const uint4*>(codes + from * (D / 2)) + part % kWords);
-    *(reinterpret_cast<uint4*>(codes + to * (D / 2)) + part % kWords) = x;
-    if (part % kWords == 0) {
+  const uint32_t step = R * (kThreads / kLanes);
+  for (uint32_t m = rank * (kThreads / kLanes) + tid / kLanes; m < n_moves; m += kU * step) {
+    int64_t to[kU], from[kU];
+    uint4 x[kU];
+    uint32_t sm[kU][kMeta], extra[kU];
 #pragma unroll
-      for (int g = 0; g < D / kC4Group; ++g) meta[to * (D / kC4Group) + g] = meta[from * (D / kC4Group) + g];
-      if (is_v)
-        p.p_out[to] = p.p_in[from];
-      else
-        p.w_out[to] = p.w_in[from];
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t j = min(m + u * step, n_moves - 1);
+      to[u] = base + __ldcg(holes + j);
+      from[u] = base + __ldcg(movers + j);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      x[u] = *(reinterpret_cast<const uint4*>(codes + from[u] * (D / 2)) + word);
+      if (word == 0) {
+#pragma unroll
+        for (int g = 0; g < kMeta; ++g) sm[u][g] = meta[from[u] * kMeta + g];
+        extra[u] = is_v ? static_cast<uint32_t>(p.p_in[from[u]]) : __float_as_uint(p.w_in[from[u]]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (m + u * step >= n_moves) break;
+      *(reinterpret_cast<uint4*>(codes + to[u] * (D / 2)) + word) = x[u];
+      if (word == 0) {
+#pragma unroll
+        for (int g = 0; g < kMeta; ++g) meta[to[u] * kMeta + g] = sm[u][g];
+        if (is_v)
+          p.p_out[to[u]] = static_cast<int32_t>(extra[u]);
+        else
+          p.w_out[to[u]] = __uint_as_float(extra[u]);
+      }
     }
   }
 }
@@ -1400,6 +1508,13 @@ __global__ void attn_cache4_cut_kernel(int32_t* len, int B, int most, int budget
 // Host side
 // ---------------------------------------------------------------------------
 
+using EvictKernel = void (*)(EvictParams);
+// by D = 128, a cluster of several CTAs, long slices
+constexpr EvictKernel kEvictKernels[8] = {
+    attn_cache4_evict_kernel<64, false, kC4EvictFew>,  attn_cache4_evict_kernel<64, false, kC4EvictMany>,
+    attn_cache4_evict_kernel<64, true, kC4EvictFew>,   attn_cache4_evict_kernel<64, true, kC4EvictMany>,
+    attn_cache4_evict_kernel<128, false, kC4EvictFew>, attn_cache4_evict_kernel<128, false, kC4EvictMany>,
+    attn_cache4_evict_kernel<128, true, kC4EvictFew>,  attn_cache4_evict_kernel<128, true, kC4EvictMany>};
 std::atomic<int> g_cache4_state[kMaxDevices];  // 1: shared-memory limits set
 
 attn_status_t prepare_cache4(int* dev, int* sms) {
@@ -1407,11 +1522,10 @@ attn_status_t prepare_cache4(int* dev, int* sms) {
   const attn_status_t ps = prepare_device(*dev);
   if (ps != ATTN_OK) return ps;
   if (g_cache4_state[*dev].load(std::memory_order_acquire) == 0) {
-    if (cudaFuncSetAttribute(attn_cache4_evict_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kC4EvictSmemKeys * 4) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_cache4_evict_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kC4EvictSmemKeys * 4) != cudaSuccess)
-      return ATTN_ERR_DEVICE;
+    for (const EvictKernel k : kEvictKernels)
+      if (cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kC4EvictSmemKeys * 4) != cudaSuccess)
+        return ATTN_ERR_DEVICE;
     g_cache4_state[*dev].store(1, std::memory_order_release);
   }
   *sms = g_dev_sms[*dev].load(std::memory_order_relaxed);
@@ -1458,10 +1572,11 @@ attn_status_t check_rows(const attn_cache4_t* c, const void* k, const void* v, i
   return ATTN_OK;
 }
 
+// key heads x chunks of rows
 template <int D>
-unsigned rows_grid(int64_t rows, int H, int sms) {
-  const int64_t units = (rows + kC4BlockRows<D> - 1) / kC4BlockRows<D> * H;
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(units, static_cast<int64_t>(sms) * 64)));
+dim3 rows_grid(int64_t rows, int H) {
+  const int64_t chunks = (rows + kC4BlockRows<D> - 1) / kC4BlockRows<D>;
+  return dim3(static_cast<unsigned>(H), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(chunks, 65535))));
 }
 
 // Workspace of a decode call: partial O, partial (m, l), and with weights the
@@ -1501,9 +1616,10 @@ attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t strea
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
-// CTAs of an eviction's clusters: enough to give the GPU about two CTAs an SM,
-// and slices of at least 1024 entries; or as many as hold the keys in shared
-// memory.
+// CTAs of an eviction's clusters: enough to give every SM one, with slices of
+// at least 1024 entries; or as many as hold the keys in shared memory.  More
+// clusters than that lose: with pairs for 256 rows of 2049 entries a call took
+// 39 us instead of 11, with fours for 192 rows of up to 8192 52 instead of 37.
 int evict_cluster(int64_t BH, int max_len) {
   int R = 1;
   while (R < kC4EvictCluster && ((BH * R < kC4WorkspaceSms && max_len / (2 * R) >= 1024) || max_len > R * kC4EvictSmemKeys)) R *= 2;
@@ -1539,17 +1655,17 @@ attn_status_t attn_cache4_append(const attn_cache4_t* cache, const void* k, cons
   int32_t* const len_out = in_place ? nullptr : length_out;
   const uint16_t* k16 = static_cast<const uint16_t*>(k);
   const uint16_t* v16 = static_cast<const uint16_t*>(v);
-  const auto run = [&](auto kernel, unsigned grid) {
-    return launch_pdl(kernel, dim3(grid), dim3(kC4RowsThreads), 0, s, k16, v16, g, c, cache->weight, cache->pos, first_pos,
+  const auto run = [&](auto kernel, dim3 grid) {
+    return launch_pdl(kernel, grid, dim3(kC4RowsThreads), 0, s, k16, v16, g, c, cache->weight, cache->pos, first_pos,
                       len_out);
   };
   cudaError_t e;
   if (cache->D == 64)
-    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<64, kBF16>, rows_grid<64>(rows, c.H, sms))
-                           : run(attn_cache4_append_kernel<64, kFP16>, rows_grid<64>(rows, c.H, sms));
+    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<64, kBF16>, rows_grid<64>(rows, c.H))
+                           : run(attn_cache4_append_kernel<64, kFP16>, rows_grid<64>(rows, c.H));
   else
-    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<128, kBF16>, rows_grid<128>(rows, c.H, sms))
-                           : run(attn_cache4_append_kernel<128, kFP16>, rows_grid<128>(rows, c.H, sms));
+    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<128, kBF16>, rows_grid<128>(rows, c.H))
+                           : run(attn_cache4_append_kernel<128, kFP16>, rows_grid<128>(rows, c.H));
   if (e == cudaSuccess && in_place)
     e = launch_pdl(attn_cache4_grow_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
                    seq_start, length_out, cache->B, cache->capacity);
@@ -1571,17 +1687,17 @@ attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int
   if (st != ATTN_OK) return st;
   const Cache4 c = cache4_of(cache);
   const Cache4Rows g{seq_start, first_slot, cache->B, rows, k_stride, v_stride};
-  const auto run = [&](auto kernel, unsigned grid) {
-    return launch_pdl(kernel, dim3(grid), dim3(kC4RowsThreads), 0, static_cast<cudaStream_t>(stream), k, v, g, c);
+  const auto run = [&](auto kernel, dim3 grid) {
+    return launch_pdl(kernel, grid, dim3(kC4RowsThreads), 0, static_cast<cudaStream_t>(stream), k, v, g, c);
   };
   cudaError_t e;
   if (cache->D == 64) {
-    const unsigned grid = rows_grid<64>(rows, c.H, sms);
+    const dim3 grid = rows_grid<64>(rows, c.H);
     e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<64, kBF16>, grid)
         : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<64, kFP16>, grid)
                              : run(attn_cache4_read_kernel<64, kFP32>, grid);
   } else {
-    const unsigned grid = rows_grid<128>(rows, c.H, sms);
+    const dim3 grid = rows_grid<128>(rows, c.H);
     e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<128, kBF16>, grid)
         : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<128, kFP16>, grid)
                              : run(attn_cache4_read_kernel<128, kFP32>, grid);
@@ -1701,13 +1817,13 @@ attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int rece
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(BH * R));
-  cfg.blockDim = dim3(kC4EvictThreads);
+  const bool many = slice > kC4EvictLong;
+  cfg.blockDim = dim3(many ? kC4EvictMany : kC4EvictFew);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t e = cache->D == 64 ? cudaLaunchKernelEx(&cfg, attn_cache4_evict_kernel<64>, p)
-                                 : cudaLaunchKernelEx(&cfg, attn_cache4_evict_kernel<128>, p);
+  cfg.numAttrs = R > 1 ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kEvictKernels[(cache->D == 128 ? 4 : 0) + (R > 1 ? 2 : 0) + (many ? 1 : 0)], p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess && in_place)
     e = launch_pdl(attn_cache4_cut_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
