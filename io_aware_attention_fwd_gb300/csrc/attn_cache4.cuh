@@ -57,36 +57,38 @@ struct Cache4Rows {
 };
 
 // Blocks of kC4RowsThreads threads; 8 channels (one 4-byte word of codes) a
-// thread.  A block takes the same 16 (D = 128) or 32 (D = 64) tokens of one
-// key head: consecutive blocks read neighbouring heads of those tokens, and
-// each block writes one contiguous piece of the cache.
+// thread.  A block takes 16 (D = 128) or 32 (D = 64) packed rows and walks a run
+// of their key heads, so the search for a row's sequence is made once; few rows
+// are spread over more blocks by shorter runs.
 constexpr int kC4RowsThreads = 256;
 template <int D>
 constexpr int kC4RowLanes = D / 8;
 template <int D>
 constexpr int kC4BlockRows = kC4RowsThreads / kC4RowLanes<D>;
 
-// Finds this thread's row: token row, head and cache entry index
-// ((b*H + h)*cap + slot), or -1 for nothing to do.
-template <int D>
-__device__ __forceinline__ int64_t c4_row(const Cache4Rows& g, const Cache4& c, int64_t row, int h, int* b_out,
-                                          int* slot_out, bool* dropped) {
-  *dropped = false;
-  if (row >= g.rows) return -1;
-  int b = static_cast<int>(row), i = 0;
+// This thread's row: where it goes in the first key head's entries (b*H*cap +
+// slot, -1 for nothing to do), sequence and slot.
+struct C4Row {
+  int64_t at;
+  int b, slot;
+  bool dropped;  // a row of a sequence, but of no slot there is
+};
+__device__ __forceinline__ C4Row c4_row(const Cache4Rows& g, const Cache4& c, int64_t row) {
+  C4Row r{-1, 0, 0, false};
+  if (row >= g.rows) return r;
+  int i = 0;
+  r.b = static_cast<int>(row);
   if (g.seq_start != nullptr) {
-    b = seq_of_row(g.seq_start, g.B, static_cast<int>(row));
-    if (b >= g.B) return -1;
-    i = static_cast<int>(row) - __ldg(g.seq_start + b);
+    r.b = seq_of_row(g.seq_start, g.B, static_cast<int>(row));
+    if (r.b >= g.B) return r;
+    i = static_cast<int>(row) - __ldg(g.seq_start + r.b);
   }
-  const int64_t slot = static_cast<int64_t>(i) + (g.slot0 != nullptr ? __ldg(g.slot0 + b) : 0);
-  *b_out = b;
-  *slot_out = static_cast<int>(slot);
-  if (slot < 0 || slot >= c.cap) {
-    *dropped = true;
-    return -1;
-  }
-  return (static_cast<int64_t>(b) * c.H + h) * c.cap + slot;
+  const int64_t slot = static_cast<int64_t>(i) + (g.slot0 != nullptr ? __ldg(g.slot0 + r.b) : 0);
+  r.dropped = slot < 0 || slot >= c.cap;
+  if (r.dropped) return r;
+  r.slot = static_cast<int>(slot);
+  r.at = static_cast<int64_t>(r.b) * c.H * c.cap + slot;
+  return r;
 }
 
 // Packed 16-bit minimum and maximum that pass a NaN on.
@@ -134,9 +136,12 @@ __device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta
     *meta = 0x7fc07fc0u;                     // (NaN, NaN)
     return 0u;
   }
-  const uint32_t sm = pack_bf16x2(__fdiv_rn(__fsub_rn(hi, lo), 15.f), lo);
-  *meta = sm;
-  const float s = bf16_lo(sm), m = bf16_hi(sm);
+  const float range = __fsub_rn(hi, lo);
+  constexpr float kFifteenth = 1.f / 15.f;
+  float q0 = __fmul_rn(range, kFifteenth);
+  uint32_t sm = pack_bf16x2(__fmaf_rn(__fmaf_rn(-q0, 15.f, range), kFifteenth, q0), lo);
+  float s = bf16_lo(sm);
+  const float m = bf16_hi(sm);
   float x[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -144,24 +149,31 @@ __device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta
     x[2 * e] = __fsub_rn(f.x, m);
     x[2 * e + 1] = __fsub_rn(f.y, m);
   }
+  uint32_t w = 0u;
   if (s >= 0x1p-100f && s <= 0x1p100f) {
     const float y = __frcp_rn(s);
+    // Rounding half to even by adding 1.5 * 2^23 leaves the code in the low bits
+    // of a constant, which comes off the packed word once.
+    // m is min x itself for bf16, so d / s lies within 0 .. 15.06; fp16's
+    // minimum is rounded to bf16, so there it may fall outside.
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q0 = __fmul_rn(x[e], y);
-      x[e] = __fmaf_rn(__fmaf_rn(-q0, s, x[e]), y, q0);
+    for (int e = 7; e >= 0; --e) {
+      q0 = __fmul_rn(x[e], y);
+      float c = __fmaf_rn(__fmaf_rn(-q0, s, x[e]), y, q0);
+      if constexpr (kType == kFP16) c = fminf(fmaxf(c, 0.f), 15.f);
+      w = w * 16u + __float_as_uint(__fadd_rn(c, 12582912.f));
     }
+    w -= 0x4b400000u * 0x11111111u;
   } else {
+    sm = pack_bf16x2(__fdiv_rn(range, 15.f), lo);
+    s = bf16_lo(sm);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s != 0.f ? __fdiv_rn(x[e], s) : 0.f;
+    for (int e = 7; e >= 0; --e) {
+      const float c = s != 0.f ? rintf(fminf(fmaxf(__fdiv_rn(x[e], s), 0.f), 15.f)) : 0.f;
+      w = w * 16u + static_cast<uint32_t>(c);
+    }
   }
-  // round half to even by adding 1.5 * 2^23; the code is then in the low bits
-  uint32_t w = 0u;
-#pragma unroll
-  for (int e = 7; e >= 0; --e) {
-    const float c = __fadd_rn(fminf(fmaxf(x[e], 0.f), 15.f), 12582912.f);
-    w = w * 16u + (__float_as_uint(c) & 15u);
-  }
+  *meta = sm;
   return w;
 }
 
@@ -172,26 +184,36 @@ __device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta
 template <int D, int kType>
 __global__ void __launch_bounds__(kC4RowsThreads)
     attn_cache4_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, Cache4Rows g, Cache4 c,
-                              float* __restrict__ weight, int32_t* __restrict__ pos,
+                              int heads, float* __restrict__ weight, int32_t* __restrict__ pos,
                               const int32_t* __restrict__ first_pos, int32_t* __restrict__ len_out) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kC4RowLanes<D>;
-  const int h = static_cast<int>(blockIdx.x);
+  const int h0 = static_cast<int>(blockIdx.x) * heads, h1 = min(c.H, h0 + heads);
   for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kC4BlockRows<D>; row0 < g.rows;
        row0 += static_cast<int64_t>(gridDim.y) * kC4BlockRows<D>) {
     const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
-    uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
-    if (row < g.rows) {  // the loads need no sequence: they go out before its search
-      xk = __ldg(reinterpret_cast<const uint4*>(k + row * g.k_stride + h * D + lane * 8));
-      xv = __ldg(reinterpret_cast<const uint4*>(v + row * g.v_stride + h * D + lane * 8));
-    }
-    int b = 0, slot = 0;
-    bool dropped;
-    const int64_t at = c4_row<D>(g, c, row, h, &b, &slot, &dropped);
-    uint32_t mk, mv;
-    const uint32_t wk = c4_quantise<kType>(xk, &mk), wv = c4_quantise<kType>(xv, &mv);
-    if (at >= 0) {
+    const C4Row r = c4_row(g, c, row);
+    if (r.dropped && lane == 0 && h0 == 0) atomicOr(&g_attn_status, kC4Overflow);
+    const int my_pos = r.at < 0 ? 0 : first_pos != nullptr ? __ldg(first_pos + r.b) + (r.slot - __ldg(g.slot0 + r.b)) : r.slot;
+    const int64_t from = r.at < 0 ? 0 : row;  // the others go through the motions: the statistics are whole warps'
+    const uint16_t* kp = k + from * g.k_stride + h0 * D + lane * 8;
+    const uint16_t* vp = v + from * g.v_stride + h0 * D + lane * 8;
+    int64_t at = r.at + static_cast<int64_t>(h0) * c.cap;
+    // the next head's values travel while this one's are quantised
+    uint4 nk = __ldg(reinterpret_cast<const uint4*>(kp)), nv = __ldg(reinterpret_cast<const uint4*>(vp));
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, at += c.cap) {
+      const uint4 xk = nk, xv = nv;
+      if (h + 1 < h1) {
+        kp += D;
+        vp += D;
+        nk = __ldg(reinterpret_cast<const uint4*>(kp));
+        nv = __ldg(reinterpret_cast<const uint4*>(vp));
+      }
+      uint32_t mk, mv;
+      const uint32_t wk = c4_quantise<kType>(xk, &mk), wv = c4_quantise<kType>(xv, &mv);
+      if (r.at < 0) continue;
       reinterpret_cast<uint32_t*>(c.k)[at * (D / 8) + lane] = wk;
       reinterpret_cast<uint32_t*>(c.v)[at * (D / 8) + lane] = wv;
       if ((lane & 7) == 0) {
@@ -200,15 +222,11 @@ __global__ void __launch_bounds__(kC4RowsThreads)
       }
       if (lane == 0) {
         if (weight != nullptr) weight[at] = 0.f;
-        if (pos != nullptr)
-          pos[at] = first_pos != nullptr ? __ldg(first_pos + b) + (slot - (g.slot0 != nullptr ? __ldg(g.slot0 + b) : 0))
-                                         : slot;
+        if (pos != nullptr) pos[at] = my_pos;
       }
-    } else if (dropped && lane == 0) {
-      atomicOr(&g_attn_status, kC4Overflow);
     }
   }
-  if (len_out != nullptr && h == 0) {
+  if (len_out != nullptr && h0 == 0) {
     for (int64_t b = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
          b += static_cast<int64_t>(gridDim.y) * blockDim.x) {
       const int64_t n = g.seq_start != nullptr ? max(0, __ldg(g.seq_start + b + 1) - __ldg(g.seq_start + b)) : 1;
@@ -234,40 +252,60 @@ __global__ void attn_cache4_grow_kernel(const int32_t* __restrict__ seq_start, i
 // Reads entries back into packed rows: c*s + m, rounded once to the output's
 // type.  c*s + m is exact in fp32 wherever s and m are within 2^12 of each
 // other (4 + 8 bits of c*s against 8 of m).
+// Codes become numbers by ORing them, where they are, into the mantissa of
+// 2^23: 2^23 + c * 16^e, of which the sum with -2^23 is exact.
 template <int D, int kType>
 __global__ void __launch_bounds__(kC4RowsThreads)
-    attn_cache4_read_kernel(void* __restrict__ k, void* __restrict__ v, Cache4Rows g, Cache4 c) {
+    attn_cache4_read_kernel(void* __restrict__ k, void* __restrict__ v, Cache4Rows g, Cache4 c, int heads) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kC4RowLanes<D>;
-  const int h = static_cast<int>(blockIdx.x);
+  const int h0 = static_cast<int>(blockIdx.x) * heads, h1 = min(c.H, h0 + heads);
   for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kC4BlockRows<D>; row0 < g.rows;
        row0 += static_cast<int64_t>(gridDim.y) * kC4BlockRows<D>) {
     const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
-    int b, slot;
-    bool dropped;
-    const int64_t at = c4_row<D>(g, c, row, h, &b, &slot, &dropped);
-    if (at < 0) continue;
-    const uint32_t wk = __ldg(reinterpret_cast<const uint32_t*>(c.k) + at * (D / 8) + lane);
-    const uint32_t wv = __ldg(reinterpret_cast<const uint32_t*>(c.v) + at * (D / 8) + lane);
-    const uint32_t mk = __ldg(c.km + at * (D / kC4Group) + (lane >> 3));
-    const uint32_t mv = __ldg(c.vm + at * (D / kC4Group) + (lane >> 3));
+    const C4Row r = c4_row(g, c, row);
+    if (r.at < 0) continue;
+    int64_t at = r.at + static_cast<int64_t>(h0) * c.cap;
+    // the next head's codes travel while this one's are turned into values
+    uint32_t n[4];
+    const auto load = [&] {
+      n[0] = __ldg(reinterpret_cast<const uint32_t*>(c.k) + at * (D / 8) + lane);
+      n[1] = __ldg(reinterpret_cast<const uint32_t*>(c.v) + at * (D / 8) + lane);
+      n[2] = __ldg(c.km + at * (D / kC4Group) + (lane >> 3));
+      n[3] = __ldg(c.vm + at * (D / kC4Group) + (lane >> 3));
+    };
+    load();
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+      const uint32_t wk = n[0], wv = n[1], mk = n[2], mv = n[3];
+      if (h + 1 < h1) {
+        at += c.cap;
+        load();
+      }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t w = kv ? wv : wk, sm = kv ? mv : mk;
-      const float s = bf16_lo(sm), m = bf16_hi(sm);
-      float x[8];
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t w = kv ? wv : wk, sm = kv ? mv : mk, half[2] = {w, w >> 16};
+        const float s = bf16_lo(sm), m = bf16_hi(sm);
+        const float scale[4] = {s, s * 0x1p-4f, s * 0x1p-8f, s * 0x1p-12f};
+        float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(static_cast<float>((w >> (4 * e)) & 15u), s, m);
-      const int64_t to = row * (kv ? g.v_stride : g.k_stride) + h * D + lane * 8;
-      if constexpr (kType == kFP32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(kv ? v : k) + to);
-        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-      } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? v : k) + to) =
-            make_uint4(pack_16x2<kType>(x[0], x[1]), pack_16x2<kType>(x[2], x[3]), pack_16x2<kType>(x[4], x[5]),
-                       pack_16x2<kType>(x[6], x[7]));
+        for (int e = 0; e < 8; ++e)
+          x[e] = fmaf(__uint_as_float((half[e >> 2] & (15u << (4 * (e & 3)))) | 0x4b000000u) - 8388608.f, scale[e & 3], m);
+        if (s < 0x1p-100f) {  // the scaled s may be subnormal
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = fmaf(static_cast<float>((w >> (4 * e)) & 15u), s, m);
+        }
+        const int64_t to = row * (kv ? g.v_stride : g.k_stride) + h * D + lane * 8;
+        if constexpr (kType == kFP32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(kv ? v : k) + to);
+          dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+          dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? v : k) + to) =
+              make_uint4(pack_16x2<kType>(x[0], x[1]), pack_16x2<kType>(x[2], x[3]), pack_16x2<kType>(x[4], x[5]),
+                         pack_16x2<kType>(x[6], x[7]));
+        }
       }
     }
   }
@@ -1572,11 +1610,20 @@ attn_status_t check_rows(const attn_cache4_t* c, const void* k, const void* v, i
   return ATTN_OK;
 }
 
-// key heads x chunks of rows
-template <int D>
-dim3 rows_grid(int64_t rows, int H) {
-  const int64_t chunks = (rows + kC4BlockRows<D> - 1) / kC4BlockRows<D>;
-  return dim3(static_cast<unsigned>(H), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(chunks, 65535))));
+// Key heads a block walks, so that there are four blocks an SM or a block for
+// every key head, and the grid: runs of key heads x chunks of rows.
+struct RowsGrid {
+  int heads;
+  dim3 grid;
+};
+RowsGrid rows_grid(int64_t rows, int D, int H, int sms) {
+  const int64_t block_rows = D == 64 ? kC4BlockRows<64> : kC4BlockRows<128>;
+  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((rows + block_rows - 1) / block_rows, 65535));
+  const int64_t runs = std::min<int64_t>(H, std::max<int64_t>(1, (4 * sms + chunks - 1) / chunks));
+  RowsGrid r;
+  r.heads = static_cast<int>((H + runs - 1) / runs);
+  r.grid = dim3(static_cast<unsigned>((H + r.heads - 1) / r.heads), static_cast<unsigned>(chunks));
+  return r;
 }
 
 // Workspace of a decode call: partial O, partial (m, l), and with weights the
@@ -1655,17 +1702,16 @@ attn_status_t attn_cache4_append(const attn_cache4_t* cache, const void* k, cons
   int32_t* const len_out = in_place ? nullptr : length_out;
   const uint16_t* k16 = static_cast<const uint16_t*>(k);
   const uint16_t* v16 = static_cast<const uint16_t*>(v);
-  const auto run = [&](auto kernel, dim3 grid) {
-    return launch_pdl(kernel, grid, dim3(kC4RowsThreads), 0, s, k16, v16, g, c, cache->weight, cache->pos, first_pos,
-                      len_out);
+  const RowsGrid rg = rows_grid(rows, cache->D, c.H, sms);
+  const auto run = [&](auto kernel) {
+    return launch_pdl(kernel, rg.grid, dim3(kC4RowsThreads), 0, s, k16, v16, g, c, rg.heads, cache->weight, cache->pos,
+                      first_pos, len_out);
   };
   cudaError_t e;
   if (cache->D == 64)
-    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<64, kBF16>, rows_grid<64>(rows, c.H))
-                           : run(attn_cache4_append_kernel<64, kFP16>, rows_grid<64>(rows, c.H));
+    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<64, kBF16>) : run(attn_cache4_append_kernel<64, kFP16>);
   else
-    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<128, kBF16>, rows_grid<128>(rows, c.H))
-                           : run(attn_cache4_append_kernel<128, kFP16>, rows_grid<128>(rows, c.H));
+    e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<128, kBF16>) : run(attn_cache4_append_kernel<128, kFP16>);
   if (e == cudaSuccess && in_place)
     e = launch_pdl(attn_cache4_grow_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
                    seq_start, length_out, cache->B, cache->capacity);
@@ -1687,21 +1733,19 @@ attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int
   if (st != ATTN_OK) return st;
   const Cache4 c = cache4_of(cache);
   const Cache4Rows g{seq_start, first_slot, cache->B, rows, k_stride, v_stride};
-  const auto run = [&](auto kernel, dim3 grid) {
-    return launch_pdl(kernel, grid, dim3(kC4RowsThreads), 0, static_cast<cudaStream_t>(stream), k, v, g, c);
+  const RowsGrid rg = rows_grid(rows, cache->D, c.H, sms);
+  const auto run = [&](auto kernel) {
+    return launch_pdl(kernel, rg.grid, dim3(kC4RowsThreads), 0, static_cast<cudaStream_t>(stream), k, v, g, c, rg.heads);
   };
   cudaError_t e;
-  if (cache->D == 64) {
-    const dim3 grid = rows_grid<64>(rows, c.H);
-    e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<64, kBF16>, grid)
-        : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<64, kFP16>, grid)
-                             : run(attn_cache4_read_kernel<64, kFP32>, grid);
-  } else {
-    const dim3 grid = rows_grid<128>(rows, c.H);
-    e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<128, kBF16>, grid)
-        : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<128, kFP16>, grid)
-                             : run(attn_cache4_read_kernel<128, kFP32>, grid);
-  }
+  if (cache->D == 64)
+    e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<64, kBF16>)
+        : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<64, kFP16>)
+                             : run(attn_cache4_read_kernel<64, kFP32>);
+  else
+    e = dtype == ATTN_BF16   ? run(attn_cache4_read_kernel<128, kBF16>)
+        : dtype == ATTN_FP16 ? run(attn_cache4_read_kernel<128, kFP16>)
+                             : run(attn_cache4_read_kernel<128, kFP32>);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
