@@ -7,6 +7,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 from .build_ext import LIB_PATH
@@ -256,6 +257,7 @@ def attn_fwd_varlen(q, k, v, o, lse, total: int, seq_start, n_seqs: int, H_q: in
         raise AttnError(st, "attn_fwd_varlen")
 
 
+@functools.lru_cache(maxsize=256)
 def attn_fwd_varlen_workspace_bytes(total: int, n_seqs: int, H_q: int, H_kv: int, D: int) -> int:
     return load().attn_fwd_varlen_workspace_bytes(total, n_seqs, H_q, H_kv, D)
 
@@ -288,6 +290,7 @@ def attn_cache4_decode(cache: attn_cache4_t, q, q_stride: int, o, lse, H_q: int,
         raise AttnError(st, "attn_cache4_decode")
 
 
+@functools.lru_cache(maxsize=256)
 def attn_cache4_decode_workspace_bytes(B: int, H_q: int, H_kv: int, D: int, max_len: int, with_weight: bool) -> int:
     return load().attn_cache4_decode_workspace_bytes(B, H_q, H_kv, D, max_len, int(bool(with_weight)))
 
@@ -301,6 +304,7 @@ def attn_cache4_evict(cache: attn_cache4_t, budget: int, recent: int, max_len: i
         raise AttnError(st, "attn_cache4_evict")
 
 
+@functools.lru_cache(maxsize=256)
 def attn_cache4_evict_workspace_bytes(B: int, H_kv: int, max_len: int, budget: int) -> int:
     return load().attn_cache4_evict_workspace_bytes(B, H_kv, max_len, budget)
 

@@ -73,17 +73,19 @@ class KVCache4:
                    torch.zeros(B, dtype=torch.int32, device=device))
 
     def _rows(self, k, v, seq_start, also_fp32=False):
-        if k.dim() != 3 or k.shape != v.shape or k.shape[1] != self.H_kv or k.shape[2] != self.D:
+        shape, device, dtype = k.shape, self.device, k.dtype
+        if len(shape) != 3 or v.shape != shape or shape[1] != self.H_kv or shape[2] != self.D:
             raise ValueError(f"k and v must be [rows, {self.H_kv}, {self.D}]")
-        if k.device != self.device or v.device != self.device:
-            raise ValueError(f"k and v must be on {self.device}")
-        if k.dtype != v.dtype:
+        if k.device != device or v.device != device:
+            raise ValueError(f"k and v must be on {device}")
+        if v.dtype != dtype:
             raise TypeError("k and v must be of one type")
+        rows = shape[0]
         if seq_start is not None:
-            check_int32(seq_start, self.B + 1, self.device, "seq_start")
-        elif k.shape[0] != self.B:
+            check_int32(seq_start, self.B + 1, device, "seq_start")
+        elif rows != self.B:
             raise ValueError(f"without seq_start k and v have one row for each of the {self.B} sequences")
-        return k.shape[0], row_stride(k, "k"), row_stride(v, "v"), element_type(k.dtype, also_fp32)
+        return rows, row_stride(k, shape, "k"), row_stride(v, shape, "v"), element_type(dtype, also_fp32)
 
     def append(self, k, v, seq_start=None, first_pos=None, length_out=None, stream=None) -> None:
         """Quantise rows of K and V (bf16 or fp16, [rows, H_kv, D]) into the next entries.
@@ -148,16 +150,16 @@ class KVCache4:
         """
         import torch
 
-        B, D, device, dtype = self.B, self.D, self.device, q.dtype
-        if q.dim() != 3 or q.shape[0] != B or q.shape[2] != D or q.shape[1] < 1 or q.shape[1] % self.H_kv:
+        B, D, device, dtype, shape = self.B, self.D, self.device, q.dtype, q.shape
+        if len(shape) != 3 or shape[0] != B or shape[2] != D or shape[1] < 1 or shape[1] % self.H_kv:
             raise ValueError(f"q must be [{B}, H_q, {D}], H_q a multiple of {self.H_kv}")
         if q.device != device:
             raise ValueError(f"q must be on {device}")
-        H_q, code, stride = q.shape[1], element_type(dtype), row_stride(q, "q")
+        H_q, code, stride = shape[1], element_type(dtype), row_stride(q, shape, "q")
         if weight_out is not None:
             check_out(weight_out, self.weight.shape, torch.float32, device, "weight_out")
         if out is not None:
-            check_out(out, q.shape, dtype, device, "out")
+            check_out(out, shape, dtype, device, "out")
         if lse is not None:
             check_out(lse, (B, H_q), torch.float32, device, "lse")
         if max_len is None:
@@ -167,7 +169,7 @@ class KVCache4:
         nbytes = _lib.attn_cache4_decode_workspace_bytes(B, H_q, self.H_kv, D, max_len, weight_out is not None)
 
         def call(handle):
-            o = out if out is not None else torch.empty((B, H_q, D), dtype=dtype, device=device)
+            o = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
             z = lse if lse is not None else torch.empty((B, H_q), dtype=torch.float32, device=device)
             ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
             _lib.attn_cache4_decode(self._c, q, stride, o, z, H_q, code, scale, max_len,
