@@ -12,7 +12,9 @@
 //   * A work unit is two such tiles of one (sequence, key head).  The lengths
 //     are on the device, so a one-block kernel lists the units there, heaviest
 //     (most kv tiles) first, by a counting sort; the persistent CTAs walk that
-//     list in the same snake order as the dense kernel's.
+//     list in the same snake order as the dense kernel's.  Where there can be no
+//     more units than SMs, no order matters: each CTA finds its one unit itself
+//     and there is no list (6 prompts of up to 61 tokens: 6.3 us instead of 7.6).
 //   * A kv tile that reaches past its sequence's end holds rows of the next one
 //     (or behind the last): their scores are masked, and the MMA warp zeroes
 //     those rows of V in shared memory, because 0 * NaN is NaN.
@@ -31,8 +33,10 @@ struct VarlenUnit {  // two query tiles of one sequence, for every key head
 struct VarlenParams {
   uint16_t* o;              // [total][H_q][D]
   float* lse;               // [H_q][total]
-  const VarlenUnit* units;  // written by the plan kernel
+  const VarlenUnit* units;  // written by the plan kernel; null: a CTA finds its unit in seq_start
   const int32_t* n_listed;
+  const int32_t* seq_start;
+  int n_seqs;
   int64_t total;
   int H_kv;
   int G;             // query heads per key head
@@ -107,13 +111,15 @@ struct VUnit {
   int n;
 };
 
-__device__ __forceinline__ VUnit varlen_unit(const VarlenParams& p, int u) {
+// Unit u: from the list, or the CTA's only one from shared memory.
+__device__ __forceinline__ VUnit varlen_unit(const VarlenParams& p, const volatile int* own, int u) {
   const VarlenUnit* e = p.units + u / p.H_kv;
+  const bool listed = p.units != nullptr;
   VUnit w;
   w.h = u % p.H_kv;
-  w.row0 = __ldg(&e->row0);
-  w.len = __ldg(&e->len);
-  const int i0 = __ldg(&e->i0);
+  w.row0 = listed ? __ldg(&e->row0) : own[1];
+  w.len = listed ? __ldg(&e->len) : own[2];
+  const int i0 = listed ? __ldg(&e->i0) : own[3];
   w.n = 1;
 #pragma unroll
   for (int t = 0; t < kQTiles; ++t) {
@@ -124,11 +130,13 @@ __device__ __forceinline__ VUnit varlen_unit(const VarlenParams& p, int u) {
   return w;
 }
 
-// The units of this CTA: the snake order over the listed ones.
+// The units of this CTA: the snake order over the listed ones, or its own one.
 struct VarlenSeq {
   int n_units, rounds, G, cta;
-  __device__ explicit VarlenSeq(const VarlenParams& p)
-      : n_units(__ldg(p.n_listed) * p.H_kv), G(static_cast<int>(gridDim.x)), cta(static_cast<int>(blockIdx.x)) {
+  __device__ VarlenSeq(const VarlenParams& p, const volatile int* own)
+      : n_units((p.units != nullptr ? __ldg(p.n_listed) : own[0]) * p.H_kv),
+        G(static_cast<int>(gridDim.x)),
+        cta(static_cast<int>(blockIdx.x)) {
     rounds = (n_units + G - 1) / G;
   }
   __device__ int at(int r) const { return unit_of(r, cta, G); }
@@ -136,18 +144,18 @@ struct VarlenSeq {
 
 // TMA producer (one thread), as load_role.
 template <int D>
-__device__ void varlen_load_role(const Smem<D, false>& sm, const CUtensorMap* tmQ, const CUtensorMap* tmK,
+__device__ void varlen_load_role(const Smem<D, false>& sm, const volatile int* own, const CUtensorMap* tmQ, const CUtensorMap* tmK,
                                  const CUtensorMap* tmV, const VarlenParams& p, const WaitCtx& w) {
   using C = Cfg<D, false>;
-  const VarlenSeq us(p);
   int it = 0;
   int k = 0;
   bool ok = true;
   const uint64_t pol_first = l2_evict_first();
+  const VarlenSeq us(p, own);
   for (int r = 0; r < us.rounds && ok; ++r) {
     const int u = us.at(r);
     if (u >= us.n_units) continue;
-    const VUnit un = varlen_unit(p, u);
+    const VUnit un = varlen_unit(p, own, u);
     if (k > 0) {
       ok = mbar_wait(sm.bar_qfree(0), (k - 1) & 1, w) && mbar_wait(sm.bar_qfree(1), (k - 1) & 1, w);
       if (!ok) break;
@@ -184,7 +192,7 @@ __device__ void varlen_load_role(const Smem<D, false>& sm, const CUtensorMap* tm
 
 // MMA issuer, as mma_role; it also zeroes the rows of V past the sequence's end.
 template <int D, int kType>
-__device__ void varlen_mma_role(const Smem<D, false>& sm, uint32_t tmem, const VarlenParams& p, const WaitCtx& w) {
+__device__ void varlen_mma_role(const Smem<D, false>& sm, const volatile int* own, uint32_t tmem, const VarlenParams& p, const WaitCtx& w) {
   using C = Cfg<D, false>;
   // kind::f16: format code 0 is fp16, 1 is bf16 (make_idesc's e4m3 flag writes 0)
   constexpr uint32_t idesc_s = make_idesc(kBM, kBN, false, false, kType == kFP16);
@@ -197,15 +205,15 @@ __device__ void varlen_mma_role(const Smem<D, false>& sm, uint32_t tmem, const V
   const uint64_t kd0 = sdesc_kmajor_sw128(sm.slot(0));
   const uint64_t vd0 = sdesc_mnmajor_sw128(sm.slot(0), kPanelBytes);
   constexpr uint64_t kSlotStep = C::kTileBytes >> 4;
-  const VarlenSeq us(p);
   int it = 0;
   int k = 0;
   int pc[kQTiles] = {0, 0};
   bool ok = true, issued = false;
+  const VarlenSeq us(p, own);
   for (int r = 0; r < us.rounds && ok; ++r) {
     const int u = us.at(r);
     if (u >= us.n_units) continue;
-    const VUnit un = varlen_unit(p, u);
+    const VUnit un = varlen_unit(p, own, u);
     const int sk0 = it % C::kSlots;
     ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_q(), k & 1, w) &&
                                      mbar_wait(sm.bar_full(sk0), (it / C::kSlots) & 1, w));
@@ -275,7 +283,7 @@ __device__ void varlen_mma_role(const Smem<D, false>& sm, uint32_t tmem, const V
 
 // Softmax of query tile t, as softmax_role: row r is token r / G of the tile.
 template <int D, int kType>
-__device__ void varlen_softmax_role(const Smem<D, false>& sm, int t, uint32_t tmem, const VarlenParams& p,
+__device__ void varlen_softmax_role(const Smem<D, false>& sm, const volatile int* own, int t, uint32_t tmem, const VarlenParams& p,
                                     const WaitCtx& w) {
   using C = Cfg<D, false>;
   const int r = static_cast<int>(threadIdx.x) - kBM * (1 + t);
@@ -284,28 +292,31 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, int t, uint32_t tm
   const uint32_t tS = tmem + lane_off + t * kBN;
   const float c = p.scale_log2;
   const int tok = static_cast<int>((static_cast<uint32_t>(r) * p.inv_G) >> 16);
-  const VarlenSeq us(p);
   int cnt = 0;
   int sbase = 0;
   int k = 0;
   bool ok = true;
+  const VarlenSeq us(p, own);
   for (int rr = 0; rr < us.rounds && ok; ++rr) {
     const int u = us.at(rr);
     if (u >= us.n_units) continue;
-    const VUnit un = varlen_unit(p, u);
+    const VUnit un = varlen_unit(p, own, u);
     const int i0 = t ? un.i0[1] : un.i0[0];
-    int lim = un.len;  // keys j < lim are allowed for this row
-    if (p.causal) lim = min(lim, i0 + tok + 1);
-    const int nkv = t ? un.nkv[1] : un.nkv[0];
-    const int n0 = un.nkv[0], n1 = un.nkv[1];
+    // Keys j < lj of the kv tile at hand are allowed for this row; tiles from
+    // `masked` on hold keys that some row may not see
+    int lj = p.causal ? min(un.len, i0 + tok + 1) : un.len;
+    const int masked = p.causal ? min(un.len, i0 + 1) / kBN : un.len / kBN;
+    const int nkv = t ? un.nkv[1] : un.nkv[0], n_other = t ? un.nkv[0] : un.nkv[1];
+    const int steps = nkv + n_other;  // of both query tiles
+    int step = sbase + t;             // of this tile's next kv tile, in the order tile 0, tile 1
 
     float m_c = -INFINITY;
     float l = 0.f;
     for (int j = 0; j < nkv; ++j) {
-      const int step = sbase + min(j, n0) + min(j, n1) + ((t == 1 && j < n0) ? 1 : 0);
-      ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_s(t), (cnt + j) & 1, w) &&
+      ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_s(t), cnt & 1, w) &&
                                        (!C::kTurn || step == 0 || mbar_wait(sm.bar_turn(), (step - 1) & 1, w)));
       if (!ok) break;
+      step += j + t < n_other ? 2 : 1;
       tc_fence_after();
       uint32_t sr[kBN];
       tmem_ld32(tS + 0, sr + 0);
@@ -317,12 +328,11 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, int t, uint32_t tm
 #pragma unroll
       for (int i = 0; i < kBN; ++i) s[i] = __uint_as_float(sr[i]);
 
-      const int kbase = j * kBN;
-      if (kbase + kBN > un.len || (p.causal && kbase + kBN - 1 > i0)) {
-        const int lj = lim - kbase;
+      if (j >= masked) {
 #pragma unroll
         for (int i = 0; i < kBN; ++i) s[i] = (i < lj) ? s[i] : -INFINITY;
       }
+      lj -= kBN;
       float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kBN; i += 8) {
@@ -343,7 +353,7 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, int t, uint32_t tm
 
       auto rescale_if_needed = [&]() {
         if (!__any_sync(0xffffffffu, rescale_o)) return;
-        ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_o(t), (cnt + j - 1) & 1, w));
+        ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_o(t), (cnt - 1) & 1, w));
         if (!ok) return;
         tc_fence_after();
         const uint32_t tO = tmem + lane_off + C::kOCol0 + t * D;
@@ -396,9 +406,9 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, int t, uint32_t tm
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(sm.bar_p(t));
+      ++cnt;
     }
-    cnt += nkv;
-    sbase += n0 + n1;
+    sbase += steps;
     if (!ok) break;
     if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_ofree(t), (k - 1) & 1, w));
     if (!ok) break;
@@ -408,9 +418,12 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, int t, uint32_t tm
   }
 }
 
-// Epilogue warpgroup, as epilogue_role, with O written row by row.
+// Epilogue warpgroup, as epilogue_role, with O written row by row.  Half a
+// panel at a time and loops that are not unrolled keep it within its 72
+// registers; unrolled, it spilt 250 bytes (16 prompts of up to 2500 tokens,
+// D = 128: 175 us instead of 156).
 template <int D, int kType>
-__device__ void varlen_epilogue_role(const Smem<D, false>& sm, uint32_t tmem, const VarlenParams& p,
+__device__ void varlen_epilogue_role(const Smem<D, false>& sm, const volatile int* own, uint32_t tmem, const VarlenParams& p,
                                      const WaitCtx& w) {
   using C = Cfg<D, false>;
   const int qw = static_cast<int>(threadIdx.x >> 5) & 3;
@@ -420,14 +433,14 @@ __device__ void varlen_epilogue_role(const Smem<D, false>& sm, uint32_t tmem, co
   const uint32_t stage = sm.stage(qw);
   const int tok = static_cast<int>((static_cast<uint32_t>(rt) * p.inv_G) >> 16);  // this row's token and head
   const int g = rt - tok * p.G;
-  const VarlenSeq us(p);
   int cnt[kQTiles] = {0, 0};
   int k = 0;
   bool ok = true;
+  const VarlenSeq us(p, own);
   for (int rr = 0; rr < us.rounds && ok; ++rr) {
     const int u = us.at(rr);
     if (u >= us.n_units) continue;
-    const VUnit un = varlen_unit(p, u);
+    const VUnit un = varlen_unit(p, own, u);
 #pragma unroll
     for (int t = 0; t < kQTiles; ++t) {
       if (!ok) break;
@@ -445,32 +458,34 @@ __device__ void varlen_epilogue_role(const Smem<D, false>& sm, uint32_t tmem, co
       // rows of this tile that exist: tokens before the sequence's end
       const int rows = min(p.rows, (un.len - un.i0[t]) * p.G);
       const int64_t tok0 = un.row0 + un.i0[t];
-#pragma unroll
+#pragma unroll 1
       for (int pn = 0; pn < C::kOPanels; ++pn) {
-        uint32_t pk[32];
+        __syncwarp();  // the staging panel's last rows have been read
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[32];
           tmem_ld32(tO + pn * 64 + h * 32, o);
           tmem_wait_ld();
+          if (pn == C::kOPanels - 1 && h == 1) {
+            tc_fence_before();
+            mbar_arrive(sm.bar_ofree(t));
+          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il2), x0, x1);
-            pk[16 * h + i] = pack_16x2<kType>(x0, x1);
+          for (int ch = 0; ch < 4; ++ch) {  // 16 bytes: 8 columns
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x0, x1;
+              unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[8 * ch + 2 * i]), __uint_as_float(o[8 * ch + 2 * i + 1])), il2),
+                           x0, x1);
+              pk[i] = pack_16x2<kType>(x0, x1);
+            }
+            st_shared_v4_b32(rowa + (static_cast<uint32_t>((4 * h + ch) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
         }
-        if (pn == C::kOPanels - 1) {
-          tc_fence_before();
-          mbar_arrive(sm.bar_ofree(t));
-        }
-        __syncwarp();  // the staging panel's last rows have been read
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          st_shared_v4_b32(rowa + (static_cast<uint32_t>(ch ^ (lane & 7)) << 4), pk[4 * ch], pk[4 * ch + 1],
-                           pk[4 * ch + 2], pk[4 * ch + 3]);
         __syncwarp();
         // eight lanes a row: 16 bytes each
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           const int lr = 4 * i + (lane >> 3), ch = lane & 7;
           const int row = qw * 32 + lr;
@@ -493,6 +508,38 @@ __device__ void varlen_epilogue_role(const Smem<D, false>& sm, uint32_t tmem, co
   }
 }
 
+// The unit of this CTA where there is no list: own[0] the number of units per
+// key head, own[1 .. 3] row0, len and i0 of unit blockIdx.x / H_kv.  One warp;
+// units are numbered sequence by sequence.
+__device__ __forceinline__ void varlen_own_unit(const VarlenParams& p, volatile int* own) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int mine = static_cast<int>(blockIdx.x) / p.H_kv, unit_tok = kQTiles * p.tok, most = static_cast<int>(p.total);
+  int before = 0;
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+    const int s = s0 + lane;
+    int row0 = 0, len = 0;
+    if (s < p.n_seqs) {
+      row0 = min(max(__ldg(p.seq_start + s), 0), most);
+      len = max(0, min(__ldg(p.seq_start + s + 1), most) - row0);
+    }
+    const int n = (len + unit_tok - 1) / unit_tok;
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    const int first = before + incl - n;
+    if (first <= mine && mine < first + n) {
+      own[1] = row0;
+      own[2] = len;
+      own[3] = (mine - first) * unit_tok;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) own[0] = min(before, static_cast<int>(gridDim.x) / p.H_kv);
+}
+
 template <int D, int kType>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_varlen_sm103a(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -503,6 +550,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const Smem<D, false> sm{base, smem};
+  volatile int* const own = reinterpret_cast<volatile int*>(smem + C::kListOff);  // (the dense kernel's unit list lies here)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
 
   const int warp = static_cast<int>(threadIdx.x >> 5);
@@ -548,20 +596,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t tmem = misc[0];
   const WaitCtx w{p.timeout_ns, misc + 1};
   grid_dependency_wait();  // the unit list, and the caller's inputs before it
+  if (p.units == nullptr) {
+    if (warp == 0) varlen_own_unit(p, own);
+    __syncthreads();
+  }
 
   if (warp < 4) {
     regs_set<kRegsRoles>();
     if (warp == 0) {
-      if (lane == 0) varlen_load_role<D>(sm, &tmQ, &tmK, &tmV, p, w);
+      if (lane == 0) varlen_load_role<D>(sm, own, &tmQ, &tmK, &tmV, p, w);
     } else if (warp == 1) {
-      varlen_mma_role<D, kType>(sm, tmem, p, w);
+      varlen_mma_role<D, kType>(sm, own, tmem, p, w);
     }
   } else if (warp < kEpiWarp0) {
     regs_set<kRegsSoftmax>();
-    varlen_softmax_role<D, kType>(sm, (warp - 4) >> 2, tmem, p, w);
+    varlen_softmax_role<D, kType>(sm, own, (warp - 4) >> 2, tmem, p, w);
   } else {
     regs_set<kRegsEpi>();
-    varlen_epilogue_role<D, kType>(sm, tmem, p, w);
+    varlen_epilogue_role<D, kType>(sm, own, tmem, p, w);
   }
   grid_launch_dependents();
 
@@ -594,6 +646,9 @@ bool encode_rows(CUtensorMap* m, const void* ptr, int D, int H, int64_t total, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Units up to which no list is made, where the device has as many SMs.
+constexpr int kVarlenDirect = 152;
+
 // Units the list can hold: one for every 2 * tok tokens and one ragged end a
 // sequence.
 int64_t varlen_cap(int64_t total, int n_seqs, int G) { return total / (kQTiles * (kBM / G)) + n_seqs; }
@@ -615,7 +670,8 @@ uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int
   if (total < 0 || total > INT_MAX || n_seqs < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || H_q / H_kv > kBM ||
       (D != 64 && D != 128))
     return 0;
-  return 16 + static_cast<uint64_t>(varlen_cap(total, n_seqs, H_q / H_kv)) * sizeof(VarlenUnit);
+  const int64_t cap = varlen_cap(total, n_seqs, H_q / H_kv);
+  return 16 + static_cast<uint64_t>(cap) * sizeof(VarlenUnit);
 }
 
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, int64_t total,
@@ -666,16 +722,20 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
       !encode_rows(&tk, k, D, H_kv, total, k_stride, 1, kBN, dtype) ||
       !encode_rows(&tv, v, D, H_kv, total, v_stride, 1, kBN, dtype))
     return ATTN_ERR_LAUNCH;
+  const int sms = g_dev_sms[dev].load(std::memory_order_relaxed);
+  const bool listed = cap * H_kv > std::min(sms, kVarlenDirect);
   int32_t* n_listed = static_cast<int32_t*>(workspace);
   VarlenUnit* units = reinterpret_cast<VarlenUnit*>(static_cast<char*>(workspace) + 16);
-  if (launch_pdl(attn_varlen_plan, dim3(1), dim3(kPlanThreads), 0, st, seq_start, n_seqs, total, kQTiles * tok, causal,
+  if (listed && launch_pdl(attn_varlen_plan, dim3(1), dim3(kPlanThreads), 0, st, seq_start, n_seqs, total, kQTiles * tok, causal,
                  units, n_listed, static_cast<int>(cap)) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
   VarlenParams prm;
   prm.o = static_cast<uint16_t*>(o);
   prm.lse = lse;
-  prm.units = units;
+  prm.units = listed ? units : nullptr;
   prm.n_listed = n_listed;
+  prm.seq_start = seq_start;
+  prm.n_seqs = n_seqs;
   prm.total = total;
   prm.H_kv = H_kv;
   prm.G = G;
@@ -685,7 +745,7 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
   prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   prm.causal = causal;
   prm.timeout_ns = kDefaultTimeoutNs;
-  const int grid = static_cast<int>(std::min<int64_t>(cap * H_kv, g_dev_sms[dev].load(std::memory_order_relaxed)));
+  const int grid = static_cast<int>(std::min<int64_t>(cap * H_kv, sms));
   if (D == 64)
     return dtype == ATTN_BF16 ? launch_varlen<64, kBF16>(tq, tk, tv, prm, grid, st)
                               : launch_varlen<64, kFP16>(tq, tk, tv, prm, grid, st);
