@@ -354,7 +354,10 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 constexpr int kC4DecThreads = 128;  // 4 warps
 constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
 constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
-constexpr int kC4DecCtasPerSm = 4;
+// Three CTAs an SM give a thread 168 registers, room for two tiles' chains of
+// instructions side by side; with four (128, spills) it took 153 us instead of
+// 140 at 64 sequences of up to 16000 entries with weights.
+constexpr int kC4DecCtasPerSm = 3;
 constexpr int kC4RowCost = 6;       // tiles' worth of time that a row costs a CTA
 // A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
 // so that a size asked for on one device (or with none) holds on any.
@@ -600,16 +603,6 @@ struct C4Copy {
   }
 };
 
-// What a lane holds of a tile: K rows kappa(r), kappa(r) + 8; V rows kappa(2c),
-// kappa(2c + 1) and those + 8; the (s, m) of keys kappa(r), kappa(r) + 8.
-template <int D>
-struct C4Raw {
-  static constexpr int kGroups = D / kC4Group;
-  uint2 k[2][kGroups];
-  uint32_t v[4][kGroups];
-  uint32_t km[2][kGroups];
-  uint32_t vm[2][kGroups];
-};
 // This lane's shared-memory addresses in stage 0.
 template <int D>
 struct C4Lane {
@@ -635,25 +628,16 @@ __device__ __forceinline__ uint32_t ld_shared_b32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+// The (s, m) of keys kappa(r) and kappa(r) + 8, of K or (at kVm - kKm) of V.
 template <int D>
-__device__ __forceinline__ void c4_load(C4Raw<D>& t, const C4Lane<D>& p, uint32_t stage) {
-  using R = C4Ring<D>;
-  constexpr int kG = D / kC4Group;
+__device__ __forceinline__ void c4_load_meta(uint32_t (*sm)[D / kC4Group], uint32_t at) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {  // 8 rows further: the same place in the row
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      t.k[i][g] = ld_shared_v2(p.k[g] + stage + i * 8 * R::kRow);
-      t.v[2 * i][g] = ld_shared_b32(p.v[0][g] + stage + i * 8 * R::kRow);
-      t.v[2 * i + 1][g] = ld_shared_b32(p.v[1][g] + stage + i * 8 * R::kRow);
-    }
-    if constexpr (kG == 2) {
-      const uint2 a = ld_shared_v2(p.meta + stage + i * 8 * R::kMeta);
-      const uint2 b = ld_shared_v2(p.meta + stage + (R::kVm - R::kKm) + i * 8 * R::kMeta);
-      t.km[i][0] = a.x, t.km[i][kG - 1] = a.y, t.vm[i][0] = b.x, t.vm[i][kG - 1] = b.y;
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (D == 128) {
+      const uint2 a = ld_shared_v2(at + i * 8 * C4Ring<D>::kMeta);
+      sm[i][0] = a.x, sm[i][1] = a.y;
     } else {
-      t.km[i][0] = ld_shared_b32(p.meta + stage + i * 8 * R::kMeta);
-      t.vm[i][0] = ld_shared_b32(p.meta + stage + (R::kVm - R::kKm) + i * 8 * R::kMeta);
+      sm[i][0] = ld_shared_b32(at + i * 8 * C4Ring<D>::kMeta);
     }
   }
 }
@@ -741,65 +725,123 @@ struct C4State {
   float o[kGroups][4][4];    // O^T in units of top_s / 2^7: channels 64g + 8r + t (+ 4), heads 2c, 2c + 1
 };
 
-// One tile's 16 keys, of which the first `left` exist (kTail; else all).
-// `scores`: where head 2c's score of key `key` goes, [head][64 keys of the tile].
-template <int D, bool kWeight, bool kTail>
-__device__ __forceinline__ void c4_step(C4State<D>& st, const C4Raw<D>& t, const C4Query<D>& q, int key, int left,
-                                        float* scores, bool head0, bool head1) {
+// Logits of a tile's 16 keys: keys kappa(r), kappa(r), kappa(r) + 8, kappa(r) + 8
+// and heads 2c, 2c + 1, 2c, 2c + 1.
+template <int D>
+__device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_t stage, const C4Query<D>& q) {
+  using R = C4Ring<D>;
   constexpr int kG = D / kC4Group;
-  float xs[4] = {0.f, 0.f, 0.f, 0.f};  // keys key, key, key + 8, key + 8; heads 2c, 2c + 1, ...
+  uint32_t sm[2][kG];
+  c4_load_meta<D>(sm, p.meta + stage);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) xs[e] = 0.f;
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
+    const uint2 ka = ld_shared_v2(p.k[g] + stage), kb = ld_shared_v2(p.k[g] + stage + 8 * R::kRow);
     float d[4];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint32_t wa = w ? t.k[0][g].y : t.k[0][g].x, wb = w ? t.k[1][g].y : t.k[1][g].x;
-      if (w == 0)
-        mma_16816_zero(d, c4_low(wa), c4_low(wb), c4_high(wa), c4_high(wb), q.q[g][0][0], q.q[g][0][1]);
-      else
-        mma_16816(d, c4_low(wa), c4_low(wb), c4_high(wa), c4_high(wb), q.q[g][2][0], q.q[g][2][1]);
-      mma_16816(d, c4_low(wa >> 8), c4_low(wb >> 8), c4_high(wa >> 8), c4_high(wb >> 8), q.q[g][2 * w + 1][0],
-                q.q[g][2 * w + 1][1]);
-    }
+    mma_16816_zero(d, c4_low(ka.x), c4_low(kb.x), c4_high(ka.x), c4_high(kb.x), q.q[g][0][0], q.q[g][0][1]);
+    mma_16816(d, c4_low(ka.x >> 8), c4_low(kb.x >> 8), c4_high(ka.x >> 8), c4_high(kb.x >> 8), q.q[g][1][0], q.q[g][1][1]);
+    mma_16816(d, c4_low(ka.y), c4_low(kb.y), c4_high(ka.y), c4_high(kb.y), q.q[g][2][0], q.q[g][2][1]);
+    mma_16816(d, c4_low(ka.y >> 8), c4_low(kb.y >> 8), c4_high(ka.y >> 8), c4_high(kb.y >> 8), q.q[g][3][0], q.q[g][3][1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float s = bf16_lo(t.km[i][g]), mm = fmaf(8.f, s, bf16_hi(t.km[i][g]));
+      const float s = bf16_lo(sm[i][g]), mm = fmaf(8.f, s, bf16_hi(sm[i][g]));
       xs[2 * i] = fmaf(s, d[2 * i], fmaf(mm, q.sum[g][0], xs[2 * i]));
       xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(mm, q.sum[g][1], xs[2 * i + 1]));
     }
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) xs[e] *= q.scale[e & 1];
-  if constexpr (kTail) {
-    if (key >= left) xs[0] = xs[1] = -INFINITY;
-    if (key + 8 >= left) xs[2] = xs[3] = -INFINITY;
+}
+
+// O^T += V^T P^T over a tile's 16 keys; pr as c4_scores lays out the logits.
+template <int D>
+__device__ __forceinline__ void c4_values(C4State<D>& st, const float* pr, const uint32_t (*sm)[D / kC4Group],
+                                          const C4Lane<D>& p, uint32_t stage) {
+  using R = C4Ring<D>;
+#pragma unroll
+  for (int g = 0; g < D / kC4Group; ++g) {
+    uint32_t pb[2];  // P^T as the B operand: keys 0-7 and 8-15 of the MMA
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = bf16_lo(sm[i][g]), mm = fmaf(8.f, s, bf16_hi(sm[i][g])), sr = s * st.inv_s[g];
+      st.bias[g][0] = fmaf(pr[2 * i], mm, st.bias[g][0]);
+      st.bias[g][1] = fmaf(pr[2 * i + 1], mm, st.bias[g][1]);
+      pb[i] = movmatrix_trans(pack_f16x2(pr[2 * i] * sr, pr[2 * i + 1] * sr));
+    }
+    // bytes j of the words of two neighbouring MMA rows side by side: their low
+    // nibbles are channel 2j, the high ones 2j + 1
+    const uint32_t v0 = ld_shared_b32(p.v[0][g] + stage), v1 = ld_shared_b32(p.v[1][g] + stage);
+    const uint32_t v2 = ld_shared_b32(p.v[0][g] + stage + 8 * R::kRow), v3 = ld_shared_b32(p.v[1][g] + stage + 8 * R::kRow);
+    uint32_t wa[4], wb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      wa[j] = __byte_perm(v0, v1, 0x0400 + 0x1111 * j);
+      wb[j] = __byte_perm(v2, v3, 0x0400 + 0x1111 * j);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // rows r: channels 8r + 2j (+ 1); rows r + 8: channels 8r + 4 + 2j (+ 1)
+      mma_16816(st.o[g][2 * j], c4_low(wa[j]), c4_low(wa[j + 2]), c4_low(wb[j]), c4_low(wb[j + 2]), pb[0], pb[1]);
+      mma_16816(st.o[g][2 * j + 1], c4_high(wa[j]), c4_high(wa[j + 2]), c4_high(wb[j]), c4_high(wb[j + 2]), pb[0], pb[1]);
+    }
   }
-  if constexpr (kWeight) {
-    if (head0) {
-      scores[0] = xs[0];
-      scores[8] = xs[2];
+}
+
+// kN tiles' 16 keys each, in stages stage[0], ...; with kTail the first `left`
+// keys of the (one) tile exist.  `scores`: where head 2c's score of key
+// kappa(r) of the first tile goes, [tile][head][64 keys], tiles sc_step apart.
+template <int D, bool kWeight, bool kTail, int kN>
+__device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, const uint32_t* stage, const C4Query<D>& q,
+                                        int key, int left, float* scores, int64_t sc_step, bool head0, bool head1) {
+  using R = C4Ring<D>;
+  constexpr int kG = D / kC4Group;
+  float xs[kN][4];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    c4_scores<D>(xs[n], p, stage[n], q);
+    if constexpr (kTail) {
+      if (key >= left) xs[n][0] = xs[n][1] = -INFINITY;
+      if (key + 8 >= left) xs[n][2] = xs[n][3] = -INFINITY;
     }
-    if (head1) {
-      scores[kC4TileKeys] = xs[1];
-      scores[kC4TileKeys + 8] = xs[3];
+    if constexpr (kWeight) {
+      float* dst = scores + n * sc_step;
+      if (head0) {
+        dst[0] = xs[n][0];
+        dst[8] = xs[n][2];
+      }
+      if (head1) {
+        dst[kC4TileKeys] = xs[n][1];
+        dst[kC4TileKeys + 8] = xs[n][3];
+      }
     }
+  }
+  uint32_t sm[kN][2][kG];
+  float top[2] = {-INFINITY, -INFINITY}, top_s[kG];
+#pragma unroll
+  for (int g = 0; g < kG; ++g) top_s[g] = 0.f;
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    c4_load_meta<D>(sm[n], p.meta + stage[n] + (R::kVm - R::kKm));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) top[e] = max3f(top[e], xs[n][e], xs[n][2 + e]);
+#pragma unroll
+    for (int g = 0; g < kG; ++g) top_s[g] = max3f(top_s[g], bf16_lo(sm[n][0][g]), bf16_lo(sm[n][1][g]));
   }
   // New references only where a score exceeds the old one by 2^8 or an s the
   // old bound: p stays below 2^8, the results do not depend on the references,
   // and most tiles need one vote instead of reductions and a rescale.
-  bool grow = (fmaxf(xs[0], xs[2]) > st.most[0]) | (fmaxf(xs[1], xs[3]) > st.most[1]);
+  bool grow = (top[0] > st.most[0]) | (top[1] > st.most[1]);
 #pragma unroll
-  for (int g = 0; g < kG; ++g) grow |= fmaxf(bf16_lo(t.vm[0][g]), bf16_lo(t.vm[1][g])) > st.top_s[g];
+  for (int g = 0; g < kG; ++g) grow |= top_s[g] > st.top_s[g];
   if (__any_sync(0xffffffffu, grow)) {
     float a[2], f[kG];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float top = fmaxf(xs[e], xs[2 + e]);
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      for (int off = 4; off < 32; off <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], off));
       // a reference that has held moves only when it has to: p of the keys so
       // far keeps its bits
-      const float to = top > st.most[e] ? top : st.ref[e];
+      const float to = top[e] > st.most[e] ? top[e] : st.ref[e];
       a[e] = to == st.ref[e] ? 1.f : ex2_approx(st.ref[e] - to);
       st.ref[e] = to;
       st.sub[e] = to == -INFINITY ? 0.f : to;
@@ -808,10 +850,9 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Raw<D>& t, const
     }
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      float top = fmaxf(bf16_lo(t.vm[0][g]), bf16_lo(t.vm[1][g]));
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const uint32_t up = (__float_as_uint(top) + 0x007fffffu) & 0x7f800000u;  // the next power of two
+      for (int off = 4; off < 32; off <<= 1) top_s[g] = fmaxf(top_s[g], __shfl_xor_sync(0xffffffffu, top_s[g], off));
+      const uint32_t up = (__float_as_uint(top_s[g]) + 0x007fffffu) & 0x7f800000u;  // the next power of two
       const uint32_t to = max(max(up, __float_as_uint(st.top_s[g])), 17u << 23);
       f[g] = st.top_s[g] == __uint_as_float(to) ? 1.f : __fdividef(st.top_s[g], __uint_as_float(to));
       st.top_s[g] = __uint_as_float(to);
@@ -824,35 +865,14 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Raw<D>& t, const
         for (int e = 0; e < 4; ++e) st.o[g][u][e] *= a[e & 1] * f[g];
     }
   }
-  float pr[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    pr[e] = ex2_approx(xs[e] - st.sub[e & 1]);
-    st.l[e & 1] += pr[e];
-  }
+  for (int n = 0; n < kN; ++n) {
 #pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    uint32_t pb[2];  // P^T as the B operand: keys 0-7 and 8-15
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float s = bf16_lo(t.vm[i][g]), mm = fmaf(8.f, s, bf16_hi(t.vm[i][g])), sr = s * st.inv_s[g];
-      st.bias[g][0] = fmaf(pr[2 * i], mm, st.bias[g][0]);
-      st.bias[g][1] = fmaf(pr[2 * i + 1], mm, st.bias[g][1]);
-      pb[i] = movmatrix_trans(pack_f16x2(pr[2 * i] * sr, pr[2 * i + 1] * sr));
+    for (int e = 0; e < 4; ++e) {
+      xs[n][e] = ex2_approx(xs[n][e] - st.sub[e & 1]);
+      st.l[e & 1] += xs[n][e];
     }
-    // bytes j of the words of two neighbouring MMA rows side by side: their low
-    // nibbles are channel 2j, the high ones 2j + 1
-    uint32_t wa[4], wb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      wa[j] = __byte_perm(t.v[0][g], t.v[1][g], 0x0400 + 0x1111 * j);
-      wb[j] = __byte_perm(t.v[2][g], t.v[3][g], 0x0400 + 0x1111 * j);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {  // rows r: channels 8r + 2j (+ 1); rows r + 8: channels 8r + 4 + 2j (+ 1)
-      mma_16816(st.o[g][2 * j], c4_low(wa[j]), c4_low(wa[j + 2]), c4_low(wb[j]), c4_low(wb[j + 2]), pb[0], pb[1]);
-      mma_16816(st.o[g][2 * j + 1], c4_high(wa[j]), c4_high(wa[j + 2]), c4_high(wb[j]), c4_high(wb[j + 2]), pb[0], pb[1]);
-    }
+    c4_values<D>(st, xs[n], sm[n], p, stage[n]);
   }
 }
 
@@ -932,24 +952,35 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
                         : nullptr;
     const int64_t sc_step = static_cast<int64_t>(p.G) * kC4TileKeys;
     const bool head0 = 2 * c < heads, head1 = 2 * c + 1 < heads;
-    uint32_t stage = 0u, free = (Ring::kStages - 1) * Ring::kStage;  // of tile i, and the one consumed before it
-    for (int i = 0; i < full; ++i) {
-      cp_async_wait<Ring::kStages - 2>();  // this lane's copies of tile i, ...
+    // Two tiles at a time (one vote, and two chains of instructions to overlap),
+    // then the odd one, then the one that ends inside.
+    int i = 0;
+    uint32_t pair = 0u;  // stage of tile i; of i + 1: the next
+    for (; i + 2 <= full; i += 2) {
+      cp_async_wait<Ring::kStages - 3>();  // this lane's copies of tiles i and i + 1, ...
       __syncwarp();                        // ... and every lane's; the stage before is consumed
-      fetch(i + Ring::kStages - 1, free);
-      C4Raw<D> raw;
-      c4_load<D>(raw, at, stage);
-      free = stage;
-      stage = stage == (Ring::kStages - 1) * Ring::kStage ? 0u : stage + Ring::kStage;
-      c4_step<D, kWeight, false>(st, raw, q, key, 16, sc, head0, head1);
+      const uint32_t stage[2] = {pair, pair + Ring::kStage};
+      fetch(i + Ring::kStages - 1, (pair == 0u ? Ring::kStages * Ring::kStage : pair) - Ring::kStage);
+      c4_step<D, kWeight, false, 2>(st, at, stage, q, key, 16, sc, sc_step, head0, head1);
+      __syncwarp();
+      fetch(i + Ring::kStages, pair);
+      pair = pair == (Ring::kStages - 2) * Ring::kStage ? 0u : pair + 2 * Ring::kStage;
+      if (kWeight) sc += 2 * sc_step;
+    }
+    if (i < full) {
+      cp_async_wait<Ring::kStages - 3>();
+      __syncwarp();
+      const uint32_t stage[1] = {pair};
+      c4_step<D, kWeight, false, 1>(st, at, stage, q, key, 16, sc, sc_step, head0, head1);
       if (kWeight) sc += sc_step;
+      pair += Ring::kStage;
+      ++i;
     }
     if (last > 0) {
       cp_async_wait<0>();
       __syncwarp();
-      C4Raw<D> raw;
-      c4_load<D>(raw, at, stage);
-      c4_step<D, kWeight, true>(st, raw, q, key, last, sc, head0, head1);
+      const uint32_t stage[1] = {pair};
+      c4_step<D, kWeight, true, 1>(st, at, stage, q, key, last, sc, sc_step, head0, head1);
     }
     __syncthreads();  // the ring is empty (the copies of every tile were waited for) and read
 
