@@ -268,10 +268,11 @@ typedef enum { ATTN_BF16 = 0, ATTN_FP16 = 1, ATTN_FP32 = 2 } attn_dtype_t;
  *   dtype       ATTN_BF16 or ATTN_FP16 (q, k, v and o).
  *   H_q / H_kv  a whole number, at most 128.  D is 64 or 128.
  *   workspace   caller-owned device buffer, 16-byte aligned, of at least
- *               attn_fwd_varlen_workspace_bytes(...) bytes; overwritten.
+ *               attn_fwd_varlen_workspace_bytes(...) bytes; overwritten.  Small
+ *               calls need none: the size is then 16, and NULL will do.
  * Values within a sequence are finite (a NaN or infinity in V reaches, as a
  * product with zero, rows of its own sequence that do not see it).
- * Asynchronous (two kernel launches); argument errors are reported before
+ * Asynchronous (one or two kernel launches); argument errors are reported before
  * anything is launched.  Calls that share a workspace must be ordered.
  */
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -280,7 +281,7 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
                               float scale, int causal, void* workspace, uint64_t workspace_bytes,
                               void* stream);
 
-/* Workspace bytes attn_fwd_varlen needs (0 for invalid arguments). */
+/* Workspace bytes attn_fwd_varlen needs (0 for invalid arguments, 16 for none). */
 uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int H_kv, int D);
 
 /*
@@ -368,16 +369,17 @@ attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int
  *               its group.  They may be the same buffer (cache->weight).  Places
  *               behind a length are left as they were.
  *   workspace   at least attn_cache4_decode_workspace_bytes(...) bytes, 16-byte
- *               aligned; overwritten.  Calls that share one must be ordered.
+ *               aligned; overwritten.  Calls that share one must be ordered.  With a
+ *               small max_len and no weights the size is 16, and NULL will do.
  * H_q / H_kv is a whole number, at most 128.  Results are the same from call to
- * call.  Asynchronous (two kernel launches).
+ * call.  Asynchronous (one or two kernel launches).
  */
 attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int64_t q_stride, void* o,
                                  float* lse, int H_q, int dtype, float scale, int max_len,
                                  const float* weight_in, float* weight_out, void* workspace,
                                  uint64_t workspace_bytes, void* stream);
 
-/* Workspace bytes attn_cache4_decode needs (0 for invalid arguments). */
+/* Workspace bytes attn_cache4_decode needs (0 for invalid arguments, 16 for none). */
 uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int max_len,
                                             int with_weight);
 

@@ -101,17 +101,19 @@ def on_stream(device, stream, call):
             return call(stream.cuda_stream)
 
 
+_TYPES = {}  # torch dtype -> attn_dtype_t
+
+
 def element_type(dtype, also_fp32: bool = False) -> int:
     """attn_dtype_t of a torch dtype the serving calls take."""
-    import torch
+    if not _TYPES:
+        import torch
 
-    if dtype == torch.bfloat16:
-        return _lib.ATTN_BF16
-    if dtype == torch.float16:
-        return _lib.ATTN_FP16
-    if also_fp32 and dtype == torch.float32:
-        return _lib.ATTN_FP32
-    raise TypeError(f"{dtype}: must be bfloat16 or float16" + (" or float32" if also_fp32 else ""))
+        _TYPES.update({torch.bfloat16: _lib.ATTN_BF16, torch.float16: _lib.ATTN_FP16, torch.float32: _lib.ATTN_FP32})
+    code = _TYPES.get(dtype, -1)
+    if code < 0 or (code == _lib.ATTN_FP32 and not also_fp32):
+        raise TypeError(f"{dtype}: must be bfloat16 or float16" + (" or float32" if also_fp32 else ""))
+    return code
 
 
 def row_stride(t, shape, name: str) -> int:
@@ -178,7 +180,7 @@ def attention_varlen(q, k, v, seq_start, scale: float | None = None, causal: boo
     def call(handle):
         o = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
         z = lse if lse is not None else torch.empty((H_q, total), dtype=torch.float32, device=device)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
         _lib.attn_fwd_varlen(q, k, v, o, z, total, seq_start, n, H_q, H_kv, D, code, q_stride, k_stride, v_stride,
                              scale, causal, ws, nbytes, handle)
         return o, z

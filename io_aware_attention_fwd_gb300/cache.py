@@ -171,7 +171,7 @@ class KVCache4:
         def call(handle):
             o = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
             z = lse if lse is not None else torch.empty((B, H_q), dtype=torch.float32, device=device)
-            ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
             _lib.attn_cache4_decode(self._c, q, stride, o, z, H_q, code, scale, max_len,
                                     None if weight_out is None else self.weight, weight_out, ws, nbytes, handle)
             return o, z

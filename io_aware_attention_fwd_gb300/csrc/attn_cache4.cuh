@@ -349,7 +349,12 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 // the lengths are.  A CTA's share of one (sequence, key head) is a segment;
 // its four warps take 16 keys of every tile each, with running statistics of
 // their own, and join at the segment's end into one partial (m, l, O).  The
-// merge kernel joins the partials of a row.
+// merge kernel joins the partials of a row.  Where max_len is at most
+// kC4DirectLen and no weights are asked for, a CTA takes a whole row instead and
+// writes O and LSE itself: one launch and no workspace.  (One sequence of 701
+// entries, 16 heads, D = 64: MEASURED us on the GPU either way, but the host
+// needs 20 us to make the two launches and the workspace and MEASURED for the
+// one.)
 
 constexpr int kC4DecThreads = 128;  // 4 warps
 constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
@@ -358,6 +363,7 @@ constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
 // instructions side by side; with four (128, spills) it took 153 us instead of
 // 140 at 64 sequences of up to 16000 entries with weights.
 constexpr int kC4DecCtasPerSm = 3;
+constexpr int kC4DirectLen = 1024;
 constexpr int kC4RowCost = 6;       // tiles' worth of time that a row costs a CTA
 // A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
 // so that a size asked for on one device (or with none) holds on any.
@@ -376,6 +382,8 @@ struct DecParams {
   float* o_part;    // [slots][8][D], unnormalised
   float2* ml_part;  // [slots][8]: (m in log2 units, l)
   float* scores;    // [tile of a (sequence, key head)][G][64], log2 units, or null
+  uint16_t* o;      // [B][H*G][D]
+  float* lse;       // [B][H*G]
 };
 
 __device__ __forceinline__ int c4_tiles(const DecParams& p, int b) {
@@ -876,9 +884,11 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
   }
 }
 
-template <int D, int kType, bool kWeight>
+// kDirect: CTA x takes the whole of row x.
+template <int D, int kType, bool kWeight, bool kDirect>
 __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     attn_cache4_decode_kernel(const DecParams p) {
+  static_assert(!(kWeight && kDirect), "weights need the merge kernel");
   constexpr int kG = D / kC4Group;
   constexpr int kWarps = kC4DecThreads / 32;
   using Ring = C4Ring<D>;
@@ -893,25 +903,33 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   const int key = c4_kappa(r);
   grid_dependency_wait();
-  int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
-  const int64_t total = c4_units(c4_total(p, sums_s, &mine_before, &mine), kC4RowCost) * rows_per_b;
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   C4Walk w;
-  w.x = static_cast<int64_t>(blockIdx.x) * share;
-  w.end = w.x + share < total ? w.x + share : total;
-  if (w.x >= w.end) {
-    grid_launch_dependents();
-    return;
+  if constexpr (kDirect) {
+    w.b = static_cast<int>(blockIdx.x) / rows_per_b;
+    w.row = static_cast<int>(blockIdx.x) % rows_per_b;
+    w.n = c4_len(p.len, w.b, p.most);
+    w.t0 = 0;
+    w.t1 = (w.n + kC4TileKeys - 1) / kC4TileKeys;
+  } else {
+    int64_t mine_before, mine;
+    const int64_t total = c4_units(c4_total(p, sums_s, &mine_before, &mine), kC4RowCost) * rows_per_b;
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    w.x = static_cast<int64_t>(blockIdx.x) * share;
+    w.end = w.x + share < total ? w.x + share : total;
+    if (w.x >= w.end) {
+      grid_launch_dependents();
+      return;
+    }
+    c4_find(p, w.x / rows_per_b, kC4RowCost, mine_before, mine, &b_s, &before_s);
+    __syncthreads();
+    w.b = b_s;
+    w.before = before_s;
   }
-  c4_find(p, w.x / rows_per_b, kC4RowCost, mine_before, mine, &b_s, &before_s);
-  __syncthreads();
-  w.b = b_s;
-  w.before = before_s;
   const uint32_t ring = smem_u32(ring_s) + static_cast<uint32_t>(warp * Ring::kWarp);
   C4Lane<D> at;
   at.start(ring, r, c);
-  while (w.next(p, rows_per_b, kC4RowCost)) {
+  for (bool once = true; kDirect ? once : w.next(p, rows_per_b, kC4RowCost); once = false) {
     const int b = w.b, n = w.n, in_b = w.row, t0 = w.t0, t1 = w.t1;
     const int h = in_b / p.HB, hb = in_b % p.HB;
     const int heads = min(kC4Heads, p.G - hb * kC4Heads);
@@ -1008,23 +1026,43 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       ml_s[warp][2 * c + 1] = make_float2(st.ref[1], st.l[1]);
     }
     __syncthreads();
-    const int64_t slot = blockIdx.x + static_cast<int64_t>(b) * rows_per_b + in_b;
-    for (int i = tid; i < heads * D; i += kC4DecThreads) {
-      const int hd = i / D, d = i % D;
-      float top = -INFINITY;
+    if constexpr (kDirect) {
+      for (int i = tid; i < heads * D / 2; i += kC4DecThreads) {
+        const int hd = i / (D / 2), d = i % (D / 2) * 2;
+        float top = -INFINITY, x0 = 0.f, x1 = 0.f, ls = 0.f;
 #pragma unroll
-      for (int i2 = 0; i2 < kWarps; ++i2) top = fmaxf(top, ml_s[i2][hd].x);
-      float sum = 0.f, ls = 0.f;
+        for (int i2 = 0; i2 < kWarps; ++i2) top = fmaxf(top, ml_s[i2][hd].x);
 #pragma unroll
-      for (int i2 = 0; i2 < kWarps; ++i2) {
-        const float a = top == -INFINITY ? 0.f : ex2_approx(ml_s[i2][hd].x - top);
-        sum = fmaf(a, o_s[i2][hd][d], sum);
-        ls = fmaf(a, ml_s[i2][hd].y, ls);
+        for (int i2 = 0; i2 < kWarps; ++i2) {
+          const float a = top == -INFINITY ? 0.f : ex2_approx(ml_s[i2][hd].x - top);
+          x0 = fmaf(a, o_s[i2][hd][d], x0);
+          x1 = fmaf(a, o_s[i2][hd][d + 1], x1);
+          ls = fmaf(a, ml_s[i2][hd].y, ls);
+        }
+        const float inv = ls == 0.f ? 0.f : 1.f / ls;  // 0: no entries
+        const int64_t row = (static_cast<int64_t>(b) * p.c.H + h) * p.G + hb * kC4Heads + hd;
+        *reinterpret_cast<uint32_t*>(p.o + row * D + d) = pack_16x2<kType>(x0 * inv, x1 * inv);
+        if (d == 0) p.lse[row] = ls == 0.f ? -INFINITY : (top + log2f(ls)) * kLn2;
       }
-      p.o_part[(slot * kC4Heads + hd) * D + d] = sum;
-      if (d == 0) p.ml_part[slot * kC4Heads + hd] = make_float2(top, ls);
+    } else {
+      const int64_t slot = blockIdx.x + static_cast<int64_t>(b) * rows_per_b + in_b;
+      for (int i = tid; i < heads * D; i += kC4DecThreads) {
+        const int hd = i / D, d = i % D;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i2 = 0; i2 < kWarps; ++i2) top = fmaxf(top, ml_s[i2][hd].x);
+        float sum = 0.f, ls = 0.f;
+#pragma unroll
+        for (int i2 = 0; i2 < kWarps; ++i2) {
+          const float a = top == -INFINITY ? 0.f : ex2_approx(ml_s[i2][hd].x - top);
+          sum = fmaf(a, o_s[i2][hd][d], sum);
+          ls = fmaf(a, ml_s[i2][hd].y, ls);
+        }
+        p.o_part[(slot * kC4Heads + hd) * D + d] = sum;
+        if (d == 0) p.ml_part[slot * kC4Heads + hd] = make_float2(top, ls);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   grid_launch_dependents();
 }
@@ -1032,8 +1070,6 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
 struct DecMergeParams {
   DecParams d;
   int dec_grid;  // CTAs of the decode kernel: the shares
-  uint16_t* o;   // [B][H*G][D]
-  float* lse;    // [B][H*G]
   const float* w_in;
   float* w_out;  // [B][H][cap]
   int warps;     // of the merge kernel that share a row's partials
@@ -1143,7 +1179,7 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
           for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, f[e], acc[e]);
         }
       }
-      if (lane == 0 && warp % step == 0) m.lse[row] = cut.count == 0 ? -INFINITY : (tl.x + log2f(tl.y)) * kLn2;
+      if (lane == 0 && warp % step == 0) p.lse[row] = cut.count == 0 ? -INFINITY : (tl.x + log2f(tl.y)) * kLn2;
     }
     if (m.warps > 1) {
 #pragma unroll
@@ -1155,7 +1191,7 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
           for (int e = 0; e < kPer; ++e) acc[e] += o_s[warp + w][lane * kPer + e];
     }
     if (head < hq && warp % m.warps == 0) {
-      uint16_t* dst = m.o + row * D + lane * kPer;
+      uint16_t* dst = p.o + row * D + lane * kPer;
       const uint32_t lo = pack_16x2<kType>(acc[0] * inv, acc[1] * inv);
       if constexpr (kPer == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack_16x2<kType>(acc[2] * inv, acc[3] * inv));
@@ -1657,6 +1693,9 @@ RowsGrid rows_grid(int64_t rows, int D, int H, int sms) {
   return r;
 }
 
+// One CTA a row, no workspace.
+bool decode_direct(int max_len, bool weight) { return max_len <= kC4DirectLen && !weight; }
+
 // Workspace of a decode call: partial O, partial (m, l), and with weights the
 // scores of every tile.
 struct DecLayout {
@@ -1678,10 +1717,16 @@ DecLayout decode_layout(int B, int H_q, int H_kv, int D, int max_len, bool weigh
 
 template <int D, int kType>
 attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(m.dec_grid));
   const bool weight = m.w_out != nullptr;
-  cudaError_t e = weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true>, grid, dim3(kC4DecThreads), 0, stream, m.d)
-                         : launch_pdl(attn_cache4_decode_kernel<D, kType, false>, grid, dim3(kC4DecThreads), 0, stream, m.d);
+  if (decode_direct(m.d.most, weight)) {
+    const dim3 rows(static_cast<unsigned>(m.d.B * m.d.c.H * m.d.HB));
+    return launch_pdl(attn_cache4_decode_kernel<D, kType, false, true>, rows, dim3(kC4DecThreads), 0, stream, m.d) == cudaSuccess
+               ? ATTN_OK
+               : ATTN_ERR_LAUNCH;
+  }
+  const dim3 grid(static_cast<unsigned>(m.dec_grid));
+  cudaError_t e = weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true, false>, grid, dim3(kC4DecThreads), 0, stream, m.d)
+                         : launch_pdl(attn_cache4_decode_kernel<D, kType, false, false>, grid, dim3(kC4DecThreads), 0, stream, m.d);
   if (e != cudaSuccess) return ATTN_ERR_LAUNCH;
   // blocks for the rows, or for the weights' tiles where those want more
   const int64_t rows = kC4MergeThreads / 32 / m.warps;
@@ -1783,6 +1828,7 @@ attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int
 uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int max_len, int with_weight) {
   if (B < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || H_q / H_kv > 128 || (D != 64 && D != 128) || max_len < 1)
     return 0;
+  if (decode_direct(max_len, with_weight != 0)) return 16;
   const DecLayout l = decode_layout(B, H_q, H_kv, D, max_len, with_weight != 0, kC4WorkspaceSms);
   return static_cast<uint64_t>(l.o_bytes + l.ml_bytes + l.score_bytes);
 }
@@ -1793,7 +1839,7 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
   attn_status_t st = check_cache4(cache);
   if (st != ATTN_OK) return st;
   if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_UNSUPPORTED;
-  if (q == nullptr || o == nullptr || lse == nullptr || workspace == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (q == nullptr || o == nullptr || lse == nullptr) return ATTN_ERR_INVALID_ARG;
   if (H_q < cache->H_kv || H_q % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
   if (H_q / cache->H_kv > 128) return ATTN_ERR_UNSUPPORTED;
   if (q_stride < static_cast<int64_t>(H_q) * cache->D) return ATTN_ERR_INVALID_ARG;
@@ -1803,7 +1849,9 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
   if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(weight_in, 4) || !aligned(weight_out, 4))
     return ATTN_ERR_ALIGNMENT;
-  if (workspace_bytes < attn_cache4_decode_workspace_bytes(cache->B, H_q, cache->H_kv, cache->D, max_len, weight_out != nullptr))
+  if (!decode_direct(max_len, weight_out != nullptr) &&
+      (workspace == nullptr ||
+       workspace_bytes < attn_cache4_decode_workspace_bytes(cache->B, H_q, cache->H_kv, cache->D, max_len, weight_out != nullptr)))
     return ATTN_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   st = prepare_cache4(&dev, &sms);
@@ -1825,8 +1873,8 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
   m.d.ml_part = reinterpret_cast<float2*>(ws + l.o_bytes);
   m.d.scores = weight_out != nullptr ? reinterpret_cast<float*>(ws + l.o_bytes + l.ml_bytes) : nullptr;
   m.dec_grid = l.grid;
-  m.o = static_cast<uint16_t*>(o);
-  m.lse = lse;
+  m.d.o = static_cast<uint16_t*>(o);
+  m.d.lse = lse;
   m.w_in = weight_in;
   m.w_out = weight_out;
   // a warp for every four partials that a row has on average

@@ -646,12 +646,13 @@ bool encode_rows(CUtensorMap* m, const void* ptr, int D, int H, int64_t total, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Units up to which no list is made, where the device has as many SMs.
-constexpr int kVarlenDirect = 152;
-
 // Units the list can hold: one for every 2 * tok tokens and one ragged end a
 // sequence.
 int64_t varlen_cap(int64_t total, int n_seqs, int G) { return total / (kQTiles * (kBM / G)) + n_seqs; }
+
+// Without a list where there are at most as many units as a GB300 has SMs.
+constexpr int kVarlenDirect = 152;
+bool varlen_listed(int64_t cap, int H_kv) { return cap * H_kv > kVarlenDirect; }
 
 template <int D, int kType>
 attn_status_t launch_varlen(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const VarlenParams& prm,
@@ -671,7 +672,7 @@ uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int
       (D != 64 && D != 128))
     return 0;
   const int64_t cap = varlen_cap(total, n_seqs, H_q / H_kv);
-  return 16 + static_cast<uint64_t>(cap) * sizeof(VarlenUnit);
+  return varlen_listed(cap, H_kv) ? 16 + static_cast<uint64_t>(cap) * sizeof(VarlenUnit) : 16;
 }
 
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, int64_t total,
@@ -680,7 +681,7 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
                               void* workspace, uint64_t workspace_bytes, void* stream) {
   if (total < 0 || n_seqs < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0) return ATTN_ERR_INVALID_ARG;
   if (total > 0 && (q == nullptr || k == nullptr || v == nullptr || o == nullptr || lse == nullptr ||
-                    seq_start == nullptr || workspace == nullptr))
+                    seq_start == nullptr))
     return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
@@ -695,7 +696,9 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
   const int G = H_q / H_kv;
   const int64_t cap = varlen_cap(total, n_seqs, G);
   if (cap * H_kv > INT_MAX / 2) return ATTN_ERR_UNSUPPORTED;
-  if (total > 0 && workspace_bytes < attn_fwd_varlen_workspace_bytes(total, n_seqs, H_q, H_kv, D))
+  const bool listed = varlen_listed(cap, H_kv);
+  if (total > 0 && listed &&
+      (workspace == nullptr || workspace_bytes < attn_fwd_varlen_workspace_bytes(total, n_seqs, H_q, H_kv, D)))
     return ATTN_ERR_INVALID_ARG;
   if (total == 0) return ATTN_OK;
 
@@ -722,17 +725,15 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
       !encode_rows(&tk, k, D, H_kv, total, k_stride, 1, kBN, dtype) ||
       !encode_rows(&tv, v, D, H_kv, total, v_stride, 1, kBN, dtype))
     return ATTN_ERR_LAUNCH;
-  const int sms = g_dev_sms[dev].load(std::memory_order_relaxed);
-  const bool listed = cap * H_kv > std::min(sms, kVarlenDirect);
-  int32_t* n_listed = static_cast<int32_t*>(workspace);
-  VarlenUnit* units = reinterpret_cast<VarlenUnit*>(static_cast<char*>(workspace) + 16);
+  int32_t* n_listed = listed ? static_cast<int32_t*>(workspace) : nullptr;
+  VarlenUnit* units = listed ? reinterpret_cast<VarlenUnit*>(static_cast<char*>(workspace) + 16) : nullptr;
   if (listed && launch_pdl(attn_varlen_plan, dim3(1), dim3(kPlanThreads), 0, st, seq_start, n_seqs, total, kQTiles * tok, causal,
                  units, n_listed, static_cast<int>(cap)) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
   VarlenParams prm;
   prm.o = static_cast<uint16_t*>(o);
   prm.lse = lse;
-  prm.units = listed ? units : nullptr;
+  prm.units = units;
   prm.n_listed = n_listed;
   prm.seq_start = seq_start;
   prm.n_seqs = n_seqs;
@@ -745,7 +746,8 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
   prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   prm.causal = causal;
   prm.timeout_ns = kDefaultTimeoutNs;
-  const int grid = static_cast<int>(std::min<int64_t>(cap * H_kv, sms));
+  const int64_t n_ctas = cap * H_kv;  // without a list a CTA to each, whatever SMs there are
+  const int grid = static_cast<int>(listed ? std::min<int64_t>(n_ctas, g_dev_sms[dev].load(std::memory_order_relaxed)) : n_ctas);
   if (D == 64)
     return dtype == ATTN_BF16 ? launch_varlen<64, kBF16>(tq, tk, tv, prm, grid, st)
                               : launch_varlen<64, kFP16>(tq, tk, tv, prm, grid, st);

@@ -24,8 +24,8 @@ INVALID, UNSUPPORTED, ALIGNMENT = attn.ATTN_ERR_INVALID_ARG, attn.ATTN_ERR_UNSUP
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
-    (dict(lse=None), INVALID), (dict(seq_start=None), INVALID), (dict(workspace=None), INVALID),
-    (dict(workspace_bytes=8), INVALID), (dict(total=-1), INVALID), (dict(n_seqs=0), INVALID),
+    (dict(lse=None), INVALID), (dict(seq_start=None), INVALID), (dict(total=-1), INVALID),
+    (dict(total=9000, workspace=None), INVALID), (dict(total=9000, workspace_bytes=16 + 12 * 73 - 1), INVALID), (dict(n_seqs=0), INVALID),
     (dict(H_kv=0), INVALID), (dict(H_q=6), INVALID), (dict(H_q=2), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
     (dict(q_stride=8 * 64 - 8), INVALID), (dict(k_stride=4 * 64 - 8), INVALID), (dict(v_stride=0), INVALID),
@@ -47,6 +47,9 @@ def test_varlen_argument_checks(kw, expect):
 def test_varlen_workspace_size():
     # a header, then 12 bytes for every 2 * (128 / G) tokens and one ragged unit a sequence
     assert attn.attn_fwd_varlen_workspace_bytes(1000, 7, 32, 8, 128) == 16 + 12 * (1000 // 64 + 7)
+    # none where those units, of every key head, are no more than 152
+    assert attn.attn_fwd_varlen_workspace_bytes(1000, 4, 32, 8, 128) == 16
+    assert attn.attn_fwd_varlen_workspace_bytes(1000, 5, 32, 8, 128) == 16 + 12 * (1000 // 64 + 5)
     for bad in ((-1, 1, 8, 8, 64), (10, 0, 8, 8, 64), (10, 1, 8, 3, 64), (10, 1, 8, 8, 96), (10, 1, 129, 1, 64)):
         assert attn.attn_fwd_varlen_workspace_bytes(*bad) == 0
 
@@ -102,12 +105,15 @@ def test_read_argument_checks(kw, expect):
     assert attn.call_status(attn.attn_cache4_read, cache(), **args) == expect
 
 
+WEIGHTS = dict(weight_in=FAKE, weight_out=FAKE)
+
+
 @pytest.mark.parametrize("kw,expect", [
-    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID), (dict(workspace=None), INVALID),
-    (dict(workspace_bytes=100), INVALID), (dict(H_q=3, q_stride=256), INVALID), (dict(H_q=0), INVALID),
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID), (dict(workspace=None, **WEIGHTS), INVALID),
+    (dict(H_q=3, q_stride=256), INVALID), (dict(H_q=0), INVALID),
     (dict(q_stride=248), INVALID), (dict(max_len=0), INVALID), (dict(max_len=101), INVALID),
     (dict(scale=-1.0), INVALID), (dict(weight_in=FAKE), INVALID), (dict(weight_out=FAKE), INVALID),
-    (dict(weight_in=FAKE, weight_out=FAKE), INVALID),  # the workspace lacks the scores' room
+    (dict(**WEIGHTS), INVALID),  # the workspace lacks the scores' room
     (dict(dtype=attn.ATTN_FP32), UNSUPPORTED), (dict(H_q=2 * 129, q_stride=2 * 129 * 64), UNSUPPORTED),
     (dict(q=FAKE + 8), ALIGNMENT), (dict(q_stride=260), ALIGNMENT), (dict(o=FAKE + 8), ALIGNMENT),
     (dict(workspace=FAKE + 4), ALIGNMENT),
@@ -145,8 +151,18 @@ def test_workspace_sizes_refuse_what_the_calls_refuse():
     for bad in ((0, 1, 10, 5), (1, 0, 10, 5), (1, 1, 0, 5), (1, 1, 10, 0)):
         assert attn.attn_cache4_evict_workspace_bytes(*bad) == 0
     # scores of every 64-key tile and query head come on top
-    a, b = (attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 1000, w) for w in (0, 1))
-    assert b - a == 2 * 8 * 16 * 3 * 64 * 4
+    a, b = (attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 2000, w) for w in (0, 1))
+    assert b - a == 2 * 8 * 32 * 3 * 64 * 4
+    # none for short caches without weights
+    assert attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 1024, 0) == 16
+    assert attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 1025, 0) > 16
+
+
+def test_long_caches_need_the_decode_workspace():
+    n = attn.attn_cache4_decode_workspace_bytes(3, 4, 2, 64, 2000, False)
+    args = dict(q=FAKE, q_stride=256, o=FAKE, lse=FAKE, H_q=4, dtype=0, scale=0.1, max_len=2000, weight_in=None, weight_out=None)
+    for ws, nbytes in ((None, n), (FAKE, n - 1)):
+        assert attn.call_status(attn.attn_cache4_decode, cache(capacity=2000), workspace=ws, workspace_bytes=nbytes, **args) == INVALID
 
 
 def test_python_calls_check_their_tensors():
