@@ -350,11 +350,10 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 // its four warps take 16 keys of every tile each, with running statistics of
 // their own, and join at the segment's end into one partial (m, l, O).  The
 // merge kernel joins the partials of a row.  Where max_len is at most
-// kC4DirectLen and no weights are asked for, a CTA takes a whole row instead and
-// writes O and LSE itself: one launch and no workspace.  (One sequence of 701
-// entries, 16 heads, D = 64: MEASURED us on the GPU either way, but the host
-// needs 20 us to make the two launches and the workspace and MEASURED for the
-// one.)
+// kC4DirectLen a CTA takes a whole row instead and writes O and LSE itself, and
+// the weights where the row has all the heads of its key head: one launch, and
+// without weights no workspace.  (One sequence of 701 entries, 16 heads, D = 64:
+// 4.2 us on the GPU instead of 7.7, and 13 us on the host instead of 20.)
 
 constexpr int kC4DecThreads = 128;  // 4 warps
 constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
@@ -363,7 +362,12 @@ constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
 // instructions side by side; with four (128, spills) it took 153 us instead of
 // 140 at 64 sequences of up to 16000 entries with weights.
 constexpr int kC4DecCtasPerSm = 3;
-constexpr int kC4DirectLen = 1024;
+// Longest caches for which a CTA takes a whole row.  GPU time per call, that way
+// against shares (us; without weights, 2048 entries): 1 sequence of 8 heads, D = 128
+// 9.1 / 9.7; 64 sequences 32.0 / 33.3; 16 of 16 heads, D = 64 10.9 / 17.5.  With 4096:
+// 14.7 / 11.2, 56.8 / 53.8, 18.6 / 23.7.  With weights, 2048 entries: 16.2 / 12.3,
+// 44.4 / 47.0, 13.3 / 18.9; 4096: 18.4 / 14.1, 94.1 / 70.9, 23.8 / 26.8.
+constexpr int kC4DirectLen = 2048;
 constexpr int kC4RowCost = 6;       // tiles' worth of time that a row costs a CTA
 // A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
 // so that a size asked for on one device (or with none) holds on any.
@@ -384,6 +388,8 @@ struct DecParams {
   float* scores;    // [tile of a (sequence, key head)][G][64], log2 units, or null
   uint16_t* o;      // [B][H*G][D]
   float* lse;       // [B][H*G]
+  const float* w_in;
+  float* w_out;     // [B][H][cap]
 };
 
 __device__ __forceinline__ int c4_tiles(const DecParams& p, int b) {
@@ -884,11 +890,42 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
   }
 }
 
-// kDirect: CTA x takes the whole of row x.
+// Adds the weights of tiles t0 .. t1 - 1 of a (sequence, key head) with n
+// entries: exp2(score - lse) summed over the heads of its group.  16 threads a
+// tile, 4 keys each.  `scores`: of the row's tile 0, [tile][G][64]; kOwn: written
+// by this block before a barrier, else by an earlier kernel.
+template <bool kOwn>
+__device__ __forceinline__ void c4_add_weights(const DecParams& p, int b, int h, int n, int t0, int t1, const float* scores,
+                                               const float* lse_s) {
+  const int k0 = (static_cast<int>(threadIdx.x) & 15) * 4;
+  for (int t = t0 + (static_cast<int>(threadIdx.x) >> 4); t < t1; t += static_cast<int>(blockDim.x) >> 4) {
+    const int64_t at = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap + static_cast<int64_t>(t) * kC4TileKeys + k0;
+    const int left = n - t * kC4TileKeys - k0;  // of these 4 keys on
+    const float4* src = reinterpret_cast<const float4*>(scores + static_cast<int64_t>(t) * p.G * kC4TileKeys + k0);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, in[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) in[e] = e < left ? p.w_in[at + e] : 0.f;
+#pragma unroll 8
+    for (int g = 0; g < p.G; ++g) {
+      const float4 x = kOwn ? src[g * (kC4TileKeys / 4)] : __ldg(src + g * (kC4TileKeys / 4));
+      const float z = lse_s[g];
+      sum[0] += ex2_approx(x.x - z);
+      sum[1] += ex2_approx(x.y - z);
+      sum[2] += ex2_approx(x.z - z);
+      sum[3] += ex2_approx(x.w - z);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) p.w_out[at + e] = in[e] + sum[e];
+  }
+}
+
+// kDirect: CTA x takes the whole of row x (with weights: one block of heads a
+// key head, so the row has all of an entry's weight).
 template <int D, int kType, bool kWeight, bool kDirect>
 __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     attn_cache4_decode_kernel(const DecParams p) {
-  static_assert(!(kWeight && kDirect), "weights need the merge kernel");
+
   constexpr int kG = D / kC4Group;
   constexpr int kWarps = kC4DecThreads / 32;
   using Ring = C4Ring<D>;
@@ -897,6 +934,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
   float(*const o_s)[kC4Heads][D + 4] = reinterpret_cast<float(*)[kC4Heads][D + 4]>(ring_s);
   static_assert(sizeof(float) * kWarps * kC4Heads * (D + 4) <= sizeof(ring_s), "O in the ring");
   __shared__ float2 ml_s[kWarps][kC4Heads];
+  __shared__ float lse_s[kC4Heads];
   __shared__ int64_t sums_s[kWarps];
   __shared__ int64_t before_s;
   __shared__ int b_s;
@@ -965,7 +1003,8 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
         for (int e = 0; e < 4; ++e) st.o[g][u][e] = 0.f;
     }
     // scores of (sequence, key head): its tiles in list order without the head blocks
-    float* sc = kWeight ? p.scores + (((w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * w.nt + t0) * p.G + hb * kC4Heads + 2 * c) * kC4TileKeys +
+    float* sc = kWeight ? p.scores + ((kDirect ? (static_cast<int64_t>(b) * p.c.H + h) * ((p.most + kC4TileKeys - 1) / kC4TileKeys)
+                                           : (w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * w.nt + t0) * p.G + hb * kC4Heads + 2 * c) * kC4TileKeys +
                               warp * 16 + key
                         : nullptr;
     const int64_t sc_step = static_cast<int64_t>(p.G) * kC4TileKeys;
@@ -1042,7 +1081,16 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
         const float inv = ls == 0.f ? 0.f : 1.f / ls;  // 0: no entries
         const int64_t row = (static_cast<int64_t>(b) * p.c.H + h) * p.G + hb * kC4Heads + hd;
         *reinterpret_cast<uint32_t*>(p.o + row * D + d) = pack_16x2<kType>(x0 * inv, x1 * inv);
-        if (d == 0) p.lse[row] = ls == 0.f ? -INFINITY : (top + log2f(ls)) * kLn2;
+        if (d == 0) {
+          p.lse[row] = ls == 0.f ? -INFINITY : (top + log2f(ls)) * kLn2;
+          if (kWeight) lse_s[hd] = top + log2f(ls);
+        }
+      }
+      if constexpr (kWeight) {
+        __syncthreads();
+        c4_add_weights<true>(p, b, h, n, t0, t1,
+                             p.scores + (static_cast<int64_t>(b) * p.c.H + h) * ((p.most + kC4TileKeys - 1) / kC4TileKeys) * p.G * kC4TileKeys,
+                             lse_s);
       }
     } else {
       const int64_t slot = blockIdx.x + static_cast<int64_t>(b) * rows_per_b + in_b;
@@ -1070,8 +1118,6 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
 struct DecMergeParams {
   DecParams d;
   int dec_grid;  // CTAs of the decode kernel: the shares
-  const float* w_in;
-  float* w_out;  // [B][H][cap]
   int warps;     // of the merge kernel that share a row's partials
 };
 
@@ -1226,29 +1272,8 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
           if (lane == 0) lse_s[g] = tl.x + log2f(tl.y);
         }
         __syncthreads();
-        const int64_t at0 = (static_cast<int64_t>(b) * p.c.H + h) * p.c.cap;
-        for (int t = w.t0 + (tid >> 4); t < w.t1; t += kC4MergeTiles) {
-          const int k0 = (tid & 15) * 4;
-          const int64_t at = at0 + static_cast<int64_t>(t) * kC4TileKeys + k0;
-          const int left = n - t * kC4TileKeys - k0;  // of these 4 keys on
-          const float4* src = reinterpret_cast<const float4*>(
-              p.scores + ((w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * nt + t) * p.G * kC4TileKeys + k0);
-          float sum[4] = {0.f, 0.f, 0.f, 0.f}, in[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) in[e] = e < left ? m.w_in[at + e] : 0.f;
-#pragma unroll 8
-          for (int g = 0; g < p.G; ++g) {
-            const float4 x = __ldg(src + g * (kC4TileKeys / 4));
-            const float z2 = lse_s[g];
-            sum[0] += ex2_approx(x.x - z2);
-            sum[1] += ex2_approx(x.y - z2);
-            sum[2] += ex2_approx(x.z - z2);
-            sum[3] += ex2_approx(x.w - z2);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < left) m.w_out[at + e] = in[e] + sum[e];
-        }
+        c4_add_weights<false>(p, b, h, n, w.t0, w.t1, p.scores + ((w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * nt) * p.G * kC4TileKeys,
+                              lse_s);
         __syncthreads();
       }
     }
@@ -1693,8 +1718,10 @@ RowsGrid rows_grid(int64_t rows, int D, int H, int sms) {
   return r;
 }
 
-// One CTA a row, no workspace.
-bool decode_direct(int max_len, bool weight) { return max_len <= kC4DirectLen && !weight; }
+// One CTA a row; the workspace then holds the scores of a call with weights.
+bool decode_direct(int max_len, int HB, bool weight) {
+  return max_len <= kC4DirectLen && (HB == 1 || !weight);
+}
 
 // Workspace of a decode call: partial O, partial (m, l), and with weights the
 // scores of every tile.
@@ -1717,12 +1744,13 @@ DecLayout decode_layout(int B, int H_q, int H_kv, int D, int max_len, bool weigh
 
 template <int D, int kType>
 attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t stream) {
-  const bool weight = m.w_out != nullptr;
-  if (decode_direct(m.d.most, weight)) {
+  const bool weight = m.d.w_out != nullptr;
+  if (decode_direct(m.d.most, m.d.HB, weight)) {
     const dim3 rows(static_cast<unsigned>(m.d.B * m.d.c.H * m.d.HB));
-    return launch_pdl(attn_cache4_decode_kernel<D, kType, false, true>, rows, dim3(kC4DecThreads), 0, stream, m.d) == cudaSuccess
-               ? ATTN_OK
-               : ATTN_ERR_LAUNCH;
+    const cudaError_t e =
+        weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true, true>, rows, dim3(kC4DecThreads), 0, stream, m.d)
+               : launch_pdl(attn_cache4_decode_kernel<D, kType, false, true>, rows, dim3(kC4DecThreads), 0, stream, m.d);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
   }
   const dim3 grid(static_cast<unsigned>(m.dec_grid));
   cudaError_t e = weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true, false>, grid, dim3(kC4DecThreads), 0, stream, m.d)
@@ -1828,7 +1856,7 @@ attn_status_t attn_cache4_read(const attn_cache4_t* cache, void* k, void* v, int
 uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int max_len, int with_weight) {
   if (B < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || H_q / H_kv > 128 || (D != 64 && D != 128) || max_len < 1)
     return 0;
-  if (decode_direct(max_len, with_weight != 0)) return 16;
+  if (with_weight == 0 && decode_direct(max_len, 1, false)) return 16;
   const DecLayout l = decode_layout(B, H_q, H_kv, D, max_len, with_weight != 0, kC4WorkspaceSms);
   return static_cast<uint64_t>(l.o_bytes + l.ml_bytes + l.score_bytes);
 }
@@ -1849,7 +1877,7 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
   if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(weight_in, 4) || !aligned(weight_out, 4))
     return ATTN_ERR_ALIGNMENT;
-  if (!decode_direct(max_len, weight_out != nullptr) &&
+  if ((weight_out != nullptr || !decode_direct(max_len, 1, false)) &&
       (workspace == nullptr ||
        workspace_bytes < attn_cache4_decode_workspace_bytes(cache->B, H_q, cache->H_kv, cache->D, max_len, weight_out != nullptr)))
     return ATTN_ERR_INVALID_ARG;
@@ -1875,8 +1903,8 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
   m.dec_grid = l.grid;
   m.d.o = static_cast<uint16_t*>(o);
   m.d.lse = lse;
-  m.w_in = weight_in;
-  m.w_out = weight_out;
+  m.d.w_in = weight_in;
+  m.d.w_out = weight_out;
   // a warp for every four partials that a row has on average
   const int64_t parts = l.grid / (static_cast<int64_t>(m.d.B) * m.d.c.H * m.d.HB) + 1;
   m.warps = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;

@@ -446,3 +446,14 @@ def test_graph_of_a_decode_step_and_a_side_stream():
         assert torch.equal(getattr(a, n), getattr(b, n)) and torch.equal(getattr(a, n), getattr(e, n))
     assert torch.equal(a.weight.nan_to_num(-1), e.weight.nan_to_num(-1))
     ok()
+
+
+@pytest.mark.parametrize("weight", [True, False])
+@pytest.mark.parametrize("max_len", [2048, 2049])
+@pytest.mark.parametrize("hq", [16, 18])
+def test_attend_both_sides_of_the_one_launch_rule(hq, max_len, weight):
+    """2048 entries a CTA a row, one more: shares; groups of 8 and 9 heads, of which the second needs two blocks."""
+    lens = [2048, 1500, 0, 64, 2047]
+    c = filled(5, 2, 2049, 128, lens, seed=hq)
+    q = torch.randn((5, hq, 128), generator=gen(1), device="cuda").half()
+    check_attend(c, q, lens, weight=weight, max_len=max_len)

@@ -151,18 +151,18 @@ def test_workspace_sizes_refuse_what_the_calls_refuse():
     for bad in ((0, 1, 10, 5), (1, 0, 10, 5), (1, 1, 0, 5), (1, 1, 10, 0)):
         assert attn.attn_cache4_evict_workspace_bytes(*bad) == 0
     # scores of every 64-key tile and query head come on top
-    a, b = (attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 2000, w) for w in (0, 1))
-    assert b - a == 2 * 8 * 32 * 3 * 64 * 4
+    a, b = (attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 5000, w) for w in (0, 1))
+    assert b - a == 2 * 8 * 79 * 3 * 64 * 4
     # none for short caches without weights
-    assert attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 1024, 0) == 16
-    assert attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 1025, 0) > 16
+    assert attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 2048, 0) == 16
+    assert attn.attn_cache4_decode_workspace_bytes(2, 24, 8, 128, 2049, 0) > 16
 
 
 def test_long_caches_need_the_decode_workspace():
-    n = attn.attn_cache4_decode_workspace_bytes(3, 4, 2, 64, 2000, False)
-    args = dict(q=FAKE, q_stride=256, o=FAKE, lse=FAKE, H_q=4, dtype=0, scale=0.1, max_len=2000, weight_in=None, weight_out=None)
+    n = attn.attn_cache4_decode_workspace_bytes(3, 4, 2, 64, 2500, False)
+    args = dict(q=FAKE, q_stride=256, o=FAKE, lse=FAKE, H_q=4, dtype=0, scale=0.1, max_len=2500, weight_in=None, weight_out=None)
     for ws, nbytes in ((None, n), (FAKE, n - 1)):
-        assert attn.call_status(attn.attn_cache4_decode, cache(capacity=2000), workspace=ws, workspace_bytes=nbytes, **args) == INVALID
+        assert attn.call_status(attn.attn_cache4_decode, cache(capacity=2500), workspace=ws, workspace_bytes=nbytes, **args) == INVALID
 
 
 def test_python_calls_check_their_tensors():
