@@ -394,7 +394,9 @@ uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int
  *   entries are no longer in the order of their positions, which attention does
  *   not need, and what lies behind the budget is left as it was.
  *
- *   budget 1 or more, recent 0 .. budget, max_len as attn_cache4_decode.
+ *   budget 1 or more, recent 0 .. budget, max_len as attn_cache4_decode, but at
+ *   most ATTN_CACHE4_EVICT_MAX_LEN unless the budget is no less
+ *   (ATTN_ERR_UNSUPPORTED).
  *   weight_out, pos_out, length_out
  *               the cache's weight, pos and length after the call.  Each may be
  *               the cache's own buffer (the length costs one more small launch)
@@ -404,6 +406,7 @@ uint64_t attn_cache4_decode_workspace_bytes(int B, int H_q, int H_kv, int D, int
  *               aligned; overwritten.  Calls that share one must be ordered.
  * cache->weight and cache->pos are needed.  Asynchronous.
  */
+#define ATTN_CACHE4_EVICT_MAX_LEN 393216
 attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int recent, int max_len,
                                 float* weight_out, int32_t* pos_out, int32_t* length_out,
                                 void* workspace, uint64_t workspace_bytes, void* stream);

@@ -185,8 +185,8 @@ class KVCache4:
         Each key head keeps the entries of the `recent` newest positions, then
         those of the highest weight (ties: the lower slot).  Kept entries from
         behind the budget move into the slots that became free; attention does not
-        depend on the entries' order.  max_len: as attend takes it; entries behind
-        it are dropped.
+        depend on the entries' order.  max_len: as attend takes it, at most 393216
+        (or the budget); entries behind it are dropped.
         """
         import torch
 

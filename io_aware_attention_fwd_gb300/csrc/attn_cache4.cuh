@@ -1297,7 +1297,8 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
 // a radix select, 8 bits a round, most significant first, over histograms
 // that the CTAs add up through distributed shared memory; counts of ties,
 // holes and movers before each slice come the same way.  Every key is read
-// from HBM once, whatever the budget.
+// from HBM once, whatever the budget.  What is left to wait for, in a CTA of a
+// long row (8192 entries to 2048, 1.9 GHz): MEASURED-EVICT
 
 // Threads of a CTA.  1024 hide more of the latency of long slices and many moves
 // (24 sequences of up to 8192 entries cut to 2048: 26 us against 37 us with 512),
@@ -1306,7 +1307,7 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
 constexpr int kC4EvictFew = 512, kC4EvictMany = 1024;
 constexpr int kC4EvictLong = 4096;  // a slice of more entries takes kC4EvictMany threads
 constexpr int kC4EvictCluster = 8;             // CTAs of a cluster at most
-constexpr int kC4EvictSmemKeys = 48 * 1024;    // keys a CTA can hold in shared memory
+constexpr int kC4EvictSmemKeys = 48 * 1024;    // keys a CTA can hold in shared memory: its slice at most
 
 struct EvictParams {
   Cache4 c;
@@ -1319,8 +1320,6 @@ struct EvictParams {
   int most;          // bound on the lengths
   int budget;
   int recent;
-  int smem_keys;     // keys that fit into this launch's shared memory
-  uint32_t* keys;    // [B*H][most] for slices that do not, or null
   int32_t* moves;    // [B*H][2][list]: holes, then movers
   int list;
 };
@@ -1355,34 +1354,33 @@ __device__ __forceinline__ uint32_t c4_rank_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum over the block of (a, b) before this thread, and the totals.
+// Exclusive sums over the block's table of `n` <= 2 * kThreads counts, in place;
+// returns the total.  Two 16-bit counts share a word (sums below 2^16).
 template <int kThreads>
-__device__ __forceinline__ uint2 block_scan2(uint2 v, uint2* warp_s, uint2* total) {
-  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
-  uint2 incl = v;
+__device__ __forceinline__ uint32_t block_scan(uint32_t* table, int n, uint32_t* warp_s) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const uint32_t v0 = 2 * tid < n ? table[2 * tid] : 0u, v1 = 2 * tid + 1 < n ? table[2 * tid + 1] : 0u;
+  uint32_t incl = v0 + v1;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, off), y = __shfl_up_sync(0xffffffffu, incl.y, off);
-    if (lane >= off) {
-      incl.x += x;
-      incl.y += y;
-    }
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
   }
-  __syncthreads();  // warp_s is free again
   if (lane == 31) warp_s[warp] = incl;
   __syncthreads();
-  uint2 before = make_uint2(incl.x - v.x, incl.y - v.y), all = make_uint2(0, 0);
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const uint2 s = warp_s[w];
-    if (w < warp) {
-      before.x += s.x;
-      before.y += s.y;
-    }
-    all.x += s.x;
-    all.y += s.y;
+  uint32_t ws = lane < kThreads / 32 ? warp_s[lane] : 0u;  // every warp sums the warps' totals
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, ws, off);
+    if (lane >= off) ws += y;
   }
-  *total = all;
-  return before;
+  const uint32_t total = __shfl_sync(0xffffffffu, ws, kThreads / 32 - 1);
+  const uint32_t before = warp > 0 ? __shfl_sync(0xffffffffu, ws, warp - 1) : 0u;
+  const uint32_t excl = before + incl - v0 - v1;
+  if (2 * tid < n) table[2 * tid] = excl;
+  if (2 * tid + 1 < n) table[2 * tid + 1] = excl + v0;
+  __syncthreads();
+  return total;
 }
 
 // kMulti: clusters of more than one CTA; without, the cluster barriers are the
@@ -1393,7 +1391,11 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
   __shared__ uint32_t hist[2][256];  // rounds alternate, so that one is cleared while the other is read
   __shared__ uint32_t share[4];      // what the other CTAs read: newest, ties, holes, movers
   __shared__ uint32_t found[3];      // digit, entries still to take, entries with it
-  __shared__ uint2 warp_s[kThreads / 32];
+  __shared__ uint32_t warp_s[kThreads / 32];
+  // of each warp's 32 slots in each round over the slice: ties, or holes and movers
+  constexpr int kWarps = kThreads / 32;
+  __shared__ uint32_t table[kThreads == kC4EvictMany ? 2 * kThreads : (kC4EvictLong / kThreads + 1) * kWarps];
+  static_assert(kThreads != kC4EvictMany || kC4EvictSmemKeys / 32 <= 2 * kThreads, "the table holds a slice in shared memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
   const uint32_t rank = kMulti ? cluster_rank() : 0u, R = kMulti ? cluster_size() : 1u;
   const auto sync_all = [] {
@@ -1424,7 +1426,7 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
     grid_launch_dependents();
     return;
   }
-  uint32_t* const key = slice <= p.smem_keys ? smem_keys : p.keys + bh * p.most + i0;
+  uint32_t* const key = smem_keys;
 
   // Rank keys of the slice, and the newest position; four entries in flight a
   // thread.
@@ -1446,10 +1448,10 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
     }
   }
   newest = __reduce_max_sync(0xffffffffu, newest);
-  if (lane == 0) warp_s[tid >> 5].x = static_cast<uint32_t>(newest);
+  if (lane == 0) warp_s[tid >> 5] = static_cast<uint32_t>(newest);
   __syncthreads();
   if (tid < 32) {
-    newest = tid < kThreads / 32 ? static_cast<int>(warp_s[tid].x) : INT_MIN;
+    newest = tid < kThreads / 32 ? static_cast<int>(warp_s[tid]) : INT_MIN;
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (tid == 0) share[0] = static_cast<uint32_t>(newest);
   }
@@ -1521,53 +1523,74 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
   }
 
   // Kept: keys above `prefix` in the digits seen, and the first `take` equal to
-  // it.  A thread walks consecutive slots (an odd count: no bank conflicts).
-  const int per = ((mine + kThreads - 1) / kThreads) | 1;
-  const int s0 = min(mine, tid * per), s1 = min(mine, s0 + per);
-  uint2 v = make_uint2(0, 0), all;
-  uint32_t eq_rank = 0u;
-  if (ties) {  // which of the equal ones: by their order
-    for (int i = s0; i < s1; ++i) v.x += (key[i] & seen) == prefix;
-    eq_rank = block_scan2<kThreads>(v, warp_s, &all).x;
+  // it, in slot order.  Ranks come from the warps' votes, a table of their
+  // counts and its sums: three coalesced passes over the keys.
+  const int warp = tid >> 5;
+  const uint32_t below = (1u << lane) - 1u;
+  const int rounds = (mine + kThreads - 1) / kThreads;
+  uint32_t eq_before = 0u;  // ties in the slices before this one
+  if (ties) {
+    for (int j = 0; j < rounds; ++j) {
+      const int i = j * kThreads + tid;
+      const uint32_t eq = __ballot_sync(0xffffffffu, i < mine && (key[i] & seen) == prefix);
+      if (lane == 0) table[j * kWarps + warp] = __popc(eq);
+    }
+    __syncthreads();
+    const uint32_t all = block_scan<kThreads>(table, rounds * kWarps, warp_s);
     if (kMulti) {
-      if (tid == 0) share[1] = all.x;
+      if (tid == 0) share[1] = all;
       sync_all();
-      for (uint32_t q = 0; q < rank; ++q) eq_rank += peer(&share[1], q);
+      for (uint32_t q = 0; q < rank; ++q) eq_before += peer(&share[1], q);
     }
   }
-  v = make_uint2(0, 0);
-  for (int i = s0; i < s1; ++i) {
-    const uint32_t k = key[i] & seen;
-    bool keep = k > prefix;
-    if (k == prefix) keep = !ties || eq_rank++ < take;
-    key[i] = keep;
-    v.x += !keep && i0 + i < left;  // a hole
-    v.y += keep && i0 + i >= left;  // a mover
+  for (int j = 0; j < rounds; ++j) {
+    const int i = j * kThreads + tid;
+    bool keep = false;
+    if (ties) {
+      const bool eq = i < mine && (key[i] & seen) == prefix;
+      const uint32_t votes = __ballot_sync(0xffffffffu, eq);
+      if (eq) keep = eq_before + table[j * kWarps + warp] + __popc(votes & below) < take;
+      __syncwarp();  // the table entry is read: it is written below
+    } else if (i < mine) {
+      keep = (key[i] & seen) == prefix;
+    }
+    if (i < mine) {
+      keep = keep || (key[i] & seen) > prefix;
+      key[i] = keep;
+    }
+    const uint32_t hole = __ballot_sync(0xffffffffu, i < mine && !keep && i0 + i < left);
+    const uint32_t mover = __ballot_sync(0xffffffffu, i < mine && keep && i0 + i >= left);
+    if (lane == 0) table[j * kWarps + warp] = __popc(hole) | __popc(mover) << 16;
   }
-  const uint2 at = block_scan2<kThreads>(v, warp_s, &all);
-  uint32_t hole = at.x, mover = at.y, n_moves = all.x;
+  __syncthreads();
+  const uint32_t all = block_scan<kThreads>(table, rounds * kWarps, warp_s);
+  uint32_t hole0 = 0u, mover0 = 0u, n_moves = all & 0xffffu;
   if (kMulti) {
     if (tid == 0) {
-      share[2] = all.x;
-      share[3] = all.y;
+      share[2] = all & 0xffffu;
+      share[3] = all >> 16;
     }
     sync_all();
     n_moves = 0u;
     for (uint32_t q = 0; q < R; ++q) {
       const uint32_t x = peer(&share[2], q);
       if (q < rank) {
-        hole += x;
-        mover += peer(&share[3], q);
+        hole0 += x;
+        mover0 += peer(&share[3], q);
       }
       n_moves += x;
     }
   }
   int32_t* const holes = p.moves + bh * 2 * p.list;
   int32_t* const movers = holes + p.list;
-  for (int i = s0; i < s1; ++i) {
-    const bool keep = key[i] != 0u;
-    if (!keep && i0 + i < left) holes[hole++] = i0 + i;
-    if (keep && i0 + i >= left) movers[mover++] = i0 + i;
+  for (int j = 0; j < rounds; ++j) {
+    const int i = j * kThreads + tid;
+    const bool keep = i < mine && key[i] != 0u;
+    const bool is_hole = i < mine && !keep && i0 + i < left, is_mover = keep && i0 + i >= left;
+    const uint32_t hole = __ballot_sync(0xffffffffu, is_hole), mover = __ballot_sync(0xffffffffu, is_mover);
+    const uint32_t at = table[j * kWarps + warp];
+    if (is_hole) holes[hole0 + (at & 0xffffu) + __popc(hole & below)] = i0 + i;
+    if (is_mover) movers[mover0 + (at >> 16) + __popc(mover & below)] = i0 + i;
   }
   sync_all();  // the lists are written; no CTA reads another's shared memory any more
   grid_launch_dependents();
@@ -1779,8 +1802,9 @@ int evict_cluster(int64_t BH, int max_len) {
 int64_t evict_list(int max_len, int budget) {
   return std::max<int64_t>(1, std::min<int64_t>(budget, static_cast<int64_t>(max_len) - budget));
 }
-// Whether some CTA's slice outgrows shared memory.
-bool evict_spills(int max_len, int R) { return (static_cast<int64_t>(max_len) + R - 1) / R > kC4EvictSmemKeys; }
+// Longest sequences whose keys a cluster holds.
+constexpr int kC4EvictMostLen = kC4EvictCluster * kC4EvictSmemKeys;
+static_assert(kC4EvictMostLen == ATTN_CACHE4_EVICT_MAX_LEN, "the header's limit");
 
 }  // namespace
 
@@ -1917,9 +1941,9 @@ attn_status_t attn_cache4_decode(const attn_cache4_t* cache, const void* q, int6
 uint64_t attn_cache4_evict_workspace_bytes(int B, int H_kv, int max_len, int budget) {
   if (B < 1 || H_kv < 1 || max_len < 1 || budget < 1) return 0;
   if (budget >= max_len) return 16;
+  if (max_len > kC4EvictMostLen) return 0;
   const int64_t BH = static_cast<int64_t>(B) * H_kv;
-  const bool spills = evict_spills(max_len, evict_cluster(BH, max_len));
-  return static_cast<uint64_t>(BH * (2 * evict_list(max_len, budget) + (spills ? max_len : 0)) * 4);
+  return static_cast<uint64_t>(BH * 2 * evict_list(max_len, budget) * 4);
 }
 
 attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int recent, int max_len, float* weight_out,
@@ -1931,6 +1955,7 @@ attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int rece
       length_out == nullptr || workspace == nullptr)
     return ATTN_ERR_INVALID_ARG;
   if (budget < 1 || recent < 0 || recent > budget || max_len < 1 || max_len > cache->capacity) return ATTN_ERR_INVALID_ARG;
+  if (max_len > kC4EvictMostLen && budget < max_len) return ATTN_ERR_UNSUPPORTED;
   if (!aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(length_out, 4) || !aligned(workspace, 16))
     return ATTN_ERR_ALIGNMENT;
   if (workspace_bytes < attn_cache4_evict_workspace_bytes(cache->B, cache->H_kv, max_len, budget)) return ATTN_ERR_INVALID_ARG;
@@ -1953,11 +1978,8 @@ attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int rece
   p.recent = recent;
   p.list = budget < max_len ? static_cast<int>(evict_list(max_len, budget)) : 1;
   p.moves = static_cast<int32_t*>(workspace);
-  const bool spills = budget < max_len && evict_spills(max_len, R);
-  p.keys = spills ? reinterpret_cast<uint32_t*>(p.moves + BH * 2 * p.list) : nullptr;
   const int slice = (max_len + R - 1) / R;
-  p.smem_keys = std::min(slice, kC4EvictSmemKeys);
-  const size_t smem = budget < max_len ? static_cast<size_t>(p.smem_keys) * 4 : 16;
+  const size_t smem = budget < max_len ? static_cast<size_t>(slice) * 4 : 16;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

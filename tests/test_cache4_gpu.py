@@ -346,17 +346,18 @@ def test_evict_long(B, H, n, budget):
     check_evict(c, lens, budget, min(budget, 100), True)
 
 
-def test_evict_keys_outgrow_shared_memory():
-    n = 8 * 48 * 1024 + 1000
+def test_evict_longest():
+    n = 8 * 48 * 1024  # a cluster's shared memory is full of keys
     c = attn.KVCache4.empty(1, 1, n, 64)
     c.weight.copy_(torch.rand((1, 1, n), generator=gen(1), device="cuda"))
+    c.weight[0, 0, 1000:300000] = 0.75  # ties across the slices of several CTAs
     c.pos.copy_(torch.arange(n, device="cuda"))
     c.k_codes.copy_(torch.randint(0, 256, c.k_codes.shape, generator=gen(2), device="cuda", dtype=torch.uint8))
     c.v_codes.copy_(c.k_codes.flip(2))
     c.k_meta.zero_()
     c.v_meta.zero_()
     c.length.fill_(n)
-    check_evict(c, [n], 1000, 10, True)
+    check_evict(c, [n], 200000, 10, True)
 
 
 def test_evict_all_weights_equal_keeps_the_first_slots():

@@ -139,6 +139,15 @@ def test_evict_argument_checks(kw, expect):
     assert attn.call_status(attn.attn_cache4_evict, cache(), **args) == expect
 
 
+def test_evict_longest_sequences():
+    n = 393216
+    c = cache(capacity=n + 1)
+    size = attn.attn_cache4_evict_workspace_bytes(3, 2, n, 10)
+    assert size == 3 * 2 * 2 * 10 * 4 and attn.attn_cache4_evict_workspace_bytes(3, 2, n + 1, 10) == 0
+    for budget, status in ((10, UNSUPPORTED), (n, UNSUPPORTED)):
+        assert attn.call_status(attn.attn_cache4_evict, c, budget, 0, n + 1, FAKE, FAKE, FAKE, FAKE, 1 << 40) == status
+
+
 def test_evict_needs_weights_and_positions():
     n = attn.attn_cache4_evict_workspace_bytes(3, 2, 100, 10)
     for kw in (dict(weight=None), dict(pos=None)):
