@@ -1389,6 +1389,7 @@ template <int D, bool kMulti, int kThreads>
 __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t smem_keys[];
   __shared__ uint32_t hist[2][256];  // rounds alternate, so that one is cleared while the other is read
+  __shared__ uint32_t sums[kMulti ? 256 : 1];
   __shared__ uint32_t share[4];      // what the other CTAs read: newest, ties, holes, movers
   __shared__ uint32_t found[3];      // digit, entries still to take, entries with it
   __shared__ uint32_t warp_s[kThreads / 32];
@@ -1483,12 +1484,24 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
       if ((k & seen) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1u);
     }
     sync_all();
+    // the other histogram was read in the round before, by every CTA before the
+    // barrier above
+    if (tid >= kThreads - 256) hist[(round & 1) ^ 1][tid - (kThreads - 256)] = 0u;
+    const uint32_t* bins = h;
+    if constexpr (kMulti) {  // a thread a bin: each waits for R remote loads, not for 8 R
+      if (tid < 256) {
+        uint32_t sum = 0u;
+        for (uint32_t q = 0; q < R; ++q) sum += peer(&h[tid], q);
+        sums[tid] = sum;
+      }
+      __syncthreads();
+      bins = sums;
+    }
     if (tid < 32) {  // digits from the top: lane j has 255 - 8j .. 248 - 8j
       uint32_t cnt[8], sum = 0u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        cnt[e] = 0u;
-        for (uint32_t q = 0; q < R; ++q) cnt[e] += peer(&h[255 - 8 * lane - e], q);
+        cnt[e] = bins[255 - 8 * lane - e];
         sum += cnt[e];
       }
       uint32_t incl = sum;
@@ -1509,10 +1522,6 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
           before += cnt[e];
         }
       }
-    } else if (tid < 32 + 256) {
-      // the other histogram: read in the round before, by every CTA before the
-      // barrier above
-      hist[(round & 1) ^ 1][tid - 32] = 0u;
     }
     __syncthreads();
     prefix |= found[0] << shift;
@@ -1793,7 +1802,7 @@ attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t strea
 // CTAs of an eviction's clusters: enough to give every SM one, with slices of
 // at least 1024 entries; or as many as hold the keys in shared memory.  More
 // clusters than that lose: with pairs for 256 rows of 2049 entries a call took
-// 39 us instead of 11, with fours for 192 rows of up to 8192 52 instead of 37.
+// 27 us instead of 11, for 192 rows of up to 8192 28 instead of 25 (fours: 39).
 int evict_cluster(int64_t BH, int max_len) {
   int R = 1;
   while (R < kC4EvictCluster && ((BH * R < kC4WorkspaceSms && max_len / (2 * R) >= 1024) || max_len > R * kC4EvictSmemKeys)) R *= 2;
