@@ -941,6 +941,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   const int key = c4_kappa(r);
   grid_dependency_wait();
+  grid_launch_dependents();  // the merge kernel's blocks come as this one's leave
   const int rows_per_b = p.c.H * p.HB;
   C4Walk w;
   if constexpr (kDirect) {
@@ -955,10 +956,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     const int64_t share = (total + gridDim.x - 1) / gridDim.x;
     w.x = static_cast<int64_t>(blockIdx.x) * share;
     w.end = w.x + share < total ? w.x + share : total;
-    if (w.x >= w.end) {
-      grid_launch_dependents();
-      return;
-    }
+    if (w.x >= w.end) return;
     c4_find(p, w.x / rows_per_b, kC4RowCost, mine_before, mine, &b_s, &before_s);
     __syncthreads();
     w.b = b_s;
@@ -1112,13 +1110,13 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       __syncthreads();
     }
   }
-  grid_launch_dependents();
 }
 
 struct DecMergeParams {
   DecParams d;
   int dec_grid;  // CTAs of the decode kernel: the shares
   int warps;     // of the merge kernel that share a row's partials
+  unsigned row_blocks;  // blocks that join rows; those behind them add weights
 };
 
 constexpr int kC4MergeThreads = 256;
@@ -1171,17 +1169,20 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
   __shared__ float lse_s[128];
   __shared__ __align__(16) float o_s[kWarps][D];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  grid_dependency_wait();
-  grid_launch_dependents();
+  // The lengths are not the decode kernel's to write, and whatever wrote them was
+  // complete before that kernel let this one start (its blocks wait for it
+  // first): they are read while it finishes.
   int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
   const int64_t count = c4_total(p, sums_s, &mine_before, &mine);
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int64_t share = max(static_cast<int64_t>(1), (c4_units(count, kC4RowCost) * rows_per_b + m.dec_grid - 1) / m.dec_grid);
 
   // O and LSE: m.warps warps a row, the blocks' rows all of one sequence.
   const int hq = p.c.H * p.G, rows = kWarps / m.warps;
   const int per_b = (hq + rows - 1) / rows;
-  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * per_b; u += gridDim.x) {
+  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * per_b && blockIdx.x < m.row_blocks; u += m.row_blocks) {
     const int b = static_cast<int>(u / per_b);
     const int head = static_cast<int>(u % per_b) * rows + warp / m.warps;
     const int stripe = (p.B + kC4MergeThreads - 1) / kC4MergeThreads;
@@ -1249,13 +1250,14 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
 
   if constexpr (kWeight) {
     // Weights: the tiles of every (sequence, key head) in equal contiguous
-    // shares, one per block, walked row by row; 4 keys a thread.
+    // shares, one for each block behind those of the rows, walked row by row.
     const int64_t all = c4_units(count, kC4MergeRowCost) * p.c.H;
-    const int64_t mine_w = (all + gridDim.x - 1) / gridDim.x;
+    const int64_t blocks = gridDim.x - m.row_blocks;
+    const int64_t mine_w = (all + blocks - 1) / blocks;
     C4Walk w;
-    w.x = static_cast<int64_t>(blockIdx.x) * mine_w;
+    w.x = (static_cast<int64_t>(blockIdx.x) - m.row_blocks) * mine_w;
     w.end = w.x + mine_w < all ? w.x + mine_w : all;
-    if (w.x < w.end) {
+    if (blockIdx.x >= m.row_blocks && w.x < w.end) {
       c4_find(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
       __syncthreads();
       w.b = b_s;
@@ -1775,7 +1777,7 @@ DecLayout decode_layout(int B, int H_q, int H_kv, int D, int max_len, bool weigh
 }
 
 template <int D, int kType>
-attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t stream) {
+attn_status_t launch_decode(DecMergeParams m, int sms, cudaStream_t stream) {
   const bool weight = m.d.w_out != nullptr;
   if (decode_direct(m.d.most, m.d.HB, weight)) {
     const dim3 rows(static_cast<unsigned>(m.d.B * m.d.c.H * m.d.HB));
@@ -1788,12 +1790,13 @@ attn_status_t launch_decode(const DecMergeParams& m, int sms, cudaStream_t strea
   cudaError_t e = weight ? launch_pdl(attn_cache4_decode_kernel<D, kType, true, false>, grid, dim3(kC4DecThreads), 0, stream, m.d)
                          : launch_pdl(attn_cache4_decode_kernel<D, kType, false, false>, grid, dim3(kC4DecThreads), 0, stream, m.d);
   if (e != cudaSuccess) return ATTN_ERR_LAUNCH;
-  // blocks for the rows, or for the weights' tiles where those want more
   const int64_t rows = kC4MergeThreads / 32 / m.warps;
   const int64_t tiles = (static_cast<int64_t>(m.d.most) + kC4TileKeys - 1) / kC4TileKeys * m.d.B * m.d.c.H;
-  int64_t blocks = m.d.B * ((static_cast<int64_t>(m.d.c.H) * m.d.G + rows - 1) / rows);
-  if (weight) blocks = std::max(blocks, (tiles + kC4MergeTiles - 1) / kC4MergeTiles);
-  const dim3 mg(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 8)));
+  m.row_blocks = static_cast<unsigned>(std::min<int64_t>(m.d.B * ((static_cast<int64_t>(m.d.c.H) * m.d.G + rows - 1) / rows),
+                                                         static_cast<int64_t>(sms) * 4));
+  const int64_t weight_blocks =
+      weight ? std::min<int64_t>((tiles + kC4MergeTiles - 1) / kC4MergeTiles, static_cast<int64_t>(sms) * 8) : 0;
+  const dim3 mg(static_cast<unsigned>(m.row_blocks + weight_blocks));
   e = weight ? launch_pdl(attn_cache4_merge_kernel<D, kType, true>, mg, dim3(kC4MergeThreads), 0, stream, m)
              : launch_pdl(attn_cache4_merge_kernel<D, kType, false>, mg, dim3(kC4MergeThreads), 0, stream, m);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
