@@ -111,6 +111,26 @@ __device__ __forceinline__ uint32_t max_16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// (w & mask) | magic in one instruction.  Left to the compiler it became two,
+// and these are the kernel's most frequent ones: ALU instructions a tile of 16
+// keys at D = 128 went from 228 to MEASURED.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+// Two fp32 operations in one instruction, each rounded as the single one.
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // One row's 8 channels of this thread (packed): the group's statistics over
 // its 8 lanes, the codes and the (s, m) word.
 //
@@ -138,39 +158,50 @@ __device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta
   }
   const float range = __fsub_rn(hi, lo);
   constexpr float kFifteenth = 1.f / 15.f;
-  float q0 = __fmul_rn(range, kFifteenth);
+  const float q0 = __fmul_rn(range, kFifteenth);
   uint32_t sm = pack_bf16x2(__fmaf_rn(__fmaf_rn(-q0, 15.f, range), kFifteenth, q0), lo);
   float s = bf16_lo(sm);
   const float m = bf16_hi(sm);
-  float x[8];
+  uint64_t x[4];  // x - m
+  const uint64_t minus_m = pack_f32x2(-m, -m);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = unpack_16x2<kType>((&raw.x)[e]);
-    x[2 * e] = __fsub_rn(f.x, m);
-    x[2 * e + 1] = __fsub_rn(f.y, m);
+    x[e] = add_f32x2(pack_f32x2(f.x, f.y), minus_m);
   }
   uint32_t w = 0u;
   if (s >= 0x1p-100f && s <= 0x1p100f) {
-    const float y = __frcp_rn(s);
+    const float y1 = __frcp_rn(s);
+    const uint64_t y = pack_f32x2(y1, y1), minus_s = pack_f32x2(-s, -s), magic = pack_f32x2(12582912.f, 12582912.f);
     // Rounding half to even by adding 1.5 * 2^23 leaves the code in the low bits
     // of a constant, which comes off the packed word once.
     // m is min x itself for bf16, so d / s lies within 0 .. 15.06; fp16's
     // minimum is rounded to bf16, so there it may fall outside.
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-      q0 = __fmul_rn(x[e], y);
-      float c = __fmaf_rn(__fmaf_rn(-q0, s, x[e]), y, q0);
-      if constexpr (kType == kFP16) c = fminf(fmaxf(c, 0.f), 15.f);
-      w = w * 16u + __float_as_uint(__fadd_rn(c, 12582912.f));
+    for (int e = 3; e >= 0; --e) {
+      const uint64_t q = mul_f32x2(x[e], y);
+      uint64_t c = fma_f32x2(fma_f32x2(q, minus_s, x[e]), y, q);
+      float c0, c1;
+      if constexpr (kType == kFP16) {
+        unpack_f32x2(c, c0, c1);
+        c = pack_f32x2(fminf(fmaxf(c0, 0.f), 15.f), fminf(fmaxf(c1, 0.f), 15.f));
+      }
+      unpack_f32x2(add_f32x2(c, magic), c0, c1);
+      w = (w * 16u + __float_as_uint(c1)) * 16u + __float_as_uint(c0);
     }
     w -= 0x4b400000u * 0x11111111u;
   } else {
     sm = pack_bf16x2(__fdiv_rn(range, 15.f), lo);
     s = bf16_lo(sm);
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-      const float c = s != 0.f ? rintf(fminf(fmaxf(__fdiv_rn(x[e], s), 0.f), 15.f)) : 0.f;
-      w = w * 16u + static_cast<uint32_t>(c);
+    for (int e = 3; e >= 0; --e) {
+      float d[2];
+      unpack_f32x2(x[e], d[0], d[1]);
+#pragma unroll
+      for (int i = 1; i >= 0; --i) {
+        const float c = s != 0.f ? rintf(fminf(fmaxf(__fdiv_rn(d[i], s), 0.f), 15.f)) : 0.f;
+        w = w * 16u + static_cast<uint32_t>(c);
+      }
     }
   }
   *meta = sm;
@@ -287,11 +318,16 @@ __global__ void __launch_bounds__(kC4RowsThreads)
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t w = kv ? wv : wk, sm = kv ? mv : mk, half[2] = {w, w >> 16};
         const float s = bf16_lo(sm), m = bf16_hi(sm);
-        const float scale[4] = {s, s * 0x1p-4f, s * 0x1p-8f, s * 0x1p-12f};
+        const uint64_t scale[2] = {pack_f32x2(s, s * 0x1p-4f), pack_f32x2(s * 0x1p-8f, s * 0x1p-12f)};
+        const uint64_t minus = pack_f32x2(-8388608.f, -8388608.f), m2 = pack_f32x2(m, m);
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[e] = fmaf(__uint_as_float((half[e >> 2] & (15u << (4 * (e & 3)))) | 0x4b000000u) - 8388608.f, scale[e & 3], m);
+        for (int e = 0; e < 8; e += 2) {
+          const uint32_t c0 = and_or(half[e >> 2], 15u << (4 * (e & 3)), 0x4b000000u);
+          const uint32_t c1 = and_or(half[e >> 2], 15u << (4 * (e & 3) + 4), 0x4b000000u);
+          unpack_f32x2(fma_f32x2(add_f32x2(pack_f32x2(__uint_as_float(c0), __uint_as_float(c1)), minus), scale[(e >> 1) & 1], m2),
+                       x[e], x[e + 1]);
+        }
         if (s < 0x1p-100f) {  // the scaled s may be subnormal
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = fmaf(static_cast<float>((w >> (4 * e)) & 15u), s, m);
@@ -500,14 +536,6 @@ __device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// (w & mask) | magic in one instruction.  Left to the compiler it became two,
-// and these are the kernel's most frequent ones: ALU instructions a tile of 16
-// keys at D = 128 went from 228 to MEASURED.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
-  return r;
-}
 // c - 8 of the low nibbles of both 16-bit halves' low bytes, and of the high
 // nibbles: exact.
 __device__ __forceinline__ uint32_t c4_low(uint32_t w) {
