@@ -32,22 +32,6 @@ __device__ __forceinline__ int c4_len(const int32_t* __restrict__ len, int b, in
   return min(max(__ldg(len + b), 0), most);
 }
 
-// The sequence that packed row `row` belongs to: the last b with start[b] <=
-// row (sequences of no rows are stepped over), or n when row lies behind them
-// all or before the first.
-__device__ __forceinline__ int seq_of_row(const int32_t* __restrict__ start, int n, int row) {
-  if (row < __ldg(start) || row >= __ldg(start + n)) return n;
-  int lo = 0, hi = n;  // start[lo] <= row < start[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(start + mid) <= row)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-
 struct Cache4Rows {
   const int32_t* seq_start;  // [B + 1], or null: row b belongs to sequence b
   const int32_t* slot0;      // [B] first slot of each sequence's rows, or null: 0
@@ -55,6 +39,32 @@ struct Cache4Rows {
   int64_t rows;
   int64_t k_stride, v_stride;  // elements from one packed row to the next
 };
+
+// Start of sequence b among the rows there are: what seq_start says outside of
+// them counts for nothing.
+__device__ __forceinline__ int c4_start(const Cache4Rows& g, int b) {
+  return static_cast<int>(min(max(static_cast<int64_t>(__ldg(g.seq_start + b)), static_cast<int64_t>(0)), g.rows));
+}
+// Rows of sequence b.
+__device__ __forceinline__ int c4_rows_of(const Cache4Rows& g, int b) {
+  return g.seq_start != nullptr ? max(0, c4_start(g, b + 1) - c4_start(g, b)) : 1;
+}
+
+// The sequence that packed row `row` belongs to: the last b with start[b] <=
+// row (sequences of no rows are stepped over), or B when row lies behind them
+// all or before the first.
+__device__ __forceinline__ int c4_sequence(const Cache4Rows& g, int row) {
+  if (row < c4_start(g, 0) || row >= c4_start(g, g.B)) return g.B;
+  int lo = 0, hi = g.B;  // start[lo] <= row < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c4_start(g, mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
 
 // Blocks of kC4RowsThreads threads; 8 channels (one 4-byte word of codes) a
 // thread.  A block takes 16 (D = 128) or 32 (D = 64) packed rows and walks a run
@@ -67,27 +77,28 @@ template <int D>
 constexpr int kC4BlockRows = kC4RowsThreads / kC4RowLanes<D>;
 
 // This thread's row: where it goes in the first key head's entries (b*H*cap +
-// slot, -1 for nothing to do), sequence and slot.
+// slot, -1 for nothing to do), sequence, and number among the sequence's rows.
 struct C4Row {
   int64_t at;
-  int b, slot;
+  int b, i;
   bool dropped;  // a row of a sequence, but of no slot there is
 };
+// kAppend: slot0 is the cache's length, which counts as 0 where it is negative.
+template <bool kAppend>
 __device__ __forceinline__ C4Row c4_row(const Cache4Rows& g, const Cache4& c, int64_t row) {
   C4Row r{-1, 0, 0, false};
   if (row >= g.rows) return r;
-  int i = 0;
   r.b = static_cast<int>(row);
   if (g.seq_start != nullptr) {
-    r.b = seq_of_row(g.seq_start, g.B, static_cast<int>(row));
+    r.b = c4_sequence(g, static_cast<int>(row));
     if (r.b >= g.B) return r;
-    i = static_cast<int>(row) - __ldg(g.seq_start + r.b);
+    r.i = static_cast<int>(row) - c4_start(g, r.b);
   }
-  const int64_t slot = static_cast<int64_t>(i) + (g.slot0 != nullptr ? __ldg(g.slot0 + r.b) : 0);
+  int slot0 = g.slot0 != nullptr ? __ldg(g.slot0 + r.b) : 0;
+  if (kAppend) slot0 = max(slot0, 0);
+  const int64_t slot = static_cast<int64_t>(slot0) + r.i;
   r.dropped = slot < 0 || slot >= c.cap;
-  if (r.dropped) return r;
-  r.slot = static_cast<int>(slot);
-  r.at = static_cast<int64_t>(r.b) * c.H * c.cap + slot;
+  if (!r.dropped) r.at = static_cast<int64_t>(r.b) * c.H * c.cap + slot;
   return r;
 }
 
@@ -224,9 +235,9 @@ __global__ void __launch_bounds__(kC4RowsThreads)
   for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kC4BlockRows<D>; row0 < g.rows;
        row0 += static_cast<int64_t>(gridDim.y) * kC4BlockRows<D>) {
     const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
-    const C4Row r = c4_row(g, c, row);
+    const C4Row r = c4_row<true>(g, c, row);
     if (r.dropped && lane == 0 && h0 == 0) atomicOr(&g_attn_status, kC4Overflow);
-    const int my_pos = r.at < 0 ? 0 : first_pos != nullptr ? __ldg(first_pos + r.b) + (r.slot - __ldg(g.slot0 + r.b)) : r.slot;
+    const int my_pos = r.at < 0 ? 0 : (first_pos != nullptr ? __ldg(first_pos + r.b) : max(__ldg(g.slot0 + r.b), 0)) + r.i;
     const int64_t from = r.at < 0 ? 0 : row;  // the others go through the motions: the statistics are whole warps'
     const uint16_t* kp = k + from * g.k_stride + h0 * D + lane * 8;
     const uint16_t* vp = v + from * g.v_stride + h0 * D + lane * 8;
@@ -260,8 +271,7 @@ __global__ void __launch_bounds__(kC4RowsThreads)
   if (len_out != nullptr && h0 == 0) {
     for (int64_t b = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
          b += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-      const int64_t n = g.seq_start != nullptr ? max(0, __ldg(g.seq_start + b + 1) - __ldg(g.seq_start + b)) : 1;
-      const int64_t l = max(0, __ldg(g.slot0 + b)) + n;
+      const int64_t l = static_cast<int64_t>(max(0, __ldg(g.slot0 + b))) + c4_rows_of(g, static_cast<int>(b));
       len_out[b] = static_cast<int32_t>(l < c.cap ? l : c.cap);
     }
   }
@@ -269,13 +279,12 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 
 // The same update where len_out is the cache's own length: a launch behind
 // the one whose blocks all read it.
-__global__ void attn_cache4_grow_kernel(const int32_t* __restrict__ seq_start, int32_t* len, int B, int cap) {
+__global__ void attn_cache4_grow_kernel(Cache4Rows g, int32_t* len, int cap) {
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < B;
+  for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t n = seq_start != nullptr ? max(0, __ldg(seq_start + b + 1) - __ldg(seq_start + b)) : 1;
-    const int64_t l = max(0, len[b]) + n;
+    const int64_t l = static_cast<int64_t>(max(0, len[b])) + c4_rows_of(g, static_cast<int>(b));
     len[b] = static_cast<int32_t>(l < cap ? l : cap);
   }
 }
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(kC4RowsThreads)
   for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kC4BlockRows<D>; row0 < g.rows;
        row0 += static_cast<int64_t>(gridDim.y) * kC4BlockRows<D>) {
     const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
-    const C4Row r = c4_row(g, c, row);
+    const C4Row r = c4_row<false>(g, c, row);
     if (r.at < 0) continue;
     int64_t at = r.at + static_cast<int64_t>(h0) * c.cap;
     // the next head's codes travel while this one's are turned into values
@@ -1881,8 +1890,8 @@ attn_status_t attn_cache4_append(const attn_cache4_t* cache, const void* k, cons
   else
     e = dtype == ATTN_BF16 ? run(attn_cache4_append_kernel<128, kBF16>) : run(attn_cache4_append_kernel<128, kFP16>);
   if (e == cudaSuccess && in_place)
-    e = launch_pdl(attn_cache4_grow_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
-                   seq_start, length_out, cache->B, cache->capacity);
+    e = launch_pdl(attn_cache4_grow_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s, g,
+                   length_out, cache->capacity);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       for (int i0 = lane * unit_tok; i0 < len; i0 += 32 * unit_tok) {
         const int b = kPlanBuckets - 1 - min(varlen_tiles(i0, len, unit_tok, causal), kPlanBuckets - 1);
         const int at = atomicAdd(&cnt[b], 1);
-        if (pass == 1 && at < cap) units[at] = VarlenUnit{row0, len, i0};
+        if (pass == 1 && static_cast<unsigned>(at) < static_cast<unsigned>(cap)) units[at] = VarlenUnit{row0, len, i0};
         if (len - i0 <= 32 * unit_tok) break;  // i0 + 32 * unit_tok may not fit an int
       }
     }
@@ -117,9 +117,11 @@ __device__ __forceinline__ VUnit varlen_unit(const VarlenParams& p, const volati
   const bool listed = p.units != nullptr;
   VUnit w;
   w.h = u % p.H_kv;
-  w.row0 = listed ? __ldg(&e->row0) : own[1];
-  w.len = listed ? __ldg(&e->len) : own[2];
-  const int i0 = listed ? __ldg(&e->i0) : own[3];
+  // (clamped once more: whatever seq_start holds, no row outside the buffers)
+  const int most = static_cast<int>(p.total);
+  w.row0 = min(max(listed ? __ldg(&e->row0) : own[1], 0), most);
+  w.len = min(max(listed ? __ldg(&e->len) : own[2], 0), most - w.row0);
+  const int i0 = max(listed ? __ldg(&e->i0) : own[3], 0);
   w.n = 1;
 #pragma unroll
   for (int t = 0; t < kQTiles; ++t) {

@@ -124,6 +124,23 @@ def test_append_single_tokens_in_place_and_beyond_the_capacity():
     assert torch.equal(back[:2].double(), ref.values(ref.pack(code), torch.stack([s, m], -1)))
 
 
+def test_append_counts_only_rows_there_are():
+    """Starts before the first row and behind the last, and a negative length: entries are as many as rows."""
+    k = torch.randn((10, 2, 64), generator=gen(1), device="cuda").bfloat16()
+    for in_place in (False, True):
+        c = filled(3, 2, 50, 64, [4, 7, 0])
+        c.length[2] = -3
+        start = torch.tensor([-5, 3, 8, 400], dtype=torch.int32, device="cuda")
+        out = c.length if in_place else torch.empty_like(c.length)
+        c.append(k, k, seq_start=start, length_out=out)
+        ok()
+        assert out.tolist() == [7, 12, 2]
+        code, s, m = ref.quantise(k)
+        for b, (row, n, slot) in enumerate(((0, 3, 4), (3, 5, 7), (8, 2, 0))):
+            assert torch.equal(c.k_codes[b, :, slot:slot + n], ref.pack(code[row:row + n]).transpose(0, 1))
+            assert c.pos[b, 0, slot:slot + n].tolist() == list(range(slot, slot + n))
+
+
 def test_not_finite_groups_stand_for_nan_alone():
     x = torch.randn((3, 1, 128), generator=gen(1), device="cuda").bfloat16()
     x[0, 0, 5], x[1, 0, 70], x[2, 0, 127] = math.nan, math.inf, -math.inf
