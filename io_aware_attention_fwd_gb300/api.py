@@ -79,26 +79,32 @@ def attention_backward(q, k, v, o, lse, d_o, scale: float | None = None, causal:
     return dq, dk, dv
 
 
-# The calls below are made once a layer and token, so their checks are kept
-# cheap: attributes are read once, and the stream is taken as the handle that
-# torch keeps (a Stream object costs 3 us to make, a whole call's launch 3 to 7).
+# The serving calls are made once a layer and token, and for few tokens their
+# time on the host is what counts (the GPU's is 3 to 8 us): attributes are read
+# once, addresses are passed as numbers, and the stream is taken as the handle
+# that torch keeps (a Stream object costs 3 us to make).
 
-def on_stream(device, stream, call):
-    """call(handle) with `device` current and, where a stream is given, that
-    stream too, so that what the call allocates belongs to it."""
+def current_handle(device):
+    """The current stream's handle where `device` is the current one, else None."""
     import torch
 
-    if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
-        with torch.cuda.device(device):
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(index) if torch._C._cuda_getDevice() == index else None
+
+
+def on_stream(device, stream, call):
+    """call() with `device` current and, where a stream is given, that stream
+    too, so that what the call allocates belongs to it."""
+    import torch
+
     with torch.cuda.device(device):
+        if stream is None:
+            return call()
         if not isinstance(stream, torch.cuda.Stream):
             handle = _lib._stream(stream)
             stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call()
 
 
 _TYPES = {}  # torch dtype -> attn_dtype_t
@@ -133,7 +139,8 @@ def check_out(t, shape, dtype, device, name: str) -> None:
 def check_int32(t, n: int, device, name: str) -> None:
     import torch
 
-    check_out(t, (n,), torch.int32, device, name)
+    if t.shape != (n,) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
 
 
 def attention_varlen(q, k, v, seq_start, scale: float | None = None, causal: bool = True, out=None, lse=None,
@@ -175,14 +182,16 @@ def attention_varlen(q, k, v, seq_start, scale: float | None = None, causal: boo
         check_out(lse, (H_q, total), torch.float32, device, "lse")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    handle = current_handle(device) if stream is None else None
+    if handle is None:
+        return on_stream(device, stream, lambda: attention_varlen(q, k, v, seq_start, scale, causal, out, lse))
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    if lse is None:
+        lse = torch.empty((H_q, total), dtype=torch.float32, device=device)
     nbytes = _lib.attn_fwd_varlen_workspace_bytes(total, n, H_q, H_kv, D)
-
-    def call(handle):
-        o = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
-        z = lse if lse is not None else torch.empty((H_q, total), dtype=torch.float32, device=device)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
-        _lib.attn_fwd_varlen(q, k, v, o, z, total, seq_start, n, H_q, H_kv, D, code, q_stride, k_stride, v_stride,
-                             scale, causal, ws, nbytes, handle)
-        return o, z
-
-    return on_stream(device, stream, call)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
+    _lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), total,
+                         seq_start.data_ptr(), n, H_q, H_kv, D, code, q_stride, k_stride, v_stride, scale, causal, ws,
+                         nbytes, handle)
+    return out, lse

@@ -8,7 +8,7 @@ from __future__ import annotations
 import math
 
 from . import _lib
-from .api import check_int32, check_out, element_type, on_stream, row_stride
+from .api import check_int32, check_out, current_handle, element_type, on_stream, row_stride
 
 GROUP = 64  # channels that share a scale and a minimum
 
@@ -97,14 +97,18 @@ class KVCache4:
         attn_fwd_debug_status then reports ATTN_ERR_CAPACITY.
         """
         rows, ks, vs, code = self._rows(k, v, seq_start)
+        device = self.device
         if first_pos is not None:
-            check_int32(first_pos, self.B, self.device, "first_pos")
+            check_int32(first_pos, self.B, device, "first_pos")
         if length_out is None:
             length_out = self.length
         else:
-            check_int32(length_out, self.B, self.device, "length_out")
-        on_stream(self.device, stream, lambda handle: _lib.attn_cache4_append(
-            self._c, k, v, rows, ks, vs, code, seq_start, first_pos, length_out, handle))
+            check_int32(length_out, self.B, device, "length_out")
+        handle = current_handle(device) if stream is None else None
+        if handle is None:
+            return on_stream(device, stream, lambda: self.append(k, v, seq_start, first_pos, length_out))
+        _lib.attn_cache4_append(self._c, k.data_ptr(), v.data_ptr(), rows, ks, vs, code, seq_start, first_pos,
+                                length_out.data_ptr(), handle)
 
     def read(self, seq_start=None, rows: int | None = None, first_slot=None, dtype=None, k_out=None, v_out=None,
              stream=None):
@@ -116,26 +120,25 @@ class KVCache4:
         capacity and rows of no sequence are left as they were (zero in new
         tensors).
         """
-        import torch
-
         if (k_out is None) != (v_out is None):
             raise ValueError("k_out and v_out go together")
         if k_out is None and rows is None:
             if seq_start is not None:
                 raise ValueError("rows is needed with seq_start where k_out and v_out are not given")
             rows = self.B
+        device = self.device
         if first_slot is not None:
-            check_int32(first_slot, self.B, self.device, "first_slot")
+            check_int32(first_slot, self.B, device, "first_slot")
+        handle = current_handle(device) if stream is None else None
+        if handle is None:
+            return on_stream(device, stream, lambda: self.read(seq_start, rows, first_slot, dtype, k_out, v_out))
+        if k_out is None:
+            import torch
 
-        def call(handle):
-            k, v = k_out, v_out
-            if k is None:
-                k, v = torch.zeros((2, rows, self.H_kv, self.D), dtype=dtype or torch.bfloat16, device=self.device)
-            n, ks, vs, code = self._rows(k, v, seq_start, True)
-            _lib.attn_cache4_read(self._c, k, v, n, ks, vs, code, seq_start, first_slot, handle)
-            return k, v
-
-        return on_stream(self.device, stream, call)
+            k_out, v_out = torch.zeros((2, rows, self.H_kv, self.D), dtype=dtype or torch.bfloat16, device=device)
+        n, ks, vs, code = self._rows(k_out, v_out, seq_start, True)
+        _lib.attn_cache4_read(self._c, k_out.data_ptr(), v_out.data_ptr(), n, ks, vs, code, seq_start, first_slot, handle)
+        return k_out, v_out
 
     def attend(self, q, scale: float | None = None, weight_out=None, max_len: int | None = None, out=None, lse=None,
                stream=None):
@@ -166,17 +169,18 @@ class KVCache4:
             max_len = self.capacity
         if scale is None:
             scale = 1.0 / math.sqrt(D)
+        handle = current_handle(device) if stream is None else None
+        if handle is None:
+            return on_stream(device, stream, lambda: self.attend(q, scale, weight_out, max_len, out, lse))
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        if lse is None:
+            lse = torch.empty((B, H_q), dtype=torch.float32, device=device)
         nbytes = _lib.attn_cache4_decode_workspace_bytes(B, H_q, self.H_kv, D, max_len, weight_out is not None)
-
-        def call(handle):
-            o = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
-            z = lse if lse is not None else torch.empty((B, H_q), dtype=torch.float32, device=device)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
-            _lib.attn_cache4_decode(self._c, q, stride, o, z, H_q, code, scale, max_len,
-                                    None if weight_out is None else self.weight, weight_out, ws, nbytes, handle)
-            return o, z
-
-        return on_stream(device, stream, call)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
+        _lib.attn_cache4_decode(self._c, q.data_ptr(), stride, out.data_ptr(), lse.data_ptr(), H_q, code, scale, max_len,
+                                None if weight_out is None else self.weight, weight_out, ws, nbytes, handle)
+        return out, lse
 
     def evict(self, budget: int, recent: int = 0, weight_out=None, pos_out=None, length_out=None,
               max_len: int | None = None, stream=None) -> None:
@@ -205,10 +209,10 @@ class KVCache4:
             check_int32(length_out, B, device, "length_out")
         if max_len is None:
             max_len = self.capacity
+        handle = current_handle(device) if stream is None else None
+        if handle is None:
+            return on_stream(device, stream, lambda: self.evict(budget, recent, weight_out, pos_out, length_out, max_len))
         nbytes = _lib.attn_cache4_evict_workspace_bytes(B, self.H_kv, max_len, budget)
-
-        def call(handle):
-            ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-            _lib.attn_cache4_evict(self._c, budget, recent, max_len, weight_out, pos_out, length_out, ws, nbytes, handle)
-
-        on_stream(device, stream, call)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        _lib.attn_cache4_evict(self._c, budget, recent, max_len, weight_out.data_ptr(), pos_out.data_ptr(),
+                               length_out.data_ptr(), ws.data_ptr(), nbytes, handle)
