@@ -2048,6 +2048,6 @@ attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
 
 // Serving: packed prompts with grouped heads, and the 4-bit K/V cache (device
 // code, host code and entry points of each in one file).
-#include "attn_types.cuh"
-#include "attn_varlen.cuh"
-#include "attn_cache4.cuh"
+#include "serving/attn_types.cuh"
+#include "serving/attn_varlen.cuh"
+#include "serving/attn_cache4.cuh"
