@@ -272,8 +272,9 @@ typedef enum { ATTN_BF16 = 0, ATTN_FP16 = 1, ATTN_FP32 = 2 } attn_dtype_t;
  *               calls need none: the size is then 16, and NULL will do.
  * Values within a sequence are finite (a NaN or infinity in V reaches, as a
  * product with zero, rows of its own sequence that do not see it).
- * Asynchronous (one or two kernel launches); argument errors are reported before
- * anything is launched.  Calls that share a workspace must be ordered.
+ * Inputs and outputs must not overlap.  Asynchronous (one or two kernel launches);
+ * argument errors are reported before anything is launched.  Calls that share a
+ * workspace must be ordered.
  */
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
                               int64_t total, const int32_t* seq_start, int n_seqs, int H_q, int H_kv,
@@ -304,7 +305,9 @@ uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int
  *   pos               int32 [B][H_kv][capacity]: position of each entry's token
  *                     in its sequence, or NULL where the call does not use it
  *   length            int32 [B]; calls clamp it to 0 .. capacity (or max_len)
- * D is 64 or 128.  Entries behind length[b] are never read.
+ * D is 64 or 128.  Entries behind length[b] are never read.  The calls below check
+ * their arguments before anything is launched, allocate nothing, and are
+ * thread-safe; calls that write a cache must be ordered with those that use it.
  */
 typedef struct {
   void* k_codes;

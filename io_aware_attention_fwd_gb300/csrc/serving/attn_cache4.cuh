@@ -385,12 +385,12 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 //
 // mma.sync m16n8k16 serves here, with keys as the M rows of S^T = K Q^T, and
 // channels as the M rows of O^T = V^T P^T: the A operands are then the cache's
-// codes, dequantised in registers straight from global memory, and N = 8 is
-// one block of up to 8 query heads.  The pass is bound by HBM (4.5 bits a
-// value), so tcgen05, which wants its operands in shared memory, would only
-// add a round trip.  The order of the channels within an MMA is free as long
-// as both operands use the same one: slot (2i, 2i + 1) takes nibbles (e, e + 4)
-// of a word, which one mask extracts together.
+// codes, turned into numbers in registers, and N = 8 is one block of up to 8
+// query heads.  The pass is bound by HBM (4.5 bits a value) and by the
+// instructions that unpack the codes, not by the products; tcgen05 would have the
+// numbers written back to shared memory first.  The order of the channels within
+// an MMA is free as long as both operands use the same one: slot (2i, 2i + 1)
+// takes nibbles (e, e + 4) of a word, which one mask extracts together.
 //
 // Work split: the cache entries of all sequences and key heads, in tiles of 64
 // keys, form one list, cut into equal contiguous shares, one per CTA, whatever
@@ -965,7 +965,6 @@ __device__ __forceinline__ void c4_add_weights(const DecParams& p, int b, int h,
 template <int D, int kType, bool kWeight, bool kDirect>
 __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     attn_cache4_decode_kernel(const DecParams p) {
-
   constexpr int kG = D / kC4Group;
   constexpr int kWarps = kC4DecThreads / 32;
   using Ring = C4Ring<D>;
