@@ -572,16 +572,10 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
 // its own, filled by asynchronous copies: four stages, and 12 warps an SM, are up
 // to 110 KB in flight.  Loads into registers kept some 40 KB there and took 192 us
 // instead of 161 (64 sequences of up to 16000 entries, one tile a step).
-// A stage is K codes, V codes, K meta, V meta, row by row.
-//
-// MMA row i of the first 8 keys is key kappa(i) = 0, 6, 1, 7, 2, 4, 3, 5, and
-// the same + 8 for the others (any order will do as long as S's rows and P's
-// agree).  With D = 128 the two halves of every second pair of rows are also
-// swapped.  Then neither the reads of K (lane 4r + c: row kappa(r), 8 bytes at
-// 8c of a group) nor those of V (row kappa(2c) or kappa(2c + 1), word r of a
-// group) meet in a bank.
-__device__ __forceinline__ int c4_kappa(int i) { return (i & 1) ? 4 + (((i >> 1) + 2) & 3) : i >> 1; }
-
+// A stage is K codes, V codes, K meta, V meta, row by row.  The 16-byte pieces of
+// a row are swapped so that eight rows' pieces of one number, which ldmatrix reads
+// at once, lie in different banks: a row has 4 pieces (D = 128) or 2, and 8 fill
+// the 32 banks.
 template <int D>
 struct C4Ring {
   static constexpr int kStages = 4;
@@ -592,9 +586,9 @@ struct C4Ring {
   static constexpr int kVm = kKm + 16 * kMeta;
   static constexpr int kStage = kVm + 16 * kMeta;
   static constexpr int kWarp = kStages * kStage;
-  // byte of row `row`'s 32-byte group g
-  __device__ static uint32_t at(int row, int g) {
-    return static_cast<uint32_t>(row * kRow + (D == 128 ? (g ^ ((row >> 1) & 1)) * 32 : 0));
+  // byte of row `row`'s piece; 8 rows further its place is the same
+  __device__ static uint32_t at(int row, int piece) {
+    return static_cast<uint32_t>(row * kRow + (piece ^ (D == 128 ? (row >> 1) & 3 : (row >> 2) & 1)) * 16);
   }
 };
 
@@ -630,7 +624,7 @@ struct C4Copy {
     k = c.k + (key0 + row) * R::kRow + piece * 16;
     v = c.v + (key0 + row) * R::kRow + piece * 16;
     meta = reinterpret_cast<const uint8_t*>(lane < 16 ? c.km : c.vm) + (key0 + meta_row) * R::kMeta;
-    dst = ring + R::at(row, piece >> 1) + static_cast<uint32_t>(piece & 1) * 16;
+    dst = ring + R::at(row, piece);
     meta_dst = ring + R::kKm + static_cast<uint32_t>(lane) * R::kMeta;
   }
   __device__ void issue(uint32_t stage) {
@@ -657,21 +651,31 @@ struct C4Copy {
   }
 };
 
-// This lane's shared-memory addresses in stage 0.
+// This lane's shared-memory addresses in stage 0: the piece that it names to
+// ldmatrix (matrices 0 and 2: rows 0-7, 1 and 3: rows 8-15; 0 and 1: a group's
+// first 32 channels, 2 and 3: the others), and its (s, m).
 template <int D>
 struct C4Lane {
-  uint32_t k[D / kC4Group], v[2][D / kC4Group], meta;
-  __device__ void start(uint32_t ring, int r, int c) {
+  uint32_t codes[D / kC4Group], meta;
+  __device__ void start(uint32_t ring, int lane) {
     using R = C4Ring<D>;
 #pragma unroll
-    for (int g = 0; g < D / kC4Group; ++g) {
-      k[g] = ring + R::at(c4_kappa(r), g) + static_cast<uint32_t>(8 * c);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) v[i][g] = ring + R::kV + R::at(c4_kappa(2 * c + i), g) + static_cast<uint32_t>(4 * r);
-    }
-    meta = ring + R::kKm + static_cast<uint32_t>(c4_kappa(r) * R::kMeta);
+    for (int g = 0; g < D / kC4Group; ++g) codes[g] = ring + R::at(lane & 15, 2 * g + (lane >> 4));
+    meta = ring + R::kKm + static_cast<uint32_t>((lane >> 2) * R::kMeta);
   }
 };
+__device__ __forceinline__ void ldmatrix_x4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -682,7 +686,7 @@ __device__ __forceinline__ uint32_t ld_shared_b32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-// The (s, m) of keys kappa(r) and kappa(r) + 8, of K or (at kVm - kKm) of V.
+// The (s, m) of keys r and r + 8, of K or (at kVm - kKm) of V.
 template <int D>
 __device__ __forceinline__ void c4_load_meta(uint32_t (*sm)[D / kC4Group], uint32_t at) {
 #pragma unroll
@@ -715,7 +719,7 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (there) x = __ldg(reinterpret_cast<const uint4*>(qr + g * kC4Group + c * 16) + w);
+      if (there) x = __ldg(reinterpret_cast<const uint4*>(qr + g * kC4Group + w * 32 + c * 8));
       raw[g][4 * w] = x.x, raw[g][4 * w + 1] = x.y, raw[g][4 * w + 2] = x.z, raw[g][4 * w + 3] = x.w;
     }
   float back = 1.f;
@@ -776,11 +780,12 @@ struct C4State {
   float bias[kGroups][2];    // this lane's share of sum p (m + 8 s)
   float top_s[kGroups];      // power of two at or above every s so far (0 at first)
   float inv_s[kGroups];      // 2^7 / top_s
-  float o[kGroups][4][4];    // O^T in units of top_s / 2^7: channels 64g + 8r + t (+ 4), heads 2c, 2c + 1
+  float o[kGroups][4][4];    // O^T in units of top_s / 2^7: channels 64g + 4r + u (+ 32), heads 2c, 2c + 1
 };
 
-// Logits of a tile's 16 keys: keys kappa(r), kappa(r), kappa(r) + 8, kappa(r) + 8
-// and heads 2c, 2c + 1, 2c, 2c + 1.
+// Logits of a tile's 16 keys: keys r, r, r + 8, r + 8 and heads 2c, 2c + 1, 2c,
+// 2c + 1.  ldmatrix gives this lane word c (8 channels) of a piece of rows r and
+// r + 8.
 template <int D>
 __device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_t stage, const C4Query<D>& q) {
   using R = C4Ring<D>;
@@ -791,12 +796,13 @@ __device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_
   for (int e = 0; e < 4; ++e) xs[e] = 0.f;
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
-    const uint2 ka = ld_shared_v2(p.k[g] + stage), kb = ld_shared_v2(p.k[g] + stage + 8 * R::kRow);
+    uint32_t w[4];
+    ldmatrix_x4(w, p.codes[g] + stage);
     float d[4];
-    mma_16816_zero(d, c4_low(ka.x), c4_low(kb.x), c4_high(ka.x), c4_high(kb.x), q.q[g][0][0], q.q[g][0][1]);
-    mma_16816(d, c4_low(ka.x >> 8), c4_low(kb.x >> 8), c4_high(ka.x >> 8), c4_high(kb.x >> 8), q.q[g][1][0], q.q[g][1][1]);
-    mma_16816(d, c4_low(ka.y), c4_low(kb.y), c4_high(ka.y), c4_high(kb.y), q.q[g][2][0], q.q[g][2][1]);
-    mma_16816(d, c4_low(ka.y >> 8), c4_low(kb.y >> 8), c4_high(ka.y >> 8), c4_high(kb.y >> 8), q.q[g][3][0], q.q[g][3][1]);
+    mma_16816_zero(d, c4_low(w[0]), c4_low(w[1]), c4_high(w[0]), c4_high(w[1]), q.q[g][0][0], q.q[g][0][1]);
+    mma_16816(d, c4_low(w[0] >> 8), c4_low(w[1] >> 8), c4_high(w[0] >> 8), c4_high(w[1] >> 8), q.q[g][1][0], q.q[g][1][1]);
+    mma_16816(d, c4_low(w[2]), c4_low(w[3]), c4_high(w[2]), c4_high(w[3]), q.q[g][2][0], q.q[g][2][1]);
+    mma_16816(d, c4_low(w[2] >> 8), c4_low(w[3] >> 8), c4_high(w[2] >> 8), c4_high(w[3] >> 8), q.q[g][3][0], q.q[g][3][1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float s = bf16_lo(sm[i][g]), mm = fmaf(8.f, s, bf16_hi(sm[i][g]));
@@ -809,13 +815,14 @@ __device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_
 }
 
 // O^T += V^T P^T over a tile's 16 keys; pr as c4_scores lays out the logits.
+// ldmatrix transposes units of 16 bits, 4 channels: this lane gets unit r of a
+// piece from keys 2c and 2c + 1 side by side (and from 2c + 8, 2c + 9).
 template <int D>
 __device__ __forceinline__ void c4_values(C4State<D>& st, const float* pr, const uint32_t (*sm)[D / kC4Group],
                                           const C4Lane<D>& p, uint32_t stage) {
-  using R = C4Ring<D>;
 #pragma unroll
   for (int g = 0; g < D / kC4Group; ++g) {
-    uint32_t pb[2];  // P^T as the B operand: keys 0-7 and 8-15 of the MMA
+    uint32_t pb[2];  // P^T as the B operand: keys 0-7 and 8-15
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float s = bf16_lo(sm[i][g]), mm = fmaf(8.f, s, bf16_hi(sm[i][g])), sr = s * st.inv_s[g];
@@ -823,30 +830,23 @@ __device__ __forceinline__ void c4_values(C4State<D>& st, const float* pr, const
       st.bias[g][1] = fmaf(pr[2 * i + 1], mm, st.bias[g][1]);
       pb[i] = movmatrix_trans(pack_f16x2(pr[2 * i] * sr, pr[2 * i + 1] * sr));
     }
-    // bytes j of the words of two neighbouring MMA rows side by side: their low
-    // nibbles are channel 2j, the high ones 2j + 1
-    const uint32_t v0 = ld_shared_b32(p.v[0][g] + stage), v1 = ld_shared_b32(p.v[1][g] + stage);
-    const uint32_t v2 = ld_shared_b32(p.v[0][g] + stage + 8 * R::kRow), v3 = ld_shared_b32(p.v[1][g] + stage + 8 * R::kRow);
-    uint32_t wa[4], wb[4];
+    uint32_t w[4];
+    ldmatrix_x4_trans(w, p.codes[g] + stage + C4Ring<D>::kV);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      wa[j] = __byte_perm(v0, v1, 0x0400 + 0x1111 * j);
-      wb[j] = __byte_perm(v2, v3, 0x0400 + 0x1111 * j);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {  // rows r: channels 8r + 2j (+ 1); rows r + 8: channels 8r + 4 + 2j (+ 1)
-      mma_16816(st.o[g][2 * j], c4_low(wa[j]), c4_low(wa[j + 2]), c4_low(wb[j]), c4_low(wb[j + 2]), pb[0], pb[1]);
-      mma_16816(st.o[g][2 * j + 1], c4_high(wa[j]), c4_high(wa[j + 2]), c4_high(wb[j]), c4_high(wb[j + 2]), pb[0], pb[1]);
+    for (int j = 0; j < 2; ++j) {  // rows r: channels 4r + 2j (+ 1); rows r + 8: those + 32
+      const uint32_t a0 = w[0] >> (8 * j), a1 = w[2] >> (8 * j), a2 = w[1] >> (8 * j), a3 = w[3] >> (8 * j);
+      mma_16816(st.o[g][2 * j], c4_low(a0), c4_low(a1), c4_low(a2), c4_low(a3), pb[0], pb[1]);
+      mma_16816(st.o[g][2 * j + 1], c4_high(a0), c4_high(a1), c4_high(a2), c4_high(a3), pb[0], pb[1]);
     }
   }
 }
 
 // kN tiles' 16 keys each, in stages stage[0], ...; with kTail the first `left`
 // keys of the (one) tile exist.  `scores`: where head 2c's score of key
-// kappa(r) of the first tile goes, [tile][head][64 keys], tiles sc_step apart.
+// r of the first tile goes, [tile][head][64 keys], tiles sc_step apart.
 template <int D, bool kWeight, bool kTail, int kN>
 __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, const uint32_t* stage, const C4Query<D>& q,
-                                        int key, int left, float* scores, int64_t sc_step, bool head0, bool head1) {
+                                        int r, int left, float* scores, int64_t sc_step, bool head0, bool head1) {
   using R = C4Ring<D>;
   constexpr int kG = D / kC4Group;
   float xs[kN][4];
@@ -854,8 +854,8 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
   for (int n = 0; n < kN; ++n) {
     c4_scores<D>(xs[n], p, stage[n], q);
     if constexpr (kTail) {
-      if (key >= left) xs[n][0] = xs[n][1] = -INFINITY;
-      if (key + 8 >= left) xs[n][2] = xs[n][3] = -INFINITY;
+      if (r >= left) xs[n][0] = xs[n][1] = -INFINITY;
+      if (r + 8 >= left) xs[n][2] = xs[n][3] = -INFINITY;
     }
     if constexpr (kWeight) {
       float* dst = scores + n * sc_step;
@@ -978,7 +978,6 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
   __shared__ int64_t before_s;
   __shared__ int b_s;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  const int key = c4_kappa(r);
   grid_dependency_wait();
   grid_launch_dependents();  // the merge kernel's blocks come as this one's leave
   const int rows_per_b = p.c.H * p.HB;
@@ -1003,7 +1002,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
   }
   const uint32_t ring = smem_u32(ring_s) + static_cast<uint32_t>(warp * Ring::kWarp);
   C4Lane<D> at;
-  at.start(ring, r, c);
+  at.start(ring, lane);
   for (bool once = true; kDirect ? once : w.next(p, rows_per_b, kC4RowCost); once = false) {
     const int b = w.b, n = w.n, in_b = w.row, t0 = w.t0, t1 = w.t1;
     const int h = in_b / p.HB, hb = in_b % p.HB;
@@ -1042,7 +1041,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     // scores of (sequence, key head): its tiles in list order without the head blocks
     float* sc = kWeight ? p.scores + ((kDirect ? (static_cast<int64_t>(b) * p.c.H + h) * ((p.most + kC4TileKeys - 1) / kC4TileKeys)
                                            : (w.before & kC4Tiles) * p.c.H + static_cast<int64_t>(h) * w.nt + t0) * p.G + hb * kC4Heads + 2 * c) * kC4TileKeys +
-                              warp * 16 + key
+                              warp * 16 + r
                         : nullptr;
     const int64_t sc_step = static_cast<int64_t>(p.G) * kC4TileKeys;
     const bool head0 = 2 * c < heads, head1 = 2 * c + 1 < heads;
@@ -1055,7 +1054,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       __syncwarp();                        // ... and every lane's; the stage before is consumed
       const uint32_t stage[2] = {pair, pair + Ring::kStage};
       fetch(i + Ring::kStages - 1, (pair == 0u ? Ring::kStages * Ring::kStage : pair) - Ring::kStage);
-      c4_step<D, kWeight, false, 2>(st, at, stage, q, key, 16, sc, sc_step, head0, head1);
+      c4_step<D, kWeight, false, 2>(st, at, stage, q, r, 16, sc, sc_step, head0, head1);
       __syncwarp();
       fetch(i + Ring::kStages, pair);
       pair = pair == (Ring::kStages - 2) * Ring::kStage ? 0u : pair + 2 * Ring::kStage;
@@ -1065,7 +1064,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       cp_async_wait<Ring::kStages - 3>();
       __syncwarp();
       const uint32_t stage[1] = {pair};
-      c4_step<D, kWeight, false, 1>(st, at, stage, q, key, 16, sc, sc_step, head0, head1);
+      c4_step<D, kWeight, false, 1>(st, at, stage, q, r, 16, sc, sc_step, head0, head1);
       if (kWeight) sc += sc_step;
       pair += Ring::kStage;
       ++i;
@@ -1074,7 +1073,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       cp_async_wait<0>();
       __syncwarp();
       const uint32_t stage[1] = {pair};
-      c4_step<D, kWeight, true, 1>(st, at, stage, q, key, last, sc, sc_step, head0, head1);
+      c4_step<D, kWeight, true, 1>(st, at, stage, q, r, last, sc, sc_step, head0, head1);
     }
     __syncthreads();  // the ring is empty (the copies of every tile were waited for) and read
 
@@ -1095,7 +1094,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          o_s[warp][2 * c + (e & 1)][g * kC4Group + 8 * r + u + 4 * (e >> 1)] =
+          o_s[warp][2 * c + (e & 1)][g * kC4Group + 4 * r + u + 32 * (e >> 1)] =
               fmaf(st.o[g][u][e], st.top_s[g] * 0x1p-7f, st.bias[g][e & 1]);
     if (r == 0) {
       ml_s[warp][2 * c] = make_float2(st.ref[0], st.l[0]);
