@@ -365,19 +365,23 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 //
 // For a group of G query heads that share a key head,
 //     x_gj = scale * <q_g, k_j>,  O_g = sum_j softmax_j(x_g.) v_j.
-// With k_j = s*(c - 8) + (m + 8 s) in each group of 64 channels, the codes go
-// through the tensor core as they are and the scales are applied to sums:
-//     <q, k_j>  = sum over groups of  s * <q, c - 8> + (m + 8 s) * sum q
+// With k_j = s c + m in each group of 64 channels, the codes go through the
+// tensor core as they are and the scales are applied to sums:
+//     <q, k_j>  = sum over groups of  s * <q, c> + m * sum q
 //     sum_j p_j v_j = sum_j (p_j s) (c - 8) + sum_j p_j (m + 8 s).
 // The products run in fp16 with fp32 sums, whatever the type of q and o:
-//   * c - 8 is exact.  A code is ORed into the mantissa of 1024: a low nibble
-//     gives 1024 + c, from which 1032 is subtracted; a high one, left where it
-//     is, gives 1024 + 16 c, which one fused multiply-add turns into c - 8.
-//     So two nibbles of a 16-bit half need one mask and one operation each, and
-//     one shift serves four of the eight.
-//   * A bf16 q is scaled by a power of two that brings its head's largest
-//     channel to 1 .. 2, which fp16 holds exactly down to 2^-14 of it and to
-//     2^-25 of it absolutely; the scale goes back into the logits.
+//   * K's codes are masked out of a word and taken as they stand, as subnormals:
+//     c * 2^-24 and c * 2^-20, exact, one operation for two.  The products' unit
+//     goes into q and the logits.
+//   * V's are centred: its sums run over thousands of keys, and a mean code of
+//     7.5 would take bits from them.  A code is ORed into the mantissa of 1024: a
+//     low nibble gives 1024 + c, from which 1032 is subtracted; a high one, left
+//     where it is, gives 1024 + 16 c, which one fused multiply-add turns into
+//     c - 8.  So two nibbles of a 16-bit half need one mask and one operation
+//     each, and one shift serves four of the eight.
+//   * q is scaled by a power of two that brings its head's largest channel to
+//     2^10 .. 2^11, which fp16 holds exactly down to 2^-24 of it and to 2^-35 of
+//     it absolutely; the scale goes back into the logits.
 //   * p s is held relative to a power of two at or above every s the warp has
 //     met in that group of channels, times 2^7: at most 2^15, with 11 bits down
 //     to 2^-29 of the largest.  When a larger s comes, O is rescaled, as it is
@@ -433,7 +437,7 @@ struct DecParams {
   float scale_log2;
   float* o_part;    // [slots][8][D], unnormalised
   float2* ml_part;  // [slots][8]: (m in log2 units, l)
-  float* scores;    // [tile of a (sequence, key head)][G][64], log2 units, or null
+  float* scores;    // [tile of a (sequence, key head)][G][64], units of kC4LogitUnit, or null
   uint16_t* o;      // [B][H*G][D]
   float* lse;       // [B][H*G]
   const float* w_in;
@@ -548,7 +552,14 @@ __device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// c - 8 of the low nibbles of both 16-bit halves' low bytes, and of the high
+// Codes as fp16 numbers, for K: masked out of a word they are c * 2^-24 (low
+// nibbles of both 16-bit halves' low bytes) and c * 2^-20 (high nibbles), subnormal
+// and exact, with nothing to subtract or scale.
+__device__ __forceinline__ uint32_t c4_tiny_low(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t c4_tiny_high(uint32_t w) { return w & 0x00f000f0u; }
+
+// For V, whose sums run over many tiles and would lose what a mean code of 7.5 adds
+// to them: c - 8 of the low nibbles of both 16-bit halves' low bytes, and of the high
 // nibbles: exact.
 __device__ __forceinline__ uint32_t c4_low(uint32_t w) {
   uint32_t r;
@@ -700,13 +711,24 @@ __device__ __forceinline__ void c4_load_meta(uint32_t (*sm)[D / kC4Group], uint3
   }
 }
 
+__device__ __forceinline__ uint32_t times16_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x4c004c00u));
+  return r;
+}
+
+// A tile's logits, and what is compared with them, are log2 units over this: so
+// they come out of the MMAs, and the multiplication joins the subtraction in the
+// exponent.
+constexpr float kC4LogitUnit = 1024.f;
+
 // Q of a block of up to 8 heads as B operands, and what goes with it.
 template <int D>
 struct C4Query {
   static constexpr int kGroups = D / kC4Group;
-  uint32_t q[kGroups][4][2];  // head r, in the channel order of the K words
-  float sum[kGroups][2];      // of heads 2c, 2c + 1, over a group's channels
-  float scale[2];             // logits of heads 2c, 2c + 1, log2 units
+  uint32_t q[kGroups][4][2];  // head r, in the channel order of the K words; [0] times 16 (low nibbles)
+  float sum[kGroups][2];      // of heads 2c, 2c + 1, over a group's channels, in the units of the MMAs' sums
+  float scale[2];             // logits of heads 2c, 2c + 1, in units of kC4LogitUnit
 };
 template <int D, int kType>
 __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* rows, int heads, float scale_log2, int r, int c) {
@@ -722,26 +744,30 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
       if (there) x = __ldg(reinterpret_cast<const uint4*>(qr + g * kC4Group + w * 32 + c * 8));
       raw[g][4 * w] = x.x, raw[g][4 * w + 1] = x.y, raw[g][4 * w + 2] = x.z, raw[g][4 * w + 3] = x.w;
     }
-  float back = 1.f;
-  if constexpr (kType == kBF16) {
-    float top = 0.f;
+  // A head's q in fp16, times 2^10 / 2^E for its largest in [2^E, 2^(E+1)): 16 q
+  // is finite too.
+  float top = 0.f;
 #pragma unroll
-    for (int g = 0; g < kG; ++g)
+  for (int g = 0; g < kG; ++g)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[g][i])), fabsf(bf16_hi(raw[g][i]))));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^-E for top in [2^E, 2^(E+1)), within 2^-126 .. 2^100; 1 for 0, and for
-    // infinity, which stays one
-    const int e = static_cast<int>(__float_as_uint(top) >> 23);
-    const int f = top == 0.f || e == 255 ? 127 : min(max(254 - e, 1), 227);
-    const float fwd = __uint_as_float(static_cast<uint32_t>(f) << 23);
-    back = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = unpack_16x2<kType>(raw[g][i]);
+      top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // 2^-E within 2^-126 .. 2^100; 1 for 0, and for infinity, which stays one
+  const int e = static_cast<int>(__float_as_uint(top) >> 23);
+  const int f = top == 0.f || e == 255 ? 127 : min(max(254 - e, 1), 227);
+  const float fwd = __uint_as_float(static_cast<uint32_t>(f + 10) << 23);
+  const float back = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
 #pragma unroll
-    for (int g = 0; g < kG; ++g)
+  for (int g = 0; g < kG; ++g)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) raw[g][i] = pack_f16x2(bf16_lo(raw[g][i]) * fwd, bf16_hi(raw[g][i]) * fwd);
-  }
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = unpack_16x2<kType>(raw[g][i]);
+      raw[g][i] = pack_f16x2(x.x * fwd, x.y * fwd);
+    }
   t.scale[0] = scale_log2 * __shfl_sync(0xffffffffu, back, 8 * c);
   t.scale[1] = scale_log2 * __shfl_sync(0xffffffffu, back, 8 * c + 4);
 #pragma unroll
@@ -754,6 +780,7 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    sum *= 0x1p-20f;  // the MMAs' sums: 2^10 q times c * 2^-20, or 2^14 q times c * 2^-24
     t.sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
     t.sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
     // nibbles e and e + 4 of a word meet in one register: channels (0, 4),
@@ -761,9 +788,9 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const uint32_t* e = raw[g] + 4 * w;
-      t.q[g][2 * w][0] = __byte_perm(e[0], e[2], 0x5410);
+      t.q[g][2 * w][0] = times16_f16x2(__byte_perm(e[0], e[2], 0x5410));
       t.q[g][2 * w][1] = __byte_perm(e[0], e[2], 0x7632);
-      t.q[g][2 * w + 1][0] = __byte_perm(e[1], e[3], 0x5410);
+      t.q[g][2 * w + 1][0] = times16_f16x2(__byte_perm(e[1], e[3], 0x5410));
       t.q[g][2 * w + 1][1] = __byte_perm(e[1], e[3], 0x7632);
     }
   }
@@ -773,9 +800,9 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
 template <int D>
 struct C4State {
   static constexpr int kGroups = D / kC4Group;
-  float ref[2];              // what p is relative to, log2 units
-  float sub[2];              // the same, 0 instead of -inf
-  float most[2];             // ref + kRescaleLog2
+  float ref[2];              // what p is relative to, units of kC4LogitUnit
+  float sub[2];              // the same in log2 units, 0 instead of -inf
+  float most[2];             // 8 log2 units above ref
   float l[2];                // this lane's share of sum p
   float bias[kGroups][2];    // this lane's share of sum p (m + 8 s)
   float top_s[kGroups];      // power of two at or above every s so far (0 at first)
@@ -799,15 +826,17 @@ __device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_
     uint32_t w[4];
     ldmatrix_x4(w, p.codes[g] + stage);
     float d[4];
-    mma_16816_zero(d, c4_low(w[0]), c4_low(w[1]), c4_high(w[0]), c4_high(w[1]), q.q[g][0][0], q.q[g][0][1]);
-    mma_16816(d, c4_low(w[0] >> 8), c4_low(w[1] >> 8), c4_high(w[0] >> 8), c4_high(w[1] >> 8), q.q[g][1][0], q.q[g][1][1]);
-    mma_16816(d, c4_low(w[2]), c4_low(w[3]), c4_high(w[2]), c4_high(w[3]), q.q[g][2][0], q.q[g][2][1]);
-    mma_16816(d, c4_low(w[2] >> 8), c4_low(w[3] >> 8), c4_high(w[2] >> 8), c4_high(w[3] >> 8), q.q[g][3][0], q.q[g][3][1]);
+    mma_16816_zero(d, c4_tiny_low(w[0]), c4_tiny_low(w[1]), c4_tiny_high(w[0]), c4_tiny_high(w[1]), q.q[g][0][0], q.q[g][0][1]);
+    mma_16816(d, c4_tiny_low(w[0] >> 8), c4_tiny_low(w[1] >> 8), c4_tiny_high(w[0] >> 8), c4_tiny_high(w[1] >> 8), q.q[g][1][0],
+              q.q[g][1][1]);
+    mma_16816(d, c4_tiny_low(w[2]), c4_tiny_low(w[3]), c4_tiny_high(w[2]), c4_tiny_high(w[3]), q.q[g][2][0], q.q[g][2][1]);
+    mma_16816(d, c4_tiny_low(w[2] >> 8), c4_tiny_low(w[3] >> 8), c4_tiny_high(w[2] >> 8), c4_tiny_high(w[3] >> 8), q.q[g][3][0],
+              q.q[g][3][1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float s = bf16_lo(sm[i][g]), mm = fmaf(8.f, s, bf16_hi(sm[i][g]));
-      xs[2 * i] = fmaf(s, d[2 * i], fmaf(mm, q.sum[g][0], xs[2 * i]));
-      xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(mm, q.sum[g][1], xs[2 * i + 1]));
+      const float s = bf16_lo(sm[i][g]), m = bf16_hi(sm[i][g]);
+      xs[2 * i] = fmaf(s, d[2 * i], fmaf(m, q.sum[g][0], xs[2 * i]));
+      xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(m, q.sum[g][1], xs[2 * i + 1]));
     }
   }
 #pragma unroll
@@ -896,10 +925,10 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
       // a reference that has held moves only when it has to: p of the keys so
       // far keeps its bits
       const float to = top[e] > st.most[e] ? top[e] : st.ref[e];
-      a[e] = to == st.ref[e] ? 1.f : ex2_approx(st.ref[e] - to);
+      a[e] = to == st.ref[e] ? 1.f : ex2_approx((st.ref[e] - to) * kC4LogitUnit);
       st.ref[e] = to;
-      st.sub[e] = to == -INFINITY ? 0.f : to;
-      st.most[e] = to + kRescaleLog2;
+      st.sub[e] = to == -INFINITY ? 0.f : to * kC4LogitUnit;
+      st.most[e] = to + kRescaleLog2 / kC4LogitUnit;
       st.l[e] *= a[e];
     }
 #pragma unroll
@@ -923,7 +952,7 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
   for (int n = 0; n < kN; ++n) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      xs[n][e] = ex2_approx(xs[n][e] - st.sub[e & 1]);
+      xs[n][e] = ex2_approx(fmaf(xs[n][e], kC4LogitUnit, -st.sub[e & 1]));
       st.l[e & 1] += xs[n][e];
     }
     c4_values<D>(st, xs[n], sm[n], p, stage[n]);
@@ -931,7 +960,7 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
 }
 
 // Adds the weights of tiles t0 .. t1 - 1 of a (sequence, key head) with n
-// entries: exp2(score - lse) summed over the heads of its group.  16 threads a
+// entries: exp2(logit - lse) summed over the heads of its group.  16 threads a
 // tile, 4 keys each.  `scores`: of the row's tile 0, [tile][G][64]; kOwn: written
 // by this block before a barrier, else by an earlier kernel.
 template <bool kOwn>
@@ -949,10 +978,10 @@ __device__ __forceinline__ void c4_add_weights(const DecParams& p, int b, int h,
     for (int g = 0; g < p.G; ++g) {
       const float4 x = kOwn ? src[g * (kC4TileKeys / 4)] : __ldg(src + g * (kC4TileKeys / 4));
       const float z = lse_s[g];
-      sum[0] += ex2_approx(x.x - z);
-      sum[1] += ex2_approx(x.y - z);
-      sum[2] += ex2_approx(x.z - z);
-      sum[3] += ex2_approx(x.w - z);
+      sum[0] += ex2_approx(fmaf(x.x, kC4LogitUnit, -z));
+      sum[1] += ex2_approx(fmaf(x.y, kC4LogitUnit, -z));
+      sum[2] += ex2_approx(fmaf(x.z, kC4LogitUnit, -z));
+      sum[3] += ex2_approx(fmaf(x.w, kC4LogitUnit, -z));
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -1097,8 +1126,8 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
           o_s[warp][2 * c + (e & 1)][g * kC4Group + 4 * r + u + 32 * (e >> 1)] =
               fmaf(st.o[g][u][e], st.top_s[g] * 0x1p-7f, st.bias[g][e & 1]);
     if (r == 0) {
-      ml_s[warp][2 * c] = make_float2(st.ref[0], st.l[0]);
-      ml_s[warp][2 * c + 1] = make_float2(st.ref[1], st.l[1]);
+      ml_s[warp][2 * c] = make_float2(st.ref[0] * kC4LogitUnit, st.l[0]);
+      ml_s[warp][2 * c + 1] = make_float2(st.ref[1] * kC4LogitUnit, st.l[1]);
     }
     __syncthreads();
     if constexpr (kDirect) {

@@ -86,8 +86,8 @@ def decode(q, cache, lens, scale):
     H, cap = cache.H_kv, cache.capacity
     g = hq // H
     u = HALF_STEP[q.dtype]
-    # p * s enters P.V in bf16, or as two bf16 terms for fp16
-    up = 2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -16
+    # p * s enters P.V in fp16, whatever the type: half a step of 11 bits
+    up = 2.0 ** -11
     o = torch.zeros((B, hq, d), dtype=torch.float64, device=q.device)
     tol, lse = torch.zeros_like(o), torch.full((B, hq), -math.inf, dtype=torch.float64, device=q.device)
     lse_tol = torch.zeros_like(lse)
@@ -101,8 +101,8 @@ def decode(q, cache, lens, scale):
             sm = [cache.k_meta[b, h, :n].double().repeat_interleave(GROUP, -2), cache.v_meta[b, h, :n].double().repeat_interleave(GROUP, -2)]
             c = [unpack(cache.k_codes[b, h, :n]), unpack(cache.v_codes[b, h, :n])]
             k, v = (c[i] * sm[i][..., 0] + sm[i][..., 1] for i in (0, 1))
-            # the calls split a value into s (c - 8) and m + 8 s
-            k_abs, v_part, v_off = ((sm[0][..., 0] * (c[0] - 8)).abs() + (sm[0][..., 1] + 8 * sm[0][..., 0]).abs(),
+            # the calls split a key into s c and m, a value into s (c - 8) and m + 8 s
+            k_abs, v_part, v_off = (sm[0][..., 0] * c[0] + sm[0][..., 1].abs(),
                                     (sm[1][..., 0] * (c[1] - 8)).abs(), (sm[1][..., 1] + 8 * sm[1][..., 0]).abs())
             qq = q[b, h * g:(h + 1) * g].double()
             x = qq @ k.T * scale

@@ -475,3 +475,15 @@ def test_attend_both_sides_of_the_one_launch_rule(hq, max_len, weight):
     c = filled(5, 2, 2049, 128, lens, seed=hq)
     q = torch.randn((5, hq, 128), generator=gen(1), device="cuda").half()
     check_attend(c, q, lens, weight=weight, max_len=max_len)
+
+
+@pytest.mark.parametrize("dtype,top", [(torch.bfloat16, 1e-30), (torch.bfloat16, 1e30), (torch.float16, 2.0 ** -20), (torch.float16, 65504.0)])
+def test_attend_queries_of_any_size(dtype, top):
+    """The largest and smallest queries: the logits' range comes back through the softmax's scale."""
+    lens, D = [333, 1], 128
+    c = filled(2, 2, 340, D, lens, seed=9)
+    q = torch.randn((2, 8, D), generator=gen(3), device="cuda")
+    q = (q / q.abs().amax() * top).to(dtype)
+    check_attend(c, q, lens, scale=2.0 / top)
+    c.k_meta.zero_()
+    check_attend(c, q, lens, scale=1.0)
