@@ -1242,6 +1242,19 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
   int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
   const int64_t count = c4_total(p, sums_s, &mine_before, &mine);
+  // Weights: the tiles of every (sequence, key head) in equal contiguous
+  // shares, one for each block behind those of the rows, walked row by row.  The
+  // share's first row is found now, too (32 sequences of up to 4001: 31.5 -> 30.9 us).
+  C4Walk w;
+  w.x = w.end = 0;
+  if (kWeight && blockIdx.x >= m.row_blocks) {
+    const int64_t all = c4_units(count, kC4MergeRowCost) * p.c.H;
+    const int64_t blocks = gridDim.x - m.row_blocks;
+    const int64_t mine_w = (all + blocks - 1) / blocks;
+    w.x = (static_cast<int64_t>(blockIdx.x) - m.row_blocks) * mine_w;
+    w.end = w.x + mine_w < all ? w.x + mine_w : all;
+    if (w.x < w.end) c4_find(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
+  }
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t share = max(static_cast<int64_t>(1), (c4_units(count, kC4RowCost) * rows_per_b + m.dec_grid - 1) / m.dec_grid);
@@ -1316,16 +1329,7 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
   }
 
   if constexpr (kWeight) {
-    // Weights: the tiles of every (sequence, key head) in equal contiguous
-    // shares, one for each block behind those of the rows, walked row by row.
-    const int64_t all = c4_units(count, kC4MergeRowCost) * p.c.H;
-    const int64_t blocks = gridDim.x - m.row_blocks;
-    const int64_t mine_w = (all + blocks - 1) / blocks;
-    C4Walk w;
-    w.x = (static_cast<int64_t>(blockIdx.x) - m.row_blocks) * mine_w;
-    w.end = w.x + mine_w < all ? w.x + mine_w : all;
-    if (blockIdx.x >= m.row_blocks && w.x < w.end) {
-      c4_find(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
+    if (w.x < w.end) {
       __syncthreads();
       w.b = b_s;
       w.before = before_s;
