@@ -1694,12 +1694,16 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
   const int part = tid % kLanes, word = part % kWords;
   const bool is_v = part >= kWords;
   uint8_t* const codes = is_v ? p.c.v : p.c.k;
-  uint32_t* const meta = is_v ? p.c.vm : p.c.km;
+  using Meta = typename std::conditional<kMeta == 2, uint2, uint32_t>::type;  // a row's (s, m)
+  Meta* const meta = reinterpret_cast<Meta*>(is_v ? p.c.vm : p.c.km);
+  const uint32_t* const in = is_v ? reinterpret_cast<const uint32_t*>(p.p_in) : reinterpret_cast<const uint32_t*>(p.w_in);
+  uint32_t* const out = is_v ? reinterpret_cast<uint32_t*>(p.p_out) : reinterpret_cast<uint32_t*>(p.w_out);
   const uint32_t step = R * (kThreads / kLanes);
   for (uint32_t m = rank * (kThreads / kLanes) + tid / kLanes; m < n_moves; m += kU * step) {
     int64_t to[kU], from[kU];
     uint4 x[kU];
-    uint32_t sm[kU][kMeta], extra[kU];
+    Meta sm[kU];
+    uint32_t extra[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const uint32_t j = min(m + u * step, n_moves - 1);
@@ -1710,9 +1714,8 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
     for (int u = 0; u < kU; ++u) {
       x[u] = *(reinterpret_cast<const uint4*>(codes + from[u] * (D / 2)) + word);
       if (word == 0) {
-#pragma unroll
-        for (int g = 0; g < kMeta; ++g) sm[u][g] = meta[from[u] * kMeta + g];
-        extra[u] = is_v ? static_cast<uint32_t>(p.p_in[from[u]]) : __float_as_uint(p.w_in[from[u]]);
+        sm[u] = meta[from[u]];
+        extra[u] = in[from[u]];
       }
     }
 #pragma unroll
@@ -1720,12 +1723,8 @@ __global__ void __launch_bounds__(kThreads) attn_cache4_evict_kernel(const Evict
       if (m + u * step >= n_moves) break;
       *(reinterpret_cast<uint4*>(codes + to[u] * (D / 2)) + word) = x[u];
       if (word == 0) {
-#pragma unroll
-        for (int g = 0; g < kMeta; ++g) meta[to[u] * kMeta + g] = sm[u][g];
-        if (is_v)
-          p.p_out[to[u]] = static_cast<int32_t>(extra[u]);
-        else
-          p.w_out[to[u]] = __uint_as_float(extra[u]);
+        meta[to[u]] = sm[u];
+        out[to[u]] = extra[u];
       }
     }
   }
