@@ -1188,7 +1188,7 @@ struct DecMergeParams {
   DecParams d;
   int dec_grid;  // CTAs of the decode kernel: the shares
   int warps;     // of the merge kernel that share a row's partials
-  unsigned row_blocks;  // blocks that join rows; those behind them add weights
+  unsigned weight_blocks;  // blocks that add weights; those behind them join rows
 };
 
 constexpr int kC4MergeThreads = 256;
@@ -1248,15 +1248,14 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
   const int rows_per_b = p.c.H * p.HB;
   const int64_t count = c4_total(p, sums_s, &mine_before, &mine);
   // Weights: the tiles of every (sequence, key head) in equal contiguous
-  // shares, one for each block behind those of the rows, walked row by row.  The
-  // share's first row is found now, too (32 sequences of up to 4001: 31.5 -> 30.9 us).
+  // shares, one for each of the first blocks, walked row by row.  The share's
+  // first row is found now, too (32 sequences of up to 4001: 31.5 -> 30.9 us).
   C4Walk w;
   w.x = w.end = 0;
-  if (kWeight && blockIdx.x >= m.row_blocks) {
+  if (kWeight && blockIdx.x < m.weight_blocks) {
     const int64_t all = c4_units(count, kC4MergeRowCost) * p.c.H;
-    const int64_t blocks = gridDim.x - m.row_blocks;
-    const int64_t mine_w = (all + blocks - 1) / blocks;
-    w.x = (static_cast<int64_t>(blockIdx.x) - m.row_blocks) * mine_w;
+    const int64_t mine_w = (all + m.weight_blocks - 1) / m.weight_blocks;
+    w.x = blockIdx.x * mine_w;
     w.end = w.x + mine_w < all ? w.x + mine_w : all;
     if (w.x < w.end) c4_find(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
   }
@@ -1267,7 +1266,8 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
   // O and LSE: m.warps warps a row, the blocks' rows all of one sequence.
   const int hq = p.c.H * p.G, rows = kWarps / m.warps;
   const int per_b = (hq + rows - 1) / rows;
-  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * per_b && blockIdx.x < m.row_blocks; u += m.row_blocks) {
+  const int64_t first = kWeight ? static_cast<int64_t>(blockIdx.x) - m.weight_blocks : blockIdx.x;
+  for (int64_t u = first; u >= 0 && u < static_cast<int64_t>(p.B) * per_b; u += gridDim.x - m.weight_blocks) {
     const int b = static_cast<int>(u / per_b);
     const int head = static_cast<int>(u % per_b) * rows + warp / m.warps;
     const int stripe = (p.B + kC4MergeThreads - 1) / kC4MergeThreads;
@@ -1869,11 +1869,15 @@ attn_status_t launch_decode(DecMergeParams m, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return ATTN_ERR_LAUNCH;
   const int64_t rows = kC4MergeThreads / 32 / m.warps;
   const int64_t tiles = (static_cast<int64_t>(m.d.most) + kC4TileKeys - 1) / kC4TileKeys * m.d.B * m.d.c.H;
-  m.row_blocks = static_cast<unsigned>(std::min<int64_t>(m.d.B * ((static_cast<int64_t>(m.d.c.H) * m.d.G + rows - 1) / rows),
-                                                         static_cast<int64_t>(sms) * 4));
-  const int64_t weight_blocks =
-      weight ? std::min<int64_t>((tiles + kC4MergeTiles - 1) / kC4MergeTiles, static_cast<int64_t>(sms) * 8) : 0;
-  const dim3 mg(static_cast<unsigned>(m.row_blocks + weight_blocks));
+  // Three blocks an SM for the weights, of the four that fit: a block's set-up is
+  // some 700 instructions a warp, ten times a tile's.  (32 sequences of up to 4001
+  // 27.8 us, 64 of up to 16000 133.2; with four 28.2 and 133.7, with eight behind
+  // the rows' blocks 30.8 and 136.8.)
+  const int64_t row_blocks = std::min<int64_t>(m.d.B * ((static_cast<int64_t>(m.d.c.H) * m.d.G + rows - 1) / rows),
+                                               static_cast<int64_t>(sms) * 4);
+  m.weight_blocks =
+      weight ? static_cast<unsigned>(std::min<int64_t>((tiles + kC4MergeTiles - 1) / kC4MergeTiles, static_cast<int64_t>(sms) * 3)) : 0u;
+  const dim3 mg(static_cast<unsigned>(row_blocks) + m.weight_blocks);
   e = weight ? launch_pdl(attn_cache4_merge_kernel<D, kType, true>, mg, dim3(kC4MergeThreads), 0, stream, m)
              : launch_pdl(attn_cache4_merge_kernel<D, kType, false>, mg, dim3(kC4MergeThreads), 0, stream, m);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
