@@ -416,8 +416,9 @@ constexpr int kC4DecThreads = 128;  // 4 warps
 constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
 constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
 // Three CTAs an SM give a thread 168 registers, room for two tiles' chains of
-// instructions side by side; with four (128, spills) it took 153 us instead of
-// 140 at 64 sequences of up to 16000 entries with weights.
+// instructions side by side; with four (128, spills) it took 142 us instead of
+// 137 at 64 sequences of up to 16000 entries with weights, and 41.5 instead of
+// 37.6 at one of 131072.
 constexpr int kC4DecCtasPerSm = 3;
 // Longest caches for which a CTA takes a whole row.  GPU time per call, that way
 // against shares (us; without weights, 2048 entries): 1 sequence of 8 heads, D = 128
@@ -1228,9 +1229,12 @@ __device__ __forceinline__ float2 c4_join_stats(const float2* ml, int count, int
 // each entry's attention weight, summed over the heads of its group, where
 // the scores were kept.  `m.warps` (1, 2, 4, 8) warps share a row's partials,
 // four of them in flight each: with one warp, the 77 partials of a row of
-// 131072 keys took 33 us, most of it waiting for memory.
+// 131072 keys took 33 us, most of it waiting for memory.  The first four are
+// fetched while the statistics are joined (that call: 37.6 -> 36.4 us), and four
+// blocks an SM hold 64 registers a thread (64 sequences of up to 16000 with
+// weights: 132.8 us with 75, 130.4 with 64).
 template <int D, int kType, bool kWeight>
-__global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(const DecMergeParams m) {
+__global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(const DecMergeParams m) {
   constexpr int kWarps = kC4MergeThreads / 32;
   constexpr int kPer = D / 32;
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
@@ -1266,8 +1270,8 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
   // O and LSE: m.warps warps a row, the blocks' rows all of one sequence.
   const int hq = p.c.H * p.G, rows = kWarps / m.warps;
   const int per_b = (hq + rows - 1) / rows;
-  const int64_t first = kWeight ? static_cast<int64_t>(blockIdx.x) - m.weight_blocks : blockIdx.x;
-  for (int64_t u = first; u >= 0 && u < static_cast<int64_t>(p.B) * per_b; u += gridDim.x - m.weight_blocks) {
+  const unsigned row_block = blockIdx.x - (kWeight ? m.weight_blocks : 0u), row_blocks = gridDim.x - (kWeight ? m.weight_blocks : 0u);
+  for (int64_t u = row_block; u < static_cast<int64_t>(p.B) * per_b && (!kWeight || blockIdx.x >= m.weight_blocks); u += row_blocks) {
     const int b = static_cast<int>(u / per_b);
     const int head = static_cast<int>(u % per_b) * rows + warp / m.warps;
     const int stripe = (p.B + kC4MergeThreads - 1) / kC4MergeThreads;
@@ -1290,18 +1294,23 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
       const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
       const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
       const float* op = p.o_part + (slot0 * kC4Heads + g % kC4Heads) * D + lane * kPer;
-      const float2 tl = c4_join_stats(ml, cut.count, lane);
-      inv = cut.count == 0 ? 0.f : 1.f / tl.y;
       const int step = m.warps;
-      for (int i = warp % step; i < cut.count; i += 4 * step) {
-        Vec v[4];
-        float a[4];
+      // the first partials come while the statistics are joined
+      Vec v[4];
+      float a[4];
+      const auto load = [&](int i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int64_t at = min(i + j * step, cut.count - 1);
           v[j] = __ldg(reinterpret_cast<const Vec*>(op + at * kC4Heads * D));
           a[j] = __ldg(&ml[at * kC4Heads].x);
         }
+      };
+      int i = warp % step;
+      if (i < cut.count) load(i);
+      const float2 tl = c4_join_stats(ml, cut.count, lane);
+      inv = cut.count == 0 ? 0.f : 1.f / tl.y;
+      while (i < cut.count) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (i + j * step >= cut.count) break;
@@ -1310,6 +1319,8 @@ __global__ void __launch_bounds__(kC4MergeThreads) attn_cache4_merge_kernel(cons
 #pragma unroll
           for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, f[e], acc[e]);
         }
+        i += 4 * step;
+        if (i < cut.count) load(i);
       }
       if (lane == 0 && warp % step == 0) p.lse[row] = cut.count == 0 ? -INFINITY : (tl.x + log2f(tl.y)) * kLn2;
     }
