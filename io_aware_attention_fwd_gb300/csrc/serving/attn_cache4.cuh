@@ -421,10 +421,16 @@ constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
 // 37.6 at one of 131072.
 constexpr int kC4DecCtasPerSm = 3;
 // Longest caches for which a CTA takes a whole row.  GPU time per call, that way
-// against shares (us; without weights, 2048 entries): 1 sequence of 8 heads, D = 128
-// 9.1 / 9.7; 64 sequences 32.0 / 33.3; 16 of 16 heads, D = 64 10.9 / 17.5.  With 4096:
-// 14.7 / 11.2, 56.8 / 53.8, 18.6 / 23.7.  With weights, 2048 entries: 16.2 / 12.3,
-// 44.4 / 47.0, 13.3 / 18.9; 4096: 18.4 / 14.1, 94.1 / 70.9, 23.8 / 26.8.
+// against shares (us; lengths from half to all of the capacity; 1 sequence of 8 key
+// heads, D = 128 | 64 of them | 16 of 16, D = 64):
+//   1024           6.8 / 7.6   | 17.4 / 22.1 | 6.1 / 10.7
+//   2048           9.9 / 7.8   | 31.7 / 32.4 | 9.8 / 13.5
+//   4096          11.7 / 10.3  | 57.1 / 50.2 | 17.4 / 17.7
+//   1024, weights  9.4 / 8.4   | 21.9 / 25.5 | 7.3 / 13.3
+//   2048, weights 14.7 / 10.1  | 42.0 / 38.6 | 11.9 / 16.2
+//   4096, weights 24.7 / 11.4  | 81.3 / 62.6 | 21.3 / 22.1
+// Shares take the host 4 us longer (a second launch, a workspace), which a call
+// outside a graph waits for where the GPU needs less than 15: so 2048, not 1024.
 constexpr int kC4DirectLen = 2048;
 constexpr int kC4RowCost = 6;       // tiles' worth of time that a row costs a CTA
 // A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
