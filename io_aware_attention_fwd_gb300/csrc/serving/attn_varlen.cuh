@@ -283,6 +283,19 @@ __device__ void varlen_mma_role(const Smem<D, false>& sm, const volatile int* ow
   }
 }
 
+// What P is held in.  bf16 has fp32's range: p is relative to the row's reference,
+// which moves when the maximum exceeds it by 2^8, as in softmax_role.  fp16 ends at
+// 2^16, and its bits go below 2^-14: there P is held 2^11 times as large and the
+// reference moves at 2^4, so p stays at or below 2^15 and keeps its 11 bits down to
+// 2^-25 of the largest (as p itself it lost them from 2^-14 on and was 0 from 2^-25
+// on, while the row sum counted it: 4096 keys 18 nats below one of V = 0 gave an O
+// that was off by all of itself).  The row sum carries the same factor, which leaves
+// O with the division and the LSE in the epilogue.
+template <int kType>
+constexpr float kVarlenUp = kType == kFP16 ? 11.f : 0.f;
+template <int kType>
+constexpr float kVarlenRescale = kType == kFP16 ? 4.f : kRescaleLog2;
+
 // Softmax of query tile t, as softmax_role: row r is token r / G of the tile.
 template <int D, int kType>
 __device__ void varlen_softmax_role(const Smem<D, false>& sm, const volatile int* own, int t, uint32_t tmem, const VarlenParams& p,
@@ -346,10 +359,12 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, const volatile int
       const float new_mc = max3f(mx0, mx1, fmaxf(mx2, mx3)) * c;
       float alpha = 1.f;
       bool rescale_o = false;
-      if (new_mc > m_c + kRescaleLog2) {
-        alpha = ex2_approx(m_c - new_mc);
+      // (m_c lies kVarlenUp below the reference: what the exponents subtract)
+      if (new_mc > m_c + (kVarlenRescale<kType> + kVarlenUp<kType>)) {
+        const float to = kType == kFP16 ? new_mc - kVarlenUp<kType> : new_mc;
+        alpha = ex2_approx(m_c - to);
         rescale_o = j > 0;
-        m_c = new_mc;
+        m_c = to;
       }
       const float mc = (m_c == -INFINITY) ? 0.f : m_c;
 
@@ -377,8 +392,7 @@ __device__ void varlen_softmax_role(const Smem<D, false>& sm, const volatile int
         tmem_wait_st();
       };
 
-      // P in the inputs' 16-bit type, handed over in two halves of 64 keys; p
-      // is below 2^8, well inside fp16
+      // P in the inputs' 16-bit type, handed over in two halves of 64 keys
       uint32_t pk[C::kPCols];
       float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
@@ -503,8 +517,10 @@ __device__ void varlen_epilogue_role(const Smem<D, false>& sm, const volatile in
           st_global_v4(p.o + at * D + pn * 64 + ch * 8, x[0], x[1], x[2], x[3]);
         }
       }
-      if (rt < rows)
-        p.lse[static_cast<int64_t>(un.h * p.G + g) * p.total + tok0 + tok] = (ml.x + log2f(ml.y)) * kLn2;
+      if (rt < rows) {  // (the factor comes off the sum first: a sum near 1 has the more exact logarithm)
+        const float l2 = kType == kFP16 ? (ml.x + kVarlenUp<kType>) + log2f(ml.y * 0x1p-11f) : ml.x + log2f(ml.y);
+        p.lse[static_cast<int64_t>(un.h * p.G + g) * p.total + tok0 + tok] = l2 * kLn2;
+      }
     }
     ++k;
   }

@@ -1,0 +1,57 @@
+"""Inputs at the edges of what the serving calls take, each against its 64-bit
+definition."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import io_aware_attention_fwd_gb300 as attn
+from tests import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+
+
+def starts_of(lens):
+    s = [0]
+    for n in lens:
+        s.append(s[-1] + n)
+    return torch.tensor(s, dtype=torch.int32, device="cuda")
+
+
+# --- packed prompts --------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nats,at", [(6, 0), (12, 0), (16, 0), (18, 0), (18, 500), (20, 700)])
+def test_fp16_prompt_of_keys_far_below_the_maximum(nats, at, D, causal):
+    """One key takes nearly all the weight and has V = 0, so O is what thousands of keys e^-nats as heavy add up to.
+
+    The bound.  p is held as 2^11 p relative to the row's reference, whose own key has p = 1, so l >= 1; fp16 is exact
+    to 2^-25 where it is subnormal: an absolute 2^-36 a key and |v|, on top of the relative half step of ref.varlen.
+    """
+    n, scale = 4096, 0.125
+    q = torch.zeros((n, 2, D), device="cuda")
+    q[..., 0] = 8.0
+    k = torch.zeros((n, 1, D), device="cuda")
+    k[at, :, 0] = nats
+    v = 1000 * (1 + torch.rand((n, 1, D), generator=gen(1), device="cuda"))
+    v[at] = 0
+    q, k, v = q.half(), k.half(), v.half()
+    o, lse = attn.attention_varlen(q, k, v, starts_of([n]), scale=scale, causal=causal)
+    ok()
+    ro, rlse, tol, lse_tol = ref.varlen(q, k, v, [0, n], scale, causal)
+    size = v.double().abs().cumsum(0) if causal else v.double().abs().sum(0, keepdim=True)
+    assert ((lse.double() - rlse).abs() <= lse_tol).all()
+    bad = (o.double() - ro).abs() > tol + 2.0 ** -36 * size
+    assert not bad.any(), (int(bad.sum()), ((o.double() - ro).abs() / ro.abs().clamp(min=1e-30)).max())
