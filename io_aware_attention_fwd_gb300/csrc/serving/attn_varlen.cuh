@@ -494,7 +494,9 @@ __device__ void varlen_epilogue_role(const Smem<D, false>& sm, const volatile in
               float x0, x1;
               unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[8 * ch + 2 * i]), __uint_as_float(o[8 * ch + 2 * i + 1])), il2),
                            x0, x1);
-              pk[i] = pack_16x2<kType>(x0, x1);
+              // A mean of fp16 values is an fp16 value, but the sum of the rounded P
+              // may exceed the row's by half a step: at 65504 that is infinity.
+              pk[i] = kType == kFP16 ? pack_f16x2_sat(x0, x1) : pack_bf16x2(x0, x1);
             }
             st_shared_v4_b32(rowa + (static_cast<uint32_t>((4 * h + ch) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }

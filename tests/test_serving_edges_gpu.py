@@ -55,3 +55,25 @@ def test_fp16_prompt_of_keys_far_below_the_maximum(nats, at, D, causal):
     assert ((lse.double() - rlse).abs() <= lse_tol).all()
     bad = (o.double() - ro).abs() > tol + 2.0 ** -36 * size
     assert not bad.any(), (int(bad.sum()), ((o.double() - ro).abs() / ro.abs().clamp(min=1e-30)).max())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp16_prompt_of_the_largest_values(D, causal):
+    """O is a mean of V: where every V is fp16's largest number it is that number, whatever the rounding of P.
+
+    All keys but the first have p = (1 + 1.02 * 2^-11) / 2, just above the middle of two fp16 numbers: rounded, their
+    sum exceeds the row's by nearly 2^-11, and 65504 * (1 + 2^-11) would round to infinity.
+    """
+    n = 400
+    q = torch.zeros((n, 4, D), device="cuda")
+    q[..., 0] = 8.0
+    k = torch.zeros((n, 2, D), device="cuda")
+    k[0, :, 0] = 8.0
+    v = torch.full((n, 2, D), 65504.0, device="cuda")
+    v[:, 1] = -65504.0
+    scale = (1 - math.log2(1 + 1.02 * 2.0 ** -11)) * math.log(2) / 64
+    o, _ = attn.attention_varlen(q.half(), k.half(), v.half(), starts_of([n]), scale=scale, causal=causal)
+    ok()
+    want = v.repeat_interleave(2, 1).double()
+    assert ((o.double() - want).abs() <= 2 * 2.0 ** -11 * 65504).all()  # P's half step and the result's
