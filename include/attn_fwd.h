@@ -263,8 +263,11 @@ typedef enum { ATTN_BF16 = 0, ATTN_FP16 = 1, ATTN_FP32 = 2 } attn_dtype_t;
  *   total       rows of the buffers, 0 .. 2^31 - 1.  Rows that belong to no
  *               sequence (behind the last one) are left as they were.
  *   seq_start   device int32[n_seqs + 1], not read by the host: ascending from
- *               0 or more to `total` or less.  A sequence may be empty.  Entries
- *               out of range or order are clamped to the rows there are.
+ *               0 or more to `total` or less.  A sequence may be empty.  An entry
+ *               out of range counts as the nearest end of the rows there are, and
+ *               a sequence that ends before it begins is empty; sequences that
+ *               overlap leave their rows undefined, and nothing outside them is
+ *               touched.
  *   dtype       ATTN_BF16 or ATTN_FP16 (q, k, v and o).
  *   H_q / H_kv  a whole number, at most 128.  D is 64 or 128.
  *   workspace   caller-owned device buffer, 16-byte aligned, of at least

@@ -56,6 +56,16 @@ __device__ __forceinline__ int varlen_tiles(int i0, int len, int unit_tok, int c
   return (lim + kBN - 1) / kBN;
 }
 
+// First row and length of sequence s, both ends taken as the rows there are: an
+// end of any value leaves the length within 0 .. most.
+struct VarlenRows {
+  int row0, len;
+};
+__device__ __forceinline__ VarlenRows varlen_rows(const int32_t* __restrict__ seq_start, int s, int most) {
+  const int row0 = min(max(__ldg(seq_start + s), 0), most);
+  return {row0, max(0, min(max(__ldg(seq_start + s + 1), 0), most) - row0)};
+}
+
 // Lists the work units of every sequence, most kv tiles first (in no fixed
 // order among equals: each unit's result is its own).  At most `cap` entries,
 // which ascending seq_start never exceeds.
@@ -73,8 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   // pass 0 counts the units of each bucket, pass 1 places them
   for (int pass = 0; pass < 2; ++pass) {
     for (int s = warp; s < n_seqs; s += kPlanThreads / 32) {
-      const int row0 = min(max(__ldg(seq_start + s), 0), most);
-      const int len = min(__ldg(seq_start + s + 1), most) - row0;
+      const auto [row0, len] = varlen_rows(seq_start, s, most);
       for (int i0 = lane * unit_tok; i0 < len; i0 += 32 * unit_tok) {
         const int b = kPlanBuckets - 1 - min(varlen_tiles(i0, len, unit_tok, causal), kPlanBuckets - 1);
         const int at = atomicAdd(&cnt[b], 1);
@@ -537,11 +546,9 @@ __device__ __forceinline__ void varlen_own_unit(const VarlenParams& p, volatile 
   int before = 0;
   for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
     const int s = s0 + lane;
-    int row0 = 0, len = 0;
-    if (s < p.n_seqs) {
-      row0 = min(max(__ldg(p.seq_start + s), 0), most);
-      len = max(0, min(__ldg(p.seq_start + s + 1), most) - row0);
-    }
+    VarlenRows r{0, 0};
+    if (s < p.n_seqs) r = varlen_rows(p.seq_start, s, most);
+    const auto [row0, len] = r;
     const int n = (len + unit_tok - 1) / unit_tok;
     int incl = n;
 #pragma unroll

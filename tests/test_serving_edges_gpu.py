@@ -77,3 +77,34 @@ def test_fp16_prompt_of_the_largest_values(D, causal):
     ok()
     want = v.repeat_interleave(2, 1).double()
     assert ((o.double() - want).abs() <= 2 * 2.0 ** -11 * 65504).all()  # P's half step and the result's
+
+
+@pytest.mark.parametrize("H", [1, 200])
+@pytest.mark.parametrize("starts", [[-(1 << 31), 20, (1 << 31) - 1], [0, 50, -(1 << 31), 64], [(1 << 31) - 1, -(1 << 31)],
+                                    [5, -(1 << 31), -1, 40, 64], [-(1 << 31), (1 << 31) - 1]], ids=str)
+def test_prompt_starts_of_any_value(starts, H):
+    """With one key head each CTA finds its unit itself, with 200 the units are listed: in both, starts count as the
+    rows there are (0 .. 64), and a sequence that then ends before it begins is empty."""
+    total = 64
+    x = torch.randn((total, 3 * H, 64), generator=gen(3), device="cuda").bfloat16()
+    q, k, v = x[:, :H], x[:, H:2 * H], x[:, 2 * H:]
+    out = torch.full((total, H, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, total), 7.0, device="cuda")
+    s = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    assert (attn.attn_fwd_varlen_workspace_bytes(total, len(starts) - 1, H, H, 64) > 16) == (H == 200)
+    attn.attention_varlen(q, k, v, s, out=out, lse=lse)
+    ok()
+    want = [min(max(a, 0), total) for a in starts]
+    heads = list(range(H)) if H == 1 else [0, 99, 199]
+    pick = torch.tensor(heads, device="cuda")
+    seen = torch.zeros(total, dtype=torch.bool, device="cuda")
+    for a, b in zip(want, want[1:]):
+        if a >= b:
+            continue
+        # (sequences that overlap are computed each for itself: only rows of one are looked at)
+        alone = [r for r in range(a, b) if sum(c <= r < d for c, d in zip(want, want[1:])) == 1]
+        ro, rlse, tol, lse_tol = ref.varlen(q[:, pick], k[:, pick], v[:, pick], [a, b], 0.125, True)
+        assert ((out[alone][:, pick].double() - ro[alone]).abs() <= tol[alone]).all()
+        assert ((lse[pick][:, alone].double() - rlse[:, alone]).abs() <= lse_tol[:, alone]).all()
+        seen[a:b] = True
+    assert (out[~seen] == 7.0).all() and (lse[:, ~seen] == 7.0).all()
