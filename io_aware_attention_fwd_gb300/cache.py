@@ -65,8 +65,10 @@ class KVCache4:
 
         if D not in (64, 128):
             raise ValueError("D must be 64 or 128")
-        codes = torch.empty((2, B, H_kv, capacity, D // 2), dtype=torch.uint8, device=device)
-        meta = torch.empty((2, B, H_kv, capacity, D // GROUP, 2), dtype=torch.bfloat16, device=device)
+        # an allocation each: a half of one for K and V begins off an 8-byte boundary
+        # where D is 64 and the number of entries odd
+        codes = [torch.empty((B, H_kv, capacity, D // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+        meta = [torch.empty((B, H_kv, capacity, D // GROUP, 2), dtype=torch.bfloat16, device=device) for _ in range(2)]
         return cls(codes[0], meta[0], codes[1], meta[1],
                    torch.zeros((B, H_kv, capacity), dtype=torch.float32, device=device),
                    torch.zeros((B, H_kv, capacity), dtype=torch.int32, device=device),

@@ -108,3 +108,22 @@ def test_prompt_starts_of_any_value(starts, H):
         assert ((lse[pick][:, alone].double() - rlse[:, alone]).abs() <= lse_tol[:, alone]).all()
         seen[a:b] = True
     assert (out[~seen] == 7.0).all() and (lse[:, ~seen] == 7.0).all()
+
+
+# --- the cache -------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,H,cap", [(1, 1, 1), (1, 1, 5), (3, 1, 7), (1, 3, 129)])
+def test_caches_of_an_odd_number_of_entries(B, H, cap):
+    D = 64
+    c = attn.KVCache4.empty(B, H, cap, D)
+    x = torch.randn((B, H, D), generator=gen(1), device="cuda").bfloat16()
+    c.append(x, x)
+    o, lse = c.attend(x, weight_out=c.weight)
+    k, v = c.read(dtype=torch.float32)
+    c.evict(1)
+    ok()
+    code, s, m = ref.quantise(x)
+    want = ref.values(ref.pack(code), torch.stack([s, m], -1))
+    assert torch.equal(k.double(), want) and torch.equal(v.double(), want)
+    assert ((o.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * want.abs().amax() * 4).all()
+    assert c.length.tolist() == [1] * B and ((c.weight[..., 0] - 1).abs() <= 1e-6).all()
