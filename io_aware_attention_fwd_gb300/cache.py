@@ -28,35 +28,51 @@ class KVCache4:
 
     The calls work in place on these buffers, on the current stream (or the one
     given), and never wait for the GPU.  Where a call has ``..._out`` arguments,
-    what it would update in place goes there instead; a ``KVCache4`` over those
-    buffers is then the cache after the call.
+    what it would update in place goes there instead; assigned to the cache
+    (``cache.length = length_out``), those buffers are then the cache after the
+    call.  A buffer may be exchanged for another of the same shape, type and device;
+    the sizes are fixed.  ``copy.copy`` gives a cache over the same buffers,
+    ``copy.deepcopy`` one over copies of them.
     """
 
     __slots__ = ("k_codes", "k_meta", "v_codes", "v_meta", "weight", "pos", "length", "B", "H_kv", "capacity", "D",
                  "device", "_c")
 
     def __init__(self, k_codes, k_meta, v_codes, v_meta, weight, pos, length):
-        import torch
-
         if k_codes.dim() != 4 or not k_codes.is_cuda:
             raise ValueError("k_codes must be a CUDA tensor [B, H_kv, capacity, D // 2]")
         B, H_kv, capacity, half = k_codes.shape
-        D, device = 2 * half, k_codes.device
-        if D % GROUP:
+        if 2 * half % GROUP:
             raise ValueError(f"D must be a multiple of {GROUP}")
-        codes, meta, entry = (B, H_kv, capacity, half), (B, H_kv, capacity, D // GROUP, 2), (B, H_kv, capacity)
-        check_out(k_codes, codes, torch.uint8, device, "k_codes")
-        check_out(v_codes, codes, torch.uint8, device, "v_codes")
-        check_out(k_meta, meta, torch.bfloat16, device, "k_meta")
-        check_out(v_meta, meta, torch.bfloat16, device, "v_meta")
-        check_out(weight, entry, torch.float32, device, "weight")
-        check_out(pos, entry, torch.int32, device, "pos")
-        check_int32(length, B, device, "length")
+        for name, value in (("B", B), ("H_kv", H_kv), ("capacity", capacity), ("D", 2 * half), ("device", k_codes.device),
+                            ("_c", _lib.attn_cache4_t(B=B, H_kv=H_kv, capacity=capacity, D=2 * half))):
+            object.__setattr__(self, name, value)
         self.k_codes, self.k_meta, self.v_codes, self.v_meta = k_codes, k_meta, v_codes, v_meta
         self.weight, self.pos, self.length = weight, pos, length
-        self.B, self.H_kv, self.capacity, self.D, self.device = B, H_kv, capacity, D, device
-        self._c = _lib.attn_cache4_t(k_codes.data_ptr(), k_meta.data_ptr(), v_codes.data_ptr(), v_meta.data_ptr(),
-                                     weight.data_ptr(), pos.data_ptr(), length.data_ptr(), B, H_kv, capacity, D)
+
+    def __setattr__(self, name, value):
+        """A buffer, checked; the struct that the calls pass on holds its address."""
+        import torch
+
+        B, H_kv, capacity, D = self.B, self.H_kv, self.capacity, self.D
+        wanted = {"k_codes": ((B, H_kv, capacity, D // 2), torch.uint8), "v_codes": ((B, H_kv, capacity, D // 2), torch.uint8),
+                  "k_meta": ((B, H_kv, capacity, D // GROUP, 2), torch.bfloat16),
+                  "v_meta": ((B, H_kv, capacity, D // GROUP, 2), torch.bfloat16),
+                  "weight": ((B, H_kv, capacity), torch.float32), "pos": ((B, H_kv, capacity), torch.int32),
+                  "length": ((B,), torch.int32)}.get(name)
+        if wanted is None:
+            raise AttributeError(f"a cache's {name} cannot be set")
+        if not isinstance(value, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        check_out(value, *wanted, self.device, name)
+        object.__setattr__(self, name, value)
+        setattr(self._c, name, value.data_ptr())
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a cache's {name} cannot be removed")
+
+    def __reduce__(self):
+        return type(self), (self.k_codes, self.k_meta, self.v_codes, self.v_meta, self.weight, self.pos, self.length)
 
     @classmethod
     def empty(cls, B: int, H_kv: int, capacity: int, D: int, device="cuda") -> "KVCache4":

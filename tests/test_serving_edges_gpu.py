@@ -127,3 +127,57 @@ def test_caches_of_an_odd_number_of_entries(B, H, cap):
     assert torch.equal(k.double(), want) and torch.equal(v.double(), want)
     assert ((o.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * want.abs().amax() * 4).all()
     assert c.length.tolist() == [1] * B and ((c.weight[..., 0] - 1).abs() <= 1e-6).all()
+
+
+def test_buffers_can_be_exchanged_and_sizes_cannot():
+    B, H, cap, D = 2, 1, 20, 64
+    c = attn.KVCache4.empty(B, H, cap, D)
+    old = {name: getattr(c, name) for name in ("k_codes", "k_meta", "v_codes", "v_meta", "weight", "pos", "length")}
+    for name in ("k_codes", "k_meta", "v_codes", "v_meta"):
+        old[name].zero_()
+    x = torch.randn((B, H, D), generator=gen(1), device="cuda").bfloat16()
+    c.append(x, x)
+    # what a call has written elsewhere takes the old buffer's place
+    grown = torch.empty_like(c.length)
+    c.append(x, x, length_out=grown)
+    c.length = grown
+    weight = torch.full_like(c.weight, 3.0)
+    c.attend(x, weight_out=weight)
+    c.weight = weight
+    c.append(x, x)
+    ok()
+    assert c.length is grown and grown.tolist() == [3, 3] and old["length"].tolist() == [1, 1]
+    assert (old["weight"] == 0).all() and (weight[:, :, 2] == 0).all() and ((weight[:, :, :2] - 0.5).abs() <= 1e-6).all()
+    for name in ("k_codes", "k_meta", "v_codes", "v_meta", "pos"):
+        setattr(c, name, old[name].clone())
+        before = old[name].clone()
+        c.length.fill_(4)
+        c.append(-x, -x)
+        ok()
+        assert torch.equal(old[name], before) and not torch.equal(getattr(c, name)[:, :, 4], before[:, :, 4]), name
+    for name, bad in (("length", torch.zeros(3, dtype=torch.int32, device="cuda")), ("weight", weight.double()), ("pos", None),
+                      ("weight", weight[..., ::2]), ("k_codes", old["k_codes"].cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            setattr(c, name, bad)
+    for name in ("B", "H_kv", "capacity", "D", "device"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, 1)
+    with pytest.raises(AttributeError):
+        del c.weight
+    assert c.weight is weight and c.length is grown
+
+
+def test_a_copied_cache_has_buffers_of_its_own_only_where_it_is_deep():
+    import copy
+
+    c = attn.KVCache4.empty(1, 1, 4, 64)
+    x = torch.randn((1, 1, 64), generator=gen(1), device="cuda").bfloat16()
+    c.append(x, x)
+    shallow, deep = copy.copy(c), copy.deepcopy(c)
+    shallow.length = torch.zeros_like(c.length)  # the copy's alone
+    c.append(x, x)
+    deep.append(-x, -x)
+    ok()
+    assert shallow.k_codes is c.k_codes and shallow.length.tolist() == [0]
+    assert c.length.tolist() == [2] and deep.length.tolist() == [2]
+    assert torch.equal(deep.k_codes[:, :, 0], c.k_codes[:, :, 0]) and not torch.equal(deep.k_meta[:, :, 1], c.k_meta[:, :, 1])
