@@ -37,6 +37,15 @@ _lock = threading.Lock()
 _lib = None
 
 
+_INT_MAX = 0x7FFFFFFF
+
+
+def _int32(*values) -> bool:
+    """Whether the values fit a C int.  ctypes would pass on their low 32 bits: a
+    budget of 2^32 + 10, meant as no limit, would be one of 10."""
+    return max(values) <= _INT_MAX and min(values) >= -_INT_MAX - 1
+
+
 class attn_cache4_t(ctypes.Structure):
     """The struct of the same name: a 4-bit K/V cache's buffers and sizes."""
 
@@ -44,6 +53,11 @@ class attn_cache4_t(ctypes.Structure):
                 ("v_meta", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("pos", ctypes.c_void_p),
                 ("length", ctypes.c_void_p), ("B", ctypes.c_int), ("H_kv", ctypes.c_int),
                 ("capacity", ctypes.c_int), ("D", ctypes.c_int)]
+
+    def __setattr__(self, name, value):
+        if name in ("B", "H_kv", "capacity", "D") and not _int32(value):
+            raise OverflowError(f"attn_cache4_t.{name}: {value} does not fit an int")
+        super().__setattr__(name, value)
 
 
 class AttnError(RuntimeError):
@@ -250,6 +264,8 @@ def attn_fwd_varlen(q, k, v, o, lse, total: int, seq_start, n_seqs: int, H_q: in
                     q_stride: int, k_stride: int, v_stride: int, scale: float, causal: bool, workspace,
                     workspace_bytes: int, stream=None) -> None:
     """Enqueue attention over packed prompts with grouped heads (see include/attn_fwd.h)."""
+    if not _int32(n_seqs, H_q, H_kv, D, dtype):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_fwd_varlen")
     st = load().attn_fwd_varlen(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), total, _addr(seq_start), n_seqs, H_q,
                                 H_kv, D, dtype, q_stride, k_stride, v_stride, scale, int(bool(causal)),
                                 _addr(workspace), workspace_bytes, _stream(stream))
@@ -259,7 +275,7 @@ def attn_fwd_varlen(q, k, v, o, lse, total: int, seq_start, n_seqs: int, H_q: in
 
 @functools.lru_cache(maxsize=256)
 def attn_fwd_varlen_workspace_bytes(total: int, n_seqs: int, H_q: int, H_kv: int, D: int) -> int:
-    return load().attn_fwd_varlen_workspace_bytes(total, n_seqs, H_q, H_kv, D)
+    return load().attn_fwd_varlen_workspace_bytes(total, n_seqs, H_q, H_kv, D) if _int32(n_seqs, H_q, H_kv, D) else 0
 
 
 def attn_cache4_append(cache: attn_cache4_t, k, v, rows: int, k_stride: int, v_stride: int, dtype: int, seq_start,
@@ -283,6 +299,8 @@ def attn_cache4_read(cache: attn_cache4_t, k, v, rows: int, k_stride: int, v_str
 def attn_cache4_decode(cache: attn_cache4_t, q, q_stride: int, o, lse, H_q: int, dtype: int, scale: float,
                        max_len: int, weight_in, weight_out, workspace, workspace_bytes: int, stream=None) -> None:
     """Enqueue attention of one token per sequence over the cache (see include/attn_fwd.h)."""
+    if not _int32(H_q, dtype, max_len):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_cache4_decode")
     st = load().attn_cache4_decode(cache, _addr(q), q_stride, _addr(o), _addr(lse), H_q, dtype, scale, max_len,
                                    _addr(weight_in), _addr(weight_out), _addr(workspace), workspace_bytes,
                                    _stream(stream))
@@ -292,12 +310,16 @@ def attn_cache4_decode(cache: attn_cache4_t, q, q_stride: int, o, lse, H_q: int,
 
 @functools.lru_cache(maxsize=256)
 def attn_cache4_decode_workspace_bytes(B: int, H_q: int, H_kv: int, D: int, max_len: int, with_weight: bool) -> int:
+    if not _int32(B, H_q, H_kv, D, max_len):
+        return 0
     return load().attn_cache4_decode_workspace_bytes(B, H_q, H_kv, D, max_len, int(bool(with_weight)))
 
 
 def attn_cache4_evict(cache: attn_cache4_t, budget: int, recent: int, max_len: int, weight_out, pos_out, length_out,
                       workspace, workspace_bytes: int, stream=None) -> None:
     """Enqueue the eviction by accumulated weight (see include/attn_fwd.h)."""
+    if not _int32(budget, recent, max_len):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_cache4_evict")
     st = load().attn_cache4_evict(cache, budget, recent, max_len, _addr(weight_out), _addr(pos_out), _addr(length_out),
                                   _addr(workspace), workspace_bytes, _stream(stream))
     if st != ATTN_OK:
@@ -306,7 +328,7 @@ def attn_cache4_evict(cache: attn_cache4_t, budget: int, recent: int, max_len: i
 
 @functools.lru_cache(maxsize=256)
 def attn_cache4_evict_workspace_bytes(B: int, H_kv: int, max_len: int, budget: int) -> int:
-    return load().attn_cache4_evict_workspace_bytes(B, H_kv, max_len, budget)
+    return load().attn_cache4_evict_workspace_bytes(B, H_kv, max_len, budget) if _int32(B, H_kv, max_len, budget) else 0
 
 
 def call_status(fn, *args, **kwargs) -> int:
