@@ -148,13 +148,13 @@ def test_buffers_can_be_exchanged_and_sizes_cannot():
     ok()
     assert c.length is grown and grown.tolist() == [3, 3] and old["length"].tolist() == [1, 1]
     assert (old["weight"] == 0).all() and (weight[:, :, 2] == 0).all() and ((weight[:, :, :2] - 0.5).abs() <= 1e-6).all()
-    for name in ("k_codes", "k_meta", "v_codes", "v_meta", "pos"):
+    for slot, name in enumerate(("k_codes", "k_meta", "v_codes", "v_meta", "pos"), 4):
         setattr(c, name, old[name].clone())
         before = old[name].clone()
-        c.length.fill_(4)
+        c.length.fill_(slot)  # a slot that no append before has written
         c.append(-x, -x)
         ok()
-        assert torch.equal(old[name], before) and not torch.equal(getattr(c, name)[:, :, 4], before[:, :, 4]), name
+        assert torch.equal(old[name], before) and not torch.equal(getattr(c, name)[:, :, slot], before[:, :, slot]), name
     for name, bad in (("length", torch.zeros(3, dtype=torch.int32, device="cuda")), ("weight", weight.double()), ("pos", None),
                       ("weight", weight[..., ::2]), ("k_codes", old["k_codes"].cpu())):
         with pytest.raises((ValueError, TypeError)):
