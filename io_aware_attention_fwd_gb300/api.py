@@ -97,6 +97,8 @@ def on_stream(device, stream, call):
     too, so that what the call allocates belongs to it."""
     import torch
 
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device):
         if stream is None:
             return call()

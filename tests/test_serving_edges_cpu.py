@@ -2,9 +2,10 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
 import io_aware_attention_fwd_gb300 as attn
-from io_aware_attention_fwd_gb300 import build_ext
+from io_aware_attention_fwd_gb300 import api, build_ext
 
 FAKE = 0x10000  # aligned, non-null, never dereferenced on these paths
 
@@ -60,3 +61,14 @@ def test_numbers_beyond_an_int_are_refused(big):
         with pytest.raises(OverflowError):
             setattr(c, name, big)
     assert (c.B, c.H_kv, c.capacity, c.D) == (3, 2, 100, 64)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    class Stream:
+        device = torch.device("cuda:1")
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    called = []
+    with pytest.raises(ValueError, match="cuda:1"):
+        api.on_stream(torch.device("cuda:0"), Stream(), lambda: called.append(1))
+    assert not called
