@@ -150,7 +150,8 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
 // multiply-add, is the correctly rounded d / s (P. Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990), as long
 // as nothing under- or overflows: s within 2^-100 .. 2^100, else the division
-// itself is used (a group of such values alone pays for it).
+// itself is used (a group of such values alone pays for it), on halves where the
+// values are large: max - min may be twice what fp32 holds, 15 times s is not.
 template <int kType>
 __device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta) {
   const uint32_t lo2 = min_16x2<kType>(min_16x2<kType>(raw.x, raw.y), min_16x2<kType>(raw.z, raw.w));
@@ -200,15 +201,16 @@ __device__ __forceinline__ uint32_t c4_quantise(const uint4& raw, uint32_t* meta
     }
     w -= 0x4b400000u * 0x11111111u;
   } else {
-    sm = pack_bf16x2(__fdiv_rn(range, 15.f), lo);
+    const float half = range > 0x1p100f ? 0.5f : 1.f;  // (exact for every value that counts next to such a range)
+    sm = pack_bf16x2(__fdiv_rn(hi * half - lo * half, 15.f * half), lo);
     s = bf16_lo(sm);
 #pragma unroll
     for (int e = 3; e >= 0; --e) {
-      float d[2];
-      unpack_f32x2(x[e], d[0], d[1]);
+      const float2 f = unpack_16x2<kType>((&raw.x)[e]);
+      const float d[2] = {f.x * half - m * half, f.y * half - m * half};
 #pragma unroll
       for (int i = 1; i >= 0; --i) {
-        const float c = s != 0.f ? rintf(fminf(fmaxf(__fdiv_rn(d[i], s), 0.f), 15.f)) : 0.f;
+        const float c = s != 0.f ? rintf(fminf(fmaxf(__fdiv_rn(d[i], s * half), 0.f), 15.f)) : 0.f;
         w = w * 16u + static_cast<uint32_t>(c);
       }
     }

@@ -181,3 +181,46 @@ def test_a_copied_cache_has_buffers_of_its_own_only_where_it_is_deep():
     assert shallow.k_codes is c.k_codes and shallow.length.tolist() == [0]
     assert c.length.tolist() == [2] and deep.length.tolist() == [2]
     assert torch.equal(deep.k_codes[:, :, 0], c.k_codes[:, :, 0]) and not torch.equal(deep.k_meta[:, :, 1], c.k_meta[:, :, 1])
+
+
+@pytest.mark.parametrize("low,high", [(-3e38, 3e38), (-3.38e38, 1e38), (0.0, 3.38e38), (-3.38e38, -1e38), (-1e31, 2e31)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_of_the_largest_finite_values(D, low, high):
+    """A group is finite where its values are, also where max - min is beyond fp32's range."""
+    n, H = 64, 2
+    x = (low + (high / 2 - low / 2) * 2 * torch.rand((n, H, D), generator=gen(1), device="cuda", dtype=torch.float64)).bfloat16()
+    x[:, :, 3::64], x[:, :, 40::64] = low, high
+    c = attn.KVCache4.empty(1, H, n, D)
+    c.append(x, x.flip(0), seq_start=starts_of([n]))
+    ok()
+    for y, codes, meta in ((x, c.k_codes, c.k_meta), (x.flip(0), c.v_codes, c.v_meta)):
+        code, s, m = ref.quantise(y.transpose(0, 1))
+        assert s.isfinite().all() and torch.equal(meta[0].double(), torch.stack([s, m], -1))
+        q = ((y.transpose(0, 1).double().unflatten(-1, (-1, 64)) - m[..., None]) / s[..., None]).flatten(-2)
+        near = (q - q.floor() - 0.5).abs() <= 16 * 2.0 ** -23  # a 32-bit quotient may fall on the half way point itself
+        got = ref.unpack(codes[0])
+        assert torch.equal(got[~near], code[~near]) and ((got - code).abs()[near] <= 1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_append_and_read_of_the_smallest_scales(dtype):
+    """Scales below 2^-100, subnormal ones among them, and 0: the read's own branch, and the append's division."""
+    n, D = 48, 128
+    x = torch.randn((n, 1, D), generator=gen(4), device="cuda", dtype=torch.float64)
+    x *= (2.0 ** torch.linspace(-131, -96, n, device="cuda", dtype=torch.float64))[:, None, None]
+    x[0] = 0
+    x = x.bfloat16()
+    c = attn.KVCache4.empty(1, 1, n, D)
+    c.append(x, x, seq_start=starts_of([n]))
+    k, _ = c.read(seq_start=starts_of([n]), rows=n, dtype=dtype)
+    ok()
+    code, s, m = ref.quantise(x.transpose(0, 1))
+    assert (s < 2.0 ** -100).any() and ((s > 0) & (s < 2.0 ** -126)).any() and (s > 2.0 ** -100).any() and (s == 0).any()
+    assert torch.equal(c.k_meta[0].double(), torch.stack([s, m], -1))
+    want = ref.values(c.k_codes, c.k_meta)[0].transpose(0, 1)
+    # one rounding to fp32, and one to the output's type; subnormal steps below the normal numbers
+    u = ref.HALF_STEP[torch.float32] + (ref.HALF_STEP[dtype] if dtype != torch.float32 else 0)
+    assert ((k.double() - want).abs() <= u * want.abs() + (2.0 ** -134 if dtype == torch.bfloat16 else 2.0 ** -150)).all()
+    q = ((x.transpose(0, 1).double().unflatten(-1, (-1, 64)) - m[..., None]) / s[..., None].where(s[..., None] != 0, torch.ones_like(s[..., None]))).flatten(-2)
+    near = (q - q.floor() - 0.5).abs() <= 2.0 ** -19
+    assert torch.equal(ref.unpack(c.k_codes[0])[~near], code[~near])
