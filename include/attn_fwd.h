@@ -342,7 +342,9 @@ typedef struct {
  * Row i of sequence b goes to slot length[b] + i of every key head, with weight
  * 0 and position first_pos[b] + i (where the cache has those buffers).  Rows for
  * which there is no room are dropped, the length stays at the capacity, and
- * attn_fwd_debug_status reports ATTN_ERR_CAPACITY.  Asynchronous.
+ * attn_fwd_debug_status reports ATTN_ERR_CAPACITY for the device.  (Which
+ * sequence it was, the lengths tell: before + rows is more than the capacity.)
+ * Asynchronous.
  */
 attn_status_t attn_cache4_append(const attn_cache4_t* cache, const void* k, const void* v, int64_t rows,
                                  int64_t k_stride, int64_t v_stride, int dtype, const int32_t* seq_start,
@@ -430,6 +432,9 @@ const char* attn_status_str(attn_status_t status);
  * entries (attn_cache4_append), or ATTN_ERR_DEVICE if the
  * synchronisation itself reported a CUDA error or the backward kernel found
  * its dynamic shared memory off a 1024-byte boundary (it then runs nothing).
+ * There is one word a device: it says that some call since the last reading
+ * failed so, on whatever stream.  A drop beside another failure is reported by
+ * the next reading.
  */
 attn_status_t attn_fwd_debug_status(void* stream);
 

@@ -112,7 +112,8 @@ class KVCache4:
         sequence b's; None: one row for each sequence.  first_pos: int32 [B],
         position of each sequence's first new token (None: its slot's number).
         The new entries' weights are 0.  Rows beyond the capacity are dropped, and
-        attn_fwd_debug_status then reports ATTN_ERR_CAPACITY.
+        attn_fwd_debug_status then reports ATTN_ERR_CAPACITY (once, for whichever
+        cache of the device it was).
         """
         rows, ks, vs, code = self._rows(k, v, seq_start)
         device = self.device

@@ -1423,6 +1423,8 @@ __global__ void attn_watchdog_kernel(unsigned long long timeout_ns) {
   __syncthreads();
 }
 
+__global__ void attn_status_clear_kernel(unsigned int bits) { atomicAnd(&g_attn_status, ~bits); }
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -2028,9 +2030,15 @@ attn_status_t attn_merge(const float* o_parts, const float* lse_parts, int n_par
 
 attn_status_t attn_fwd_debug_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_DEVICE;
-  unsigned int word = 0, zero = 0;
+  unsigned int word = 0;
   if (cudaMemcpyFromSymbol(&word, g_attn_status, sizeof word) != cudaSuccess) return ATTN_ERR_DEVICE;
-  if (word != 0u && cudaMemcpyToSymbol(g_attn_status, &zero, sizeof zero) != cudaSuccess) return ATTN_ERR_DEVICE;
+  if (word != 0u) {
+    // What is reported is cleared, bit by bit on the device: a kernel of another
+    // stream may have set one meanwhile, and a drop waits for its own report.
+    attn_status_clear_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>((word & 3u) != 0u ? word & 3u : word);
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return ATTN_ERR_DEVICE;
+  }
   if (word & 2u) return ATTN_ERR_DEVICE;  // a kernel found its shared memory misaligned and did not run
   if (word & 1u) return ATTN_ERR_TIMEOUT;
   return word != 0u ? ATTN_ERR_CAPACITY : ATTN_OK;

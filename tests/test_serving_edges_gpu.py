@@ -224,3 +224,15 @@ def test_append_and_read_of_the_smallest_scales(dtype):
     q = ((x.transpose(0, 1).double().unflatten(-1, (-1, 64)) - m[..., None]) / s[..., None].where(s[..., None] != 0, torch.ones_like(s[..., None]))).flatten(-2)
     near = (q - q.floor() - 0.5).abs() <= 2.0 ** -19
     assert torch.equal(ref.unpack(c.k_codes[0])[~near], code[~near])
+
+
+def test_a_drop_outlives_the_report_of_another_failure():
+    c = attn.KVCache4.empty(1, 1, 1, 128)
+    x = torch.zeros((2, 1, 128), dtype=torch.bfloat16, device="cuda")
+    ok()
+    c.append(x, x, seq_start=starts_of([2]))
+    torch.cuda.synchronize()
+    # the self-test waits its limit out and returns: its report comes first, the drop's stays for the next call
+    assert attn.attn_watchdog_selftest(1_000_000) == attn.ATTN_ERR_TIMEOUT
+    assert attn.attn_fwd_debug_status() == attn.ATTN_ERR_CAPACITY
+    assert attn.attn_fwd_debug_status() == attn.ATTN_OK
