@@ -389,10 +389,13 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 //   * q is scaled by a power of two that brings its head's largest channel to
 //     2^10 .. 2^11, which fp16 holds exactly down to 2^-24 of it and to 2^-35 of
 //     it absolutely; the scale goes back into the logits.
-//   * p s is held relative to a power of two at or above every s the warp has
-//     met in that group of channels, times 2^7: at most 2^15, with 11 bits down
-//     to 2^-29 of the largest.  When a larger s comes, O is rescaled, as it is
-//     when the running maximum grows.
+//   * p s is held relative to a power of two T at or above every p s of that head
+//     and group of channels when it was set, times 2^11: a tile that brings more
+//     than 2^15 sets it anew, and O is rescaled, as it is when the running maximum
+//     grows (p s of the keys so far shrinks with it, and so does T).  So p s has 11
+//     bits down to 2^-25 of the largest and is off by 2^-36 T at most below.  It has
+//     to be the largest product: relative to the largest s, one key of no weight
+//     with an s 2^25 times the others' took the bits from all of them.
 //
 // mma.sync m16n8k16 serves here, with keys as the M rows of S^T = K Q^T, and
 // channels as the M rows of O^T = V^T P^T: the A operands are then the cache's
@@ -819,10 +822,13 @@ struct C4State {
   float most[2];             // 8 log2 units above ref
   float l[2];                // this lane's share of sum p
   float bias[kGroups][2];    // this lane's share of sum p (m + 8 s)
-  float top_s[kGroups];      // power of two at or above every s so far (0 at first)
-  float inv_s[kGroups];      // 2^7 / top_s
-  float o[kGroups][4][4];    // O^T in units of top_s / 2^7: channels 64g + 4r + u (+ 32), heads 2c, 2c + 1
+  float inv[kGroups][2];     // what p s is held times, a power of two (0 at first)
+  float o[kGroups][4][4];    // O^T, times inv: channels 64g + 4r + u (+ 32), heads 2c, 2c + 1
 };
+// 1 / inv, 0 where inv is.
+__device__ __forceinline__ float c4_unit(float inv) {
+  return inv == 0.f ? 0.f : __uint_as_float((254u << 23) - __float_as_uint(inv));
+}
 
 // Logits of a tile's 16 keys: keys r, r, r + 8, r + 8 and heads 2c, 2c + 1, 2c,
 // 2c + 1.  ldmatrix gives this lane word c (8 channels) of a piece of rows r and
@@ -857,21 +863,40 @@ __device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_
   for (int e = 0; e < 4; ++e) xs[e] *= q.scale[e & 1];
 }
 
-// O^T += V^T P^T over a tile's 16 keys; pr as c4_scores lays out the logits.
+// p of a tile's 16 keys and, in fp16, p s times st.inv; pr as c4_scores lays out the
+// logits.  Returns the largest of the products and `most`.
+template <int D>
+__device__ __forceinline__ float c4_weigh(float* pr, uint32_t (*ps)[2], const float* xs, const C4State<D>& st,
+                                          const uint32_t (*sm)[D / kC4Group], float most) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(fmaf(xs[e], kC4LogitUnit, -st.sub[e & 1]));
+#pragma unroll
+  for (int g = 0; g < D / kC4Group; ++g)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // (s last: a p of 0 stays 0, whatever s times inv is)
+      const float s = bf16_lo(sm[i][g]), y0 = pr[2 * i] * st.inv[g][0] * s, y1 = pr[2 * i + 1] * st.inv[g][1] * s;
+      most = max3f(most, fabsf(y0), fabsf(y1));
+      ps[g][i] = pack_f16x2(y0, y1);
+    }
+  return most;
+}
+
+// O^T += V^T P^T over a tile's 16 keys; pr and ps as c4_weigh leaves them.
 // ldmatrix transposes units of 16 bits, 4 channels: this lane gets unit r of a
 // piece from keys 2c and 2c + 1 side by side (and from 2c + 8, 2c + 9).
 template <int D>
-__device__ __forceinline__ void c4_values(C4State<D>& st, const float* pr, const uint32_t (*sm)[D / kC4Group],
-                                          const C4Lane<D>& p, uint32_t stage) {
+__device__ __forceinline__ void c4_values(C4State<D>& st, const float* pr, const uint32_t (*ps)[2],
+                                          const uint32_t (*sm)[D / kC4Group], const C4Lane<D>& p, uint32_t stage) {
 #pragma unroll
   for (int g = 0; g < D / kC4Group; ++g) {
     uint32_t pb[2];  // P^T as the B operand: keys 0-7 and 8-15
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float s = bf16_lo(sm[i][g]), mm = fmaf(8.f, s, bf16_hi(sm[i][g])), sr = s * st.inv_s[g];
+      const float mm = fmaf(8.f, bf16_lo(sm[i][g]), bf16_hi(sm[i][g]));
       st.bias[g][0] = fmaf(pr[2 * i], mm, st.bias[g][0]);
       st.bias[g][1] = fmaf(pr[2 * i + 1], mm, st.bias[g][1]);
-      pb[i] = movmatrix_trans(pack_f16x2(pr[2 * i] * sr, pr[2 * i + 1] * sr));
+      pb[i] = movmatrix_trans(ps[g][i]);
     }
     uint32_t w[4];
     ldmatrix_x4_trans(w, p.codes[g] + stage + C4Ring<D>::kV);
@@ -912,26 +937,20 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
       }
     }
   }
-  uint32_t sm[kN][2][kG];
-  float top[2] = {-INFINITY, -INFINITY}, top_s[kG];
-#pragma unroll
-  for (int g = 0; g < kG; ++g) top_s[g] = 0.f;
+  uint32_t sm[kN][2][kG], ps[kN][kG][2];
+  float pr[kN][4], top[2] = {-INFINITY, -INFINITY}, most = 0.f;
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
     c4_load_meta<D>(sm[n], p.meta + stage[n] + (R::kVm - R::kKm));
 #pragma unroll
     for (int e = 0; e < 2; ++e) top[e] = max3f(top[e], xs[n][e], xs[n][2 + e]);
-#pragma unroll
-    for (int g = 0; g < kG; ++g) top_s[g] = max3f(top_s[g], bf16_lo(sm[n][0][g]), bf16_lo(sm[n][1][g]));
+    most = c4_weigh<D>(pr[n], ps[n], xs[n], st, sm[n], most);
   }
-  // New references only where a score exceeds the old one by 2^8 or an s the
-  // old bound: p stays below 2^8, the results do not depend on the references,
-  // and most tiles need one vote instead of reductions and a rescale.
-  bool grow = (top[0] > st.most[0]) | (top[1] > st.most[1]);
-#pragma unroll
-  for (int g = 0; g < kG; ++g) grow |= top_s[g] > st.top_s[g];
-  if (__any_sync(0xffffffffu, grow)) {
-    float a[2], f[kG];
+  // New references only where a score exceeds the old one by 2^8 or a product fp16's
+  // range: p stays below 2^8, and most tiles need one vote instead of reductions and
+  // a rescale.  (Where all scores are NaN there is no reference, and none is needed.)
+  if (__any_sync(0xffffffffu, (top[0] > st.most[0]) | (top[1] > st.most[1]) | (most > 0x1p15f))) {
+    float a[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -945,31 +964,38 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
       st.most[e] = to + kRescaleLog2 / kC4LogitUnit;
       st.l[e] *= a[e];
     }
+    // T / 2^16 of a head and group (p s itself may be beyond fp32's range): the next
+    // power of two above these tiles' products, or the old one as far as it has not
+    // shrunk with p
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
+    for (int g = 0; g < kG; ++g)
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) top_s[g] = fmaxf(top_s[g], __shfl_xor_sync(0xffffffffu, top_s[g], off));
-      const uint32_t up = (__float_as_uint(top_s[g]) + 0x007fffffu) & 0x7f800000u;  // the next power of two
-      const uint32_t to = max(max(up, __float_as_uint(st.top_s[g])), 17u << 23);
-      f[g] = st.top_s[g] == __uint_as_float(to) ? 1.f : __fdividef(st.top_s[g], __uint_as_float(to));
-      st.top_s[g] = __uint_as_float(to);
-      st.inv_s[g] = __uint_as_float((261u << 23) - to);
-      st.bias[g][0] *= a[0];
-      st.bias[g][1] *= a[1];
+      for (int e = 0; e < 2; ++e) {
+        float x = 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[g][u][e] *= a[e & 1] * f[g];
-    }
+          for (int i = 0; i < 2; ++i)
+            x = fmaxf(x, fabsf(ex2_approx(fmaf(xs[n][2 * i + e], kC4LogitUnit, -st.sub[e])) * (bf16_lo(sm[n][i][g]) * 0x1p-16f)));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+        const float old = c4_unit(st.inv[g][e]) * 0x1p-5f * a[e];
+        const uint32_t up = max((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u, __float_as_uint(old) & 0x7f800000u);
+        const uint32_t to = min(max(up, 17u << 23), 247u << 23);
+        const float f = old * __uint_as_float((254u << 23) - to);
+        st.inv[g][e] = __uint_as_float((249u << 23) - to);  // 2^-5 / to: 2^11 / T
+        st.bias[g][e] *= a[e];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) st.o[g][u][e] *= f, st.o[g][u][2 + e] *= f;
+      }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) c4_weigh<D>(pr[n], ps[n], xs[n], st, sm[n], 0.f);
   }
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      xs[n][e] = ex2_approx(fmaf(xs[n][e], kC4LogitUnit, -st.sub[e & 1]));
-      st.l[e & 1] += xs[n][e];
-    }
-    c4_values<D>(st, xs[n], sm[n], p, stage[n]);
+    for (int e = 0; e < 4; ++e) st.l[e & 1] += pr[n][e];
+    c4_values<D>(st, pr[n], ps[n], sm[n], p, stage[n]);
   }
 }
 
@@ -1075,7 +1101,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
     for (int e = 0; e < 2; ++e) st.ref[e] = st.most[e] = -INFINITY, st.sub[e] = st.l[e] = 0.f;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      st.top_s[g] = st.inv_s[g] = st.bias[g][0] = st.bias[g][1] = 0.f;
+      st.inv[g][0] = st.inv[g][1] = st.bias[g][0] = st.bias[g][1] = 0.f;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -1138,7 +1164,7 @@ __global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o_s[warp][2 * c + (e & 1)][g * kC4Group + 4 * r + u + 32 * (e >> 1)] =
-              fmaf(st.o[g][u][e], st.top_s[g] * 0x1p-7f, st.bias[g][e & 1]);
+              fmaf(st.o[g][u][e], c4_unit(st.inv[g][e & 1]), st.bias[g][e & 1]);
     if (r == 0) {
       ml_s[warp][2 * c] = make_float2(st.ref[0] * kC4LogitUnit, st.l[0]);
       ml_s[warp][2 * c + 1] = make_float2(st.ref[1] * kC4LogitUnit, st.l[1]);

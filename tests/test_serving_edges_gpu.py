@@ -236,3 +236,43 @@ def test_a_drop_outlives_the_report_of_another_failure():
     assert attn.attn_watchdog_selftest(1_000_000) == attn.ATTN_ERR_TIMEOUT
     assert attn.attn_fwd_debug_status() == attn.ATTN_ERR_CAPACITY
     assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("n", [200, 1900, 9000])
+def test_attend_values_of_very_unlike_scales(n, order, D, dtype):
+    """Keys of little weight have the largest scales in V: what the heavy keys add has to keep its bits.
+
+    Half of the keys' scales are 2^e, e up to 48, at a weight of 4^-e; a second head gives the largest scales the largest
+    weights, 2^e.  The bound: p s is held in fp16 to 2^-36 of at most twice the largest p s of its head (subnormals),
+    times |c - 8| <= 8, on top of ref.decode's relative half step.
+    """
+    g = gen(n)
+    e = torch.randint(0, 49, (n,), generator=g, device="cuda").float()
+    e[torch.rand(n, generator=g, device="cuda") < 0.5] = 0
+    e[:3] = torch.tensor([48.0, 0.0, 24.0])
+    if order != "mixed":
+        e = e.sort(descending=order == "falling")[0]
+    c = attn.KVCache4.empty(1, 1, n, D)
+    code, s, m = ref.quantise(torch.randn((1, 1, n, D), generator=g, device="cuda").bfloat16())
+    c.v_codes.copy_(ref.pack(code))
+    c.v_meta.copy_(torch.stack([s, m], -1) * (2.0 ** e)[:, None, None])
+    c.k_codes.zero_()
+    c.k_meta.zero_()
+    c.k_meta[..., 1] = -e[:, None]  # every channel of key j is -e_j
+    c.length.fill_(n)
+    q = torch.zeros((1, 2, D), device="cuda")
+    q[0, 0, 0], q[0, 1, 0] = 2.0, -1.0
+    q = q.to(dtype)
+    o, lse = c.attend(q, scale=math.log(2))
+    ok()
+    ro, rlse, _, tol, lse_tol, _ = ref.decode(q, c, [n], math.log(2))
+    x = -e.double()[None] * torch.tensor([[2.0], [-1.0]], device="cuda", dtype=torch.float64) * math.log(2)
+    ps = (torch.softmax(x, 1)[..., None] * c.v_meta[0, 0, :, :, 0].double()[None]).amax(1)  # [head, group]
+    tol = tol + (n * 8 * 2.0 ** -35 * ps).repeat_interleave(64, 1)
+    keep = ro.abs() < 60000 if dtype == torch.float16 else torch.ones_like(ro, dtype=torch.bool)
+    bad = ((o.double() - ro).abs() > tol) & keep
+    assert not bad.any(), (int(bad.sum()), ((o.double() - ro).abs() / tol)[keep].max())
+    assert ((lse.double() - rlse).abs() <= lse_tol).all()
