@@ -310,7 +310,9 @@ uint64_t attn_fwd_varlen_workspace_bytes(int64_t total, int n_seqs, int H_q, int
  *   length            int32 [B]; calls clamp it to 0 .. capacity (or max_len)
  * D is 64 or 128.  Entries behind length[b] are never read.  The calls below check
  * their arguments before anything is launched, allocate nothing, and are
- * thread-safe; calls that write a cache must be ordered with those that use it.
+ * thread-safe; calls that write a cache must be ordered with those that use it, as
+ * whole calls: one may be several launches, and two threads on one stream may
+ * interleave theirs.
  */
 typedef struct {
   void* k_codes;

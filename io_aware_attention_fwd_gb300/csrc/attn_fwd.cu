@@ -1464,8 +1464,11 @@ bool encode_3d(CUtensorMap* m, const void* ptr, int D, int S, int64_t BH, int eb
 }
 
 // Every kernel of the library is launched with programmatic dependent launch:
-// it may begin while the previous kernel in the stream is finishing, and
-// waits (griddepcontrol.wait) before its first global memory access.
+// it may begin while the previous kernel in the stream is finishing, and every
+// thread of it waits (griddepcontrol.wait) before its first access to memory that
+// the kernels before it in the stream may still write or read.  Nearly always that
+// is its first access of all; attn_cache4_merge_kernel reads the cache's lengths
+// before (the reason is there).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args&&... args) {

@@ -1279,9 +1279,12 @@ __global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(c
   __shared__ float lse_s[128];
   __shared__ __align__(16) float o_s[kWarps][D];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  // The lengths are not the decode kernel's to write, and whatever wrote them was
-  // complete before that kernel let this one start (its blocks wait for it
-  // first): they are read while it finishes.
+  // The lengths are read before the wait, while the decode kernel finishes.  What
+  // wrote them is complete: this kernel starts when every kernel before it in the
+  // stream has started and let it, and the decode kernel of the same call is one of
+  // them, whose blocks let it only after their own wait.  That holds with launches
+  // of other threads in between, too; only a launch that writes these lengths may
+  // not come there, as nothing may that writes the cache during the call.
   int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
   const int64_t count = c4_total(p, sums_s, &mine_before, &mine);

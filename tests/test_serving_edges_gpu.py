@@ -276,3 +276,45 @@ def test_attend_values_of_very_unlike_scales(n, order, D, dtype):
     bad = ((o.double() - ro).abs() > tol) & keep
     assert not bad.any(), (int(bad.sum()), ((o.double() - ro).abs() / tol)[keep].max())
     assert ((lse.double() - rlse).abs() <= lse_tol).all()
+
+
+def filled(B, H, cap, D, n, seed):
+    """A cache whose first n entries of every row are random."""
+    c = attn.KVCache4.empty(B, H, cap, D)
+    x = torch.randn((2, B, H, n, D), generator=gen(seed), device="cuda")
+    for codes, meta, y in ((c.k_codes, c.k_meta, x[0]), (c.v_codes, c.v_meta, x[1])):
+        code, s, m = ref.quantise(y.bfloat16())
+        codes[:, :, :n] = ref.pack(code)
+        meta[:, :, :n] = torch.stack([s, m], -1).bfloat16()
+    c.weight[:, :, :n] = torch.rand((B, H, n), generator=gen(seed + 1), device="cuda")
+    c.pos[:, :, :n] = torch.arange(n, dtype=torch.int32, device="cuda")
+    c.length.fill_(n)
+    return c
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two threads, each on a cache of its own, whose launches may interleave on the stream they share."""
+    import threading
+
+    B, H, cap, D = 3, 2, 6000, 128
+    caches = [filled(B, H, cap, D, 5000, seed) for seed in (1, 2)]
+    q = torch.randn((B, 8, D), generator=gen(3), device="cuda").bfloat16()
+    caches[1].length.copy_(torch.tensor([5, 0, 4999], dtype=torch.int32))
+    want = [c.attend(q, weight_out=torch.zeros_like(c.weight)) for c in caches]
+    ok()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(40):
+            got[i].append(caches[i].attend(q, weight_out=torch.zeros_like(caches[i].weight)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    for i in range(2):
+        assert len(got[i]) == 40
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
