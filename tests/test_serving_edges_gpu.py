@@ -318,3 +318,72 @@ def test_two_threads_on_one_stream():
         assert len(got[i]) == 40
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+# --- offsets beyond 32 bits ------------------------------------------------------------------------------------------
+
+def test_cache_offsets_beyond_32_bits():
+    """More than 2^33 bytes of codes a buffer, so that the last sequence's lie beyond 2^31 four-byte words, too: append,
+    read, attention in one launch and in shares, with and without weights, and eviction, all on that sequence."""
+    B, H, cap, D, n = 18, 8, 1 << 20, 128, 5000
+    small = filled(1, H, n, D, n, seed=5)
+    c = attn.KVCache4.empty(B, H, cap, D)
+    last = B - 1
+    assert c.k_codes.stride(0) * last // 4 > 1 << 31 and c.k_codes.stride(0) * last > 1 << 32
+    names = ("k_codes", "k_meta", "v_codes", "v_meta", "weight", "pos")
+    lens = [3] + [0] * (B - 2) + [n]
+    for name in names:
+        getattr(c, name)[last, :, :n] = getattr(small, name)[0]
+        getattr(c, name)[0, :, :3] = getattr(small, name)[0, :, :3]
+    c.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    q = torch.randn((B, 16, D), generator=gen(1), device="cuda").bfloat16()
+    for held, max_len in ((n, None), (n, n), (200, 200)):  # the capacity's shares, the length's, one launch
+        if held < n:
+            small.length.fill_(held)
+        ro, rlse, rw, tol, lse_tol, w_tol = ref.decode(q[last:], small, [held], D ** -0.5)
+        for weight in (False, True):
+            out = torch.zeros_like(c.weight) if weight else None
+            o, lse = c.attend(q, weight_out=out, max_len=max_len)
+            ok()
+            assert ((o[last].double() - ro[0]).abs() <= tol[0]).all() and ((lse[last].double() - rlse[0]).abs() <= lse_tol[0]).all()
+            assert (o[1:last] == 0).all() and (lse[1:last] == -math.inf).all()
+            if weight:
+                err = (out[last, :, :held].double() - small.weight[0, :, :held].double() - rw[0, :, :held]).abs()
+                assert (err <= w_tol[0, :, :held] + 2.0 ** -23 * (small.weight[0, :, :held].double() + rw[0, :, :held])).all()
+                assert (out[last, :, held:] == 0).all()
+                del out
+    x = torch.randn((B, H, D), generator=gen(2), device="cuda").bfloat16()
+    c.append(x, x)
+    k, v = c.read(first_slot=torch.tensor(lens, dtype=torch.int32, device="cuda"), dtype=torch.float32)
+    ok()
+    code, s, m = ref.quantise(x)
+    want = ref.values(ref.pack(code), torch.stack([s, m], -1))
+    assert torch.equal(k.double(), want) and torch.equal(v.double(), want)
+    assert c.length.tolist() == [a + 1 for a in lens] and (c.pos[last, :, n] == n).all()
+    before = {name: getattr(c, name)[last, :, :n + 1].clone() for name in names}
+    budget, recent = 3000, 50
+    c.evict(budget, recent, max_len=n + 1)
+    ok()
+    assert c.length.tolist() == [min(a + 1, budget) for a in lens]
+    for h in range(H):
+        src = torch.tensor(ref.evict(before["weight"][h].tolist(), before["pos"][h].tolist(), n + 1, budget, recent), device="cuda")
+        for name in names:
+            assert torch.equal(getattr(c, name)[last, h, :budget], before[name][h, src]), name
+
+
+def test_prompt_offsets_beyond_32_bits():
+    """Rows that lie beyond 2^32 bytes and 2^31 elements of q, k, v and o."""
+    total, hq, hkv, d, lens = 1_200_000, 16, 1, 128, [37, 300]
+    first = total - sum(lens)
+    x = torch.empty((total, hq + 2 * hkv, d), dtype=torch.bfloat16, device="cuda")
+    x[first:] = torch.randn((sum(lens), hq + 2 * hkv, d), generator=gen(6), device="cuda").bfloat16()
+    out = torch.zeros((total, hq, d), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((hq, total), device="cuda")
+    assert first * hq * d > 1 << 31 and first * hq * d * 2 > 1 << 32
+    starts = torch.tensor([first, first + lens[0], total], dtype=torch.int32, device="cuda")
+    attn.attention_varlen(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], starts, out=out, lse=lse)
+    ok()
+    y = x[first:]
+    ro, rlse, tol, lse_tol = ref.varlen(y[:, :hq], y[:, hq:hq + hkv], y[:, hq + hkv:], [0, lens[0], sum(lens)], d ** -0.5, True)
+    assert ((out[first:].double() - ro).abs() <= tol).all() and ((lse[:, first:].double() - rlse).abs() <= lse_tol).all()
+    assert not out[:first].any() and not lse[:, :first].any()
