@@ -36,17 +36,28 @@ class KVCache4:
     """
 
     __slots__ = ("k_codes", "k_meta", "v_codes", "v_meta", "weight", "pos", "length", "B", "H_kv", "capacity", "D",
-                 "device", "_c")
+                 "device", "_c", "_layout")
 
     def __init__(self, k_codes, k_meta, v_codes, v_meta, weight, pos, length):
+        import torch
+
         if k_codes.dim() != 4 or not k_codes.is_cuda:
             raise ValueError("k_codes must be a CUDA tensor [B, H_kv, capacity, D // 2]")
         B, H_kv, capacity, half = k_codes.shape
-        if 2 * half % GROUP:
+        D, device = 2 * half, k_codes.device
+        if D % GROUP:
             raise ValueError(f"D must be a multiple of {GROUP}")
-        for name, value in (("B", B), ("H_kv", H_kv), ("capacity", capacity), ("D", 2 * half), ("device", k_codes.device),
-                            ("_c", _lib.attn_cache4_t(B=B, H_kv=H_kv, capacity=capacity, D=2 * half))):
-            object.__setattr__(self, name, value)
+        codes, meta, entry = (B, H_kv, capacity, half), (B, H_kv, capacity, D // GROUP, 2), (B, H_kv, capacity)
+        fixed = object.__setattr__
+        fixed(self, "B", B)
+        fixed(self, "H_kv", H_kv)
+        fixed(self, "capacity", capacity)
+        fixed(self, "D", D)
+        fixed(self, "device", device)
+        fixed(self, "_c", _lib.attn_cache4_t(B=B, H_kv=H_kv, capacity=capacity, D=D))
+        fixed(self, "_layout", {"k_codes": (codes, torch.uint8), "v_codes": (codes, torch.uint8),
+                                "k_meta": (meta, torch.bfloat16), "v_meta": (meta, torch.bfloat16),
+                                "weight": (entry, torch.float32), "pos": (entry, torch.int32), "length": ((B,), torch.int32)})
         self.k_codes, self.k_meta, self.v_codes, self.v_meta = k_codes, k_meta, v_codes, v_meta
         self.weight, self.pos, self.length = weight, pos, length
 
@@ -54,17 +65,12 @@ class KVCache4:
         """A buffer, checked; the struct that the calls pass on holds its address."""
         import torch
 
-        B, H_kv, capacity, D = self.B, self.H_kv, self.capacity, self.D
-        wanted = {"k_codes": ((B, H_kv, capacity, D // 2), torch.uint8), "v_codes": ((B, H_kv, capacity, D // 2), torch.uint8),
-                  "k_meta": ((B, H_kv, capacity, D // GROUP, 2), torch.bfloat16),
-                  "v_meta": ((B, H_kv, capacity, D // GROUP, 2), torch.bfloat16),
-                  "weight": ((B, H_kv, capacity), torch.float32), "pos": ((B, H_kv, capacity), torch.int32),
-                  "length": ((B,), torch.int32)}.get(name)
-        if wanted is None:
+        layout = self._layout.get(name)
+        if layout is None:
             raise AttributeError(f"a cache's {name} cannot be set")
         if not isinstance(value, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        check_out(value, *wanted, self.device, name)
+        check_out(value, *layout, self.device, name)
         object.__setattr__(self, name, value)
         setattr(self._c, name, value.data_ptr())
 
