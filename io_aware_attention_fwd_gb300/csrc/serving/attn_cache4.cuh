@@ -373,22 +373,26 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 // For a group of G query heads that share a key head,
 //     x_gj = scale * <q_g, k_j>,  O_g = sum_j softmax_j(x_g.) v_j.
 // With k_j = s c + m in each group of 64 channels, the codes go through the
-// tensor core as they are and the scales are applied to sums:
-//     <q, k_j>  = sum over groups of  s * <q, c> + m * sum q
+// tensor core, centred, and the scales are applied to sums:
+//     <q, k_j>  = sum over groups of  s * <q, c - 8> + (m + 8 s) * sum q
 //     sum_j p_j v_j = sum_j (p_j s) (c - 8) + sum_j p_j (m + 8 s).
 // The products run in fp16 with fp32 sums, whatever the type of q and o:
-//   * K's codes are masked out of a word and taken as they stand, as subnormals:
-//     c * 2^-24 and c * 2^-20, exact, one operation for two.  The products' unit
-//     goes into q and the logits.
-//   * V's are centred: its sums run over thousands of keys, and a mean code of
-//     7.5 would take bits from them.  A code is ORed into the mantissa of 1024: a
-//     low nibble gives 1024 + c, from which 1032 is subtracted; a high one, left
-//     where it is, gives 1024 + 16 c, which one fused multiply-add turns into
-//     c - 8.  So two nibbles of a 16-bit half need one mask and one operation
-//     each, and one shift serves four of the eight.
+//   * A code is ORed into the mantissa of 1024 (the conversion of 4-bit weights in
+//     Y. J. Kim et al., "Who says elephants can't run", 2022): a low nibble gives
+//     1024 + c, a high one, left where it is, 1024 + 16 c, and one fused
+//     multiply-add turns either into a multiple of c - 8.  So two nibbles of a
+//     16-bit half need one mask and one operation each, and one shift serves four
+//     of the eight.
+//   * Both are centred: a mean code of 7.5 would take bits from the sums.  And both
+//     are normal numbers, K's (c - 8) * 2^-14: the tensor core lines its products up
+//     by their exponents, and a subnormal's is that of the smallest normal number.
+//     K's codes taken as they stand in the word, c * 2^-24 and c * 2^-20, need no
+//     such operation (1 sequence of 131072 entries 36.5 us instead of 38.2, 64 of up
+//     to 16000 with weights 131.1 instead of 133.0), but the logits then lost 3 to
+//     4 bits against fp32 products; as it is they are as exact as those.
 //   * q is scaled by a power of two that brings its head's largest channel to
-//     2^10 .. 2^11, which fp16 holds exactly down to 2^-24 of it and to 2^-35 of
-//     it absolutely; the scale goes back into the logits.
+//     2^4 .. 2^5, which fp16 holds to its 11 bits down to 2^-18 of it and to 2^-29
+//     of it absolutely; the scale goes back into the logits.
 //   * p s is held relative to a power of two T at or above every p s of that head
 //     and group of channels when it was set, times 2^11: a tile that brings more
 //     than 2^15 sets it anew, and O is rescaled, as it is when the running maximum
@@ -569,15 +573,19 @@ __device__ __forceinline__ void mma_16816_zero(float* d, uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Codes as fp16 numbers, for K: masked out of a word they are c * 2^-24 (low
-// nibbles of both 16-bit halves' low bytes) and c * 2^-20 (high nibbles), subnormal
-// and exact, with nothing to subtract or scale.
-__device__ __forceinline__ uint32_t c4_tiny_low(uint32_t w) { return w & 0x000f000fu; }
-__device__ __forceinline__ uint32_t c4_tiny_high(uint32_t w) { return w & 0x00f000f0u; }
-
-// For V, whose sums run over many tiles and would lose what a mean code of 7.5 adds
-// to them: c - 8 of the low nibbles of both 16-bit halves' low bytes, and of the high
-// nibbles: exact.
+// Codes as fp16 numbers.  K's: (c - 8) * 2^-14 of the low nibbles of both 16-bit
+// halves' low bytes, and of the high nibbles: exact, and normal numbers.
+__device__ __forceinline__ uint32_t c4_key_low(uint32_t w) {  // (1024 + c) 2^-14 - 1032 * 2^-14
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(and_or(w, 0x000f000fu, 0x64006400u)), "r"(0x04000400u), "r"(0xac08ac08u));
+  return r;
+}
+__device__ __forceinline__ uint32_t c4_key_high(uint32_t w) {  // (1024 + 16 c) 2^-18 - 72 * 2^-14
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(and_or(w, 0x00f000f0u, 0x64006400u)), "r"(0x00400040u), "r"(0x9c809c80u));
+  return r;
+}
+// V's: c - 8 of the same nibbles: exact.
 __device__ __forceinline__ uint32_t c4_low(uint32_t w) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or(w, 0x000f000fu, 0x64006400u)), "r"(0x64086408u));
@@ -728,12 +736,6 @@ __device__ __forceinline__ void c4_load_meta(uint32_t (*sm)[D / kC4Group], uint3
   }
 }
 
-__device__ __forceinline__ uint32_t times16_f16x2(uint32_t x) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x4c004c00u));
-  return r;
-}
-
 // A tile's logits, and what is compared with them, are log2 units over this: so
 // they come out of the MMAs, and the multiplication joins the subtraction in the
 // exponent.
@@ -743,7 +745,7 @@ constexpr float kC4LogitUnit = 1024.f;
 template <int D>
 struct C4Query {
   static constexpr int kGroups = D / kC4Group;
-  uint32_t q[kGroups][4][2];  // head r, in the channel order of the K words; [0] times 16 (low nibbles)
+  uint32_t q[kGroups][4][2];  // head r, in the channel order of the K words
   float sum[kGroups][2];      // of heads 2c, 2c + 1, over a group's channels, in the units of the MMAs' sums
   float scale[2];             // logits of heads 2c, 2c + 1, in units of kC4LogitUnit
 };
@@ -761,8 +763,7 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
       if (there) x = __ldg(reinterpret_cast<const uint4*>(qr + g * kC4Group + w * 32 + c * 8));
       raw[g][4 * w] = x.x, raw[g][4 * w + 1] = x.y, raw[g][4 * w + 2] = x.z, raw[g][4 * w + 3] = x.w;
     }
-  // A head's q in fp16, times 2^10 / 2^E for its largest in [2^E, 2^(E+1)): 16 q
-  // is finite too.
+  // A head's q in fp16, times 2^4 / 2^E for its largest in [2^E, 2^(E+1)).
   float top = 0.f;
 #pragma unroll
   for (int g = 0; g < kG; ++g)
@@ -776,7 +777,7 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
   // 2^-E within 2^-126 .. 2^100; 1 for 0, and for infinity, which stays one
   const int e = static_cast<int>(__float_as_uint(top) >> 23);
   const int f = top == 0.f || e == 255 ? 127 : min(max(254 - e, 1), 227);
-  const float fwd = __uint_as_float(static_cast<uint32_t>(f + 10) << 23);
+  const float fwd = __uint_as_float(static_cast<uint32_t>(f + 4) << 23);
   const float back = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
 #pragma unroll
   for (int g = 0; g < kG; ++g)
@@ -797,7 +798,7 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    sum *= 0x1p-20f;  // the MMAs' sums: 2^10 q times c * 2^-20, or 2^14 q times c * 2^-24
+    sum *= 0x1p-14f;  // the MMAs' sums: 2^4 q times (c - 8) * 2^-14
     t.sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
     t.sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
     // nibbles e and e + 4 of a word meet in one register: channels (0, 4),
@@ -805,9 +806,9 @@ __device__ __forceinline__ void c4_load_query(C4Query<D>& t, const uint16_t* row
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const uint32_t* e = raw[g] + 4 * w;
-      t.q[g][2 * w][0] = times16_f16x2(__byte_perm(e[0], e[2], 0x5410));
+      t.q[g][2 * w][0] = __byte_perm(e[0], e[2], 0x5410);
       t.q[g][2 * w][1] = __byte_perm(e[0], e[2], 0x7632);
-      t.q[g][2 * w + 1][0] = times16_f16x2(__byte_perm(e[1], e[3], 0x5410));
+      t.q[g][2 * w + 1][0] = __byte_perm(e[1], e[3], 0x5410);
       t.q[g][2 * w + 1][1] = __byte_perm(e[1], e[3], 0x7632);
     }
   }
@@ -846,15 +847,15 @@ __device__ __forceinline__ void c4_scores(float* xs, const C4Lane<D>& p, uint32_
     uint32_t w[4];
     ldmatrix_x4(w, p.codes[g] + stage);
     float d[4];
-    mma_16816_zero(d, c4_tiny_low(w[0]), c4_tiny_low(w[1]), c4_tiny_high(w[0]), c4_tiny_high(w[1]), q.q[g][0][0], q.q[g][0][1]);
-    mma_16816(d, c4_tiny_low(w[0] >> 8), c4_tiny_low(w[1] >> 8), c4_tiny_high(w[0] >> 8), c4_tiny_high(w[1] >> 8), q.q[g][1][0],
+    mma_16816_zero(d, c4_key_low(w[0]), c4_key_low(w[1]), c4_key_high(w[0]), c4_key_high(w[1]), q.q[g][0][0], q.q[g][0][1]);
+    mma_16816(d, c4_key_low(w[0] >> 8), c4_key_low(w[1] >> 8), c4_key_high(w[0] >> 8), c4_key_high(w[1] >> 8), q.q[g][1][0],
               q.q[g][1][1]);
-    mma_16816(d, c4_tiny_low(w[2]), c4_tiny_low(w[3]), c4_tiny_high(w[2]), c4_tiny_high(w[3]), q.q[g][2][0], q.q[g][2][1]);
-    mma_16816(d, c4_tiny_low(w[2] >> 8), c4_tiny_low(w[3] >> 8), c4_tiny_high(w[2] >> 8), c4_tiny_high(w[3] >> 8), q.q[g][3][0],
+    mma_16816(d, c4_key_low(w[2]), c4_key_low(w[3]), c4_key_high(w[2]), c4_key_high(w[3]), q.q[g][2][0], q.q[g][2][1]);
+    mma_16816(d, c4_key_low(w[2] >> 8), c4_key_low(w[3] >> 8), c4_key_high(w[2] >> 8), c4_key_high(w[3] >> 8), q.q[g][3][0],
               q.q[g][3][1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float s = bf16_lo(sm[i][g]), m = bf16_hi(sm[i][g]);
+      const float s = bf16_lo(sm[i][g]), m = fmaf(8.f, s, bf16_hi(sm[i][g]));
       xs[2 * i] = fmaf(s, d[2 * i], fmaf(m, q.sum[g][0], xs[2 * i]));
       xs[2 * i + 1] = fmaf(s, d[2 * i + 1], fmaf(m, q.sum[g][1], xs[2 * i + 1]));
     }
