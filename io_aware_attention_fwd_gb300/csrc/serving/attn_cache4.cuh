@@ -419,29 +419,36 @@ __global__ void __launch_bounds__(kC4RowsThreads)
 // kC4DirectLen a CTA takes a whole row instead and writes O and LSE itself, and
 // the weights where the row has all the heads of its key head: one launch, and
 // without weights no workspace.  (One sequence of 701 entries, 16 heads, D = 64:
-// 4.2 us on the GPU instead of 7.7, and 13 us on the host instead of 20.)
+// 4.3 us on the GPU instead of 7.7, and 13 us on the host instead of 20.)
 
 constexpr int kC4DecThreads = 128;  // 4 warps
 constexpr int kC4TileKeys = 64;     // keys of a tile: 16 a warp
 constexpr int kC4Heads = 8;         // query heads of a block (N of the MMA)
 // Three CTAs an SM give a thread 168 registers, room for two tiles' chains of
-// instructions side by side; with four (128, spills) it took 142 us instead of
-// 137 at 64 sequences of up to 16000 entries with weights, and 41.5 instead of
-// 37.6 at one of 131072.
+// instructions side by side; with four (128, spills) it takes 145 us instead of
+// 133 at 64 sequences of up to 16000 entries with weights, and 44.6 instead of
+// 38.3 at one of 131072.  At D = 64, where a CTA takes a whole row, 128 registers
+// do without spills, and four let more of the next call's rows start early (16
+// sequences of 16 key heads, up to 1024 entries, with weights: 10.0 -> 7.9 us).
 constexpr int kC4DecCtasPerSm = 3;
 // Longest caches for which a CTA takes a whole row.  GPU time per call, that way
 // against shares (us; lengths from half to all of the capacity; 1 sequence of 8 key
 // heads, D = 128 | 64 of them | 16 of 16, D = 64):
-//   1024           6.8 / 7.6   | 17.4 / 22.1 | 6.1 / 10.7
-//   2048           9.9 / 7.8   | 31.7 / 32.4 | 9.8 / 13.5
-//   4096          11.7 / 10.3  | 57.1 / 50.2 | 17.4 / 17.7
-//   1024, weights  9.4 / 8.4   | 21.9 / 25.5 | 7.3 / 13.3
-//   2048, weights 14.7 / 10.1  | 42.0 / 38.6 | 11.9 / 16.2
-//   4096, weights 24.7 / 11.4  | 81.3 / 62.6 | 21.3 / 22.1
-// Shares take the host 4 us longer (a second launch, a workspace), which a call
-// outside a graph waits for where the GPU needs less than 15: so 2048, not 1024.
+//   1024           7.3 / 7.8   | 19.6 / 23.5 | 6.5 / 11.4
+//   2048          10.7 / 8.0   | 34.7 / 34.9 | 10.5 / 14.4
+//   4096          12.5 / 10.6  | 61.0 / 53.8 | 19.0 / 19.0
+//   1024, weights  9.9 / 8.8   | 22.6 / 28.2 | 8.0 / 13.9
+//   2048, weights 15.3 / 10.3  | 43.5 / 41.4 | 13.4 / 17.1
+//   4096, weights 25.4 / 12.2  | 83.9 / 65.8 | 23.5 / 23.0
+// On the GPU alone the border would lie lower for few rows, which leave most SMs
+// idle (2048 entries of one sequence with weights: 5 us).  Shares take the host 4 us
+// longer (a second launch, a workspace), and a call outside a graph waits for the
+// host where the GPU needs less than 15: so 2048, whatever the rows.
 constexpr int kC4DirectLen = 2048;
-constexpr int kC4RowCost = 6;       // tiles' worth of time that a row costs a CTA
+// Tiles' worth of time that a row costs a CTA.  1 sequence of 131072 | 32 of up to
+// 4001 with weights | 64 of up to 16000 with weights: 38.3 | 29.9 | 132.8 us; with 3
+// 37.4 | 31.6 | 137.0, with 12 38.4 | 31.9 | 134.1.
+constexpr int kC4RowCost = 6;
 // A GB300's SMs.  Workspaces are sized, and their use laid out, by this count,
 // so that a size asked for on one device (or with none) holds on any.
 constexpr int kC4WorkspaceSms = 152;
@@ -1033,7 +1040,7 @@ __device__ __forceinline__ void c4_add_weights(const DecParams& p, int b, int h,
 // kDirect: CTA x takes the whole of row x (with weights: one block of heads a
 // key head, so the row has all of an entry's weight).
 template <int D, int kType, bool kWeight, bool kDirect>
-__global__ void __launch_bounds__(kC4DecThreads, kC4DecCtasPerSm)
+__global__ void __launch_bounds__(kC4DecThreads, D == 64 && kDirect ? 4 : kC4DecCtasPerSm)
     attn_cache4_decode_kernel(const DecParams p) {
   constexpr int kG = D / kC4Group;
   constexpr int kWarps = kC4DecThreads / 32;
@@ -1229,7 +1236,9 @@ struct DecMergeParams {
 
 constexpr int kC4MergeThreads = 256;
 constexpr int kC4MergeTiles = 16;  // tiles of weights a block takes at once: 16 threads a tile, 4 keys each
-constexpr int kC4MergeRowCost = 24;  // tiles' worth of time that a row costs a block
+// Tiles' worth of time that a row costs a block that adds weights (the same calls with
+// weights: 29.9 | 132.8 us; with 12 30.3 | 134.3, with 48 30.2 | 134.0).
+constexpr int kC4MergeRowCost = 24;
 
 // The CTAs that hold a segment of a row whose units begin at `start` of the list.
 struct C4Parts {
