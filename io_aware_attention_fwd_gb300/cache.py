@@ -172,7 +172,8 @@ class KVCache4:
         weight_out: where not None, the entries' weights plus what this token gave
         each, summed over the query heads of its key head; pass ``cache.weight`` to
         add in place.  max_len: a bound on the lengths, which are clamped to it
-        (None: the capacity); it sizes the workspace.  Returns (o, lse): o
+        (None: the capacity); it sizes the workspace and picks the kernel, so a
+        close one pays where the capacity is much larger than what is held.  Returns (o, lse): o
         [B, H_q, D] of q's type, lse fp32 [B, H_q]; 0 and -inf for a sequence
         without entries.
         """
@@ -215,7 +216,7 @@ class KVCache4:
         those of the highest weight (ties: the lower slot).  Kept entries from
         behind the budget move into the slots that became free; attention does not
         depend on the entries' order.  max_len: as attend takes it, at most 393216
-        (or the budget); entries behind it are dropped.
+        (or the budget); entries behind it are dropped, and it picks the kernel.
         """
         import torch
 

@@ -613,8 +613,8 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
 
 // A warp's 16 keys of a tile travel through a ring of shared-memory stages of
 // its own, filled by asynchronous copies: four stages, and 12 warps an SM, are up
-// to 110 KB in flight.  Loads into registers kept some 40 KB there and took 192 us
-// instead of 161 (64 sequences of up to 16000 entries, one tile a step).
+// to 110 KB in flight.  Loads into registers kept some 40 KB there and took a fifth
+// longer (64 sequences of up to 16000 entries, one tile a step).
 // A stage is K codes, V codes, K meta, V meta, row by row.  The 16-byte pieces of
 // a row are swapped so that eight rows' pieces of one number, which ldmatrix reads
 // at once, lie in different banks: a row has 4 pieces (D = 128) or 2, and 8 fill
@@ -1274,9 +1274,9 @@ __device__ __forceinline__ float2 c4_join_stats(const float2* ml, int count, int
 // the scores were kept.  `m.warps` (1, 2, 4, 8) warps share a row's partials,
 // four of them in flight each: with one warp, the 77 partials of a row of
 // 131072 keys took 33 us, most of it waiting for memory.  The first four are
-// fetched while the statistics are joined (that call: 37.6 -> 36.4 us), and four
+// fetched while the statistics are joined (that call: 1.2 us less), and four
 // blocks an SM hold 64 registers a thread (64 sequences of up to 16000 with
-// weights: 132.8 us with 75, 130.4 with 64).
+// weights: 2.4 us less than with 75).
 template <int D, int kType, bool kWeight>
 __global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(const DecMergeParams m) {
   constexpr int kWarps = kC4MergeThreads / 32;
@@ -1300,7 +1300,7 @@ __global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(c
   const int64_t count = c4_total(p, sums_s, &mine_before, &mine);
   // Weights: the tiles of every (sequence, key head) in equal contiguous
   // shares, one for each of the first blocks, walked row by row.  The share's
-  // first row is found now, too (32 sequences of up to 4001: 31.5 -> 30.9 us).
+  // first row is found now, too (32 sequences of up to 4001: 0.6 us less).
   C4Walk w;
   w.x = w.end = 0;
   if (kWeight && blockIdx.x < m.weight_blocks) {
@@ -1929,8 +1929,8 @@ attn_status_t launch_decode(DecMergeParams m, int sms, cudaStream_t stream) {
   const int64_t tiles = (static_cast<int64_t>(m.d.most) + kC4TileKeys - 1) / kC4TileKeys * m.d.B * m.d.c.H;
   // Three blocks an SM for the weights, of the four that fit: a block's set-up is
   // some 700 instructions a warp, ten times a tile's.  (32 sequences of up to 4001
-  // 27.8 us, 64 of up to 16000 133.2; with four 28.2 and 133.7, with eight behind
-  // the rows' blocks 30.8 and 136.8.)
+  // and 64 of up to 16000: with four 0.4 and 0.5 us more, with eight behind the
+  // rows' blocks 3.0 and 3.6.)
   const int64_t row_blocks = std::min<int64_t>(m.d.B * ((static_cast<int64_t>(m.d.c.H) * m.d.G + rows - 1) / rows),
                                                static_cast<int64_t>(sms) * 4);
   m.weight_blocks =
