@@ -989,7 +989,7 @@ __device__ __forceinline__ void c4_step(C4State<D>& st, const C4Lane<D>& p, cons
         for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
         const float old = c4_unit(st.inv[g][e]) * 0x1p-5f * a[e];
         const uint32_t up = max((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u, __float_as_uint(old) & 0x7f800000u);
-        const uint32_t to = min(max(up, 17u << 23), 247u << 23);
+        const uint32_t to = min(max(up, 1u << 23), 247u << 23);  // inv within 2^-125 .. 2^121
         const float f = old * __uint_as_float((254u << 23) - to);
         st.inv[g][e] = __uint_as_float((249u << 23) - to);  // 2^-5 / to: 2^11 / T
         st.bias[g][e] *= a[e];

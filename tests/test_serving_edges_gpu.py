@@ -408,3 +408,35 @@ def test_attend_logits_are_as_exact_as_fp32_products(D, dtype, ratio):
     plain = (q.float() @ k.float()[:, :, None])[..., 0]
     off = [((x.double() - want) / reach).square().mean().sqrt() for x in (lse, plain)]
     assert off[0] <= 3 * off[1], off
+
+
+@pytest.mark.parametrize("power", [-100, -40, 40, 100])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1000, 5000])
+def test_attend_values_times_a_power_of_two(n, D, power):
+    """Every step is exact in powers of two, so V times 2^power gives O times 2^power, bit by bit."""
+    c = filled(2, 2, n, D, n, seed=13)
+    q = 3 * torch.randn((2, 6, D), generator=gen(14), device="cuda").bfloat16()
+    o, lse = c.attend(q)
+    c.v_meta = c.v_meta * 2.0 ** power
+    o2, lse2 = c.attend(q)
+    ok()
+    assert torch.equal(lse, lse2) and torch.equal(o.double() * 2.0 ** power, o2.double())
+
+
+def test_attend_nan_values_stay_in_their_channels():
+    """An entry whose V is not finite in one group of channels: those channels alone; in K: the heads that see it."""
+    for n in (100, 5000):
+        c = filled(2, 2, n, 128, n, seed=15)
+        q = torch.randn((2, 8, 128), generator=gen(16), device="cuda").bfloat16()
+        good, lse = c.attend(q)
+        c.v_meta[1, 0, n // 2, 1] = math.nan
+        o, z = c.attend(q)
+        ok()
+        assert o[1, :4, 64:].isnan().all() and torch.equal(z, lse)
+        assert torch.equal(o[1, :4, :64], good[1, :4, :64]) and torch.equal(o[1, 4:], good[1, 4:]) and torch.equal(o[0], good[0])
+        c.v_meta[1, 0, n // 2, 1] = 1.0
+        c.k_meta[0, 1, 3, 0] = math.nan
+        o, z = c.attend(q)
+        ok()
+        assert o[0, 4:].isnan().all() and z[0, 4:].isnan().all() and torch.equal(o[0, :4], good[0, :4]) and torch.equal(z[1], lse[1])
