@@ -48,7 +48,8 @@ typedef enum {
   ATTN_ERR_LAUNCH = 4,       /* the CUDA launch (or tensor-map encoding) failed */
   ATTN_ERR_TIMEOUT = 5,      /* a bounded in-kernel wait gave up (see attn_fwd_debug_status) */
   ATTN_ERR_DEVICE = 6,       /* CUDA runtime / driver error outside the launch */
-  ATTN_ERR_CAPACITY = 7      /* an append dropped entries (see attn_cache4_append) */
+  ATTN_ERR_CAPACITY = 7,     /* an append dropped entries (see attn_cache4_append) */
+  ATTN_ERR_PAGE = 8          /* a page table named no page (see attn_pages_t) */
 } attn_status_t;
 
 /*
@@ -424,6 +425,144 @@ attn_status_t attn_cache4_evict(const attn_cache4_t* cache, int budget, int rece
 /* Workspace bytes attn_cache4_evict needs (0 for invalid arguments). */
 uint64_t attn_cache4_evict_workspace_bytes(int B, int H_kv, int max_len, int budget);
 
+/*
+ * attn_heads_t -- rows of heads: head h of row s of batch b is D elements at
+ * ptr + b * batch_stride + s * row_stride + h * head_stride (strides in elements,
+ * multiples of 8; ptr 16-byte aligned).  So both [B][S][H][D], slices of a fused
+ * projection's rows among them, and the [B][H][S][D] of attn_fwd can be named.
+ */
+typedef struct {
+  void* ptr;
+  int64_t batch_stride;
+  int64_t row_stride;
+  int64_t head_stride;
+} attn_heads_t;
+
+/*
+ * attn_rotary_t -- a rotation by position.
+ *   turns        device int64[rot / 2], 8-byte aligned: radians a position of pair
+ *                i as a fraction of a turn, f_i / (2 pi) * 2^64 modulo 2^64; angles
+ *                are then exact for every position.  May be NULL where rot is 0.
+ *   rot          channels of a head that are turned, its first ones: a multiple
+ *                of 16, 0 .. D.
+ *   interleaved  0: pair i is channels (i, i + rot / 2); 1: (2i, 2i + 1).
+ *   amplitude    factor on the turned channels (finite; 1 for a pure rotation).
+ */
+typedef struct {
+  const int64_t* turns;
+  int rot;
+  int interleaved;
+  float amplitude;
+} attn_rotary_t;
+
+/*
+ * attn_qk_norm_rope -- the norm of every query and key head and the rotation by
+ * its row's position:
+ *     y = x / sqrt(mean(x^2) + eps) * weight,
+ *     (a, b) -> amplitude * (a cos t - b sin t, a sin t + b cos t), t = position * f_i
+ * for the pairs of y's first rot channels.  fp32 throughout, rounded once.
+ *
+ *   q, k             bf16 or fp16 (dtype), H_q and H_k heads of D elements in each
+ *                    of B * S rows.  q_out, k_out the same, written; each may be
+ *                    its input (same pointer and strides), else nothing overlaps.
+ *   rope             NULL: no rotation.
+ *   positions        device int32 [B][S]; may be NULL without a rotation.  Any
+ *                    int will do.
+ *   q_weight, k_weight
+ *                    device [D], of weight_dtype: dtype, or ATTN_FP32.  NULL: no
+ *                    norm of q or k.
+ *   eps              finite, 0 or more.
+ * D is 64 or 128; H_q, H_k 1 .. 65535; B * S 0 .. 2^31 - 1.  Asynchronous (one
+ * launch); argument errors are reported before anything is launched.
+ */
+attn_status_t attn_qk_norm_rope(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* q_out,
+                                const attn_heads_t* k_out, int B, int S, int H_q, int H_k, int D, int dtype,
+                                const attn_rotary_t* rope, const int32_t* positions, const void* q_weight,
+                                const void* k_weight, int weight_dtype, float eps, void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd -- its gradient: of q and k, and of the weights (summed
+ * over all rows and heads).
+ *   dq_out, dk_out   gradients of attn_qk_norm_rope's results.
+ *   q, k             its inputs; NULL will do where there is no norm.
+ *   dq, dk           written; each may be dq_out or dk_out (same pointer and
+ *                    strides).
+ *   dq_weight, dk_weight
+ *                    fp32 [D], written; NULL exactly where the weight is.
+ *   workspace        at least attn_qk_norm_rope_bwd_workspace_bytes(...) bytes,
+ *                    16-byte aligned; overwritten.  May be NULL without a norm.
+ *                    Calls that share one must be ordered.
+ * Results are the same from call to call.  Asynchronous (one or two launches).
+ */
+attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads_t* dk_out, const attn_heads_t* q,
+                                    const attn_heads_t* k, const attn_heads_t* dq, const attn_heads_t* dk, int B, int S,
+                                    int H_q, int H_k, int D, int dtype, const attn_rotary_t* rope,
+                                    const int32_t* positions, const void* q_weight, const void* k_weight,
+                                    int weight_dtype, float eps, float* dq_weight, float* dk_weight, void* workspace,
+                                    uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_qk_norm_rope_bwd needs with a norm (0 for invalid arguments). */
+uint64_t attn_qk_norm_rope_bwd_workspace_bytes(int B, int S, int H_q, int H_k, int D);
+
+/*
+ * attn_pages_t -- a K/V cache in pages.  Every buffer is the caller's, in device
+ * memory; the host reads only this struct.
+ *
+ *   Entry j of sequence b is row j % page of page page_table[b][j / page], and
+ *   the cache of sequence b is its first length[b] entries.
+ *
+ *   k_pages, v_pages  bf16 or fp16 (dtype) [n_pages][H_kv][page][D], 16-byte aligned
+ *   page_table        int32 [B][max_pages]; what lies behind the entries that a
+ *                     call needs is not read.  An entry's place that names no page
+ *                     (below 0, or n_pages or more): an append drops the entry, an
+ *                     attention takes K and V as zeros there, and
+ *                     attn_fwd_debug_status reports ATTN_ERR_PAGE for the device.
+ *   length            int32 [B]; calls clamp it to 0 .. max_pages * page (or max_len)
+ *   page              16, 32, 64, 128 or 256
+ * D is 64 or 128.  Sequences may share pages that neither writes.  The calls below
+ * check their arguments before anything is launched, allocate nothing, and are
+ * thread-safe; calls that write a cache must be ordered with those that use it.
+ */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  const int32_t* page_table;
+  int32_t* length;
+  int B;
+  int H_kv;
+  int D;
+  int page;
+  int n_pages;
+  int max_pages;
+  int dtype;
+} attn_pages_t;
+
+/*
+ * attn_paged_append -- write new rows of K and V into the next entries: row i of
+ * sequence b becomes its entry length[b] + i, whose number is its position.
+ *
+ *   k, v        the cache's type: row t is H_kv heads of D elements at
+ *               k + t * k_stride; 16-byte aligned, strides multiples of 8.
+ *   seq_start   device int32[B + 1] as attn_fwd_varlen takes it; rows behind the
+ *               last sequence are left out.  NULL: one row for each (rows = B).
+ *   q, q_out    NULL, or the tokens' queries, H_q heads of D elements at
+ *               q + t * q_stride, and [rows][H_q][D] for what becomes of them
+ *               (another buffer); rows of no sequence are left as they were.
+ *   rope, q_weight, k_weight, weight_dtype, eps
+ *               as attn_qk_norm_rope: q and k are normed and turned by their
+ *               positions on the way, v is written as it is.
+ *   length_out  device int32[B], written: the lengths after the call.  It may be
+ *               cache->length (one more small launch).
+ * Rows for which there is no room are dropped, the length stays at the capacity
+ * (max_pages * page), and attn_fwd_debug_status reports ATTN_ERR_CAPACITY; their
+ * queries are still written.  No two sequences may write one page.  Asynchronous.
+ */
+attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const void* v, int64_t rows,
+                                int64_t k_stride, int64_t v_stride, const int32_t* seq_start, const void* q,
+                                int64_t q_stride, void* q_out, int H_q, const attn_rotary_t* rope,
+                                const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                                int32_t* length_out, void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* attn_status_str(attn_status_t status);
 
@@ -431,12 +570,13 @@ const char* attn_status_str(attn_status_t status);
  * attn_fwd_debug_status -- synchronise `stream`, then read and clear the
  * device status word that the kernels set when a bounded wait gives up.
  * Returns ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_CAPACITY if an append dropped
- * entries (attn_cache4_append), or ATTN_ERR_DEVICE if the
+ * entries (attn_cache4_append, attn_paged_append), ATTN_ERR_PAGE if an entry's
+ * place in a page table named no page (attn_pages_t), or ATTN_ERR_DEVICE if the
  * synchronisation itself reported a CUDA error or the backward kernel found
  * its dynamic shared memory off a 1024-byte boundary (it then runs nothing).
  * There is one word a device: it says that some call since the last reading
- * failed so, on whatever stream.  A drop beside another failure is reported by
- * the next reading.
+ * failed so, on whatever stream.  A drop or a missing page beside another failure
+ * is reported by the next reading.
  */
 attn_status_t attn_fwd_debug_status(void* stream);
 

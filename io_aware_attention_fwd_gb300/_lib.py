@@ -20,6 +20,7 @@ ATTN_ERR_LAUNCH = 4
 ATTN_ERR_TIMEOUT = 5
 ATTN_ERR_DEVICE = 6
 ATTN_ERR_CAPACITY = 7
+ATTN_ERR_PAGE = 8
 
 # attn_dtype_t
 ATTN_BF16 = 0
@@ -31,7 +32,8 @@ EXPORTED = ("attn_fwd", "attn_fwd_fp8", "attn_bwd", "attn_bwd_workspace_bytes", 
             "attn_fwd_splitkv_suggest", "attn_fwd_schedule", "attn_merge", "attn_fwd_splitkv_static", "attn_status_str", "attn_fwd_debug_status",
             "attn_watchdog_selftest", "attn_fwd_abi_version", "attn_fwd_varlen", "attn_fwd_varlen_workspace_bytes",
             "attn_cache4_append", "attn_cache4_read", "attn_cache4_decode", "attn_cache4_decode_workspace_bytes",
-            "attn_cache4_evict", "attn_cache4_evict_workspace_bytes")
+            "attn_cache4_evict", "attn_cache4_evict_workspace_bytes", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
+            "attn_qk_norm_rope_bwd_workspace_bytes", "attn_paged_append")
 
 _lock = threading.Lock()
 _lib = None
@@ -57,6 +59,36 @@ class attn_cache4_t(ctypes.Structure):
     def __setattr__(self, name, value):
         if name in ("B", "H_kv", "capacity", "D") and not _int32(value):
             raise OverflowError(f"attn_cache4_t.{name}: {value} does not fit an int")
+        super().__setattr__(name, value)
+
+
+class attn_heads_t(ctypes.Structure):
+    """The struct of the same name: rows of heads and their strides."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class attn_rotary_t(ctypes.Structure):
+    """The struct of the same name: a rotation by position."""
+
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float)]
+
+
+class attn_pages_t(ctypes.Structure):
+    """The struct of the same name: a paged K/V cache's buffers and sizes."""
+
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("length", ctypes.c_void_p), ("B", ctypes.c_int), ("H_kv", ctypes.c_int), ("D", ctypes.c_int),
+                ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+    def __init__(self, *args, **kw):
+        for name, value in (*zip((f[0] for f in self._fields_), args), *kw.items()):
+            setattr(self, name, value)
+
+    def __setattr__(self, name, value):
+        if name in ("B", "H_kv", "D", "page", "n_pages", "max_pages", "dtype") and not _int32(value):
+            raise OverflowError(f"attn_pages_t.{name}: {value} does not fit an int")
         super().__setattr__(name, value)
 
 
@@ -120,6 +152,15 @@ def load() -> ctypes.CDLL:
             lib.attn_cache4_evict.argtypes = [c4, i, i, i, p, p, p, p, u64, p]
             lib.attn_cache4_evict_workspace_bytes.restype = u64
             lib.attn_cache4_evict_workspace_bytes.argtypes = [i, i, i, i]
+            hp, rp, pp = (ctypes.POINTER(x) for x in (attn_heads_t, attn_rotary_t, attn_pages_t))
+            lib.attn_qk_norm_rope.restype = i
+            lib.attn_qk_norm_rope.argtypes = [hp, hp, hp, hp, i, i, i, i, i, i, rp, p, p, p, i, f, p]
+            lib.attn_qk_norm_rope_bwd.restype = i
+            lib.attn_qk_norm_rope_bwd.argtypes = [hp, hp, hp, hp, hp, hp, i, i, i, i, i, i, rp, p, p, p, i, f, p, p, p, u64, p]
+            lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = u64
+            lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, i, i, i]
+            lib.attn_paged_append.restype = i
+            lib.attn_paged_append.argtypes = [pp, p, p, i64, i64, i64, p, p, i64, p, i, rp, p, p, i, f, p, p]
             lib.attn_status_str.restype = ctypes.c_char_p
             lib.attn_status_str.argtypes = [i]
             lib.attn_fwd_debug_status.restype = i
@@ -329,6 +370,47 @@ def attn_cache4_evict(cache: attn_cache4_t, budget: int, recent: int, max_len: i
 @functools.lru_cache(maxsize=256)
 def attn_cache4_evict_workspace_bytes(B: int, H_kv: int, max_len: int, budget: int) -> int:
     return load().attn_cache4_evict_workspace_bytes(B, H_kv, max_len, budget) if _int32(B, H_kv, max_len, budget) else 0
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, B: int, S: int, H_q: int, H_k: int, D: int, dtype: int, rope, positions, q_weight,
+                      k_weight, weight_dtype: int, eps: float, stream=None) -> None:
+    """Enqueue the head norm and rotation (see include/attn_fwd.h)."""
+    if not _int32(B, S, H_q, H_k, D, dtype, weight_dtype):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_qk_norm_rope")
+    st = load().attn_qk_norm_rope(q, k, q_out, k_out, B, S, H_q, H_k, D, dtype, rope, _addr(positions), _addr(q_weight),
+                                  _addr(k_weight), weight_dtype, eps, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_qk_norm_rope")
+
+
+def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, B: int, S: int, H_q: int, H_k: int, D: int, dtype: int, rope, positions,
+                          q_weight, k_weight, weight_dtype: int, eps: float, dq_weight, dk_weight, workspace,
+                          workspace_bytes: int, stream=None) -> None:
+    """Enqueue the gradient of the head norm and rotation (see include/attn_fwd.h)."""
+    if not _int32(B, S, H_q, H_k, D, dtype, weight_dtype):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_qk_norm_rope_bwd")
+    st = load().attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, B, S, H_q, H_k, D, dtype, rope, _addr(positions),
+                                      _addr(q_weight), _addr(k_weight), weight_dtype, eps, _addr(dq_weight), _addr(dk_weight),
+                                      _addr(workspace), workspace_bytes, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_qk_norm_rope_bwd")
+
+
+@functools.lru_cache(maxsize=256)
+def attn_qk_norm_rope_bwd_workspace_bytes(B: int, S: int, H_q: int, H_k: int, D: int) -> int:
+    return load().attn_qk_norm_rope_bwd_workspace_bytes(B, S, H_q, H_k, D) if _int32(B, S, H_q, H_k, D) else 0
+
+
+def attn_paged_append(cache: attn_pages_t, k, v, rows: int, k_stride: int, v_stride: int, seq_start, q, q_stride: int, q_out,
+                      H_q: int, rope, q_weight, k_weight, weight_dtype: int, eps: float, length_out, stream=None) -> None:
+    """Enqueue the append of K and V rows to the pages (see include/attn_fwd.h)."""
+    if not _int32(H_q, weight_dtype):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_paged_append")
+    st = load().attn_paged_append(cache, _addr(k), _addr(v), rows, k_stride, v_stride, _addr(seq_start), _addr(q), q_stride,
+                                  _addr(q_out), H_q, rope, _addr(q_weight), _addr(k_weight), weight_dtype, eps,
+                                  _addr(length_out), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_append")
 
 
 def call_status(fn, *args, **kwargs) -> int:

@@ -143,7 +143,7 @@ struct Params {
 // Read and cleared by attn_fwd_debug_status.  Bit 0: a bounded wait gave up.
 // Bit 1: the backward kernel found its dynamic shared memory off a 1024-byte
 // boundary and ran nothing.  Bit 2: an append dropped entries for which a
-// 4-bit cache had no room.
+// cache had no room.  Bit 3: an entry's place in a page table named no page.
 __device__ unsigned int g_attn_status = 0;
 
 namespace {
@@ -1808,6 +1808,7 @@ const char* attn_status_str(attn_status_t s) {
     case ATTN_ERR_TIMEOUT: return "in-kernel wait timed out";
     case ATTN_ERR_DEVICE: return "CUDA device error";
     case ATTN_ERR_CAPACITY: return "entries beyond a cache's capacity were dropped";
+    case ATTN_ERR_PAGE: return "a page table names no page of the cache where an entry needs one";
   }
   return "unknown status";
 }
@@ -2037,14 +2038,16 @@ attn_status_t attn_fwd_debug_status(void* stream) {
   if (cudaMemcpyFromSymbol(&word, g_attn_status, sizeof word) != cudaSuccess) return ATTN_ERR_DEVICE;
   if (word != 0u) {
     // What is reported is cleared, bit by bit on the device: a kernel of another
-    // stream may have set one meanwhile, and a drop waits for its own report.
-    attn_status_clear_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>((word & 3u) != 0u ? word & 3u : word);
+    // stream may have set one meanwhile, and a drop or a missing page waits for its own report.
+    const unsigned int said = (word & 3u) != 0u ? word & 3u : (word & 4u) != 0u ? 4u : word;
+    attn_status_clear_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(said);
     if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return ATTN_ERR_DEVICE;
   }
   if (word & 2u) return ATTN_ERR_DEVICE;  // a kernel found its shared memory misaligned and did not run
   if (word & 1u) return ATTN_ERR_TIMEOUT;
-  return word != 0u ? ATTN_ERR_CAPACITY : ATTN_OK;
+  if (word & 4u) return ATTN_ERR_CAPACITY;
+  return word != 0u ? ATTN_ERR_PAGE : ATTN_OK;
 }
 
 attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
@@ -2057,8 +2060,11 @@ attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
 
 }  // extern "C"
 
-// Serving: packed prompts with grouped heads, and the 4-bit K/V cache (device
-// code, host code and entry points of each in one file).
+// Serving: packed prompts with grouped heads, the 4-bit K/V cache, the head norm
+// and position rotation (training's too), and the paged K/V cache (device code,
+// host code and entry points of each in one file).
 #include "serving/attn_types.cuh"
 #include "serving/attn_varlen.cuh"
 #include "serving/attn_cache4.cuh"
+#include "attn_rotary.cuh"
+#include "serving/attn_paged.cuh"
