@@ -563,6 +563,41 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
                                 const void* q_weight, const void* k_weight, int weight_dtype, float eps,
                                 int32_t* length_out, void* stream);
 
+/*
+ * attn_paged_attend -- attention of new tokens over the pages.  A sequence's rows of
+ * q are its newest entries, which the cache holds already: row i of n has position
+ * p = length[b] - n + i and sees entry j if
+ *     j <= p  and  (window is 0, or j > p - window, or j < sinks).
+ * Query head h sees key head h / (H_q / H_kv).
+ *
+ *   q           the cache's type: row t is H_q heads of D elements at
+ *               q + t * q_stride; 16-byte aligned, stride a multiple of 8.
+ *   o           the cache's type, [rows][H_q][D], written.  lse fp32 [rows][H_q].
+ *               A row that sees nothing gets O = 0, LSE = -inf.
+ *   rows, seq_start
+ *               as attn_paged_append; rows of no sequence are left as they were.
+ *   window      0: none; else each token sees its own entry and window - 1 before
+ *               it, and the first `sinks` entries (0 or more).  Pages that no token
+ *               sees are not read, whatever the table has for them.
+ *   max_new     a bound on a sequence's rows: those behind it are left as they were.
+ *   max_len     0 .. max_pages * page: a bound on the lengths (they are clamped to
+ *               it).  Both pick the kernel and size the workspace: close ones pay.
+ *   workspace   at least attn_paged_attend_workspace_bytes(...) bytes, 16-byte
+ *               aligned; overwritten.  Calls that share one must be ordered.  Where
+ *               the size is 16, NULL will do.
+ * H_q / H_kv is a whole number, at most 128.  Entries that a token's sequence holds
+ * are finite (a NaN or infinity in V reaches, as a product with zero, tokens of its
+ * own sequence that do not see it); what lies behind a length may be anything.
+ * Results are the same from call to call.  Asynchronous (one to three launches).
+ */
+attn_status_t attn_paged_attend(const attn_pages_t* cache, const void* q, int64_t q_stride, void* o, float* lse,
+                                int64_t rows, const int32_t* seq_start, int H_q, float scale, int window, int sinks,
+                                int max_new, int max_len, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_paged_attend needs (0 for invalid arguments, 16 for none). */
+uint64_t attn_paged_attend_workspace_bytes(int B, int H_q, int H_kv, int D, int64_t rows, int max_new, int max_len,
+                                           int window, int sinks);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* attn_status_str(attn_status_t status);
 

@@ -15,7 +15,8 @@ from ._lib import (ATTN_BF16, ATTN_ERR_ALIGNMENT, ATTN_ERR_CAPACITY, ATTN_ERR_DE
                    attn_cache4_append, attn_cache4_decode, attn_cache4_decode_workspace_bytes, attn_cache4_evict,
                    attn_cache4_evict_workspace_bytes, attn_cache4_read, attn_cache4_t, attn_fwd,
                    attn_fwd_fp8, attn_bwd, attn_bwd_workspace_bytes,
-                   attn_heads_t, attn_paged_append, attn_pages_t, attn_qk_norm_rope, attn_qk_norm_rope_bwd,
+                   attn_heads_t, attn_paged_append, attn_paged_attend,
+                   attn_paged_attend_workspace_bytes, attn_pages_t, attn_qk_norm_rope, attn_qk_norm_rope_bwd,
                    attn_qk_norm_rope_bwd_workspace_bytes, attn_rotary_t,
                    attn_fwd_abi_version, attn_fwd_debug_status, attn_fwd_schedule, attn_fwd_splitkv,
                    attn_fwd_splitkv_static, attn_fwd_splitkv_suggest,
@@ -46,4 +47,5 @@ __all__ = [
     "attn_cache4_evict", "attn_cache4_evict_workspace_bytes", "ATTN_ERR_PAGE", "Rotary", "rotary_frequencies", "qk_norm_rope",
     "qk_norm_rope_backward", "PagedKVCache", "attn_heads_t", "attn_rotary_t", "attn_pages_t", "attn_qk_norm_rope",
     "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_paged_append",
+    "attn_paged_attend", "attn_paged_attend_workspace_bytes",
 ]

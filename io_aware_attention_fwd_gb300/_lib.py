@@ -33,7 +33,8 @@ EXPORTED = ("attn_fwd", "attn_fwd_fp8", "attn_bwd", "attn_bwd_workspace_bytes", 
             "attn_watchdog_selftest", "attn_fwd_abi_version", "attn_fwd_varlen", "attn_fwd_varlen_workspace_bytes",
             "attn_cache4_append", "attn_cache4_read", "attn_cache4_decode", "attn_cache4_decode_workspace_bytes",
             "attn_cache4_evict", "attn_cache4_evict_workspace_bytes", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
-            "attn_qk_norm_rope_bwd_workspace_bytes", "attn_paged_append")
+            "attn_qk_norm_rope_bwd_workspace_bytes", "attn_paged_append", "attn_paged_attend",
+            "attn_paged_attend_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
@@ -161,6 +162,10 @@ def load() -> ctypes.CDLL:
             lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, i, i, i]
             lib.attn_paged_append.restype = i
             lib.attn_paged_append.argtypes = [pp, p, p, i64, i64, i64, p, p, i64, p, i, rp, p, p, i, f, p, p]
+            lib.attn_paged_attend.restype = i
+            lib.attn_paged_attend.argtypes = [pp, p, i64, p, p, i64, p, i, f, i, i, i, i, p, u64, p]
+            lib.attn_paged_attend_workspace_bytes.restype = u64
+            lib.attn_paged_attend_workspace_bytes.argtypes = [i, i, i, i, i64, i, i, i, i]
             lib.attn_status_str.restype = ctypes.c_char_p
             lib.attn_status_str.argtypes = [i]
             lib.attn_fwd_debug_status.restype = i
@@ -411,6 +416,25 @@ def attn_paged_append(cache: attn_pages_t, k, v, rows: int, k_stride: int, v_str
                                   _addr(length_out), _stream(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_append")
+
+
+def attn_paged_attend(cache: attn_pages_t, q, q_stride: int, o, lse, rows: int, seq_start, H_q: int, scale: float, window: int,
+                      sinks: int, max_new: int, max_len: int, workspace, workspace_bytes: int, stream=None) -> None:
+    """Enqueue attention of new tokens over the pages (see include/attn_fwd.h)."""
+    if not _int32(H_q, window, sinks, max_new, max_len):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_paged_attend")
+    st = load().attn_paged_attend(cache, _addr(q), q_stride, _addr(o), _addr(lse), rows, _addr(seq_start), H_q, scale, window,
+                                  sinks, max_new, max_len, _addr(workspace), workspace_bytes, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_attend")
+
+
+@functools.lru_cache(maxsize=256)
+def attn_paged_attend_workspace_bytes(B: int, H_q: int, H_kv: int, D: int, rows: int, max_new: int, max_len: int, window: int,
+                                      sinks: int) -> int:
+    if not _int32(B, H_q, H_kv, D, max_new, max_len, window, sinks):
+        return 0
+    return load().attn_paged_attend_workspace_bytes(B, H_q, H_kv, D, rows, max_new, max_len, window, sinks)
 
 
 def call_status(fn, *args, **kwargs) -> int:

@@ -2068,3 +2068,4 @@ attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
 #include "serving/attn_cache4.cuh"
 #include "attn_rotary.cuh"
 #include "serving/attn_paged.cuh"
+#include "serving/attn_paged_token.cuh"

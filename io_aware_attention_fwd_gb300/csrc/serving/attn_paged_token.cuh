@@ -1,0 +1,779 @@
+// Attention of few query rows per sequence over the pages: one new token each, or
+// as many as fit 16 rows of (token, query head) a key head.  Part of attn_fwd.cu.
+//
+// Every key and value row is read once and meets at most 16 query rows, so the
+// pass is bound by HBM: 4 D bytes a key and key head.  What the kernel is built
+// around is therefore bytes in flight and nothing that stops them:
+//
+//   * One CTA an SM.  A producer warp brings tiles of 64 keys (K and V, 32 KB at
+//     D = 128) into a ring of 192 KB with TMA, page by page, and never stops at the
+//     end of a sequence or head: the next one's tiles are on their way while the
+//     last one's results are joined.
+//   * Eight consumer warps: four take 16 keys each of one tile, four of the next.
+//     S^T = K Q^T and O^T += V^T P^T on mma.sync m16n8k16, keys and channels as the
+//     M rows, 8 query rows a tile of N; ldmatrix reads both from the 128-byte
+//     swizzle.  (With so few rows a product of the tensor core's own
+//     width would be nine tenths padding; the pipe is idle most of the time as it is.)
+//   * P enters P V as the sum of two 16-bit numbers, which leaves 16 (bf16) or 22
+//     bits of it: the products are there for the taking, and O is as exact as from
+//     fp32 products.
+//   * Work split.  The visible tiles of all (sequence, key head, block of rows)
+//     form one list, cut into equal shares, one a CTA, whatever the lengths; a row
+//     counts kTokRowCost tiles more for its start and end.  A row within a share is
+//     written at once; of a row that was cut, each share leaves a partial (m, l, O),
+//     and a second kernel joins them.  Few short rows have a CTA each instead:
+//     one launch.
+//   * With a window the list holds the tiles of the first `sinks` keys and those
+//     from the first new token's window on; no other page is looked at.
+
+namespace {
+
+constexpr int kTokTile = 64;       // keys a tile
+constexpr int kTokWarps = 8;       // consumers
+constexpr int kTokThreads = 32 * (kTokWarps + 1);
+constexpr int kTokRowCost = 4;     // tiles that a row's start and end count as
+
+// What a call gives its tokens.
+struct PagedAttn {
+  PagedSeqs s;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  int64_t q_stride;
+  int G;               // query heads per key head
+  int window, sinks;   // window: INT_MAX / 2 for none
+  int most, max_new;   // bounds on lengths and new tokens
+  float scale_log2;
+  unsigned long long timeout_ns;
+};
+
+// A sequence's new tokens and the tiles of `kTile` keys that some of them see: the
+// first `first_tiles`, then those from `from` on.
+struct PagedSpan {
+  int row0, n;   // packed row of its first new token; tokens that are looked at
+  int len, p0;   // entries; position of the first new token (below 0: it sees nothing)
+  int first_tiles, from, tiles;
+  template <int kTile>
+  __device__ static PagedSpan of(const PagedAttn& p, int b) {
+    PagedSpan w;
+    w.row0 = p.s.seq_start != nullptr ? p.s.start(b) : b;
+    const int all = p.s.rows_of(b);
+    w.n = min(all, p.max_new);
+    w.len = min(max(__ldg(p.s.len + b), 0), p.most);
+    w.p0 = w.len - all;
+    w.visible<kTile>(p, w.p0, w.p0 + w.n);
+    return w;
+  }
+  // The tiles that tokens at positions p0 .. end - 1 see.
+  template <int kTile>
+  __device__ void visible(const PagedAttn& p, int p0, int end) {
+    const int hi = max(0, min(end, len)), lo = max(0, p0 - p.window + 1);
+    from = min(lo, hi) / kTile;
+    first_tiles = min((min(p.sinks, hi) + kTile - 1) / kTile, from);
+    tiles = hi > 0 && n > 0 ? first_tiles + (hi + kTile - 1) / kTile - from : 0;
+  }
+  __device__ int tile(int i) const { return i < first_tiles ? i : from + (i - first_tiles); }
+};
+
+// Whether some token at p0 .. p1 sees some key of k0 .. k1 - 1.
+__device__ __forceinline__ bool paged_seen(const PagedAttn& p, int k0, int k1, int p0, int p1) {
+  return k0 <= p1 && (k1 - 1 > p0 - p.window || k0 < p.sinks);
+}
+// Whether every token sees all of them.
+__device__ __forceinline__ bool paged_all_seen(const PagedAttn& p, int k0, int k1, int p0, int p1) {
+  return k1 - 1 <= p0 && (k0 > p1 - p.window || k1 <= p.sinks);
+}
+
+template <int D, int kNT>
+struct TokCfg {
+  static constexpr int kRows = 8 * kNT;                    // query rows a block
+  static constexpr int kPanels = D / 64;                   // 128-byte panels of a row
+  static constexpr int kPanel = kTokTile * 128;            // bytes of one
+  static constexpr int kV = kPanels * kPanel;              // V of a stage
+  static constexpr int kStage = 2 * kV;
+  static constexpr int kStages = (kNT == 1 ? 192 * 1024 : 160 * 1024) / kStage;  // 6 or 5 (D = 128), 12 or 10
+  static constexpr int kOStride = D + 4;                   // floats; 4: lanes' banks differ
+  static constexpr int kO = kStages * kStage;              // float [4][kRows][kOStride]: the warps' O as they are joined
+  static constexpr int kMl = kO + 4 * kRows * kOStride * 4;  // float2 [2][kTokWarps][kRows]
+  static constexpr int kBar = kMl + 2 * kTokWarps * kRows * 8;
+  static constexpr int kMisc = kBar + 2 * kStages * 8;     // abort flag; int64 sums of the block's scan
+  static constexpr int kBytes = kMisc + 16 + 8 * (kTokThreads / 32 + 4) + 1024;
+  static_assert(kBytes <= 232448, "shared memory per CTA");
+};
+
+struct TokParams {
+  PagedAttn a;
+  float* o_part;    // [2 * CTAs][rows of a block][D]; null: a CTA a row
+  float2* ml_part;  // [2 * CTAs][rows of a block]
+  int blocks_bound; // blocks of rows a sequence may have (a CTA a row)
+  int box_rows, box_log2;  // rows of a TMA box: the page's, at most a tile's
+  int missing;      // third coordinate behind the pages: reads zeros
+};
+
+__device__ __forceinline__ int tok_blocks(const PagedAttn& p, int n, int rows) {
+  return static_cast<int>((static_cast<int64_t>(n) * p.G + rows - 1) / rows);
+}
+template <int kRows>
+__device__ __forceinline__ int64_t tok_units(const PagedAttn& p, int b) {
+  const PagedSpan w = PagedSpan::of<kTokTile>(p, b);
+  return static_cast<int64_t>(w.tiles + kTokRowCost) * p.s.H_kv * tok_blocks(p, w.n, kRows);
+}
+
+// Units of all sequences, and those before this thread's (contiguous) ones; sums: a
+// block's scratch of warps + 1 words.  The whole block calls it.
+template <int kRows, int kThreads>
+__device__ int64_t tok_total(const PagedAttn& p, volatile int64_t* sums, int64_t* before) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const int per = (p.s.B + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < p.s.B) mine += tok_units<kRows>(p, b);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) sums[tid >> 5] = incl;
+  __syncthreads();
+  int64_t total = 0, first = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == (tid >> 5)) first = total;
+    total += sums[w];
+  }
+  *before = first + incl - mine;
+  return total;
+}
+// The sequence in whose units x lies, and the units before it, by the thread that has it.
+template <int kRows, int kThreads>
+__device__ void tok_find(const PagedAttn& p, int64_t x, int64_t before, volatile int* b_out, volatile int64_t* before_out) {
+  const int per = (p.s.B + kThreads - 1) / kThreads;
+  if (x < before) return;
+  for (int i = 0; i < per; ++i) {
+    const int b = static_cast<int>(threadIdx.x) * per + i;
+    if (b >= p.s.B) return;
+    const int64_t u = tok_units<kRows>(p, b);
+    if (x < before + u) {
+      *b_out = b;
+      *before_out = before;
+      return;
+    }
+    before += u;
+  }
+}
+
+// A CTA's share, row by row.
+template <int kRows>
+struct TokWalk {
+  int64_t x, end, before;
+  int b, blocks, per_row;
+  PagedSpan w;
+  int h, rb, t0, t1;  // key head, block of rows, tiles of the list
+  __device__ void load(const PagedAttn& p) {
+    w = PagedSpan::of<kTokTile>(p, b);
+    blocks = tok_blocks(p, w.n, kRows);
+    per_row = w.tiles + kTokRowCost;
+  }
+  __device__ bool next(const PagedAttn& p) {
+    while (x < end) {
+      const int64_t row = (x - before) / per_row;
+      if (row >= static_cast<int64_t>(blocks) * p.s.H_kv) {
+        before += static_cast<int64_t>(per_row) * blocks * p.s.H_kv;
+        if (++b >= p.s.B) return false;
+        load(p);
+        continue;
+      }
+      const int64_t x0 = before + row * per_row;
+      h = static_cast<int>(row) / blocks;
+      rb = static_cast<int>(row) - h * blocks;
+      const bool starts = x == x0;
+      t0 = static_cast<int>(max(static_cast<int64_t>(0), x - x0 - kTokRowCost));
+      t1 = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(w.tiles), end - x0 - kTokRowCost)));
+      x = x0 + per_row;
+      if (t0 < t1 || (w.tiles == 0 && starts)) return true;
+    }
+    return false;
+  }
+};
+
+// Sets this CTA's walk up; false: there is nothing for it.  kDirect: row blockIdx.x.
+template <int kRows, int kThreads, bool kDirect>
+__device__ __forceinline__ bool tok_start(TokWalk<kRows>& k, const TokParams& p, volatile int64_t* sums) {
+  if constexpr (kDirect) {
+    const int per_b = p.a.s.H_kv * p.blocks_bound;
+    k.b = static_cast<int>(blockIdx.x) / per_b;
+    const int i = static_cast<int>(blockIdx.x) - k.b * per_b;
+    k.load(p.a);
+    k.h = i / p.blocks_bound;
+    k.rb = i - k.h * p.blocks_bound;
+    k.t0 = 0, k.t1 = k.w.tiles;
+    return k.rb < k.blocks;
+  } else {
+    int64_t before;
+    const int64_t total = tok_total<kRows, kThreads>(p.a, sums, &before);
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    k.x = static_cast<int64_t>(blockIdx.x) * share;
+    k.end = k.x + share < total ? k.x + share : total;
+    volatile int* const b_s = reinterpret_cast<volatile int*>(sums + kThreads / 32 + 1);
+    if (k.x < k.end) tok_find<kRows, kThreads>(p.a, k.x, before, b_s, sums + kThreads / 32);
+    __syncthreads();
+    if (k.x >= k.end) return false;
+    k.b = *b_s;
+    k.before = sums[kThreads / 32];
+    k.load(p.a);
+    return true;
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ void tok_mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (kType == kFP16) {
+    mma_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+__device__ __forceinline__ void tok_join_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTokWarps * 32) : "memory"); }
+
+// What P is held times, and how far a score may exceed its row's reference before
+// that moves, in log2: bf16 has fp32's range; fp16 ends at 2^16 and below 2^-14 its
+// bits go, so there p is 2^11 times as large and the reference moves at 2^4.
+template <int kType>
+constexpr float kTokUp = kType == kFP16 ? 11.f : 0.f;
+template <int kType>
+constexpr float kTokMove = kType == kFP16 ? 4.f : kRescaleLog2;
+
+// Four channels of a row's O, and its LSE, from the joined sums.
+template <int kType>
+__device__ __forceinline__ void tok_write(const PagedAttn& p, int64_t at, int64_t row, const float4& v, float m, float sum, bool lse) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  // (a mean of fp16 values is one, but may be rounded up past the largest)
+  const uint32_t lo = kType == kFP16 ? pack_f16x2_sat(v.x * inv, v.y * inv) : pack_bf16x2(v.x * inv, v.y * inv);
+  const uint32_t hi = kType == kFP16 ? pack_f16x2_sat(v.z * inv, v.w * inv) : pack_bf16x2(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(p.o + at) = make_uint2(lo, hi);
+  if (lse) {
+    // (the factor comes off the sum first: a sum near 1 has the more exact logarithm)
+    const float l2 = kType == kFP16 ? (m + kTokUp<kType>) + log2f(sum * 0x1p-11f) : m + log2f(sum);
+    p.lse[row] = sum == 0.f ? -INFINITY : l2 * kLn2;
+  }
+}
+
+// Producer warp.
+template <int D, int kNT, bool kDirect>
+__device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV, uint32_t base,
+                         const WaitCtx& wc) {
+  using C = TokCfg<D, kNT>;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int boxes = kTokTile >> p.box_log2;
+  const int box = lane & (boxes - 1), panel = (lane / boxes) % C::kPanels, kv = lane / (boxes * C::kPanels);
+  const bool mine = kv < 2;
+  const uint32_t dst0 = base + kv * C::kV + panel * C::kPanel + (box << p.box_log2) * 128;
+  const CUtensorMap* const map = kv ? tmV : tmK;
+  const int page_mask = (1 << p.a.s.page_log2) - 1;
+  int it = 0;
+  bool ok = true, missing = false;
+  bool more = kDirect ? true : k.next(p.a);
+  while (more && ok) {
+    const int p1 = k.w.p0 + k.w.n - 1;
+    // where this lane's box of the list's tile i lies
+    const auto place = [&](int i, int* y) {
+      const int key = k.w.tile(i) * kTokTile + (box << p.box_log2);
+      int z = p.missing;
+      *y = key & page_mask;
+      if (mine && key < k.w.len && paged_seen(p.a, key, key + p.box_rows, k.w.p0, p1)) {
+        const int pg = p.a.s.page_of(k.b, key >> p.a.s.page_log2);
+        if (pg >= 0)
+          z = pg * p.a.s.H_kv + k.h;
+        else
+          missing = true;
+      }
+      return z;
+    };
+    int y = 0, z = k.t0 < k.t1 ? place(k.t0, &y) : 0;
+    for (int i = k.t0; i < k.t1 && ok; ++i, ++it) {
+      int y2 = 0, z2 = 0;
+      if (i + 1 < k.t1) z2 = place(i + 1, &y2);  // its table entry travels meanwhile
+      const int s = it % C::kStages;
+      const uint32_t full = base + C::kBar + 8 * s;
+      if (it >= C::kStages)
+        ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * C::kStages, (it / C::kStages - 1) & 1, wc));
+      if (!ok) break;
+      if (lane == 0) mbar_expect_tx(full, C::kStage);
+      __syncwarp();
+      if (mine) tma_load_3d(dst0 + s * C::kStage, map, full, panel * 64, y, z);
+      y = y2, z = z2;
+    }
+    more = kDirect ? false : k.next(p.a);
+  }
+  if (missing) atomicOr(&g_attn_status, kPagedNoPage);
+  // what is in flight lands before the CTA leaves
+  bool drained = true;
+  for (int i = it > C::kStages ? it - C::kStages : 0; i < it && drained; ++i)
+    drained = __all_sync(0xffffffffu, mbar_wait_drain(base + C::kBar + 8 * (i % C::kStages), (i / C::kStages) & 1, wc));
+}
+
+// Consumer warp `warp`.
+template <int D, int kType, int kNT, bool kDirect>
+__device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t base, uint8_t* smem, int warp, const WaitCtx& wc) {
+  using C = TokCfg<D, kNT>;
+  constexpr int kSteps = D / 16;
+  const int lane = static_cast<int>(threadIdx.x) & 31, r = lane >> 2, c = lane & 3;
+  const int group = warp >> 2, key_w = (warp & 3) * 16;
+  // ldmatrix addresses in a stage: K rows 0-15 by 16-byte pieces 0 and 1; V rows 0-7 and 8-15, transposed
+  const int krow = key_w + (lane & 15), vrow = key_w + (lane & 7) + ((lane >> 4) << 3);
+  const uint32_t kaddr = base + krow * 128, vaddr = base + C::kV + vrow * 128;
+  const int kpiece = lane >> 4, vpiece = (lane >> 3) & 1;
+  float* const o_s = reinterpret_cast<float*>(smem + C::kO);
+  float2* const ml_s = reinterpret_cast<float2*>(smem + C::kMl);
+  int it = 0, seg = 0;
+  bool ok = true;
+  const float cl = p.a.scale_log2;
+  bool more = kDirect ? true : k.next(p.a);
+  while (more) {
+    const PagedSpan& w = k.w;
+    const int row_b = k.rb * C::kRows;                     // first (token, head) row of the block
+    const int rows = min(C::kRows, w.n * p.a.G - row_b);
+    // Q as B operands, and the positions of this lane's columns
+    uint32_t q[kNT][kSteps][2];
+    int pos[kNT][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int rr = nt * 8 + r;
+      const int tok = (row_b + min(rr, rows - 1)) / p.a.G, g = row_b + min(rr, rows - 1) - tok * p.a.G;
+      const uint16_t* src = p.a.q + (w.row0 + tok) * p.a.q_stride + (k.h * p.a.G + g) * static_cast<int64_t>(D) + 2 * c;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          q[nt][ks][i] = rr < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + i * 8)) : 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) pos[nt][e] = w.p0 + (row_b + min(nt * 8 + 2 * c + e, rows - 1)) / p.a.G;
+    }
+    const int p_first = w.p0 + row_b / p.a.G, p_last = w.p0 + (row_b + rows - 1) / p.a.G;
+    float ref[kNT][2], sub[kNT][2], l[kNT][2], o[kNT][kSteps][4];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[nt][e] = -INFINITY, sub[nt][e] = l[nt][e] = 0.f;
+#pragma unroll
+      for (int mb = 0; mb < kSteps; ++mb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][mb][e] = 0.f;
+    }
+    for (int i = k.t0; i < k.t1; ++i, ++it) {
+      if ((it & 1) != group) continue;
+      const int s = it % C::kStages;
+      const uint32_t full = base + C::kBar + 8 * s, stage = static_cast<uint32_t>(s) * C::kStage;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(full, (it / C::kStages) & 1, wc));
+      if (!ok) continue;  // (the barriers below still have all warps)
+      const int key0 = w.tile(i) * kTokTile + key_w;
+      float d[kNT][4], d2[kNT][4];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[nt][e] = d2[nt][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        uint32_t a[4];
+        ldmatrix_x4(a, kaddr + stage + (ks >> 2) * C::kPanel + ((((ks & 3) * 2 + kpiece) ^ (krow & 7)) << 4));
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) tok_mma<kType>((ks & 1) ? d2[nt] : d[nt], a, q[nt][ks][0], q[nt][ks][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[nt][e] += d2[nt][e];
+      if (!paged_all_seen(p.a, key0, key0 + 16, p_first, p_last)) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = key0 + r + (e >> 1) * 8, at = pos[nt][e & 1];
+            if (!(j <= at && (j > at - p.a.window || j < p.a.sinks))) d[nt][e] = -INFINITY;
+          }
+        // rows behind the sequence's end hold anything, and 0 * NaN is NaN
+        const int past = key0 + 16 - w.len;
+        if (past > 0) {
+          for (int x = lane; x < min(past, 16) * C::kPanels * 8; x += 32) {
+            const int row = key_w + 15 - x / (C::kPanels * 8), piece = x % (C::kPanels * 8);
+            st_shared_v4_b32(base + stage + C::kV + (piece >> 3) * C::kPanel + row * 128 + ((piece & 7) << 4), 0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+      }
+      // New references only where a score exceeds the old one by more than kTokMove
+      bool move = false;
+      float top[kNT][2];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nt][e] = fmaxf(d[nt][e], d[nt][e + 2]) * cl;
+          move |= top[nt][e] > ref[nt][e] + (kTokMove<kType> + kTokUp<kType>);
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          float a[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], off));
+            const bool moves = top[nt][e] > ref[nt][e] + (kTokMove<kType> + kTokUp<kType>);
+            const float to = moves ? top[nt][e] - kTokUp<kType> : ref[nt][e];
+            a[e] = moves ? ex2_approx(ref[nt][e] - to) : 1.f;
+            ref[nt][e] = to;
+            sub[nt][e] = to == -INFINITY ? 0.f : to;
+            l[nt][e] *= a[e];
+          }
+#pragma unroll
+          for (int mb = 0; mb < kSteps; ++mb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][mb][e] *= a[e & 1];
+        }
+      }
+      uint32_t hi[kNT][2], lo[kNT][2];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const float x0 = ex2_approx(fmaf(d[nt][2 * i2], cl, -sub[nt][0])), x1 = ex2_approx(fmaf(d[nt][2 * i2 + 1], cl, -sub[nt][1]));
+          l[nt][0] += x0;
+          l[nt][1] += x1;
+          const uint32_t h2 = pack_16x2<kType>(x0, x1);
+          const float2 back = unpack_16x2<kType>(h2);
+          hi[nt][i2] = movmatrix_trans(h2);
+          lo[nt][i2] = movmatrix_trans(pack_16x2<kType>(x0 - back.x, x1 - back.y));
+        }
+#pragma unroll
+      for (int mb = 0; mb < kSteps; ++mb) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(a, vaddr + stage + (mb >> 2) * C::kPanel + ((((mb & 3) * 2 + vpiece) ^ (vrow & 7)) << 4));
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          tok_mma<kType>(o[nt][mb], a, hi[nt][0], hi[nt][1]);
+          tok_mma<kType>(o[nt][mb], a, lo[nt][0], lo[nt][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * C::kStages);
+    }
+    // The eight warps' statistics and O become the row's, or the share's partial.
+    float2* const ml = ml_s + (seg & 1) * kTokWarps * C::kRows;
+    ++seg;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
+        if (r == 0) ml[warp * C::kRows + nt * 8 + 2 * c + e] = make_float2(ref[nt][e], l[nt][e]);
+      }
+    tok_join_sync();
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kTokWarps; ++x) m = fmaxf(m, ml[x * C::kRows + nt * 8 + 2 * c + e].x);
+        const float f = ref[nt][e] == -INFINITY ? 0.f : ex2_approx(ref[nt][e] - m);
+        // (a warp without keys has nothing to add, and 0 * NaN would be something)
+        if (ref[nt][e] != -INFINITY || l[nt][e] != 0.f) {
+#pragma unroll
+          for (int mb = 0; mb < kSteps; ++mb) o[nt][mb][e] *= f, o[nt][mb][e + 2] *= f;
+        }
+      }
+    float* const mine = o_s + (warp & 3) * C::kRows * C::kOStride;
+    const auto slot = [&](int nt, int mb, int e) -> float& {
+      return mine[(nt * 8 + 2 * c + (e & 1)) * C::kOStride + mb * 16 + r + (e >> 1) * 8];
+    };
+    if (group == 1) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int mb = 0; mb < kSteps; ++mb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) slot(nt, mb, e) = o[nt][mb][e];
+    }
+    tok_join_sync();
+    if (group == 0) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int mb = 0; mb < kSteps; ++mb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) slot(nt, mb, e) += o[nt][mb][e];
+    }
+    tok_join_sync();
+    const bool whole = kDirect || (k.t0 == 0 && k.t1 == w.tiles);
+    const int part = 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0);
+    for (int x = warp * 32 + lane; x < C::kRows * (D / 4); x += kTokWarps * 32) {
+      const int n = x / (D / 4), ch = (x % (D / 4)) * 4;
+      if (n >= rows || !ok) continue;
+      float m = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int y = 0; y < kTokWarps; ++y) m = fmaxf(m, ml[y * C::kRows + n].x);
+#pragma unroll
+      for (int y = 0; y < kTokWarps; ++y) {
+        const float2 v = ml[y * C::kRows + n];
+        if (v.x != -INFINITY || v.y != 0.f) sum += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - m);
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float4 u = *reinterpret_cast<const float4*>(o_s + (y * C::kRows + n) * C::kOStride + ch);
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
+      if (whole) {
+        const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
+        const int64_t at = static_cast<int64_t>(w.row0 + tok) * p.a.s.H_kv * p.a.G + k.h * p.a.G + g;
+        tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
+      } else {
+        *reinterpret_cast<float4*>(p.o_part + (static_cast<int64_t>(part) * C::kRows + n) * D + ch) = v;
+        if (ch == 0) p.ml_part[static_cast<int64_t>(part) * C::kRows + n] = make_float2(m, sum);
+      }
+    }
+    more = kDirect ? false : k.next(p.a);
+  }
+}
+
+template <int D, int kType, int kNT, bool kDirect>
+__global__ void __launch_bounds__(kTokThreads, 1)
+    attn_paged_token_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const __grid_constant__ TokParams p) {
+  using C = TokCfg<D, kNT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  volatile uint32_t* const misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMisc);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(base + C::kBar + 8 * s, 1);
+      mbar_init(base + C::kBar + 8 * (C::kStages + s), 4);
+    }
+    misc[0] = 0u;
+    fence_barrier_init();
+  } else if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  __syncthreads();
+  const WaitCtx wc{p.a.timeout_ns, misc};
+  grid_dependency_wait();
+  grid_launch_dependents();
+  TokWalk<C::kRows> k;
+  if (!tok_start<C::kRows, kTokThreads, kDirect>(k, p, reinterpret_cast<volatile int64_t*>(smem + C::kMisc + 16))) return;
+  if (warp == kTokWarps)
+    tok_load<D, kNT, kDirect>(k, p, &tmK, &tmV, base, wc);
+  else
+    tok_compute<D, kType, kNT, kDirect>(k, p, base, smem, warp, wc);
+}
+
+// Joins the partials of the rows that the shares' ends cut: block c the row across
+// the beginning of share c, if that is the first one within it.
+constexpr int kTokMergeThreads = 256;
+template <int D, int kType, int kRows>
+__global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(const __grid_constant__ TokParams p) {
+  __shared__ int64_t sums[kTokMergeThreads / 32 + 2];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t c = blockIdx.x;
+  int64_t before;
+  const int64_t total = tok_total<kRows, kTokMergeThreads>(p.a, sums, &before);
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x, x = c * share;
+  if (c == 0 || x >= total) return;
+  volatile int* const b_s = reinterpret_cast<volatile int*>(sums + kTokMergeThreads / 32 + 1);
+  tok_find<kRows, kTokMergeThreads>(p.a, x, before, b_s, sums + kTokMergeThreads / 32);
+  __syncthreads();
+  const int b = *b_s;
+  before = sums[kTokMergeThreads / 32];
+  const PagedSpan w = PagedSpan::of<kTokTile>(p.a, b);
+  const int blocks = tok_blocks(p.a, w.n, kRows), per_row = w.tiles + kTokRowCost;
+  const int64_t row = (x - before) / per_row, x0 = before + row * per_row + kTokRowCost;
+  const int64_t ca = x0 / share, cb = (x0 + w.tiles - 1) / share;
+  if (w.tiles == 0 || cb <= ca || c != ca + 1) return;
+  const int h = static_cast<int>(row) / blocks, row_b = (static_cast<int>(row) - h * blocks) * kRows;
+  const int rows = min(kRows, w.n * p.a.G - row_b);
+  for (int i = static_cast<int>(threadIdx.x); i < rows * (D / 4); i += kTokMergeThreads) {
+    const int n = i / (D / 4), ch = (i % (D / 4)) * 4;
+    const auto part = [&](int64_t y) { return (2 * y + (y == ca ? 1 : 0)) * kRows + n; };
+    float m = -INFINITY;
+    for (int64_t y = ca; y <= cb; ++y) m = fmaxf(m, __ldg(&p.ml_part[part(y)].x));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int64_t y = ca; y <= cb; ++y) {
+      const float2 s = __ldg(p.ml_part + part(y));
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p.o_part + part(y) * D + ch));
+      if (s.x == -INFINITY && s.y == 0.f) continue;  // no key of it was seen
+      const float f = s.x == -INFINITY ? 1.f : ex2_approx(s.x - m);
+      sum = fmaf(s.y, f, sum);
+      v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+    }
+    const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
+    const int64_t at = static_cast<int64_t>(w.row0 + tok) * p.a.s.H_kv * p.a.G + h * p.a.G + g;
+    tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Few rows with few keys each: a CTA a row and no second kernel.
+constexpr int kTokDirectLen = 2048;
+constexpr int kTokSms = 152;  // (the workspace's size is asked for without a device)
+
+// What an attention over pages takes: blocks of 8 or 16 rows, and a CTA a row or shares.
+struct TokPlan {
+  int nt, blocks;   // tiles of 8 rows a block; blocks a sequence may have
+  bool direct;
+};
+TokPlan tok_plan(int B, int H_kv, int G, int max_new, int max_len, int window, int sinks) {
+  TokPlan t;
+  const int64_t rows = static_cast<int64_t>(max_new) * G;
+  t.nt = rows <= 8 ? 1 : 2;
+  t.blocks = static_cast<int>(std::min<int64_t>((rows + 8 * t.nt - 1) / (8 * t.nt), INT_MAX));
+  const int64_t keys = window > 0 ? std::min<int64_t>(max_len, static_cast<int64_t>(window) + sinks + max_new) : max_len;
+  t.direct = static_cast<int64_t>(B) * H_kv * t.blocks <= kTokSms && keys <= kTokDirectLen;
+  return t;
+}
+uint64_t tok_workspace(const TokPlan& t, int D) {
+  return t.direct ? 16 : static_cast<uint64_t>(2 * kTokSms) * 8 * t.nt * (D * sizeof(float) + sizeof(float2));
+}
+
+std::atomic<int> g_paged_state[kMaxDevices];  // 1: shared-memory limits set
+
+template <int D, int kType>
+bool tok_limits() {
+  const auto limit = [](const void* f, int bytes) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  return limit(reinterpret_cast<const void*>(attn_paged_token_kernel<D, kType, 1, false>), TokCfg<D, 1>::kBytes) &&
+         limit(reinterpret_cast<const void*>(attn_paged_token_kernel<D, kType, 1, true>), TokCfg<D, 1>::kBytes) &&
+         limit(reinterpret_cast<const void*>(attn_paged_token_kernel<D, kType, 2, false>), TokCfg<D, 2>::kBytes) &&
+         limit(reinterpret_cast<const void*>(attn_paged_token_kernel<D, kType, 2, true>), TokCfg<D, 2>::kBytes);
+}
+
+// Pages as a tensor map {D, page, n_pages * H_kv} with boxes of 64 channels x `rows`, 128-byte swizzle.
+bool encode_pages(CUtensorMap* m, const void* ptr, const attn_pages_t* c, int rows) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->D), static_cast<cuuint64_t>(c->page),
+                        static_cast<cuuint64_t>(c->n_pages) * static_cast<cuuint64_t>(c->H_kv)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(c->D) * 2, static_cast<cuuint64_t>(c->page) * c->D * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, c->dtype == ATTN_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int kType, int kNT>
+cudaError_t tok_launch(const CUtensorMap& tk, const CUtensorMap& tv, const TokParams& p, bool direct, int64_t rows, cudaStream_t s) {
+  using C = TokCfg<D, kNT>;
+  if (direct)
+    return launch_pdl(attn_paged_token_kernel<D, kType, kNT, true>, dim3(static_cast<unsigned>(rows)), dim3(kTokThreads), C::kBytes,
+                      s, tk, tv, p);
+  const cudaError_t e = launch_pdl(attn_paged_token_kernel<D, kType, kNT, false>, dim3(kTokSms), dim3(kTokThreads), C::kBytes, s,
+                                   tk, tv, p);
+  return e != cudaSuccess ? e
+                          : launch_pdl(attn_paged_merge_kernel<D, kType, C::kRows>, dim3(kTokSms), dim3(kTokMergeThreads), 0, s, p);
+}
+
+attn_status_t tok_run(const attn_pages_t* c, const PagedAttn& a, const TokPlan& t, void* workspace, cudaStream_t s) {
+  const int box = std::min(c->page, kTokTile);
+  CUtensorMap tk, tv;
+  if (!encode_pages(&tk, c->k_pages, c, box) || !encode_pages(&tv, c->v_pages, c, box)) return ATTN_ERR_LAUNCH;
+  TokParams p;
+  p.a = a;
+  p.o_part = static_cast<float*>(workspace);
+  p.ml_part = reinterpret_cast<float2*>(p.o_part + static_cast<int64_t>(2 * kTokSms) * 8 * t.nt * c->D);
+  p.blocks_bound = t.blocks;
+  p.box_rows = box;
+  p.box_log2 = 0;
+  while ((1 << p.box_log2) < box) ++p.box_log2;
+  p.missing = c->n_pages * c->H_kv;
+  const int64_t rows = static_cast<int64_t>(c->B) * c->H_kv * t.blocks;
+  const auto run = [&](auto d, auto type) {
+    return t.nt == 1 ? tok_launch<d(), type(), 1>(tk, tv, p, t.direct, rows, s) : tok_launch<d(), type(), 2>(tk, tv, p, t.direct, rows, s);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  using Bf = std::integral_constant<int, kBF16>;
+  using Fp = std::integral_constant<int, kFP16>;
+  const bool bf = c->dtype == ATTN_BF16;
+  const cudaError_t e = c->D == 64 ? (bf ? run(D64(), Bf()) : run(D64(), Fp())) : (bf ? run(D128(), Bf()) : run(D128(), Fp()));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t attn_paged_attend_workspace_bytes(int B, int H_q, int H_kv, int D, int64_t rows, int max_new, int max_len, int window,
+                                           int sinks) {
+  if (B < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || H_q / H_kv > kBM || (D != 64 && D != 128) || rows < 0 || max_new < 0 ||
+      max_len < 0 || window < 0 || sinks < 0)
+    return 0;
+  return tok_workspace(tok_plan(B, H_kv, H_q / H_kv, max_new, max_len, window, sinks), D);
+}
+
+attn_status_t attn_paged_attend(const attn_pages_t* cache, const void* q, int64_t q_stride, void* o, float* lse, int64_t rows,
+                                const int32_t* seq_start, int H_q, float scale, int window, int sinks, int max_new, int max_len,
+                                void* workspace, uint64_t workspace_bytes, void* stream) {
+  attn_status_t st = check_pages(cache);
+  if (st != ATTN_OK) return st;
+  const int D = cache->D, H_kv = cache->H_kv, B = cache->B;
+  if (rows < 0 || H_q < H_kv || H_q % H_kv != 0 || (seq_start == nullptr && rows != B)) return ATTN_ERR_INVALID_ARG;
+  if (rows > 0 && (q == nullptr || o == nullptr || lse == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f) || window < 0 || sinks < 0 || max_new < 0 || max_len < 0 ||
+      max_len > static_cast<int64_t>(cache->max_pages) * cache->page)
+    return ATTN_ERR_INVALID_ARG;
+  if (H_q / H_kv > kBM || rows > INT_MAX / 2 || q_stride > (int64_t{1} << 40)) return ATTN_ERR_UNSUPPORTED;
+  if (q_stride < static_cast<int64_t>(H_q) * D) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seq_start, 4) || !aligned(workspace, 16) || q_stride % 8 != 0)
+    return ATTN_ERR_ALIGNMENT;
+  const int G = H_q / H_kv;
+  max_new = static_cast<int>(std::min<int64_t>(max_new, rows));
+  const TokPlan t = tok_plan(B, H_kv, G, max_new, max_len, window, sinks);
+  const uint64_t need = attn_paged_attend_workspace_bytes(B, H_q, H_kv, D, rows, max_new, max_len, window, sinks);
+  if (rows > 0 && need > 16 && (workspace == nullptr || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  if (rows == 0 || max_new == 0) return ATTN_OK;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_DEVICE;
+  st = prepare_device(dev);
+  if (st != ATTN_OK) return st;
+  if (g_paged_state[dev].load(std::memory_order_acquire) == 0) {
+    if (!tok_limits<64, kBF16>() || !tok_limits<64, kFP16>() || !tok_limits<128, kBF16>() || !tok_limits<128, kFP16>())
+      return ATTN_ERR_DEVICE;
+    g_paged_state[dev].store(1, std::memory_order_release);
+  }
+  if (!get_encoder()) return ATTN_ERR_DEVICE;
+  PagedAttn a;
+  a.s = paged_seqs(cache, seq_start, rows);
+  a.q = static_cast<const uint16_t*>(q);
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.q_stride = q_stride;
+  a.G = G;
+  // beyond what positions reach, a window and a number of sinks say nothing more
+  a.window = window > 0 ? std::min(window, INT_MAX / 2) : INT_MAX / 2;
+  a.sinks = window > 0 ? std::min(sinks, INT_MAX / 2) : 0;
+  a.most = max_len;
+  a.max_new = max_new;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  a.timeout_ns = kDefaultTimeoutNs;
+  return tok_run(cache, a, t, workspace, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -138,3 +138,59 @@ class PagedKVCache:
         _lib.attn_paged_append(self._c, k.data_ptr(), v.data_ptr(), rows, k_stride, v_stride, seq_start, q, q_stride, q_out, H_q, r,
                                qw, kw, w_code, eps, length_out.data_ptr(), handle)
         return q_out
+
+    def attend(self, q, seq_start=None, scale: float | None = None, window: int | None = None, sinks: int = 0,
+               max_new: int | None = None, max_len: int | None = None, out=None, lse=None, stream=None):
+        """Attention of new tokens, q [rows, H_q, D] of the cache's type, over the entries held.
+
+        A sequence's rows are its newest entries (append first, then attend): of n, the i-th has
+        position length - n + i and sees entry j if j <= position and (there is no window, or
+        j > position - window, or j < sinks).  seq_start: int32 [B + 1] as append takes it; None:
+        one row for each sequence.  max_new and max_len: bounds on a sequence's rows and length
+        (None: the rows there are, the capacity).  Rows behind max_new are left as they were,
+        lengths are clamped to max_len; both pick the kernel and size the workspace, so close
+        ones pay.  Pages that no token sees are not read.  Returns (o, lse): o of q's shape and
+        type, lse fp32 [rows, H_q]; 0 and -inf for a token that sees nothing.  Rows of no
+        sequence are left as they were, which in outputs allocated here means undefined.
+        """
+        import torch
+
+        shape, device, dtype, D, B, H_kv = q.shape, self.device, self.dtype, self.D, self.B, self.H_kv
+        if len(shape) != 3 or shape[2] != D or shape[1] < 1 or shape[1] % H_kv:
+            raise ValueError(f"q must be [rows, H_q, {D}], H_q a multiple of {H_kv}")
+        if q.device != device:
+            raise ValueError(f"q must be on {device}")
+        if q.dtype != dtype:
+            raise TypeError(f"q must be {dtype}, as the cache is")
+        rows, H_q = shape[0], shape[1]
+        if seq_start is not None:
+            check_int32(seq_start, B + 1, device, "seq_start")
+        elif rows != B:
+            raise ValueError(f"without seq_start q has one row for each of the {B} sequences")
+        if window is None:
+            window = 0
+        elif window < 1:
+            raise ValueError("window must be 1 or more, or None")
+        if max_new is None:
+            max_new = rows if seq_start is not None else 1
+        if max_len is None:
+            max_len = self.max_pages * self.page
+        if scale is None:
+            scale = 1.0 / math.sqrt(D)
+        stride = row_stride(q, shape, "q")
+        if out is not None:
+            check_out(out, shape, dtype, device, "out")
+        if lse is not None:
+            check_out(lse, (rows, H_q), torch.float32, device, "lse")
+        handle = current_handle(device) if stream is None else None
+        if handle is None:
+            return on_stream(device, stream, lambda: self.attend(q, seq_start, scale, window or None, sinks, max_new, max_len, out, lse))
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        if lse is None:
+            lse = torch.empty((rows, H_q), dtype=torch.float32, device=device)
+        nbytes = _lib.attn_paged_attend_workspace_bytes(B, H_q, H_kv, D, rows, min(max_new, rows), max_len, window, sinks)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 16 else None
+        _lib.attn_paged_attend(self._c, q.data_ptr(), stride, out.data_ptr(), lse.data_ptr(), rows, seq_start, H_q, scale, window,
+                               sinks, max_new, max_len, ws, nbytes, handle)
+        return out, lse

@@ -154,3 +154,317 @@ def test_append_no_rows():
     cache.append(e, e, seq_start=s)
     torch.cuda.synchronize()
     assert out.tolist() == [7, 3] and cache.length.tolist() == [7, 3]
+
+
+# --- attention -------------------------------------------------------------------------------------------------------
+
+def queries(rows, hq, d, dtype, seed=7):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn((rows, hq, d), generator=g, device=DEV).to(dtype)
+
+
+def check(got, want):
+    o, lse = got
+    ro, rlse, tol, lse_tol = want
+    torch.cuda.synchronize()
+    assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+    own = ~rlse.isnan()
+    none = own & (rlse == -math.inf)
+    assert (lse[none] == -math.inf).all() and not o[none].any()
+    some = own & ~none
+    assert ((lse.double() - rlse).abs() <= lse_tol)[some].all(), (lse.double() - rlse).abs()[some].max()
+    bad = ~((o.double() - ro).abs() <= tol)[some]
+    assert not bad.any(), (int(bad.sum()), ((o.double() - ro).abs() / tol)[some].max())
+
+
+def attend(cache, q, starts=None, scale=None, window=None, sinks=0, max_new=None, max_len=None):
+    """The call with outputs that hold a mark, and its reference."""
+    out, lse = torch.full(q.shape, 7.0, dtype=q.dtype, device=DEV), torch.full(q.shape[:2], 7.0, device=DEV)
+    s = None if starts is None else torch.tensor(starts, dtype=torch.int32, device=DEV)
+    got = cache.attend(q, s, scale, window, sinks, max_new, max_len, out, lse)
+    assert got[0] is out and got[1] is lse
+    want = ref.attend(q, cache.k_pages, cache.v_pages, cache.page_table, cache.length.tolist(), starts,
+                      cache.D ** -0.5 if scale is None else scale, window, sinks, max_len, max_new)
+    check(got, want)
+    left = want[1].isnan()
+    assert (out[left] == 7.0).all() and (lse[left] == 7.0).all()
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_token_pages(page, d, dtype):
+    lens = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 500, 701]
+    cache = make_cache(lens, [0] * len(lens), 2, d, page, dtype, seed=page)
+    attend(cache, queries(len(lens), 8, d, dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 3), (7, 1), (16, 2), (9, 1), (24, 2), (16, 1), (17, 1), (40, 1), (128, 1)])
+def test_token_groups(hq, hkv, d, dtype):
+    """One launch (short) and shares with a merge (long); groups that fill no block, one and several."""
+    for lens in ([70, 1, 300], [3000, 0, 17, 2500]):
+        cache = make_cache(lens, [0] * len(lens), hkv, d, 32, dtype, seed=hq)
+        attend(cache, queries(len(lens), hq, d, dtype), scale=0.2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_token_many_sequences(d):
+    """More rows than SMs, lengths of every kind: rows within a share, cut by one end, cut by several."""
+    lens = [(i * 37) % 900 for i in range(200)] + [20000, 0, 0, 5, 9000]
+    cache = make_cache(lens, [0] * len(lens), 2, d, 64, torch.bfloat16, seed=3)
+    attend(cache, queries(len(lens), 8, d, torch.bfloat16))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (63, 2), (64, 4), (65, 64), (100, 65), (1000, 4), (5000, 300), (1 << 30, 7),
+                                          ((1 << 31) - 1, (1 << 31) - 1)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (64, 256)])
+def test_token_window(d, page, window, sinks):
+    lens = [0, 1, 16, 64, 65, 130, 700, 1064, 1065, 6000]
+    cache = make_cache(lens, [0] * len(lens), 2, d, page, torch.bfloat16, seed=window % 1000)
+    attend(cache, queries(len(lens), 8, d, torch.bfloat16), window=window, sinks=sinks)
+
+
+def test_token_pages_out_of_the_window_are_not_read():
+    """The table's places that no token sees name no page, pages of them hold NaN: nothing of it shows."""
+    for page, window, sinks in ((16, 100, 5), (64, 200, 0), (256, 300, 1)):
+        lens = [1000, 3000]
+        cache = make_cache(lens, [0, 0], 2, 64, page, torch.bfloat16, seed=1)
+        q = queries(2, 8, 64, torch.bfloat16)
+        want = cache.attend(q, window=window, sinks=sinks)
+        for b, n in enumerate(lens):
+            lo = n - window
+            for x in range(-(-n // page)):
+                if x * page >= sinks and (x + 1) * page <= lo:
+                    p = int(cache.page_table[b, x])
+                    cache.k_pages[p], cache.v_pages[p] = math.nan, math.inf
+                    cache.page_table[b, x] = (-1, 1 << 30, -(1 << 31))[x % 3]
+        got = cache.attend(q, window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_missing_pages_read_as_zeros_and_are_reported():
+    for lens in ([200, 90], [5000, 90]):
+        cache = make_cache(lens, [0, 0], 2, 64, 16, torch.bfloat16, seed=2)
+        cache.page_table[0, 3], cache.page_table[0, 5], cache.page_table[1, 0] = -1, cache.n_pages, (1 << 31) - 1
+        q = queries(2, 4, 64, torch.bfloat16)
+        got = cache.attend(q)
+        torch.cuda.synchronize()
+        assert attn.attn_fwd_debug_status() == attn.ATTN_ERR_PAGE and attn.attn_fwd_debug_status() == attn.ATTN_OK
+        check(got, ref.attend(q, cache.k_pages, cache.v_pages, cache.page_table, lens, None, 0.125))
+
+
+def test_lengths_are_clamped():
+    cache = make_cache([100, 400, 30], [0, 0, 0], 2, 64, 16, torch.bfloat16, seed=5)
+    cap = cache.max_pages * 16
+    q = queries(3, 4, 64, torch.bfloat16)
+    attend(cache, q, max_len=50)
+    cache.length[0] = -4
+    attend(cache, q, max_len=200)
+    attend(cache, q, max_len=0)
+    cache.page_table[:] = 0
+    cache.length[1] = cap + 1000
+    cache.k_pages.nan_to_num_(0.5)
+    cache.v_pages.nan_to_num_(0.5)
+    attend(cache, q)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (5, 1), (14, 2), (100, 1)])
+def test_few_tokens(hq, hkv, d, dtype):
+    """Two to five new tokens of some sequences, one or none of others."""
+    new, had = [3, 0, 1, 5, 2, 4], [0, 10, 700, 63, 1500, 12]
+    cache = make_cache([a + b for a, b in zip(had, new)], [0] * 6, hkv, d, 16, dtype, seed=hq)
+    starts, _ = starts_of(new)
+    q = queries(starts[-1] + 2, hq, d, dtype)
+    attend(cache, q, starts, max_new=5)
+    attend(cache, q, starts, window=40, sinks=3, max_new=5)
+    attend(cache, q, starts, max_new=3)
+
+
+CHUNKS = [([1], [0]), ([40], [0]), ([128], [0]), ([200], [77]), ([1, 64, 0, 300], [500, 0, 9, 1]), ([257, 3, 90], [1000, 2000, 17]),
+          ([700], [3000])]
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,had", CHUNKS, ids=str)
+def test_chunks(new, had, d, page):
+    cache = make_cache([a + b for a, b in zip(had, new)], [0] * len(new), 2, d, page, torch.bfloat16, seed=d)
+    starts, _ = starts_of(new)
+    q = queries(starts[-1] + 5, 8, d, torch.bfloat16)
+    attend(cache, q, starts)
+    attend(cache, q, starts, window=100, sinks=10)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 3), (3, 1), (10, 2), (7, 1), (12, 1), (24, 2), (100, 1), (128, 1)])
+def test_chunk_groups(hq, hkv, dtype):
+    for d in (64, 128):
+        cache = make_cache([150, 40, 333], [0] * 3, hkv, d, 32, dtype, seed=hq)
+        q = queries(150 + 9 + 33, hq, d, dtype)
+        attend(cache, q, [0, 150, 159, 192], scale=0.2)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (50, 0), (127, 1), (128, 128), (129, 129), (300, 4), (2000, 200)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 128)])
+def test_chunk_window(d, page, window, sinks):
+    new, had = [300, 1, 40, 700], [900, 200, 0, 100]
+    cache = make_cache([a + b for a, b in zip(had, new)], [0] * 4, 2, d, page, torch.bfloat16, seed=window)
+    starts, _ = starts_of(new)
+    attend(cache, queries(starts[-1], 8, d, torch.bfloat16), starts, window=window, sinks=sinks)
+
+
+def test_chunk_pages_out_of_the_window_are_not_read():
+    for page, window, sinks in ((16, 100, 5), (128, 200, 0)):
+        new, n = 150, 3000
+        cache = make_cache([n], [0], 2, 64, page, torch.bfloat16, seed=1)
+        q, s = queries(new, 8, 64, torch.bfloat16), torch.tensor([0, new], dtype=torch.int32, device=DEV)
+        want = cache.attend(q, s, window=window, sinks=sinks)
+        for x in range(-(-n // page)):
+            if x * page >= sinks and (x + 1) * page <= n - new + 1 - window:
+                p = int(cache.page_table[0, x])
+                cache.k_pages[p], cache.v_pages[p] = math.nan, math.inf
+                cache.page_table[0, x] = (-1, 1 << 30, -(1 << 31))[x % 3]
+        got = cache.attend(q, s, window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_more_tokens_than_entries():
+    """Tokens before a sequence's first entry see nothing: 0 and -inf."""
+    cache = make_cache([3, 0, 70], [0] * 3, 2, 64, 16, torch.bfloat16, seed=4)
+    for new in ([5, 2, 70], [100, 90, 200]):
+        starts, _ = starts_of(new)
+        q = queries(starts[-1], 4, 64, torch.bfloat16)
+        attend(cache, q, starts)
+        attend(cache, q, starts, window=2, sinks=1)
+    q = queries(7, 4, 64, torch.bfloat16)
+    attend(cache, q, [0, 5, 7, 7], max_new=5)
+
+
+def test_starts_out_of_range_and_rows_left_out():
+    cache = make_cache([300, 200], [0, 0], 2, 64, 32, torch.bfloat16, seed=6)
+    q = queries(64, 4, 64, torch.bfloat16)
+    attend(cache, q, [-5, 20, 2000])
+    attend(cache, q, [10, 40, 45])
+    attend(cache, q, [10, 40, 45], max_new=20)
+
+
+def test_large_logits():
+    """Logits that grow along the keys: the reference moves many times."""
+    for new in (1, 200):
+        cache = make_cache([2500], [0], 2, 64, 64, torch.bfloat16, seed=9)
+        for x, p in enumerate(cache.page_table[0, :40].tolist()):
+            cache.k_pages[p] *= 0.1 + 0.3 * x
+        q = queries(new, 4, 64, torch.bfloat16)
+        attend(cache, q, [0, new], scale=0.5)
+
+
+def test_low_values_keep_their_bits_in_fp16():
+    """The largest key's V is 0; what is left comes from keys many nats below."""
+    for new in (1, 130):
+        cache = make_cache([1500], [0], 1, 64, 64, torch.float16, seed=3)
+        cache.k_pages.zero_()
+        q = torch.zeros((new, 4, 64), dtype=torch.float16, device=DEV)
+        q[..., 0] = 1.0
+        p0 = int(cache.page_table[0, 0])
+        cache.k_pages[p0, 0, 0, 0], cache.v_pages[p0, 0, 0] = 16.0, 0.0
+        attend(cache, q, [0, new], scale=1.0)
+
+
+@pytest.mark.parametrize("new", [1, 4, 150])
+def test_streams_graphs_and_repeats(new):
+    lens = [3000, 200, 1024]
+    cache = make_cache([n + new for n in lens], [0] * 3, 2, 128, 64, torch.bfloat16, seed=8)
+    starts, s = starts_of([new] * 3)
+    q = queries(3 * new, 8, 128, torch.bfloat16)
+    want = cache.attend(q, s, max_new=new)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = cache.attend(q, s, max_new=new, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = cache.attend(q, s, max_new=new)
+    cache.length -= 5  # a graph takes the lengths as they are when it runs
+    graph.replay()
+    torch.cuda.synchronize()
+    later = cache.attend(q, s, max_new=new)
+    assert torch.equal(held[0], later[0]) and torch.equal(held[1], later[1]) and not torch.equal(held[0], want[0])
+
+
+def test_exchanged_buffers_and_copies():
+    cache = make_cache([100, 50], [0, 0], 2, 64, 16, torch.bfloat16)
+    q = queries(2, 4, 64, torch.bfloat16)
+    want = cache.attend(q)
+    for other in (copy.copy(cache), copy.deepcopy(cache)):
+        got = other.attend(q)
+        assert torch.equal(got[0], want[0])
+    other = copy.deepcopy(cache)
+    other.length = torch.tensor([60, 50], dtype=torch.int32, device=DEV)
+    got = other.attend(q)
+    assert not torch.equal(got[0], want[0]) and torch.equal(got[0][1], want[0][1])
+    for name, bad in (("length", cache.length.long()), ("page_table", cache.page_table[:1]), ("k_pages", cache.k_pages.half()),
+                      ("v_pages", None), ("B", 7), ("other", 1)):
+        with pytest.raises((ValueError, TypeError, AttributeError)):
+            setattr(cache, name, bad)
+
+
+def test_python_refusals_on_the_device():
+    cache = make_cache([100, 50], [0, 0], 2, 64, 16, torch.bfloat16)
+    q = queries(2, 4, 64, torch.bfloat16)
+    for bad in (dict(q=q[:1]), dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q.cpu()), dict(seq_start=torch.zeros(4, dtype=torch.int32, device=DEV)),
+                dict(window=0), dict(out=q.float()), dict(lse=torch.zeros(4, 2, device=DEV))):
+        with pytest.raises(ValueError):
+            cache.attend(**{**dict(q=q), **bad})
+    with pytest.raises(TypeError):
+        cache.attend(q.half())
+    for bad in (dict(sinks=-1), dict(max_len=1 << 20), dict(scale=0.0), dict(max_len=1 << 33), dict(window=1 << 33)):
+        with pytest.raises(attn.AttnError):
+            cache.attend(q, **bad)
+    k = queries(2, 2, 64, torch.bfloat16)
+    for bad in (dict(k=k[:1]), dict(v=k[:, :1]), dict(q=q[:1]), dict(q_out=q), dict(q_weight=k[0, 0]), dict(q=q, q_out=q[:1]),
+                dict(length_out=cache.length.long())):
+        with pytest.raises(ValueError):
+            cache.append(**{**dict(k=k, v=k), **bad})
+    with pytest.raises(TypeError):
+        cache.append(k.half(), k.half())
+    with pytest.raises(ValueError):
+        attn.PagedKVCache.empty(1, 1, 4, 24, 2, 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_conversation(dtype):
+    """A prompt, tokens, another message and tokens again, normed and turned on the way, against one pass over it all in 64 bits."""
+    H, G, d, page = 2, 4, 64, 16
+    f = attn.rotary_frequencies(d)
+    rope = attn.Rotary(f)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    w = list((1 + 0.2 * torch.randn((2, d), generator=g, device=DEV)).to(dtype))
+    steps = [[37, 90, 1], [1, 1, 1], [1, 1, 1], [60, 1, 5], [1, 1, 1]]
+    total = [sum(s[b] for s in steps) for b in range(3)]
+    cache = make_cache([0, 0, 0], total, H, d, page, dtype)
+    rows = [[], [], []]
+    for step in steps:
+        starts, s = starts_of(step)
+        qkv = torch.randn((starts[-1], H * (G + 2), d), generator=g, device=DEV).to(dtype)
+        q, k, v = qkv[:, :H * G], qkv[:, H * G:H * G + H], qkv[:, H * G + H:]
+        q = cache.append(k, v, seq_start=s, q=q, rope=rope, q_weight=w[0], k_weight=w[1])
+        o, lse = cache.attend(q, s, window=50, sinks=2, max_new=max(step))
+        for b in range(3):
+            rows[b].append((q[starts[b]:starts[b + 1]], k[starts[b]:starts[b + 1]], v[starts[b]:starts[b + 1]], o[starts[b]:starts[b + 1]]))
+        check((o, lse), ref.attend(q, cache.k_pages, cache.v_pages, cache.page_table, cache.length.tolist(), starts, d ** -0.5, 50, 2))
+    assert cache.length.tolist() == total
+    for b in range(3):
+        k = torch.cat([r[1] for r in rows[b]])
+        want, tol = ref.forward(k, w[1], torch.arange(total[b], device=DEV), f, False, 1.0, 1e-6)
+        kk, vv = rows_of(cache, b, 0, total[b])
+        assert ((kk.double() - want).abs() <= tol).all() and torch.equal(vv, torch.cat([r[2] for r in rows[b]]))
