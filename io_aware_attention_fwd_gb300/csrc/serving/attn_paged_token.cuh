@@ -91,10 +91,14 @@ struct TokCfg {
   static constexpr int kPanel = kTokTile * 128;            // bytes of one
   static constexpr int kV = kPanels * kPanel;              // V of a stage
   static constexpr int kStage = 2 * kV;
-  static constexpr int kStages = (kNT == 1 ? 192 * 1024 : 160 * 1024) / kStage;  // 6 or 5 (D = 128), 12 or 10
+  // 6 (D = 128) or 12.  Even, so that a stage is always the same four warps': a warp
+  // that did not see every phase of a barrier could take one for the next but one.
+  static constexpr int kStages = (192 * 1024) / kStage;
+  static_assert(kStages % 2 == 0, "a stage belongs to one group of warps");
   static constexpr int kOStride = D + 4;                   // floats; 4: lanes' banks differ
-  static constexpr int kO = kStages * kStage;              // float [4][kRows][kOStride]: the warps' O as they are joined
-  static constexpr int kMl = kO + 4 * kRows * kOStride * 4;  // float2 [2][kTokWarps][kRows]
+  static constexpr int kSlots = kNT == 1 ? 4 : 2;          // places for a warp's O as the eight are added up
+  static constexpr int kO = kStages * kStage;              // float [kSlots][kRows][kOStride]
+  static constexpr int kMl = kO + kSlots * kRows * kOStride * 4;  // float2 [2][kTokWarps][kRows]
   static constexpr int kBar = kMl + 2 * kTokWarps * kRows * 8;
   static constexpr int kMisc = kBar + 2 * kStages * 8;     // abort flag; int64 sums of the block's scan
   static constexpr int kBytes = kMisc + 16 + 8 * (kTokThreads / 32 + 4) + 1024;
@@ -492,28 +496,24 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
           for (int mb = 0; mb < kSteps; ++mb) o[nt][mb][e] *= f, o[nt][mb][e + 2] *= f;
         }
       }
-    float* const mine = o_s + (warp & 3) * C::kRows * C::kOStride;
-    const auto slot = [&](int nt, int mb, int e) -> float& {
-      return mine[(nt * 8 + 2 * c + (e & 1)) * C::kOStride + mb * 16 + r + (e >> 1) * 8];
-    };
-    if (group == 1) {
+    // kSlots warps at a time, always in the same order
+    const int rank = warp ^ 4;
+    float* const mine = o_s + (rank % C::kSlots) * C::kRows * C::kOStride;
+#pragma unroll 1
+    for (int step = 0; step < kTokWarps / C::kSlots; ++step) {
+      if (rank / C::kSlots == step) {
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int mb = 0; mb < kSteps; ++mb)
+          for (int mb = 0; mb < kSteps; ++mb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) slot(nt, mb, e) = o[nt][mb][e];
+            for (int e = 0; e < 4; ++e) {
+              float& to = mine[(nt * 8 + 2 * c + (e & 1)) * C::kOStride + mb * 16 + r + (e >> 1) * 8];
+              to = step == 0 ? o[nt][mb][e] : to + o[nt][mb][e];
+            }
+      }
+      tok_join_sync();
     }
-    tok_join_sync();
-    if (group == 0) {
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int mb = 0; mb < kSteps; ++mb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) slot(nt, mb, e) += o[nt][mb][e];
-    }
-    tok_join_sync();
     const bool whole = kDirect || (k.t0 == 0 && k.t1 == w.tiles);
     const int part = 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0);
     for (int x = warp * 32 + lane; x < C::kRows * (D / 4); x += kTokWarps * 32) {
@@ -529,7 +529,7 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
       }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < C::kSlots; ++y) {
         const float4 u = *reinterpret_cast<const float4*>(o_s + (y * C::kRows + n) * C::kOStride + ch);
         v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
       }

@@ -468,3 +468,19 @@ def test_a_conversation(dtype):
         want, tol = ref.forward(k, w[1], torch.arange(total[b], device=DEV), f, False, 1.0, 1e-6)
         kk, vv = rows_of(cache, b, 0, total[b])
         assert ((kk.double() - want).abs() <= tol).all() and torch.equal(vv, torch.cat([r[2] for r in rows[b]]))
+
+
+@pytest.mark.parametrize("new,hq", [(1, 8), (1, 16), (40, 8), (300, 8)])
+def test_back_to_back(new, hq):
+    """Many calls without a wait between them, over more tiles than the rings hold: the same each time."""
+    cache = make_cache([6000 + new] * 4, [0] * 4, 4 if hq == 16 else 2, 128, 64, torch.bfloat16, seed=new)
+    if hq == 16:
+        hq = 64  # 16 query heads a key head: two tiles of 8 rows
+    starts, s = starts_of([new] * 4)
+    q = queries(4 * new, hq, 128, torch.bfloat16)
+    first = attend(cache, q, starts, max_new=new)
+    got = [cache.attend(q, s, max_new=new) for _ in range(30)]
+    torch.cuda.synchronize()
+    assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+    for o, lse in got:
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
