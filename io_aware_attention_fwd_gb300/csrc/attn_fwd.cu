@@ -2069,3 +2069,4 @@ attn_status_t attn_watchdog_selftest(uint64_t timeout_ns, void* stream) {
 #include "attn_rotary.cuh"
 #include "serving/attn_paged.cuh"
 #include "serving/attn_paged_token.cuh"
+#include "serving/attn_paged_chunk.cuh"

@@ -717,63 +717,3 @@ attn_status_t tok_run(const attn_pages_t* c, const PagedAttn& a, const TokPlan& 
 }
 
 }  // namespace
-
-extern "C" {
-
-uint64_t attn_paged_attend_workspace_bytes(int B, int H_q, int H_kv, int D, int64_t rows, int max_new, int max_len, int window,
-                                           int sinks) {
-  if (B < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || H_q / H_kv > kBM || (D != 64 && D != 128) || rows < 0 || max_new < 0 ||
-      max_len < 0 || window < 0 || sinks < 0)
-    return 0;
-  return tok_workspace(tok_plan(B, H_kv, H_q / H_kv, max_new, max_len, window, sinks), D);
-}
-
-attn_status_t attn_paged_attend(const attn_pages_t* cache, const void* q, int64_t q_stride, void* o, float* lse, int64_t rows,
-                                const int32_t* seq_start, int H_q, float scale, int window, int sinks, int max_new, int max_len,
-                                void* workspace, uint64_t workspace_bytes, void* stream) {
-  attn_status_t st = check_pages(cache);
-  if (st != ATTN_OK) return st;
-  const int D = cache->D, H_kv = cache->H_kv, B = cache->B;
-  if (rows < 0 || H_q < H_kv || H_q % H_kv != 0 || (seq_start == nullptr && rows != B)) return ATTN_ERR_INVALID_ARG;
-  if (rows > 0 && (q == nullptr || o == nullptr || lse == nullptr)) return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f) || window < 0 || sinks < 0 || max_new < 0 || max_len < 0 ||
-      max_len > static_cast<int64_t>(cache->max_pages) * cache->page)
-    return ATTN_ERR_INVALID_ARG;
-  if (H_q / H_kv > kBM || rows > INT_MAX / 2 || q_stride > (int64_t{1} << 40)) return ATTN_ERR_UNSUPPORTED;
-  if (q_stride < static_cast<int64_t>(H_q) * D) return ATTN_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seq_start, 4) || !aligned(workspace, 16) || q_stride % 8 != 0)
-    return ATTN_ERR_ALIGNMENT;
-  const int G = H_q / H_kv;
-  max_new = static_cast<int>(std::min<int64_t>(max_new, rows));
-  const TokPlan t = tok_plan(B, H_kv, G, max_new, max_len, window, sinks);
-  const uint64_t need = attn_paged_attend_workspace_bytes(B, H_q, H_kv, D, rows, max_new, max_len, window, sinks);
-  if (rows > 0 && need > 16 && (workspace == nullptr || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
-  if (rows == 0 || max_new == 0) return ATTN_OK;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_DEVICE;
-  st = prepare_device(dev);
-  if (st != ATTN_OK) return st;
-  if (g_paged_state[dev].load(std::memory_order_acquire) == 0) {
-    if (!tok_limits<64, kBF16>() || !tok_limits<64, kFP16>() || !tok_limits<128, kBF16>() || !tok_limits<128, kFP16>())
-      return ATTN_ERR_DEVICE;
-    g_paged_state[dev].store(1, std::memory_order_release);
-  }
-  if (!get_encoder()) return ATTN_ERR_DEVICE;
-  PagedAttn a;
-  a.s = paged_seqs(cache, seq_start, rows);
-  a.q = static_cast<const uint16_t*>(q);
-  a.o = static_cast<uint16_t*>(o);
-  a.lse = lse;
-  a.q_stride = q_stride;
-  a.G = G;
-  // beyond what positions reach, a window and a number of sinks say nothing more
-  a.window = window > 0 ? std::min(window, INT_MAX / 2) : INT_MAX / 2;
-  a.sinks = window > 0 ? std::min(sinks, INT_MAX / 2) : 0;
-  a.most = max_len;
-  a.max_new = max_new;
-  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  a.timeout_ns = kDefaultTimeoutNs;
-  return tok_run(cache, a, t, workspace, static_cast<cudaStream_t>(stream));
-}
-
-}  // extern "C"

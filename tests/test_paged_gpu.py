@@ -357,6 +357,32 @@ def test_starts_out_of_range_and_rows_left_out():
     attend(cache, q, [10, 40, 45], max_new=20)
 
 
+def test_starts_that_overlap_stay_within_the_buffers():
+    """Disordered starts leave their sequences' rows undefined, and nothing else touched."""
+    cache = make_cache([3000] * 6, [0] * 6, 2, 64, 32, torch.bfloat16, seed=6)
+    q = queries(400, 8, 64, torch.bfloat16)
+    for starts, new in (([0, 390, 0, 390, 0, 390, 0], 390), ([0, 4, 0, 4, 0, 4, 0], 2), ([390, 5, 390, -7, 390, 1 << 30, 0], 400)):
+        out, lse = torch.full((404, 8, 64), 7.0, dtype=q.dtype, device=DEV), torch.full((404, 8), 7.0, device=DEV)
+        s = torch.tensor(starts, dtype=torch.int32, device=DEV)
+        cache.attend(q, s, max_new=new, out=out[:400], lse=lse[:400])
+        cache.attend(q, s, max_new=new, max_len=500, out=out[:400], lse=lse[:400])
+        torch.cuda.synchronize()
+        assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+        assert (out[400:] == 7.0).all() and (lse[400:] == 7.0).all()
+
+
+def test_more_sequences_than_the_list_takes_at_once():
+    """More than 1024 sequences of a few tokens."""
+    new = [(i * 7) % 5 for i in range(1500)]
+    had = [(i * 13) % 70 for i in range(1500)]
+    had[700] = 5000
+    cache = make_cache([a + b for a, b in zip(had, new)], [0] * 1500, 1, 64, 16, torch.bfloat16, seed=6)
+    starts, _ = starts_of(new)
+    q = queries(starts[-1], 8, 64, torch.bfloat16)
+    attend(cache, q, starts, max_new=4)
+    attend(cache, q, starts, window=20, sinks=1)
+
+
 def test_large_logits():
     """Logits that grow along the keys: the reference moves many times."""
     for new in (1, 200):
