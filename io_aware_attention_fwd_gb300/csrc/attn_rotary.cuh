@@ -15,15 +15,22 @@
 // upper 32 bits, as a signed number of half turns, go through sincospif.
 //
 // Both passes are bound by HBM: 4 (forward) or 6 (gradient) bytes a channel.
-// A row of 256 (128) bytes is 16 (8) lanes of 8 channels; what pairs with them is
-// one shuffle of the 16-bit words away.  A block takes up to 8 tokens: their
-// cosines and sines are worked out once, in shared memory, for all heads.
+// A row of 256 (128) bytes is 16 (8) lanes of 8 channels, so a warp takes 2 (4) heads
+// of a token at once; what pairs with a lane's channels is one shuffle of the 16-bit
+// words away.  All groups of heads of all tokens form one list, cut into equal
+// shares, one a warp, and a warp has the next four groups on their way while it works
+// on one, across the tokens' ends too.  The sine and cosine of a token are worked out
+// by the warp that comes to it; what they and the weights make of a lane's channels,
+//     y = r (x A + x' B)   (x' the paired channels),
+// stays in registers for all heads of the token.  With a block's tokens' tables in
+// shared memory, read for each head, the pass took 186 us instead of REPLACE_FWD for
+// 16384 tokens of 64 heads, D = 128 (537 MB).
 
 namespace {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotWarps = kRotThreads / 32;
-constexpr int kRotTokens = 8;  // tokens a block takes at once, at most
+constexpr int kRotFwdBlocks = 3;  // blocks an SM
 
 struct RotRows {  // rows [B][S][H][D], strides in elements
   uint16_t* p;
@@ -41,352 +48,406 @@ struct RotParams {
   RotRows out[3];  // append: q alone, the others go to the pages
   RotRows dy[2];   // gradient
   int heads[3];
-  int groups[3];   // of the heads a warp takes at once
+  int first[4];    // first group of q, k, v in a token's list, and their number
   const void* w[2];  // weights, or null: no norm
   int w_fp32;
   float eps;
   RotTurn turn;
   const int32_t* pos;  // [B][S]
-  int B, S;
-  int tokens;      // a block's
-  int tiles;       // ceil(S / tokens)
-  int per_block;   // groups a block takes (its blockIdx.y-th part of them)
+  int S;
+  int64_t total, share;  // groups of all tokens; of a warp
   float* dw;       // gradient: [blocks][2][D]
 };
 
-// What the lanes of a row hold.
+// What a lane holds of a row.
 template <int D>
 struct RotLane {
-  static constexpr int kLanes = D / 8;          // lanes a row
-  static constexpr int kRows = 32 / kLanes;     // rows a warp
-  int sub, c0;                                  // this lane's row of the warp's, and first channel
-  int partner;                                  // lane with the paired channels (half layout)
-  float sign;                                   // of the paired channel's sine
-  bool turned;
-  int at;                                       // of its first cosine
+  static constexpr int kLanes = D / 8;       // lanes a row
+  static constexpr int kRows = 32 / kLanes;  // rows a warp
+  int sub, c0;                               // this lane's row of the warp's, and first channel
+  int partner;                               // lane with the paired channels (half layout)
+  bool turned, low;
+  int at;                                    // of its first cosine
   __device__ RotLane(int lane, const RotTurn& t) {
     sub = lane / kLanes;
     c0 = (lane % kLanes) * 8;
     const int half = t.rot / 2;
     turned = c0 < t.rot;
-    const bool low = c0 < half;
+    low = c0 < half;
     partner = t.inter || !turned ? lane : lane + (low ? half : -half) / 8;
-    sign = low ? -1.f : 1.f;
     at = t.inter ? c0 / 2 : low ? c0 : c0 - half;
   }
 };
 
-// Cosines and sines of a block's tokens: cs[token][0 .. rot/2 - 1] and the sines behind.
-__device__ __forceinline__ void rot_table(float* cs, const int* pos, int tokens, const RotTurn& t) {
-  const int half = t.rot / 2;
-  for (int i = static_cast<int>(threadIdx.x); i < tokens * half; i += kRotThreads) {
-    const int tok = i / half, j = i - tok * half;
-    const uint64_t turn = static_cast<uint64_t>(__ldg(t.turns + j)) * static_cast<uint64_t>(static_cast<int64_t>(pos[tok]));
-    const int32_t half_turns = static_cast<int32_t>(turn >> 32);
-    float s, c;
-    sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s, &c);
-    cs[tok * t.rot + j] = c * t.amp;
-    cs[tok * t.rot + half + j] = s * t.amp;
+// This lane's share of a token's cosines and sines, cs[0 .. rot/2 - 1] and behind them.
+struct RotTable {
+  int64_t turn[2];  // of pairs lane and lane + 32
+  __device__ RotTable(int lane, const RotTurn& t) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) turn[i] = lane + 32 * i < t.rot / 2 ? __ldg(t.turns + lane + 32 * i) : 0;
   }
+  __device__ void fill(float* cs, int lane, int pos, const RotTurn& t) const {
+    __syncwarp();  // the last token's have been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = lane + 32 * i;
+      if (j < t.rot / 2) {
+        const uint64_t a = static_cast<uint64_t>(turn[i]) * static_cast<uint64_t>(static_cast<int64_t>(pos));
+        float s, c;
+        sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f, &s, &c);
+        cs[j] = c * t.amp;
+        cs[t.rot / 2 + j] = s * t.amp;
+      }
+    }
+    __syncwarp();
+  }
+};
+
+// A warp's part of the list, run by run: groups g0 .. g1 - 1 of token (row s of batch
+// b), all of one kind (q, k or v).
+struct RotWalk {
+  int64_t left;
+  int b, s, g0, g1, kind;
+  bool token;  // the run is the token's first here
+  __device__ RotWalk(const RotParams& p, int64_t i, int64_t n) : left(n), kind(0), token(true) {
+    const int64_t row = i / p.first[3];
+    g0 = g1 = static_cast<int>(i - row * p.first[3]);
+    b = static_cast<int>(row / p.S);
+    s = static_cast<int>(row - static_cast<int64_t>(b) * p.S);
+    run(p);
+  }
+  __device__ void run(const RotParams& p) {
+    kind = (g0 >= p.first[1]) + (g0 >= p.first[2]);
+    const int end = kind == 0 ? p.first[1] : kind == 1 ? p.first[2] : p.first[3];
+    g1 = static_cast<int>(min(static_cast<int64_t>(end), g0 + left));
+  }
+  __device__ bool next(const RotParams& p) {
+    left -= g1 - g0;
+    if (left <= 0) return false;
+    g0 = g1;
+    token = g0 == p.first[3];
+    if (token) {
+      g0 = 0;
+      if (++s == p.S) s = 0, ++b;
+    }
+    run(p);
+    return true;
+  }
+};
+__device__ __forceinline__ uint16_t* rot_at(const RotRows& r, int b, int s, int head, int c0) {
+  return r.p + b * r.b + s * r.row + head * r.head + c0;
 }
 
+// 8 packed channels as 4 pairs of fp32.
 template <int kType>
-__device__ __forceinline__ void rot_unpack(float* x, const uint4& w) {
+__device__ __forceinline__ void rot_unpack(uint64_t* x, const uint4& w) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = unpack_16x2<kType>((&w.x)[e]);
-    x[2 * e] = f.x;
-    x[2 * e + 1] = f.y;
+    x[e] = pack_f32x2(f.x, f.y);
   }
 }
 template <int kType>
-__device__ __forceinline__ uint4 rot_pack(const float* x) {
-  return make_uint4(pack_16x2<kType>(x[0], x[1]), pack_16x2<kType>(x[2], x[3]), pack_16x2<kType>(x[4], x[5]),
-                    pack_16x2<kType>(x[6], x[7]));
-}
-__device__ __forceinline__ uint4 rot_shuffle(const uint4& w, int from) {
-  return make_uint4(__shfl_sync(0xffffffffu, w.x, from), __shfl_sync(0xffffffffu, w.y, from),
-                    __shfl_sync(0xffffffffu, w.z, from), __shfl_sync(0xffffffffu, w.w, from));
-}
-__device__ __forceinline__ void rot_load8(float* x, const float* s) {
-  const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-// Turns x (this lane's 8 channels) by the token's angles, backwards if kBack; y
-// holds the paired channels in the half layout.
-template <bool kBack>
-__device__ __forceinline__ void rot_turn(float* x, const float* y, const float* cs, const RotTurn& t, float sign, int at) {
-  if (t.inter) {
-    const float4 c = *reinterpret_cast<const float4*>(cs + at), s = *reinterpret_cast<const float4*>(cs + t.rot / 2 + at);
-    const float co[4] = {c.x, c.y, c.z, c.w}, si[4] = {s.x, s.y, s.z, s.w};
+__device__ __forceinline__ uint4 rot_pack(const uint64_t* x) {
+  uint4 w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = x[2 * e], b = x[2 * e + 1], sn = kBack ? -si[e] : si[e];
-      x[2 * e] = fmaf(a, co[e], -b * sn);
-      x[2 * e + 1] = fmaf(a, sn, b * co[e]);
-    }
-  } else {
-    float co[8], si[8];
-    rot_load8(co, cs + at);
-    rot_load8(si, cs + t.rot / 2 + at);
-    if (kBack) sign = -sign;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], co[e], sign * y[e] * si[e]);
+  for (int e = 0; e < 4; ++e) {
+    float a, b;
+    unpack_f32x2(x[e], a, b);
+    (&w.x)[e] = pack_16x2<kType>(a, b);
   }
+  return w;
+}
+// The words that hold the paired channels: another lane's, or this one's with their halves exchanged.
+__device__ __forceinline__ uint4 rot_paired(const uint4& w, const RotTurn& t, int partner) {
+  if (t.inter) return make_uint4(__byte_perm(w.x, w.x, 0x1032), __byte_perm(w.y, w.y, 0x1032), __byte_perm(w.z, w.z, 0x1032),
+                                 __byte_perm(w.w, w.w, 0x1032));
+  return make_uint4(__shfl_sync(0xffffffffu, w.x, partner), __shfl_sync(0xffffffffu, w.y, partner),
+                    __shfl_sync(0xffffffffu, w.z, partner), __shfl_sync(0xffffffffu, w.w, partner));
+}
+__device__ __forceinline__ float rot_sum(uint64_t v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
+  return a + b;
 }
 
-// The weights of q and k as fp32, in shared memory.
+// The weights of q and k (1 without a norm) as fp32, in shared memory.
 template <int D, int kType>
 __device__ __forceinline__ void rot_weights(float (*ws)[D], const RotParams& p) {
   for (int i = static_cast<int>(threadIdx.x); i < 2 * D; i += kRotThreads) {
     const int kv = i / D, c = i % D;
     float w = 1.f;
-    if (p.w[kv] != nullptr) {
-      if (p.w_fp32) {
-        w = __ldg(static_cast<const float*>(p.w[kv]) + c);
-      } else {
-        const float2 f = unpack_16x2<kType>(__ldg(static_cast<const unsigned short*>(p.w[kv]) + c));
-        w = f.x;
-      }
-    }
+    if (p.w[kv] != nullptr)
+      w = p.w_fp32 ? __ldg(static_cast<const float*>(p.w[kv]) + c)
+                   : unpack_16x2<kType>(__ldg(static_cast<const unsigned short*>(p.w[kv]) + c)).x;
     ws[kv][c] = w;
   }
 }
-
-// One group of heads of one token, as a warp takes them.
-struct RotItem {
-  int tok, kind, head;
-  bool there;
-};
+__device__ __forceinline__ void rot_load8(float* x, const float* s) {
+  const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+// Cosines of this lane's channels, and sines with the sign that the paired channel has
+// (forward; the gradient's is the other one).
 template <int D>
-__device__ __forceinline__ RotItem rot_item(const RotParams& p, int tok, int group, int sub, int tokens) {
-  RotItem it{tok, 0, 0, false};
-  if (tok >= tokens) return it;
-  if (group >= p.groups[0]) group -= p.groups[0], it.kind = 1;
-  if (it.kind == 1 && group >= p.groups[1]) group -= p.groups[1], it.kind = 2;
-  it.head = group * RotLane<D>::kRows + sub;
-  it.there = it.head < p.heads[it.kind];
-  return it;
-}
-
-template <int D, int kType>
-__device__ __forceinline__ uint4 rot_load(const RotRows& r, int64_t at) {
-  return *reinterpret_cast<const uint4*>(r.p + at);
-}
-
-// x normed (w: this lane's weights and, half layout, its partners') and turned.
-template <int D, int kType>
-__device__ __forceinline__ uint4 rot_forward(const uint4& raw, const float* w, const float* cs, const RotParams& p, bool norm,
-                                             const RotLane<D>& ln, int partner_c0) {
-  float x[8], y[8];
-  rot_unpack<kType>(x, raw);
-  float r = 1.f;
-  if (norm) {
-    float ss = 0.f;
+__device__ __forceinline__ void rot_angles(float* co, float* si, const RotLane<D>& ln, const RotTurn& t, const float* cs) {
+  if (!ln.turned) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int e = 0; e < 8; ++e) co[e] = 1.f, si[e] = 0.f;
+  } else if (t.inter) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + ln.at), s = *reinterpret_cast<const float4*>(cs + t.rot / 2 + ln.at);
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int off = 1; off < RotLane<D>::kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-  }
-  if (!p.turn.inter && p.turn.rot > 0) rot_unpack<kType>(y, rot_shuffle(raw, ln.partner));
-  if (norm) {
-    float ww[8];
-    rot_load8(ww, w + ln.c0);
+    for (int e = 0; e < 8; ++e) co[e] = cc[e / 2], si[e] = e % 2 == 0 ? -ss[e / 2] : ss[e / 2];
+  } else {
+    rot_load8(co, cs + ln.at);
+    rot_load8(si, cs + t.rot / 2 + ln.at);
+    if (ln.low) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= r * ww[e];
-    if (!p.turn.inter && p.turn.rot > 0) {
-      rot_load8(ww, w + partner_c0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= r * ww[e];
+      for (int e = 0; e < 8; ++e) si[e] = -si[e];
     }
   }
-  if (ln.turned) rot_turn<false>(x, y, cs, p.turn, ln.sign, ln.at);
-  return rot_pack<kType>(x);
 }
 
-// Forward.  kPaged: tokens are packed rows, q goes to its rows and k and v to
-// the pages (attn_paged.cuh says where: paged_place).
+struct NoPages {};
+
+// Forward.  kPaged: tokens are packed rows, q goes to its rows and k and v to the
+// pages (attn_paged.cuh says where).
 template <int D, int kType, bool kPaged, typename Paged>
-__device__ __forceinline__ void rot_forward_body(const RotParams& p, const Paged& pg) {
+__device__ __forceinline__ void rot_forward_body(const RotParams& p, Paged pg) {
   using Lane = RotLane<D>;
-  constexpr int kBatch = 4;  // rows a lane has in flight
-  __shared__ __align__(16) float cs_s[kRotTokens * D];
+  constexpr int kBatch = 4;  // groups on their way at once
+  __shared__ __align__(16) float cs_s[kRotWarps][D];
   __shared__ __align__(16) float w_s[2][D];
-  __shared__ int pos_s[kRotTokens];
-  __shared__ int64_t to_s[kRotTokens];  // kPaged: first element of the token's row in its page; -1: in none
-  __shared__ int live_s[kRotTokens];    // kPaged: the row belongs to a sequence
-  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const Lane ln(lane, p.turn);
-  const int partner_c0 = (ln.partner % Lane::kLanes) * 8;
-  const int b = static_cast<int>(blockIdx.x) / p.tiles, tile = static_cast<int>(blockIdx.x) - b * p.tiles;
-  const int s0 = tile * p.tokens, tokens = min(p.tokens, p.S - s0);
-  const int g0 = static_cast<int>(blockIdx.y) * p.per_block;
-  const int all = p.groups[0] + p.groups[1] + (kPaged ? p.groups[2] : 0);
-  const int ng = min(p.per_block, all - g0);
   grid_dependency_wait();
   grid_launch_dependents();
-
-  int tok = 0, g = warp;  // this warp's next item
-  while (g >= ng && tok < tokens) g -= ng, ++tok;
-  uint4 raw[kBatch];
-  RotItem it[kBatch];
-  const auto fetch = [&]() {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      it[u] = rot_item<D>(p, tok, g0 + g, ln.sub, tokens);
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (it[u].there) {
-        const RotRows& r = p.in[it[u].kind];
-        raw[u] = rot_load<D, kType>(r, b * r.b + (s0 + tok) * r.row + it[u].head * r.head + ln.c0);
-      }
-      g += kRotWarps;
-      while (g >= ng && tok < tokens) g -= ng, ++tok;
-    }
-  };
-  fetch();  // on their way while the angles are worked out
-  if (tid < tokens) {
-    if constexpr (kPaged) {
-      int pos, live;
-      to_s[tid] = pg.template place<D>(s0 + tid, &pos, &live, blockIdx.y == 0);
-      pos_s[tid] = pos;
-      live_s[tid] = live;
-    } else {
-      pos_s[tid] = p.pos != nullptr ? __ldg(p.pos + static_cast<int64_t>(b) * p.S + s0 + tid) : 0;
-    }
-  }
   rot_weights<D, kType>(w_s, p);
   __syncthreads();
-  rot_table(cs_s, pos_s, tokens, p.turn);
-  __syncthreads();
-  while (it[0].tok < tokens) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int t = min(it[u].tok, tokens - 1), kind = it[u].kind;
-      uint4 y = raw[u];
-      if (!kPaged || kind < 2)  // (the whole warp: an item is of one kind)
-        y = rot_forward<D, kType>(raw[u], w_s[kind & 1], cs_s + t * p.turn.rot, p, p.w[kind & 1] != nullptr, ln, partner_c0);
-      if (!it[u].there) continue;
-      if (kPaged && kind > 0) {
-        const int64_t to = to_s[t];
-        if (to >= 0)
-          *reinterpret_cast<uint4*>((kind == 1 ? pg.k : pg.v) + to + static_cast<int64_t>(it[u].head) * pg.head_step + ln.c0) = y;
-      } else if (!kPaged || live_s[t]) {
-        const RotRows& r = p.out[kind];
-        *reinterpret_cast<uint4*>(r.p + b * r.b + (s0 + t) * r.row + it[u].head * r.head + ln.c0) = y;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kRotWarps + warp) * p.share;
+  if (i >= p.total) return;
+  const RotTable table(lane, p.turn);
+  float* const cs = cs_s[warp];
+  RotWalk w(p, i, min(p.share, p.total - i));
+  if constexpr (kPaged) pg.find(w.s);
+  bool more = true;
+  while (more) {
+    const RotRows& in = p.in[w.kind];
+    // this lane's head of the next group, and where its heads end
+    int head = (w.g0 - p.first[w.kind]) * Lane::kRows + ln.sub, left = w.g1 - w.g0;
+    const int end = min(p.heads[w.kind], (w.g1 - p.first[w.kind]) * Lane::kRows);
+    const uint16_t* src = rot_at(in, w.b, w.s, head, ln.c0);
+    const int64_t in_step = in.head * Lane::kRows;
+    uint16_t* dst;
+    int64_t out_step;
+    bool keep = true;
+    if constexpr (kPaged) {
+      if (w.kind > 0) {
+        keep = pg.to >= 0;
+        out_step = pg.head_step * Lane::kRows;
+        dst = (w.kind == 1 ? pg.k : pg.v) + (keep ? pg.to + head * pg.head_step + ln.c0 : 0);
+      } else {
+        keep = pg.live();
+        out_step = p.out[0].head * Lane::kRows;
+        dst = rot_at(p.out[0], 0, w.s, head, ln.c0);
       }
+    } else {
+      out_step = p.out[w.kind].head * Lane::kRows;
+      dst = rot_at(p.out[w.kind], w.b, w.s, head, ln.c0);
     }
-    fetch();
+    const bool turns = !kPaged || w.kind < 2, norm = turns && p.w[w.kind & 1] != nullptr;
+    uint64_t A[4], B[4];
+    bool fresh = turns;
+    while (left > 0) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (head + u * Lane::kRows < end) raw[u] = *reinterpret_cast<const uint4*>(src + u * in_step);
+      }
+      if (fresh) {  // while the first groups are on their way
+        fresh = false;
+        if (w.token && p.turn.rot > 0) {
+          int pos;
+          if constexpr (kPaged)
+            pos = pg.pos;
+          else
+            pos = __ldg(p.pos + static_cast<int64_t>(w.b) * p.S + w.s);
+          table.fill(cs, lane, pos, p.turn);
+        }
+        float co[8], si[8], own[8], other[8];
+        rot_angles<D>(co, si, ln, p.turn, cs);
+        rot_load8(own, w_s[w.kind & 1] + ln.c0);
+        rot_load8(other, w_s[w.kind & 1] + (ln.partner % Lane::kLanes) * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float o0 = p.turn.inter ? other[2 * e + 1] : other[2 * e], o1 = p.turn.inter ? other[2 * e] : other[2 * e + 1];
+          A[e] = pack_f32x2(co[2 * e] * own[2 * e], co[2 * e + 1] * own[2 * e + 1]);
+          B[e] = pack_f32x2(si[2 * e] * o0, si[2 * e + 1] * o1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (u >= left) break;
+        uint4 out = raw[u];
+        if (turns) {
+          uint64_t y[4], z[4];
+          rot_unpack<kType>(y, raw[u]);
+          rot_unpack<kType>(z, rot_paired(raw[u], p.turn, ln.partner));
+          float r = 1.f;
+          if (norm) {
+            uint64_t sq = mul_f32x2(y[0], y[0]);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) sq = fma_f32x2(y[e], y[e], sq);
+            float ss = rot_sum(sq);
+#pragma unroll
+            for (int off = 1; off < Lane::kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+          }
+          const uint64_t r2 = pack_f32x2(r, r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = mul_f32x2(fma_f32x2(z[e], B[e], mul_f32x2(y[e], A[e])), r2);
+          out = rot_pack<kType>(y);
+        }
+        if (head + u * Lane::kRows < end && keep) *reinterpret_cast<uint4*>(dst + u * out_step) = out;
+      }
+      head += kBatch * Lane::kRows;
+      left -= kBatch;
+      src += kBatch * in_step;
+      dst += kBatch * out_step;
+    }
+    more = w.next(p);
+    if constexpr (kPaged)
+      if (more && w.token) pg.step(w.s);
   }
 }
 
-struct NoPages {
-  uint16_t *k, *v;
-  int64_t head_step;
-};
 template <int D, int kType>
-__global__ void __launch_bounds__(kRotThreads) attn_norm_rope_kernel(const __grid_constant__ RotParams p) {
+__global__ void __launch_bounds__(kRotThreads, kRotFwdBlocks) attn_norm_rope_kernel(const __grid_constant__ RotParams p) {
   rot_forward_body<D, kType, false>(p, NoPages{});
 }
 
-// Gradient.  A block walks tiles of tokens; its lanes add up g r x of their
-// channels, for q and for k, in fp32 (some hundred rows each), the block's sums
-// are added in shared memory, and a second kernel adds the blocks' in 64 bits:
-// the same from call to call.
+// Gradient, walked the same way.  A lane adds up g r x of its channels, for q and for
+// k, in fp32 (its share's rows, a few hundred at most); the block's sums are added in
+// shared memory, and a second kernel adds the blocks' in 64 bits: the same from call
+// to call.
+constexpr int kRotBwdBlocks = 2;  // blocks an SM
+
+// A run of the gradient: heads of one kind; dw: its weight's sums.
 template <int D, int kType>
-__global__ void __launch_bounds__(kRotThreads) attn_norm_rope_bwd_kernel(const __grid_constant__ RotParams p) {
+__device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWalk& w, const RotLane<D>& ln, const uint64_t* A,
+                                                 const uint64_t* B, const float* w_s, uint64_t* dw) {
   using Lane = RotLane<D>;
-  constexpr int kBatch = 2;
-  __shared__ __align__(16) float cs_s[kRotTokens * D];
+  constexpr int kBatch = 4;
+  int head = (w.g0 - p.first[w.kind]) * Lane::kRows + ln.sub, left = w.g1 - w.g0;
+  const int end = min(p.heads[w.kind], (w.g1 - p.first[w.kind]) * Lane::kRows);
+  const bool norm = p.w[w.kind] != nullptr;
+  const uint16_t* gsrc = rot_at(p.dy[w.kind], w.b, w.s, head, ln.c0);
+  const uint16_t* xsrc = norm ? rot_at(p.in[w.kind], w.b, w.s, head, ln.c0) : gsrc;
+  uint16_t* dst = rot_at(p.out[w.kind], w.b, w.s, head, ln.c0);
+  const int64_t g_step = p.dy[w.kind].head * Lane::kRows, x_step = norm ? p.in[w.kind].head * Lane::kRows : 0,
+                out_step = p.out[w.kind].head * Lane::kRows;
+  uint64_t wt[4];
+  {
+    float own[8];
+    rot_load8(own, w_s + ln.c0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) wt[e] = pack_f32x2(own[2 * e], own[2 * e + 1]);
+  }
+  while (left > 0) {
+    uint4 draw[kBatch], raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      raw[u] = draw[u] = make_uint4(0, 0, 0, 0);
+      if (head + u * Lane::kRows < end) {
+        draw[u] = *reinterpret_cast<const uint4*>(gsrc + u * g_step);
+        if (norm) raw[u] = *reinterpret_cast<const uint4*>(xsrc + u * x_step);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (u >= left) break;
+      const bool there = head + u * Lane::kRows < end;
+      uint64_t g[4], z[4];
+      rot_unpack<kType>(g, draw[u]);
+      rot_unpack<kType>(z, rot_paired(draw[u], p.turn, ln.partner));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = fma_f32x2(z[e], B[e], mul_f32x2(g[e], A[e]));
+      if (norm) {
+        rot_unpack<kType>(z, raw[u]);
+        uint64_t gw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gw[e] = mul_f32x2(g[e], wt[e]);
+        uint64_t sq = mul_f32x2(z[0], z[0]), dt = mul_f32x2(gw[0], z[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) {
+          sq = fma_f32x2(z[e], z[e], sq);
+          dt = fma_f32x2(gw[e], z[e], dt);
+        }
+        float ss = rot_sum(sq), dot = rot_sum(dt);
+#pragma unroll
+        for (int off = 1; off < Lane::kLanes; off <<= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        }
+        const float r = there ? rsqrtf(fmaf(ss, 1.f / D, p.eps)) : 0.f;  // (an eps of 0 is allowed)
+        const float k = -r * r * dot * (1.f / D);
+        const uint64_t r2 = pack_f32x2(r, r), k2 = pack_f32x2(k, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dw[e] = fma_f32x2(g[e], mul_f32x2(r2, z[e]), dw[e]);
+          g[e] = mul_f32x2(r2, fma_f32x2(k2, z[e], gw[e]));
+        }
+      }
+      if (there) *reinterpret_cast<uint4*>(dst + u * out_step) = rot_pack<kType>(g);
+    }
+    head += kBatch * Lane::kRows;
+    left -= kBatch;
+    gsrc += kBatch * g_step;
+    xsrc += kBatch * x_step;
+    dst += kBatch * out_step;
+  }
+}
+
+template <int D, int kType>
+__global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks) attn_norm_rope_bwd_kernel(const __grid_constant__ RotParams p) {
+  using Lane = RotLane<D>;
+  __shared__ __align__(16) float cs_s[kRotWarps][D];
   __shared__ __align__(16) float w_s[2][D];
-  __shared__ int pos_s[kRotTokens];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const Lane ln(lane, p.turn);
-  const int g0 = static_cast<int>(blockIdx.y) * p.per_block;
-  const int ng = min(p.per_block, p.groups[0] + p.groups[1] - g0);
   grid_dependency_wait();
   grid_launch_dependents();
   rot_weights<D, kType>(w_s, p);
-  float dw[2][8];
+  __syncthreads();
+  uint64_t dw[2][4];
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[kv][e] = 0.f;
-  const int n_tiles = p.B * p.tiles;
-  for (int x = static_cast<int>(blockIdx.x); x < n_tiles; x += static_cast<int>(gridDim.x)) {
-    const int b = x / p.tiles, tile = x - b * p.tiles;
-    const int s0 = tile * p.tokens, tokens = min(p.tokens, p.S - s0);
-    int tok = 0, g = warp;
-    while (g >= ng && tok < tokens) g -= ng, ++tok;
-    uint4 raw[kBatch], draw[kBatch];
-    RotItem it[kBatch];
-    const auto fetch = [&]() {
+    for (int e = 0; e < 4; ++e) dw[kv][e] = 0ull;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kRotWarps + warp) * p.share;
+  if (i < p.total) {
+    const RotTable table(lane, p.turn);
+    float* const cs = cs_s[warp];
+    RotWalk w(p, i, min(p.share, p.total - i));
+    uint64_t A[4], B[4];
+    do {
+      if (w.token) {
+        if (p.turn.rot > 0) table.fill(cs, lane, __ldg(p.pos + static_cast<int64_t>(w.b) * p.S + w.s), p.turn);
+        float co[8], si[8];
+        rot_angles<D>(co, si, ln, p.turn, cs);
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        it[u] = rot_item<D>(p, tok, g0 + g, ln.sub, tokens);
-        raw[u] = draw[u] = make_uint4(0, 0, 0, 0);
-        if (it[u].there) {
-          const int kind = it[u].kind;
-          const RotRows& r = p.dy[kind];
-          draw[u] = rot_load<D, kType>(r, b * r.b + (s0 + tok) * r.row + it[u].head * r.head + ln.c0);
-          if (p.w[kind] != nullptr) {
-            const RotRows& q = p.in[kind];
-            raw[u] = rot_load<D, kType>(q, b * q.b + (s0 + tok) * q.row + it[u].head * q.head + ln.c0);
-          }
+        for (int e = 0; e < 4; ++e) {
+          A[e] = pack_f32x2(co[2 * e], co[2 * e + 1]);
+          B[e] = pack_f32x2(-si[2 * e], -si[2 * e + 1]);
         }
-        g += kRotWarps;
-        while (g >= ng && tok < tokens) g -= ng, ++tok;
       }
-    };
-    fetch();
-    __syncthreads();  // the last tile's angles have been used
-    if (tid < tokens) pos_s[tid] = p.pos != nullptr ? __ldg(p.pos + static_cast<int64_t>(b) * p.S + s0 + tid) : 0;
-    __syncthreads();
-    rot_table(cs_s, pos_s, tokens, p.turn);
-    __syncthreads();
-    while (it[0].tok < tokens) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int t = min(it[u].tok, tokens - 1), kind = it[u].kind;
-        float gr[8], y[8];
-        rot_unpack<kType>(gr, draw[u]);
-        if (!p.turn.inter && p.turn.rot > 0) rot_unpack<kType>(y, rot_shuffle(draw[u], ln.partner));
-        if (ln.turned) rot_turn<true>(gr, y, cs_s + t * p.turn.rot, p.turn, ln.sign, ln.at);
-        if (p.w[kind] != nullptr) {
-          float xv[8], ww[8];
-          rot_unpack<kType>(xv, raw[u]);
-          rot_load8(ww, w_s[kind] + ln.c0);
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(xv[e], xv[e], ss);
-            ww[e] *= gr[e];
-            dot = fmaf(ww[e], xv[e], dot);
-          }
-#pragma unroll
-          for (int off = 1; off < Lane::kLanes; off <<= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            dot += __shfl_xor_sync(0xffffffffu, dot, off);
-          }
-          const float r = it[u].there ? rsqrtf(fmaf(ss, 1.f / D, p.eps)) : 0.f;  // (an eps of 0 is allowed)
-          const float k = r * r * dot * (1.f / D);
-          if (kind == 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dw[0][e] = fmaf(gr[e], r * xv[e], dw[0][e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dw[1][e] = fmaf(gr[e], r * xv[e], dw[1][e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) gr[e] = r * fmaf(-k, xv[e], ww[e]);
-        }
-        if (!it[u].there) continue;
-        const RotRows& o = p.out[kind];
-        *reinterpret_cast<uint4*>(o.p + b * o.b + (s0 + t) * o.row + it[u].head * o.head + ln.c0) = rot_pack<kType>(gr);
-      }
-      fetch();
-    }
+      if (w.kind == 0)
+        rot_backward_run<D, kType>(p, w, ln, A, B, w_s[0], dw[0]);
+      else
+        rot_backward_run<D, kType>(p, w, ln, A, B, w_s[1], dw[1]);
+    } while (w.next(p));
   }
   if (p.dw == nullptr) return;
   // the warp's rows, then the block's warps in their order
@@ -395,18 +456,19 @@ __global__ void __launch_bounds__(kRotThreads) attn_norm_rope_bwd_kernel(const _
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float v = dw[kv][e];
+      float v[2];
+      unpack_f32x2(dw[kv][e / 2], v[0], v[1]);
+      float x = v[e % 2];
 #pragma unroll
-      for (int off = Lane::kLanes; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (ln.sub == 0) part_s[warp][kv][ln.c0 + e] = v;
+      for (int off = Lane::kLanes; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (ln.sub == 0) part_s[warp][kv][ln.c0 + e] = x;
     }
   __syncthreads();
-  const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-  for (int i = tid; i < 2 * D; i += kRotThreads) {
+  for (int j = tid; j < 2 * D; j += kRotThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRotWarps; ++w) v += part_s[w][i / D][i % D];
-    p.dw[block * 2 * D + i] = v;
+    for (int x = 0; x < kRotWarps; ++x) v += part_s[x][j / D][j % D];
+    p.dw[static_cast<int64_t>(blockIdx.x) * 2 * D + j] = v;
   }
 }
 
@@ -435,28 +497,21 @@ __global__ void __launch_bounds__(1024) attn_norm_dw_kernel(const float* __restr
 // Host side
 // ---------------------------------------------------------------------------
 
-// Blocks of a pass over rows [B][S]: tokens a block, and parts of the heads
-// (more of both for few rows, so that they fill the SMs: two blocks each).
+// Shares of a pass: one a warp, at most as many warps as the SMs hold at once.
 struct RotGrid {
-  int tokens, tiles, per_block;
-  unsigned parts;
-  int64_t blocks;  // B * tiles
+  int64_t total, share;
+  unsigned blocks;
 };
-RotGrid rot_grid(int B, int S, int groups, int sms) {
+RotGrid rot_grid(int64_t tokens, int groups, int sms, int blocks_per_sm) {
   RotGrid g;
-  g.tokens = std::min(kRotTokens, S);
-  const auto count = [&](int t) { return static_cast<int64_t>(B) * ((S + t - 1) / t); };
-  while (g.tokens > 1 && count(g.tokens) < 2 * sms) g.tokens /= 2;
-  g.blocks = count(g.tokens);
-  g.tiles = (S + g.tokens - 1) / g.tokens;
-  g.parts = 1;
-  if (g.blocks < 2 * sms) g.parts = static_cast<unsigned>((groups + kRotWarps - 1) / kRotWarps);
-  g.per_block = (groups + static_cast<int>(g.parts) - 1) / static_cast<int>(g.parts);
-  g.parts = static_cast<unsigned>((groups + g.per_block - 1) / g.per_block);
+  g.total = tokens * groups;
+  const int64_t warps = static_cast<int64_t>(sms) * blocks_per_sm * kRotWarps;
+  g.share = (g.total + warps - 1) / warps;
+  const int64_t used = g.share > 0 ? (g.total + g.share - 1) / g.share : 0;
+  g.blocks = static_cast<unsigned>((used + kRotWarps - 1) / kRotWarps);
   return g;
 }
 
-constexpr int kRotBwdBlocks = 4;  // blocks an SM that walk the tiles
 
 bool rot_rows_ok(const attn_heads_t* r, int D, attn_status_t* st) {
   *st = r == nullptr || r->ptr == nullptr ? ATTN_ERR_INVALID_ARG
@@ -490,19 +545,15 @@ attn_status_t rot_check_norm(const void* qw, const void* kw, int w_dtype, int dt
   return aligned(qw, a) && aligned(kw, a) ? ATTN_OK : ATTN_ERR_ALIGNMENT;
 }
 
-template <int D>
-void rot_groups(RotParams* p, int H_q, int H_k, int H_v) {
-  const int h[3] = {H_q, H_k, H_v};
+// Heads of q, k and v, and their groups in a token's list; returns the groups.
+int rot_groups(RotParams* p, int D, int H_q, int H_k, int H_v) {
+  const int h[3] = {H_q, H_k, H_v}, rows = 32 / (D / 8);
+  p->first[0] = 0;
   for (int i = 0; i < 3; ++i) {
     p->heads[i] = h[i];
-    p->groups[i] = (h[i] + RotLane<D>::kRows - 1) / RotLane<D>::kRows;
+    p->first[i + 1] = p->first[i] + (h[i] + rows - 1) / rows;
   }
-}
-void rot_groups(RotParams* p, int D, int H_q, int H_k, int H_v) {
-  if (D == 64)
-    rot_groups<64>(p, H_q, H_k, H_v);
-  else
-    rot_groups<128>(p, H_q, H_k, H_v);
+  return p->first[3];
 }
 
 attn_status_t rot_check_shape(int B, int S, int H_q, int H_k, int D, int dtype) {
@@ -512,8 +563,6 @@ attn_status_t rot_check_shape(int B, int S, int H_q, int H_k, int D, int dtype) 
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
-
-int64_t rot_bwd_blocks(const RotGrid& g, int sms) { return std::min<int64_t>(g.blocks, static_cast<int64_t>(kRotBwdBlocks) * sms); }
 
 // (SMs of a GB300: the workspace's size is asked for without a device)
 constexpr int kRotSms = 152;
@@ -547,13 +596,12 @@ attn_status_t attn_qk_norm_rope(const attn_heads_t* q, const attn_heads_t* k, co
   p.w_fp32 = weight_dtype == ATTN_FP32;
   p.eps = eps;
   p.pos = positions;
-  p.B = B, p.S = S;
-  rot_groups(&p, D, H_q, H_k, 0);
-  const RotGrid g = rot_grid(B, S, p.groups[0] + p.groups[1], g_dev_sms[dev].load(std::memory_order_relaxed));
-  p.tokens = g.tokens, p.tiles = g.tiles, p.per_block = g.per_block;
+  p.S = S;
+  const RotGrid g = rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0),
+                             g_dev_sms[dev].load(std::memory_order_relaxed), kRotFwdBlocks);
+  p.total = g.total, p.share = g.share;
   const auto run = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(g.blocks), g.parts), dim3(kRotThreads), 0,
-                      static_cast<cudaStream_t>(stream), p);
+    return launch_pdl(kernel, dim3(g.blocks), dim3(kRotThreads), 0, static_cast<cudaStream_t>(stream), p);
   };
   const bool bf = dtype == ATTN_BF16;
   const cudaError_t e = D == 64 ? (bf ? run(attn_norm_rope_kernel<64, kBF16>) : run(attn_norm_rope_kernel<64, kFP16>))
@@ -565,9 +613,8 @@ uint64_t attn_qk_norm_rope_bwd_workspace_bytes(int B, int S, int H_q, int H_k, i
   if (rot_check_shape(B, S, H_q, H_k, D, ATTN_BF16) != ATTN_OK) return 0;
   if (B == 0 || S == 0) return 16;
   RotParams p{};
-  rot_groups(&p, D, H_q, H_k, 0);
-  const RotGrid g = rot_grid(B, S, p.groups[0] + p.groups[1], kRotSms);
-  return static_cast<uint64_t>(rot_bwd_blocks(g, kRotSms)) * g.parts * 2 * D * sizeof(float);
+  return static_cast<uint64_t>(rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0), kRotSms, kRotBwdBlocks).blocks) * 2 *
+         D * sizeof(float);
 }
 
 attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads_t* dk_out, const attn_heads_t* q,
@@ -599,7 +646,7 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads
   if (st != ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  int64_t blocks = 0;
+  unsigned blocks = 0;
   if (rows) {
     p.dy[0] = rot_rows_of(dq_out), p.dy[1] = rot_rows_of(dk_out);
     if (q_weight != nullptr) p.in[0] = rot_rows_of(q);
@@ -609,17 +656,13 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads
     p.w_fp32 = weight_dtype == ATTN_FP32;
     p.eps = eps;
     p.pos = positions;
-    p.B = B, p.S = S;
-    rot_groups(&p, D, H_q, H_k, 0);
+    p.S = S;
     // (the grid is a GB300's whatever the device has: it sizes the workspace)
-    const RotGrid g = rot_grid(B, S, p.groups[0] + p.groups[1], kRotSms);
-    p.tokens = g.tokens, p.tiles = g.tiles, p.per_block = g.per_block;
+    const RotGrid g = rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0), kRotSms, kRotBwdBlocks);
+    p.total = g.total, p.share = g.share;
     p.dw = norm ? static_cast<float*>(workspace) : nullptr;
-    const int64_t gx = rot_bwd_blocks(g, kRotSms);
-    blocks = gx * g.parts;
-    const auto run = [&](auto kernel) {
-      return launch_pdl(kernel, dim3(static_cast<unsigned>(gx), g.parts), dim3(kRotThreads), 0, s, p);
-    };
+    blocks = g.blocks;
+    const auto run = [&](auto kernel) { return launch_pdl(kernel, dim3(g.blocks), dim3(kRotThreads), 0, s, p); };
     const bool bf = dtype == ATTN_BF16;
     e = D == 64 ? (bf ? run(attn_norm_rope_bwd_kernel<64, kBF16>) : run(attn_norm_rope_bwd_kernel<64, kFP16>))
                 : (bf ? run(attn_norm_rope_bwd_kernel<128, kBF16>) : run(attn_norm_rope_bwd_kernel<128, kFP16>));

@@ -44,32 +44,55 @@ struct PagedSeqs {
   }
 };
 
-// Where an append's rows go, as rot_forward_body asks for it.
+// Where an append's rows go, row by row, as rot_forward_body walks them.
 struct PagedPlaces {
   PagedSeqs s;
   uint16_t *k, *v;
   int64_t head_step;  // page * D: from one key head's rows in a page to the next's
-  // First element of row `row`'s place in its page for key head 0, or -1; its position, and whether it is a sequence's.
-  template <int D>
-  __device__ int64_t place(int row, int* pos, int* live, bool report) const {
-    *pos = *live = 0;
-    const int b = s.sequence(row);
-    if (b >= s.B) return -1;
-    const int i = s.seq_start != nullptr ? row - s.start(b) : 0;
+  // of the row at hand:
+  int64_t to;         // first element of its place in its page, for key head 0, or -1
+  int b, end;         // its sequence, or B, and the row behind its sequence's (or the next to look up)
+  int pos;            // its entry's number
+  __device__ bool live() const { return b < s.B; }
+  __device__ void find(int row) {
+    b = s.sequence(row);
+    to = -1;
+    pos = 0;
+    end = row + 1;
+    if (b >= s.B) return;
+    int i = 0;
+    if (s.seq_start != nullptr) {
+      i = row - s.start(b);
+      end = s.start(b + 1);
+    }
     const int64_t at = static_cast<int64_t>(max(__ldg(s.len + b), 0)) + i;
-    *live = 1;
-    *pos = static_cast<int>(min(at, static_cast<int64_t>(INT_MAX)));
-    if (at >= s.capacity()) {
-      if (report) atomicOr(&g_attn_status, kPagedOverflow);
-      return -1;
+    pos = static_cast<int>(min(at, static_cast<int64_t>(INT_MAX)));
+    place();
+  }
+  // The next row: nearly always the same sequence's next entry.
+  __device__ void step(int row) {
+    if (row >= end || b >= s.B) {
+      find(row);
+      return;
     }
-    const int pg = s.page_of(b, static_cast<int>(at >> s.page_log2));
+    pos = min(pos, INT_MAX - 1) + 1;
+    if (to >= 0 && (pos & ((1 << s.page_log2) - 1)) != 0)
+      to += head_step >> s.page_log2;
+    else
+      place();
+  }
+  __device__ void place() {
+    to = -1;
+    if (pos >= s.capacity()) {
+      atomicOr(&g_attn_status, kPagedOverflow);
+      return;
+    }
+    const int pg = s.page_of(b, pos >> s.page_log2);
     if (pg < 0) {
-      if (report) atomicOr(&g_attn_status, kPagedNoPage);
-      return -1;
+      atomicOr(&g_attn_status, kPagedNoPage);
+      return;
     }
-    const int in_page = static_cast<int>(at) & ((1 << s.page_log2) - 1);
-    return static_cast<int64_t>(pg) * s.H_kv * head_step + static_cast<int64_t>(in_page) * D;
+    to = static_cast<int64_t>(pg) * s.H_kv * head_step + static_cast<int64_t>(pos & ((1 << s.page_log2) - 1)) * (head_step >> s.page_log2);
   }
 };
 
@@ -77,10 +100,10 @@ struct PagedPlaces {
 // is to their pages, and the lengths after it.
 // HBM-bound, 4 bytes a channel.
 template <int D, int kType>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, kRotFwdBlocks)
     attn_paged_append_kernel(const __grid_constant__ RotParams p, const __grid_constant__ PagedPlaces places, int32_t* len_out) {
   rot_forward_body<D, kType, true>(p, places);
-  if (len_out == nullptr || blockIdx.y != 0) return;
+  if (len_out == nullptr) return;
   for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < places.s.B;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t l = static_cast<int64_t>(max(0, __ldg(places.s.len + b))) + places.s.rows_of(static_cast<int>(b));
@@ -156,7 +179,7 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
   if (st != ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedPlaces places{paged_seqs(cache, seq_start, rows), static_cast<uint16_t*>(cache->k_pages),
-                     static_cast<uint16_t*>(cache->v_pages), static_cast<int64_t>(cache->page) * D};
+                     static_cast<uint16_t*>(cache->v_pages), static_cast<int64_t>(cache->page) * D, -1, 0, 0, 0};
   const bool in_place = length_out == cache->length;
   cudaError_t e = cudaSuccess;
   if (rows > 0) {
@@ -172,13 +195,12 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
     p.w[0] = q_weight, p.w[1] = k_weight;
     p.w_fp32 = weight_dtype == ATTN_FP32;
     p.eps = eps;
-    p.B = 1, p.S = static_cast<int>(rows);
-    rot_groups(&p, D, q != nullptr ? H_q : 0, H_kv, H_kv);
-    const RotGrid g = rot_grid(1, p.S, p.groups[0] + p.groups[1] + p.groups[2], g_dev_sms[dev].load(std::memory_order_relaxed));
-    p.tokens = g.tokens, p.tiles = g.tiles, p.per_block = g.per_block;
+    p.S = static_cast<int>(rows);
+    const RotGrid g = rot_grid(rows, rot_groups(&p, D, q != nullptr ? H_q : 0, H_kv, H_kv),
+                               g_dev_sms[dev].load(std::memory_order_relaxed), kRotFwdBlocks);
+    p.total = g.total, p.share = g.share;
     const auto run = [&](auto kernel) {
-      return launch_pdl(kernel, dim3(static_cast<unsigned>(g.blocks), g.parts), dim3(kRotThreads), 0, s, p, places,
-                        in_place ? nullptr : length_out);
+      return launch_pdl(kernel, dim3(g.blocks), dim3(kRotThreads), 0, s, p, places, in_place ? nullptr : length_out);
     };
     const bool bf = cache->dtype == ATTN_BF16;
     e = D == 64 ? (bf ? run(attn_paged_append_kernel<64, kBF16>) : run(attn_paged_append_kernel<64, kFP16>))
