@@ -153,15 +153,15 @@ def load() -> ctypes.CDLL:
             lib.attn_cache4_evict.argtypes = [c4, i, i, i, p, p, p, p, u64, p]
             lib.attn_cache4_evict_workspace_bytes.restype = u64
             lib.attn_cache4_evict_workspace_bytes.argtypes = [i, i, i, i]
-            hp, rp, pp = (ctypes.POINTER(x) for x in (attn_heads_t, attn_rotary_t, attn_pages_t))
+            pp = ctypes.POINTER(attn_pages_t)
             lib.attn_qk_norm_rope.restype = i
-            lib.attn_qk_norm_rope.argtypes = [hp, hp, hp, hp, i, i, i, i, i, i, rp, p, p, p, i, f, p]
+            lib.attn_qk_norm_rope.argtypes = [p, p, p, p, i, i, i, i, i, i, p, p, p, p, i, f, p]
             lib.attn_qk_norm_rope_bwd.restype = i
-            lib.attn_qk_norm_rope_bwd.argtypes = [hp, hp, hp, hp, hp, hp, i, i, i, i, i, i, rp, p, p, p, i, f, p, p, p, u64, p]
+            lib.attn_qk_norm_rope_bwd.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, p, p, p, p, i, f, p, p, p, u64, p]
             lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = u64
             lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, i, i, i]
             lib.attn_paged_append.restype = i
-            lib.attn_paged_append.argtypes = [pp, p, p, i64, i64, i64, p, p, i64, p, i, rp, p, p, i, f, p, p]
+            lib.attn_paged_append.argtypes = [pp, p, p, i64, i64, i64, p, p, i64, p, i, p, p, p, i, f, p, p]
             lib.attn_paged_attend.restype = i
             lib.attn_paged_attend.argtypes = [pp, p, i64, p, p, i64, p, i, f, i, i, i, i, p, u64, p]
             lib.attn_paged_attend_workspace_bytes.restype = u64
@@ -185,6 +185,11 @@ def _addr(x):
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
     return int(x)
+
+
+def _struct(x):
+    """Address of an attn_heads_t or attn_rotary_t, or a plain int/None."""
+    return x if x is None or type(x) is int else ctypes.addressof(x)
 
 
 def _stream(s):
@@ -382,7 +387,7 @@ def attn_qk_norm_rope(q, k, q_out, k_out, B: int, S: int, H_q: int, H_k: int, D:
     """Enqueue the head norm and rotation (see include/attn_fwd.h)."""
     if not _int32(B, S, H_q, H_k, D, dtype, weight_dtype):
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_qk_norm_rope")
-    st = load().attn_qk_norm_rope(q, k, q_out, k_out, B, S, H_q, H_k, D, dtype, rope, _addr(positions), _addr(q_weight),
+    st = load().attn_qk_norm_rope(_struct(q), _struct(k), _struct(q_out), _struct(k_out), B, S, H_q, H_k, D, dtype, _struct(rope), _addr(positions), _addr(q_weight),
                                   _addr(k_weight), weight_dtype, eps, _stream(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_qk_norm_rope")
@@ -394,7 +399,8 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, B: int, S: int, H_q: int
     """Enqueue the gradient of the head norm and rotation (see include/attn_fwd.h)."""
     if not _int32(B, S, H_q, H_k, D, dtype, weight_dtype):
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_qk_norm_rope_bwd")
-    st = load().attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, B, S, H_q, H_k, D, dtype, rope, _addr(positions),
+    st = load().attn_qk_norm_rope_bwd(_struct(dq_out), _struct(dk_out), _struct(q), _struct(k), _struct(dq), _struct(dk), B, S, H_q,
+                                      H_k, D, dtype, _struct(rope), _addr(positions),
                                       _addr(q_weight), _addr(k_weight), weight_dtype, eps, _addr(dq_weight), _addr(dk_weight),
                                       _addr(workspace), workspace_bytes, _stream(stream))
     if st != ATTN_OK:
@@ -412,7 +418,7 @@ def attn_paged_append(cache: attn_pages_t, k, v, rows: int, k_stride: int, v_str
     if not _int32(H_q, weight_dtype):
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_paged_append")
     st = load().attn_paged_append(cache, _addr(k), _addr(v), rows, k_stride, v_stride, _addr(seq_start), _addr(q), q_stride,
-                                  _addr(q_out), H_q, rope, _addr(q_weight), _addr(k_weight), weight_dtype, eps,
+                                  _addr(q_out), H_q, _struct(rope), _addr(q_weight), _addr(k_weight), weight_dtype, eps,
                                   _addr(length_out), _stream(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_append")

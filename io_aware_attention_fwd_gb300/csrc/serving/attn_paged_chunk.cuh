@@ -23,9 +23,10 @@ constexpr int kChunkUnitCost = 2;  // tiles that a unit's start and end count as
 constexpr int kChunkCtas = 152;    // shares (the workspace's size is asked for without a device)
 constexpr int kChunkRows = kQTiles * kBM;
 
-struct ChunkUnit {  // as the list holds it
+struct __align__(16) ChunkUnit {  // as the list holds it
   int64_t before;   // tiles (and costs) of the units before it, for one key head
   int32_t b, i0;    // sequence, first token
+  int32_t row0, n, len, p0;  // as PagedSpan's
 };
 struct ChunkHead {  // the list's head
   int64_t total, share;    // tiles and costs of all key heads; of a CTA
@@ -49,9 +50,20 @@ struct ChunkAt {
   PagedSpan w;       // (n, len, p0 are the sequence's; the tiles are the unit's)
   int b, h, i0, j0, n;
   bool whole;        // all of the unit's tiles
+  // (one read of a list's unit: what the roles wait for where units change)
+  __device__ int64_t load(const ChunkParams& p, const ChunkUnit* unit) {
+    const int4 x = __ldg(reinterpret_cast<const int4*>(unit)), y = __ldg(reinterpret_cast<const int4*>(unit) + 1);
+    b = x.z, i0 = x.w;
+    w.row0 = y.x, w.n = y.y, w.len = y.z, w.p0 = y.w;
+    tiles(p);
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(x.x)) | static_cast<uint64_t>(static_cast<uint32_t>(x.y)) << 32);
+  }
   __device__ void load(const ChunkParams& p, int seq, int first) {
     b = seq, i0 = first;
     w = PagedSpan::of<kBN>(p.a, b);
+    tiles(p);
+  }
+  __device__ void tiles(const ChunkParams& p) {
     const int p0 = w.p0 + i0;
     w.visible<kBN>(p.a, p0, p0 + min(kQTiles * p.tok, w.n - i0));
     w.tiles = max(w.tiles, 1);  // (a unit that sees nothing visits one tile, masked)
@@ -67,31 +79,35 @@ struct ChunkAt {
   }
 };
 
-// A CTA's units.
+// A CTA's units: its share of the list, or one.
 struct ChunkWalk {
-  int64_t x, end, before;  // before: of the unit, in tiles of one head
+  int64_t first, end;  // where the unit's tiles begin in the list, and the share ends
+  int64_t from;        // where the share begins
   int u;
   ChunkAt at;
   bool one;
-  // own: sequence and first token of the CTA's only unit, or -1
-  __device__ ChunkWalk(const ChunkParams& p, const volatile int* own) : x(0), end(0), before(0), u(0), one(p.head == nullptr) {
+  __device__ explicit ChunkWalk(const ChunkParams& p) : first(0), end(0), from(0), u(0), one(p.head == nullptr) {
+    at.h = -1;
+    at.w.tiles = 0;
     if (one) return;
     const int64_t total = __ldg(&p.head->total), share = __ldg(&p.head->share);
-    x = static_cast<int64_t>(blockIdx.x) * share;
-    end = min(x + share, total);
-    if (x < end) {
-      u = __ldg(&p.head->start[blockIdx.x]);
-      fetch(p);
+    from = static_cast<int64_t>(blockIdx.x) * share;
+    end = min(from + share, total);
+    if (from >= end) {
+      end = 0;
+      return;
     }
+    u = __ldg(&p.head->start[blockIdx.x]);
+    const int64_t unit = at.load(p, p.units + u) * p.a.s.H_kv;
+    const int per = at.w.tiles + kChunkUnitCost;
+    const int h = static_cast<int>((from - unit) / per);  // the key head that the share begins in
+    at.h = h - 1;
+    first = unit + static_cast<int64_t>(h - 1) * per + kChunkUnitCost;
   }
-  __device__ void fetch(const ChunkParams& p) {
-    before = __ldg(&p.units[u].before);
-    at.load(p, __ldg(&p.units[u].b), __ldg(&p.units[u].i0));
-  }
+  // The next unit, or false.  own: sequence and first token of the CTA's only one, or -1.
   __device__ bool next(const ChunkParams& p, const volatile int* own) {
     if (one) {
-      if (x != 0 || own[0] < 0) return false;
-      x = 1;
+      if (at.h >= 0 || own[0] < 0) return false;
       at.load(p, own[0], own[1]);
       at.h = static_cast<int>(blockIdx.x) % p.a.s.H_kv;
       at.j0 = 0;
@@ -99,26 +115,19 @@ struct ChunkWalk {
       at.whole = true;
       return true;
     }
-    while (x < end) {
-      const int per = at.w.tiles + kChunkUnitCost, H = p.a.s.H_kv;
-      const int64_t first = before * H, h = (x - first) / per;
-      if (h >= H) {
+    while (true) {
+      first += at.w.tiles + kChunkUnitCost;
+      if (first >= end) return false;  // (also where the share is empty)
+      if (++at.h == p.a.s.H_kv) {
         ++u;
-        fetch(p);
-        continue;
+        at.load(p, p.units + u);
+        at.h = 0;
       }
-      const int64_t x0 = first + h * per + kChunkUnitCost;
-      const int j0 = static_cast<int>(max(static_cast<int64_t>(0), x - x0));
-      const int j1 = static_cast<int>(min(static_cast<int64_t>(at.w.tiles), end - x0));
-      x = x0 + at.w.tiles;
-      if (j0 >= j1) continue;
-      at.h = static_cast<int>(h);
-      at.j0 = j0;
-      at.n = j1 - j0;
+      at.j0 = static_cast<int>(max(static_cast<int64_t>(0), from - first));
+      at.n = static_cast<int>(min(static_cast<int64_t>(at.w.tiles), end - first)) - at.j0;
       at.whole = at.n == at.w.tiles;
-      return true;
+      if (at.n > 0) return true;
     }
-    return false;
   }
 };
 
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             }
             if (mine > 0 && u < cap) {
               const int64_t before = at + incl - mine;
-              units[u] = ChunkUnit{before, b, static_cast<int>(i0)};
+              units[u] = ChunkUnit{before, b, static_cast<int>(i0), w.row0, w.n, w.len, w.p0};
               if (u == cap - 1) end_s = (before + mine) * p.a.s.H_kv;
               const int64_t lo = before * p.a.s.H_kv, hi = (before + mine) * p.a.s.H_kv;
               for (int64_t c2 = (lo + share - 1) / share; c2 < kChunkCtas && c2 * share < hi; ++c2) head->start[c2] = u;
@@ -247,7 +256,7 @@ __device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* ow
   int it = 0, k = 0;
   bool ok = true, missing = false;
   const uint64_t pol_first = l2_evict_first();
-  ChunkWalk us(p, own);
+  ChunkWalk us(p);
   while (ok && us.next(p, own)) {
     const ChunkAt& un = us.at;
     if (k > 0) {
@@ -264,36 +273,40 @@ __device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* ow
     }
     ++k;
     const int p0 = un.w.p0 + un.i0, p1 = un.w.p0 + min(un.i0 + kQTiles * p.tok, un.w.n) - 1;
-    // where this lane's box of the unit's tile i lies
-    const auto place = [&](int i, int* y) {
+    // Whether this lane's box of the unit's tile i is needed, and its entry in the table.
+    // That is asked for a tile ahead and looked at only then: an instruction that needs
+    // it would hold the warp up for the time that it travels.
+    const auto needed = [&](int i) {
       const int key = un.w.tile(i) * kBN + (box << p.box_log2);
-      int z = p.missing;
-      *y = key & page_mask;
-      if (mine && key < un.w.len && paged_seen(p.a, key, key + p.box_rows, p0, p1)) {
-        const int pg = p.a.s.page_of(un.b, key >> p.a.s.page_log2);
-        if (pg >= 0)
-          z = pg * p.a.s.H_kv + un.h;
-        else
-          missing = true;
-      }
-      return z;
+      return mine && i < un.j0 + un.n && key < un.w.len && paged_seen(p.a, key, key + p.box_rows, p0, p1);
     };
-    int y, z = place(un.j0, &y);
+    const auto entry = [&](int i) {
+      const int block = (un.w.tile(i) * kBN + (box << p.box_log2)) >> p.a.s.page_log2;
+      return needed(i) ? __ldg(p.a.s.table + static_cast<int64_t>(un.b) * p.a.s.max_pages + block) : -1;
+    };
+    int pg = entry(un.j0);
     for (int j = 0; j < un.n && ok; ++j) {
-      int y2 = 0, z2 = 0;
-      if (j + 1 < un.n) z2 = place(un.j0 + j + 1, &y2);  // its table entry travels meanwhile
+      const int next = entry(un.j0 + j + 1);
+      const int y = (un.w.tile(un.j0 + j) * kBN + (box << p.box_log2)) & page_mask;
+      int z = p.missing;
       for (int kv = 0; kv < 2; ++kv) {
         const int s = it % C::kSlots, round = it / C::kSlots;
         if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(sm.bar_empty(s), (round - 1) & 1, wc))) {
           ok = false;
           break;
         }
+        if (kv == 0) {
+          if (pg >= 0 && pg < p.a.s.n_pages)
+            z = pg * p.a.s.H_kv + un.h;
+          else
+            missing |= needed(un.j0 + j);
+        }
         if (lane == 0) mbar_expect_tx(sm.bar_full(s), C::kTileBytes);
         __syncwarp();
         if (mine) tma_load_3d(sm.slot(s) + dst, kv ? tmV : tmK, sm.bar_full(s), panel * C::kBoxCols, y, z);
         ++it;
       }
-      y = y2, z = z2;
+      pg = next;
     }
   }
   if (missing) atomicOr(&g_attn_status, kPagedNoPage);
@@ -321,10 +334,12 @@ __device__ void chunk_mma_role(const Smem<D, false>& sm, const volatile int* own
   int k = 0;
   int pc[kQTiles] = {0, 0};
   bool ok = true, issued = false;
-  ChunkWalk us(p, own);
+  ChunkWalk us(p);
   while (ok && us.next(p, own)) {
     const int n = us.at.n;
     const int nkv[kQTiles] = {us.at.nkv(p, 0), us.at.nkv(p, 1)};
+    // rows of the last tile at hand that lie behind the sequence
+    const int past = min((us.at.w.tile(us.at.j0 + n - 1) + 1) * kBN - us.at.w.len, kBN);
     const int sk0 = it % C::kSlots;
     ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_q(), k & 1, w) &&
                                      mbar_wait(sm.bar_full(sk0), (it / C::kSlots) & 1, w));
@@ -345,8 +360,7 @@ __device__ void chunk_mma_role(const Smem<D, false>& sm, const volatile int* own
       const bool has_next = j + 1 < n;
       ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_full(sv), (iv / C::kSlots) & 1, w) &&
                                        (!has_next || mbar_wait(sm.bar_full(skn), (ik / C::kSlots) & 1, w)));
-      const int past = min((us.at.w.tile(us.at.j0 + j) + 1) * kBN - us.at.w.len, kBN);  // rows of this tile behind the sequence
-      if (ok && past > 0) {  // (at most one tile of a unit)
+      if (ok && !has_next && past > 0) {
         for (int pn = 0; pn < C::kPanels; ++pn) {
           const uint32_t end = sm.slot(sv) + static_cast<uint32_t>((pn + 1) * kPanelBytes);
           for (uint32_t a = end - static_cast<uint32_t>(past * 128 - lane * 16); a < end; a += 32 * 16)
@@ -407,18 +421,22 @@ __device__ void chunk_softmax_role(const Smem<D, false>& sm, const volatile int*
   int sbase = 0;
   int k = 0;
   bool ok = true;
-  ChunkWalk us(p, own);
+  ChunkWalk us(p);
   while (ok && us.next(p, own)) {
     const int nkv = us.at.nkv(p, t), n_other = us.at.nkv(p, 1 - t);
     const int first = us.at.w.p0 + us.at.i0 + t * p.tok;  // positions of the tile's first and last token, and this row's
     const int last = us.at.w.p0 + min(us.at.i0 + (t + 1) * p.tok, us.at.w.n) - 1, pos = first + tok;
+    // Of the tiles at hand, full0 .. full1 - 1 are seen whole by every token here: those of
+    // the list's second part from the last token's window on and up to the first token.
+    const int shift = us.at.w.first_tiles - us.at.w.from - us.at.j0;  // number at hand of the part's key tile k is k + shift
+    const int full0 = max(us.at.w.first_tiles - us.at.j0, (max(0, last - p.a.window + 1) + kBN - 1) / kBN + shift);
+    const int full1 = max(0, first + 1) / kBN + shift;
     const int steps = nkv + n_other;
     int step = sbase + t;
 
     float m_c = -INFINITY;
     float l = 0.f;
     for (int j = 0; j < nkv; ++j) {
-      const int key0 = us.at.w.tile(us.at.j0 + j) * kBN;
       ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_s(t), cnt & 1, w) &&
                                        (!C::kTurn || step == 0 || mbar_wait(sm.bar_turn(), (step - 1) & 1, w)));
       if (!ok) break;
@@ -434,11 +452,16 @@ __device__ void chunk_softmax_role(const Smem<D, false>& sm, const volatile int*
 #pragma unroll
       for (int i = 0; i < kBN; ++i) s[i] = __uint_as_float(sr[i]);
 
-      if (!paged_all_seen(p.a, key0, key0 + kBN, first, last)) {
+      if (j < full0) {
         // keys i < hi of the tile that are at or behind lo, or before sinks
+        const int key0 = us.at.w.tile(us.at.j0 + j) * kBN;
         const int hi = pos + 1 - key0, lo = pos - p.a.window + 1 - key0, sinks = p.a.sinks - key0;
 #pragma unroll
         for (int i = 0; i < kBN; ++i) s[i] = (i < hi && (i >= lo || i < sinks)) ? s[i] : -INFINITY;
+      } else if (j >= full1) {
+        const int hi = pos + 1 - us.at.w.tile(us.at.j0 + j) * kBN;
+#pragma unroll
+        for (int i = 0; i < kBN; ++i) s[i] = i < hi ? s[i] : -INFINITY;
       }
       float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -549,7 +572,7 @@ __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int
   int cnt[kQTiles] = {0, 0};
   int k = 0;
   bool ok = true;
-  ChunkWalk us(p, own);
+  ChunkWalk us(p);
   while (ok && us.next(p, own)) {
 #pragma unroll
     for (int t = 0; t < kQTiles; ++t) {
@@ -772,9 +795,8 @@ __global__ void __launch_bounds__(256) attn_paged_chunk_merge(const __grid_const
   const int64_t c = blockIdx.x, total = __ldg(&p.head->total), share = __ldg(&p.head->share), x = c * share;
   if (c == 0 || x >= total) return;
   const int u = __ldg(&p.head->start[c]);
-  const int64_t before = __ldg(&p.units[u].before) * p.a.s.H_kv;
   ChunkAt un;
-  un.load(p, __ldg(&p.units[u].b), __ldg(&p.units[u].i0));
+  const int64_t before = un.load(p, p.units + u) * p.a.s.H_kv;
   const int per = un.w.tiles + kChunkUnitCost;
   const int64_t h = (x - before) / per, x0 = before + h * per + kChunkUnitCost;
   const int64_t ca = x0 / share, cb = (x0 + un.w.tiles - 1) / share;

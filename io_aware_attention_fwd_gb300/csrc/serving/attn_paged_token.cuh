@@ -286,33 +286,35 @@ __device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, const CUtensorM
   bool more = kDirect ? true : k.next(p.a);
   while (more && ok) {
     const int p1 = k.w.p0 + k.w.n - 1;
-    // where this lane's box of the list's tile i lies
-    const auto place = [&](int i, int* y) {
+    // Whether this lane's box of the list's tile i is needed, and its entry in the table.
+    // That is asked for two tiles ahead and looked at only then: an instruction that
+    // needs it would hold the warp up for the time that it travels.
+    const auto needed = [&](int i) {
       const int key = k.w.tile(i) * kTokTile + (box << p.box_log2);
-      int z = p.missing;
-      *y = key & page_mask;
-      if (mine && key < k.w.len && paged_seen(p.a, key, key + p.box_rows, k.w.p0, p1)) {
-        const int pg = p.a.s.page_of(k.b, key >> p.a.s.page_log2);
-        if (pg >= 0)
-          z = pg * p.a.s.H_kv + k.h;
-        else
-          missing = true;
-      }
-      return z;
+      return mine && i < k.t1 && key < k.w.len && paged_seen(p.a, key, key + p.box_rows, k.w.p0, p1);
     };
-    int y = 0, z = k.t0 < k.t1 ? place(k.t0, &y) : 0;
+    const auto entry = [&](int i) {
+      const int block = (k.w.tile(i) * kTokTile + (box << p.box_log2)) >> p.a.s.page_log2;
+      return needed(i) ? __ldg(p.a.s.table + static_cast<int64_t>(k.b) * p.a.s.max_pages + block) : -1;
+    };
+    int pg = entry(k.t0), pg1 = entry(k.t0 + 1);
     for (int i = k.t0; i < k.t1 && ok; ++i, ++it) {
-      int y2 = 0, z2 = 0;
-      if (i + 1 < k.t1) z2 = place(i + 1, &y2);  // its table entry travels meanwhile
+      const int pg2 = entry(i + 2);
       const int s = it % C::kStages;
       const uint32_t full = base + C::kBar + 8 * s;
       if (it >= C::kStages)
         ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * C::kStages, (it / C::kStages - 1) & 1, wc));
       if (!ok) break;
+      const int y = (k.w.tile(i) * kTokTile + (box << p.box_log2)) & page_mask;
+      int z = p.missing;
+      if (pg >= 0 && pg < p.a.s.n_pages)
+        z = pg * p.a.s.H_kv + k.h;
+      else
+        missing |= needed(i);
       if (lane == 0) mbar_expect_tx(full, C::kStage);
       __syncwarp();
       if (mine) tma_load_3d(dst0 + s * C::kStage, map, full, panel * 64, y, z);
-      y = y2, z = z2;
+      pg = pg1, pg1 = pg2;
     }
     more = kDirect ? false : k.next(p.a);
   }

@@ -9,7 +9,7 @@ import math
 
 from . import _lib
 from .api import check_int32, check_out, current_handle, element_type, on_stream, row_stride
-from .rotary import norm_weights, rope_struct
+from .rotary import norm_weights, rope_address
 
 
 class PagedKVCache:
@@ -123,7 +123,7 @@ class PagedKVCache:
                 check_out(q_out, q_shape, dtype, device, "q_out")
         elif q_out is not None or q_weight is not None:
             raise ValueError("q_out and q_weight go with q")
-        r = rope_struct(rope, device)
+        r = rope_address(rope, device)
         qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device, D)
         if length_out is None:
             length_out = self.length

@@ -5,13 +5,14 @@ library's.
 """
 from __future__ import annotations
 
+import ctypes
 import math
-from fractions import Fraction
 
 from . import _lib
 from .api import current_handle, element_type, on_stream
 
-_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582")
+# 2^256 / (2 pi), from 75 digits of pi
+_TURN = 2 ** 256 * 10 ** 75 // (2 * 3141592653589793238462643383279502884197169399375105820974944592307816406286)
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -53,7 +54,7 @@ class Rotary:
     of a turn, so that angles are exact at every position.
     """
 
-    __slots__ = ("frequencies", "turns", "rot", "interleaved", "amplitude", "device", "_c")
+    __slots__ = ("frequencies", "turns", "rot", "interleaved", "amplitude", "device", "_c", "_address")
 
     def __init__(self, frequencies, interleaved: bool = False, amplitude: float = 1.0, device="cuda"):
         import torch
@@ -63,13 +64,15 @@ class Rotary:
             raise ValueError("frequencies and amplitude must be finite")
         if len(f) % 8:
             raise ValueError("there must be a multiple of 8 frequencies (16 channels)")
-        bits = [round(Fraction(x) * 2 ** 64 / _TWO_PI) % 2 ** 64 for x in f]
+        # f / (2 pi) * 2^64, rounded down, modulo 2^64: f is n / d exactly
+        bits = [(n * _TURN // d >> 192) % 2 ** 64 for n, d in (x.as_integer_ratio() for x in f)]
         turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in bits], dtype=torch.int64).to(device)
         fixed = object.__setattr__
         for name, value in (("frequencies", f), ("turns", turns), ("rot", 2 * len(f)), ("interleaved", bool(interleaved)),
                             ("amplitude", float(amplitude)), ("device", turns.device)):
             fixed(self, name, value)
         fixed(self, "_c", _lib.attn_rotary_t(turns.data_ptr() if f else None, self.rot, int(self.interleaved), self.amplitude))
+        fixed(self, "_address", ctypes.addressof(self._c))
 
     def __setattr__(self, name, value):
         raise AttributeError("a Rotary does not change")
@@ -81,57 +84,79 @@ class Rotary:
         return type(self), (self.frequencies, self.interleaved, self.amplitude, self.device)
 
 
-def rope_struct(rope, device):
-    """The struct a call passes on for a Rotary, or None."""
+# As the serving calls, these are made once a layer and token: attributes are read once,
+# addresses are passed as numbers, and the four rows' strides go over in one array.
+
+def rope_address(rope, device):
+    """The address of the struct a call passes on for a Rotary, or None."""
     if rope is None:
         return None
     if rope.device != device:
         raise ValueError(f"the rotation is on {rope.device}, the tensors are on {device}")
-    return rope._c
+    return rope._address
+
+
+def check_weight(w, dtype, device, D, name) -> int:
+    """attn_dtype_t of a norm's weight."""
+    import torch
+
+    kind = w.dtype
+    if w.shape != (D,) or w.device != device or not w.is_contiguous() or (kind != dtype and kind != torch.float32):
+        raise ValueError(f"{name} must be a contiguous tensor of {D} entries on {device}, {dtype} or float32")
+    return element_type(kind, True)
 
 
 def norm_weights(q_weight, k_weight, dtype, device, D):
     """(address of q's, of k's, attn_dtype_t of both)."""
-    import torch
-
-    code = None
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is None:
-            continue
-        if w.shape != (D,) or w.device != device or not w.is_contiguous() or w.dtype not in (dtype, torch.float32):
-            raise ValueError(f"{name} must be a contiguous tensor of {D} entries on {device}, {dtype} or float32")
-        if code is not None and w.dtype != q_weight.dtype:
-            raise TypeError("q_weight and k_weight must be of one type")
-        code = element_type(w.dtype, True)
-    return (None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            _lib.ATTN_FP32 if code is None else code)
+    if q_weight is None:
+        return None, *((None, _lib.ATTN_FP32) if k_weight is None else
+                       (k_weight.data_ptr(), check_weight(k_weight, dtype, device, D, "k_weight")))
+    code = check_weight(q_weight, dtype, device, D, "q_weight")
+    if k_weight is None:
+        return q_weight.data_ptr(), None, code
+    if check_weight(k_weight, dtype, device, D, "k_weight") != code:
+        raise TypeError("q_weight and k_weight must be of one type")
+    return q_weight.data_ptr(), k_weight.data_ptr(), code
 
 
 def _heads(t, shape, dtype, device, name, out=False):
-    """attn_heads_t of rows [S, H, D] or [B, S, H, D]."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    """What attn_heads_t holds of rows [S, H, D] or [B, S, H, D]: address, strides."""
+    if t.dtype != dtype or t.device != device or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on {device}")
     stride = t.stride()
-    if stride[-1] != 1:
-        raise ValueError(f"{name}: the channels of a head must be contiguous")
-    if out and any(n > 1 and s == 0 for n, s in zip(shape, stride)):
-        raise ValueError(f"{name}: rows of an output must lie apart")
-    b, s, h = stride[:3] if len(shape) == 4 else (0, stride[0], stride[1])
     # where there is one of something, its stride says nothing (and may be anything)
-    if len(shape) == 4 and shape[0] < 2:
+    if len(stride) == 4:
+        n, S, H, _ = shape
+        b, s, h, one = stride
+        if n < 2:
+            b = 0
+        elif out and b == 0:
+            raise ValueError(f"{name}: rows of an output must lie apart")
+    else:
+        S, H, _ = shape
+        s, h, one = stride
         b = 0
-    if shape[-3] < 2:
+    if S < 2:
         s = 0
-    if shape[-2] < 2:
+    elif out and s == 0:
+        raise ValueError(f"{name}: rows of an output must lie apart")
+    if H < 2:
         h = 0
-    return _lib.attn_heads_t(t.data_ptr(), b, s, h)
+    elif out and h == 0:
+        raise ValueError(f"{name}: rows of an output must lie apart")
+    if one != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return t.data_ptr(), b, s, h
 
 
-def _shapes(q, k, what="q and k"):
+_Rows4 = ctypes.c_int64 * 16  # four attn_heads_t
+_Rows6 = ctypes.c_int64 * 24
+
+
+def _shapes(a, b):
     """(B, S, H_q, H_k, D) of rows [S, H, D] or [B, S, H, D]."""
-    a, b = q.shape, k.shape
     if len(a) not in (3, 4) or len(b) != len(a) or a[:-2] != b[:-2] or a[-1] != b[-1] or a[-2] < 1 or b[-2] < 1:
-        raise ValueError(f"{what} must be [S, H, D] or [B, S, H, D] with the same rows and D")
+        raise ValueError("q and k must be [S, H, D] or [B, S, H, D] with the same rows and D")
     return (a[0] if len(a) == 4 else 1), a[-3], a[-2], b[-2], a[-1]
 
 
@@ -142,7 +167,7 @@ def _positions(positions, rope, shape, device):
         if rope is not None and rope.rot:
             raise ValueError("positions are needed for a rotation")
         return None
-    if positions.shape != shape or positions.dtype != torch.int32 or positions.device != device or not positions.is_contiguous():
+    if positions.dtype != torch.int32 or positions.device != device or positions.shape != shape or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous int32 tensor {tuple(shape)} on {device}")
     return positions.data_ptr()
 
@@ -160,14 +185,13 @@ def qk_norm_rope(q, k, rope, positions=None, q_weight=None, k_weight=None, eps: 
     """
     import torch
 
-    B, S, H_q, H_k, D = _shapes(q, k)
-    dtype, device = q.dtype, q.device
+    shape, k_shape, dtype, device = q.shape, k.shape, q.dtype, q.device
+    B, S, H_q, H_k, D = _shapes(shape, k_shape)
     code = element_type(dtype)
     if device.type != "cuda":
         raise ValueError("q and k must be CUDA tensors of one device")
-    shape, k_shape = q.shape, k.shape
     hq, hk = _heads(q, shape, dtype, device, "q"), _heads(k, k_shape, dtype, device, "k")
-    r = rope_struct(rope, device)
+    r = rope_address(rope, device)
     pos = _positions(positions, rope, shape[:-2], device)
     qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device, D)
     handle = current_handle(device) if stream is None else None
@@ -177,9 +201,9 @@ def qk_norm_rope(q, k, rope, positions=None, q_weight=None, k_weight=None, eps: 
         q_out = torch.empty(shape, dtype=dtype, device=device)
     if k_out is None:
         k_out = torch.empty(k_shape, dtype=dtype, device=device)
-    _lib.attn_qk_norm_rope(hq, hk, _heads(q_out, shape, dtype, device, "q_out", True),
-                           _heads(k_out, k_shape, dtype, device, "k_out", True), B, S, H_q, H_k, D, code, r, pos, qw, kw, w_code,
-                           eps, handle)
+    rows = _Rows4(*hq, *hk, *_heads(q_out, shape, dtype, device, "q_out", True), *_heads(k_out, k_shape, dtype, device, "k_out", True))
+    at = ctypes.addressof(rows)
+    _lib.attn_qk_norm_rope(at, at + 32, at + 64, at + 96, B, S, H_q, H_k, D, code, r, pos, qw, kw, w_code, eps, handle)
     return q_out, k_out
 
 
@@ -194,15 +218,14 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, rope, positions=None, q_weight=N
     """
     import torch
 
-    B, S, H_q, H_k, D = _shapes(q, k)
-    dtype, device = q.dtype, q.device
+    shape, k_shape, dtype, device = q.shape, k.shape, q.dtype, q.device
+    B, S, H_q, H_k, D = _shapes(shape, k_shape)
     code = element_type(dtype)
     if device.type != "cuda":
         raise ValueError("q and k must be CUDA tensors of one device")
-    shape, k_shape = q.shape, k.shape
     hq, hk = _heads(q, shape, dtype, device, "q"), _heads(k, k_shape, dtype, device, "k")
     gq, gk = _heads(dq_out, shape, dtype, device, "dq_out"), _heads(dk_out, k_shape, dtype, device, "dk_out")
-    r = rope_struct(rope, device)
+    r = rope_address(rope, device)
     pos = _positions(positions, rope, shape[:-2], device)
     qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device, D)
     handle = current_handle(device) if stream is None else None
@@ -218,7 +241,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, rope, positions=None, q_weight=N
     if qw is not None or kw is not None:
         nbytes = _lib.attn_qk_norm_rope_bwd_workspace_bytes(B, S, H_q, H_k, D)
         ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    _lib.attn_qk_norm_rope_bwd(gq, gk, hq, hk, _heads(dq, shape, dtype, device, "dq", True),
-                               _heads(dk, k_shape, dtype, device, "dk", True), B, S, H_q, H_k, D, code, r, pos, qw, kw, w_code, eps,
-                               dqw, dkw, ws, nbytes, handle)
+    rows = _Rows6(*gq, *gk, *hq, *hk, *_heads(dq, shape, dtype, device, "dq", True), *_heads(dk, k_shape, dtype, device, "dk", True))
+    at = ctypes.addressof(rows)
+    _lib.attn_qk_norm_rope_bwd(at, at + 32, at + 64, at + 96, at + 128, at + 160, B, S, H_q, H_k, D, code, r, pos, qw, kw, w_code,
+                               eps, dqw, dkw, ws, nbytes, handle)
     return dq, dk, dqw, dkw

@@ -250,7 +250,7 @@ def test_token_pages_out_of_the_window_are_not_read():
 def test_missing_pages_read_as_zeros_and_are_reported():
     for lens in ([200, 90], [5000, 90]):
         cache = make_cache(lens, [0, 0], 2, 64, 16, torch.bfloat16, seed=2)
-        cache.page_table[0, 3], cache.page_table[0, 5], cache.page_table[1, 0] = -1, cache.n_pages, (1 << 31) - 1
+        cache.page_table[0, 3], cache.page_table[0, 5], cache.page_table[0, 7], cache.page_table[1, 0] = -1, cache.n_pages, -(1 << 31), (1 << 31) - 1
         q = queries(2, 4, 64, torch.bfloat16)
         got = cache.attend(q)
         torch.cuda.synchronize()

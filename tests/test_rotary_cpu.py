@@ -71,9 +71,11 @@ def test_workspace_size():
     size = attn.attn_qk_norm_rope_bwd_workspace_bytes
     for bad in ((-1, 8, 4, 4, 64), (1, -8, 4, 4, 64), (1, 8, 0, 4, 64), (1, 8, 4, 4, 80), (1, 8, 4, 65536, 64), (1, 1 << 31, 4, 4, 64)):
         assert size(*bad) == 0
-    # two rows of D sums a block, four blocks an SM at most
-    assert size(2, 8192, 32, 8, 128) == 4 * 152 * 2 * 128 * 4
+    # two rows of D sums a block, of which there are no more than the SMs hold at once
     assert size(1, 1, 1, 1, 64) == 2 * 64 * 4
+    for rows in (1, 40, 8192, 1 << 20):
+        n = size(2, rows, 32, 8, 128)
+        assert n % (2 * 128 * 4) == 0 and 0 < n <= 8 * 152 * 2 * 128 * 4
 
 
 def test_python_calls_check_their_tensors():
