@@ -19,7 +19,8 @@
 
 namespace {
 
-constexpr int kChunkUnitCost = 2;  // tiles that a unit's start and end count as
+constexpr int kChunkUnitCost = 4;  // tiles that a unit's start and end count as
+constexpr int kChunkLeast = 4;     // tiles of a unit that are cut off, at least
 constexpr int kChunkCtas = 152;    // shares (the workspace's size is asked for without a device)
 constexpr int kChunkRows = kQTiles * kBM;
 
@@ -32,6 +33,18 @@ struct ChunkHead {  // the list's head
   int64_t total, share;    // tiles and costs of all key heads; of a CTA
   int32_t start[kChunkCtas];  // unit in which each share begins
 };
+
+// Where a share's end cuts a unit of `tiles` tiles, `v` tiles behind its first one: not
+// within kChunkLeast of its ends, where the piece would cost more than it brings.
+__device__ __forceinline__ int chunk_cut(int64_t v, int tiles) {
+  return v < min(kChunkLeast, tiles) ? 0 : v > tiles - kChunkLeast ? tiles : static_cast<int>(v);
+}
+// First float of column c (a multiple of 4) of row r in a partial's O: blocks of 32 rows
+// x 32 columns, as the epilogue's staging buffer holds them, 16-byte pieces swapped.
+template <int D>
+__device__ __forceinline__ int chunk_part_at(int r, int c) {
+  return ((r >> 5) * (D / 32) + (c >> 5)) * 1024 + (r & 31) * 32 + ((((c >> 2) & 7) ^ (r & 7)) << 2);
+}
 
 struct ChunkParams {
   PagedAttn a;
@@ -123,8 +136,8 @@ struct ChunkWalk {
         at.load(p, p.units + u);
         at.h = 0;
       }
-      at.j0 = static_cast<int>(max(static_cast<int64_t>(0), from - first));
-      at.n = static_cast<int>(min(static_cast<int64_t>(at.w.tiles), end - first)) - at.j0;
+      at.j0 = chunk_cut(from - first, at.w.tiles);
+      at.n = chunk_cut(end - first, at.w.tiles) - at.j0;
       at.whole = at.n == at.w.tiles;
       if (at.n > 0) return true;
     }
@@ -259,19 +272,6 @@ __device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* ow
   ChunkWalk us(p);
   while (ok && us.next(p, own)) {
     const ChunkAt& un = us.at;
-    if (k > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_qfree(0), (k - 1) & 1, wc) && mbar_wait(sm.bar_qfree(1), (k - 1) & 1, wc));
-      if (!ok) break;
-    }
-    if (lane == 0) {
-      mbar_expect_tx(sm.bar_q(), static_cast<uint32_t>(kQTiles * C::kPanels * p.rows * 128));
-      for (int t = 0; t < kQTiles; ++t) {
-        const int i0 = un.i0 + t * p.tok < un.w.n ? un.i0 + t * p.tok : un.i0;  // a tile past the end reloads tile 0
-        for (int pn = 0; pn < C::kPanels; ++pn)
-          tma_load_3d_hint(sm.q(t) + pn * kPanelBytes, tmQ, sm.bar_q(), pn * C::kBoxCols, un.h * p.a.G, un.w.row0 + i0, pol_first);
-      }
-    }
-    ++k;
     const int p0 = un.w.p0 + un.i0, p1 = un.w.p0 + min(un.i0 + kQTiles * p.tok, un.w.n) - 1;
     // Whether this lane's box of the unit's tile i is needed, and its entry in the table.
     // That is asked for a tile ahead and looked at only then: an instruction that needs
@@ -285,6 +285,19 @@ __device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* ow
       return needed(i) ? __ldg(p.a.s.table + static_cast<int64_t>(un.b) * p.a.s.max_pages + block) : -1;
     };
     int pg = entry(un.j0);
+    if (k > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_qfree(0), (k - 1) & 1, wc) && mbar_wait(sm.bar_qfree(1), (k - 1) & 1, wc));
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      mbar_expect_tx(sm.bar_q(), static_cast<uint32_t>(kQTiles * C::kPanels * p.rows * 128));
+      for (int t = 0; t < kQTiles; ++t) {
+        const int i0 = un.i0 + t * p.tok < un.w.n ? un.i0 + t * p.tok : un.i0;  // a tile past the end reloads tile 0
+        for (int pn = 0; pn < C::kPanels; ++pn)
+          tma_load_3d_hint(sm.q(t) + pn * kPanelBytes, tmQ, sm.bar_q(), pn * C::kBoxCols, un.h * p.a.G, un.w.row0 + i0, pol_first);
+      }
+    }
+    ++k;
     for (int j = 0; j < un.n && ok; ++j) {
       const int next = entry(un.j0 + j + 1);
       const int y = (un.w.tile(un.j0 + j) * kBN + (box << p.box_log2)) & page_mask;
@@ -556,8 +569,14 @@ __device__ __forceinline__ float chunk_lse(float m, float l) {
   return l == 0.f ? -INFINITY : l2 * kLn2;
 }
 
+// shared -> global copy of contiguous bytes (both sides 16-byte aligned)
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 // Epilogue warpgroup, as varlen_epilogue_role; a unit that a share's end cut leaves
-// O in fp32, undivided, and (m, l), 32 columns a turn of the staging buffer.
+// O in fp32, undivided, and (m, l): the staging buffer's 32 columns a turn, as they lie
+// there, by one bulk copy.
 template <int D, int kType>
 __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int* own, uint32_t tmem, const ChunkParams& p,
                                     const WaitCtx& w) {
@@ -638,10 +657,10 @@ __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int
         if (rt < rows)
           p.a.lse[((tok0 + tok) * p.a.s.H_kv + us.at.h) * p.a.G + (rt - tok * p.a.G)] = chunk_lse<kType>(ml.x, ml.y);
       } else {
-        const int64_t row0 = (2 * static_cast<int64_t>(blockIdx.x) + (us.at.j0 == 0 ? 1 : 0)) * kChunkRows + t * kBM;
+        const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (us.at.j0 == 0 ? 1 : 0);
+        float* const to = p.o_part + part * (kChunkRows * D) + (t * kBM + qw * 32) * D;
 #pragma unroll 1
         for (int cc = 0; cc < D; cc += 32) {
-          __syncwarp();
           uint32_t o[32];
           tmem_ld32(tO + cc, o);
           tmem_wait_ld();
@@ -649,28 +668,26 @@ __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int
             tc_fence_before();
             mbar_arrive(sm.bar_ofree(t));
           }
+          if (lane == 0) bulk_wait_read_all();  // the buffer's last block is on its way
+          __syncwarp();
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch)
             st_shared_v4_b32(rowa + (static_cast<uint32_t>(ch ^ (lane & 7)) << 4), o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+          fence_async_smem();
           __syncwarp();
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const int lr = 4 * i + (lane >> 3), ch = lane & 7;
-            const int row = qw * 32 + lr;
-            if (row >= rows) continue;
-            uint32_t x[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(stage + static_cast<uint32_t>(lr * 128) + (static_cast<uint32_t>(ch ^ (lr & 7)) << 4))
-                         : "memory");
-            st_global_v4(p.o_part + (row0 + row) * D + cc + ch * 4, x[0], x[1], x[2], x[3]);
+          if (lane == 0) {
+            bulk_store(to + cc * 32, stage, 32 * 128);
+            bulk_commit();
           }
         }
-        if (rt < rows) p.ml_part[row0 + rt] = ml;
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        p.ml_part[part * kChunkRows + t * kBM + rt] = ml;
       }
     }
     ++k;
   }
+  if (lane == 0) bulk_wait_all();
 }
 
 // The unit of this CTA where there is no list: own[0] its sequence (-1: none), own[1]
@@ -785,41 +802,57 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-// Joins the partials of the units that the shares' ends cut: blocks (c, y) a quarter
-// of the rows of the one across the beginning of share c, if that is the first within it.
-constexpr int kChunkMergeParts = 4;
+// Joins the partials of the units that the shares' ends cut: blocks (c, y) the y-th part
+// of the rows of the one across the beginning of share c, if that is the first cut of it.
+// A warp takes a row (D = 128) or two, four pieces at a time.
+constexpr int kChunkMergeParts = 16;
 template <int D, int kType>
 __global__ void __launch_bounds__(256) attn_paged_chunk_merge(const __grid_constant__ ChunkParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t c = blockIdx.x, total = __ldg(&p.head->total), share = __ldg(&p.head->share), x = c * share;
   if (c == 0 || x >= total) return;
-  const int u = __ldg(&p.head->start[c]);
   ChunkAt un;
-  const int64_t before = un.load(p, p.units + u) * p.a.s.H_kv;
+  const ChunkUnit* const unit = p.units + __ldg(&p.head->start[c]);
+  const int64_t before = un.load(p, unit) * p.a.s.H_kv;
   const int per = un.w.tiles + kChunkUnitCost;
-  const int64_t h = (x - before) / per, x0 = before + h * per + kChunkUnitCost;
-  const int64_t ca = x0 / share, cb = (x0 + un.w.tiles - 1) / share;
+  const int64_t h = (x - before) / per, first = before + h * per + kChunkUnitCost;
+  // cuts at the beginnings of shares ca + 1 .. cb (chunk_cut)
+  const int64_t ca = (first + kChunkLeast + share - 1) / share - 1, cb = (first + un.w.tiles - kChunkLeast) / share;
   if (cb <= ca || c != ca + 1) return;
-  constexpr int kRows = kChunkRows / kChunkMergeParts;
-  for (int i = static_cast<int>(threadIdx.x); i < kRows * (D / 4); i += 256) {
-    const int rr = static_cast<int>(blockIdx.y) * kRows + i / (D / 4), ch = (i % (D / 4)) * 4;
+  constexpr int kRows = kChunkRows / kChunkMergeParts, kLanes = D / 4;
+  for (int i = static_cast<int>(threadIdx.x); i < kRows * kLanes; i += 256) {
+    const int rr = static_cast<int>(blockIdx.y) * kRows + i / kLanes, ch = (i % kLanes) * 4;
     const int t = rr / kBM, r = rr % kBM;
     const int tok = static_cast<int>((static_cast<uint32_t>(r) * p.inv_G) >> 16), token = un.i0 + t * p.tok + tok;
     if (r >= p.rows || token >= un.w.n) continue;
-    const auto part = [&](int64_t y) { return (2 * y + (y == ca ? 1 : 0)) * kChunkRows + rr; };
-    float m = -INFINITY;
-    for (int64_t y = ca; y <= cb; ++y) m = fmaxf(m, __ldg(&p.ml_part[part(y)].x));
+    const int at_o = chunk_part_at<D>(rr, ch);
+    float m = -INFINITY, sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int64_t y = ca; y <= cb; ++y) {
-      const float2 s = __ldg(p.ml_part + part(y));
-      const float4 o = __ldg(reinterpret_cast<const float4*>(p.o_part + part(y) * D + ch));
-      if (s.x == -INFINITY && s.y == 0.f) continue;  // it saw none of these keys
-      const float f = s.x == -INFINITY ? 1.f : ex2_approx(s.x - m);
-      sum = fmaf(s.y, f, sum);
-      v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+    for (int64_t y0 = ca; y0 <= cb; y0 += 4) {
+      float2 s[4];
+      float4 o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = make_float2(-INFINITY, 0.f);
+        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y0 + e <= cb) {
+          const int64_t part = 2 * (y0 + e) + (y0 + e == ca ? 1 : 0);
+          s[e] = __ldg(p.ml_part + part * kChunkRows + rr);
+          o[e] = __ldg(reinterpret_cast<const float4*>(p.o_part + part * (kChunkRows * D) + at_o));
+        }
+      }
+      const float to = fmaxf(fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)), m);
+      const float keep = m == -INFINITY ? 1.f : ex2_approx(m - to);  // (without a reference there is nothing, or NaN)
+      m = to;
+      sum *= keep, v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (s[e].x == -INFINITY && s[e].y == 0.f) continue;  // it saw none of these keys
+        const float f = s[e].x == -INFINITY ? 1.f : ex2_approx(s[e].x - m);
+        sum = fmaf(s[e].y, f, sum);
+        v.x = fmaf(o[e].x, f, v.x), v.y = fmaf(o[e].y, f, v.y), v.z = fmaf(o[e].z, f, v.z), v.w = fmaf(o[e].w, f, v.w);
+      }
     }
     const int64_t at = (static_cast<int64_t>(un.w.row0 + token) * p.a.s.H_kv + h) * p.a.G + (r - tok * p.a.G);
     tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);

@@ -582,12 +582,17 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     tok_compute<D, kType, kNT, kDirect>(k, p, base, smem, warp, wc);
 }
 
-// Joins the partials of the rows that the shares' ends cut: block c the row across
-// the beginning of share c, if that is the first one within it.
-constexpr int kTokMergeThreads = 256;
+// Joins the partials of the rows that the shares' ends cut: blocks (c, y) query row y of
+// those across the beginning of share c, if that is the first one within them.  The
+// warps (and, at D = 64, half-warps) take turns at the partials, four on their way at
+// once, and join through shared memory in their order.
+constexpr int kTokMergeThreads = 128;
 template <int D, int kType, int kRows>
 __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(const __grid_constant__ TokParams p) {
+  constexpr int kLanes = D / 4, kGroups = kTokMergeThreads / kLanes;
   __shared__ int64_t sums[kTokMergeThreads / 32 + 2];
+  __shared__ float2 ml_s[kGroups];
+  __shared__ float4 o_s[kGroups][kLanes];
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t c = blockIdx.x;
@@ -606,27 +611,56 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
   const int64_t ca = x0 / share, cb = (x0 + w.tiles - 1) / share;
   if (w.tiles == 0 || cb <= ca || c != ca + 1) return;
   const int h = static_cast<int>(row) / blocks, row_b = (static_cast<int>(row) - h * blocks) * kRows;
-  const int rows = min(kRows, w.n * p.a.G - row_b);
-  for (int i = static_cast<int>(threadIdx.x); i < rows * (D / 4); i += kTokMergeThreads) {
-    const int n = i / (D / 4), ch = (i % (D / 4)) * 4;
-    const auto part = [&](int64_t y) { return (2 * y + (y == ca ? 1 : 0)) * kRows + n; };
-    float m = -INFINITY;
-    for (int64_t y = ca; y <= cb; ++y) m = fmaxf(m, __ldg(&p.ml_part[part(y)].x));
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int64_t y = ca; y <= cb; ++y) {
-      const float2 s = __ldg(p.ml_part + part(y));
-      const float4 u = __ldg(reinterpret_cast<const float4*>(p.o_part + part(y) * D + ch));
-      if (s.x == -INFINITY && s.y == 0.f) continue;  // no key of it was seen
-      const float f = s.x == -INFINITY ? 1.f : ex2_approx(s.x - m);
-      sum = fmaf(s.y, f, sum);
-      v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+  const int n = static_cast<int>(blockIdx.y), group = static_cast<int>(threadIdx.x) / kLanes;
+  const int ch = (static_cast<int>(threadIdx.x) % kLanes) * 4;
+  if (n >= min(kRows, w.n * p.a.G - row_b)) return;
+  float m = -INFINITY, sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](const float2* s, const float4* o) {
+    const float to = fmaxf(fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)), m);
+    const float keep = m == -INFINITY ? 1.f : ex2_approx(m - to);  // (without a reference there is nothing, or NaN)
+    m = to;
+    sum *= keep, v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (s[e].x == -INFINITY && s[e].y == 0.f) continue;  // no key of it was seen
+      const float f = s[e].x == -INFINITY ? 1.f : ex2_approx(s[e].x - m);
+      sum = fmaf(s[e].y, f, sum);
+      v.x = fmaf(o[e].x, f, v.x), v.y = fmaf(o[e].y, f, v.y), v.z = fmaf(o[e].z, f, v.z), v.w = fmaf(o[e].w, f, v.w);
     }
-    const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
-    const int64_t at = static_cast<int64_t>(w.row0 + tok) * p.a.s.H_kv * p.a.G + h * p.a.G + g;
-    tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
+  };
+  float2 s[4];
+  float4 o[4];
+  for (int64_t y0 = ca + group; y0 <= cb; y0 += 4 * kGroups) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t y = y0 + e * kGroups;
+      s[e] = make_float2(-INFINITY, 0.f);
+      o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (y <= cb) {
+        const int64_t part = (2 * y + (y == ca ? 1 : 0)) * kRows + n;
+        s[e] = __ldg(p.ml_part + part);
+        o[e] = __ldg(reinterpret_cast<const float4*>(p.o_part + part * D + ch));
+      }
+    }
+    add(s, o);
   }
+  o_s[group][ch / 4] = v;
+  if (ch == 0) ml_s[group] = make_float2(m, sum);
+  __syncthreads();
+  if (group != 0) return;
+  for (int g0 = 1; g0 < kGroups; g0 += 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool there = g0 + e < kGroups;
+      s[e] = there ? ml_s[g0 + e] : make_float2(-INFINITY, 0.f);
+      o[e] = there ? o_s[g0 + e][ch / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    add(s, o);
+  }
+  const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
+  const int64_t at = static_cast<int64_t>(w.row0 + tok) * p.a.s.H_kv * p.a.G + h * p.a.G + g;
+  tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -689,7 +723,8 @@ cudaError_t tok_launch(const CUtensorMap& tk, const CUtensorMap& tv, const TokPa
   const cudaError_t e = launch_pdl(attn_paged_token_kernel<D, kType, kNT, false>, dim3(kTokSms), dim3(kTokThreads), C::kBytes, s,
                                    tk, tv, p);
   return e != cudaSuccess ? e
-                          : launch_pdl(attn_paged_merge_kernel<D, kType, C::kRows>, dim3(kTokSms), dim3(kTokMergeThreads), 0, s, p);
+                          : launch_pdl(attn_paged_merge_kernel<D, kType, C::kRows>, dim3(kTokSms, static_cast<unsigned>(std::min<int64_t>(C::kRows, static_cast<int64_t>(p.a.max_new) * p.a.G))),
+                                       dim3(kTokMergeThreads), 0, s, p);
 }
 
 attn_status_t tok_run(const attn_pages_t* c, const PagedAttn& a, const TokPlan& t, void* workspace, cudaStream_t s) {
