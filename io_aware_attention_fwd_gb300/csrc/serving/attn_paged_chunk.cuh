@@ -92,16 +92,21 @@ struct ChunkAt {
   }
 };
 
-// A CTA's units: its share of the list, or one.
+// A CTA's units: its share of the list, or one.  Each warp has a walk of its own in
+// shared memory (its lanes write the same there): held in registers across the MMA
+// warp's loop, it had cost that its descriptors' places, and a step a fifth of its time.
 struct ChunkWalk {
   int64_t first, end;  // where the unit's tiles begin in the list, and the share ends
   int64_t from;        // where the share begins
   int u;
   ChunkAt at;
   bool one;
-  __device__ explicit ChunkWalk(const ChunkParams& p) : first(0), end(0), from(0), u(0), one(p.head == nullptr) {
+  __device__ void start(const ChunkParams& p) {
+    first = end = from = 0;
+    u = 0;
     at.h = -1;
     at.w.tiles = 0;
+    one = p.head == nullptr;
     if (one) return;
     const int64_t total = __ldg(&p.head->total), share = __ldg(&p.head->share);
     from = static_cast<int64_t>(blockIdx.x) * share;
@@ -117,8 +122,15 @@ struct ChunkWalk {
     at.h = h - 1;
     first = unit + static_cast<int64_t>(h - 1) * per + kChunkUnitCost;
   }
-  // The next unit, or false.  own: sequence and first token of the CTA's only one, or -1.
+  // The next unit, or false (the whole warp).  own: sequence and first token of the
+  // CTA's only one, or -1.
   __device__ bool next(const ChunkParams& p, const volatile int* own) {
+    __syncwarp();
+    const bool more = step(p, own);
+    __syncwarp();
+    return more;
+  }
+  __device__ bool step(const ChunkParams& p, const volatile int* own) {
     if (one) {
       if (at.h >= 0 || own[0] < 0) return false;
       at.load(p, own[0], own[1]);
@@ -143,6 +155,14 @@ struct ChunkWalk {
     }
   }
 };
+
+// This warp's walk: behind the CTA's only unit in the room of the dense kernel's list.
+template <int D>
+__device__ __forceinline__ ChunkWalk& chunk_walk(const Smem<D, false>& sm) {
+  static_assert(64 + (kFwdThreads / 32) * sizeof(ChunkWalk) <= 2 * kListMax, "the walks in the list's room");
+  ChunkWalk* const all = reinterpret_cast<ChunkWalk*>(sm.ptr + Cfg<D, false>::kListOff + 64);
+  return all[threadIdx.x >> 5];
+}
 
 // The list: units in the sequences' order, what lies before each, and in which one
 // every share begins.  One block; a warp walks a sequence's units, 32 at a time.
@@ -269,7 +289,8 @@ __device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* ow
   int it = 0, k = 0;
   bool ok = true, missing = false;
   const uint64_t pol_first = l2_evict_first();
-  ChunkWalk us(p);
+  ChunkWalk& us = chunk_walk<D>(sm);
+  us.start(p);
   while (ok && us.next(p, own)) {
     const ChunkAt& un = us.at;
     const int p0 = un.w.p0 + un.i0, p1 = un.w.p0 + min(un.i0 + kQTiles * p.tok, un.w.n) - 1;
@@ -347,7 +368,8 @@ __device__ void chunk_mma_role(const Smem<D, false>& sm, const volatile int* own
   int k = 0;
   int pc[kQTiles] = {0, 0};
   bool ok = true, issued = false;
-  ChunkWalk us(p);
+  ChunkWalk& us = chunk_walk<D>(sm);
+  us.start(p);
   while (ok && us.next(p, own)) {
     const int n = us.at.n;
     const int nkv[kQTiles] = {us.at.nkv(p, 0), us.at.nkv(p, 1)};
@@ -434,7 +456,8 @@ __device__ void chunk_softmax_role(const Smem<D, false>& sm, const volatile int*
   int sbase = 0;
   int k = 0;
   bool ok = true;
-  ChunkWalk us(p);
+  ChunkWalk& us = chunk_walk<D>(sm);
+  us.start(p);
   while (ok && us.next(p, own)) {
     const int nkv = us.at.nkv(p, t), n_other = us.at.nkv(p, 1 - t);
     const int first = us.at.w.p0 + us.at.i0 + t * p.tok;  // positions of the tile's first and last token, and this row's
@@ -591,7 +614,8 @@ __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int
   int cnt[kQTiles] = {0, 0};
   int k = 0;
   bool ok = true;
-  ChunkWalk us(p);
+  ChunkWalk& us = chunk_walk<D>(sm);
+  us.start(p);
   while (ok && us.next(p, own)) {
 #pragma unroll
     for (int t = 0; t < kQTiles; ++t) {
