@@ -275,25 +275,29 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// TMA producer (warp 0), as varlen_load_role.
+// TMA producers, as varlen_load_role: warp 0 brings Q and the K tiles (kv 0), warp 2
+// the V tiles (kv 1): a tile in pages of 16 rows is 16 copies, and one warp for both took
+// 930 cycles a tile where a step of the tensor core, which needs two, takes 2048.
 template <int D>
-__device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* own, const CUtensorMap* tmQ, const CUtensorMap* tmK,
-                                const CUtensorMap* tmV, const ChunkParams& p, const WaitCtx& wc) {
+__device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* own, int kv, const CUtensorMap* tmQ,
+                                const CUtensorMap* map, const ChunkParams& p, const WaitCtx& wc) {
   using C = Cfg<D, false>;
+  static_assert(C::kSlots % 2 == 0, "a slot always has K tiles or always V tiles");
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int boxes = kBN >> p.box_log2;
   const int box = lane & (boxes - 1), panel = lane / boxes;
   const bool mine = panel < C::kPanels;
   const uint32_t dst = panel * kPanelBytes + static_cast<uint32_t>(box << p.box_log2) * 128;
   const int page_mask = (1 << p.a.s.page_log2) - 1;
-  int it = 0, k = 0;
+  int it = kv, k = 0;
   bool ok = true, missing = false;
   const uint64_t pol_first = l2_evict_first();
   ChunkWalk& us = chunk_walk<D>(sm);
   us.start(p);
   while (ok && us.next(p, own)) {
-    const ChunkAt& un = us.at;
+    const ChunkAt un = us.at;  // (here in registers)
     const int p0 = un.w.p0 + un.i0, p1 = un.w.p0 + min(un.i0 + kQTiles * p.tok, un.w.n) - 1;
+    const int32_t* const table = p.a.s.table + static_cast<int64_t>(un.b) * p.a.s.max_pages;
     // Whether this lane's box of the unit's tile i is needed, and its entry in the table.
     // That is asked for a tile ahead and looked at only then: an instruction that needs
     // it would hold the warp up for the time that it travels.
@@ -303,50 +307,46 @@ __device__ void chunk_load_role(const Smem<D, false>& sm, const volatile int* ow
     };
     const auto entry = [&](int i) {
       const int block = (un.w.tile(i) * kBN + (box << p.box_log2)) >> p.a.s.page_log2;
-      return needed(i) ? __ldg(p.a.s.table + static_cast<int64_t>(un.b) * p.a.s.max_pages + block) : -1;
+      return needed(i) ? __ldg(table + block) : -1;
     };
     int pg = entry(un.j0);
-    if (k > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_qfree(0), (k - 1) & 1, wc) && mbar_wait(sm.bar_qfree(1), (k - 1) & 1, wc));
-      if (!ok) break;
-    }
-    if (lane == 0) {
-      mbar_expect_tx(sm.bar_q(), static_cast<uint32_t>(kQTiles * C::kPanels * p.rows * 128));
-      for (int t = 0; t < kQTiles; ++t) {
-        const int i0 = un.i0 + t * p.tok < un.w.n ? un.i0 + t * p.tok : un.i0;  // a tile past the end reloads tile 0
-        for (int pn = 0; pn < C::kPanels; ++pn)
-          tma_load_3d_hint(sm.q(t) + pn * kPanelBytes, tmQ, sm.bar_q(), pn * C::kBoxCols, un.h * p.a.G, un.w.row0 + i0, pol_first);
+    if (kv == 0) {
+      if (k > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_qfree(0), (k - 1) & 1, wc) && mbar_wait(sm.bar_qfree(1), (k - 1) & 1, wc));
+        if (!ok) break;
       }
+      if (lane == 0) {
+        mbar_expect_tx(sm.bar_q(), static_cast<uint32_t>(kQTiles * C::kPanels * p.rows * 128));
+        for (int t = 0; t < kQTiles; ++t) {
+          const int i0 = un.i0 + t * p.tok < un.w.n ? un.i0 + t * p.tok : un.i0;  // a tile past the end reloads tile 0
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d_hint(sm.q(t) + pn * kPanelBytes, tmQ, sm.bar_q(), pn * C::kBoxCols, un.h * p.a.G, un.w.row0 + i0, pol_first);
+        }
+      }
+      __syncwarp();
     }
     ++k;
-    for (int j = 0; j < un.n && ok; ++j) {
-      const int next = entry(un.j0 + j + 1);
-      const int y = (un.w.tile(un.j0 + j) * kBN + (box << p.box_log2)) & page_mask;
+    for (int i = un.j0; i < un.j0 + un.n; ++i, it += 2) {
+      const int next = entry(i + 1);
+      const int y = (un.w.tile(i) * kBN + (box << p.box_log2)) & page_mask;
+      const int s = it % C::kSlots, round = it / C::kSlots;
+      if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.bar_empty(s), (round - 1) & 1, wc));
+      if (!ok) break;
       int z = p.missing;
-      for (int kv = 0; kv < 2; ++kv) {
-        const int s = it % C::kSlots, round = it / C::kSlots;
-        if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(sm.bar_empty(s), (round - 1) & 1, wc))) {
-          ok = false;
-          break;
-        }
-        if (kv == 0) {
-          if (pg >= 0 && pg < p.a.s.n_pages)
-            z = pg * p.a.s.H_kv + un.h;
-          else
-            missing |= needed(un.j0 + j);
-        }
-        if (lane == 0) mbar_expect_tx(sm.bar_full(s), C::kTileBytes);
-        __syncwarp();
-        if (mine) tma_load_3d(sm.slot(s) + dst, kv ? tmV : tmK, sm.bar_full(s), panel * C::kBoxCols, y, z);
-        ++it;
-      }
+      if (pg >= 0 && pg < p.a.s.n_pages)
+        z = pg * p.a.s.H_kv + un.h;
+      else
+        missing |= needed(i);
+      if (lane == 0) mbar_expect_tx(sm.bar_full(s), C::kTileBytes);
+      __syncwarp();
+      if (mine) tma_load_3d(sm.slot(s) + dst, map, sm.bar_full(s), panel * C::kBoxCols, y, z);
       pg = next;
     }
   }
   if (missing) atomicOr(&g_attn_status, kPagedNoPage);
   grid_launch_dependents();
-  bool drained = k == 0 || __all_sync(0xffffffffu, mbar_wait_drain(sm.bar_q(), (k - 1) & 1, wc));
-  for (int i = it > C::kSlots ? it - C::kSlots : 0; i < it && drained; ++i)
+  bool drained = kv != 0 || k == 0 || __all_sync(0xffffffffu, mbar_wait_drain(sm.bar_q(), (k - 1) & 1, wc));
+  for (int i = it > C::kSlots ? it - C::kSlots : kv; i < it && drained; i += 2)
     drained = __all_sync(0xffffffffu, mbar_wait_drain(sm.bar_full(i % C::kSlots), (i / C::kSlots) & 1, wc));
 }
 
@@ -803,8 +803,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (warp < 4) {
     regs_set<kRegsRoles>();
-    if (warp == 0) {
-      chunk_load_role<D>(sm, own, &tmQ, &tmK, &tmV, p, w);
+    if (warp == 0 || warp == 2) {
+      chunk_load_role<D>(sm, own, warp >> 1, &tmQ, warp == 0 ? &tmK : &tmV, p, w);
     } else if (warp == 1) {
       chunk_mma_role<D, kType>(sm, own, tmem, p, w);
     }
