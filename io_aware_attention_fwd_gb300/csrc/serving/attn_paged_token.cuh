@@ -5,10 +5,11 @@
 // pass is bound by HBM: 4 D bytes a key and key head.  What the kernel is built
 // around is therefore bytes in flight and nothing that stops them:
 //
-//   * One CTA an SM.  A producer warp brings tiles of 64 keys (K and V, 32 KB at
-//     D = 128) into a ring of 192 KB with TMA, page by page, and never stops at the
+//   * One CTA an SM.  Two producer warps bring tiles of 64 keys (K and V, 32 KB at
+//     D = 128) into a ring of 192 KB with TMA, page by page, and never stop at the
 //     end of a sequence or head: the next one's tiles are on their way while the
-//     last one's results are joined.
+//     last one's results are joined.  (In pages of 16 rows a tile is 16 copies; one
+//     warp for all of them held the pass up: 64 sequences of up to 16000 took 360 us instead of 328.)
 //   * Eight consumer warps: four take 16 keys each of one tile, four of the next.
 //     S^T = K Q^T and O^T += V^T P^T on mma.sync m16n8k16, keys and channels as the
 //     M rows, 8 query rows a tile of N; ldmatrix reads both from the 128-byte
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kTokTile = 64;       // keys a tile
 constexpr int kTokWarps = 8;       // consumers
-constexpr int kTokThreads = 32 * (kTokWarps + 1);
+constexpr int kTokThreads = 32 * (kTokWarps + 2);  // and a producer each for K and V
 constexpr int kTokRowCost = 4;     // tiles that a row's start and end count as
 
 // What a call gives its tokens.
@@ -269,17 +270,15 @@ __device__ __forceinline__ void tok_write(const PagedAttn& p, int64_t at, int64_
   }
 }
 
-// Producer warp.
+// Producer warp of K (kv 0) or V (1).
 template <int D, int kNT, bool kDirect>
-__device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV, uint32_t base,
-                         const WaitCtx& wc) {
+__device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, int kv, const CUtensorMap* map, uint32_t base, const WaitCtx& wc) {
   using C = TokCfg<D, kNT>;
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int boxes = kTokTile >> p.box_log2;
-  const int box = lane & (boxes - 1), panel = (lane / boxes) % C::kPanels, kv = lane / (boxes * C::kPanels);
-  const bool mine = kv < 2;
+  const int box = lane & (boxes - 1), panel = lane / boxes;
+  const bool mine = panel < C::kPanels;
   const uint32_t dst0 = base + kv * C::kV + panel * C::kPanel + (box << p.box_log2) * 128;
-  const CUtensorMap* const map = kv ? tmV : tmK;
   const int page_mask = (1 << p.a.s.page_log2) - 1;
   int it = 0;
   bool ok = true, missing = false;
@@ -311,7 +310,7 @@ __device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, const CUtensorM
         z = pg * p.a.s.H_kv + k.h;
       else
         missing |= needed(i);
-      if (lane == 0) mbar_expect_tx(full, C::kStage);
+      if (lane == 0) mbar_expect_tx(full, C::kStage / 2);
       __syncwarp();
       if (mine) tma_load_3d(dst0 + s * C::kStage, map, full, panel * 64, y, z);
       pg = pg1, pg1 = pg2;
@@ -561,8 +560,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const int warp = static_cast<int>(threadIdx.x >> 5);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(base + C::kBar + 8 * s, 1);
-      mbar_init(base + C::kBar + 8 * (C::kStages + s), 4);
+      mbar_init(base + C::kBar + 8 * s, 2);                 // both producers
+      mbar_init(base + C::kBar + 8 * (C::kStages + s), 4);  // the four warps that use the stage
     }
     misc[0] = 0u;
     fence_barrier_init();
@@ -576,8 +575,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   grid_launch_dependents();
   TokWalk<C::kRows> k;
   if (!tok_start<C::kRows, kTokThreads, kDirect>(k, p, reinterpret_cast<volatile int64_t*>(smem + C::kMisc + 16))) return;
-  if (warp == kTokWarps)
-    tok_load<D, kNT, kDirect>(k, p, &tmK, &tmV, base, wc);
+  if (warp >= kTokWarps)
+    tok_load<D, kNT, kDirect>(k, p, warp - kTokWarps, warp == kTokWarps ? &tmK : &tmV, base, wc);
   else
     tok_compute<D, kType, kNT, kDirect>(k, p, base, smem, warp, wc);
 }
