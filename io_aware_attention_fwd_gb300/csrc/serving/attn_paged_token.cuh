@@ -106,8 +106,18 @@ struct TokCfg {
   static_assert(kBytes <= 232448, "shared memory per CTA");
 };
 
+// What the merge needs of a row that is cut at the beginning of a share, and nowhere
+// before in it: the share's CTA leaves it (first is -1 where there is none).
+struct __align__(16) TokCut {
+  int32_t first, last;   // shares that have pieces of it
+  int32_t h, row_b;      // key head, first (token, head) row of its block
+  int32_t row0, rows;    // packed row of the sequence's first token; rows of the block
+  int32_t pad[2];
+};
+
 struct TokParams {
   PagedAttn a;
+  TokCut* cuts;     // [CTAs]
   float* o_part;    // [2 * CTAs][rows of a block][D]; null: a CTA a row
   float2* ml_part;  // [2 * CTAs][rows of a block]
   int blocks_bound; // blocks of rows a sequence may have (a CTA a row)
@@ -173,10 +183,11 @@ __device__ void tok_find(const PagedAttn& p, int64_t x, int64_t before, volatile
 // A CTA's share, row by row.
 template <int kRows>
 struct TokWalk {
-  int64_t x, end, before;
+  int64_t x, end, before, share;
   int b, blocks, per_row;
   PagedSpan w;
   int h, rb, t0, t1;  // key head, block of rows, tiles of the list
+  int64_t at;         // place of the row's first tile in the list
   __device__ void load(const PagedAttn& p) {
     w = PagedSpan::of<kTokTile>(p, b);
     blocks = tok_blocks(p, w.n, kRows);
@@ -198,6 +209,7 @@ struct TokWalk {
       t0 = static_cast<int>(max(static_cast<int64_t>(0), x - x0 - kTokRowCost));
       t1 = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(w.tiles), end - x0 - kTokRowCost)));
       x = x0 + per_row;
+      at = x0 + kTokRowCost;
       if (t0 < t1 || (w.tiles == 0 && starts)) return true;
     }
     return false;
@@ -220,8 +232,10 @@ __device__ __forceinline__ bool tok_start(TokWalk<kRows>& k, const TokParams& p,
     int64_t before;
     const int64_t total = tok_total<kRows, kThreads>(p.a, sums, &before);
     const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    k.share = share;
     k.x = static_cast<int64_t>(blockIdx.x) * share;
     k.end = k.x + share < total ? k.x + share : total;
+    if (threadIdx.x == 0) p.cuts[blockIdx.x].first = -1;  // (the first row writes it again, behind a barrier)
     volatile int* const b_s = reinterpret_cast<volatile int*>(sums + kThreads / 32 + 1);
     if (k.x < k.end) tok_find<kRows, kThreads>(p.a, k.x, before, b_s, sums + kThreads / 32);
     __syncthreads();
@@ -459,14 +473,19 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
           lo[nt][i2] = movmatrix_trans(pack_16x2<kType>(x0 - back.x, x1 - back.y));
         }
 #pragma unroll
-      for (int mb = 0; mb < kSteps; ++mb) {
-        uint32_t a[4];
-        ldmatrix_x4_trans(a, vaddr + stage + (mb >> 2) * C::kPanel + ((((mb & 3) * 2 + vpiece) ^ (vrow & 7)) << 4));
+      for (int mb = 0; mb < kSteps; mb += 2) {  // two at a time: an accumulator's second product waits for its first
+        uint32_t a[2][4];
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          tok_mma<kType>(o[nt][mb], a, hi[nt][0], hi[nt][1]);
-          tok_mma<kType>(o[nt][mb], a, lo[nt][0], lo[nt][1]);
-        }
+        for (int x = 0; x < 2; ++x)
+          ldmatrix_x4_trans(a[x], vaddr + stage + (mb >> 2) * C::kPanel + (((((mb + x) & 3) * 2 + vpiece) ^ (vrow & 7)) << 4));
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) tok_mma<kType>(o[nt][mb + x], a[x], hi[nt][0], hi[nt][1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) tok_mma<kType>(o[nt][mb + x], a[x], lo[nt][0], lo[nt][1]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8 * C::kStages);
@@ -514,6 +533,14 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
             }
       }
       tok_join_sync();
+    }
+    if constexpr (!kDirect) {
+      if (warp == 0 && lane == 0 && seg == 1) {
+        // the CTA's first row: is this the first cut of it?
+        const int64_t share = k.share, first = k.at / share, last = (k.at + w.tiles - 1) / share;
+        const bool here = k.t0 > 0 && first + 1 == static_cast<int64_t>(blockIdx.x);
+        *(p.cuts + blockIdx.x) = TokCut{here ? static_cast<int>(first) : -1, static_cast<int>(last), k.h, row_b, w.row0, rows, {0, 0}};
+      }
     }
     const bool whole = kDirect || (k.t0 == 0 && k.t1 == w.tiles);
     const int part = 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0);
@@ -589,30 +616,15 @@ constexpr int kTokMergeThreads = 128;
 template <int D, int kType, int kRows>
 __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(const __grid_constant__ TokParams p) {
   constexpr int kLanes = D / 4, kGroups = kTokMergeThreads / kLanes;
-  __shared__ int64_t sums[kTokMergeThreads / 32 + 2];
   __shared__ float2 ml_s[kGroups];
   __shared__ float4 o_s[kGroups][kLanes];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t c = blockIdx.x;
-  int64_t before;
-  const int64_t total = tok_total<kRows, kTokMergeThreads>(p.a, sums, &before);
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x, x = c * share;
-  if (c == 0 || x >= total) return;
-  volatile int* const b_s = reinterpret_cast<volatile int*>(sums + kTokMergeThreads / 32 + 1);
-  tok_find<kRows, kTokMergeThreads>(p.a, x, before, b_s, sums + kTokMergeThreads / 32);
-  __syncthreads();
-  const int b = *b_s;
-  before = sums[kTokMergeThreads / 32];
-  const PagedSpan w = PagedSpan::of<kTokTile>(p.a, b);
-  const int blocks = tok_blocks(p.a, w.n, kRows), per_row = w.tiles + kTokRowCost;
-  const int64_t row = (x - before) / per_row, x0 = before + row * per_row + kTokRowCost;
-  const int64_t ca = x0 / share, cb = (x0 + w.tiles - 1) / share;
-  if (w.tiles == 0 || cb <= ca || c != ca + 1) return;
-  const int h = static_cast<int>(row) / blocks, row_b = (static_cast<int>(row) - h * blocks) * kRows;
+  const int4 c0 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x)), c1 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x) + 1);
+  const int ca = c0.x, cb = c0.y, h = c0.z, row_b = c0.w, row0 = c1.x, rows = c1.y;
   const int n = static_cast<int>(blockIdx.y), group = static_cast<int>(threadIdx.x) / kLanes;
   const int ch = (static_cast<int>(threadIdx.x) % kLanes) * 4;
-  if (n >= min(kRows, w.n * p.a.G - row_b)) return;
+  if (ca < 0 || n >= rows) return;
   float m = -INFINITY, sum = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   const auto add = [&](const float2* s, const float4* o) {
@@ -630,14 +642,14 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
   };
   float2 s[4];
   float4 o[4];
-  for (int64_t y0 = ca + group; y0 <= cb; y0 += 4 * kGroups) {
+  for (int y0 = ca + group; y0 <= cb; y0 += 4 * kGroups) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int64_t y = y0 + e * kGroups;
+      const int y = y0 + e * kGroups;
       s[e] = make_float2(-INFINITY, 0.f);
       o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (y <= cb) {
-        const int64_t part = (2 * y + (y == ca ? 1 : 0)) * kRows + n;
+        const int64_t part = static_cast<int64_t>(2 * y + (y == ca ? 1 : 0)) * kRows + n;
         s[e] = __ldg(p.ml_part + part);
         o[e] = __ldg(reinterpret_cast<const float4*>(p.o_part + part * D + ch));
       }
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
     add(s, o);
   }
   const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
-  const int64_t at = static_cast<int64_t>(w.row0 + tok) * p.a.s.H_kv * p.a.G + h * p.a.G + g;
+  const int64_t at = static_cast<int64_t>(row0 + tok) * p.a.s.H_kv * p.a.G + h * p.a.G + g;
   tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
 }
 
@@ -667,7 +679,7 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
 // ---------------------------------------------------------------------------
 
 // Few rows with few keys each: a CTA a row and no second kernel.
-constexpr int kTokDirectLen = 2048;
+constexpr int kTokDirectLen = 1536;
 constexpr int kTokSms = 152;  // (the workspace's size is asked for without a device)
 
 // What an attention over pages takes: blocks of 8 or 16 rows, and a CTA a row or shares.
@@ -685,7 +697,7 @@ TokPlan tok_plan(int B, int H_kv, int G, int max_new, int max_len, int window, i
   return t;
 }
 uint64_t tok_workspace(const TokPlan& t, int D) {
-  return t.direct ? 16 : static_cast<uint64_t>(2 * kTokSms) * 8 * t.nt * (D * sizeof(float) + sizeof(float2));
+  return t.direct ? 16 : static_cast<uint64_t>(2 * kTokSms) * 8 * t.nt * (D * sizeof(float) + sizeof(float2)) + kTokSms * sizeof(TokCut);
 }
 
 std::atomic<int> g_paged_state[kMaxDevices];  // 1: shared-memory limits set
@@ -734,6 +746,7 @@ attn_status_t tok_run(const attn_pages_t* c, const PagedAttn& a, const TokPlan& 
   p.a = a;
   p.o_part = static_cast<float*>(workspace);
   p.ml_part = reinterpret_cast<float2*>(p.o_part + static_cast<int64_t>(2 * kTokSms) * 8 * t.nt * c->D);
+  p.cuts = reinterpret_cast<TokCut*>(p.ml_part + static_cast<int64_t>(2 * kTokSms) * 8 * t.nt);
   p.blocks_bound = t.blocks;
   p.box_rows = box;
   p.box_log2 = 0;
