@@ -33,6 +33,14 @@ struct ChunkHead {  // the list's head
   int64_t total, share;    // tiles and costs of all key heads; of a CTA
   int32_t start[kChunkCtas];  // unit in which each share begins
 };
+// What the merge needs of a unit that is cut at the beginning of a share, and nowhere
+// before in it: the share's CTA leaves it (first is -1 where there is none).
+struct __align__(16) ChunkCut {
+  int32_t first, last;  // shares that have pieces of it
+  int32_t h, row0;      // key head, packed row of the sequence's first token
+  int32_t i0, n;        // the unit's first token, and the sequence's number of them
+  int32_t pad[2];
+};
 
 // Where a share's end cuts a unit of `tiles` tiles, `v` tiles behind its first one: not
 // within kChunkLeast of its ends, where the piece would cost more than it brings.
@@ -50,6 +58,7 @@ struct ChunkParams {
   PagedAttn a;
   const ChunkHead* head;  // null: CTA x takes unit x / H_kv
   const ChunkUnit* units;
+  ChunkCut* cuts;         // [CTAs]
   float* o_part;          // [2 * CTAs][256][D]
   float2* ml_part;        // [2 * CTAs][256]
   int tok, rows;          // tokens and rows of a query tile
@@ -712,6 +721,19 @@ __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int
     ++k;
   }
   if (lane == 0) bulk_wait_all();
+  if (p.head != nullptr && qw == 0 && lane == 0) {
+    // the CTA's first unit: is this the first cut of it?  (chunk_cut says where cuts are)
+    ChunkCut cut{-1, 0, 0, 0, 0, 0, {0, 0}};
+    ChunkWalk first;
+    first.start(p);
+    if (first.step(p, own) && first.at.j0 > 0) {
+      const int64_t share = __ldg(&p.head->share);
+      const int64_t ca = (first.first + kChunkLeast + share - 1) / share - 1, cb = (first.first + first.at.w.tiles - kChunkLeast) / share;
+      if (ca + 1 == static_cast<int64_t>(blockIdx.x))
+        cut = ChunkCut{static_cast<int>(ca), static_cast<int>(cb), first.at.h, first.at.w.row0, first.at.i0, first.at.w.n, {0, 0}};
+    }
+    p.cuts[blockIdx.x] = cut;
+  }
 }
 
 // The unit of this CTA where there is no list: own[0] its sequence (-1: none), own[1]
@@ -834,26 +856,19 @@ template <int D, int kType>
 __global__ void __launch_bounds__(256) attn_paged_chunk_merge(const __grid_constant__ ChunkParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t c = blockIdx.x, total = __ldg(&p.head->total), share = __ldg(&p.head->share), x = c * share;
-  if (c == 0 || x >= total) return;
-  ChunkAt un;
-  const ChunkUnit* const unit = p.units + __ldg(&p.head->start[c]);
-  const int64_t before = un.load(p, unit) * p.a.s.H_kv;
-  const int per = un.w.tiles + kChunkUnitCost;
-  const int64_t h = (x - before) / per, first = before + h * per + kChunkUnitCost;
-  // cuts at the beginnings of shares ca + 1 .. cb (chunk_cut)
-  const int64_t ca = (first + kChunkLeast + share - 1) / share - 1, cb = (first + un.w.tiles - kChunkLeast) / share;
-  if (cb <= ca || c != ca + 1) return;
+  const int4 c0 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x)), c1 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x) + 1);
+  const int ca = c0.x, cb = c0.y, h = c0.z, row0 = c0.w, i0 = c1.x, n = c1.y;
+  if (ca < 0) return;
   constexpr int kRows = kChunkRows / kChunkMergeParts, kLanes = D / 4;
   for (int i = static_cast<int>(threadIdx.x); i < kRows * kLanes; i += 256) {
     const int rr = static_cast<int>(blockIdx.y) * kRows + i / kLanes, ch = (i % kLanes) * 4;
     const int t = rr / kBM, r = rr % kBM;
-    const int tok = static_cast<int>((static_cast<uint32_t>(r) * p.inv_G) >> 16), token = un.i0 + t * p.tok + tok;
-    if (r >= p.rows || token >= un.w.n) continue;
+    const int tok = static_cast<int>((static_cast<uint32_t>(r) * p.inv_G) >> 16), token = i0 + t * p.tok + tok;
+    if (r >= p.rows || token >= n) continue;
     const int at_o = chunk_part_at<D>(rr, ch);
     float m = -INFINITY, sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t y0 = ca; y0 <= cb; y0 += 4) {
+    for (int y0 = ca; y0 <= cb; y0 += 4) {
       float2 s[4];
       float4 o[4];
 #pragma unroll
@@ -878,7 +893,7 @@ __global__ void __launch_bounds__(256) attn_paged_chunk_merge(const __grid_const
         v.x = fmaf(o[e].x, f, v.x), v.y = fmaf(o[e].y, f, v.y), v.z = fmaf(o[e].z, f, v.z), v.w = fmaf(o[e].w, f, v.w);
       }
     }
-    const int64_t at = (static_cast<int64_t>(un.w.row0 + token) * p.a.s.H_kv + h) * p.a.G + (r - tok * p.a.G);
+    const int64_t at = (static_cast<int64_t>(row0 + token) * p.a.s.H_kv + h) * p.a.G + (r - tok * p.a.G);
     tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
   }
 }
@@ -905,7 +920,9 @@ ChunkPlan chunk_plan(int B, int H_kv, int G, int64_t rows, int max_new, int max_
 constexpr uint64_t kChunkHeadBytes = (sizeof(ChunkHead) + 255) / 256 * 256;
 uint64_t chunk_list_bytes(const ChunkPlan& c) { return kChunkHeadBytes + (static_cast<uint64_t>(c.cap) * sizeof(ChunkUnit) + 255) / 256 * 256; }
 uint64_t chunk_workspace(const ChunkPlan& c, int D) {
-  return c.direct ? 16 : chunk_list_bytes(c) + static_cast<uint64_t>(2 * kChunkCtas) * kChunkRows * (D * sizeof(float) + sizeof(float2));
+  return c.direct ? 16
+                  : chunk_list_bytes(c) + static_cast<uint64_t>(2 * kChunkCtas) * kChunkRows * (D * sizeof(float) + sizeof(float2)) +
+                        kChunkCtas * sizeof(ChunkCut);
 }
 
 template <int D, int kType>
@@ -942,6 +959,7 @@ attn_status_t chunk_run(const attn_pages_t* cache, const PagedAttn& a, const Chu
   p.units = c.direct ? nullptr : reinterpret_cast<const ChunkUnit*>(static_cast<char*>(workspace) + kChunkHeadBytes);
   p.o_part = c.direct ? nullptr : reinterpret_cast<float*>(static_cast<char*>(workspace) + chunk_list_bytes(c));
   p.ml_part = c.direct ? nullptr : reinterpret_cast<float2*>(p.o_part + static_cast<int64_t>(2 * kChunkCtas) * kChunkRows * D);
+  p.cuts = c.direct ? nullptr : reinterpret_cast<ChunkCut*>(p.ml_part + static_cast<int64_t>(2 * kChunkCtas) * kChunkRows);
   p.tok = c.tok;
   p.rows = c.tok * a.G;
   p.inv_G = static_cast<uint32_t>((65536 + a.G - 1) / a.G);
