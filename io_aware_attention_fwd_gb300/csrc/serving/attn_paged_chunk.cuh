@@ -259,12 +259,18 @@ __global__ void __launch_bounds__(kPlanThreads)
               const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
               if (lane >= off) incl += y;
             }
+            int64_t c_lo = 0, c_hi = 0;  // shares that begin in this lane's unit
             if (mine > 0 && u < cap) {
               const int64_t before = at + incl - mine;
               units[u] = ChunkUnit{before, b, static_cast<int>(i0), w.row0, w.n, w.len, w.p0};
               if (u == cap - 1) end_s = (before + mine) * p.a.s.H_kv;
-              const int64_t lo = before * p.a.s.H_kv, hi = (before + mine) * p.a.s.H_kv;
-              for (int64_t c2 = (lo + share - 1) / share; c2 < kChunkCtas && c2 * share < hi; ++c2) head->start[c2] = u;
+              c_lo = (before * p.a.s.H_kv + share - 1) / share;
+              c_hi = min(static_cast<int64_t>(kChunkCtas), ((before + mine) * p.a.s.H_kv + share - 1) / share);
+            }
+            for (unsigned rest = __ballot_sync(0xffffffffu, c_lo < c_hi); rest != 0; rest &= rest - 1) {
+              const int from = __ffs(static_cast<int>(rest)) - 1, unit = __shfl_sync(0xffffffffu, u, from);
+              const int lo = __shfl_sync(0xffffffffu, static_cast<int>(c_lo), from), hi = __shfl_sync(0xffffffffu, static_cast<int>(c_hi), from);
+              for (int x = lo + lane; x < hi; x += 32) head->start[x] = unit;
             }
             at += __shfl_sync(0xffffffffu, incl, 31);
           }

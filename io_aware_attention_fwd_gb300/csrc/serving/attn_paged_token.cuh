@@ -85,22 +85,30 @@ __device__ __forceinline__ bool paged_all_seen(const PagedAttn& p, int k0, int k
   return k1 - 1 <= p0 && (k0 > p1 - p.window || k1 <= p.sinks);
 }
 
+// kNT: tiles of 8 query rows a block.  With one, the two groups of four consumer warps
+// take tiles of keys in turn; with two, each takes every tile for 8 of the rows: 16 rows a
+// warp spilt and kept half the pace (64 sequences of up to 16000 entries with 16 query
+// heads a key head: 358 us instead of 323).
 template <int D, int kNT>
 struct TokCfg {
   static constexpr int kRows = 8 * kNT;                    // query rows a block
+  static constexpr bool kSplit = kNT == 2;
+  static constexpr int kUsers = kSplit ? 8 : 4;            // warps that use a stage
+  static constexpr int kJoin = kSplit ? 4 : 8;             // warps that have keys of a row
   static constexpr int kPanels = D / 64;                   // 128-byte panels of a row
   static constexpr int kPanel = kTokTile * 128;            // bytes of one
   static constexpr int kV = kPanels * kPanel;              // V of a stage
   static constexpr int kStage = 2 * kV;
-  // 6 (D = 128) or 12.  Even, so that a stage is always the same four warps': a warp
-  // that did not see every phase of a barrier could take one for the next but one.
+  // 6 (D = 128) or 12.  Even, so that where the groups take turns a stage is always the
+  // same four warps': a warp that did not see every phase of a barrier could take one for
+  // the next but one.
   static constexpr int kStages = (192 * 1024) / kStage;
   static_assert(kStages % 2 == 0, "a stage belongs to one group of warps");
   static constexpr int kOStride = D + 4;                   // floats; 4: lanes' banks differ
-  static constexpr int kSlots = kNT == 1 ? 4 : 2;          // places for a warp's O as the eight are added up
+  static constexpr int kSlots = kNT == 1 ? 4 : 2;          // places for warps' O as they are added up
   static constexpr int kO = kStages * kStage;              // float [kSlots][kRows][kOStride]
-  static constexpr int kMl = kO + kSlots * kRows * kOStride * 4;  // float2 [2][kTokWarps][kRows]
-  static constexpr int kBar = kMl + 2 * kTokWarps * kRows * 8;
+  static constexpr int kMl = kO + kSlots * kRows * kOStride * 4;  // float2 [2][kTokWarps][8]
+  static constexpr int kBar = kMl + 2 * kTokWarps * 8 * 8;
   static constexpr int kMisc = kBar + 2 * kStages * 8;     // abort flag; int64 sums of the block's scan
   static constexpr int kBytes = kMisc + 16 + 8 * (kTokThreads / 32 + 4) + 1024;
   static_assert(kBytes <= 232448, "shared memory per CTA");
@@ -351,6 +359,7 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
   const int kpiece = lane >> 4, vpiece = (lane >> 3) & 1;
   float* const o_s = reinterpret_cast<float*>(smem + C::kO);
   float2* const ml_s = reinterpret_cast<float2*>(smem + C::kMl);
+  const int r0 = C::kSplit ? group * 8 : 0;  // this warp's rows of the block
   int it = 0, seg = 0;
   bool ok = true;
   const float cl = p.a.scale_log2;
@@ -360,64 +369,53 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
     const int row_b = k.rb * C::kRows;                     // first (token, head) row of the block
     const int rows = min(C::kRows, w.n * p.a.G - row_b);
     // Q as B operands, and the positions of this lane's columns
-    uint32_t q[kNT][kSteps][2];
-    int pos[kNT][2];
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const int rr = nt * 8 + r;
-      const int tok = (row_b + min(rr, rows - 1)) / p.a.G, g = row_b + min(rr, rows - 1) - tok * p.a.G;
+    uint32_t q[kSteps][2];
+    int pos[2];
+    {
+      const int mine = row_b + min(r0 + r, rows - 1), tok = mine / p.a.G, g = mine - tok * p.a.G;
       const uint16_t* src = p.a.q + (w.row0 + tok) * p.a.q_stride + (k.h * p.a.G + g) * static_cast<int64_t>(D) + 2 * c;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          q[nt][ks][i] = rr < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + i * 8)) : 0u;
+          q[ks][i] = r0 + r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + i * 8)) : 0u;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) pos[nt][e] = w.p0 + (row_b + min(nt * 8 + 2 * c + e, rows - 1)) / p.a.G;
+      for (int e = 0; e < 2; ++e) pos[e] = w.p0 + (row_b + min(r0 + 2 * c + e, rows - 1)) / p.a.G;
     }
     const int p_first = w.p0 + row_b / p.a.G, p_last = w.p0 + (row_b + rows - 1) / p.a.G;
-    float ref[kNT][2], sub[kNT][2], l[kNT][2], o[kNT][kSteps][4];
+    float ref[2], sub[2], l[2], o[kSteps][4];
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
+    for (int e = 0; e < 2; ++e) ref[e] = -INFINITY, sub[e] = l[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref[nt][e] = -INFINITY, sub[nt][e] = l[nt][e] = 0.f;
+    for (int mb = 0; mb < kSteps; ++mb)
 #pragma unroll
-      for (int mb = 0; mb < kSteps; ++mb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][mb][e] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[mb][e] = 0.f;
     for (int i = k.t0; i < k.t1; ++i, ++it) {
-      if ((it & 1) != group) continue;
+      if (!C::kSplit && (it & 1) != group) continue;
       const int s = it % C::kStages;
       const uint32_t full = base + C::kBar + 8 * s, stage = static_cast<uint32_t>(s) * C::kStage;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(full, (it / C::kStages) & 1, wc));
       if (!ok) continue;  // (the barriers below still have all warps)
       const int key0 = w.tile(i) * kTokTile + key_w;
-      float d[kNT][4], d2[kNT][4];
+      float d[4], d2[4];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[nt][e] = d2[nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) d[e] = d2[e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
         uint32_t a[4];
         ldmatrix_x4(a, kaddr + stage + (ks >> 2) * C::kPanel + ((((ks & 3) * 2 + kpiece) ^ (krow & 7)) << 4));
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) tok_mma<kType>((ks & 1) ? d2[nt] : d[nt], a, q[nt][ks][0], q[nt][ks][1]);
+        tok_mma<kType>((ks & 1) ? d2 : d, a, q[ks][0], q[ks][1]);
       }
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[nt][e] += d2[nt][e];
+      for (int e = 0; e < 4; ++e) d[e] += d2[e];
       if (!paged_all_seen(p.a, key0, key0 + 16, p_first, p_last)) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = key0 + r + (e >> 1) * 8, at = pos[nt][e & 1];
-            if (!(j <= at && (j > at - p.a.window || j < p.a.sinks))) d[nt][e] = -INFINITY;
-          }
-        // rows behind the sequence's end hold anything, and 0 * NaN is NaN
+        for (int e = 0; e < 4; ++e) {
+          const int j = key0 + r + (e >> 1) * 8, at = pos[e & 1];
+          if (!(j <= at && (j > at - p.a.window || j < p.a.sinks))) d[e] = -INFINITY;
+        }
+        // rows behind the sequence's end hold anything, and 0 * NaN is NaN (where both groups
+        // read them, both write the same zeros)
         const int past = key0 + 16 - w.len;
         if (past > 0) {
           for (int x = lane; x < min(past, 16) * C::kPanels * 8; x += 32) {
@@ -429,49 +427,39 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
         }
       }
       // New references only where a score exceeds the old one by more than kTokMove
-      bool move = false;
-      float top[kNT][2];
+      float top[2];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int e = 0; e < 2; ++e) top[e] = fmaxf(d[e], d[e + 2]) * cl;
+      constexpr float kFar = kTokMove<kType> + kTokUp<kType>;
+      if (__any_sync(0xffffffffu, (top[0] > ref[0] + kFar) | (top[1] > ref[1] + kFar))) {
+        float a[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          top[nt][e] = fmaxf(d[nt][e], d[nt][e + 2]) * cl;
-          move |= top[nt][e] > ref[nt][e] + (kTokMove<kType> + kTokUp<kType>);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], off));
+          const bool moves = top[e] > ref[e] + kFar;
+          const float to = moves ? top[e] - kTokUp<kType> : ref[e];
+          a[e] = moves ? ex2_approx(ref[e] - to) : 1.f;
+          ref[e] = to;
+          sub[e] = to == -INFINITY ? 0.f : to;
+          l[e] *= a[e];
         }
-      if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          float a[2];
+        for (int mb = 0; mb < kSteps; ++mb)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], off));
-            const bool moves = top[nt][e] > ref[nt][e] + (kTokMove<kType> + kTokUp<kType>);
-            const float to = moves ? top[nt][e] - kTokUp<kType> : ref[nt][e];
-            a[e] = moves ? ex2_approx(ref[nt][e] - to) : 1.f;
-            ref[nt][e] = to;
-            sub[nt][e] = to == -INFINITY ? 0.f : to;
-            l[nt][e] *= a[e];
-          }
-#pragma unroll
-          for (int mb = 0; mb < kSteps; ++mb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][mb][e] *= a[e & 1];
-        }
+          for (int e = 0; e < 4; ++e) o[mb][e] *= a[e & 1];
       }
-      uint32_t hi[kNT][2], lo[kNT][2];
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const float x0 = ex2_approx(fmaf(d[nt][2 * i2], cl, -sub[nt][0])), x1 = ex2_approx(fmaf(d[nt][2 * i2 + 1], cl, -sub[nt][1]));
-          l[nt][0] += x0;
-          l[nt][1] += x1;
-          const uint32_t h2 = pack_16x2<kType>(x0, x1);
-          const float2 back = unpack_16x2<kType>(h2);
-          hi[nt][i2] = movmatrix_trans(h2);
-          lo[nt][i2] = movmatrix_trans(pack_16x2<kType>(x0 - back.x, x1 - back.y));
-        }
+      for (int i2 = 0; i2 < 2; ++i2) {
+        const float x0 = ex2_approx(fmaf(d[2 * i2], cl, -sub[0])), x1 = ex2_approx(fmaf(d[2 * i2 + 1], cl, -sub[1]));
+        l[0] += x0;
+        l[1] += x1;
+        const uint32_t h2 = pack_16x2<kType>(x0, x1);
+        const float2 back = unpack_16x2<kType>(h2);
+        hi[i2] = movmatrix_trans(h2);
+        lo[i2] = movmatrix_trans(pack_16x2<kType>(x0 - back.x, x1 - back.y));
+      }
 #pragma unroll
       for (int mb = 0; mb < kSteps; mb += 2) {  // two at a time: an accumulator's second product waits for its first
         uint32_t a[2][4];
@@ -479,58 +467,49 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
         for (int x = 0; x < 2; ++x)
           ldmatrix_x4_trans(a[x], vaddr + stage + (mb >> 2) * C::kPanel + (((((mb + x) & 3) * 2 + vpiece) ^ (vrow & 7)) << 4));
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) tok_mma<kType>(o[mb + x], a[x], hi[0], hi[1]);
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) tok_mma<kType>(o[nt][mb + x], a[x], hi[nt][0], hi[nt][1]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) tok_mma<kType>(o[nt][mb + x], a[x], lo[nt][0], lo[nt][1]);
+        for (int x = 0; x < 2; ++x) tok_mma<kType>(o[mb + x], a[x], lo[0], lo[1]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8 * C::kStages);
     }
-    // The eight warps' statistics and O become the row's, or the share's partial.
-    float2* const ml = ml_s + (seg & 1) * kTokWarps * C::kRows;
+    // The warps' statistics and O become the row's, or the share's partial.
+    float2* const ml = ml_s + (seg & 1) * kTokWarps * 8;
     ++seg;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-        if (r == 0) ml[warp * C::kRows + nt * 8 + 2 * c + e] = make_float2(ref[nt][e], l[nt][e]);
-      }
+      for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+      if (r == 0) ml[warp * 8 + 2 * c + e] = make_float2(ref[e], l[e]);
+    }
     tok_join_sync();
+    const int join0 = C::kSplit ? group * 4 : 0;  // the first warp of those that have keys of this one's rows
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int e = 0; e < 2; ++e) {
+      float m = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = -INFINITY;
+      for (int x = 0; x < C::kJoin; ++x) m = fmaxf(m, ml[(join0 + x) * 8 + 2 * c + e].x);
+      const float f = ref[e] == -INFINITY ? 0.f : ex2_approx(ref[e] - m);
+      // (a warp without keys has nothing to add, and 0 * NaN would be something)
+      if (ref[e] != -INFINITY || l[e] != 0.f) {
 #pragma unroll
-        for (int x = 0; x < kTokWarps; ++x) m = fmaxf(m, ml[x * C::kRows + nt * 8 + 2 * c + e].x);
-        const float f = ref[nt][e] == -INFINITY ? 0.f : ex2_approx(ref[nt][e] - m);
-        // (a warp without keys has nothing to add, and 0 * NaN would be something)
-        if (ref[nt][e] != -INFINITY || l[nt][e] != 0.f) {
-#pragma unroll
-          for (int mb = 0; mb < kSteps; ++mb) o[nt][mb][e] *= f, o[nt][mb][e + 2] *= f;
-        }
+        for (int mb = 0; mb < kSteps; ++mb) o[mb][e] *= f, o[mb][e + 2] *= f;
       }
-    // kSlots warps at a time, always in the same order
-    const int rank = warp ^ 4;
-    float* const mine = o_s + (rank % C::kSlots) * C::kRows * C::kOStride;
+    }
+    // kSlots of a row's warps at a time, always in the same order
+    const int rank = C::kSplit ? warp & 3 : warp ^ 4;
+    float* const mine = o_s + ((rank % C::kSlots) * C::kRows + r0) * C::kOStride;
 #pragma unroll 1
-    for (int step = 0; step < kTokWarps / C::kSlots; ++step) {
+    for (int step = 0; step < C::kJoin / C::kSlots; ++step) {
       if (rank / C::kSlots == step) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int mb = 0; mb < kSteps; ++mb)
 #pragma unroll
-          for (int mb = 0; mb < kSteps; ++mb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float& to = mine[(nt * 8 + 2 * c + (e & 1)) * C::kOStride + mb * 16 + r + (e >> 1) * 8];
-              to = step == 0 ? o[nt][mb][e] : to + o[nt][mb][e];
-            }
+          for (int e = 0; e < 4; ++e) {
+            float& to = mine[(2 * c + (e & 1)) * C::kOStride + mb * 16 + r + (e >> 1) * 8];
+            to = step == 0 ? o[mb][e] : to + o[mb][e];
+          }
       }
       tok_join_sync();
     }
@@ -549,10 +528,10 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
       if (n >= rows || !ok) continue;
       float m = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int y = 0; y < kTokWarps; ++y) m = fmaxf(m, ml[y * C::kRows + n].x);
+      for (int y = 0; y < C::kJoin; ++y) m = fmaxf(m, ml[((n >> 3) * C::kJoin + y) * 8 + (n & 7)].x);
 #pragma unroll
-      for (int y = 0; y < kTokWarps; ++y) {
-        const float2 v = ml[y * C::kRows + n];
+      for (int y = 0; y < C::kJoin; ++y) {
+        const float2 v = ml[((n >> 3) * C::kJoin + y) * 8 + (n & 7)];
         if (v.x != -INFINITY || v.y != 0.f) sum += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - m);
       }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -588,7 +567,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(base + C::kBar + 8 * s, 2);                 // both producers
-      mbar_init(base + C::kBar + 8 * (C::kStages + s), 4);  // the four warps that use the stage
+      mbar_init(base + C::kBar + 8 * (C::kStages + s), C::kUsers);
     }
     misc[0] = 0u;
     fence_barrier_init();
