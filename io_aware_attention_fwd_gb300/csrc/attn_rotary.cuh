@@ -174,7 +174,7 @@ __device__ __forceinline__ float rot_sum(uint64_t v) {
 // The weights of q and k (1 without a norm) as fp32, in shared memory.
 template <int D, int kType>
 __device__ __forceinline__ void rot_weights(float (*ws)[D], const RotParams& p) {
-  for (int i = static_cast<int>(threadIdx.x); i < 2 * D; i += kRotThreads) {
+  for (int i = static_cast<int>(threadIdx.x); i < 2 * D; i += static_cast<int>(blockDim.x)) {
     const int kv = i / D, c = i % D;
     float w = 1.f;
     if (p.w[kv] != nullptr)
@@ -207,6 +207,12 @@ __device__ __forceinline__ void rot_angles(float* co, float* si, const RotLane<D
       for (int e = 0; e < 8; ++e) si[e] = -si[e];
     }
   }
+}
+
+__device__ __forceinline__ uint4 rot_shared(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 struct NoPages {};
@@ -332,15 +338,19 @@ __global__ void __launch_bounds__(kRotThreads, kRotFwdBlocks) attn_norm_rope_ker
 // k, in fp32 (its share's rows, a few hundred at most); the block's sums are added in
 // shared memory, and a second kernel adds the blocks' in 64 bits: the same from call
 // to call.
+constexpr int kRotBwdThreads = 256;
+constexpr int kRotBwdWarps = kRotBwdThreads / 32;
 constexpr int kRotBwdBlocks = 2;  // blocks an SM
 
-// A run of the gradient: heads of one kind; dw: its weight's sums.
+// A run of the gradient: heads of one kind; dw: its weight's sums.  dy and x come
+// through a ring of this warp's in shared memory, each lane's own 16 bytes: in
+// registers they left the SM 16 warps and four groups each on their way.
+constexpr int kRotRing = 4;  // groups on their way
 template <int D, int kType>
 __device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWalk& w, const RotLane<D>& ln, const uint64_t* A,
-                                                 const uint64_t* B, const float* w_s, uint64_t* dw) {
+                                                 const uint64_t* B, const float* w_s, uint64_t* dw, uint32_t ring) {
   using Lane = RotLane<D>;
-  constexpr int kBatch = 4;
-  int head = (w.g0 - p.first[w.kind]) * Lane::kRows + ln.sub, left = w.g1 - w.g0;
+  int head = (w.g0 - p.first[w.kind]) * Lane::kRows + ln.sub, left = w.g1 - w.g0, ahead = head;
   const int end = min(p.heads[w.kind], (w.g1 - p.first[w.kind]) * Lane::kRows);
   const bool norm = p.w[w.kind] != nullptr;
   const uint16_t* gsrc = rot_at(p.dy[w.kind], w.b, w.s, head, ln.c0);
@@ -348,6 +358,18 @@ __device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWa
   uint16_t* dst = rot_at(p.out[w.kind], w.b, w.s, head, ln.c0);
   const int64_t g_step = p.dy[w.kind].head * Lane::kRows, x_step = norm ? p.in[w.kind].head * Lane::kRows : 0,
                 out_step = p.out[w.kind].head * Lane::kRows;
+  const auto fetch = [&](int slot) {
+    if (ahead < end) {
+      cp_async_16(ring + slot * 1024, gsrc);
+      if (norm) cp_async_16(ring + slot * 1024 + 512, xsrc);
+    }
+    cp_async_commit();
+    ahead += Lane::kRows;
+    gsrc += g_step;
+    xsrc += x_step;
+  };
+#pragma unroll
+  for (int u = 0; u < kRotRing; ++u) fetch(u);
   uint64_t wt[4];
   {
     float own[8];
@@ -356,26 +378,24 @@ __device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWa
     for (int e = 0; e < 4; ++e) wt[e] = pack_f32x2(own[2 * e], own[2 * e + 1]);
   }
   while (left > 0) {
-    uint4 draw[kBatch], raw[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      raw[u] = draw[u] = make_uint4(0, 0, 0, 0);
-      if (head + u * Lane::kRows < end) {
-        draw[u] = *reinterpret_cast<const uint4*>(gsrc + u * g_step);
-        if (norm) raw[u] = *reinterpret_cast<const uint4*>(xsrc + u * x_step);
+    for (int u = 0; u < kRotRing; ++u) {
+      if (left == 0) break;
+      const bool there = head < end;
+      cp_async_wait<kRotRing - 1>();  // this lane's copies of this group
+      uint4 dy = make_uint4(0, 0, 0, 0), x = dy;
+      if (there) {
+        dy = rot_shared(ring + u * 1024);
+        if (norm) x = rot_shared(ring + u * 1024 + 512);
       }
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (u >= left) break;
-      const bool there = head + u * Lane::kRows < end;
       uint64_t g[4], z[4];
-      rot_unpack<kType>(g, draw[u]);
-      rot_unpack<kType>(z, rot_paired(draw[u], p.turn, ln.partner));
+      rot_unpack<kType>(g, dy);
+      rot_unpack<kType>(z, rot_paired(dy, p.turn, ln.partner));
 #pragma unroll
       for (int e = 0; e < 4; ++e) g[e] = fma_f32x2(z[e], B[e], mul_f32x2(g[e], A[e]));
+      rot_unpack<kType>(z, x);
+      fetch(u);
       if (norm) {
-        rot_unpack<kType>(z, raw[u]);
         uint64_t gw[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) gw[e] = mul_f32x2(g[e], wt[e]);
@@ -400,23 +420,24 @@ __device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWa
           g[e] = mul_f32x2(r2, fma_f32x2(k2, z[e], gw[e]));
         }
       }
-      if (there) *reinterpret_cast<uint4*>(dst + u * out_step) = rot_pack<kType>(g);
+      if (there) *reinterpret_cast<uint4*>(dst) = rot_pack<kType>(g);
+      head += Lane::kRows;
+      dst += out_step;
+      --left;
     }
-    head += kBatch * Lane::kRows;
-    left -= kBatch;
-    gsrc += kBatch * g_step;
-    xsrc += kBatch * x_step;
-    dst += kBatch * out_step;
   }
+  cp_async_wait<0>();
 }
 
 template <int D, int kType>
-__global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks) attn_norm_rope_bwd_kernel(const __grid_constant__ RotParams p) {
+__global__ void __launch_bounds__(kRotBwdThreads, kRotBwdBlocks) attn_norm_rope_bwd_kernel(const __grid_constant__ RotParams p) {
   using Lane = RotLane<D>;
-  __shared__ __align__(16) float cs_s[kRotWarps][D];
+  __shared__ __align__(16) float cs_s[kRotBwdWarps][D];
   __shared__ __align__(16) float w_s[2][D];
+  __shared__ __align__(16) uint4 ring_s[kRotBwdWarps][kRotRing][2][32];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const Lane ln(lane, p.turn);
+  const uint32_t ring = smem_u32(&ring_s[warp][0][0][lane]);
   grid_dependency_wait();
   grid_launch_dependents();
   rot_weights<D, kType>(w_s, p);
@@ -426,7 +447,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks) attn_norm_rope_bwd
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw[kv][e] = 0ull;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kRotWarps + warp) * p.share;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kRotBwdWarps + warp) * p.share;
   if (i < p.total) {
     const RotTable table(lane, p.turn);
     float* const cs = cs_s[warp];
@@ -444,14 +465,16 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks) attn_norm_rope_bwd
         }
       }
       if (w.kind == 0)
-        rot_backward_run<D, kType>(p, w, ln, A, B, w_s[0], dw[0]);
+        rot_backward_run<D, kType>(p, w, ln, A, B, w_s[0], dw[0], ring);
       else
-        rot_backward_run<D, kType>(p, w, ln, A, B, w_s[1], dw[1]);
+        rot_backward_run<D, kType>(p, w, ln, A, B, w_s[1], dw[1], ring);
     } while (w.next(p));
   }
   if (p.dw == nullptr) return;
   // the warp's rows, then the block's warps in their order
-  __shared__ float part_s[kRotWarps][2][D];
+  float(*const part_s)[2][D] = reinterpret_cast<float(*)[2][D]>(ring_s);  // (no copy is under way any more)
+  static_assert(sizeof(float) * kRotBwdWarps * 2 * D <= sizeof(ring_s), "the sums in the ring's room");
+  __syncthreads();
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
@@ -464,10 +487,10 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks) attn_norm_rope_bwd
       if (ln.sub == 0) part_s[warp][kv][ln.c0 + e] = x;
     }
   __syncthreads();
-  for (int j = tid; j < 2 * D; j += kRotThreads) {
+  for (int j = tid; j < 2 * D; j += kRotBwdThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int x = 0; x < kRotWarps; ++x) v += part_s[x][j / D][j % D];
+    for (int x = 0; x < kRotBwdWarps; ++x) v += part_s[x][j / D][j % D];
     p.dw[static_cast<int64_t>(blockIdx.x) * 2 * D + j] = v;
   }
 }
@@ -502,13 +525,13 @@ struct RotGrid {
   int64_t total, share;
   unsigned blocks;
 };
-RotGrid rot_grid(int64_t tokens, int groups, int sms, int blocks_per_sm) {
+RotGrid rot_grid(int64_t tokens, int groups, int sms, int blocks_per_sm, int warps_per_block) {
   RotGrid g;
   g.total = tokens * groups;
-  const int64_t warps = static_cast<int64_t>(sms) * blocks_per_sm * kRotWarps;
+  const int64_t warps = static_cast<int64_t>(sms) * blocks_per_sm * warps_per_block;
   g.share = (g.total + warps - 1) / warps;
   const int64_t used = g.share > 0 ? (g.total + g.share - 1) / g.share : 0;
-  g.blocks = static_cast<unsigned>((used + kRotWarps - 1) / kRotWarps);
+  g.blocks = static_cast<unsigned>((used + warps_per_block - 1) / warps_per_block);
   return g;
 }
 
@@ -598,7 +621,7 @@ attn_status_t attn_qk_norm_rope(const attn_heads_t* q, const attn_heads_t* k, co
   p.pos = positions;
   p.S = S;
   const RotGrid g = rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0),
-                             g_dev_sms[dev].load(std::memory_order_relaxed), kRotFwdBlocks);
+                             g_dev_sms[dev].load(std::memory_order_relaxed), kRotFwdBlocks, kRotWarps);
   p.total = g.total, p.share = g.share;
   const auto run = [&](auto kernel) {
     return launch_pdl(kernel, dim3(g.blocks), dim3(kRotThreads), 0, static_cast<cudaStream_t>(stream), p);
@@ -613,7 +636,7 @@ uint64_t attn_qk_norm_rope_bwd_workspace_bytes(int B, int S, int H_q, int H_k, i
   if (rot_check_shape(B, S, H_q, H_k, D, ATTN_BF16) != ATTN_OK) return 0;
   if (B == 0 || S == 0) return 16;
   RotParams p{};
-  return static_cast<uint64_t>(rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0), kRotSms, kRotBwdBlocks).blocks) * 2 *
+  return static_cast<uint64_t>(rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0), kRotSms, kRotBwdBlocks, kRotBwdWarps).blocks) * 2 *
          D * sizeof(float);
 }
 
@@ -658,11 +681,11 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads
     p.pos = positions;
     p.S = S;
     // (the grid is a GB300's whatever the device has: it sizes the workspace)
-    const RotGrid g = rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0), kRotSms, kRotBwdBlocks);
+    const RotGrid g = rot_grid(static_cast<int64_t>(B) * S, rot_groups(&p, D, H_q, H_k, 0), kRotSms, kRotBwdBlocks, kRotBwdWarps);
     p.total = g.total, p.share = g.share;
     p.dw = norm ? static_cast<float*>(workspace) : nullptr;
     blocks = g.blocks;
-    const auto run = [&](auto kernel) { return launch_pdl(kernel, dim3(g.blocks), dim3(kRotThreads), 0, s, p); };
+    const auto run = [&](auto kernel) { return launch_pdl(kernel, dim3(g.blocks), dim3(kRotBwdThreads), 0, s, p); };
     const bool bf = dtype == ATTN_BF16;
     e = D == 64 ? (bf ? run(attn_norm_rope_bwd_kernel<64, kBF16>) : run(attn_norm_rope_bwd_kernel<64, kFP16>))
                 : (bf ? run(attn_norm_rope_bwd_kernel<128, kBF16>) : run(attn_norm_rope_bwd_kernel<128, kFP16>));

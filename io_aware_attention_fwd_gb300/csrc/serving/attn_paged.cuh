@@ -197,7 +197,7 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
     p.eps = eps;
     p.S = static_cast<int>(rows);
     const RotGrid g = rot_grid(rows, rot_groups(&p, D, q != nullptr ? H_q : 0, H_kv, H_kv),
-                               g_dev_sms[dev].load(std::memory_order_relaxed), kRotFwdBlocks);
+                               g_dev_sms[dev].load(std::memory_order_relaxed), kRotFwdBlocks, kRotWarps);
     p.total = g.total, p.share = g.share;
     const auto run = [&](auto kernel) {
       return launch_pdl(kernel, dim3(g.blocks), dim3(kRotThreads), 0, s, p, places, in_place ? nullptr : length_out);
