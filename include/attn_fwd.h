@@ -460,7 +460,8 @@ typedef struct {
  * its row's position:
  *     y = x / sqrt(mean(x^2) + eps) * weight,
  *     (a, b) -> amplitude * (a cos t - b sin t, a sin t + b cos t), t = position * f_i
- * for the pairs of y's first rot channels.  fp32 throughout, rounded once.
+ * for the pairs of y's first rot channels.  fp32 throughout, rounded once (so the sum
+ * of a head's squares counts within fp32's range).
  *
  *   q, k             bf16 or fp16 (dtype), H_q and H_k heads of D elements in each
  *                    of B * S rows.  q_out, k_out the same, written; each may be
@@ -588,7 +589,9 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
  * H_q / H_kv is a whole number, at most 128.  Entries that a token's sequence holds
  * are finite (a NaN or infinity in V reaches, as a product with zero, tokens of its
  * own sequence that do not see it); what lies behind a length may be anything.
- * Results are the same from call to call.  Asynchronous (one to three launches).
+ * Results are the same from call to call; the bounds and what else is in the batch
+ * decide in which order sums are made, so they count in the last bits.  Asynchronous
+ * (one to three launches).
  */
 attn_status_t attn_paged_attend(const attn_pages_t* cache, const void* q, int64_t q_stride, void* o, float* lse,
                                 int64_t rows, const int32_t* seq_start, int H_q, float scale, int window, int sinks,

@@ -510,3 +510,93 @@ def test_back_to_back(new, hq):
     assert attn.attn_fwd_debug_status() == attn.ATTN_OK
     for o, lse in got:
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_queries_of_any_row_stride(new):
+    """q as slices of a fused projection's rows, lengths that differ."""
+    cache = make_cache([700, 30 + new], [0, 0], 2, 128, 32, torch.bfloat16, seed=new)
+    starts, s = starts_of([new, new])
+    wide = queries(2 * new, 12, 128, torch.bfloat16)
+    q = wide[:, 2:10]
+    a, b = attend(cache, q, starts, max_new=new), attend(cache, q.contiguous(), starts, max_new=new)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with pytest.raises(attn.AttnError):
+        cache.attend(q[:1].expand(2 * new, 8, 128), s, max_new=new)
+    with pytest.raises(ValueError):
+        cache.attend(wide[:, ::2], s, max_new=new)
+
+
+def test_places_beyond_32_bits():
+    """Pages whose elements, and queries whose rows, lie behind 2^32 and 2^31 of their buffers."""
+    H, page, d = 8, 256, 128
+    n_pages = (1 << 32) // (H * page * d) + 40
+    cache = attn.PagedKVCache.empty(2, H, n_pages, page, 5, d)  # 8.6 GB each of K and V
+    last = torch.arange(n_pages - 10, n_pages, dtype=torch.int32, device=DEV)
+    cache.page_table.copy_(last.flip(0).view(2, 5))
+    rows = (1 << 31) // (32 * d) + 600
+    g = torch.Generator(device=DEV).manual_seed(3)
+    new = [1100, 250]
+    at, s = starts_of(new)
+    k, v = torch.randn((2, at[-1], H, d), generator=g, device=DEV).bfloat16()
+    cache.append(k, v, seq_start=s)
+    for b in range(2):
+        kk, vv = rows_of(cache, b, 0, new[b])
+        assert torch.equal(kk, k[at[b]:at[b + 1]]) and torch.equal(vv, v[at[b]:at[b + 1]])
+    first = rows - 250  # the queries are the last rows of 4.3 GB
+    big = torch.empty((rows, 32, d), dtype=torch.bfloat16, device=DEV)
+    big[first:] = torch.randn((250, 32, d), generator=g, device=DEV).bfloat16()
+    out, lse = torch.empty_like(big), torch.empty((rows, 32), device=DEV)
+    for n in ([1, 2], [50, 200]):
+        e = first + sum(n)
+        starts = torch.tensor([first, first + n[0], e], dtype=torch.int32, device=DEV)
+        cache.attend(big, starts, max_new=max(n), out=out, lse=lse)
+        check((out[first:e], lse[first:e]), ref.attend(big[first:e], cache.k_pages[n_pages - 10:], cache.v_pages[n_pages - 10:],
+                                                       cache.page_table - (n_pages - 10), new, [0, n[0], sum(n)], d ** -0.5))
+
+
+def test_decoding_steps_in_one_graph():
+    """A step's append and attention, captured once: lengths grow in place with each replay."""
+    had, H, d = [37, 0, 300], 2, 64
+    cache = make_cache(had, [8] * 3, H, d, 16, torch.bfloat16, seed=5)
+    twin = copy.deepcopy(cache)
+    rope = attn.Rotary(attn.rotary_frequencies(d))
+    qkv = torch.empty((3, 8 + 2 * H, d), dtype=torch.bfloat16, device=DEV)
+
+    def step(c):
+        q = c.append(qkv[:, 8:8 + H], qkv[:, 8 + H:], q=qkv[:, :8], rope=rope)
+        return c.attend(q, max_len=310)
+
+    g = torch.Generator(device=DEV).manual_seed(6)
+    qkv.normal_(generator=g)
+    warm = copy.deepcopy(cache)
+    step(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(cache)
+    for i in range(5):
+        qkv.normal_(generator=g)
+        graph.replay()
+        want = step(twin)
+        torch.cuda.synchronize()
+        assert cache.length.tolist() == [n + i + 1 for n in had]
+        assert torch.equal(held[0], want[0]) and torch.equal(held[1], want[1])
+    assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+
+
+def test_calls_on_two_streams_at_once():
+    """Reads of one cache side by side, each with a workspace of its own."""
+    cache = make_cache([5000, 3000], [0, 0], 2, 128, 64, torch.bfloat16, seed=7)
+    s = torch.tensor([0, 60, 100], dtype=torch.int32, device=DEV)
+    q1, q2 = queries(2, 8, 128, torch.bfloat16, 1), queries(100, 8, 128, torch.bfloat16, 2)
+    want = cache.attend(q1), cache.attend(q2, s, max_new=60)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        got.append((cache.attend(q1, stream=streams[0]), cache.attend(q2, s, max_new=60, stream=streams[1])))
+    torch.cuda.synchronize()
+    for pair in got:
+        for (o, lse), (wo, wl) in zip(pair, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)

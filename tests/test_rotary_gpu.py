@@ -235,3 +235,28 @@ def test_training_step_through_attention():
     for got, leaf in ((grad[:, :, 0], leaves[0]), (grad[:, :, 1], leaves[1]), (dqw, leaves[2]), (dkw, leaves[3])):
         err = (got.double() - leaf.grad).norm() / leaf.grad.norm()
         assert err < 2e-2, err
+
+
+def test_places_beyond_32_bits():
+    """Rows whose elements lie behind 2^31 of their buffers, as slices of fused rows and one head behind the other."""
+    S, hq, hk, d = 120000, 96, 24, 128
+    qkv = torch.empty((1, S, hq + 2 * hk, d), dtype=torch.bfloat16, device=DEV)
+    assert qkv.numel() > 1 << 31
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for x in qkv[0].split(20000):
+        x.normal_(generator=g)
+    q, k = qkv[:, :, :hq], qkv[:, :, hq:hq + hk]
+    f = attn.rotary_frequencies(d)
+    rope, w = attn.Rotary(f), (1 + 0.3 * torch.randn((2, d), generator=g, device=DEV)).bfloat16()
+    pos = torch.arange(S, device=DEV, dtype=torch.int32)[None]
+    out = torch.empty((1, hq, S, d), dtype=torch.bfloat16, device=DEV)
+    a, b = attn.qk_norm_rope(q, k, rope, pos, w[0], w[1], q_out=out.transpose(1, 2))
+    rows = torch.tensor([0, 1, 777, 59999, 87381, 87382, 119998, 119999], device=DEV)
+    for got, x, ww in ((a, q, w[0]), (b, k, w[1])):
+        check(got[:, rows], *ref.forward(x[:, rows], ww, pos[:, rows], f, False, 1.0, 1e-6), "rows")
+    # the gradient, written over its operand
+    attn.qk_norm_rope_backward(a, b, q, k, rope, pos, w[0], w[1], dq=a, dk=b)
+    again = attn.qk_norm_rope(q[:, rows].contiguous(), k[:, rows].contiguous(), rope, pos[:, rows].contiguous(), w[0], w[1])
+    for got, dy, x, ww in ((a, again[0], q, w[0]), (b, again[1], k, w[1])):
+        dx, tol, _, _ = ref.backward(dy, x[:, rows], ww, pos[:, rows], f, False, 1.0, 1e-6, 1)
+        check(got[:, rows], dx, tol, "gradient")
