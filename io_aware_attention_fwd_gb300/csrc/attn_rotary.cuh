@@ -500,22 +500,28 @@ __global__ void __launch_bounds__(kRotBwdThreads, kRotBwdBlocks) attn_norm_rope_
   }
 }
 
-// Sums of the blocks' weight gradients: 32 columns a block, a column's rows over
-// 32 threads.
+// Sums of the blocks' weight gradients: 8 columns a block, a column's rows over 32
+// threads.
+constexpr int kRotSumThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(1024) attn_norm_dw_kernel(const float* __restrict__ part, int blocks, float* __restrict__ dqw,
-                                                            float* __restrict__ dkw) {
-  __shared__ double sum_s[32][33];
-  const int cx = static_cast<int>(threadIdx.x) & 31, y = static_cast<int>(threadIdx.x) >> 5;
-  const int col = static_cast<int>(blockIdx.x) * 32 + cx;
+__global__ void __launch_bounds__(kRotSumThreads) attn_norm_dw_kernel(const float* __restrict__ part, int blocks,
+                                                                      float* __restrict__ dqw, float* __restrict__ dkw) {
+  __shared__ double sum_s[kRotSumThreads / 32][8];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const int col = static_cast<int>(blockIdx.x) * 8 + (tid & 7);
   grid_dependency_wait();
   grid_launch_dependents();
   double v = 0.0;
-  for (int i = y; i < blocks; i += 32) v += static_cast<double>(__ldg(part + static_cast<int64_t>(i) * 2 * D + col));
-  sum_s[y][cx] = v;
+#pragma unroll 4
+  for (int i = tid >> 3; i < blocks; i += kRotSumThreads / 8) v += static_cast<double>(__ldg(part + static_cast<int64_t>(i) * 2 * D + col));
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  if (lane < 8) sum_s[tid >> 5][lane] = v;
   __syncthreads();
-  if (y == 0) {
-    for (int i = 1; i < 32; ++i) v += sum_s[i][cx];
+  if (tid < 8) {
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < kRotSumThreads / 32; ++i) v += sum_s[i][tid];
     float* const out = col < D ? dqw : dkw;
     if (out != nullptr) out[col % D] = static_cast<float>(v);
   }
@@ -697,7 +703,7 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads
   }
   if (e == cudaSuccess && norm) {
     const auto run = [&](auto kernel) {
-      return launch_pdl(kernel, dim3(static_cast<unsigned>(2 * D / 32)), dim3(1024), 0, s, static_cast<const float*>(workspace),
+      return launch_pdl(kernel, dim3(static_cast<unsigned>(2 * D / 8)), dim3(kRotSumThreads), 0, s, static_cast<const float*>(workspace),
                         static_cast<int>(blocks), dq_weight, dk_weight);
     };
     e = D == 64 ? run(attn_norm_dw_kernel<64>) : run(attn_norm_dw_kernel<128>);
