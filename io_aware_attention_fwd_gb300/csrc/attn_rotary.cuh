@@ -18,18 +18,18 @@
 // A row of 256 (128) bytes is 16 (8) lanes of 8 channels, so a warp takes 2 (4) heads
 // of a token at once; what pairs with a lane's channels is one shuffle of the 16-bit
 // words away.  All groups of heads of all tokens form one list, cut into equal
-// shares, one a warp, which has four groups on their way at once.  The sine and cosine
-// of a token are worked out by the warp that comes to it, while its first groups travel;
+// shares, one a warp, which has a few groups on their way, copied asynchronously into a
+// ring of its own in shared memory (each lane its own 16 bytes).  The sine and cosine of a
+// token are worked out by the warp that comes to it, while its first groups travel;
 // what they and the weights make of a lane's channels,
 //     y = r (x A + x' B)   (x' the paired channels),
 // stays in registers for all heads of the token.
-// 16384 tokens of 64 heads, D = 128 (537 MB): 95 us, 5.6 TB/s, against 86 us for a copy
-// of the same tensors and 88 us without the norm.  With a block's tokens' tables in
-// shared memory, read for each head, it took 186 us; walking group by group with the
-// addresses worked out anew, 159 (226 instructions a group); with each group asked for
-// when one was done, 110.  The gradient of as many tokens of 40 heads (503 MB): 106 us,
-// 4.7 TB/s; it is held up by its 128 registers a thread (two blocks an SM), but three
-// blocks spill and take 128 to 138.
+// 16384 tokens of 64 heads, D = 128 (537 MB): 88 us, 6.1 TB/s, against 86 us for a copy
+// of the same tensors.  With a block's tokens' tables in shared memory, read for each
+// head, it took 186 us; walking group by group with the addresses worked out anew, 159
+// (226 instructions a group); four groups at once in registers, 96.  The gradient of as
+// many tokens of 40 heads (503 MB): 106 us, 4.7 TB/s; it is held up by its 128 registers
+// a thread (two blocks an SM), but three blocks spill and take 128 to 138.
 
 namespace {
 
@@ -227,11 +227,16 @@ struct NoPages {};
 template <int D, int kType, bool kPaged, typename Paged>
 __device__ __forceinline__ void rot_forward_body(const RotParams& p, Paged pg) {
   using Lane = RotLane<D>;
-  constexpr int kBatch = 4;  // groups on their way at once
+  // Groups on their way.  16384 tokens of 64 heads took 92 / 89 / 92 / 97 / 98 us with 2 to
+  // 6 (2 at four blocks an SM), 33021 tokens into pages of 16 138 / 139 / 132 / 134 with 3
+  // to 6; in registers, four at once, 96 and 152.
+  constexpr int kRing = kPaged ? 5 : 3;
+  __shared__ __align__(16) uint4 ring_s[kRotWarps][kRing][32];
   __shared__ __align__(16) float cs_s[kRotWarps][D];
   __shared__ __align__(16) float w_s[2][D];
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const Lane ln(lane, p.turn);
+  const uint32_t ring = smem_u32(&ring_s[warp][0][lane]);
   grid_dependency_wait();
   grid_launch_dependents();
   rot_weights<D, kType>(w_s, p);
@@ -269,43 +274,48 @@ __device__ __forceinline__ void rot_forward_body(const RotParams& p, Paged pg) {
     }
     const bool turns = !kPaged || w.kind < 2, norm = turns && p.w[w.kind & 1] != nullptr;
     uint64_t A[4], B[4];
-    bool fresh = turns;
+    int ahead = head;
+    const auto fetch = [&](int slot) {
+      if (ahead < end) cp_async_16(ring + slot * 512, src);
+      cp_async_commit();
+      ahead += Lane::kRows;
+      src += in_step;
+    };
+#pragma unroll
+    for (int u = 0; u < kRing; ++u) fetch(u);
+    if (turns) {  // while the first groups are on their way
+      if (w.token && p.turn.rot > 0) {
+        int pos;
+        if constexpr (kPaged)
+          pos = pg.pos;
+        else
+          pos = __ldg(p.pos + static_cast<int64_t>(w.b) * p.S + w.s);
+        table.fill(cs, lane, pos, p.turn);
+      }
+      float co[8], si[8], own[8], other[8];
+      rot_angles<D>(co, si, ln, p.turn, cs);
+      rot_load8(own, w_s[w.kind & 1] + ln.c0);
+      rot_load8(other, w_s[w.kind & 1] + (ln.partner % Lane::kLanes) * 8);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float o0 = p.turn.inter ? other[2 * e + 1] : other[2 * e], o1 = p.turn.inter ? other[2 * e] : other[2 * e + 1];
+        A[e] = pack_f32x2(co[2 * e] * own[2 * e], co[2 * e + 1] * own[2 * e + 1]);
+        B[e] = pack_f32x2(si[2 * e] * o0, si[2 * e + 1] * o1);
+      }
+    }
     while (left > 0) {
-      uint4 raw[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (head + u * Lane::kRows < end) raw[u] = *reinterpret_cast<const uint4*>(src + u * in_step);
-      }
-      if (fresh) {  // while the first groups are on their way
-        fresh = false;
-        if (w.token && p.turn.rot > 0) {
-          int pos;
-          if constexpr (kPaged)
-            pos = pg.pos;
-          else
-            pos = __ldg(p.pos + static_cast<int64_t>(w.b) * p.S + w.s);
-          table.fill(cs, lane, pos, p.turn);
-        }
-        float co[8], si[8], own[8], other[8];
-        rot_angles<D>(co, si, ln, p.turn, cs);
-        rot_load8(own, w_s[w.kind & 1] + ln.c0);
-        rot_load8(other, w_s[w.kind & 1] + (ln.partner % Lane::kLanes) * 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float o0 = p.turn.inter ? other[2 * e + 1] : other[2 * e], o1 = p.turn.inter ? other[2 * e] : other[2 * e + 1];
-          A[e] = pack_f32x2(co[2 * e] * own[2 * e], co[2 * e + 1] * own[2 * e + 1]);
-          B[e] = pack_f32x2(si[2 * e] * o0, si[2 * e + 1] * o1);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (u >= left) break;
-        uint4 out = raw[u];
+      for (int u = 0; u < kRing; ++u) {
+        if (left == 0) break;
+        const bool there = head < end;
+        cp_async_wait<kRing - 1>();  // this lane's copy of this group
+        uint4 out = make_uint4(0, 0, 0, 0);
+        if (there) out = rot_shared(ring + u * 512);
         if (turns) {
           uint64_t y[4], z[4];
-          rot_unpack<kType>(y, raw[u]);
-          rot_unpack<kType>(z, rot_paired(raw[u], p.turn, ln.partner));
+          rot_unpack<kType>(y, out);
+          rot_unpack<kType>(z, rot_paired(out, p.turn, ln.partner));
+          fetch(u);
           float r = 1.f;
           if (norm) {
             uint64_t sq = mul_f32x2(y[0], y[0]);
@@ -320,14 +330,16 @@ __device__ __forceinline__ void rot_forward_body(const RotParams& p, Paged pg) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = mul_f32x2(fma_f32x2(z[e], B[e], mul_f32x2(y[e], A[e])), r2);
           out = rot_pack<kType>(y);
+        } else {
+          fetch(u);
         }
-        if (head + u * Lane::kRows < end && keep) *reinterpret_cast<uint4*>(dst + u * out_step) = out;
+        if (there && keep) *reinterpret_cast<uint4*>(dst) = out;
+        head += Lane::kRows;
+        dst += out_step;
+        --left;
       }
-      head += kBatch * Lane::kRows;
-      left -= kBatch;
-      src += kBatch * in_step;
-      dst += kBatch * out_step;
     }
+    cp_async_wait<0>();
     more = w.next(p);
     if constexpr (kPaged)
       if (more && w.token) pg.step(w.s);
@@ -340,7 +352,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotFwdBlocks) attn_norm_rope_ker
 }
 
 // Gradient, walked the same way.  A lane adds up g r x of its channels, for q and for
-// k, in fp32 (its share's rows, a few hundred at most); the block's sums are added in
+// k, in fp32 (its share's rows: 135 of 16384 tokens with 40 heads); the block's sums are added in
 // shared memory, and a second kernel adds the blocks' in 64 bits: the same from call
 // to call.
 constexpr int kRotBwdThreads = 256;
@@ -348,9 +360,8 @@ constexpr int kRotBwdWarps = kRotBwdThreads / 32;
 constexpr int kRotBwdBlocks = 2;  // blocks an SM
 
 // A run of the gradient: heads of one kind; dw: its weight's sums.  dy and x come
-// through a ring of this warp's in shared memory, each lane's own 16 bytes: in
-// registers they left the SM 16 warps and four groups each on their way.
-constexpr int kRotRing = 4;  // groups on their way
+// through the ring (in registers, four groups at once, it took 112 us instead of 108).
+constexpr int kRotRing = 3;  // groups on their way (2 to 6: 111, 108, 109, 115, 119 us for 16384 tokens of 40 heads)
 template <int D, int kType>
 __device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWalk& w, const RotLane<D>& ln, const uint64_t* A,
                                                  const uint64_t* B, const float* w_s, uint64_t* dw, uint32_t ring) {
