@@ -107,16 +107,21 @@ struct ChunkAt {
 };
 
 // A CTA's units: its share of the list, or one.  Each warp has a walk of its own in
-// shared memory (its lanes write the same there): held in registers across the MMA
-// warp's loop, it took the descriptors' places (512 tokens over 32768 entries: 208 us
-// instead of 190).
+// shared memory, which its first lane moves on: held in registers across the MMA warp's
+// loop, it took the descriptors' places (512 tokens over 32768 entries: 208 us instead
+// of 190).
 struct ChunkWalk {
   int64_t first, end;  // where the unit's tiles begin in the list, and the share ends
   int64_t from;        // where the share begins
   int u;
   ChunkAt at;
   bool one;
+  // (the whole warp)
   __device__ void start(const ChunkParams& p) {
+    if ((threadIdx.x & 31) == 0) init(p);
+    __syncwarp();
+  }
+  __device__ void init(const ChunkParams& p) {
     first = end = from = 0;
     u = 0;
     at.h = -1;
@@ -140,10 +145,12 @@ struct ChunkWalk {
   // The next unit, or false (the whole warp).  own: sequence and first token of the
   // CTA's only one, or -1.
   __device__ bool next(const ChunkParams& p, const volatile int* own) {
+    __syncwarp();  // the unit at hand has been read
+    int more = 0;
+    if ((threadIdx.x & 31) == 0) more = step(p, own);
+    more = __shfl_sync(0xffffffffu, more, 0);
     __syncwarp();
-    const bool more = step(p, own);
-    __syncwarp();
-    return more;
+    return more != 0;
   }
   __device__ bool step(const ChunkParams& p, const volatile int* own) {
     if (one) {
@@ -748,7 +755,7 @@ __device__ void chunk_epilogue_role(const Smem<D, false>& sm, const volatile int
     // the CTA's first unit: is this the first cut of it?  (chunk_cut says where cuts are)
     ChunkCut cut{-1, 0, 0, 0, 0, 0, {0, 0}};
     ChunkWalk first;
-    first.start(p);
+    first.init(p);
     if (first.step(p, own) && first.at.j0 > 0) {
       const int64_t share = __ldg(&p.head->share);
       const int64_t ca = (first.first + kChunkLeast + share - 1) / share - 1, cb = (first.first + first.at.w.tiles - kChunkLeast) / share;
