@@ -124,7 +124,7 @@ class PagedKVCache:
         elif q_out is not None or q_weight is not None:
             raise ValueError("q_out and q_weight go with q")
         r = rope_address(rope, device)
-        qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device, D)
+        qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device.index, D)
         if length_out is None:
             length_out = self.length
         else:

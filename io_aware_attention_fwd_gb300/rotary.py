@@ -96,45 +96,42 @@ def rope_address(rope, device):
     return rope._address
 
 
-def check_weight(w, dtype, device, D, name) -> int:
+def check_weight(w, dtype, index, D, name) -> int:
     """attn_dtype_t of a norm's weight."""
     import torch
 
     kind = w.dtype
-    if w.shape != (D,) or w.device != device or not w.is_contiguous() or (kind != dtype and kind != torch.float32):
-        raise ValueError(f"{name} must be a contiguous tensor of {D} entries on {device}, {dtype} or float32")
+    if w.shape != (D,) or w.get_device() != index or not w.is_contiguous() or (kind != dtype and kind != torch.float32):
+        raise ValueError(f"{name} must be a contiguous tensor of {D} entries on device {index}, {dtype} or float32")
     return element_type(kind, True)
 
 
-def norm_weights(q_weight, k_weight, dtype, device, D):
-    """(address of q's, of k's, attn_dtype_t of both)."""
+def norm_weights(q_weight, k_weight, dtype, index, D):
+    """(address of q's, of k's, attn_dtype_t of both); index: the device's."""
     if q_weight is None:
         return None, *((None, _lib.ATTN_FP32) if k_weight is None else
-                       (k_weight.data_ptr(), check_weight(k_weight, dtype, device, D, "k_weight")))
-    code = check_weight(q_weight, dtype, device, D, "q_weight")
+                       (k_weight.data_ptr(), check_weight(k_weight, dtype, index, D, "k_weight")))
+    code = check_weight(q_weight, dtype, index, D, "q_weight")
     if k_weight is None:
         return q_weight.data_ptr(), None, code
-    if check_weight(k_weight, dtype, device, D, "k_weight") != code:
+    if check_weight(k_weight, dtype, index, D, "k_weight") != code:
         raise TypeError("q_weight and k_weight must be of one type")
     return q_weight.data_ptr(), k_weight.data_ptr(), code
 
 
-def _heads(t, shape, dtype, device, name, out=False):
-    """What attn_heads_t holds of rows [S, H, D] or [B, S, H, D]: address, strides."""
-    if t.dtype != dtype or t.device != device or t.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on {device}")
-    stride = t.stride()
-    # where there is one of something, its stride says nothing (and may be anything)
+def _strides(stride, shape, name, out=False):
+    """(batch, row, head) strides of rows [S, H, D] or [B, S, H, D].  Where there is one of
+    something, its stride says nothing (and may be anything)."""
     if len(stride) == 4:
-        n, S, H, _ = shape
         b, s, h, one = stride
+        n, S, H, _ = shape
         if n < 2:
             b = 0
         elif out and b == 0:
             raise ValueError(f"{name}: rows of an output must lie apart")
     else:
-        S, H, _ = shape
         s, h, one = stride
+        S, H, _ = shape
         b = 0
     if S < 2:
         s = 0
@@ -146,7 +143,14 @@ def _heads(t, shape, dtype, device, name, out=False):
         raise ValueError(f"{name}: rows of an output must lie apart")
     if one != 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
-    return t.data_ptr(), b, s, h
+    return b, s, h
+
+
+def _heads(t, shape, dtype, index, name, out=False):
+    """What attn_heads_t holds of rows [S, H, D] or [B, S, H, D]: address, strides."""
+    if t.dtype != dtype or t.get_device() != index or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on device {index}")
+    return t.data_ptr(), *_strides(t.stride(), shape, name, out)
 
 
 _Rows4 = ctypes.c_int64 * 16  # four attn_heads_t
@@ -160,15 +164,15 @@ def _shapes(a, b):
     return (a[0] if len(a) == 4 else 1), a[-3], a[-2], b[-2], a[-1]
 
 
-def _positions(positions, rope, shape, device):
+def _positions(positions, rope, shape, index):
     import torch
 
     if positions is None:
         if rope is not None and rope.rot:
             raise ValueError("positions are needed for a rotation")
         return None
-    if positions.dtype != torch.int32 or positions.device != device or positions.shape != shape or not positions.is_contiguous():
-        raise ValueError(f"positions must be a contiguous int32 tensor {tuple(shape)} on {device}")
+    if positions.dtype != torch.int32 or positions.get_device() != index or positions.shape != shape or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous int32 tensor {tuple(shape)} on device {index}")
     return positions.data_ptr()
 
 
@@ -190,10 +194,11 @@ def qk_norm_rope(q, k, rope, positions=None, q_weight=None, k_weight=None, eps: 
     code = element_type(dtype)
     if device.type != "cuda":
         raise ValueError("q and k must be CUDA tensors of one device")
-    hq, hk = _heads(q, shape, dtype, device, "q"), _heads(k, k_shape, dtype, device, "k")
+    index = q.get_device()
+    hq, hk = _strides(q.stride(), shape, "q"), _heads(k, k_shape, dtype, index, "k")
     r = rope_address(rope, device)
-    pos = _positions(positions, rope, shape[:-2], device)
-    qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device, D)
+    pos = _positions(positions, rope, shape[:-2], index)
+    qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, index, D)
     handle = current_handle(device) if stream is None else None
     if handle is None:
         return on_stream(device, stream, lambda: qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, q_out, k_out))
@@ -201,7 +206,8 @@ def qk_norm_rope(q, k, rope, positions=None, q_weight=None, k_weight=None, eps: 
         q_out = torch.empty(shape, dtype=dtype, device=device)
     if k_out is None:
         k_out = torch.empty(k_shape, dtype=dtype, device=device)
-    rows = _Rows4(*hq, *hk, *_heads(q_out, shape, dtype, device, "q_out", True), *_heads(k_out, k_shape, dtype, device, "k_out", True))
+    rows = _Rows4(q.data_ptr(), *hq, *hk, *_heads(q_out, shape, dtype, index, "q_out", True),
+                  *_heads(k_out, k_shape, dtype, index, "k_out", True))
     at = ctypes.addressof(rows)
     _lib.attn_qk_norm_rope(at, at + 32, at + 64, at + 96, B, S, H_q, H_k, D, code, r, pos, qw, kw, w_code, eps, handle)
     return q_out, k_out
@@ -223,11 +229,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, rope, positions=None, q_weight=N
     code = element_type(dtype)
     if device.type != "cuda":
         raise ValueError("q and k must be CUDA tensors of one device")
-    hq, hk = _heads(q, shape, dtype, device, "q"), _heads(k, k_shape, dtype, device, "k")
-    gq, gk = _heads(dq_out, shape, dtype, device, "dq_out"), _heads(dk_out, k_shape, dtype, device, "dk_out")
+    index = q.get_device()
+    hq, hk = _strides(q.stride(), shape, "q"), _heads(k, k_shape, dtype, index, "k")
+    gq, gk = _heads(dq_out, shape, dtype, index, "dq_out"), _heads(dk_out, k_shape, dtype, index, "dk_out")
     r = rope_address(rope, device)
-    pos = _positions(positions, rope, shape[:-2], device)
-    qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, device, D)
+    pos = _positions(positions, rope, shape[:-2], index)
+    qw, kw, w_code = norm_weights(q_weight, k_weight, dtype, index, D)
     handle = current_handle(device) if stream is None else None
     if handle is None:
         return on_stream(device, stream, lambda: qk_norm_rope_backward(dq_out, dk_out, q, k, rope, positions, q_weight, k_weight,
@@ -236,12 +243,14 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, rope, positions=None, q_weight=N
         dq = torch.empty(shape, dtype=dtype, device=device)
     if dk is None:
         dk = torch.empty(k_shape, dtype=dtype, device=device)
-    dqw, dkw = (None if w is None else torch.empty(D, dtype=torch.float32, device=device) for w in (q_weight, k_weight))
+    dqw = None if qw is None else torch.empty(D, dtype=torch.float32, device=device)
+    dkw = None if kw is None else torch.empty(D, dtype=torch.float32, device=device)
     ws, nbytes = None, 0
     if qw is not None or kw is not None:
         nbytes = _lib.attn_qk_norm_rope_bwd_workspace_bytes(B, S, H_q, H_k, D)
         ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    rows = _Rows6(*gq, *gk, *hq, *hk, *_heads(dq, shape, dtype, device, "dq", True), *_heads(dk, k_shape, dtype, device, "dk", True))
+    rows = _Rows6(*gq, *gk, q.data_ptr(), *hq, *hk, *_heads(dq, shape, dtype, index, "dq", True),
+                  *_heads(dk, k_shape, dtype, index, "dk", True))
     at = ctypes.addressof(rows)
     _lib.attn_qk_norm_rope_bwd(at, at + 32, at + 64, at + 96, at + 128, at + 160, B, S, H_q, H_k, D, code, r, pos, qw, kw, w_code,
                                eps, dqw, dkw, ws, nbytes, handle)
