@@ -553,7 +553,7 @@ typedef struct {
  *               as attn_qk_norm_rope: q and k are normed and turned by their
  *               positions on the way, v is written as it is.
  *   length_out  device int32[B], written: the lengths after the call.  It may be
- *               cache->length (one more small launch).
+ *               cache->length (one more small launch), but not overlap it otherwise.
  * Rows for which there is no room are dropped, the length stays at the capacity
  * (max_pages * page), and attn_fwd_debug_status reports ATTN_ERR_CAPACITY; their
  * queries are still written.  No two sequences may write one page.  Asynchronous.

@@ -53,6 +53,10 @@ struct PagedPlaces {
   int64_t to;         // first element of its place in its page, for key head 0, or -1
   int b, end;         // its sequence, or B, and the row behind its sequence's (or the next to look up)
   int pos;            // its entry's number
+  // A length, past the SM's own cache: a line that also holds new lengths (another row of
+  // one buffer, or other sequences of `length`) must not stay there for the next kernel,
+  // whose blocks may be on the SM before the new ones are written.
+  __device__ static int length(const int32_t* len) { return max(__ldcg(len), 0); }
   __device__ bool live() const { return b < s.B; }
   __device__ void find(int row) {
     b = s.sequence(row);
@@ -65,7 +69,7 @@ struct PagedPlaces {
       i = row - s.start(b);
       end = s.start(b + 1);
     }
-    const int64_t at = static_cast<int64_t>(max(__ldg(s.len + b), 0)) + i;
+    const int64_t at = static_cast<int64_t>(length(s.len + b)) + i;
     pos = static_cast<int>(min(at, static_cast<int64_t>(INT_MAX)));
     place();
   }
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotFwdBlocks)
   if (len_out == nullptr) return;
   for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < places.s.B;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t l = static_cast<int64_t>(max(0, __ldg(places.s.len + b))) + places.s.rows_of(static_cast<int>(b));
+    const int64_t l = static_cast<int64_t>(PagedPlaces::length(places.s.len + b)) + places.s.rows_of(static_cast<int>(b));
     len_out[b] = static_cast<int32_t>(min(l, places.s.capacity()));
   }
 }
@@ -117,7 +121,7 @@ __global__ void attn_paged_grow_kernel(const __grid_constant__ PagedSeqs s, cons
   grid_launch_dependents();
   for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < s.B;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t l = static_cast<int64_t>(max(0, len[b])) + s.rows_of(static_cast<int>(b));
+    const int64_t l = static_cast<int64_t>(PagedPlaces::length(len + b)) + s.rows_of(static_cast<int>(b));
     len_out[b] = static_cast<int32_t>(min(l, s.capacity()));
   }
 }
@@ -173,6 +177,10 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
       (q != nullptr && q_stride % 8 != 0) || !aligned(seq_start, 4) || !aligned(length_out, 4))
     return ATTN_ERR_ALIGNMENT;
+  // new lengths over the old ones of other sequences
+  if (length_out != cache->length && std::less<>()(length_out, cache->length + cache->B) &&
+      std::less<>()(static_cast<const int32_t*>(cache->length), length_out + cache->B))
+    return ATTN_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_DEVICE;
   st = prepare_device(dev);

@@ -94,7 +94,7 @@ class PagedKVCache:
         them; K, and the tokens' queries q [rows, H_q, D] if given, are normed and turned by
         their entries' numbers on the way.  Returns q_out (a new tensor if None; rows of no
         sequence are left as they were), or None without q.  length_out: where the new lengths
-        go (None: ``length`` itself).  Rows beyond the capacity (max_pages * page) are dropped,
+        go (None: ``length`` itself, which it must not overlap in part).  Rows beyond the capacity (max_pages * page) are dropped,
         and attn_fwd_debug_status then reports ATTN_ERR_CAPACITY.
         """
         import torch

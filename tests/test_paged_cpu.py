@@ -64,6 +64,7 @@ def test_sizes_beyond_an_int():
     (dict(eps=math.nan), INVALID), (dict(weight_dtype=attn.ATTN_FP16), UNSUPPORTED), (dict(k_weight=FAKE + 1), ALIGNMENT),
     (dict(rope=attn.attn_rotary_t(FAKE, 24, 0, 1.0)), UNSUPPORTED), (dict(rope=attn.attn_rotary_t(None, 32, 0, 1.0)), INVALID),
     (dict(q=None, q_out=None), INVALID),  # a weight for queries that are not there
+    (dict(length_out=FAKE + 4), INVALID), (dict(length_out=FAKE - 4), INVALID),  # over the old ones of other sequences
 ])
 def test_append_argument_checks(kw, expect):
     assert attn.call_status(attn.attn_paged_append, pages(), **{**APPEND, **kw}) == expect

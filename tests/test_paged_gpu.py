@@ -585,6 +585,38 @@ def test_decoding_steps_in_one_graph():
     assert attn.attn_fwd_debug_status() == attn.ATTN_OK
 
 
+@pytest.mark.parametrize("B,turns", [(3, 40), (300, 6)])
+def test_old_and_new_lengths_side_by_side(B, turns):
+    """Two rows of one buffer in turn, and a piece of a longer one in place, against buffers of their own."""
+    H, d, page = 2, 64, 16
+    apart = attn.PagedKVCache.empty(B, H, B * 4, page, 4, d)
+    apart.page_table.copy_(torch.arange(B * 4, dtype=torch.int32, device=DEV).view(B, 4))
+    pair = torch.zeros((2, B), dtype=torch.int32, device=DEV)
+    piece = torch.full((B + 7,), 9, dtype=torch.int32, device=DEV)
+    turned, inside = (attn.PagedKVCache(torch.empty_like(apart.k_pages), torch.empty_like(apart.v_pages), apart.page_table, x)
+                      for x in (pair[0], piece[5:5 + B]))
+    turned.length.zero_(), inside.length.zero_()
+    g = torch.Generator(device=DEV).manual_seed(9)
+    qkv = torch.randn((turns, B, 4 + 2 * H, d), generator=g, device=DEV).bfloat16()
+    rope = attn.Rotary(attn.rotary_frequencies(d))
+    got = []
+    for c in (apart, turned, inside):
+        steps = []
+        for i in range(turns):
+            out = pair[1 - i % 2] if c is turned else None
+            q = c.append(qkv[i, :, 4:4 + H], qkv[i, :, 4 + H:], q=qkv[i, :, :4], rope=rope, length_out=out)
+            if c is turned:
+                c.length = out
+            steps.append(c.attend(q))
+        got.append(steps)
+    torch.cuda.synchronize()
+    assert attn.attn_fwd_debug_status() == attn.ATTN_OK
+    assert (piece[:5] == 9).all() and (piece[5 + B:] == 9).all() and (piece[5:5 + B] == turns).all() and (turned.length == turns).all()
+    for steps in got[1:]:
+        for x, y in zip(steps, got[0]):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 def test_calls_on_two_streams_at_once():
     """Reads of one cache side by side, each with a workspace of its own."""
     cache = make_cache([5000, 3000], [0, 0], 2, 128, 64, torch.bfloat16, seed=7)
