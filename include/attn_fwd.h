@@ -444,7 +444,9 @@ typedef struct {
  *                i as a fraction of a turn, f_i / (2 pi) * 2^64 modulo 2^64; angles
  *                are then exact for every position.  May be NULL where rot is 0.
  *   rot          channels of a head that are turned, its first ones: a multiple
- *                of 16, 0 .. D.
+ *                of 16, 0 .. D.  The others meet no other channel: without a norm they
+ *                are passed on bit by bit, infinities and signed zeros too (a NaN as
+ *                some NaN).
  *   interleaved  0: pair i is channels (i, i + rot / 2); 1: (2i, 2i + 1).
  *   amplitude    factor on the turned channels (finite; 1 for a pure rotation).
  */

@@ -70,7 +70,7 @@ struct RotLane {
   static constexpr int kLanes = D / 8;       // lanes a row
   static constexpr int kRows = 32 / kLanes;  // rows a warp
   int sub, c0;                               // this lane's row of the warp's, and first channel
-  int partner;                               // lane with the paired channels (half layout)
+  int pair;                                  // where the paired channels are: a lane (half layout), or bytes of the same word
   bool turned, low;
   int at;                                    // of its first cosine
   __device__ RotLane(int lane, const RotTurn& t) {
@@ -79,7 +79,7 @@ struct RotLane {
     const int half = t.rot / 2;
     turned = c0 < t.rot;
     low = c0 < half;
-    partner = t.inter || !turned ? lane : lane + (low ? half : -half) / 8;
+    pair = t.inter ? (turned ? 0x1032 : 0x3210) : !turned ? lane : lane + (low ? half : -half) / 8;
     at = t.inter ? c0 / 2 : low ? c0 : c0 - half;
   }
 };
@@ -163,12 +163,13 @@ __device__ __forceinline__ uint4 rot_pack(const uint64_t* x) {
   }
   return w;
 }
-// The words that hold the paired channels: another lane's, or this one's with their halves exchanged.
-__device__ __forceinline__ uint4 rot_paired(const uint4& w, const RotTurn& t, int partner) {
-  if (t.inter) return make_uint4(__byte_perm(w.x, w.x, 0x1032), __byte_perm(w.y, w.y, 0x1032), __byte_perm(w.z, w.z, 0x1032),
-                                 __byte_perm(w.w, w.w, 0x1032));
-  return make_uint4(__shfl_sync(0xffffffffu, w.x, partner), __shfl_sync(0xffffffffu, w.y, partner),
-                    __shfl_sync(0xffffffffu, w.z, partner), __shfl_sync(0xffffffffu, w.w, partner));
+// The words that hold the paired channels: another lane's, or this one's with their halves
+// exchanged.  A channel that is not turned is paired with itself.
+__device__ __forceinline__ uint4 rot_paired(const uint4& w, const RotTurn& t, int pair) {
+  if (t.inter) return make_uint4(__byte_perm(w.x, 0u, pair), __byte_perm(w.y, 0u, pair), __byte_perm(w.z, 0u, pair),
+                                 __byte_perm(w.w, 0u, pair));
+  return make_uint4(__shfl_sync(0xffffffffu, w.x, pair), __shfl_sync(0xffffffffu, w.y, pair),
+                    __shfl_sync(0xffffffffu, w.z, pair), __shfl_sync(0xffffffffu, w.w, pair));
 }
 __device__ __forceinline__ float rot_sum(uint64_t v) {
   float a, b;
@@ -193,12 +194,13 @@ __device__ __forceinline__ void rot_load8(float* x, const float* s) {
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 // Cosines of this lane's channels, and sines with the sign that the paired channel has
-// (forward; the gradient's is the other one).
+// (forward; the gradient's is the other one).  A channel that is not turned is half of itself and
+// half of itself again, which is itself: products with 0 would make NaN of an infinity.
 template <int D>
 __device__ __forceinline__ void rot_angles(float* co, float* si, const RotLane<D>& ln, const RotTurn& t, const float* cs) {
   if (!ln.turned) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) co[e] = 1.f, si[e] = 0.f;
+    for (int e = 0; e < 8; ++e) co[e] = 0.5f, si[e] = 0.5f;
   } else if (t.inter) {
     const float4 c = *reinterpret_cast<const float4*>(cs + ln.at), s = *reinterpret_cast<const float4*>(cs + t.rot / 2 + ln.at);
     const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
@@ -295,10 +297,11 @@ __device__ __forceinline__ void rot_forward_body(const RotParams& p, Paged pg) {
       float co[8], si[8], own[8], other[8];
       rot_angles<D>(co, si, ln, p.turn, cs);
       rot_load8(own, w_s[w.kind & 1] + ln.c0);
-      rot_load8(other, w_s[w.kind & 1] + (ln.partner % Lane::kLanes) * 8);
+      rot_load8(other, w_s[w.kind & 1] + (p.turn.inter ? ln.c0 : (ln.pair % Lane::kLanes) * 8));
+      const bool swap = p.turn.inter && ln.turned;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float o0 = p.turn.inter ? other[2 * e + 1] : other[2 * e], o1 = p.turn.inter ? other[2 * e] : other[2 * e + 1];
+        const float o0 = swap ? other[2 * e + 1] : other[2 * e], o1 = swap ? other[2 * e] : other[2 * e + 1];
         A[e] = pack_f32x2(co[2 * e] * own[2 * e], co[2 * e + 1] * own[2 * e + 1]);
         B[e] = pack_f32x2(si[2 * e] * o0, si[2 * e + 1] * o1);
       }
@@ -314,7 +317,7 @@ __device__ __forceinline__ void rot_forward_body(const RotParams& p, Paged pg) {
         if (turns) {
           uint64_t y[4], z[4];
           rot_unpack<kType>(y, out);
-          rot_unpack<kType>(z, rot_paired(out, p.turn, ln.partner));
+          rot_unpack<kType>(z, rot_paired(out, p.turn, ln.pair));
           fetch(u);
           float r = 1.f;
           if (norm) {
@@ -406,7 +409,7 @@ __device__ __forceinline__ void rot_backward_run(const RotParams& p, const RotWa
       }
       uint64_t g[4], z[4];
       rot_unpack<kType>(g, dy);
-      rot_unpack<kType>(z, rot_paired(dy, p.turn, ln.partner));
+      rot_unpack<kType>(z, rot_paired(dy, p.turn, ln.pair));
 #pragma unroll
       for (int e = 0; e < 4; ++e) g[e] = fma_f32x2(z[e], B[e], mul_f32x2(g[e], A[e]));
       rot_unpack<kType>(z, x);
@@ -477,7 +480,8 @@ __global__ void __launch_bounds__(kRotBwdThreads, kRotBwdBlocks) attn_norm_rope_
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           A[e] = pack_f32x2(co[2 * e], co[2 * e + 1]);
-          B[e] = pack_f32x2(-si[2 * e], -si[2 * e + 1]);
+          const float sign = ln.turned ? -1.f : 1.f;
+          B[e] = pack_f32x2(sign * si[2 * e], sign * si[2 * e + 1]);
         }
       }
       if (w.kind == 0)
