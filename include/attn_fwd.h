@@ -558,7 +558,8 @@ typedef struct {
  *               cache->length (one more small launch), but not overlap it otherwise.
  * Rows for which there is no room are dropped, the length stays at the capacity
  * (max_pages * page), and attn_fwd_debug_status reports ATTN_ERR_CAPACITY; their
- * queries are still written.  No two sequences may write one page.  Asynchronous.
+ * queries are still written.  No two sequences may write one page.  Without rows (a
+ * step without tokens) k, v, q and q_out may be NULL.  Asynchronous.
  */
 attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const void* v, int64_t rows,
                                 int64_t k_stride, int64_t v_stride, const int32_t* seq_start, const void* q,

@@ -166,9 +166,11 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
   if (st != ATTN_OK) return st;
   st = rot_check_norm(q_weight, k_weight, weight_dtype, cache->dtype, eps);
   if (st != ATTN_OK) return st;
-  if (rows < 0 || length_out == nullptr || (q == nullptr) != (q_out == nullptr) || (q == nullptr && q_weight != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (rows < 0 || length_out == nullptr) return ATTN_ERR_INVALID_ARG;
   if (seq_start == nullptr && rows != cache->B) return ATTN_ERR_INVALID_ARG;
-  if (rows > 0 && (k == nullptr || v == nullptr)) return ATTN_ERR_INVALID_ARG;
+  // (without rows every buffer of rows may be null, as empty tensors are)
+  if (rows > 0 && (k == nullptr || v == nullptr || (q == nullptr) != (q_out == nullptr) || (q == nullptr && q_weight != nullptr)))
+    return ATTN_ERR_INVALID_ARG;
   if (q != nullptr && (H_q < 1 || H_q > 65535)) return H_q < 1 ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED;
   if (rows > INT_MAX || H_kv > 65535) return ATTN_ERR_UNSUPPORTED;
   if (k_stride < static_cast<int64_t>(H_kv) * D || v_stride < static_cast<int64_t>(H_kv) * D ||
