@@ -37,6 +37,10 @@ struct PagedSeqs {
     return lo;
   }
   __device__ int64_t capacity() const { return static_cast<int64_t>(max_pages) << page_log2; }
+  // Entries held.  Lengths are read past the SM's own cache: a kernel's blocks may be on the SM
+  // while the append before it runs, which reads starts, table and old lengths and writes new
+  // ones, and a line of all of these that came to that cache meanwhile has the old ones.
+  __device__ int held(int b) const { return max(__ldcg(len + b), 0); }
   // Page of a sequence's block of entries, or -1.
   __device__ int page_of(int b, int block) const {
     const int pg = __ldg(table + static_cast<int64_t>(b) * max_pages + block);
@@ -53,10 +57,6 @@ struct PagedPlaces {
   int64_t to;         // first element of its place in its page, for key head 0, or -1
   int b, end;         // its sequence, or B, and the row behind its sequence's (or the next to look up)
   int pos;            // its entry's number
-  // A length, past the SM's own cache: a line that also holds new lengths (another row of
-  // one buffer, or other sequences of `length`) must not stay there for the next kernel,
-  // whose blocks may be on the SM before the new ones are written.
-  __device__ static int length(const int32_t* len) { return max(__ldcg(len), 0); }
   __device__ bool live() const { return b < s.B; }
   __device__ void find(int row) {
     b = s.sequence(row);
@@ -69,7 +69,7 @@ struct PagedPlaces {
       i = row - s.start(b);
       end = s.start(b + 1);
     }
-    const int64_t at = static_cast<int64_t>(length(s.len + b)) + i;
+    const int64_t at = static_cast<int64_t>(s.held(b)) + i;
     pos = static_cast<int>(min(at, static_cast<int64_t>(INT_MAX)));
     place();
   }
@@ -110,18 +110,18 @@ __global__ void __launch_bounds__(kRotThreads, kRotFwdBlocks)
   if (len_out == nullptr) return;
   for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < places.s.B;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t l = static_cast<int64_t>(PagedPlaces::length(places.s.len + b)) + places.s.rows_of(static_cast<int>(b));
+    const int64_t l = static_cast<int64_t>(places.s.held(static_cast<int>(b))) + places.s.rows_of(static_cast<int>(b));
     len_out[b] = static_cast<int32_t>(min(l, places.s.capacity()));
   }
 }
 // The same update where len_out is the cache's own length (a launch behind the one
 // whose blocks all read it), or where there are no rows.
-__global__ void attn_paged_grow_kernel(const __grid_constant__ PagedSeqs s, const int32_t* len, int32_t* len_out) {
+__global__ void attn_paged_grow_kernel(const __grid_constant__ PagedSeqs s, int32_t* len_out) {
   grid_dependency_wait();
   grid_launch_dependents();
   for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < s.B;
        b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t l = static_cast<int64_t>(PagedPlaces::length(len + b)) + s.rows_of(static_cast<int>(b));
+    const int64_t l = static_cast<int64_t>(s.held(static_cast<int>(b))) + s.rows_of(static_cast<int>(b));
     len_out[b] = static_cast<int32_t>(min(l, s.capacity()));
   }
 }
@@ -218,7 +218,7 @@ attn_status_t attn_paged_append(const attn_pages_t* cache, const void* k, const 
   }
   if (e == cudaSuccess && (in_place || rows == 0))
     e = launch_pdl(attn_paged_grow_kernel, dim3(static_cast<unsigned>(std::min((cache->B + 255) / 256, 64))), dim3(256), 0, s,
-                   places.s, static_cast<const int32_t*>(cache->length), length_out);
+                   places.s, length_out);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
