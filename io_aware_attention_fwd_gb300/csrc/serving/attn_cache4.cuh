@@ -27,9 +27,15 @@ struct Cache4 {
   int cap;
 };
 
-// Number of cache entries of sequence b that a call sees.
-__device__ __forceinline__ int c4_len(const int32_t* __restrict__ len, int b, int most) {
-  return min(max(__ldg(len + b), 0), most);
+// Entries that sequence b holds, by a coherent load: a kernel's blocks may be on the GPU
+// while the append or eviction before it writes lengths, and the read-only path's loads
+// promise that nothing does.
+__device__ __forceinline__ int c4_held(const int32_t* len, int b) { return max(__ldca(len + b), 0); }
+// Number of cache entries of sequence b that a call sees.  kKept: in a kernel that begins
+// when they are written (attn_cache4_merge_kernel), which may keep them.
+template <bool kKept = false>
+__device__ __forceinline__ int c4_len(const int32_t* len, int b, int most) {
+  return min(kKept ? max(__ldg(len + b), 0) : c4_held(len, b), most);
 }
 
 struct Cache4Rows {
@@ -94,8 +100,7 @@ __device__ __forceinline__ C4Row c4_row(const Cache4Rows& g, const Cache4& c, in
     if (r.b >= g.B) return r;
     r.i = static_cast<int>(row) - c4_start(g, r.b);
   }
-  int slot0 = g.slot0 != nullptr ? __ldg(g.slot0 + r.b) : 0;
-  if (kAppend) slot0 = max(slot0, 0);
+  const int slot0 = kAppend ? c4_held(g.slot0, r.b) : g.slot0 != nullptr ? __ldg(g.slot0 + r.b) : 0;
   const int64_t slot = static_cast<int64_t>(slot0) + r.i;
   r.dropped = slot < 0 || slot >= c.cap;
   if (!r.dropped) r.at = static_cast<int64_t>(r.b) * c.H * c.cap + slot;
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kC4RowsThreads, 4)
     const int64_t row = row0 + threadIdx.x / kC4RowLanes<D>;
     const C4Row r = c4_row<true>(g, c, row);
     if (r.dropped && lane == 0 && h0 == 0) atomicOr(&g_attn_status, kC4Overflow);
-    const int my_pos = r.at < 0 ? 0 : (first_pos != nullptr ? __ldg(first_pos + r.b) : max(__ldg(g.slot0 + r.b), 0)) + r.i;
+    const int my_pos = r.at < 0 ? 0 : (first_pos != nullptr ? __ldg(first_pos + r.b) : c4_held(g.slot0, r.b)) + r.i;
     const int64_t from = r.at < 0 ? 0 : row;  // the others go through the motions: the statistics are whole warps'
     const uint16_t* kp = k + from * g.k_stride + h0 * D + lane * 8;
     const uint16_t* vp = v + from * g.v_stride + h0 * D + lane * 8;
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kC4RowsThreads, 4)
   if (len_out != nullptr && h0 == 0) {
     for (int64_t b = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < g.B;
          b += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-      const int64_t l = static_cast<int64_t>(max(0, __ldg(g.slot0 + b))) + c4_rows_of(g, static_cast<int>(b));
+      const int64_t l = static_cast<int64_t>(c4_held(g.slot0, static_cast<int>(b))) + c4_rows_of(g, static_cast<int>(b));
       len_out[b] = static_cast<int32_t>(l < c.cap ? l : c.cap);
     }
   }
@@ -472,8 +477,9 @@ struct DecParams {
   float* w_out;     // [B][H][cap]
 };
 
+template <bool kKept>
 __device__ __forceinline__ int c4_tiles(const DecParams& p, int b) {
-  return (c4_len(p.len, b, p.most) + kC4TileKeys - 1) / kC4TileKeys;
+  return (c4_len<kKept>(p.len, b, p.most) + kC4TileKeys - 1) / kC4TileKeys;
 }
 
 // The list that is cut into shares: each row (a sequence's key head, or block of
@@ -490,12 +496,13 @@ __device__ __forceinline__ int c4_row_units(int nt, int cost) { return nt > 0 ? 
 
 // Counts over all sequences, over those before this thread's stripe of them and
 // over its stripe.  All threads of the block call it.
+template <bool kKept>
 __device__ __forceinline__ int64_t c4_total(const DecParams& p, int64_t* warp_sums, int64_t* mine_before, int64_t* mine) {
   const int tid = static_cast<int>(threadIdx.x), n_thr = static_cast<int>(blockDim.x);
   const int stripe = (p.B + n_thr - 1) / n_thr;
   const int b0 = min(p.B, tid * stripe), b1 = min(p.B, b0 + stripe);
   int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += c4_count(c4_tiles(p, b));
+  for (int b = b0; b < b1; ++b) sum += c4_count(c4_tiles<kKept>(p, b));
   int64_t incl = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -516,6 +523,7 @@ __device__ __forceinline__ int64_t c4_total(const DecParams& p, int64_t* warp_su
 // The sequence with unit y (of one row's units; 0 <= y < their sum) and the
 // counts before it: the thread whose stripe holds it walks the stripe and
 // tells the block.
+template <bool kKept>
 __device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int cost, int64_t mine_before, int64_t mine,
                                         int* b_out, int64_t* before_out) {
   if (c4_units(mine_before, cost) <= y && y < c4_units(mine_before + mine, cost)) {
@@ -523,7 +531,7 @@ __device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int cost,
     int b = static_cast<int>(threadIdx.x) * stripe;
     int64_t at = mine_before;
     while (true) {
-      const int64_t next = at + c4_count(c4_tiles(p, b));
+      const int64_t next = at + c4_count(c4_tiles<kKept>(p, b));
       if (y < c4_units(next, cost)) break;
       at = next;
       ++b;
@@ -534,6 +542,7 @@ __device__ __forceinline__ void c4_find(const DecParams& p, int64_t y, int cost,
 }
 
 // A block's walk over its share [x, end) of a list with `rows` rows a sequence.
+template <bool kKept>
 struct C4Walk {
   int64_t x, end;
   int64_t before;   // counts before sequence b
@@ -542,7 +551,7 @@ struct C4Walk {
   // Moves to the next row whose tiles the share holds; false at the share's end.
   __device__ bool next(const DecParams& p, int rows, int cost) {
     while (x < end) {
-      n = c4_len(p.len, b, p.most);
+      n = c4_len<kKept>(p.len, b, p.most);
       nt = (n + kC4TileKeys - 1) / kC4TileKeys;
       const int units = c4_row_units(nt, cost);
       const int64_t at = x - c4_units(before, cost) * rows;
@@ -1058,7 +1067,7 @@ __global__ void __launch_bounds__(kC4DecThreads, D == 64 && kDirect ? 4 : kC4Dec
   grid_dependency_wait();
   grid_launch_dependents();  // the merge kernel's blocks come as this one's leave
   const int rows_per_b = p.c.H * p.HB;
-  C4Walk w;
+  C4Walk<false> w;
   if constexpr (kDirect) {
     w.b = static_cast<int>(blockIdx.x) / rows_per_b;
     w.row = static_cast<int>(blockIdx.x) % rows_per_b;
@@ -1067,12 +1076,12 @@ __global__ void __launch_bounds__(kC4DecThreads, D == 64 && kDirect ? 4 : kC4Dec
     w.t1 = (w.n + kC4TileKeys - 1) / kC4TileKeys;
   } else {
     int64_t mine_before, mine;
-    const int64_t total = c4_units(c4_total(p, sums_s, &mine_before, &mine), kC4RowCost) * rows_per_b;
+    const int64_t total = c4_units(c4_total<false>(p, sums_s, &mine_before, &mine), kC4RowCost) * rows_per_b;
     const int64_t share = (total + gridDim.x - 1) / gridDim.x;
     w.x = static_cast<int64_t>(blockIdx.x) * share;
     w.end = w.x + share < total ? w.x + share : total;
     if (w.x >= w.end) return;
-    c4_find(p, w.x / rows_per_b, kC4RowCost, mine_before, mine, &b_s, &before_s);
+    c4_find<false>(p, w.x / rows_per_b, kC4RowCost, mine_before, mine, &b_s, &before_s);
     __syncthreads();
     w.b = b_s;
     w.before = before_s;
@@ -1297,18 +1306,18 @@ __global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(c
   // not come there, as nothing may that writes the cache during the call.
   int64_t mine_before, mine;
   const int rows_per_b = p.c.H * p.HB;
-  const int64_t count = c4_total(p, sums_s, &mine_before, &mine);
+  const int64_t count = c4_total<true>(p, sums_s, &mine_before, &mine);
   // Weights: the tiles of every (sequence, key head) in equal contiguous
   // shares, one for each of the first blocks, walked row by row.  The share's
   // first row is found now, too (32 sequences of up to 4001: 0.6 us less).
-  C4Walk w;
+  C4Walk<true> w;
   w.x = w.end = 0;
   if (kWeight && blockIdx.x < m.weight_blocks) {
     const int64_t all = c4_units(count, kC4MergeRowCost) * p.c.H;
     const int64_t mine_w = (all + m.weight_blocks - 1) / m.weight_blocks;
     w.x = blockIdx.x * mine_w;
     w.end = w.x + mine_w < all ? w.x + mine_w : all;
-    if (w.x < w.end) c4_find(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
+    if (w.x < w.end) c4_find<true>(p, w.x / p.c.H, kC4MergeRowCost, mine_before, mine, &b_s, &before_s);
   }
   grid_dependency_wait();
   grid_launch_dependents();
@@ -1324,7 +1333,7 @@ __global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(c
     const int stripe = (p.B + kC4MergeThreads - 1) / kC4MergeThreads;
     if (b / stripe == tid) {  // what lies before sequence b: its stripe's owner knows
       int64_t at = mine_before;
-      for (int i = tid * stripe; i < b; ++i) at += c4_count(c4_tiles(p, i));
+      for (int i = tid * stripe; i < b; ++i) at += c4_count(c4_tiles<true>(p, i));
       before_s = at;
     }
     __syncthreads();
@@ -1336,7 +1345,7 @@ __global__ void __launch_bounds__(kC4MergeThreads, 4) attn_cache4_merge_kernel(c
     if (head < hq) {
       const int h = head / p.G, g = head % p.G, hb = g / kC4Heads;
       const int in_b = h * p.HB + hb;
-      const int nt = c4_tiles(p, b);
+      const int nt = c4_tiles<true>(p, b);
       const C4Parts cut = c4_parts(before + static_cast<int64_t>(in_b) * c4_row_units(nt, kC4RowCost), nt, share);
       const int64_t slot0 = cut.first + static_cast<int64_t>(b) * rows_per_b + in_b;
       const float2* ml = p.ml_part + slot0 * kC4Heads + g % kC4Heads;
