@@ -119,30 +119,45 @@ def norm_weights(q_weight, k_weight, dtype, index, D):
     return q_weight.data_ptr(), k_weight.data_ptr(), code
 
 
+def _apart(b, B, s, S, h, H, D) -> bool:
+    """Whether no two of B x S x H rows of D elements, at these strides, share an element."""
+    heads, rows = h * (H - 1) + D, s * (S - 1) + D  # extents
+    if (H < 2 or h >= D) and (S < 2 or s >= heads) and (B < 2 or b >= s * (S - 1) + heads):
+        return True  # [B, S, H, D] and its slices
+    if (S < 2 or s >= D) and (H < 2 or h >= rows) and (B < 2 or b >= h * (H - 1) + rows):
+        return True  # [B, H, S, D]
+    # any other layout: of every difference in the two shorter counts, the nearest in the longest
+    (n1, s1), (n2, s2), (n3, s3) = sorted(((B, b), (S, s), (H, h)))
+    for i in range(n1):
+        for j in range(-(n2 - 1), n2):
+            x = i * s1 + j * s2
+            k = 0 if n3 < 2 or s3 == 0 else min(max(-x // s3, 1 - n3), n3 - 1)
+            for c in (k, min(k + 1, n3 - 1)):
+                if (i or j or c) and abs(x + c * s3) < D:
+                    return False
+    return True
+
+
 def _strides(stride, shape, name, out=False):
     """(batch, row, head) strides of rows [S, H, D] or [B, S, H, D].  Where there is one of
-    something, its stride says nothing (and may be anything)."""
+    something, its stride says nothing (and may be anything).  out: its rows must lie apart."""
     if len(stride) == 4:
         b, s, h, one = stride
-        n, S, H, _ = shape
-        if n < 2:
+        B, S, H, D = shape
+        if B < 2:
             b = 0
-        elif out and b == 0:
-            raise ValueError(f"{name}: rows of an output must lie apart")
     else:
         s, h, one = stride
-        S, H, _ = shape
-        b = 0
+        S, H, D = shape
+        B, b = 1, 0
     if S < 2:
         s = 0
-    elif out and s == 0:
-        raise ValueError(f"{name}: rows of an output must lie apart")
     if H < 2:
         h = 0
-    elif out and h == 0:
-        raise ValueError(f"{name}: rows of an output must lie apart")
     if one != 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
+    if out and S and B and not _apart(b, B, s, S, h, H, D):
+        raise ValueError(f"{name}: rows of an output must lie apart")
     return b, s, h
 
 
@@ -185,7 +200,8 @@ def qk_norm_rope(q, k, rope, positions=None, q_weight=None, k_weight=None, eps: 
     elements): slices of a projection's output, or [B, H, S, D] tensors transposed.  rope: a
     Rotary, or None for no rotation.  positions: int32 [S] or [B, S].  q_weight, k_weight: [D] of
     q's type or float32; None: no norm of that one.  q_out, k_out: what to write to, of any
-    strides, q and k themselves among them (None: new contiguous tensors).  Returns (q_out, k_out).
+    strides that keep rows apart, q and k themselves among them (None: new contiguous tensors).
+    Returns (q_out, k_out).
     """
     import torch
 

@@ -101,3 +101,17 @@ def test_append_writes_keys_as_they_are(d, rot, inter, dtype):
     kk, vv = cache.k_pages[where, :, j % page], cache.v_pages[where, :, j % page]
     assert torch.equal(bits(q_out[..., rot:]), bits(q[..., rot:]))
     assert torch.equal(bits(kk[..., rot:]), bits(k[..., rot:])) and torch.equal(bits(vv), bits(v))
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    q, k = (torch.randn((2, 5, 4, 64), device=DEV).bfloat16() for _ in range(2))
+    buffer = torch.zeros(4000, dtype=torch.bfloat16, device=DEV)
+    for strides in ((5 * 4 * 64, 4 * 64, 32, 1), (640, 64, 64, 1), (1024, 256, 64, 1)):
+        bad = buffer.as_strided(q.shape, strides)
+        for name in ("q_out", "k_out"):
+            with pytest.raises(ValueError, match="apart"):
+                attn.qk_norm_rope(q, k, None, **{name: bad})
+        for name in ("dq", "dk"):
+            with pytest.raises(ValueError, match="apart"):
+                attn.qk_norm_rope_backward(q, k, q, k, None, **{name: bad})
+    assert not buffer.any()
