@@ -1005,11 +1005,6 @@ attn_status_t chunk_run(const attn_pages_t* cache, const PagedAttn& a, const Chu
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
-// Up to how many (token, head) rows of a key head the token kernel takes a sequence: one
-// block's.  16 rows over 32260 entries of 8 key heads take 30 us there, 32 rows 54 us here.
-constexpr int kTokMaxRows = 16;
-bool paged_is_token(int max_new, int G) { return static_cast<int64_t>(max_new) * G <= kTokMaxRows; }
-
 }  // namespace
 
 extern "C" {

@@ -19,9 +19,9 @@
 //   * P enters P V as the sum of two 16-bit numbers, which leaves 16 (bf16) or 22
 //     bits of it: the products are there for the taking, and O is as exact as from
 //     fp32 products.
-//   * Work split.  The visible tiles of all (sequence, key head, block of rows)
-//     form one list, cut into equal shares, one a CTA, whatever the lengths; a row
-//     counts kTokRowCost tiles more for its start and end.  A row within a share is
+//   * Work split.  The visible tiles of all (sequence, key head) form one list, cut
+//     into equal shares, one a CTA, whatever the lengths; each of its rows counts
+//     kTokRowCost tiles more for its start and end.  A row within a share is
 //     written at once; of a row that was cut, each share leaves a partial (m, l, O),
 //     and a second kernel joins them.  Few short rows have a CTA each instead:
 //     one launch.
@@ -91,13 +91,14 @@ __device__ __forceinline__ bool paged_all_seen(const PagedAttn& p, int k0, int k
   return k1 - 1 <= p0 && (k0 > p1 - p.window || k1 <= p.sinks);
 }
 
-// kNT: tiles of 8 query rows a block.  With one, the two groups of four consumer warps
+// kNT: tiles of 8 query rows, which hold a sequence's (token, query head) rows of a key
+// head.  With one, the two groups of four consumer warps
 // take tiles of keys in turn; with two, each takes every tile for 8 of the rows: 16 rows a
 // warp spilt and kept half the pace (64 sequences of up to 16000 entries with 16 query
 // heads a key head: 358 us instead of 323).
 template <int D, int kNT>
 struct TokCfg {
-  static constexpr int kRows = 8 * kNT;                    // query rows a block
+  static constexpr int kRows = 8 * kNT;                    // query rows
   static constexpr bool kSplit = kNT == 2;
   static constexpr int kUsers = kSplit ? 8 : 4;            // warps that use a stage
   static constexpr int kJoin = kSplit ? 4 : 8;             // warps that have keys of a row
@@ -124,40 +125,35 @@ struct TokCfg {
 // before in it: the share's CTA leaves it (first is -1 where there is none).
 struct __align__(16) TokCut {
   int32_t first, last;   // shares that have pieces of it
-  int32_t h, row_b;      // key head, first (token, head) row of its block
-  int32_t row0, rows;    // packed row of the sequence's first token; rows of the block
-  int32_t pad[2];
+  int32_t h, row0;       // key head, packed row of the sequence's first token
+  int32_t rows;          // query rows
+  int32_t pad[3];
 };
 
 struct TokParams {
   PagedAttn a;
   TokCut* cuts;     // [CTAs]
-  float* o_part;    // [2 * CTAs][rows of a block][D]; null: a CTA a row
-  float2* ml_part;  // [2 * CTAs][rows of a block]
-  int blocks_bound; // blocks of rows a sequence may have (a CTA a row)
+  float* o_part;    // [2 * CTAs][kRows][D]
+  float2* ml_part;  // [2 * CTAs][kRows]
   int box_rows, box_log2;  // rows of a TMA box: the page's, at most a tile's
   int missing;      // third coordinate behind the pages: reads zeros
 };
 
-__device__ __forceinline__ int tok_blocks(const PagedAttn& p, int n, int rows) {
-  return static_cast<int>((static_cast<int64_t>(n) * p.G + rows - 1) / rows);
-}
-template <int kRows>
 __device__ __forceinline__ int64_t tok_units(const PagedAttn& p, int b) {
   const PagedSpan w = PagedSpan::of<kTokTile>(p, b);
-  return static_cast<int64_t>(w.tiles + kTokRowCost) * p.s.H_kv * tok_blocks(p, w.n, kRows);
+  return w.n > 0 ? static_cast<int64_t>(w.tiles + kTokRowCost) * p.s.H_kv : 0;
 }
 
 // Units of all sequences, and those before this thread's (contiguous) ones; sums: a
 // block's scratch of warps + 1 words.  The whole block calls it.
-template <int kRows, int kThreads>
+template <int kThreads>
 __device__ int64_t tok_total(const PagedAttn& p, volatile int64_t* sums, int64_t* before) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
   const int per = (p.s.B + kThreads - 1) / kThreads;
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < p.s.B) mine += tok_units<kRows>(p, b);
+    if (b < p.s.B) mine += tok_units(p, b);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -177,14 +173,14 @@ __device__ int64_t tok_total(const PagedAttn& p, volatile int64_t* sums, int64_t
   return total;
 }
 // The sequence in whose units x lies, and the units before it, by the thread that has it.
-template <int kRows, int kThreads>
+template <int kThreads>
 __device__ void tok_find(const PagedAttn& p, int64_t x, int64_t before, volatile int* b_out, volatile int64_t* before_out) {
   const int per = (p.s.B + kThreads - 1) / kThreads;
   if (x < before) return;
   for (int i = 0; i < per; ++i) {
     const int b = static_cast<int>(threadIdx.x) * per + i;
     if (b >= p.s.B) return;
-    const int64_t u = tok_units<kRows>(p, b);
+    const int64_t u = tok_units(p, b);
     if (x < before + u) {
       *b_out = b;
       *before_out = before;
@@ -195,30 +191,28 @@ __device__ void tok_find(const PagedAttn& p, int64_t x, int64_t before, volatile
 }
 
 // A CTA's share, row by row.
-template <int kRows>
 struct TokWalk {
   int64_t x, end, before, share;
-  int b, blocks, per_row;
+  int b, heads, per_row;  // sequence; its rows (none without tokens), and what each counts
   PagedSpan w;
-  int h, rb, t0, t1;  // key head, block of rows, tiles of the list
-  int64_t at;         // place of the row's first tile in the list
+  int h, t0, t1;  // key head, tiles of the list
+  int64_t at;     // place of the row's first tile in the list
   __device__ void load(const PagedAttn& p) {
     w = PagedSpan::of<kTokTile>(p, b);
-    blocks = tok_blocks(p, w.n, kRows);
+    heads = w.n > 0 ? p.s.H_kv : 0;
     per_row = w.tiles + kTokRowCost;
   }
   __device__ bool next(const PagedAttn& p) {
     while (x < end) {
       const int64_t row = (x - before) / per_row;
-      if (row >= static_cast<int64_t>(blocks) * p.s.H_kv) {
-        before += static_cast<int64_t>(per_row) * blocks * p.s.H_kv;
+      if (row >= heads) {
+        before += static_cast<int64_t>(per_row) * heads;
         if (++b >= p.s.B) return false;
         load(p);
         continue;
       }
       const int64_t x0 = before + row * per_row;
-      h = static_cast<int>(row) / blocks;
-      rb = static_cast<int>(row) - h * blocks;
+      h = static_cast<int>(row);
       const bool starts = x == x0;
       t0 = static_cast<int>(max(static_cast<int64_t>(0), x - x0 - kTokRowCost));
       t1 = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(w.tiles), end - x0 - kTokRowCost)));
@@ -231,27 +225,24 @@ struct TokWalk {
 };
 
 // Sets this CTA's walk up; false: there is nothing for it.  kDirect: row blockIdx.x.
-template <int kRows, int kThreads, bool kDirect>
-__device__ __forceinline__ bool tok_start(TokWalk<kRows>& k, const TokParams& p, volatile int64_t* sums) {
+template <int kThreads, bool kDirect>
+__device__ __forceinline__ bool tok_start(TokWalk& k, const TokParams& p, volatile int64_t* sums) {
   if constexpr (kDirect) {
-    const int per_b = p.a.s.H_kv * p.blocks_bound;
-    k.b = static_cast<int>(blockIdx.x) / per_b;
-    const int i = static_cast<int>(blockIdx.x) - k.b * per_b;
+    k.b = static_cast<int>(blockIdx.x) / p.a.s.H_kv;
     k.load(p.a);
-    k.h = i / p.blocks_bound;
-    k.rb = i - k.h * p.blocks_bound;
+    k.h = static_cast<int>(blockIdx.x) - k.b * p.a.s.H_kv;
     k.t0 = 0, k.t1 = k.w.tiles;
-    return k.rb < k.blocks;
+    return k.h < k.heads;
   } else {
     int64_t before;
-    const int64_t total = tok_total<kRows, kThreads>(p.a, sums, &before);
+    const int64_t total = tok_total<kThreads>(p.a, sums, &before);
     const int64_t share = (total + gridDim.x - 1) / gridDim.x;
     k.share = share;
     k.x = static_cast<int64_t>(blockIdx.x) * share;
     k.end = k.x + share < total ? k.x + share : total;
     if (threadIdx.x == 0) p.cuts[blockIdx.x].first = -1;  // (the first row writes it again, behind a barrier)
     volatile int* const b_s = reinterpret_cast<volatile int*>(sums + kThreads / 32 + 1);
-    if (k.x < k.end) tok_find<kRows, kThreads>(p.a, k.x, before, b_s, sums + kThreads / 32);
+    if (k.x < k.end) tok_find<kThreads>(p.a, k.x, before, b_s, sums + kThreads / 32);
     __syncthreads();
     if (k.x >= k.end) return false;
     k.b = *b_s;
@@ -300,7 +291,7 @@ __device__ __forceinline__ void tok_write(const PagedAttn& p, int64_t at, int64_
 
 // Producer warp of K (kv 0) or V (1).
 template <int D, int kNT, bool kDirect>
-__device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, int kv, const CUtensorMap* map, uint32_t base, const WaitCtx& wc) {
+__device__ void tok_load(TokWalk k, const TokParams& p, int kv, const CUtensorMap* map, uint32_t base, const WaitCtx& wc) {
   using C = TokCfg<D, kNT>;
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int boxes = kTokTile >> p.box_log2;
@@ -354,7 +345,7 @@ __device__ void tok_load(TokWalk<8 * kNT> k, const TokParams& p, int kv, const C
 
 // Consumer warp `warp`.
 template <int D, int kType, int kNT, bool kDirect>
-__device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t base, uint8_t* smem, int warp, const WaitCtx& wc) {
+__device__ void tok_compute(TokWalk k, const TokParams& p, uint32_t base, uint8_t* smem, int warp, const WaitCtx& wc) {
   using C = TokCfg<D, kNT>;
   constexpr int kSteps = D / 16;
   const int lane = static_cast<int>(threadIdx.x) & 31, r = lane >> 2, c = lane & 3;
@@ -365,15 +356,14 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
   const int kpiece = lane >> 4, vpiece = (lane >> 3) & 1;
   float* const o_s = reinterpret_cast<float*>(smem + C::kO);
   float2* const ml_s = reinterpret_cast<float2*>(smem + C::kMl);
-  const int r0 = C::kSplit ? group * 8 : 0;  // this warp's rows of the block
+  const int r0 = C::kSplit ? group * 8 : 0;  // this warp's query rows
   int it = 0, seg = 0;
   bool ok = true;
   const float cl = p.a.scale_log2;
   bool more = kDirect ? true : k.next(p.a);
   while (more) {
     const PagedSpan& w = k.w;
-    const int row_b = k.rb * C::kRows;                     // first (token, head) row of the block
-    const int rows = min(C::kRows, w.n * p.a.G - row_b);
+    const int rows = w.n * p.a.G;  // (at most kRows)
     // Q as B operands, and the positions of this lane's columns.  (Coherent loads, not the
     // read-only path's: the append before may have written Q since this kernel began.  They
     // may stay in the SM's cache, where the other warps find them: past it, one sequence of
@@ -381,7 +371,7 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
     uint32_t q[kSteps][2];
     int pos[2];
     {
-      const int mine = row_b + min(r0 + r, rows - 1), tok = mine / p.a.G, g = mine - tok * p.a.G;
+      const int mine = min(r0 + r, rows - 1), tok = mine / p.a.G, g = mine - tok * p.a.G;
       const uint16_t* src = p.a.q + (w.row0 + tok) * p.a.q_stride + (k.h * p.a.G + g) * static_cast<int64_t>(D) + 2 * c;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks)
@@ -389,9 +379,9 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
         for (int i = 0; i < 2; ++i)
           q[ks][i] = r0 + r < rows ? __ldca(reinterpret_cast<const uint32_t*>(src + ks * 16 + i * 8)) : 0u;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) pos[e] = w.p0 + (row_b + min(r0 + 2 * c + e, rows - 1)) / p.a.G;
+      for (int e = 0; e < 2; ++e) pos[e] = w.p0 + min(r0 + 2 * c + e, rows - 1) / p.a.G;
     }
-    const int p_first = w.p0 + row_b / p.a.G, p_last = w.p0 + (row_b + rows - 1) / p.a.G;
+    const int p_first = w.p0, p_last = w.p0 + w.n - 1;
     float ref[2], sub[2], l[2], o[kSteps][4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) ref[e] = -INFINITY, sub[e] = l[e] = 0.f;
@@ -527,7 +517,7 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
         // the CTA's first row: is this the first cut of it?
         const int64_t share = k.share, first = k.at / share, last = (k.at + w.tiles - 1) / share;
         const bool here = k.t0 > 0 && first + 1 == static_cast<int64_t>(blockIdx.x);
-        *(p.cuts + blockIdx.x) = TokCut{here ? static_cast<int>(first) : -1, static_cast<int>(last), k.h, row_b, w.row0, rows, {0, 0}};
+        *(p.cuts + blockIdx.x) = TokCut{here ? static_cast<int>(first) : -1, static_cast<int>(last), k.h, w.row0, rows, {0, 0, 0}};
       }
     }
     const bool whole = kDirect || (k.t0 == 0 && k.t1 == w.tiles);
@@ -550,7 +540,7 @@ __device__ void tok_compute(TokWalk<8 * kNT> k, const TokParams& p, uint32_t bas
         v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
       }
       if (whole) {
-        const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
+        const int tok = n / p.a.G, g = n - tok * p.a.G;
         const int64_t at = static_cast<int64_t>(w.row0 + tok) * p.a.s.H_kv * p.a.G + k.h * p.a.G + g;
         tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
       } else {
@@ -588,8 +578,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const WaitCtx wc{p.a.timeout_ns, misc};
   grid_dependency_wait();
   grid_launch_dependents();
-  TokWalk<C::kRows> k;
-  if (!tok_start<C::kRows, kTokThreads, kDirect>(k, p, reinterpret_cast<volatile int64_t*>(smem + C::kMisc + 16))) return;
+  TokWalk k;
+  if (!tok_start<kTokThreads, kDirect>(k, p, reinterpret_cast<volatile int64_t*>(smem + C::kMisc + 16))) return;
   if (warp >= kTokWarps)
     tok_load<D, kNT, kDirect>(k, p, warp - kTokWarps, warp == kTokWarps ? &tmK : &tmV, base, wc);
   else
@@ -608,8 +598,9 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
   __shared__ float4 o_s[kGroups][kLanes];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int4 c0 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x)), c1 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x) + 1);
-  const int ca = c0.x, cb = c0.y, h = c0.z, row_b = c0.w, row0 = c1.x, rows = c1.y;
+  const int4 c0 = __ldg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x));
+  const int rows = __ldg(&p.cuts[blockIdx.x].rows);
+  const int ca = c0.x, cb = c0.y, h = c0.z, row0 = c0.w;
   const int n = static_cast<int>(blockIdx.y), group = static_cast<int>(threadIdx.x) / kLanes;
   const int ch = (static_cast<int>(threadIdx.x) % kLanes) * 4;
   if (ca < 0 || n >= rows) return;
@@ -657,7 +648,7 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
     }
     add(s, o);
   }
-  const int tok = (row_b + n) / p.a.G, g = row_b + n - tok * p.a.G;
+  const int tok = n / p.a.G, g = n - tok * p.a.G;
   const int64_t at = static_cast<int64_t>(row0 + tok) * p.a.s.H_kv * p.a.G + h * p.a.G + g;
   tok_write<kType>(p.a, at * D + ch, at, v, m, sum, ch == 0);
 }
@@ -672,18 +663,22 @@ __global__ void __launch_bounds__(kTokMergeThreads) attn_paged_merge_kernel(cons
 constexpr int kTokDirectLen = 1536;
 constexpr int kTokSms = 152;  // (the workspace's size is asked for without a device)
 
-// What an attention over pages takes: blocks of 8 or 16 rows, and a CTA a row or shares.
+// Up to how many (token, head) rows of a key head a sequence may have here.  16 rows over
+// 32260 entries of 8 key heads take 30 us, 32 rows 54 us in the chunks' kernel.
+constexpr int kTokMaxRows = 16;
+static_assert(kTokMaxRows <= TokCfg<64, 2>::kRows && kTokMaxRows <= TokCfg<128, 2>::kRows, "a sequence's rows are one block");
+bool paged_is_token(int max_new, int G) { return static_cast<int64_t>(max_new) * G <= kTokMaxRows; }
+
+// What an attention over pages takes: 8 or 16 query rows, and a CTA a row or shares.
 struct TokPlan {
-  int nt, blocks;   // tiles of 8 rows a block; blocks a sequence may have
+  int nt;  // tiles of 8 query rows
   bool direct;
 };
 TokPlan tok_plan(int B, int H_kv, int G, int max_new, int max_len, int window, int sinks) {
   TokPlan t;
-  const int64_t rows = static_cast<int64_t>(max_new) * G;
-  t.nt = rows <= 8 ? 1 : 2;
-  t.blocks = static_cast<int>(std::min<int64_t>((rows + 8 * t.nt - 1) / (8 * t.nt), INT_MAX));
+  t.nt = max_new * G <= 8 ? 1 : 2;  // (paged_is_token holds)
   const int64_t keys = window > 0 ? std::min<int64_t>(max_len, static_cast<int64_t>(window) + sinks + max_new) : max_len;
-  t.direct = static_cast<int64_t>(B) * H_kv * t.blocks <= kTokSms && keys <= kTokDirectLen;
+  t.direct = static_cast<int64_t>(B) * H_kv <= kTokSms && keys <= kTokDirectLen;
   return t;
 }
 uint64_t tok_workspace(const TokPlan& t, int D) {
@@ -724,7 +719,7 @@ cudaError_t tok_launch(const CUtensorMap& tk, const CUtensorMap& tv, const TokPa
   const cudaError_t e = launch_pdl(attn_paged_token_kernel<D, kType, kNT, false>, dim3(kTokSms), dim3(kTokThreads), C::kBytes, s,
                                    tk, tv, p);
   return e != cudaSuccess ? e
-                          : launch_pdl(attn_paged_merge_kernel<D, kType, C::kRows>, dim3(kTokSms, static_cast<unsigned>(std::min<int64_t>(C::kRows, static_cast<int64_t>(p.a.max_new) * p.a.G))),
+                          : launch_pdl(attn_paged_merge_kernel<D, kType, C::kRows>, dim3(kTokSms, static_cast<unsigned>(p.a.max_new * p.a.G)),
                                        dim3(kTokMergeThreads), 0, s, p);
 }
 
@@ -737,12 +732,11 @@ attn_status_t tok_run(const attn_pages_t* c, const PagedAttn& a, const TokPlan& 
   p.o_part = static_cast<float*>(workspace);
   p.ml_part = reinterpret_cast<float2*>(p.o_part + static_cast<int64_t>(2 * kTokSms) * 8 * t.nt * c->D);
   p.cuts = reinterpret_cast<TokCut*>(p.ml_part + static_cast<int64_t>(2 * kTokSms) * 8 * t.nt);
-  p.blocks_bound = t.blocks;
   p.box_rows = box;
   p.box_log2 = 0;
   while ((1 << p.box_log2) < box) ++p.box_log2;
   p.missing = c->n_pages * c->H_kv;
-  const int64_t rows = static_cast<int64_t>(c->B) * c->H_kv * t.blocks;
+  const int64_t rows = static_cast<int64_t>(c->B) * c->H_kv;
   const auto run = [&](auto d, auto type) {
     return t.nt == 1 ? tok_launch<d(), type(), 1>(tk, tv, p, t.direct, rows, s) : tok_launch<d(), type(), 2>(tk, tv, p, t.direct, rows, s);
   };
