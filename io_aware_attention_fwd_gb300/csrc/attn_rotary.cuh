@@ -561,13 +561,11 @@ RotGrid rot_grid(int64_t tokens, int groups, int sms, int blocks_per_sm, int war
   return g;
 }
 
-
-bool rot_rows_ok(const attn_heads_t* r, int D, attn_status_t* st) {
+bool rot_rows_ok(const attn_heads_t* r, attn_status_t* st) {
   *st = r == nullptr || r->ptr == nullptr ? ATTN_ERR_INVALID_ARG
         : !aligned(r->ptr, 16) || r->batch_stride % 8 != 0 || r->row_stride % 8 != 0 || r->head_stride % 8 != 0
             ? ATTN_ERR_ALIGNMENT
             : ATTN_OK;
-  (void)D;
   return *st == ATTN_OK;
 }
 RotRows rot_rows_of(const attn_heads_t* r) {
@@ -633,7 +631,7 @@ attn_status_t attn_qk_norm_rope(const attn_heads_t* q, const attn_heads_t* k, co
   if (st != ATTN_OK) return st;
   if (B == 0 || S == 0) return ATTN_OK;
   if (p.turn.rot > 0 && positions == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (!rot_rows_ok(q, D, &st) || !rot_rows_ok(k, D, &st) || !rot_rows_ok(q_out, D, &st) || !rot_rows_ok(k_out, D, &st)) return st;
+  if (!rot_rows_ok(q, &st) || !rot_rows_ok(k, &st) || !rot_rows_ok(q_out, &st) || !rot_rows_ok(k_out, &st)) return st;
   if (!aligned(positions, 4)) return ATTN_ERR_ALIGNMENT;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_DEVICE;
@@ -683,8 +681,8 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_heads_t* dq_out, const attn_heads
   const bool norm = q_weight != nullptr || k_weight != nullptr, rows = B > 0 && S > 0;
   if (rows) {
     if (p.turn.rot > 0 && positions == nullptr) return ATTN_ERR_INVALID_ARG;
-    if (!rot_rows_ok(dq_out, D, &st) || !rot_rows_ok(dk_out, D, &st) || !rot_rows_ok(dq, D, &st) || !rot_rows_ok(dk, D, &st)) return st;
-    if ((q_weight != nullptr && !rot_rows_ok(q, D, &st)) || (k_weight != nullptr && !rot_rows_ok(k, D, &st))) return st;
+    if (!rot_rows_ok(dq_out, &st) || !rot_rows_ok(dk_out, &st) || !rot_rows_ok(dq, &st) || !rot_rows_ok(dk, &st)) return st;
+    if ((q_weight != nullptr && !rot_rows_ok(q, &st)) || (k_weight != nullptr && !rot_rows_ok(k, &st))) return st;
   }
   if (!aligned(positions, 4) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(workspace, 16)) return ATTN_ERR_ALIGNMENT;
   if (norm && (workspace == nullptr || workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(B, S, H_q, H_k, D))) return ATTN_ERR_INVALID_ARG;
