@@ -1468,7 +1468,9 @@ bool encode_3d(CUtensorMap* m, const void* ptr, int D, int S, int64_t BH, int eb
 // thread of it waits (griddepcontrol.wait) before its first access to memory that
 // the kernels before it in the stream may still write or read.  Nearly always that
 // is its first access of all; attn_cache4_merge_kernel reads the cache's lengths
-// before (the reason is there).
+// before (the reason is there).  As the memory may be written while the kernel is on
+// the GPU already, what shares lines with anything that is read meanwhile (a cache's
+// lengths) is read by coherent loads or past the SM's cache, not by read-only ones.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args&&... args) {
