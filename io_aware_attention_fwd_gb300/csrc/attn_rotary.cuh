@@ -24,11 +24,11 @@
 // what they and the weights make of a lane's channels,
 //     y = r (x A + x' B)   (x' the paired channels),
 // stays in registers for all heads of the token.
-// 16384 tokens of 64 heads, D = 128 (537 MB): 88 us, 6.1 TB/s, against 86 us for a copy
+// 16384 tokens of 64 heads, D = 128 (537 MB): 87 us, 6.2 TB/s, against 86 us for a copy
 // of the same tensors.  With a block's tokens' tables in shared memory, read for each
 // head, it took 186 us; walking group by group with the addresses worked out anew, 159
 // (226 instructions a group); four groups at once in registers, 96.  The gradient of as
-// many tokens of 40 heads (503 MB): 106 us, 4.7 TB/s; it is held up by its 128 registers
+// many tokens of 40 heads (503 MB): 104 us, 4.8 TB/s; it is held up by its 128 registers
 // a thread (two blocks an SM), but three blocks spill and take 128 to 138.
 
 namespace {

@@ -17,10 +17,11 @@
 //     end cuts leave partials (m, l, O in fp32), which a third kernel joins.  Where
 //     there are few units of few keys each CTA takes one: one launch.
 //
-// 512 tokens over 32768 entries, 32/8 heads, D = 128: 188 us, 1450 TFLOP/s, of which the
-// list takes 7, the attention 173 (its MMAs 71% of the tensor pipe's nominal time) and the
-// merge 10.  A prompt of 16384 with windows of 4096: 684 us, 1425 TFLOP/s of visible pairs,
-// 1490 with the masked halves of edge tiles.
+// 512 tokens over 32768 entries, 32/8 heads, D = 128: 186 to 199 us from run to run, 1370
+// to 1470 TFLOP/s, of which the list takes 7, the attention 171 to 176 (its MMAs 70% of the
+// tensor pipe's nominal time) and the merge 11.  A prompt of 16384 with windows of 4096: 677
+// to 738 us as the power cap has it, 1320 to 1440 TFLOP/s of visible pairs, 4% more with the
+// masked halves of edge tiles.
 
 namespace {
 

@@ -30,7 +30,7 @@
 //
 // 64 sequences of up to 16000 entries, 64/8 heads, D = 128: 311 us, 6.85 TB/s.  One of
 // 131072, 32/8: 84 us, 6.4 TB/s (80 in the attention, then the merge).  32 windows of
-// 4096 in pages of 16: 87 us, 5.9 TB/s: each CTA has one to three rows to start and end.
+// 4096 in pages of 16: 87 to 91 us, 5.8 TB/s: each CTA has one to three rows to start and end.
 // One of 701, 16/16, D = 64: 6.8 us on the GPU.
 
 namespace {
